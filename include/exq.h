@@ -319,6 +319,137 @@ exq_status exq_plan_create(int count, const exq_layer_t* layers, const void* con
 exq_status exq_plan_run(exq_plan_t plan, void* stream);
 void exq_plan_destroy(exq_plan_t plan);
 
+/* ------------------------------------------------------- key-value cache */
+
+/* A paged cache of attention keys and values, quantized as it is written (the
+ * exllamav2 report, sections 创新之处 and 关键设计决策: 4-bit cache, pages of
+ * 256 tokens; the ExlLamaV3 page, section 核心能力: cache widths chosen apart
+ * for keys and values).  It is what stands between a block's q/k/v linears and
+ * its output linear: exq_cache_append stores the new tokens' keys and values,
+ * exq_attend attends to them with one query token per sequence, and
+ * exq_cache_read gives the stored values back.
+ *
+ * Quantizer: exq_pack's, over groups of 32 consecutive channels of one token
+ * and head, for a width b of 4 or 8:
+ *   s = fp16_RNE(fp32(max|x|) / fp32(2^(b-1)-1)), an fp32 division;
+ *   c = clamp(rint_even(fp32(x)/fp32(s)), -(2^(b-1)-1), 2^(b-1)-1) + 2^(b-1),
+ *   2^(b-1) if s == 0;  the value held is x_hat = fp16_RNE((c - 2^(b-1)) * s).
+ * A group that holds an infinity or a NaN gets a NaN scale: all of it reads
+ * back as NaN.  Width 16 holds the fp16 values themselves.
+ *
+ * Layout.  A page holds page_size tokens of every head and is one run of
+ * exq_cache_page_bytes bytes: [kv head][tile of 16 tokens][tile bytes].  A
+ * tile is [key codes][key scales][value codes][value scales]; parts of width
+ * 16 have no scales.  With G = head_dim/32 groups and gpc = 16/b groups to a
+ * chunk, chunk j of a code part starts at its byte 1024 j and holds n_j =
+ * min(gpc, G - j gpc) groups for 64 lanes, n_j * b bytes a lane, b bytes (8
+ * elements) a group:
+ *   keys    lane 16 q + t: channels 32 g + 8 q + e (e = 0..7) of token t; b = 4:
+ *           one dword, element e at bit 4 (e/2) + 16 (e%2); b = 8, 16: in order.
+ *   values  lane 16 (t/4) + c: channels 32 g + 16 h + c (h = 0, 1) of tokens
+ *           4 (t/4) .. + 3; b = 4: one dword, token t at bit 16 (t%2) +
+ *           8 (t%4/2) + 4 h; b = 8, 16: element 4 h + t%4 in order.
+ *   scales  fp16: keys [token][G], values [token/4][G][token%4].
+ * So every element of a token owns whole bytes with others of that token
+ * only, a wave reads a chunk as one contiguous run, and a lane's 8 elements
+ * are one operand of v_mfma_f32_16x16x32_f16: keys with the channels of a group
+ * as its inner dimension, values with the tokens of two tiles.
+ *
+ * Addressing: a table, int32 [rows][table_width] with rows table_stride
+ * elements apart, names each sequence's pages: position p of sequence s lies in
+ * page table[s][p / page_size], at token p % page_size of it.  Sequences may
+ * share pages that no one writes.
+ *
+ * The handle holds the geometry and the borrowed pages pointer, on the host
+ * only: no device memory, no scratch, so any number of streams may use it at
+ * once.  No call below allocates, waits or copies, so all may be captured. */
+typedef struct exq_cache* exq_cache_t;
+
+/* Bytes of a page; 0 if an argument is invalid or unsupported. */
+size_t exq_cache_page_bytes(int page_size, int kv_heads, int head_dim, int k_bits, int v_bits);
+
+/* Describe a cache.
+ *   pages      device, 16-byte aligned, n_pages * exq_cache_page_bytes() bytes
+ *              (borrowed: must outlive the handle); any content
+ *   n_pages    1 .. 2^31 - 1
+ *   page_size  tokens, a multiple of 16, 16 .. 65536
+ *   kv_heads   1 .. 65535
+ *   head_dim   64, 96, 128 or 256 (another multiple of 32: UNSUPPORTED)
+ *   k_bits, v_bits   each 4 or 8, or both 16 (else UNSUPPORTED)
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM. */
+exq_status exq_cache_create(void* pages, int64_t n_pages, int page_size, int kv_heads, int head_dim, int k_bits,
+                            int v_bits, exq_cache_t* out);
+
+/* Release a handle (not the pages).  NULL is a no-op.  Work already launched
+ * keeps no reference to the handle. */
+void exq_cache_destroy(exq_cache_t cache);
+
+/* Quantize and store `rows` tokens.
+ *   k, v       device fp16, 16-byte aligned; element (r, h, d) at
+ *              r * row_stride + h * head_stride + d; strides are multiples of 8
+ *              elements, >= 0 (0 broadcasts)
+ *   table      device int32 [table_rows][table_width], rows table_stride apart
+ *   seqs, positions   device int32 [rows]: row r goes to position positions[r]
+ *              of sequence seqs[r].  A row with seqs[r] < 0 is padding and is
+ *              skipped; so is a row whose sequence, position or page is outside
+ *              the table or the cache.  The destinations of one call must
+ *              differ: of two rows sent to one place either may be stored, or a
+ *              mixture of both.
+ * Nothing but the bytes of those rows is written.  rows == 0 is a no-op.
+ * Errors: INVALID_ARG (NULL, misaligned, bad size or stride, k or v overlapping
+ * the pages), UNSUPPORTED (rows * heads beyond a launch's 2^31 - 1 workgroups), HIP. */
+exq_status exq_cache_append(exq_cache_t cache, const void* k, int64_t k_row_stride, int64_t k_head_stride,
+                            const void* v, int64_t v_row_stride, int64_t v_head_stride, int rows,
+                            const int32_t* table, int table_rows, int table_width, int64_t table_stride,
+                            const int32_t* seqs, const int32_t* positions, void* stream);
+
+/* Read `rows` tokens back as the fp16 values the cache holds for them, bit for
+ * bit x_hat.  Arguments as exq_cache_append, with k and v written (their rows
+ * and heads must not overlap themselves or each other); positions may repeat.
+ * A row with seqs[r] < 0 is left as it was; a row whose sequence, position or
+ * page is outside the table or the cache is filled with NaN. */
+exq_status exq_cache_read(exq_cache_t cache, void* k, int64_t k_row_stride, int64_t k_head_stride, void* v,
+                          int64_t v_row_stride, int64_t v_head_stride, int rows, const int32_t* table,
+                          int table_rows, int table_width, int64_t table_stride, const int32_t* seqs,
+                          const int32_t* positions, void* stream);
+
+/* Bytes of workspace exq_attend needs for these sizes (0: none, or an argument
+ * is invalid).  It depends on nothing else: not on lengths or strides. */
+size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int table_width);
+
+/* Attention of one new token per sequence over the cache.  For row r, query
+ * head h and its key-value head h / (q_heads / kv_heads), over the tokens j in
+ * [max(0, n - window), n) of row r's sequence (window 0: [0, n)), n = lengths[r]:
+ *   S_j = scale * sum_d q_d K_hat_jd,   out = sum_j e^{S_j} V_hat_j / sum_j e^{S_j},
+ *   lse = ln sum_j e^{S_j}
+ *   q          device fp16 [rows][q_heads][head_dim] with strides as for k above
+ *   q_heads    a positive multiple of kv_heads
+ *   table      device int32 [rows][table_width], rows table_stride apart
+ *   lengths    device int32 [rows].  0: out is 0 and lse -infinity.  Negative:
+ *              a padding row, out and lse left as they were.  Above
+ *              table_width * page_size, or a page outside the cache among those
+ *              read: out and lse are NaN.
+ *   scale      finite;  window >= 0
+ *   out        device fp16 with strides as for q, no element twice, no overlap
+ *              with q or the pages
+ *   lse        device fp32 [rows][q_heads] or NULL
+ *   workspace  device, 16-byte aligned, exq_attend_workspace_bytes() bytes, any
+ *              content; NULL if that is 0.  Calls that may run at the same time
+ *              (other streams, replays of two graphs) need one each.
+ * What a page holds behind a sequence's end, or before its window, never
+ * reaches the result, NaN included.  Scores, softmax sums and output sums are
+ * fp32; the weights e^{S_j - max} enter the second product rounded to fp16.
+ * The order of summation depends on the sizes and lengths only: deterministic.
+ * Accuracy, with S_j the exact scores, A = max_j |scale| sum_d |q_d K_hat_jd| and
+ * P = sum_j e^{S_j} |V_hat_j| / sum_j e^{S_j} the average of the magnitudes:
+ *   |out - out_ref| <= (2^-10 + 2^-14 + 2^-17 A) P + 2^-11 |out_ref| + 2^-24
+ *   |lse - lse_ref| <= 2^-18 (1 + A) + 2^-22 |lse_ref|
+ * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, HIP. */
+exq_status exq_attend(exq_cache_t cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int rows,
+                      int q_heads, const int32_t* table, int table_width, int64_t table_stride,
+                      const int32_t* lengths, float scale, int window, void* out, int64_t out_row_stride,
+                      int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------ diagnostic */
 
 /* A plain streaming read, the practical HBM read ceiling that the decode

@@ -12,6 +12,7 @@ ownership and errors.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -72,10 +73,23 @@ def _load():
     lib.exq_autotune.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, vp]
     lib.exq_set_variant.argtypes = [vp, i32, i32]
     lib.exq_allocate_widths.argtypes = [vp, vp, i32, ctypes.c_int64, vp, ctypes.c_uint64, ctypes.c_int64, vp, vp]
+    i64 = ctypes.c_int64
+    lib.exq_cache_page_bytes.argtypes = [i32, i32, i32, i32, i32]
+    lib.exq_cache_page_bytes.restype = u64
+    lib.exq_cache_create.argtypes = [vp, i64, i32, i32, i32, i32, i32, ctypes.POINTER(vp)]
+    lib.exq_cache_destroy.argtypes = [vp]
+    lib.exq_cache_destroy.restype = None
+    rows_call = [vp, vp, i64, i64, vp, i64, i64, i32, vp, i32, i32, i64, vp, vp, vp]
+    lib.exq_cache_append.argtypes = rows_call
+    lib.exq_cache_read.argtypes = rows_call
+    lib.exq_attend_workspace_bytes.argtypes = [vp, i32, i32, i32]
+    lib.exq_attend_workspace_bytes.restype = u64
+    lib.exq_attend.argtypes = [vp, vp, i64, i64, i32, i32, vp, i32, i64, vp, ctypes.c_float, i32, vp, i64, i64, vp, vp,
+                               u64, vp]
     for f in (lib.exq_pack, lib.exq_layer_create, lib.exq_gemm, lib.exq_gemm_noalloc, lib.exq_dequant, lib.exq_plan_create,
               lib.exq_plan_run, lib.exq_stream_read, lib.exq_gemm_gated, lib.exq_group_errors,
               lib.exq_allocate_widths, lib.exq_autotune, lib.exq_set_variant, lib.exq_pack_qs,
-              lib.exq_layer_create_qs):
+              lib.exq_layer_create_qs, lib.exq_cache_create, lib.exq_cache_append, lib.exq_cache_read, lib.exq_attend):
         f.restype = i32
     return lib
 
@@ -88,6 +102,8 @@ EXPORTED = (
     "exq_layer_destroy", "exq_gemm", "exq_dequant", "exq_plan_create", "exq_plan_run", "exq_plan_destroy",
     "exq_stream_read", "exq_gemm_gated", "exq_group_errors", "exq_allocate_widths", "exq_trimmed_mean",
     "exq_autotune", "exq_set_variant", "exq_pack_qs", "exq_layer_create_qs", "exq_gemm_noalloc",
+    "exq_cache_page_bytes", "exq_cache_create", "exq_cache_destroy", "exq_cache_append", "exq_cache_read",
+    "exq_attend_workspace_bytes", "exq_attend",
 )
 
 VARIANT_DEFAULT, VARIANT_DECODE16, VARIANT_DECODE64, VARIANT_PREFILL = 0, 1, 2, 3
@@ -258,7 +274,76 @@ def exq_plan_destroy(plan: int) -> None:
     lib.exq_plan_destroy(plan)
 
 
+def exq_cache_page_bytes(page_size: int, kv_heads: int, head_dim: int, k_bits: int, v_bits: int) -> int:
+    return int(lib.exq_cache_page_bytes(page_size, kv_heads, head_dim, k_bits, v_bits))
+
+
+def exq_cache_create(pages_ptr: int, n_pages: int, page_size: int, kv_heads: int, head_dim: int, k_bits: int,
+                     v_bits: int) -> int:
+    h = ctypes.c_void_p()
+    _check(lib.exq_cache_create(pages_ptr, n_pages, page_size, kv_heads, head_dim, k_bits, v_bits, ctypes.byref(h)),
+           "exq_cache_create")
+    return h.value
+
+
+def exq_cache_destroy(cache: int) -> None:
+    lib.exq_cache_destroy(cache)
+
+
+def exq_cache_append(cache: int, k_ptr: int, k_strides, v_ptr: int, v_strides, rows: int, table_ptr: int,
+                     table_rows: int, table_width: int, table_stride: int, seqs_ptr: int, positions_ptr: int,
+                     stream=None) -> None:
+    """k_strides, v_strides: (row, head) in elements."""
+    _check(lib.exq_cache_append(cache, k_ptr, k_strides[0], k_strides[1], v_ptr, v_strides[0], v_strides[1], rows,
+                                table_ptr, table_rows, table_width, table_stride, seqs_ptr, positions_ptr,
+                                _stream_ptr(stream)), "exq_cache_append")
+
+
+def exq_cache_read(cache: int, k_ptr: int, k_strides, v_ptr: int, v_strides, rows: int, table_ptr: int,
+                   table_rows: int, table_width: int, table_stride: int, seqs_ptr: int, positions_ptr: int,
+                   stream=None) -> None:
+    _check(lib.exq_cache_read(cache, k_ptr, k_strides[0], k_strides[1], v_ptr, v_strides[0], v_strides[1], rows,
+                              table_ptr, table_rows, table_width, table_stride, seqs_ptr, positions_ptr,
+                              _stream_ptr(stream)), "exq_cache_read")
+
+
+def exq_attend_workspace_bytes(cache: int, rows: int, q_heads: int, table_width: int) -> int:
+    return int(lib.exq_attend_workspace_bytes(cache, rows, q_heads, table_width))
+
+
+def exq_attend(cache: int, q_ptr: int, q_strides, rows: int, q_heads: int, table_ptr: int, table_width: int,
+               table_stride: int, lengths_ptr: int, scale: float, window: int, out_ptr: int, out_strides, lse_ptr=None,
+               workspace_ptr=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(lib.exq_attend(cache, q_ptr, q_strides[0], q_strides[1], rows, q_heads, table_ptr, table_width, table_stride,
+                          lengths_ptr, scale, window, out_ptr, out_strides[0], out_strides[1], lse_ptr, workspace_ptr,
+                          workspace_bytes, _stream_ptr(stream)), "exq_attend")
+
+
 # ------------------------------------------------------------ conveniences
+
+def _require(ok: bool, what: str):
+    """Argument checks of tensors, which the library never sees as such."""
+    if not ok:
+        raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", what)
+
+
+def _on(device):
+    """The device a call runs on: its tensors', whatever the current one is."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _allocating_on(stream, device):
+    """Tensors allocated inside belong to the stream that the call uses."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
 
 class Layer:
     """A packed layer resident on the GPU: owns its torch buffers and the handle."""
@@ -345,6 +430,123 @@ class Plan:
     def close(self):
         if self.handle:
             exq_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """A paged key-value cache on the GPU: owns (or borrows) its pages and the handle.
+
+    K and V are held in `k_bits` and `v_bits` bits (each 4 or 8, or both 16).  `table` is int32 [sequences][width] and
+    names each sequence's pages; position p of sequence s lies in page table[s][p // page_size].  Every call runs on
+    `stream` (default: the current stream of the cache's device) and may be captured; all tensors are on that device.
+    """
+
+    def __init__(self, n_pages: int, page_size: int, kv_heads: int, head_dim: int, k_bits: int = 4, v_bits: int = 4,
+                 device="cuda", pages=None):
+        """`pages`: uint8 [n_pages][page_bytes], contiguous, any content (default: allocated and zeroed)."""
+        import torch
+        self.handle = None
+        page_bytes = exq_cache_page_bytes(page_size, kv_heads, head_dim, k_bits, v_bits)
+        if page_bytes == 0:   # let the library say what is wrong
+            exq_cache_create(None, n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
+        if pages is None:
+            pages = torch.zeros((n_pages, page_bytes), dtype=torch.uint8, device=device)
+        _require(pages.dtype == torch.uint8 and pages.is_contiguous() and pages.is_cuda
+                 and pages.numel() == n_pages * page_bytes,
+                 "pages must be contiguous uint8 of %d x %d bytes on the GPU" % (n_pages, page_bytes))
+        self.pages, self.n_pages, self.page_size, self.page_bytes = pages, n_pages, page_size, page_bytes
+        self.kv_heads, self.head_dim, self.k_bits, self.v_bits = kv_heads, head_dim, k_bits, v_bits
+        self.device = pages.device
+        self.handle = exq_cache_create(pages.data_ptr(), n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
+
+    def _operand(self, name, x, rows, heads):
+        import torch
+        _require(x.dtype == torch.float16 and x.device == self.device and x.dim() == 3
+                 and x.shape == (rows, heads, self.head_dim) and x.stride(2) == 1,
+                 "%s must be fp16 [%d][%d][%d] on %s with contiguous channels" % (name, rows, heads, self.head_dim,
+                                                                                  self.device))
+        return x.data_ptr(), (x.stride(0), x.stride(1))
+
+    def _indices(self, name, x, rows):
+        import torch
+        _require(x.dtype == torch.int32 and x.device == self.device and x.dim() == 1 and x.shape[0] == rows
+                 and x.is_contiguous(), "%s must be contiguous int32 [%d] on %s" % (name, rows, self.device))
+        return x.data_ptr()
+
+    def _table(self, table, rows=None):
+        import torch
+        _require(table.dtype == torch.int32 and table.device == self.device and table.dim() == 2
+                 and (table.stride(1) == 1 or table.shape[1] == 1) and (rows is None or table.shape[0] == rows),
+                 "table must be int32 [%s][pages] on %s with contiguous rows" % (rows or "sequences", self.device))
+        return table.data_ptr(), table.shape[0], table.shape[1], table.stride(0)
+
+    def append(self, k, v, table, seqs, positions, stream=None):
+        """Store rows k, v (fp16 [rows][kv_heads][head_dim]) at positions[r] of sequence seqs[r] (int32 [rows]; < 0: skipped)."""
+        rows = k.shape[0]
+        kp, vp = self._operand("k", k, rows, self.kv_heads), self._operand("v", v, rows, self.kv_heads)
+        idx = self._indices("seqs", seqs, rows), self._indices("positions", positions, rows)
+        tab = self._table(table)
+        with _on(self.device):
+            exq_cache_append(self.handle, *kp, *vp, rows, *tab, *idx, stream)
+
+    def read(self, table, seqs, positions, k_out=None, v_out=None, stream=None):
+        """The values held for positions[r] of sequence seqs[r]: fp16 k, v [rows][kv_heads][head_dim].
+
+        Rows with seqs[r] < 0 are left as they were in k_out and v_out (in tensors allocated here: unspecified)."""
+        import torch
+        rows = seqs.shape[0]
+        idx = self._indices("seqs", seqs, rows), self._indices("positions", positions, rows)
+        tab = self._table(table)
+        with _on(self.device), _allocating_on(stream, self.device):
+            k_out, v_out = (torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float16, device=self.device)
+                            if x is None else x for x in (k_out, v_out))
+            kp, vp = self._operand("k_out", k_out, rows, self.kv_heads), self._operand("v_out", v_out, rows, self.kv_heads)
+            exq_cache_read(self.handle, *kp, *vp, rows, *tab, *idx, stream)
+        return k_out, v_out
+
+    def attend(self, q, table, lengths, scale=None, window: int = 0, out=None, return_lse: bool = False, lse=None,
+               workspace=None, stream=None):
+        """Attention of one query token per row: q fp16 [rows][q_heads][head_dim] over the first lengths[r] tokens of
+        table row r (the last `window` of them if window > 0) -> out, or (out, lse fp32 [rows][q_heads]).
+
+        scale: default head_dim ** -0.5.  lengths[r] == 0 gives zeros (lse -inf); < 0 leaves the row as it was.
+        workspace: uint8 of at least exq_attend_workspace_bytes (default: allocated by this call)."""
+        import torch
+        _require(q.dim() == 3, "q must be [rows][q_heads][head_dim]")
+        rows, q_heads = q.shape[0], q.shape[1]
+        qp = self._operand("q", q, rows, q_heads)
+        tab = self._table(table, rows)
+        n = self._indices("lengths", lengths, rows)
+        with _on(self.device), _allocating_on(stream, self.device):
+            if out is None:
+                out = torch.empty((rows, q_heads, self.head_dim), dtype=torch.float16, device=self.device)
+            op = self._operand("out", out, rows, q_heads)
+            if lse is None and return_lse:
+                lse = torch.empty((rows, q_heads), dtype=torch.float32, device=self.device)
+            if lse is not None:
+                _require(lse.dtype == torch.float32 and lse.device == self.device and lse.shape == (rows, q_heads)
+                         and lse.is_contiguous(), "lse must be contiguous fp32 [%d][%d] on %s" % (rows, q_heads, self.device))
+            nbytes = exq_attend_workspace_bytes(self.handle, rows, q_heads, table.shape[1])
+            if workspace is None and nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            if workspace is not None:
+                _require(workspace.device == self.device and workspace.is_contiguous(),
+                         "workspace must be contiguous on %s" % self.device)
+            exq_attend(self.handle, *qp, rows, q_heads, tab[0], tab[2], tab[3], n,
+                       self.head_dim ** -0.5 if scale is None else scale, window, *op,
+                       None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                       0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+        return (out, lse) if return_lse else out
+
+    def close(self):
+        if self.handle:
+            exq_cache_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

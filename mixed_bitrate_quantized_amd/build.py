@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libexq.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-HIP_SOURCES = ("exq_device.hip", "exq_prefill.hip")
+HIP_SOURCES = ("exq_device.hip", "exq_prefill.hip", "exq_cache.hip")
 HOST_SOURCES = ("exq_host.cpp",)
 
 HIPCC_FLAGS = [

@@ -1,0 +1,1110 @@
+// Paged key-value cache of libexq for gfx950: quantized append, read-back, and
+// attention of one new token over it.  include/exq.h documents the layout;
+// every kernel here reads or writes it directly.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "exq_device_common.h"
+#include "exq_internal.h"
+
+// Geometry of a cache and its borrowed pages (the exq_cache_t handle).
+struct exq_cache {
+    uint8_t* pages;
+    int64_t n_pages;
+    int page_size, kv_heads, head_dim, k_bits, v_bits;
+    size_t page_bytes;
+};
+
+namespace exq {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+constexpr int kCacheTile = 16;    // tokens per tile
+constexpr int kCacheGroup = 32;   // channels per scale
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Bytes of one part (codes, then scales) of a tile, and the byte in the code
+// part of lane l's b-byte unit of group g (see the layout in include/exq.h).
+template <int D, int B> struct CachePart {
+    static constexpr int G = D / kCacheGroup;
+    static constexpr int GPC = 16 / B;                            // groups per full chunk
+    static constexpr int CHUNKS = (G + GPC - 1) / GPC;
+    static constexpr int CODES = kCacheTile * D * B / 8;
+    static constexpr int SCALES = B < 16 ? kCacheTile * G * 2 : 0;
+    static constexpr int BYTES = CODES + SCALES;
+    __device__ static constexpr int chunk_groups(int j) { return G - j * GPC < GPC ? G - j * GPC : GPC; }
+    __device__ static int unit(int lane, int g) {
+        const int j = g / GPC;
+        return 1024 * j + lane * (chunk_groups(j) * B) + (g - j * GPC) * B;
+    }
+};
+
+// What the kernels know about a cache.
+struct CacheDev {
+    uint8_t* pages;
+    int64_t page_bytes;
+    uint32_t n_pages, page_size, kv_heads;
+    uint32_t tiles;   // per page and head
+};
+
+struct TableDev {
+    const int32_t* pages;
+    int64_t stride;
+    uint32_t rows, width;
+};
+
+// The fp16 values of a lane's eight elements of a group: x_hat = (c - z) * s,
+// the difference exact in fp16, the product rounded once.  W: the unit's
+// B / 4 dwords; s0, s1: the scales of halves 0 and 1 of a pair (keys: the
+// token's, twice; values: tokens 0, 1, and s2, s3 for tokens 2, 3).
+__device__ __forceinline__ uint32_t scaled(uint32_t biased, uint32_t zero, uint32_t s) {
+    const h2 v = (as_h2(biased) - as_h2(zero)) * as_h2(s);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// 0x6400 is fp16 1024, whose last bit is worth 1: an integer code below 1024
+// OR-ed into it gives 1024 + c.
+template <int B> constexpr uint32_t kBiasedZero = B == 4 ? 0x64086408u : 0x64806480u;   // 1024 + 2^(B-1)
+
+__device__ __forceinline__ uint32_t nibbles(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }
+
+// ------------------------------------------------------------------ append
+
+// Where row r goes: its tile's first byte (of head 0) and token in the tile.
+// at < 0: nowhere (-1 padding, -2 outside the table or the cache).
+struct RowPlace {
+    int64_t at;
+    int token;
+};
+
+__device__ __forceinline__ RowPlace row_place(const CacheDev& c, const TableDev& t, const int32_t* seqs,
+                                              const int32_t* positions, int r, int tile_bytes) {
+    const int32_t s = gptr<int32_t>(seqs)[r], p = gptr<int32_t>(positions)[r];
+    if (s < 0) return {-1, 0};
+    if ((uint32_t)s >= t.rows || p < 0) return {-2, 0};
+    const uint32_t pi = (uint32_t)p / c.page_size, in = (uint32_t)p % c.page_size;
+    if (pi >= t.width) return {-2, 0};
+    const uint32_t page = (uint32_t)gptr<int32_t>(t.pages)[(int64_t)s * t.stride + pi];
+    if (page >= c.n_pages) return {-2, 0};
+    return {(int64_t)page * c.page_bytes + (int64_t)(in / kCacheTile) * tile_bytes, (int)(in % kCacheTile)};
+}
+
+constexpr int kRowsThreads = 256;   // workgroup of the append and read kernels: 16 rows of one head
+
+// The quantizer of one group of 32 values in LDS.
+__device__ __forceinline__ uint16_t group_scale_bits(const uint16_t* x, float top) {
+    float m = 0.0f;
+    bool odd = false;
+    for (int i = 0; i < kCacheGroup; ++i) {
+        const float a = __builtin_fabsf((float)__builtin_bit_cast(_Float16, x[i]));
+        odd |= !(a <= 65504.0f);
+        m = __builtin_fmaxf(m, a);
+    }
+    return odd ? (uint16_t)0x7E00u : f32_to_f16_bits(m / top);
+}
+
+template <int B>
+__device__ __forceinline__ uint32_t code_of(uint16_t x, uint16_t s) {
+    constexpr float top = (float)((1 << (B - 1)) - 1);
+    const float f = (float)__builtin_bit_cast(_Float16, x), d = (float)__builtin_bit_cast(_Float16, s);
+    float c = 0.0f;
+    if (d > 0.0f) c = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(f / d), -top), top);   // NaN scale: zero point
+    return (uint32_t)((int)c + (1 << (B - 1)));
+}
+
+// One workgroup: 16 rows of one head.
+template <int D, int KB, int VB>
+__global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableDev t, const uint16_t* __restrict__ k,
+                                                              int64_t k_row, int64_t k_head,
+                                                              const uint16_t* __restrict__ v, int64_t v_row,
+                                                              int64_t v_head, int rows,
+                                                              const int32_t* __restrict__ seqs,
+                                                              const int32_t* __restrict__ positions) {
+    using PK = CachePart<D, KB>;
+    using PV = CachePart<D, VB>;
+    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
+    __shared__ __attribute__((aligned(16))) uint16_t x[2][kCacheTile][D];
+    __shared__ uint16_t scale[2][kCacheTile][G];
+    __shared__ RowPlace place[kCacheTile];
+    const int tid = threadIdx.x, head = blockIdx.x % c.kv_heads, r0 = (int)(blockIdx.x / c.kv_heads) * kCacheTile;
+    if (tid < kCacheTile)
+        place[tid] = r0 + tid < rows ? row_place(c, t, seqs, positions, r0 + tid, TILE) : RowPlace{-1, 0};
+    for (int i = tid; i < 2 * kCacheTile * (D / 8); i += kRowsThreads) {
+        const int part = i / (kCacheTile * (D / 8)), r = i / (D / 8) % kCacheTile, d = i % (D / 8) * 8;
+        u4v w = {0, 0, 0, 0};
+        if (r0 + r < rows) {
+            const uint16_t* src = part ? v + (int64_t)(r0 + r) * v_row + head * v_head : k + (int64_t)(r0 + r) * k_row + head * k_head;
+            w = *gptr<u4v>(src + d);
+        }
+        *reinterpret_cast<u4v*>(&x[part][r][d]) = w;
+    }
+    __syncthreads();
+    for (int i = tid; i < 2 * kCacheTile * G; i += kRowsThreads) {
+        const int part = i / (kCacheTile * G), r = i / G % kCacheTile, g = i % G;
+        const int bits = part ? VB : KB;
+        if (bits < 16)
+            scale[part][r][g] = group_scale_bits(&x[part][r][g * kCacheGroup], (float)((1 << (bits - 1)) - 1));
+    }
+    __syncthreads();
+    uint8_t* head0 = c.pages + (int64_t)head * c.tiles * TILE;
+    // keys: one b-byte unit (8 channels) of one token at a time
+    for (int i = tid; i < kCacheTile * G * 4; i += kRowsThreads) {
+        const int r = i / (G * 4), g = i / 4 % G, q = i % 4;
+        const RowPlace p = place[r];
+        if (p.at < 0) continue;
+        uint8_t* tile = head0 + p.at;
+        uint8_t* dst = tile + PK::unit(16 * q + p.token, g);
+        const uint16_t* src = &x[0][r][g * kCacheGroup + 8 * q];
+        if constexpr (KB == 16) {
+            *gptr_w<u4v>(dst) = *reinterpret_cast<const u4v*>(src);
+        } else {
+            const uint16_t s = scale[0][r][g];
+            uint32_t w[KB / 4] = {};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t code = code_of<KB>(src[e], s);
+                if constexpr (KB == 4) w[0] |= code << (4 * (e / 2) + 16 * (e % 2));
+                else w[e / 4] |= code << (8 * (e % 4));
+            }
+#pragma unroll
+            for (int j = 0; j < KB / 4; ++j) gptr_w<uint32_t>(dst)[j] = w[j];
+            if (q == 0) *gptr_w<uint16_t>(tile + PK::CODES + 2 * (p.token * G + g)) = s;
+        }
+    }
+    // values: the two channels 32 g + c and 32 g + 16 + c of one token at a time
+    for (int i = tid; i < kCacheTile * G * 16; i += kRowsThreads) {
+        const int r = i / (G * 16), g = i / 16 % G, col = i % 16;
+        const RowPlace p = place[r];
+        if (p.at < 0) continue;
+        uint8_t* part = head0 + p.at + PK::BYTES;
+        const int t4 = p.token % 4;
+        uint8_t* dst = part + PV::unit(16 * (p.token / 4) + col, g);
+        const uint16_t a = x[1][r][g * kCacheGroup + col], b = x[1][r][g * kCacheGroup + 16 + col];
+        if constexpr (VB == 16) {
+            gptr_w<uint16_t>(dst)[t4] = a;
+            gptr_w<uint16_t>(dst)[4 + t4] = b;
+        } else {
+            const uint16_t s = scale[1][r][g];
+            const uint32_t ca = code_of<VB>(a, s), cb = code_of<VB>(b, s);
+            if constexpr (VB == 4) {
+                gptr_w<uint8_t>(dst)[2 * (t4 % 2) + t4 / 2] = (uint8_t)(ca | (cb << 4));
+            } else {
+                gptr_w<uint8_t>(dst)[t4] = (uint8_t)ca;
+                gptr_w<uint8_t>(dst)[4 + t4] = (uint8_t)cb;
+            }
+            if (col == 0) *gptr_w<uint16_t>(part + PV::CODES + 8 * G * (p.token / 4) + 8 * g + 2 * t4) = s;
+        }
+    }
+}
+
+// -------------------------------------------------------------------- read
+
+// One workgroup: 16 rows of one head, eight channels a thread at a time.
+template <int D, int KB, int VB>
+__global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, TableDev t, uint16_t* __restrict__ k,
+                                                                  int64_t k_row, int64_t k_head,
+                                                                  uint16_t* __restrict__ v, int64_t v_row,
+                                                                  int64_t v_head, int rows,
+                                                                  const int32_t* __restrict__ seqs,
+                                                                  const int32_t* __restrict__ positions) {
+    using PK = CachePart<D, KB>;
+    using PV = CachePart<D, VB>;
+    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
+    __shared__ RowPlace place[kCacheTile];
+    const int tid = threadIdx.x, head = blockIdx.x % c.kv_heads, r0 = (int)(blockIdx.x / c.kv_heads) * kCacheTile;
+    if (tid < kCacheTile)
+        place[tid] = r0 + tid < rows ? row_place(c, t, seqs, positions, r0 + tid, TILE) : RowPlace{-1, 0};
+    __syncthreads();
+    const uint8_t* head0 = c.pages + (int64_t)head * c.tiles * TILE;
+    for (int i = tid; i < kCacheTile * G * 4; i += kRowsThreads) {
+        const int r = i / (G * 4), g = i / 4 % G, q = i % 4;
+        const RowPlace p = place[r];
+        if (p.at == -1) continue;
+        u4v kw = {0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u}, vw = kw;
+        if (p.at >= 0) {
+            const uint8_t* tile = head0 + p.at;
+            const uint8_t* ku = tile + PK::unit(16 * q + p.token, g);
+            if constexpr (KB == 16) {
+                kw = *gptr<u4v>(ku);
+            } else {
+                const uint32_t s = (uint32_t)*gptr<uint16_t>(tile + PK::CODES + 2 * (p.token * G + g)) * 0x10001u;
+                if constexpr (KB == 4) {
+                    const uint32_t w = *gptr<uint32_t>(ku);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) kw[e] = scaled(nibbles(w >> (4 * e)), kBiasedZero<4>, s);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t w = gptr<uint16_t>(ku)[e];
+                        kw[e] = scaled((w & 0xFFu) | ((w & 0xFF00u) << 8) | 0x64006400u, kBiasedZero<8>, s);
+                    }
+                }
+            }
+            // channels 8 q .. 8 q + 7 of the group: half h = q / 2, c from 8 (q % 2)
+            const uint8_t* part = tile + PK::BYTES;
+            const int t4 = p.token % 4, h = q / 2;
+            uint32_t s = 0;
+            if constexpr (VB < 16)
+                s = (uint32_t)*gptr<uint16_t>(part + PV::CODES + 8 * G * (p.token / 4) + 8 * g + 2 * t4) * 0x10001u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t half[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const uint8_t* vu = part + PV::unit(16 * (p.token / 4) + 8 * (q % 2) + 2 * e + f, g);
+                    if constexpr (VB == 16) half[f] = gptr<uint16_t>(vu)[4 * h + t4];
+                    else if constexpr (VB == 8) half[f] = gptr<uint8_t>(vu)[4 * h + t4];
+                    else half[f] = ((uint32_t)gptr<uint8_t>(vu)[2 * (t4 % 2) + t4 / 2] >> (4 * h)) & 15u;
+                }
+                const uint32_t w = half[0] | (half[1] << 16);
+                if constexpr (VB == 16) vw[e] = w;
+                else vw[e] = scaled(w | 0x64006400u, kBiasedZero<VB>, s);
+            }
+        }
+        const int64_t row = r0 + r;
+        const int d = g * kCacheGroup + 8 * q;
+        *gptr_w<u4v>(k + row * k_row + head * k_head + d) = kw;
+        *gptr_w<u4v>(v + row * v_row + head * v_head + d) = vw;
+    }
+}
+
+// ------------------------------------------------------------------ attend
+
+constexpr int kAttendWaves = 4;
+constexpr int kAttendThreads = 64 * kAttendWaves;
+constexpr int kUnitTokens = 32 * kAttendWaves;   // tokens a workgroup takes in one step: 32 a wave
+constexpr int kAttendMaxWgs = 1024;              // workgroups of a split launch
+constexpr int kWholeUnits = 4;                   // sequences of at most this many units are not split
+
+struct AttendArgs {
+    CacheDev c;
+    TableDev t;
+    const uint16_t* q;
+    int64_t q_row, q_head;
+    uint16_t* out;
+    int64_t out_row, out_head;
+    float* lse;                // may be null
+    const int32_t* lengths;
+    float* ws;
+    float scale;               // scale * log2(e)
+    int window;
+    int rows, q_heads, group;  // group: query heads per key-value head
+    int head_tiles;            // kv_heads * ceil(group / 16): segments of a row
+    uint32_t tile_magic;       // floor(2^32 / tiles per page) + 1
+    bool split;
+};
+
+// Tokens [lo, hi) that row r attends to, and its number of units of
+// kUnitTokens from the one that holds lo.  Rows left alone have no unit;
+// empty rows and rows to be filled with NaN have one without tokens.
+struct RowSpan {
+    int lo, hi, units;
+    bool bad;
+};
+__device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int r) {
+    const int n = gptr<int32_t>(a.lengths)[r];
+    if (n < 0) return {0, 0, 0, false};
+    const uint64_t cap = (uint64_t)a.t.width * a.c.page_size;
+    if (n == 0 || (uint64_t)n > cap) return {0, 0, 1, n != 0};
+    const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
+    return {lo, n, (n - 1) / kUnitTokens - lo / kUnitTokens + 1, false};
+}
+
+// Sum of `v` over the workgroup's threads before this one, and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* lds, int64_t& total) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int64_t s = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up(s, d);
+        if (lane >= d) s += o;
+    }
+    __syncthreads();
+    if (lane == 63) lds[wave] = s;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttendWaves; ++w) {
+        if (w < wave) before += lds[w];
+        total += lds[w];
+    }
+    return before + s - v;
+}
+
+// The units of all rows, and the row that holds unit `u` of them (with the
+// units before it), found by one pass of the workgroup over the lengths.
+struct UnitMap {
+    int64_t total;
+    int row;
+    int64_t before;
+};
+
+// Partial results in the workspace: slot s (two per workgroup) holds group
+// rows of head_dim sums, then the references and the sums of weights.
+__device__ __forceinline__ size_t slot_floats(int heads, int D) { return (size_t)heads * (D + 2); }
+
+template <int D, int B> struct RawPart {
+    static constexpr int WORDS = D / kCacheGroup * B / 4;   // dwords of codes of a lane
+    uint32_t w[WORDS];
+};
+
+template <int D, int B>
+__device__ __forceinline__ void load_codes(RawPart<D, B>& r, const uint8_t* part, int lane) {
+    using P = CachePart<D, B>;
+    static_for<0, P::CHUNKS>([&](auto jc) {
+        constexpr int j = jc, n = (P::G - j * P::GPC < P::GPC ? P::G - j * P::GPC : P::GPC) * B / 4;
+        const uint8_t* src = part + 1024 * j + lane * (4 * n);
+        if constexpr (n == 4) {
+            const u4v v = *gptr<u4v>(src);
+            r.w[4 * j] = v[0]; r.w[4 * j + 1] = v[1]; r.w[4 * j + 2] = v[2]; r.w[4 * j + 3] = v[3];
+        } else if constexpr (n == 2) {
+            const u2v v = *gptr<u2v>(src);
+            r.w[4 * j] = v[0]; r.w[4 * j + 1] = v[1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i) r.w[4 * j + i] = gptr<uint32_t>(src)[i];
+        }
+    });
+}
+
+// WORDS consecutive dwords, in the widest loads their alignment allows (src is
+// aligned to the run's length, to 8 bytes if that is no power of two).
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t (&s)[WORDS], const uint8_t* src) {
+    if constexpr (WORDS % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS / 4; ++i) {
+            const u4v v = gptr<u4v>(src)[i];
+            s[4 * i] = v[0]; s[4 * i + 1] = v[1]; s[4 * i + 2] = v[2]; s[4 * i + 3] = v[3];
+        }
+    } else if constexpr (WORDS % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < WORDS / 2; ++i) {
+            const u2v v = gptr<u2v>(src)[i];
+            s[2 * i] = v[0]; s[2 * i + 1] = v[1];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) s[i] = gptr<uint32_t>(src)[i];
+    }
+}
+
+// A lane's share of a tile, as loaded.
+template <int D, int KB, int VB> struct RawTile {
+    static constexpr int G = D / kCacheGroup;
+    RawPart<D, KB> k;
+    RawPart<D, VB> v;
+    uint32_t ks[(G + 1) / 2];
+    uint32_t vs[2 * G];
+};
+
+template <int D, int KB, int VB>
+__device__ __forceinline__ void load_tile(RawTile<D, KB, VB>& r, const uint8_t* tile, int lane) {
+    using PK = CachePart<D, KB>;
+    using PV = CachePart<D, VB>;
+    constexpr int G = D / kCacheGroup;
+    load_codes<D, KB>(r.k, tile, lane);
+    if constexpr (KB < 16) {
+        const uint8_t* s = tile + PK::CODES + (lane & 15) * (2 * G);
+        if constexpr (G % 2) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint32_t v = gptr<uint16_t>(s)[g];
+                r.ks[g / 2] = g % 2 ? r.ks[g / 2] | (v << 16) : v;
+            }
+        } else {
+            load_words(r.ks, s);
+        }
+    }
+    load_codes<D, VB>(r.v, tile + PK::BYTES, lane);
+    if constexpr (VB < 16) load_words(r.vs, tile + PK::BYTES + PV::CODES + (lane >> 4) * (8 * G));
+}
+
+// Key operand of group g: channels 32 g + 8 q + (0..7) of the lane's token.
+template <int D, int KB, int VB>
+__device__ __forceinline__ h8 key_operand(const RawTile<D, KB, VB>& r, int g) {
+    u4v o;
+    if constexpr (KB == 16) {
+        o = u4v{r.k.w[4 * g], r.k.w[4 * g + 1], r.k.w[4 * g + 2], r.k.w[4 * g + 3]};
+    } else {
+        const uint32_t sw = r.ks[g / 2], s = __builtin_amdgcn_perm(sw, sw, g % 2 ? 0x03020302u : 0x01000100u);
+        if constexpr (KB == 4) {
+            const uint32_t w = r.k.w[g];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = scaled(nibbles(w >> (4 * e)), kBiasedZero<4>, s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t w = r.k.w[2 * g + e / 2];
+                o[e] = scaled(__builtin_amdgcn_perm(w, 0x64006400u, e % 2 ? 0x01070106u : 0x01050104u), kBiasedZero<8>, s);
+            }
+        }
+    }
+    return __builtin_bit_cast(h8, o);
+}
+
+// Value operand words of group g, half h, of one tile: the lane's four tokens
+// of channel 32 g + 16 h + c (two words).
+template <int D, int KB, int VB>
+__device__ __forceinline__ u2v value_words(const RawTile<D, KB, VB>& r, int g, int h) {
+    if constexpr (VB == 16) {
+        return u2v{r.v.w[4 * g + 2 * h], r.v.w[4 * g + 2 * h + 1]};
+    } else if constexpr (VB == 4) {
+        const uint32_t w = r.v.w[g];
+        return u2v{scaled(nibbles(w >> (4 * h)), kBiasedZero<4>, r.vs[2 * g]),
+                   scaled(nibbles(w >> (8 + 4 * h)), kBiasedZero<4>, r.vs[2 * g + 1])};
+    } else {
+        const uint32_t w = r.v.w[2 * g + h];
+        return u2v{scaled(__builtin_amdgcn_perm(w, 0x64006400u, 0x01050104u), kBiasedZero<8>, r.vs[2 * g]),
+                   scaled(__builtin_amdgcn_perm(w, 0x64006400u, 0x01070106u), kBiasedZero<8>, r.vs[2 * g + 1])};
+    }
+}
+
+// Clears what the tokens of a tile outside [lo, hi) contribute to the second
+// product (weights of 0 would still turn a NaN or infinity there into NaN):
+// their scales, or in 16 bits their values.  t0: the lane's first token.
+template <int D, int KB, int VB>
+__device__ __forceinline__ void clear_values(RawTile<D, KB, VB>& r, int t0, int lo, int hi) {
+    constexpr int G = D / kCacheGroup;
+    uint32_t m[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = t0 + 2 * i;
+        m[i] = (t >= lo && t < hi ? 0xFFFFu : 0u) | (t + 1 >= lo && t + 1 < hi ? 0xFFFF0000u : 0u);
+    }
+    if constexpr (VB == 16) {
+#pragma unroll
+        for (int i = 0; i < RawPart<D, VB>::WORDS; ++i) r.v.w[i] &= m[i % 2];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) r.vs[i] &= m[i % 2];
+    }
+}
+
+// Attention of one wave over its tokens: online softmax with the running
+// reference r (log2 domain) of each head (column lane % 16), the lane's share
+// l of the weights' sum, and the output sums o.  Scores are computed
+// transposed (rows: tokens, columns: heads), so the accumulator registers of
+// two tiles are, after the exponential, the lane's operand of the second
+// product as they stand: lane (q, head) holds tokens 4 q .. 4 q + 3 of each.
+template <int D, int KB, int VB> struct AttendWave {
+    static constexpr int G = D / kCacheGroup;
+    h8 q[G];
+    f4 o[2 * G];
+    float r, l;
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) o[i] = f4{0, 0, 0, 0};
+        r = -3e38f;
+        l = 0.0f;
+    }
+
+    // One step: the 32 tokens of two tiles.
+    __device__ __forceinline__ void step(const RawTile<D, KB, VB>& a, const RawTile<D, KB, VB>& b, float c,
+                                         bool partial, int ta, int tb, int lo, int hi) {
+        f4 sa = {0, 0, 0, 0}, sb = {0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < G; ++g) sa = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(a, g), q[g], sa, 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < G; ++g) sb = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(b, g), q[g], sb, 0, 0, 0);
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            t[i] = __builtin_fmaf(sa[i], c, -r);
+            t[4 + i] = __builtin_fmaf(sb[i], c, -r);
+        }
+        if (partial) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (ta + i < lo || ta + i >= hi) t[i] = -__builtin_inff();
+                if (tb + i < lo || tb + i >= hi) t[4 + i] = -__builtin_inff();
+            }
+        }
+        float m = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(t[0], t[1]), __builtin_fmaxf(t[2], t[3])),
+                                  __builtin_fmaxf(__builtin_fmaxf(t[4], t[5]), __builtin_fmaxf(t[6], t[7])));
+        // The reference starts 2^7 below the largest weight seen and moves only
+        // when a weight would pass 2^15: fp16 weights stay finite, and one is
+        // lost to underflow only below 2^-31 of the largest.
+        if (__builtin_amdgcn_ballot_w64(m > 15.0f)) {
+            m = __builtin_fmaxf(m, __shfl_xor(m, 16));
+            m = __builtin_fmaxf(m, __shfl_xor(m, 32));
+            if (m > 15.0f) {
+                // t was taken against the old reference; the scores again, exactly
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (!(partial && (ta + i < lo || ta + i >= hi))) top = __builtin_fmaxf(top, sa[i] * c);
+                    if (!(partial && (tb + i < lo || tb + i >= hi))) top = __builtin_fmaxf(top, sb[i] * c);
+                }
+                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+                const float nr = top - 7.0f, f = __builtin_amdgcn_exp2f(r - nr);
+                r = nr;
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < 2 * G; ++i) o[i] *= f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    t[i] = __builtin_fmaf(sa[i], c, -r);
+                    t[4 + i] = __builtin_fmaf(sb[i], c, -r);
+                    if (partial && (ta + i < lo || ta + i >= hi)) t[i] = -__builtin_inff();
+                    if (partial && (tb + i < lo || tb + i >= hi)) t[4 + i] = -__builtin_inff();
+                }
+            }
+        }
+        h8 p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float e = __builtin_amdgcn_exp2f(t[i]);
+            l += e;
+            p[i] = (_Float16)e;
+        }
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u2v x = value_words(a, g, h), y = value_words(b, g, h);
+                const u4v w = {x[0], x[1], y[0], y[1]};
+                o[2 * g + h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w), p, o[2 * g + h], 0, 0, 0);
+            }
+    }
+};
+
+template <int D, int KB, int VB>
+__global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
+    using PK = CachePart<D, KB>;
+    using PV = CachePart<D, VB>;
+    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
+    __shared__ __attribute__((aligned(16))) float part_o[kAttendWaves][16][D];
+    __shared__ float part_r[kAttendWaves][16], part_l[kAttendWaves][16];
+    __shared__ int64_t scan[kAttendWaves];
+    __shared__ int found_row;
+    __shared__ int64_t found_before;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int quad = lane >> 4, col = lane & 15;
+
+    // This workgroup's units: of one segment (row, kv head, 16 query heads),
+    // or its share of all of them.
+    int row, seg;            // current row and its segment
+    int64_t u, end;          // units of all segments, in order: [u, end)
+    int64_t base = 0;        // first unit of the current segment
+    if (!a.split) {
+        row = (int)(blockIdx.x / (uint32_t)a.head_tiles);
+        seg = (int)(blockIdx.x % (uint32_t)a.head_tiles);
+        u = 0;
+        end = row_span(a, row).units;
+    } else {
+        const int per = (a.rows + kAttendThreads - 1) / kAttendThreads;
+        const int r0 = tid * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
+        int64_t mine = 0, total;
+        for (int r = r0; r < r1; ++r) mine += row_span(a, r).units;
+        const int64_t before = block_scan(mine, scan, total);
+        total *= a.head_tiles;
+        const int64_t wgs = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
+        if ((int64_t)blockIdx.x >= wgs) return;
+        u = (int64_t)blockIdx.x * total / wgs;
+        end = ((int64_t)blockIdx.x + 1) * total / wgs;
+        if (before * a.head_tiles <= u && u < (before + mine) * a.head_tiles) {
+            int64_t b = before;
+            int r = r0;
+            for (;; ++r) {
+                const int n = row_span(a, r).units;
+                if (u < (b + n) * a.head_tiles) break;
+                b += n;
+            }
+            found_row = r;
+            found_before = b;
+        }
+        __syncthreads();
+        row = __builtin_amdgcn_readfirstlane(found_row);
+        const int n = row_span(a, row).units;
+        const int64_t b = found_before * a.head_tiles;
+        seg = (int)((u - b) / n);
+        base = b + (int64_t)seg * n;
+    }
+    bool first = true;
+    AttendWave<D, KB, VB> W;
+    while (u < end) {
+        row = __builtin_amdgcn_readfirstlane(row);
+        seg = __builtin_amdgcn_readfirstlane(seg);
+        RowSpan span = row_span(a, row);
+        if (span.units == 0) {   // a padding row
+            ++row;
+            seg = 0;
+            continue;
+        }
+        const int head_tiles_per_kv = (a.group + 15) / 16;
+        const int kvh = seg / head_tiles_per_kv, h0 = kvh * a.group + seg % head_tiles_per_kv * 16;
+        const int heads = a.group - seg % head_tiles_per_kv * 16 < 16 ? a.group - seg % head_tiles_per_kv * 16 : 16;
+        const int64_t stop = base + span.units < end ? base + span.units : end;
+        // Query operand: channels 32 g + 8 q + (0..7) of head h0 + col.
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            u4v w = {0, 0, 0, 0};
+            if (col < heads)
+                w = *gptr<u4v>(a.q + (int64_t)row * a.q_row + (int64_t)(h0 + col) * a.q_head + g * kCacheGroup + 8 * quad);
+            W.q[g] = __builtin_bit_cast(h8, w);
+        }
+        W.reset();
+        bool bad = span.bad;
+        const int32_t* pages = a.t.pages + (int64_t)row * a.t.stride;
+        const uint8_t* head0 = a.c.pages + (int64_t)kvh * a.c.tiles * TILE;
+        const int first_unit = span.lo / kUnitTokens;
+        auto tile_at = [&](int token) -> const uint8_t* {
+            const uint32_t tile = (uint32_t)token / kCacheTile;
+            uint32_t pi = __umulhi(tile, a.tile_magic);
+            if (a.tile_magic == 0) pi = tile;
+            if (pi * a.c.tiles > tile) --pi;
+            uint32_t page = (uint32_t)gptr<int32_t>(pages)[pi];
+            if (page >= a.c.n_pages) {
+                page = 0;
+                bad = true;
+            }
+            return head0 + (int64_t)page * a.c.page_bytes + (int64_t)(tile - pi * a.c.tiles) * TILE;
+        };
+        for (int64_t i = u - base; i < stop - base; ++i) {
+            const int token = __builtin_amdgcn_readfirstlane((int)(first_unit + i) * kUnitTokens + 32 * wave);
+            // tiles with no token in the span are not read: the page table may end before them
+            const bool ina = token < span.hi && token + 16 > span.lo, inb = token + 16 < span.hi && token + 32 > span.lo;
+            if (!ina && !inb) continue;
+            RawTile<D, KB, VB> x, y;
+            load_tile(x, tile_at(ina ? token : token + 16), lane);
+            load_tile(y, tile_at(inb ? token + 16 : token), lane);
+            const bool partial = token < span.lo || token + 32 > span.hi;
+            if (partial) {
+                clear_values(x, token + 4 * quad, span.lo, span.hi);
+                clear_values(y, token + 16 + 4 * quad, span.lo, span.hi);
+            }
+            W.step(x, y, a.scale, partial, token + 4 * quad, token + 16 + 4 * quad, span.lo, span.hi);
+        }
+        // Join the waves.
+        float l = W.l;
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        if (bad) l = __builtin_nanf("");
+        if (quad == 0) {
+            part_r[wave][col] = W.r;
+            part_l[wave][col] = l;
+        }
+        __syncthreads();
+        float ref = part_r[0][col];
+#pragma unroll
+        for (int w = 1; w < kAttendWaves; ++w) ref = __builtin_fmaxf(ref, part_r[w][col]);
+        const float f = __builtin_amdgcn_exp2f(W.r - ref);
+#pragma unroll
+        for (int i = 0; i < 2 * G; ++i) *reinterpret_cast<f4*>(&part_o[wave][col][16 * i + 4 * quad]) = W.o[i] * f;
+        __syncthreads();
+        const bool whole = u == base && stop == base + span.units;
+        const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
+        const int hp = a.group < 16 ? a.group : 16;
+        float* ws = a.ws + slot * slot_floats(hp, D);
+        for (int i = tid; i < heads * (D / 4); i += kAttendThreads) {
+            const int h = i / (D / 4), d = i % (D / 4) * 4;
+            float top = part_r[0][h], sum = 0.0f;
+#pragma unroll
+            for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, part_r[w][h]);
+            f4 o = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < kAttendWaves; ++w) {
+                sum += part_l[w][h] * __builtin_amdgcn_exp2f(part_r[w][h] - top);
+                o += *reinterpret_cast<const f4*>(&part_o[w][h][d]);
+            }
+            if (whole) {
+                const bool empty = span.hi == 0 && !span.bad;
+                const float inv = empty ? 0.0f : 1.0f / sum;
+                u2v w;
+                w[0] = (uint32_t)f32_to_f16_bits(o[0] * inv) | ((uint32_t)f32_to_f16_bits(o[1] * inv) << 16);
+                w[1] = (uint32_t)f32_to_f16_bits(o[2] * inv) | ((uint32_t)f32_to_f16_bits(o[3] * inv) << 16);
+                *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)(h0 + h) * a.out_head + d) = w;
+                if (d == 0 && a.lse)
+                    gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + h0 + h] =
+                        empty ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+            } else {
+                *gptr_w<f4>(ws + (size_t)h * D + d) = o;
+                if (d == 0) {
+                    ws[(size_t)hp * D + h] = top;
+                    ws[(size_t)hp * (D + 1) + h] = sum;
+                }
+            }
+        }
+        __syncthreads();
+        first = false;
+        u = stop;
+        base += span.units;
+        if (++seg == a.head_tiles) {
+            seg = 0;
+            ++row;
+        }
+    }
+}
+
+// Joins the partial results of segments that several workgroups shared: one
+// workgroup per (row, query head).  Which workgroup of attend_kernel holds
+// which unit follows from the lengths alone.
+template <int D>
+__global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs a, int grid) {
+    __shared__ int64_t scan[kAttendWaves];
+    constexpr int LANES = D / 4, PARTS = kAttendThreads / LANES;
+    __shared__ __attribute__((aligned(16))) f4 red_o[PARTS][LANES];
+    __shared__ float red_l[PARTS];
+    const int tid = threadIdx.x, row = (int)(blockIdx.x / (uint32_t)a.q_heads), head = (int)(blockIdx.x % (uint32_t)a.q_heads);
+    const int per = (a.rows + kAttendThreads - 1) / kAttendThreads;
+    const int r0 = tid * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
+    int64_t all = 0, earlier = 0, total, before;
+    for (int r = r0; r < r1; ++r) {
+        const int n = row_span(a, r).units;
+        all += n;
+        if (r < row) earlier += n;
+    }
+    (void)block_scan(all, scan, total);
+    (void)block_scan(earlier, scan, before);
+    const RowSpan span = row_span(a, row);
+    if (span.units == 0) return;
+    total *= a.head_tiles;
+    const int64_t wgs = total < (int64_t)grid ? total : (int64_t)grid;
+    const int tiles_per_kv = (a.group + 15) / 16, in_group = head % a.group;
+    const int seg = head / a.group * tiles_per_kv + in_group / 16, h = in_group % 16;
+    const int64_t base = before * a.head_tiles + (int64_t)seg * span.units;
+    const int64_t w0 = ((base + 1) * wgs - 1) / total, w1 = ((base + span.units) * wgs - 1) / total;
+    if (w0 == w1) return;   // written whole by one workgroup
+    const int hp = a.group < 16 ? a.group : 16;
+    const size_t floats = slot_floats(hp, D);
+    const int slot0 = w0 * total / wgs == base ? 0 : 1;   // the segment is its first workgroup's first, or its last
+    const int n = (int)(w1 - w0) + 1;
+    auto slot = [&](int i) -> const float* { return a.ws + (2 * (size_t)(w0 + i) + (i == 0 ? slot0 : 0)) * floats; };
+    float top = -3e38f;
+    for (int i = 0; i < n; ++i) top = __builtin_fmaxf(top, slot(i)[(size_t)hp * D + h]);
+    const int part = tid / LANES, d = tid % LANES * 4;
+    f4 o = {0, 0, 0, 0};
+    float l = 0.0f;
+    if (part < PARTS) {
+        for (int i = part; i < n; i += PARTS) {
+            const float* s = slot(i);
+            const float f = __builtin_amdgcn_exp2f(s[(size_t)hp * D + h] - top);
+            l += s[(size_t)hp * (D + 1) + h] * f;
+            o += *gptr<f4>(s + (size_t)h * D + d) * f;
+        }
+        red_o[part][d / 4] = o;
+        if (d == 0) red_l[part] = l;
+    }
+    __syncthreads();
+    if (tid >= LANES) return;
+    o = red_o[0][tid];
+    l = red_l[0];
+    for (int p = 1; p < PARTS; ++p) {
+        o += red_o[p][tid];
+        l += red_l[p];
+    }
+    const float inv = 1.0f / l;
+    u2v w;
+    w[0] = (uint32_t)f32_to_f16_bits(o[0] * inv) | ((uint32_t)f32_to_f16_bits(o[1] * inv) << 16);
+    w[1] = (uint32_t)f32_to_f16_bits(o[2] * inv) | ((uint32_t)f32_to_f16_bits(o[3] * inv) << 16);
+    *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)head * a.out_head + d) = w;
+    if (d == 0 && a.lse)
+        gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + head] = (top + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+}  // namespace exq
+
+// =================================================================== host
+
+using namespace exq;
+
+namespace {
+
+bool cache_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+exq_status check_geometry(int page_size, int kv_heads, int head_dim, int k_bits, int v_bits) {
+    if (page_size < 16 || page_size > 65536 || page_size % 16)
+        return fail(EXQ_ERR_INVALID_ARG, "page_size=%d is not a multiple of 16 in 16..65536", page_size);
+    if (kv_heads < 1 || kv_heads > 65535) return fail(EXQ_ERR_INVALID_ARG, "kv_heads=%d outside 1..65535", kv_heads);
+    if (head_dim < 32 || head_dim % 32) return fail(EXQ_ERR_INVALID_ARG, "head_dim=%d is not a positive multiple of 32", head_dim);
+    if (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256)
+        return fail(EXQ_ERR_UNSUPPORTED, "head_dim=%d (only 64, 96, 128 and 256)", head_dim);
+    const bool ks = k_bits == 4 || k_bits == 8, vs = v_bits == 4 || v_bits == 8;
+    if (!((ks && vs) || (k_bits == 16 && v_bits == 16)))
+        return fail(EXQ_ERR_UNSUPPORTED, "k_bits=%d v_bits=%d (each 4 or 8, or both 16)", k_bits, v_bits);
+    return EXQ_OK;
+}
+
+int row_bytes(int head_dim, int k_bits, int v_bits) {
+    const int scales = 2 * (head_dim / kCacheGroup);
+    return head_dim * k_bits / 8 + head_dim * v_bits / 8 + (k_bits < 16 ? scales : 0) + (v_bits < 16 ? scales : 0);
+}
+
+CacheDev cache_dev(const exq_cache* c) {
+    return CacheDev{c->pages, (int64_t)c->page_bytes, (uint32_t)c->n_pages, (uint32_t)c->page_size, (uint32_t)c->kv_heads,
+                    (uint32_t)(c->page_size / kCacheTile)};
+}
+
+// An fp16 operand of (rows, heads, head_dim) with element strides.
+struct Operand {
+    const char* name;
+    const void* p;
+    int64_t row, head;
+    int rows, heads, dim;
+};
+
+constexpr int64_t kMaxStride = (int64_t)1 << 30;   // elements: with 2^31 rows and heads extents stay inside 64 bits
+
+exq_status check_operand(const Operand& x) {
+    if (!x.p) return fail(EXQ_ERR_INVALID_ARG, "%s is NULL", x.name);
+    if (!cache_aligned(x.p, 16)) return fail(EXQ_ERR_INVALID_ARG, "%s must be 16-byte aligned", x.name);
+    if (x.row < 0 || x.head < 0 || x.row % 8 || x.head % 8 || x.row > kMaxStride || x.head > kMaxStride)
+        return fail(EXQ_ERR_INVALID_ARG, "%s: strides (%lld, %lld) must be multiples of 8 in 0..2^30", x.name,
+                    (long long)x.row, (long long)x.head);
+    return EXQ_OK;
+}
+
+size_t extent(const Operand& x) {   // bytes from its first element to past its last
+    return 2 * ((size_t)(x.rows - 1) * (size_t)x.row + (size_t)(x.heads - 1) * (size_t)x.head + (size_t)x.dim);
+}
+
+bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + nb && b0 < a0 + na;
+}
+
+// Whether no element of x is written twice.
+bool distinct(const Operand& x) {
+    const int64_t rows = x.rows, heads = x.heads, dim = x.dim;
+    const bool rows_outer = (heads == 1 || x.head >= dim) && (rows == 1 || x.row >= (heads - 1) * x.head + dim);
+    const bool heads_outer = (rows == 1 || x.row >= dim) && (heads == 1 || x.head >= (rows - 1) * x.row + dim);
+    return rows_outer || heads_outer;
+}
+
+// Whether two operands may share memory.  Slices of one buffer's rows (equal
+// row strides, disjoint within the row) do not, although their extents meet.
+bool operands_meet(const Operand& a, const Operand& b) {
+    if (!ranges_meet(a.p, extent(a), b.p, extent(b))) return false;
+    if (a.row != b.row || a.row == 0) return true;
+    const int64_t stride = 2 * a.row, na = 2 * ((a.heads - 1) * a.head + a.dim), nb = 2 * ((b.heads - 1) * b.head + b.dim);
+    const int64_t diff = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+    const int64_t at = ((diff % stride) + stride) % stride;   // where b's rows start within a's stride
+    return !(na <= at && at + nb <= stride);
+}
+
+exq_status check_table(const int32_t* table, int rows, int width, int64_t stride) {
+    if (!table || !cache_aligned(table, 4)) return fail(EXQ_ERR_INVALID_ARG, "table is NULL or misaligned");
+    if (rows < 1 || width < 1) return fail(EXQ_ERR_INVALID_ARG, "table of %d x %d", rows, width);
+    if (stride < 0 || stride > kMaxStride || (rows > 1 && stride != 0 && stride < width))
+        return fail(EXQ_ERR_INVALID_ARG, "table_stride=%lld", (long long)stride);
+    return EXQ_OK;
+}
+
+// Calls f(IC<D>, IC<KB>, IC<VB>) for the cache's geometry.
+template <class F>
+void with_geometry(const exq_cache* c, F&& f) {
+    auto bits = [&](auto d) {
+        if (c->k_bits == 16) f(d, IC<16>{}, IC<16>{});
+        else if (c->k_bits == 8 && c->v_bits == 8) f(d, IC<8>{}, IC<8>{});
+        else if (c->k_bits == 8) f(d, IC<8>{}, IC<4>{});
+        else if (c->v_bits == 8) f(d, IC<4>{}, IC<8>{});
+        else f(d, IC<4>{}, IC<4>{});
+    };
+    switch (c->head_dim) {
+        case 64: bits(IC<64>{}); break;
+        case 96: bits(IC<96>{}); break;
+        case 128: bits(IC<128>{}); break;
+        default: bits(IC<256>{}); break;
+    }
+}
+
+exq_status launched(const char* what) {
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess ? EXQ_OK : fail(EXQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& v, int rows, const int32_t* table,
+                           int table_rows, int table_width, int64_t table_stride, const int32_t* seqs,
+                           const int32_t* positions) {
+    if (rows < 0) return fail(EXQ_ERR_INVALID_ARG, "rows=%d", rows);
+    exq_status st;
+    if ((st = check_table(table, table_rows, table_width, table_stride)) != EXQ_OK) return st;
+    if (rows == 0) return EXQ_OK;
+    if ((st = check_operand(k)) != EXQ_OK || (st = check_operand(v)) != EXQ_OK) return st;
+    if (!seqs || !positions || !cache_aligned(seqs, 4) || !cache_aligned(positions, 4))
+        return fail(EXQ_ERR_INVALID_ARG, "seqs or positions is NULL or misaligned");
+    const size_t bytes = (size_t)c->n_pages * c->page_bytes;
+    if (ranges_meet(k.p, extent(k), c->pages, bytes) || ranges_meet(v.p, extent(v), c->pages, bytes))
+        return fail(EXQ_ERR_INVALID_ARG, "k or v overlaps the cache's pages");
+    if (((int64_t)rows + kCacheTile - 1) / kCacheTile * c->kv_heads > 0x7FFFFFFFll)
+        return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, c->kv_heads);
+    return EXQ_OK;
+}
+
+// Sizes of an exq_attend launch.
+struct AttendPlan {
+    int head_tiles, wgs;
+    bool split;
+    size_t ws_bytes;
+};
+
+exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_width, AttendPlan* out) {
+    if (rows < 0) return fail(EXQ_ERR_INVALID_ARG, "rows=%d", rows);
+    if (q_heads < 1 || q_heads % c->kv_heads)
+        return fail(EXQ_ERR_INVALID_ARG, "q_heads=%d is not a positive multiple of kv_heads=%d", q_heads, c->kv_heads);
+    if (table_width < 1) return fail(EXQ_ERR_INVALID_ARG, "table_width=%d", table_width);
+    const int group = q_heads / c->kv_heads;
+    const int64_t tiles = (int64_t)c->kv_heads * ((group + 15) / 16), segments = tiles * rows;
+    if (segments > 0x7FFFFFFFll || (int64_t)rows * q_heads > 0x7FFFFFFFll)
+        return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, q_heads);
+    const int64_t units = ((int64_t)table_width * c->page_size + kUnitTokens - 1) / kUnitTokens;   // of the longest row
+    out->head_tiles = (int)tiles;
+    out->split = units > kWholeUnits;
+    // (a wide table times many rows may pass 64 bits' comfort, hence the early clamp)
+    out->wgs = out->split ? (int)std::min<int64_t>(kAttendMaxWgs, std::min<int64_t>(units, kAttendMaxWgs) * std::max<int64_t>(segments, 1))
+                          : (int)segments;
+    out->ws_bytes = out->split ? 2 * (size_t)out->wgs * 4 * (size_t)std::min(group, 16) * (size_t)(c->head_dim + 2) : 0;
+    return EXQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t exq_cache_page_bytes(int page_size, int kv_heads, int head_dim, int k_bits, int v_bits) {
+    if (check_geometry(page_size, kv_heads, head_dim, k_bits, v_bits) != EXQ_OK) return 0;
+    return (size_t)page_size * kv_heads * row_bytes(head_dim, k_bits, v_bits);
+}
+
+exq_status exq_cache_create(void* pages, int64_t n_pages, int page_size, int kv_heads, int head_dim, int k_bits,
+                            int v_bits, exq_cache_t* out) {
+    if (!out) return fail(EXQ_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    const exq_status st = check_geometry(page_size, kv_heads, head_dim, k_bits, v_bits);
+    if (st != EXQ_OK) return st;
+    if (!pages || !cache_aligned(pages, 16)) return fail(EXQ_ERR_INVALID_ARG, "pages is NULL or not 16-byte aligned");
+    if (n_pages < 1 || n_pages > 0x7FFFFFFFll)
+        return fail(EXQ_ERR_INVALID_ARG, "n_pages=%lld outside 1..2^31-1", (long long)n_pages);
+    exq_cache* c = new (std::nothrow) exq_cache();
+    if (!c) return fail(EXQ_ERR_OOM, "host allocation");
+    *c = exq_cache{static_cast<uint8_t*>(pages), n_pages, page_size, kv_heads, head_dim, k_bits, v_bits,
+                   exq_cache_page_bytes(page_size, kv_heads, head_dim, k_bits, v_bits)};
+    *out = c;
+    return EXQ_OK;
+}
+
+void exq_cache_destroy(exq_cache_t c) { delete c; }
+
+exq_status exq_cache_append(exq_cache_t c, const void* k, int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                            int64_t v_row_stride, int64_t v_head_stride, int rows, const int32_t* table, int table_rows,
+                            int table_width, int64_t table_stride, const int32_t* seqs, const int32_t* positions,
+                            void* stream) {
+    if (!c) return fail(EXQ_ERR_INVALID_ARG, "cache is NULL");
+    const Operand ko{"k", k, k_row_stride, k_head_stride, rows, c->kv_heads, c->head_dim};
+    const Operand vo{"v", v, v_row_stride, v_head_stride, rows, c->kv_heads, c->head_dim};
+    const exq_status st =
+        check_rows_call(c, ko, vo, rows, table, table_rows, table_width, table_stride, seqs, positions);
+    if (st != EXQ_OK || rows == 0) return st;
+    const CacheDev d = cache_dev(c);
+    const TableDev t{table, table_stride, (uint32_t)table_rows, (uint32_t)table_width};
+    const dim3 grid((unsigned)((rows + (int64_t)kCacheTile - 1) / kCacheTile * c->kv_heads));
+    with_geometry(c, [&](auto D, auto KB, auto VB) {
+        hipLaunchKernelGGL((append_kernel<D.value, KB.value, VB.value>), grid, dim3(kRowsThreads), 0,
+                           static_cast<hipStream_t>(stream), d, t, static_cast<const uint16_t*>(k), k_row_stride,
+                           k_head_stride, static_cast<const uint16_t*>(v), v_row_stride, v_head_stride, rows, seqs, positions);
+    });
+    return launched("cache append launch");
+}
+
+exq_status exq_cache_read(exq_cache_t c, void* k, int64_t k_row_stride, int64_t k_head_stride, void* v,
+                          int64_t v_row_stride, int64_t v_head_stride, int rows, const int32_t* table, int table_rows,
+                          int table_width, int64_t table_stride, const int32_t* seqs, const int32_t* positions,
+                          void* stream) {
+    if (!c) return fail(EXQ_ERR_INVALID_ARG, "cache is NULL");
+    const Operand ko{"k", k, k_row_stride, k_head_stride, rows, c->kv_heads, c->head_dim};
+    const Operand vo{"v", v, v_row_stride, v_head_stride, rows, c->kv_heads, c->head_dim};
+    const exq_status st =
+        check_rows_call(c, ko, vo, rows, table, table_rows, table_width, table_stride, seqs, positions);
+    if (st != EXQ_OK || rows == 0) return st;
+    if (!distinct(ko) || !distinct(vo)) return fail(EXQ_ERR_INVALID_ARG, "rows or heads of k or v overlap themselves");
+    if (operands_meet(ko, vo)) return fail(EXQ_ERR_INVALID_ARG, "k and v overlap");
+    const CacheDev d = cache_dev(c);
+    const TableDev t{table, table_stride, (uint32_t)table_rows, (uint32_t)table_width};
+    const dim3 grid((unsigned)((rows + (int64_t)kCacheTile - 1) / kCacheTile * c->kv_heads));
+    with_geometry(c, [&](auto D, auto KB, auto VB) {
+        hipLaunchKernelGGL((cache_read_kernel<D.value, KB.value, VB.value>), grid, dim3(kRowsThreads), 0,
+                           static_cast<hipStream_t>(stream), d, t, static_cast<uint16_t*>(k), k_row_stride, k_head_stride,
+                           static_cast<uint16_t*>(v), v_row_stride, v_head_stride, rows, seqs, positions);
+    });
+    return launched("cache read launch");
+}
+
+size_t exq_attend_workspace_bytes(exq_cache_t c, int rows, int q_heads, int table_width) {
+    AttendPlan p;
+    if (!c) {
+        (void)fail(EXQ_ERR_INVALID_ARG, "cache is NULL");
+        return 0;
+    }
+    return plan_attend(c, rows, q_heads, table_width, &p) == EXQ_OK ? p.ws_bytes : 0;
+}
+
+exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_t q_head_stride, int rows, int q_heads,
+                      const int32_t* table, int table_width, int64_t table_stride, const int32_t* lengths, float scale,
+                      int window, void* out, int64_t out_row_stride, int64_t out_head_stride, float* lse,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    if (!c) return fail(EXQ_ERR_INVALID_ARG, "cache is NULL");
+    AttendPlan p;
+    exq_status st = plan_attend(c, rows, q_heads, table_width, &p);
+    if (st != EXQ_OK) return st;
+    if (!std::isfinite(scale)) return fail(EXQ_ERR_INVALID_ARG, "scale is not finite");
+    if (window < 0) return fail(EXQ_ERR_INVALID_ARG, "window=%d", window);
+    if (rows == 0) return EXQ_OK;
+    if ((st = check_table(table, rows, table_width, table_stride)) != EXQ_OK) return st;
+    const Operand qo{"q", q, q_row_stride, q_head_stride, rows, q_heads, c->head_dim};
+    const Operand oo{"out", out, out_row_stride, out_head_stride, rows, q_heads, c->head_dim};
+    if ((st = check_operand(qo)) != EXQ_OK || (st = check_operand(oo)) != EXQ_OK) return st;
+    if (!lengths || !cache_aligned(lengths, 4) || !cache_aligned(lse, 4))
+        return fail(EXQ_ERR_INVALID_ARG, "lengths is NULL, or lengths or lse misaligned");
+    if (!distinct(oo)) return fail(EXQ_ERR_INVALID_ARG, "rows or heads of out overlap themselves");
+    const size_t bytes = (size_t)c->n_pages * c->page_bytes;
+    if (operands_meet(qo, oo) || ranges_meet(out, extent(oo), c->pages, bytes))
+        return fail(EXQ_ERR_INVALID_ARG, "out overlaps q or the cache's pages");
+    const size_t lse_bytes = lse ? 4 * (size_t)rows * q_heads : 0;
+    if (lse && (ranges_meet(lse, lse_bytes, out, extent(oo)) || ranges_meet(lse, lse_bytes, q, extent(qo)) ||
+                ranges_meet(lse, lse_bytes, c->pages, bytes)))
+        return fail(EXQ_ERR_INVALID_ARG, "lse overlaps q, out or the cache's pages");
+    if (p.ws_bytes) {
+        if (!workspace || !cache_aligned(workspace, 16) || workspace_bytes < p.ws_bytes)
+            return fail(EXQ_ERR_INVALID_ARG, "workspace of %zu bytes: %zu 16-byte aligned ones are needed", workspace_bytes, p.ws_bytes);
+        if (ranges_meet(workspace, p.ws_bytes, out, extent(oo)) || ranges_meet(workspace, p.ws_bytes, q, extent(qo)) ||
+            ranges_meet(workspace, p.ws_bytes, c->pages, bytes) || (lse && ranges_meet(workspace, p.ws_bytes, lse, lse_bytes)))
+            return fail(EXQ_ERR_INVALID_ARG, "workspace overlaps q, out, lse or the cache's pages");
+    }
+    AttendArgs a;
+    a.c = cache_dev(c);
+    a.t = TableDev{table, table_stride, (uint32_t)rows, (uint32_t)table_width};
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_row = q_row_stride;
+    a.q_head = q_head_stride;
+    a.out = static_cast<uint16_t*>(out);
+    a.out_row = out_row_stride;
+    a.out_head = out_head_stride;
+    a.lse = lse;
+    a.lengths = lengths;
+    a.ws = static_cast<float*>(workspace);
+    a.scale = scale * kLog2e;
+    a.window = window;
+    a.rows = rows;
+    a.q_heads = q_heads;
+    a.group = q_heads / c->kv_heads;
+    a.head_tiles = p.head_tiles;
+    a.tile_magic = a.c.tiles == 1 ? 0u : (uint32_t)((1ull << 32) / a.c.tiles + 1);
+    a.split = p.split;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    with_geometry(c, [&](auto D, auto KB, auto VB) {
+        hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value>), dim3((unsigned)p.wgs), dim3(kAttendThreads), 0, s, a);
+        if (p.split)
+            hipLaunchKernelGGL((attend_join_kernel<D.value>), dim3((unsigned)rows * (unsigned)q_heads), dim3(kAttendThreads), 0, s, a, p.wgs);
+    });
+    return launched("attend launch");
+}
+
+}  // extern "C"

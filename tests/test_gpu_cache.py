@@ -1,0 +1,519 @@
+"""The paged key-value cache on the GPU against the plain reference (oracle/cacheref.py): appended bytes and values read
+back bit for bit, attention within the bounds of include/exq.h, and what masks, strides, streams, graphs and bad tables do."""
+import numpy as np
+import pytest
+
+import synth
+from oracle import cacheref as ref
+from tests.gpu_helpers import note, to_dev
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+BITS = [(4, 4), (8, 8), (8, 4), (4, 8), (16, 16)]
+
+
+@pytest.fixture(scope="module")
+def exq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mixed_bitrate_quantized_amd as m
+    return m
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def values(rng, *shape, spread=1.0):
+    x = rng.standard_normal(shape) * np.exp(spread * rng.standard_normal(shape[-2:]))
+    return x.astype(np.float16)
+
+
+class Case:
+    """A cache of sequences with random pages in random order, filled through the reference."""
+
+    def __init__(self, exq, seed, lengths, page, kv_heads, dim, bits, garbage=True, spare=1, spread=1.0):
+        rng = np.random.default_rng(seed)
+        self.rng, self.bits, self.lengths = rng, bits, list(lengths)
+        self.geo = ref.Geometry(page, kv_heads, dim, *bits)
+        width = max(1, -(-max(max(lengths), 1) // page)) + spare
+        n_pages = len(lengths) * width
+        self.table = rng.permutation(n_pages).astype(np.int32).reshape(len(lengths), width)
+        # what lies where nothing was written: for 16-bit values NaN patterns, for scales too
+        self.pages = np.full(n_pages * self.geo.page_bytes, 0xFF if garbage else 0, dtype=np.uint8)
+        self.k, self.v = [], []
+        for s, n in enumerate(lengths):
+            n = max(n, 0)
+            k, v = values(rng, n, kv_heads, dim, spread=spread), values(rng, n, kv_heads, dim, spread=spread)
+            ref.append(self.geo, self.pages, k, v, self.table, [s] * n, range(n))
+            self.k.append(ref.held(k, bits[0]) if n else k)
+            self.v.append(ref.held(v, bits[1]) if n else v)
+        self.dev = to_dev(self.pages)
+        self.cache = exq.KVCache(n_pages, page, kv_heads, dim, *bits, pages=self.dev)
+        self.dtable = i32(self.table)
+
+    def check(self, out, lse, q, scale, window=0, lengths=None, what=""):
+        out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+        worst = 0.0
+        for r, n in enumerate(self.lengths if lengths is None else lengths):
+            if n < 0:
+                continue
+            lo = max(0, n - window) if window else 0
+            o, l, bo, bl = ref.attend(q[r], self.k[r][lo:n], self.v[r][lo:n], scale)
+            if n == 0:
+                assert np.all(out[r] == 0) and np.all(lse[r] == -np.inf), what
+                continue
+            e = np.abs(out[r] - o) / bo
+            f = np.abs(lse[r] - l) / bl
+            assert e.max() <= 1 and f.max() <= 1, "%s row %d (n=%d): out %.3f lse %.3f of the bound" % (what, r, n, e.max(), f.max())
+            worst = max(worst, e.max(), f.max())
+        return worst
+
+
+# ------------------------------------------------------------------ append, read
+
+@pytest.mark.parametrize("bits", BITS, ids=str)
+@pytest.mark.parametrize("dim,kv_heads,page", [(64, 3, 16), (96, 2, 48), (128, 1, 256), (256, 2, 32)])
+def test_append_writes_exactly_the_references_bytes(exq, dim, kv_heads, page, bits):
+    rng = np.random.default_rng(dim + page)
+    geo = ref.Geometry(page, kv_heads, dim, *bits)
+    n_pages, width = 9, 3
+    table = rng.permutation(n_pages).astype(np.int32).reshape(3, width)
+    pages = rng.integers(0, 256, n_pages * geo.page_bytes).astype(np.uint8)
+    # a prompt from inside a tile over a page's end, single tokens, one whole aligned tile, padding
+    spots = [(0, p) for p in range(page - 11, page + 26)] + [(1, 0), (2, 2 * page + 3), (-1, 5)] + [
+        (1, p) for p in range(page, page + 16)] + [(-7, -3)]
+    seqs, pos = np.array([s for s, _ in spots]), np.array([p for _, p in spots])
+    k, v = values(rng, len(spots), kv_heads, dim), values(rng, len(spots), kv_heads, dim)
+    k[3, 0, :32] = 0
+    v[5, 0, 5] = 65504
+    k[7, 0, 33] = np.float16(6e-8)
+    note("append dim=%d page=%d bits=%s" % (dim, page, bits))
+    dev = to_dev(pages)
+    cache = exq.KVCache(n_pages, page, kv_heads, dim, *bits, pages=dev)
+    cache.append(to_dev(k), to_dev(v), i32(table), i32(seqs), i32(pos))
+    want = pages.copy()
+    ref.append(geo, want, k, v, table, seqs, pos)
+    np.testing.assert_array_equal(dev.cpu().numpy(), want)
+    ko, vo = cache.read(i32(table), i32(seqs), i32(pos))
+    live = seqs >= 0
+    np.testing.assert_array_equal(ko.cpu().numpy()[live].view(np.uint16), ref.held(k, bits[0])[live].view(np.uint16))
+    np.testing.assert_array_equal(vo.cpu().numpy()[live].view(np.uint16), ref.held(v, bits[1])[live].view(np.uint16))
+
+
+@pytest.mark.parametrize("bits", [(4, 4), (8, 8), (16, 16)], ids=str)
+def test_aligned_prompt_and_long_read(exq, bits):
+    """Whole tiles in order, from position 0: 2 sequences of 200 and 64 tokens, written in one call and read in two orders."""
+    rng = np.random.default_rng(3)
+    geo = ref.Geometry(64, 2, 128, *bits)
+    table = rng.permutation(8).astype(np.int32).reshape(2, 4)
+    seqs = np.repeat([0, 1], [200, 64])
+    pos = np.concatenate([np.arange(200), np.arange(64)])
+    k, v = values(rng, 264, 2, 128), values(rng, 264, 2, 128)
+    want = np.zeros(8 * geo.page_bytes, dtype=np.uint8)
+    ref.append(geo, want, k, v, table, seqs, pos)
+    note("aligned prompt bits=%s" % (bits,))
+    cache = exq.KVCache(8, 64, 2, 128, *bits)
+    cache.append(to_dev(k), to_dev(v), i32(table), i32(seqs), i32(pos))
+    np.testing.assert_array_equal(cache.pages.cpu().numpy().reshape(-1), want)
+    for order in (np.arange(264), rng.permutation(264), np.concatenate([np.arange(1, 264), [5]])):
+        ko, vo = cache.read(i32(table), i32(seqs[order]), i32(pos[order]))
+        np.testing.assert_array_equal(ko.cpu().numpy(), ref.held(k, bits[0])[order])
+        np.testing.assert_array_equal(vo.cpu().numpy(), ref.held(v, bits[1])[order])
+
+
+@pytest.mark.parametrize("bits", [(4, 8), (16, 16)], ids=str)
+def test_rows_outside_are_skipped_and_read_as_nan(exq, bits):
+    rng = np.random.default_rng(4)
+    geo = ref.Geometry(16, 2, 64, *bits)
+    table = np.array([[1, 7, -1], [0, 2, 1 << 30]], dtype=np.int32)     # 4 pages: 7, -1 and 2^30 are none
+    spots = [(0, 3), (0, 16), (0, 40), (1, 40), (2, 0), (1 << 30, 0), (1, 48), (1, 1 << 30), (1, -1), (1, 20), (-1, 0),
+             (-(1 << 31), 1)]
+    seqs, pos = np.array([s for s, _ in spots]), np.array([p for _, p in spots])
+    k, v = values(rng, len(spots), 2, 64), values(rng, len(spots), 2, 64)
+    pages = rng.integers(0, 256, 4 * geo.page_bytes).astype(np.uint8)
+    want = pages.copy()
+    ref.append(geo, want, k, v, table, seqs, pos)
+    note("rows outside bits=%s" % (bits,))
+    dev = to_dev(pages)
+    cache = exq.KVCache(4, 16, 2, 64, *bits, pages=dev)
+    cache.append(to_dev(k), to_dev(v), i32(table), i32(seqs), i32(pos))
+    np.testing.assert_array_equal(dev.cpu().numpy(), want)
+    ko, vo = (torch.full((len(spots), 2, 64), 7.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    cache.read(i32(table), i32(seqs), i32(pos), ko, vo)
+    ko, vo = ko.cpu().numpy(), vo.cpu().numpy()
+    for r in range(len(spots)):
+        if r in (0, 9):
+            np.testing.assert_array_equal(ko[r], ref.held(k[r], bits[0]))
+            np.testing.assert_array_equal(vo[r], ref.held(v[r], bits[1]))
+        elif seqs[r] < 0:
+            assert np.all(ko[r] == 7) and np.all(vo[r] == 7)
+        else:
+            assert np.all(np.isnan(ko[r])) and np.all(np.isnan(vo[r]))
+
+
+@pytest.mark.parametrize("bits", [(4, 8), (16, 16)], ids=str)
+def test_infinities_and_nan_poison_their_group_only(exq, bits):
+    rng = np.random.default_rng(5)
+    k, v = values(rng, 3, 1, 64), values(rng, 3, 1, 64)
+    k[0, 0, 3], k[1, 0, 40], v[2, 0, 0], v[2, 0, 63] = np.inf, np.nan, -np.inf, np.nan
+    note("non-finite bits=%s" % (bits,))
+    cache = exq.KVCache(1, 16, 1, 64, *bits)
+    t, s, p = i32([[0]]), i32([0, 0, 0]), i32([0, 1, 15])
+    cache.append(to_dev(k), to_dev(v), t, s, p)
+    ko, vo = (x.cpu().numpy() for x in cache.read(t, s, p))
+    np.testing.assert_array_equal(ko, ref.held(k, bits[0]))
+    np.testing.assert_array_equal(vo, ref.held(v, bits[1]))
+
+
+def test_strided_and_broadcast_rows(exq):
+    """k and v as slices of one projection's rows and as [heads][rows] views; one value broadcast to all rows."""
+    rng = np.random.default_rng(6)
+    rows, heads, dim = 21, 2, 64
+    fused = values(rng, rows, 6, dim)                       # [q q | k k | v v]
+    d = to_dev(fused)
+    t, s, p = i32([[1, 0]]), i32([0] * rows), i32(np.arange(rows) + 3)
+    note("strided rows")
+    cache = exq.KVCache(2, 16, heads, dim, 8, 4)
+    cache.append(d[:, 2:4], d[:, 4:6], t, s, p)
+    hold = to_dev(np.zeros((rows, 4, dim), dtype=np.float16))
+    cache.read(t, s, p, hold[:, :2], hold[:, 2:])           # two slices of one buffer
+    h = hold.cpu().numpy()
+    np.testing.assert_array_equal(h[:, :2], ref.held(fused[:, 2:4], 8))
+    np.testing.assert_array_equal(h[:, 2:], ref.held(fused[:, 4:6], 4))
+    turned = to_dev(np.ascontiguousarray(fused[:, 2:4].transpose(1, 0, 2))).transpose(0, 1)
+    one = to_dev(fused[0, 4:6])[None].expand(rows, heads, dim)
+    cache.append(turned, one, t, s, p)
+    ko, vo = (x.cpu().numpy() for x in cache.read(t, s, p))
+    np.testing.assert_array_equal(ko, ref.held(fused[:, 2:4], 8))
+    np.testing.assert_array_equal(vo, np.broadcast_to(ref.held(fused[0, 4:6], 4), vo.shape))
+
+
+# ------------------------------------------------------------------ attend
+
+@pytest.mark.parametrize("bits", BITS, ids=str)
+@pytest.mark.parametrize("dim,kv_heads,group,page", [(64, 2, 1, 16), (96, 2, 7, 48), (128, 2, 8, 256), (256, 1, 16, 32),
+                                                     (128, 1, 20, 64)])
+def test_attend_matches_reference(exq, dim, kv_heads, group, page, bits):
+    lengths = [1, 0, 15, 16, 17, 31, 33, 127, 128, 129, 513, 700]
+    c = Case(exq, dim + group, lengths, page, kv_heads, dim, bits)
+    q = values(c.rng, len(lengths), kv_heads * group, dim, spread=0.5)
+    scale = dim ** -0.5
+    note("attend dim=%d group=%d page=%d bits=%s" % (dim, group, page, bits))
+    out, lse = c.cache.attend(to_dev(q), c.dtable, i32(lengths), scale=scale, return_lse=True)
+    c.check(out, lse, q, scale, what="all rows")
+    # the same rows alone: another split, within the same bounds
+    for r in (0, 4, 11):
+        o, l = c.cache.attend(to_dev(q[r:r + 1]), c.dtable[r:r + 1], i32(lengths[r:r + 1]), return_lse=True)
+        one = Case.__new__(Case)
+        one.k, one.v, one.lengths = [c.k[r]], [c.v[r]], [lengths[r]]
+        one.check(o, l, q[r:r + 1], scale, what="alone")
+
+
+@pytest.mark.parametrize("bits", [(4, 4), (16, 16)], ids=str)
+@pytest.mark.parametrize("window", [1, 16, 100, 129, 400, 1000])
+def test_window(exq, window, bits):
+    lengths = [0, 1, 16, 99, 130, 300, 515]
+    c = Case(exq, window, lengths, 32, 2, 64, bits)
+    q = values(c.rng, len(lengths), 6, 64, spread=0.5)
+    note("window=%d bits=%s" % (window, bits))
+    # pages wholly before the window may have been given away: their entries are no pages
+    t = c.table.copy()
+    for r, n in enumerate(lengths):
+        t[r, :max(0, n - window) // 32] = -1
+        t[r, -(-n // 32):] = 1 << 30
+    out, lse = c.cache.attend(to_dev(q), i32(t), i32(lengths), scale=0.2, window=window, return_lse=True)
+    c.check(out, lse, q, 0.2, window, what="window %d" % window)
+
+
+def test_long_sequence_split_and_ragged_batch(exq):
+    """One long sequence over many workgroups, beside short ones: 9000, 40, 0 and 2500 tokens."""
+    lengths = [9000, 40, 0, 2500]
+    c = Case(exq, 9, lengths, 256, 1, 64, (8, 4), spread=0.5)
+    q = values(c.rng, 4, 4, 64, spread=0.5)
+    note("long ragged")
+    out, lse = c.cache.attend(to_dev(q), c.dtable, i32(lengths), scale=0.125, return_lse=True)
+    c.check(out, lse, q, 0.125)
+    again, _ = c.cache.attend(to_dev(q), c.dtable, i32(lengths), scale=0.125, return_lse=True)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("bits", [(4, 4), (16, 16)], ids=str)
+def test_sharp_and_rising_scores(exq, bits):
+    """Scores that rise by far more than the reference's slack along the sequence, fall, and are all but one negligible."""
+    n, dim = 700, 64
+    for kind in ("rising", "falling", "spike"):
+        c = Case(exq, 10, [n], 64, 1, dim, bits)
+        ramp = {"rising": np.linspace(-40, 40, n), "falling": np.linspace(40, -40, n),
+                "spike": np.where(np.arange(n) == 345, 60, -20)}[kind]
+        k = np.ones((n, 1, dim)) * ramp[:, None, None] / 8
+        k[:, 0, ::2] *= 0.5
+        k = k.astype(np.float16)
+        v = values(c.rng, n, 1, dim)
+        ref.append(c.geo, c.pages, k, v, c.table, [0] * n, range(n))
+        c.k, c.v = [ref.held(k, bits[0])], [ref.held(v, bits[1])]
+        c.cache.pages.copy_(to_dev(c.pages))
+        q = np.ones((1, 2, dim), dtype=np.float16)
+        q[0, 1] = -1
+        note("%s bits=%s" % (kind, bits))
+        for scale in (0.125, 1.0, -0.5, 0.0):
+            out, lse = c.cache.attend(to_dev(q), c.dtable, i32([n]), scale=scale, return_lse=True)
+            c.check(out, lse, q, scale, what="%s scale %g" % (kind, scale))
+
+
+def test_padding_rows_bad_pages_and_too_long_rows(exq):
+    lengths = [40, -1, 33, 40, -(1 << 31), 200]
+    for page, width_note in ((16, "split"), (48, "whole")):
+        c = Case(exq, 12, [40, 40, 40, 40, 40, 40], page, 2, 64, (4, 4), spare=0 if page == 48 else 30)
+        t = c.table.copy()
+        t[3, 0] = c.cache.n_pages                 # read: not a page
+        t[2, -(-33 // page):] = -5                # behind the end: never looked at
+        n = [x if x != 200 else t.shape[1] * page + 1 for x in lengths]
+        q = values(c.rng, 6, 4, 64)
+        out = torch.full((6, 4, 64), 3.0, dtype=torch.float16, device="cuda")
+        lse = torch.full((6, 4), 3.0, dtype=torch.float32, device="cuda")
+        note("padding and bad pages, %s" % width_note)
+        c.cache.attend(to_dev(q), i32(t), i32(n), out=out, lse=lse)
+        assert torch.all(out[[1, 4]] == 3) and torch.all(lse[[1, 4]] == 3)
+        assert torch.all(torch.isnan(out[[3, 5]])) and torch.all(torch.isnan(lse[[3, 5]]))
+        c.check(out, lse, q, 0.125, lengths=[40, -1, 33, -1, -1, -1])
+
+
+def test_only_padding_and_empty_rows(exq):
+    c = Case(exq, 13, [5, 5, 5], 256, 1, 64, (8, 8), spare=4)
+    q = to_dev(values(c.rng, 3, 1, 64))
+    for n in ([-1, -1, -1], [0, 0, 0], [-1, 0, -1], [0, 3, -1]):
+        out = torch.full((3, 1, 64), 3.0, dtype=torch.float16, device="cuda")
+        note("lengths %s" % n)
+        c.cache.attend(q, c.dtable, i32(n), out=out)
+        for r in range(3):
+            if n[r] < 0:
+                assert torch.all(out[r] == 3)
+            elif n[r] == 0:
+                assert torch.all(out[r] == 0)
+            else:
+                assert torch.all(torch.isfinite(out[r])) and torch.any(out[r] != 0)
+
+
+@pytest.mark.parametrize("bits", [(4, 4), (16, 16)], ids=str)
+def test_infinite_and_nan_values_that_are_attended_to_show(exq, bits):
+    """A NaN in a key makes its row NaN; a NaN in one group of a value only that group; other rows and heads stay."""
+    n = 150
+    c = Case(exq, 14, [n, n], 64, 2, 64, bits, spare=8)
+    k, v = values(c.rng, n, 2, 64), values(c.rng, n, 2, 64)
+    k[77, 0, 5] = np.nan
+    v[140, 1, 40] = np.nan
+    ref.append(c.geo, c.pages, k, v, c.table, [0] * n, range(n))
+    c.cache.pages.copy_(to_dev(c.pages))
+    q = values(c.rng, 2, 4, 64)
+    note("attended NaN bits=%s" % (bits,))
+    out, lse = c.cache.attend(to_dev(q), c.dtable, i32([n, n]), return_lse=True)
+    o = out.cpu().numpy()
+    assert np.all(np.isnan(o[0, :2])) and np.all(torch.isnan(lse[0, :2]).cpu().numpy())
+    bad = slice(32, 64) if bits[1] < 16 else slice(40, 41)
+    assert np.all(np.isnan(o[0, 2:, bad]))
+    rest = np.ones(64, bool)
+    rest[bad] = False
+    assert np.all(np.isfinite(o[0, 2:][:, rest])) and np.all(np.isfinite(o[1]))
+
+
+def test_many_rows_and_heads(exq):
+    """More rows than a workgroup has threads, in both split and whole launches."""
+    for spare in (0, 40):
+        c = Case(exq, 15, [3 + r % 29 for r in range(300)], 16, 1, 64, (4, 4), spare=spare)
+        q = values(c.rng, 300, 2, 64)
+        note("300 rows, spare %d" % spare)
+        out, lse = c.cache.attend(to_dev(q), c.dtable, i32(c.lengths), return_lse=True)
+        c.check(out, lse, q, 0.125)
+
+
+def test_strided_queries_and_outputs(exq):
+    lengths = [70, 5, 260]
+    c = Case(exq, 16, lengths, 32, 2, 64, (8, 8), spare=20)
+    fused = values(c.rng, 3, 12, 64)                        # [4 query heads | something | 4 output heads]
+    d = to_dev(fused)
+    note("strided attend")
+    lse = torch.empty((3, 4), dtype=torch.float32, device="cuda")
+    c.cache.attend(d[:, :4], c.dtable, i32(lengths), out=d[:, 8:], lse=lse)
+    c.check(d[:, 8:], lse, fused[:, :4], 0.125)
+    np.testing.assert_array_equal(d[:, :8].cpu().numpy(), fused[:, :8])
+    wide = i32(np.concatenate([c.table, np.full_like(c.table, 1 << 30)], 1))[:, :c.table.shape[1]]
+    plain, lse = c.cache.attend(d[:, :4].contiguous(), wide, i32(lengths), return_lse=True)
+    assert torch.equal(plain, d[:, 8:])
+    turned = torch.zeros((4, 3, 64), dtype=torch.float16, device="cuda").transpose(0, 1)
+    c.cache.attend(d[:, :4], c.dtable, i32(lengths), out=turned)
+    assert torch.equal(turned, plain)
+    same = to_dev(fused[0, :4])[None].expand(3, 4, 64)
+    o, l = c.cache.attend(same, c.dtable, i32(lengths), return_lse=True)
+    c.check(o, l, np.broadcast_to(fused[0, :4], (3, 4, 64)), 0.125)
+
+
+def test_pages_beyond_32_bit_offsets(exq):
+    """A cache of over 8 GiB whose used pages lie at its very end."""
+    page, heads, dim, bits = 256, 8, 256, (16, 16)
+    geo = ref.Geometry(page, heads, dim, *bits)
+    n_pages = (9 << 30) // geo.page_bytes
+    cache = exq.KVCache(n_pages, page, heads, dim, *bits, pages=torch.empty(n_pages * geo.page_bytes, dtype=torch.uint8, device="cuda"))
+    rng = np.random.default_rng(17)
+    n = 300
+    k, v = values(rng, n, heads, dim, spread=0.3), values(rng, n, heads, dim, spread=0.3)
+    t = i32([[n_pages - 1, n_pages - 2]])
+    note("9 GiB of pages")
+    cache.append(to_dev(k), to_dev(v), t, i32([0] * n), i32(np.arange(n)))
+    ko, vo = cache.read(t, i32([0] * n), i32(np.arange(n)))
+    np.testing.assert_array_equal(ko.cpu().numpy(), k)
+    np.testing.assert_array_equal(vo.cpu().numpy(), v)
+    q = values(rng, 1, heads, dim, spread=0.3)
+    one = Case.__new__(Case)
+    one.k, one.v, one.lengths = [k], [v], [n]
+    out, lse = cache.attend(to_dev(q), t, i32([n]), return_lse=True)
+    one.check(out, lse, q, dim ** -0.5)
+
+
+# ------------------------------------------------- streams, graphs, guard bands, together
+
+def test_guard_bands(exq):
+    c = Case(exq, 18, [37, 600], 64, 2, 96, (4, 8))
+    q = to_dev(values(c.rng, 2, 6, 96))
+    note("guard bands")
+    buf = torch.full((2 * 6 * 96 + 128,), 9.0, dtype=torch.float16, device="cuda")
+    lbuf = torch.full((2 * 6 + 64,), 9.0, dtype=torch.float32, device="cuda")
+    need = exq.exq_attend_workspace_bytes(c.cache.handle, 2, 6, c.dtable.shape[1])
+    ws = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+    out, lse = buf[64:-64].view(2, 6, 96), lbuf[32:-32].view(2, 6)
+    c.cache.attend(q, c.dtable, i32([37, 600]), out=out, lse=lse, workspace=ws[256:256 + need])
+    c.check(out, lse, q.cpu().numpy(), 96 ** -0.5)
+    assert torch.all(buf[:64] == 9) and torch.all(buf[-64:] == 9) and torch.all(lbuf[:32] == 9) and torch.all(lbuf[-32:] == 9)
+    assert torch.all(ws[:256] == 77) and torch.all(ws[-256:] == 77)
+    np.testing.assert_array_equal(c.cache.pages.cpu().numpy().reshape(-1), c.pages)
+
+
+def test_other_streams_at_once(exq):
+    c = Case(exq, 19, [1500, 700, 20], 64, 2, 64, (4, 4))
+    qs = [values(c.rng, 3, 4, 64) for _ in range(4)]
+    dq, n = [to_dev(q) for q in qs], i32(c.lengths)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    note("four streams")
+    got = [c.cache.attend(dq[i], c.dtable, n, return_lse=True, stream=streams[i]) for i in range(4)]
+    raw = c.cache.attend(dq[0], c.dtable, n, return_lse=True, stream=streams[1].cuda_stream)
+    torch.cuda.synchronize()
+    for i in range(4):
+        c.check(*got[i], qs[i], 0.125)
+    assert torch.equal(raw[0], got[0][0])
+
+
+def test_graphs_replay_append_and_attend(exq):
+    """Two captured graphs of one decoding step each, replayed several times with eager calls between: new tokens written,
+    then attended to.  Lengths, tables and inputs are read at replay."""
+    lengths = [700, 3, 120, 0]
+    c = Case(exq, 20, lengths, 64, 2, 64, (8, 4), spare=2)
+    rng = c.rng
+    q, k, v = (torch.zeros((4, h, 64), dtype=torch.float16, device="cuda") for h in (6, 2, 2))
+    seqs, pos, n = i32(np.arange(4)), i32([0] * 4), i32([0] * 4)
+
+    def step():
+        c.cache.append(k, v, c.dtable, seqs, pos)
+        return c.cache.attend(q, c.dtable, n, return_lse=True)
+
+    pos.copy_(i32(lengths))
+    note("graph capture")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = step()
+        graphs.append((g, res))
+    held = [list(x) for x in zip(c.k, c.v)]
+    now = list(lengths)
+    for rep in range(6):
+        g, (out, lse) = graphs[rep % 2]
+        hq, hk, hv = values(rng, 4, 6, 64), values(rng, 4, 2, 64), values(rng, 4, 2, 64)
+        q.copy_(to_dev(hq)); k.copy_(to_dev(hk)); v.copy_(to_dev(hv))
+        pos.copy_(i32(now))
+        now = [x + 1 for x in now]
+        n.copy_(i32(now))
+        g.replay()
+        torch.cuda.synchronize()
+        for s in range(4):
+            held[s][0] = np.concatenate([held[s][0], ref.held(hk[s:s + 1], 8)])
+            held[s][1] = np.concatenate([held[s][1], ref.held(hv[s:s + 1], 4)])
+        c.k, c.v = [h[0] for h in held], [h[1] for h in held]
+        c.check(out, lse, hq, 0.125, lengths=now, what="replay %d" % rep)
+        eager, elog = c.cache.attend(q, c.dtable, n, return_lse=True)
+        assert torch.equal(eager, out) and torch.equal(elog, lse)
+
+
+def test_a_block_decodes_through_its_cache(exq):
+    """The cache between a block's linears, as a decoding loop runs it: q/k/v in one plan, append, attend, output linear.
+    Every step's attention is checked against the reference on the values the plan gave."""
+    heads, kv_heads, dim, K, M, steps = 8, 2, 64, 512, 3, 20
+    widths = [2, 4, 6, 8]
+    mk = lambda tag, N: exq.Layer.from_weight(synth.weight(synth.seed_for("block", tag), N, K), widths)
+    lq, lk, lv, lo = mk("q", heads * dim), mk("k", kv_heads * dim), mk("v", kv_heads * dim), mk("o", K)
+    x = torch.empty((M, K), dtype=torch.float16, device="cuda")
+    yq, yk, yv = (torch.empty((M, h * dim), dtype=torch.float16, device="cuda") for h in (heads, kv_heads, kv_heads))
+    plan = exq.Plan([lq, lk, lv], [x, x, x], [yq, yk, yv], M)
+    cache = exq.KVCache(M * 2, 16, kv_heads, dim, 4, 4)
+    table = i32(np.arange(2 * M).reshape(M, 2)[:, ::-1].copy())
+    seqs = i32(np.arange(M))
+    ks, vs = [], []
+    note("block decode")
+    for t in range(steps):
+        x.copy_(to_dev(synth.activations(synth.seed_for("block-x", t), M, K)))
+        plan.run()
+        cache.append(yk.view(M, kv_heads, dim), yv.view(M, kv_heads, dim), table, seqs, i32([t] * M))
+        out, lse = cache.attend(yq.view(M, heads, dim), table, i32([t + 1] * M), return_lse=True)
+        y = lo.gemm(out.view(M, heads * dim))
+        torch.cuda.synchronize()
+        ks.append(ref.held(yk.cpu().numpy().reshape(M, kv_heads, dim), 4))
+        vs.append(ref.held(yv.cpu().numpy().reshape(M, kv_heads, dim), 4))
+        one = Case.__new__(Case)
+        one.k, one.v = list(np.stack(ks, 1)), list(np.stack(vs, 1))
+        one.lengths = [t + 1] * M
+        one.check(out, lse, yq.cpu().numpy().reshape(M, heads, dim), dim ** -0.5, what="step %d" % t)
+        assert y.shape == (M, K) and torch.all(torch.isfinite(y))
+    for l in (lq, lk, lv, lo):
+        l.close()
+
+
+def test_binding_checks_tensors(exq):
+    c = Case(exq, 21, [5, 5], 16, 2, 64, (4, 4))
+    q = to_dev(values(c.rng, 2, 4, 64))
+    n = i32([5, 5])
+    k = to_dev(values(c.rng, 2, 2, 64))
+    s, p = i32([0, 1]), i32([5, 5])
+    bad = [
+        lambda: c.cache.attend(q.float(), c.dtable, n), lambda: c.cache.attend(q.cpu(), c.dtable, n),
+        lambda: c.cache.attend(q[:, :3], c.dtable, n), lambda: c.cache.attend(q[:, :, ::2], c.dtable, n),
+        lambda: c.cache.attend(q, c.dtable.long(), n), lambda: c.cache.attend(q, c.dtable[:1], n),
+        lambda: c.cache.attend(q, c.dtable, n.long()), lambda: c.cache.attend(q, c.dtable, n[:1]),
+        lambda: c.cache.attend(q, c.dtable, n, out=q), lambda: c.cache.attend(q, c.dtable, n, window=-1),
+        lambda: c.cache.attend(q, c.dtable, n, scale=float("nan")),
+        lambda: c.cache.attend(q, c.dtable, n, lse=torch.zeros((2, 3), device="cuda")),
+        lambda: c.cache.append(k, k[:1], c.dtable, s, p), lambda: c.cache.append(k, k, c.dtable, s, p.long()),
+        lambda: c.cache.append(k, k.bfloat16(), c.dtable, s, p), lambda: c.cache.append(k, k, c.dtable.T, s, p),
+        lambda: c.cache.read(c.dtable, s, p, k, k), lambda: c.cache.read(c.dtable, s, p, k[:1], None),
+    ]
+    before = c.cache.pages.clone()
+    note("binding checks")
+    for i, f in enumerate(bad):
+        with pytest.raises(exq.ExqError) as ei:
+            f()
+        assert ei.value.status == exq.EXQ_ERR_INVALID_ARG, i
+    assert torch.equal(before, c.cache.pages)
+    e = torch.empty((0, 4, 64), dtype=torch.float16, device="cuda")
+    assert c.cache.attend(e, c.dtable[:0], n[:0]).shape == (0, 4, 64)
+    c.cache.append(e[:, :2], e[:, :2], c.dtable, s[:0], p[:0])
+    assert c.cache.read(c.dtable, s[:0], p[:0])[0].shape == (0, 2, 64)
+    c.cache.close()
+    with pytest.raises(exq.ExqError):
+        c.cache.attend(q, c.dtable, n)
