@@ -371,7 +371,8 @@ size_t exq_cache_page_bytes(int page_size, int kv_heads, int head_dim, int k_bit
 /* Describe a cache.
  *   pages      device, 16-byte aligned, n_pages * exq_cache_page_bytes() bytes
  *              (borrowed: must outlive the handle); any content
- *   n_pages    1 .. 2^31 - 1
+ *   n_pages    1 .. 2^31 - 1 (n_pages * kv_heads * page_size / 16 below 2^32, else
+ *              UNSUPPORTED)
  *   page_size  tokens, a multiple of 16, 16 .. 65536
  *   kv_heads   1 .. 65535
  *   head_dim   64, 96, 128 or 256 (another multiple of 32: UNSUPPORTED)

@@ -72,6 +72,31 @@ template <int B> constexpr uint32_t kBiasedZero = B == 4 ? 0x64086408u : 0x64806
 
 __device__ __forceinline__ uint32_t nibbles(uint32_t w) { return (w & 0x000F000Fu) | 0x64006400u; }
 
+// Constants of the 4-bit decoding in registers.  The compiler is not shown
+// their values: it would rather write a mask and the 0x6400 as literals of two
+// instructions than as registers of one v_and_or_b32.
+struct Nibbles {
+    uint32_t even, odd, one;
+    __device__ __forceinline__ void init() {
+        even = 0x000F000Fu;
+        odd = 0x00F000F0u;
+        one = 0x64006400u;
+        asm volatile("" : "+v"(even), "+v"(odd), "+s"(one));
+    }
+    // The pair of codes at bits 4 e and 4 e + 16 of w, less 8, exactly: at bit
+    // 0 it reads 1024 + c, at bit 4 1024 + 16 c, and one shift by 8 serves the
+    // other two.
+    template <int E> __device__ __forceinline__ h2 pair(uint32_t w) const {
+        const uint32_t x = E >= 2 ? w >> 8 : w;
+        if constexpr (E % 2 == 0) {
+            return as_h2((x & even) | one) - h2{1032, 1032};
+        } else {
+            const h2 sixteenth = {0.0625f, 0.0625f}, zero = {-72, -72};
+            return __builtin_elementwise_fma(as_h2((x & odd) | one), sixteenth, zero);
+        }
+    }
+};
+
 // ------------------------------------------------------------------ append
 
 // Where row r goes: its tile's first byte (of head 0) and token in the tile.
@@ -314,129 +339,146 @@ __device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int r) {
     return {lo, n, (n - 1) / kUnitTokens - lo / kUnitTokens + 1, false};
 }
 
-// Sum of `v` over the workgroup's threads before this one, and the total.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* lds, int64_t& total) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int64_t s = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(s, d);
-        if (lane >= d) s += o;
-    }
-    __syncthreads();
-    if (lane == 63) lds[wave] = s;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttendWaves; ++w) {
-        if (w < wave) before += lds[w];
-        total += lds[w];
-    }
-    return before + s - v;
+// A value equal in all lanes, in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// The units of all rows, and the row that holds unit `u` of them (with the
-// units before it), found by one pass of the workgroup over the lengths.
-struct UnitMap {
-    int64_t total;
-    int row;
-    int64_t before;
-};
+// a / b, a >= 0 and b > 0, uniform: the 64-bit division only where 32 bits do not do.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Units of rows [0, n), by one wave: 64 rows at a time.
+__device__ __forceinline__ int64_t units_before(const AttendArgs& a, int n) {
+    int64_t total = 0;
+    for (int r0 = 0; r0 < n; r0 += 64) {
+        const int r = r0 + (int)(threadIdx.x & 63);
+        int v = r < n ? row_span(a, r).units : 0;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+        total += uniform(v);
+    }
+    return total;
+}
+
+// The row that holds unit `u` of all rows' (u in units of rows, not of
+// segments), and the units before it.
+__device__ __forceinline__ int row_of_unit(const AttendArgs& a, int64_t u, int64_t& before) {
+    before = 0;
+    for (int r0 = 0;; r0 += 64) {
+        const int lane = (int)(threadIdx.x & 63), r = r0 + lane;
+        const int mine = r < a.rows ? row_span(a, r).units : 0;
+        int v = mine;   // inclusive prefix sum over the lanes
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(v, d);
+            if (lane >= d) v += o;
+        }
+        const int sum = __builtin_amdgcn_readlane(v, 63);
+        if (u < before + sum) {
+            const int at = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before + v <= u));   // rows that end at or before u
+            before += __builtin_amdgcn_readlane(v - mine, at);
+            return r0 + at;
+        }
+        before += sum;
+    }
+}
+
+// Shares of a split launch: workgroup w of `grid` takes units [w c, (w + 1) c)
+// of all segments, c = ceil(total / grid).
+__device__ __forceinline__ int64_t share_of(int64_t total, int grid) { return divide(total + grid - 1, grid); }
 
 // Partial results in the workspace: slot s (two per workgroup) holds group
 // rows of head_dim sums, then the references and the sums of weights.
 __device__ __forceinline__ size_t slot_floats(int heads, int D) { return (size_t)heads * (D + 2); }
 
+// Reads go through one buffer descriptor a tile: its address in scalar
+// registers, a lane's place as a 32-bit offset from a compile-time start.
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t* dst, __amdgpu_buffer_rsrc_t tile, int at, int start) {
+    if constexpr (WORDS >= 4) {
+        const u4v v = __builtin_amdgcn_raw_buffer_load_b128(tile, at, start, 0);
+        dst[0] = v[0]; dst[1] = v[1]; dst[2] = v[2]; dst[3] = v[3];
+        load_words<WORDS - 4>(dst + 4, tile, at, start + 16);
+    } else if constexpr (WORDS == 3) {
+        typedef uint32_t u3v __attribute__((ext_vector_type(3)));
+        const u3v v = __builtin_amdgcn_raw_buffer_load_b96(tile, at, start, 0);
+        dst[0] = v[0]; dst[1] = v[1]; dst[2] = v[2];
+    } else if constexpr (WORDS == 2) {
+        const u2v v = __builtin_amdgcn_raw_buffer_load_b64(tile, at, start, 0);
+        dst[0] = v[0]; dst[1] = v[1];
+    } else if constexpr (WORDS == 1) {
+        dst[0] = __builtin_amdgcn_raw_buffer_load_b32(tile, at, start, 0);
+    }
+}
+
+// A lane's share of the codes of a tile's keys or values, from byte `start` of it.
 template <int D, int B> struct RawPart {
-    static constexpr int WORDS = D / kCacheGroup * B / 4;   // dwords of codes of a lane
+    static constexpr int WORDS = D / kCacheGroup * B / 4;
     uint32_t w[WORDS];
 };
 
 template <int D, int B>
-__device__ __forceinline__ void load_codes(RawPart<D, B>& r, const uint8_t* part, int lane) {
+__device__ __forceinline__ void load_codes(RawPart<D, B>& r, __amdgpu_buffer_rsrc_t tile, int start, int lane) {
     using P = CachePart<D, B>;
     static_for<0, P::CHUNKS>([&](auto jc) {
         constexpr int j = jc, n = (P::G - j * P::GPC < P::GPC ? P::G - j * P::GPC : P::GPC) * B / 4;
-        const uint8_t* src = part + 1024 * j + lane * (4 * n);
-        if constexpr (n == 4) {
-            const u4v v = *gptr<u4v>(src);
-            r.w[4 * j] = v[0]; r.w[4 * j + 1] = v[1]; r.w[4 * j + 2] = v[2]; r.w[4 * j + 3] = v[3];
-        } else if constexpr (n == 2) {
-            const u2v v = *gptr<u2v>(src);
-            r.w[4 * j] = v[0]; r.w[4 * j + 1] = v[1];
-        } else {
-#pragma unroll
-            for (int i = 0; i < n; ++i) r.w[4 * j + i] = gptr<uint32_t>(src)[i];
-        }
+        load_words<n>(r.w + 4 * j, tile, lane * (4 * n), start + 1024 * j);
     });
 }
 
-// WORDS consecutive dwords, in the widest loads their alignment allows (src is
-// aligned to the run's length, to 8 bytes if that is no power of two).
-template <int WORDS>
-__device__ __forceinline__ void load_words(uint32_t (&s)[WORDS], const uint8_t* src) {
-    if constexpr (WORDS % 4 == 0) {
+// A lane's share of a tile's keys or values, as loaded: codes, and the scales
+// of its token (keys) or of [G][its 4 tokens] (values).
+template <int D, int B> struct RawKeys {
+    RawPart<D, B> k;
+    uint32_t s[(D / kCacheGroup + 1) / 2];
+};
+template <int D, int B> struct RawValues {
+    RawPart<D, B> v;
+    uint32_t s[2 * (D / kCacheGroup)];
+};
+
+template <int D, int B>
+__device__ __forceinline__ void load_keys(RawKeys<D, B>& r, __amdgpu_buffer_rsrc_t tile, int lane) {
+    constexpr int G = D / kCacheGroup, S = CachePart<D, B>::CODES;
+    load_codes<D, B>(r.k, tile, 0, lane);
+    if constexpr (B < 16) {
+        const int at = (lane & 15) * (2 * G);
+        if constexpr (G % 2) {   // a token's scales start at an even half: by halves
 #pragma unroll
-        for (int i = 0; i < WORDS / 4; ++i) {
-            const u4v v = gptr<u4v>(src)[i];
-            s[4 * i] = v[0]; s[4 * i + 1] = v[1]; s[4 * i + 2] = v[2]; s[4 * i + 3] = v[3];
+            for (int g = 0; g < G; ++g) {
+                const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(tile, at, S + 2 * g, 0);
+                r.s[g / 2] = g % 2 ? r.s[g / 2] | (v << 16) : v;
+            }
+        } else {
+            load_words<G / 2>(r.s, tile, at, S);
         }
-    } else if constexpr (WORDS % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i < WORDS / 2; ++i) {
-            const u2v v = gptr<u2v>(src)[i];
-            s[2 * i] = v[0]; s[2 * i + 1] = v[1];
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) s[i] = gptr<uint32_t>(src)[i];
     }
 }
 
-// A lane's share of a tile, as loaded.
-template <int D, int KB, int VB> struct RawTile {
-    static constexpr int G = D / kCacheGroup;
-    RawPart<D, KB> k;
-    RawPart<D, VB> v;
-    uint32_t ks[(G + 1) / 2];
-    uint32_t vs[2 * G];
-};
-
-template <int D, int KB, int VB>
-__device__ __forceinline__ void load_tile(RawTile<D, KB, VB>& r, const uint8_t* tile, int lane) {
-    using PK = CachePart<D, KB>;
-    using PV = CachePart<D, VB>;
-    constexpr int G = D / kCacheGroup;
-    load_codes<D, KB>(r.k, tile, lane);
-    if constexpr (KB < 16) {
-        const uint8_t* s = tile + PK::CODES + (lane & 15) * (2 * G);
-        if constexpr (G % 2) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const uint32_t v = gptr<uint16_t>(s)[g];
-                r.ks[g / 2] = g % 2 ? r.ks[g / 2] | (v << 16) : v;
-            }
-        } else {
-            load_words(r.ks, s);
-        }
-    }
-    load_codes<D, VB>(r.v, tile + PK::BYTES, lane);
-    if constexpr (VB < 16) load_words(r.vs, tile + PK::BYTES + PV::CODES + (lane >> 4) * (8 * G));
+template <int D, int KB, int B>
+__device__ __forceinline__ void load_values(RawValues<D, B>& r, __amdgpu_buffer_rsrc_t tile, int lane) {
+    constexpr int G = D / kCacheGroup, V = CachePart<D, KB>::BYTES;
+    load_codes<D, B>(r.v, tile, V, lane);
+    if constexpr (B < 16) load_words<2 * G>(r.s, tile, (lane >> 4) * (8 * G), V + CachePart<D, B>::CODES);
 }
 
 // Key operand of group g: channels 32 g + 8 q + (0..7) of the lane's token.
-template <int D, int KB, int VB>
-__device__ __forceinline__ h8 key_operand(const RawTile<D, KB, VB>& r, int g) {
+template <int D, int KB>
+__device__ __forceinline__ h8 key_operand(const RawKeys<D, KB>& r, int g, const Nibbles& nib) {
     u4v o;
     if constexpr (KB == 16) {
         o = u4v{r.k.w[4 * g], r.k.w[4 * g + 1], r.k.w[4 * g + 2], r.k.w[4 * g + 3]};
     } else {
-        const uint32_t sw = r.ks[g / 2], s = __builtin_amdgcn_perm(sw, sw, g % 2 ? 0x03020302u : 0x01000100u);
+        const uint32_t sw = r.s[g / 2], s = __builtin_amdgcn_perm(sw, sw, g % 2 ? 0x03020302u : 0x01000100u);
         if constexpr (KB == 4) {
             const uint32_t w = r.k.w[g];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = scaled(nibbles(w >> (4 * e)), kBiasedZero<4>, s);
+            static_for<0, 4>([&](auto e) { o[e.value] = __builtin_bit_cast(uint32_t, nib.pair<e.value>(w) * as_h2(s)); });
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -450,26 +492,26 @@ __device__ __forceinline__ h8 key_operand(const RawTile<D, KB, VB>& r, int g) {
 
 // Value operand words of group g, half h, of one tile: the lane's four tokens
 // of channel 32 g + 16 h + c (two words).
-template <int D, int KB, int VB>
-__device__ __forceinline__ u2v value_words(const RawTile<D, KB, VB>& r, int g, int h) {
+template <int D, int VB>
+__device__ __forceinline__ u2v value_words(const RawValues<D, VB>& r, int g, int h, const Nibbles& nib) {
     if constexpr (VB == 16) {
         return u2v{r.v.w[4 * g + 2 * h], r.v.w[4 * g + 2 * h + 1]};
     } else if constexpr (VB == 4) {
         const uint32_t w = r.v.w[g];
-        return u2v{scaled(nibbles(w >> (4 * h)), kBiasedZero<4>, r.vs[2 * g]),
-                   scaled(nibbles(w >> (8 + 4 * h)), kBiasedZero<4>, r.vs[2 * g + 1])};
+        const h2 a = h ? nib.pair<1>(w) : nib.pair<0>(w), b = h ? nib.pair<3>(w) : nib.pair<2>(w);
+        return u2v{__builtin_bit_cast(uint32_t, a * as_h2(r.s[2 * g])), __builtin_bit_cast(uint32_t, b * as_h2(r.s[2 * g + 1]))};
     } else {
         const uint32_t w = r.v.w[2 * g + h];
-        return u2v{scaled(__builtin_amdgcn_perm(w, 0x64006400u, 0x01050104u), kBiasedZero<8>, r.vs[2 * g]),
-                   scaled(__builtin_amdgcn_perm(w, 0x64006400u, 0x01070106u), kBiasedZero<8>, r.vs[2 * g + 1])};
+        return u2v{scaled(__builtin_amdgcn_perm(w, 0x64006400u, 0x01050104u), kBiasedZero<8>, r.s[2 * g]),
+                   scaled(__builtin_amdgcn_perm(w, 0x64006400u, 0x01070106u), kBiasedZero<8>, r.s[2 * g + 1])};
     }
 }
 
 // Clears what the tokens of a tile outside [lo, hi) contribute to the second
 // product (weights of 0 would still turn a NaN or infinity there into NaN):
 // their scales, or in 16 bits their values.  t0: the lane's first token.
-template <int D, int KB, int VB>
-__device__ __forceinline__ void clear_values(RawTile<D, KB, VB>& r, int t0, int lo, int hi) {
+template <int D, int VB>
+__device__ __forceinline__ void clear_values(RawValues<D, VB>& r, int t0, int lo, int hi) {
     constexpr int G = D / kCacheGroup;
     uint32_t m[2];
 #pragma unroll
@@ -482,7 +524,7 @@ __device__ __forceinline__ void clear_values(RawTile<D, KB, VB>& r, int t0, int 
         for (int i = 0; i < RawPart<D, VB>::WORDS; ++i) r.v.w[i] &= m[i % 2];
     } else {
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) r.vs[i] &= m[i % 2];
+        for (int i = 0; i < 2 * G; ++i) r.s[i] &= m[i % 2];
     }
 }
 
@@ -494,25 +536,30 @@ __device__ __forceinline__ void clear_values(RawTile<D, KB, VB>& r, int t0, int 
 // product as they stand: lane (q, head) holds tokens 4 q .. 4 q + 3 of each.
 template <int D, int KB, int VB> struct AttendWave {
     static constexpr int G = D / kCacheGroup;
+    Nibbles nib;
     h8 q[G];
     f4 o[2 * G];
     float r, l;
+    float limit;   // a score that passes r by more moves r; below any score until r is set
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) o[i] = f4{0, 0, 0, 0};
-        r = -3e38f;
-        l = 0.0f;
+        r = l = 0.0f;
+        limit = -3e38f;
     }
+    __device__ __forceinline__ float reference() const { return limit < 0.0f ? -3e38f : r; }
 
-    // One step: the 32 tokens of two tiles.
-    __device__ __forceinline__ void step(const RawTile<D, KB, VB>& a, const RawTile<D, KB, VB>& b, float c,
-                                         bool partial, int ta, int tb, int lo, int hi) {
+    // The first half of a step: weights of the 32 tokens of two tiles.  ta, tb:
+    // the lane's first token of each; partial: some lie outside [lo, hi).
+    __device__ __forceinline__ h8 weights(const RawKeys<D, KB>& a, const RawKeys<D, KB>& b, float c, bool partial,
+                                          int ta, int tb, int lo, int hi) {
         f4 sa = {0, 0, 0, 0}, sb = {0, 0, 0, 0};
 #pragma unroll
-        for (int g = 0; g < G; ++g) sa = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(a, g), q[g], sa, 0, 0, 0);
-#pragma unroll
-        for (int g = 0; g < G; ++g) sb = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(b, g), q[g], sb, 0, 0, 0);
+        for (int g = 0; g < G; ++g) {
+            sa = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(a, g, nib), q[g], sa, 0, 0, 0);
+            sb = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand(b, g, nib), q[g], sb, 0, 0, 0);
+        }
         float t[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -531,32 +578,19 @@ template <int D, int KB, int VB> struct AttendWave {
         // The reference starts 2^7 below the largest weight seen and moves only
         // when a weight would pass 2^15: fp16 weights stay finite, and one is
         // lost to underflow only below 2^-31 of the largest.
-        if (__builtin_amdgcn_ballot_w64(m > 15.0f)) {
+        if (__builtin_amdgcn_ballot_w64(m > limit)) {
             m = __builtin_fmaxf(m, __shfl_xor(m, 16));
             m = __builtin_fmaxf(m, __shfl_xor(m, 32));
-            if (m > 15.0f) {
-                // t was taken against the old reference; the scores again, exactly
-                float top = -__builtin_inff();
+            const bool up = m > limit;
+            const float by = up ? m - 7.0f : 0.0f;
+            const float f = !up ? 1.0f : limit < 0.0f ? 0.0f : __builtin_amdgcn_exp2f(-by);   // nothing is summed before r is set
+            if (up) limit = 15.0f;
+            r += by;
+            l *= f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!(partial && (ta + i < lo || ta + i >= hi))) top = __builtin_fmaxf(top, sa[i] * c);
-                    if (!(partial && (tb + i < lo || tb + i >= hi))) top = __builtin_fmaxf(top, sb[i] * c);
-                }
-                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                const float nr = top - 7.0f, f = __builtin_amdgcn_exp2f(r - nr);
-                r = nr;
-                l *= f;
+            for (int i = 0; i < 2 * G; ++i) o[i] *= f;
 #pragma unroll
-                for (int i = 0; i < 2 * G; ++i) o[i] *= f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    t[i] = __builtin_fmaf(sa[i], c, -r);
-                    t[4 + i] = __builtin_fmaf(sb[i], c, -r);
-                    if (partial && (ta + i < lo || ta + i >= hi)) t[i] = -__builtin_inff();
-                    if (partial && (tb + i < lo || tb + i >= hi)) t[4 + i] = -__builtin_inff();
-                }
-            }
+            for (int i = 0; i < 8; ++i) t[i] -= by;
         }
         h8 p;
 #pragma unroll
@@ -565,27 +599,35 @@ template <int D, int KB, int VB> struct AttendWave {
             l += e;
             p[i] = (_Float16)e;
         }
+        return p;
+    }
+
+    // The second half: their values' weighted sums.
+    __device__ __forceinline__ void sums(const RawValues<D, VB>& a, const RawValues<D, VB>& b, h8 p) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const u2v x = value_words(a, g, h), y = value_words(b, g, h);
+                const u2v x = value_words(a, g, h, nib), y = value_words(b, g, h, nib);
                 const u4v w = {x[0], x[1], y[0], y[1]};
                 o[2 * g + h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, w), p, o[2 * g + h], 0, 0, 0);
             }
     }
 };
 
+// Waves per SIMD a geometry's kernel is compiled for: as many as its raw
+// data, query and sums leave registers for.
+template <int D, int KB, int VB> struct AttendShape {
+    static constexpr int WAVES_PER_EU = D * (KB + VB) <= 128 * 8 ? 4 : D * (KB + VB) <= 128 * 16 ? 3 : 2;
+};
+
 template <int D, int KB, int VB>
-__global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kAttendThreads, (AttendShape<D, KB, VB>::WAVES_PER_EU)) void attend_kernel(AttendArgs a) {
     using PK = CachePart<D, KB>;
     using PV = CachePart<D, VB>;
     constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
     __shared__ __attribute__((aligned(16))) float part_o[kAttendWaves][16][D];
     __shared__ float part_r[kAttendWaves][16], part_l[kAttendWaves][16];
-    __shared__ int64_t scan[kAttendWaves];
-    __shared__ int found_row;
-    __shared__ int64_t found_before;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
 
@@ -600,40 +642,27 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
         u = 0;
         end = row_span(a, row).units;
     } else {
-        const int per = (a.rows + kAttendThreads - 1) / kAttendThreads;
-        const int r0 = tid * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
-        int64_t mine = 0, total;
-        for (int r = r0; r < r1; ++r) mine += row_span(a, r).units;
-        const int64_t before = block_scan(mine, scan, total);
-        total *= a.head_tiles;
-        const int64_t wgs = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x;
-        if ((int64_t)blockIdx.x >= wgs) return;
-        u = (int64_t)blockIdx.x * total / wgs;
-        end = ((int64_t)blockIdx.x + 1) * total / wgs;
-        if (before * a.head_tiles <= u && u < (before + mine) * a.head_tiles) {
-            int64_t b = before;
-            int r = r0;
-            for (;; ++r) {
-                const int n = row_span(a, r).units;
-                if (u < (b + n) * a.head_tiles) break;
-                b += n;
-            }
-            found_row = r;
-            found_before = b;
-        }
-        __syncthreads();
-        row = __builtin_amdgcn_readfirstlane(found_row);
-        const int n = row_span(a, row).units;
-        const int64_t b = found_before * a.head_tiles;
-        seg = (int)((u - b) / n);
-        base = b + (int64_t)seg * n;
+        const int64_t total = units_before(a, a.rows) * a.head_tiles, share = share_of(total, (int)gridDim.x);
+        u = uniform64((int64_t)blockIdx.x * share);
+        if (u >= total) return;
+        end = u + share < total ? u + share : total;
+        int64_t before;
+        row = row_of_unit(a, divide(u, a.head_tiles), before);
+        const int64_t in_row = u - before * a.head_tiles;
+        const int n = uniform(row_span(a, row).units);
+        seg = (int)divide(in_row, n);
+        base = u - (in_row - (int64_t)seg * n);
     }
     bool first = true;
     AttendWave<D, KB, VB> W;
+    W.nib.init();
     while (u < end) {
-        row = __builtin_amdgcn_readfirstlane(row);
-        seg = __builtin_amdgcn_readfirstlane(seg);
+        row = uniform(row);
+        seg = uniform(seg);
         RowSpan span = row_span(a, row);
+        span.lo = uniform(span.lo);
+        span.hi = uniform(span.hi);
+        span.units = uniform(span.units);
         if (span.units == 0) {   // a padding row
             ++row;
             seg = 0;
@@ -644,59 +673,109 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
         const int heads = a.group - seg % head_tiles_per_kv * 16 < 16 ? a.group - seg % head_tiles_per_kv * 16 : 16;
         const int64_t stop = base + span.units < end ? base + span.units : end;
         // Query operand: channels 32 g + 8 q + (0..7) of head h0 + col.
+        const uint16_t* qsrc = a.q + (int64_t)row * a.q_row + (int64_t)(h0 + (col < heads ? col : 0)) * a.q_head + 8 * quad;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            u4v w = {0, 0, 0, 0};
-            if (col < heads)
-                w = *gptr<u4v>(a.q + (int64_t)row * a.q_row + (int64_t)(h0 + col) * a.q_head + g * kCacheGroup + 8 * quad);
+            u4v w = *gptr<u4v>(qsrc + g * kCacheGroup);
+            w &= col < heads ? 0xFFFFFFFFu : 0u;
             W.q[g] = __builtin_bit_cast(h8, w);
         }
         W.reset();
+        // The wave's steps: those of the units that hold a token of the span.
+        const int first_unit = span.lo / kUnitTokens, my = 32 * wave;
+        int i0 = (int)(u - base), i1 = (int)(stop - base);
+        {
+            const int lo_steps = (span.lo - my - 32 + kUnitTokens) / kUnitTokens - first_unit;      // first with a token >= lo
+            const int hi_steps = (span.hi - my + kUnitTokens - 1) / kUnitTokens - first_unit;       // past the last with one < hi
+            i0 = i0 > lo_steps ? i0 : lo_steps;
+            i1 = i1 < hi_steps ? i1 : hi_steps;
+        }
         bool bad = span.bad;
         const int32_t* pages = a.t.pages + (int64_t)row * a.t.stride;
-        const uint8_t* head0 = a.c.pages + (int64_t)kvh * a.c.tiles * TILE;
-        const int first_unit = span.lo / kUnitTokens;
-        auto tile_at = [&](int token) -> const uint8_t* {
-            const uint32_t tile = (uint32_t)token / kCacheTile;
-            uint32_t pi = __umulhi(tile, a.tile_magic);
-            if (a.tile_magic == 0) pi = tile;
-            if (pi * a.c.tiles > tile) --pi;
-            uint32_t page = (uint32_t)gptr<int32_t>(pages)[pi];
-            if (page >= a.c.n_pages) {
-                page = 0;
-                bad = true;
-            }
-            return head0 + (int64_t)page * a.c.page_bytes + (int64_t)(tile - pi * a.c.tiles) * TILE;
+        // Lane j holds the numbers, among the cache's tiles, of the two tiles
+        // of step c0 + j, 64 steps at a time: one look at the page table per
+        // 64 steps.
+        const uint32_t page_tiles = a.c.tiles * a.c.kv_heads, head_tile = (uint32_t)kvh * a.c.tiles;
+        uint32_t tile_a = 0, tile_b = 0;
+        int c0 = 0;
+        auto look_up = [&](int from) {
+            c0 = from;
+            const int i = from + lane;
+            const int token = (first_unit + i) * kUnitTokens + my;
+            const bool live = i < i1;
+            const bool ina = live && token + 16 > span.lo, inb = live && token + 16 < span.hi;
+            auto number = [&](bool in, int tok, bool& odd) -> uint32_t {
+                const uint32_t tile = (uint32_t)tok / kCacheTile;
+                uint32_t pi = a.tile_magic ? __umulhi(tile, a.tile_magic) : tile;
+                if (pi * a.c.tiles > tile) --pi;
+                uint32_t page = in ? (uint32_t)gptr<int32_t>(pages)[pi] : 0u;
+                odd = page >= a.c.n_pages;
+                if (odd) page = 0;
+                return page * page_tiles + head_tile + (tile - pi * a.c.tiles);
+            };
+            bool odd_a, odd_b;
+            tile_a = number(ina, token, odd_a);
+            tile_b = number(inb, token + 16, odd_b);
+            if (!ina) tile_a = tile_b;   // tiles without a token of the span are not read
+            if (!inb) tile_b = tile_a;
+            bad |= __builtin_amdgcn_ballot_w64(odd_a || odd_b) != 0;
         };
-        for (int64_t i = u - base; i < stop - base; ++i) {
-            const int token = __builtin_amdgcn_readfirstlane((int)(first_unit + i) * kUnitTokens + 32 * wave);
-            // tiles with no token in the span are not read: the page table may end before them
-            const bool ina = token < span.hi && token + 16 > span.lo, inb = token + 16 < span.hi && token + 32 > span.lo;
-            if (!ina && !inb) continue;
-            RawTile<D, KB, VB> x, y;
-            load_tile(x, tile_at(ina ? token : token + 16), lane);
-            load_tile(y, tile_at(inb ? token + 16 : token), lane);
-            const bool partial = token < span.lo || token + 32 > span.hi;
-            if (partial) {
-                clear_values(x, token + 4 * quad, span.lo, span.hi);
-                clear_values(y, token + 16 + 4 * quad, span.lo, span.hi);
+        auto tile_at = [&](uint32_t number, int i) {
+            const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)number, i - c0);
+            return buffer_rsrc(a.c.pages + (uint64_t)n * TILE, (uint32_t)TILE);
+        };
+        // Keys and values of one step each in registers: a step's keys are
+        // asked for once the keys before are used up, under the second product,
+        // and its values under the next step's first.  Past the end the last
+        // step is loaded again, so that every wait knows what is in flight.
+        if (i0 < i1) {
+            RawKeys<D, KB> ka, kb;
+            RawValues<D, VB> va, vb;
+            look_up(i0);
+            __amdgpu_buffer_rsrc_t pa = tile_at(tile_a, i0), pb = tile_at(tile_b, i0);
+            load_keys(ka, pa, lane);
+            load_keys(kb, pb, lane);
+            load_values<D, KB>(va, pa, lane);
+            load_values<D, KB>(vb, pb, lane);
+            for (int i = i0; i < i1; ++i) {
+                const int next = i + 1 < i1 ? i + 1 : i;
+                if (next - c0 >= 64) look_up(next);
+                pa = tile_at(tile_a, next);
+                pb = tile_at(tile_b, next);
+                const int token = (first_unit + i) * kUnitTokens + my;
+                const bool partial = token < span.lo || token + 32 > span.hi;
+                const h8 p = W.weights(ka, kb, a.scale, partial, token + 4 * quad, token + 16 + 4 * quad, span.lo, span.hi);
+                __builtin_amdgcn_sched_barrier(0);   // not before the keys' registers are free
+                load_keys(ka, pa, lane);
+                load_keys(kb, pb, lane);
+                if (partial) {
+                    clear_values(va, token + 4 * quad, span.lo, span.hi);
+                    clear_values(vb, token + 16 + 4 * quad, span.lo, span.hi);
+                }
+                W.sums(va, vb, p);
+                __builtin_amdgcn_sched_barrier(0);
+                load_values<D, KB>(va, pa, lane);
+                load_values<D, KB>(vb, pb, lane);
             }
-            W.step(x, y, a.scale, partial, token + 4 * quad, token + 16 + 4 * quad, span.lo, span.hi);
         }
-        // Join the waves.
+        // Join the waves.  (The thread's index through a register the compiler
+        // does not see through: addresses made here stay out of the loop above.)
+        int id = tid;
+        asm volatile("" : "+v"(id));
+        const int quad = (id & 63) >> 4, col = id & 15;
         float l = W.l;
         l += __shfl_xor(l, 16);
         l += __shfl_xor(l, 32);
         if (bad) l = __builtin_nanf("");
         if (quad == 0) {
-            part_r[wave][col] = W.r;
+            part_r[wave][col] = W.reference();
             part_l[wave][col] = l;
         }
         __syncthreads();
         float ref = part_r[0][col];
 #pragma unroll
         for (int w = 1; w < kAttendWaves; ++w) ref = __builtin_fmaxf(ref, part_r[w][col]);
-        const float f = __builtin_amdgcn_exp2f(W.r - ref);
+        const float f = __builtin_amdgcn_exp2f(W.reference() - ref);
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) *reinterpret_cast<f4*>(&part_o[wave][col][16 * i + 4 * quad]) = W.o[i] * f;
         __syncthreads();
@@ -704,7 +783,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
         const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
         const int hp = a.group < 16 ? a.group : 16;
         float* ws = a.ws + slot * slot_floats(hp, D);
-        for (int i = tid; i < heads * (D / 4); i += kAttendThreads) {
+        for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
             const int h = i / (D / 4), d = i % (D / 4) * 4;
             float top = part_r[0][h], sum = 0.0f;
 #pragma unroll
@@ -749,45 +828,44 @@ __global__ __launch_bounds__(kAttendThreads) void attend_kernel(AttendArgs a) {
 // which unit follows from the lengths alone.
 template <int D>
 __global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs a, int grid) {
-    __shared__ int64_t scan[kAttendWaves];
     constexpr int LANES = D / 4, PARTS = kAttendThreads / LANES;
     __shared__ __attribute__((aligned(16))) f4 red_o[PARTS][LANES];
-    __shared__ float red_l[PARTS];
+    __shared__ float red_l[PARTS > kAttendWaves ? PARTS : kAttendWaves];
     const int tid = threadIdx.x, row = (int)(blockIdx.x / (uint32_t)a.q_heads), head = (int)(blockIdx.x % (uint32_t)a.q_heads);
-    const int per = (a.rows + kAttendThreads - 1) / kAttendThreads;
-    const int r0 = tid * per, r1 = r0 + per < a.rows ? r0 + per : a.rows;
-    int64_t all = 0, earlier = 0, total, before;
-    for (int r = r0; r < r1; ++r) {
-        const int n = row_span(a, r).units;
-        all += n;
-        if (r < row) earlier += n;
-    }
-    (void)block_scan(all, scan, total);
-    (void)block_scan(earlier, scan, before);
     const RowSpan span = row_span(a, row);
     if (span.units == 0) return;
-    total *= a.head_tiles;
-    const int64_t wgs = total < (int64_t)grid ? total : (int64_t)grid;
+    const int64_t before = units_before(a, row);
+    const int64_t total = units_before(a, a.rows) * a.head_tiles, share = share_of(total, grid);
     const int tiles_per_kv = (a.group + 15) / 16, in_group = head % a.group;
     const int seg = head / a.group * tiles_per_kv + in_group / 16, h = in_group % 16;
     const int64_t base = before * a.head_tiles + (int64_t)seg * span.units;
-    const int64_t w0 = ((base + 1) * wgs - 1) / total, w1 = ((base + span.units) * wgs - 1) / total;
+    const int64_t w0 = divide(base, share), w1 = divide(base + span.units - 1, share);
     if (w0 == w1) return;   // written whole by one workgroup
     const int hp = a.group < 16 ? a.group : 16;
     const size_t floats = slot_floats(hp, D);
-    const int slot0 = w0 * total / wgs == base ? 0 : 1;   // the segment is its first workgroup's first, or its last
+    const int slot0 = w0 * share == base ? 0 : 1;   // the segment is its first workgroup's first, or its last
     const int n = (int)(w1 - w0) + 1;
     auto slot = [&](int i) -> const float* { return a.ws + (2 * (size_t)(w0 + i) + (i == 0 ? slot0 : 0)) * floats; };
+    // the parts' common reference, then their factors and sums, a chunk of parts at a time
     float top = -3e38f;
-    for (int i = 0; i < n; ++i) top = __builtin_fmaxf(top, slot(i)[(size_t)hp * D + h]);
+    for (int i = tid; i < n; i += kAttendThreads) top = __builtin_fmaxf(top, gptr<float>(slot(i))[(size_t)hp * D + h]);
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
+    if ((tid & 63) == 0) red_l[tid >> 6] = top;
+    __syncthreads();
+    top = red_l[0];
+#pragma unroll
+    for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, red_l[w]);
+    __syncthreads();
     const int part = tid / LANES, d = tid % LANES * 4;
     f4 o = {0, 0, 0, 0};
     float l = 0.0f;
     if (part < PARTS) {
+#pragma unroll 4
         for (int i = part; i < n; i += PARTS) {
             const float* s = slot(i);
-            const float f = __builtin_amdgcn_exp2f(s[(size_t)hp * D + h] - top);
-            l += s[(size_t)hp * (D + 1) + h] * f;
+            const float f = __builtin_amdgcn_exp2f(gptr<float>(s)[(size_t)hp * D + h] - top);
+            l += gptr<float>(s)[(size_t)hp * (D + 1) + h] * f;
             o += *gptr<f4>(s + (size_t)h * D + d) * f;
         }
         red_o[part][d / 4] = o;
@@ -983,6 +1061,9 @@ exq_status exq_cache_create(void* pages, int64_t n_pages, int page_size, int kv_
     if (!pages || !cache_aligned(pages, 16)) return fail(EXQ_ERR_INVALID_ARG, "pages is NULL or not 16-byte aligned");
     if (n_pages < 1 || n_pages > 0x7FFFFFFFll)
         return fail(EXQ_ERR_INVALID_ARG, "n_pages=%lld outside 1..2^31-1", (long long)n_pages);
+    if (n_pages * kv_heads > 0xFFFFFFFFll / (page_size / kCacheTile))   // tiles are numbered in 32 bits
+        return fail(EXQ_ERR_UNSUPPORTED, "%lld pages of %d tokens and %d heads: over 2^32 tiles of 16 tokens",
+                    (long long)n_pages, page_size, kv_heads);
     exq_cache* c = new (std::nothrow) exq_cache();
     if (!c) return fail(EXQ_ERR_OOM, "host allocation");
     *c = exq_cache{static_cast<uint8_t*>(pages), n_pages, page_size, kv_heads, head_dim, k_bits, v_bits,

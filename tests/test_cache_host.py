@@ -56,6 +56,8 @@ def test_create_rejects():
     expect(I, exq.exq_cache_create, FAKE, 4, 20, 8, 128, 4, 4)
     expect(U, exq.exq_cache_create, FAKE, 4, 16, 8, 192, 4, 4)
     expect(U, exq.exq_cache_create, FAKE, 4, 16, 8, 128, 3, 4)
+    expect(U, exq.exq_cache_create, FAKE, 1 << 29, 16, 8, 128, 4, 4)        # 2^32 tiles
+    exq.exq_cache_destroy(exq.exq_cache_create(FAKE, (1 << 29) - 1, 16, 8, 128, 4, 4))
     assert exq.lib.exq_cache_create(FAKE, 4, 16, 8, 128, 4, 4, None) == I
     exq.exq_cache_destroy(None)
 
