@@ -416,6 +416,7 @@ exq_status exq_cache_read(exq_cache_t cache, void* k, int64_t k_row_stride, int6
 
 /* Bytes of workspace exq_attend needs for these sizes (0: none, or an argument
  * is invalid).  It depends on nothing else: not on lengths or strides. */
+#define EXQ_ATTEND_COUNTER_BYTES 16384
 size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int table_width);
 
 /* Attention of one new token per sequence over the cache.  For row r, query
@@ -434,9 +435,12 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  *   out        device fp16 with strides as for q, no element twice, no overlap
  *              with q or the pages
  *   lse        device fp32 [rows][q_heads] or NULL
- *   workspace  device, 16-byte aligned, exq_attend_workspace_bytes() bytes, any
- *              content; NULL if that is 0.  Calls that may run at the same time
- *              (other streams, replays of two graphs) need one each.
+ *   workspace  device, 16-byte aligned, exq_attend_workspace_bytes() bytes; NULL if
+ *              that is 0.  Its first EXQ_ATTEND_COUNTER_BYTES must be zero before the
+ *              first call that uses it, and every call leaves them zero; the rest
+ *              may hold anything.  Calls of any sizes may share one in stream
+ *              order; calls that may run at the same time (other streams, replays
+ *              of two graphs) need one each.
  * What a page holds behind a sequence's end, or before its window, never
  * reaches the result, NaN included.  Scores, softmax sums and output sums are
  * fp32; the weights e^{S_j - max} enter the second product rounded to fp16.

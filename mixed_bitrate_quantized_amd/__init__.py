@@ -321,28 +321,22 @@ def exq_attend(cache: int, q_ptr: int, q_strides, rows: int, q_heads: int, table
 
 # ------------------------------------------------------------ conveniences
 
-def _require(ok: bool, what: str):
+def _refuse(what: str):
     """Argument checks of tensors, which the library never sees as such."""
-    if not ok:
-        raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", what)
+    raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", what)
 
 
-def _on(device):
-    """The device a call runs on: its tensors', whatever the current one is."""
+def _on(stream, device):
+    """What a call runs under when it names a stream or its tensors' device is not the current one: that device and, for
+    what the call allocates, that stream."""
     import torch
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _allocating_on(stream, device):
-    """Tensors allocated inside belong to the stream that the call uses."""
-    import torch
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
+    scope = contextlib.ExitStack()
+    scope.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        scope.enter_context(torch.cuda.stream(stream))
+    return scope
 
 
 class Layer:
@@ -439,6 +433,9 @@ class Plan:
             pass
 
 
+ATTEND_COUNTER_BYTES = 16384   # EXQ_ATTEND_COUNTER_BYTES
+
+
 class KVCache:
     """A paged key-value cache on the GPU: owns (or borrows) its pages and the handle.
 
@@ -457,58 +454,97 @@ class KVCache:
             exq_cache_create(None, n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
         if pages is None:
             pages = torch.zeros((n_pages, page_bytes), dtype=torch.uint8, device=device)
-        _require(pages.dtype == torch.uint8 and pages.is_contiguous() and pages.is_cuda
-                 and pages.numel() == n_pages * page_bytes,
-                 "pages must be contiguous uint8 of %d x %d bytes on the GPU" % (n_pages, page_bytes))
+        if not (pages.dtype is torch.uint8 and pages.is_contiguous() and pages.is_cuda
+                and pages.numel() == n_pages * page_bytes):
+            _refuse("pages must be contiguous uint8 of %d x %d bytes on the GPU" % (n_pages, page_bytes))
         self.pages, self.n_pages, self.page_size, self.page_bytes = pages, n_pages, page_size, page_bytes
         self.kv_heads, self.head_dim, self.k_bits, self.v_bits = kv_heads, head_dim, k_bits, v_bits
-        self.device = pages.device
+        self.device, self._index = pages.device, pages.device.index
+        self._torch = torch
+        self._workspaces = {}   # by stream: calls on one stream run one after another
         self.handle = exq_cache_create(pages.data_ptr(), n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
 
-    def _operand(self, name, x, rows, heads):
-        import torch
-        _require(x.dtype == torch.float16 and x.device == self.device and x.dim() == 3
-                 and x.shape == (rows, heads, self.head_dim) and x.stride(2) == 1,
-                 "%s must be fp16 [%d][%d][%d] on %s with contiguous channels" % (name, rows, heads, self.head_dim,
-                                                                                  self.device))
-        return x.data_ptr(), (x.stride(0), x.stride(1))
+    # Calls cost the host a few microseconds, as much as a small launch: the
+    # checks below are written for that.
 
-    def _indices(self, name, x, rows):
-        import torch
-        _require(x.dtype == torch.int32 and x.device == self.device and x.dim() == 1 and x.shape[0] == rows
-                 and x.is_contiguous(), "%s must be contiguous int32 [%d] on %s" % (name, rows, self.device))
-        return x.data_ptr()
+    def _is(self, x, dtype):
+        return x.dtype is dtype and x.get_device() == self._index
 
-    def _table(self, table, rows=None):
-        import torch
-        _require(table.dtype == torch.int32 and table.device == self.device and table.dim() == 2
-                 and (table.stride(1) == 1 or table.shape[1] == 1) and (rows is None or table.shape[0] == rows),
-                 "table must be int32 [%s][pages] on %s with contiguous rows" % (rows or "sequences", self.device))
-        return table.data_ptr(), table.shape[0], table.shape[1], table.stride(0)
+    def _strides(self, name, x, shape):
+        """(row, head) strides of an fp16 operand."""
+        if x.shape == shape and self._is(x, self._torch.float16):
+            row, head, channel = x.stride()
+            if channel == 1:
+                return row, head
+        _refuse("%s must be fp16 %s on %s with contiguous channels" % (name, list(shape), self.device))
+
+    def _check_indices(self, rows, **indices):
+        for name, x in indices.items():
+            if not (x.shape == (rows,) and self._is(x, self._torch.int32) and (rows < 2 or x.stride(0) == 1)):
+                _refuse("%s must be contiguous int32 [%d] on %s" % (name, rows, self.device))
+
+    def _table(self, table):
+        """(pointer, rows, width, stride) of a page table."""
+        if table.dim() == 2 and self._is(table, self._torch.int32):
+            rows, width = table.shape
+            stride, page = table.stride()
+            if page == 1 or width == 1:
+                return table.data_ptr(), rows, width, stride
+        _refuse("table must be int32 [sequences][pages] on %s with contiguous rows" % self.device)
+
+    def _current(self, stream):
+        """The raw current stream if a call can go straight to it, else None."""
+        C = self._torch._C
+        if stream is None and C._cuda_getDevice() == self._index:
+            return C._cuda_getCurrentRawStream(self._index)
+        return None
 
     def append(self, k, v, table, seqs, positions, stream=None):
         """Store rows k, v (fp16 [rows][kv_heads][head_dim]) at positions[r] of sequence seqs[r] (int32 [rows]; < 0: skipped)."""
+        raw = self._current(stream)
+        if raw is None:
+            with _on(stream, self.device):
+                return self.append(k, v, table, seqs, positions)
         rows = k.shape[0]
-        kp, vp = self._operand("k", k, rows, self.kv_heads), self._operand("v", v, rows, self.kv_heads)
-        idx = self._indices("seqs", seqs, rows), self._indices("positions", positions, rows)
-        tab = self._table(table)
-        with _on(self.device):
-            exq_cache_append(self.handle, *kp, *vp, rows, *tab, *idx, stream)
+        shape = (rows, self.kv_heads, self.head_dim)
+        ks, vs = self._strides("k", k, shape), self._strides("v", v, shape)
+        self._check_indices(rows, seqs=seqs, positions=positions)
+        st = lib.exq_cache_append(self.handle, k.data_ptr(), *ks, v.data_ptr(), *vs, rows, *self._table(table),
+                                  seqs.data_ptr(), positions.data_ptr(), raw)
+        if st:
+            _check(st, "exq_cache_append")
 
     def read(self, table, seqs, positions, k_out=None, v_out=None, stream=None):
         """The values held for positions[r] of sequence seqs[r]: fp16 k, v [rows][kv_heads][head_dim].
 
         Rows with seqs[r] < 0 are left as they were in k_out and v_out (in tensors allocated here: unspecified)."""
-        import torch
+        raw = self._current(stream)
+        if raw is None:
+            with _on(stream, self.device):
+                return self.read(table, seqs, positions, k_out, v_out)
         rows = seqs.shape[0]
-        idx = self._indices("seqs", seqs, rows), self._indices("positions", positions, rows)
-        tab = self._table(table)
-        with _on(self.device), _allocating_on(stream, self.device):
-            k_out, v_out = (torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float16, device=self.device)
-                            if x is None else x for x in (k_out, v_out))
-            kp, vp = self._operand("k_out", k_out, rows, self.kv_heads), self._operand("v_out", v_out, rows, self.kv_heads)
-            exq_cache_read(self.handle, *kp, *vp, rows, *tab, *idx, stream)
+        shape = (rows, self.kv_heads, self.head_dim)
+        self._check_indices(rows, seqs=seqs, positions=positions)
+        torch = self._torch
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.float16, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.float16, device=self.device)
+        ks, vs = self._strides("k_out", k_out, shape), self._strides("v_out", v_out, shape)
+        st = lib.exq_cache_read(self.handle, k_out.data_ptr(), *ks, v_out.data_ptr(), *vs, rows, *self._table(table),
+                                seqs.data_ptr(), positions.data_ptr(), raw)
+        if st:
+            _check(st, "exq_cache_read")
         return k_out, v_out
+
+    def workspace(self, rows: int, q_heads: int, table_width: int):
+        """A workspace for attend calls of up to these sizes, to pass where calls must not share the cache's own: its
+        counters are zeroed on the current stream."""
+        torch = self._torch
+        nbytes = exq_attend_workspace_bytes(self.handle, rows, q_heads, table_width)
+        ws = torch.empty(max(nbytes, ATTEND_COUNTER_BYTES), dtype=torch.uint8, device=self.device)
+        ws[:ATTEND_COUNTER_BYTES].view(torch.int32).zero_()
+        return ws
 
     def attend(self, q, table, lengths, scale=None, window: int = 0, out=None, return_lse: bool = False, lse=None,
                workspace=None, stream=None):
@@ -516,32 +552,48 @@ class KVCache:
         table row r (the last `window` of them if window > 0) -> out, or (out, lse fp32 [rows][q_heads]).
 
         scale: default head_dim ** -0.5.  lengths[r] == 0 gives zeros (lse -inf); < 0 leaves the row as it was.
-        workspace: uint8 of at least exq_attend_workspace_bytes (default: allocated by this call)."""
-        import torch
-        _require(q.dim() == 3, "q must be [rows][q_heads][head_dim]")
+        workspace: from workspace(); by default the cache keeps one for each stream, and a call under graph capture makes
+        one that belongs to the graph."""
+        raw = self._current(stream)
+        if raw is None:
+            with _on(stream, self.device):
+                return self.attend(q, table, lengths, scale, window, out, return_lse, lse, workspace)
+        torch = self._torch
+        if q.dim() != 3:
+            _refuse("q must be [rows][q_heads][head_dim]")
         rows, q_heads = q.shape[0], q.shape[1]
-        qp = self._operand("q", q, rows, q_heads)
-        tab = self._table(table, rows)
-        n = self._indices("lengths", lengths, rows)
-        with _on(self.device), _allocating_on(stream, self.device):
-            if out is None:
-                out = torch.empty((rows, q_heads, self.head_dim), dtype=torch.float16, device=self.device)
-            op = self._operand("out", out, rows, q_heads)
-            if lse is None and return_lse:
-                lse = torch.empty((rows, q_heads), dtype=torch.float32, device=self.device)
-            if lse is not None:
-                _require(lse.dtype == torch.float32 and lse.device == self.device and lse.shape == (rows, q_heads)
-                         and lse.is_contiguous(), "lse must be contiguous fp32 [%d][%d] on %s" % (rows, q_heads, self.device))
-            nbytes = exq_attend_workspace_bytes(self.handle, rows, q_heads, table.shape[1])
-            if workspace is None and nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            if workspace is not None:
-                _require(workspace.device == self.device and workspace.is_contiguous(),
-                         "workspace must be contiguous on %s" % self.device)
-            exq_attend(self.handle, *qp, rows, q_heads, tab[0], tab[2], tab[3], n,
-                       self.head_dim ** -0.5 if scale is None else scale, window, *op,
-                       None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
-                       0 if workspace is None else workspace.numel() * workspace.element_size(), stream)
+        shape = (rows, q_heads, self.head_dim)
+        qs = self._strides("q", q, shape)
+        tab, table_rows, width, table_stride = self._table(table)
+        if table_rows != rows:
+            _refuse("table must have q's %d rows" % rows)
+        self._check_indices(rows, lengths=lengths)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float16, device=self.device)
+        os = self._strides("out", out, shape)
+        if lse is not None:
+            if not (lse.shape == (rows, q_heads) and self._is(lse, torch.float32) and lse.is_contiguous()):
+                _refuse("lse must be contiguous fp32 [%d][%d] on %s" % (rows, q_heads, self.device))
+        elif return_lse:
+            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=self.device)
+        need = lib.exq_attend_workspace_bytes(self.handle, rows, q_heads, width)
+        if need:
+            if workspace is None:
+                workspace = self._workspaces.get(raw)
+                if torch._C._cuda_isCurrentStreamCapturing():
+                    workspace = self.workspace(rows, q_heads, width)
+                elif workspace is None or workspace.numel() < need:
+                    workspace = self._workspaces[raw] = self.workspace(rows, q_heads, width)
+            elif not (workspace.get_device() == self._index and workspace.is_contiguous()):
+                _refuse("workspace must be contiguous on %s" % self.device)
+            wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        else:
+            wp, wn = None, 0
+        st = lib.exq_attend(self.handle, q.data_ptr(), *qs, rows, q_heads, tab, width, table_stride, lengths.data_ptr(),
+                            self.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), *os,
+                            None if lse is None else lse.data_ptr(), wp, wn, raw)
+        if st:
+            _check(st, "exq_attend")
         return (out, lse) if return_lse else out
 
     def close(self):

@@ -302,8 +302,22 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
 constexpr int kAttendWaves = 4;
 constexpr int kAttendThreads = 64 * kAttendWaves;
 constexpr int kUnitTokens = 32 * kAttendWaves;   // tokens a workgroup takes in one step: 32 a wave
-constexpr int kAttendMaxWgs = 1024;              // workgroups of a split launch
 constexpr int kWholeUnits = 4;                   // sequences of at most this many units are not split
+
+// Waves per SIMD a geometry's kernel is compiled for: as many as its raw data,
+// query and sums leave registers for.  A split launch has that many
+// workgroups (of one wave per SIMD) for each CU, all resident at once.
+constexpr int attend_waves_per_simd(int D, int KB, int VB) {
+    return D <= 96 ? 4 : D == 128 ? (KB + VB <= 8 ? 4 : 3) : KB + VB <= 16 ? 2 : 1;
+}
+constexpr int kCus = 256;
+constexpr int kAttendMaxWgs = 4 * kCus;          // workgroups of a split launch, at most
+constexpr int kJoinSet = 16;                     // parts that one workgroup joins at a time
+
+// The workspace starts with the arrival counters of sets of parts and of
+// segments, one for each slot (two slots a workgroup), zero between launches.
+constexpr size_t kCounterBytes = 2 * (2 * kAttendMaxWgs) * sizeof(uint32_t);
+static_assert(kCounterBytes == EXQ_ATTEND_COUNTER_BYTES, "documented size");
 
 struct AttendArgs {
     CacheDev c;
@@ -393,9 +407,52 @@ __device__ __forceinline__ int row_of_unit(const AttendArgs& a, int64_t u, int64
 // of all segments, c = ceil(total / grid).
 __device__ __forceinline__ int64_t share_of(int64_t total, int grid) { return divide(total + grid - 1, grid); }
 
-// Partial results in the workspace: slot s (two per workgroup) holds group
-// rows of head_dim sums, then the references and the sums of weights.
-__device__ __forceinline__ size_t slot_floats(int heads, int D) { return (size_t)heads * (D + 2); }
+// Partial results follow the counters: slot s holds group rows of head_dim
+// sums, then the references and the sums of weights.  Workgroup w's first
+// segment uses slot 2 w, its last, if that is another, slot 2 w + 1 (those
+// between are whole); a set's joined result goes to its first part's slot in
+// a second array of slots.
+constexpr size_t slot_floats(int heads, int D) { return (size_t)heads * (D + 2); }
+
+// Workspace traffic between workgroups, which may run on XCDs with L2s of
+// their own: agent-scope accesses, ordered by the counters.
+__device__ __forceinline__ void put(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ float get(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// Whether this workgroup is the last of `n` to arrive at a counter, which then
+// reads zero again.  What the workgroups put before is visible to the last.
+__device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n, bool* flag) {
+    // each thread's stores have completed (a workgroup barrier does not wait for them), then one count
+    __builtin_amdgcn_s_waitcnt((0 & 15) | ((0 >> 4) << 14) | (7 << 4) | (15 << 8));   // vmcnt(0)
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        *flag = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+        if (*flag) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (*flag) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    return *flag;
+}
+
+// One head's four channels from d on, joined over `n` parts (part(i): its slot).
+struct Joined {
+    f4 o;
+    float top, sum;
+};
+template <int D, class F>
+__device__ __forceinline__ Joined join_parts(int n, F&& part, int hp, int h, int d) {
+    Joined j = {{0, 0, 0, 0}, -3e38f, 0.0f};
+    for (int i = 0; i < n; ++i) j.top = __builtin_fmaxf(j.top, get(part(i) + (size_t)hp * D + h));
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float* p = part(i);
+        const float f = __builtin_amdgcn_exp2f(get(p + (size_t)hp * D + h) - j.top);
+        j.sum += get(p + (size_t)hp * (D + 1) + h) * f;
+        const float* o = p + (size_t)h * D + d;
+        j.o += f4{get(o), get(o + 1), get(o + 2), get(o + 3)} * f;
+    }
+    return j;
+}
 
 // Reads go through one buffer descriptor a tile: its address in scalar
 // registers, a lane's place as a 32-bit offset from a compile-time start.
@@ -615,19 +672,14 @@ template <int D, int KB, int VB> struct AttendWave {
     }
 };
 
-// Waves per SIMD a geometry's kernel is compiled for: as many as its raw
-// data, query and sums leave registers for.
-template <int D, int KB, int VB> struct AttendShape {
-    static constexpr int WAVES_PER_EU = D * (KB + VB) <= 128 * 8 ? 4 : D * (KB + VB) <= 128 * 16 ? 3 : 2;
-};
-
 template <int D, int KB, int VB>
-__global__ __launch_bounds__(kAttendThreads, (AttendShape<D, KB, VB>::WAVES_PER_EU)) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kAttendThreads, (attend_waves_per_simd(D, KB, VB))) void attend_kernel(AttendArgs a) {
     using PK = CachePart<D, KB>;
     using PV = CachePart<D, VB>;
     constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
     __shared__ __attribute__((aligned(16))) float part_o[kAttendWaves][16][D];
     __shared__ float part_r[kAttendWaves][16], part_l[kAttendWaves][16];
+    __shared__ bool last;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
 
@@ -636,13 +688,15 @@ __global__ __launch_bounds__(kAttendThreads, (AttendShape<D, KB, VB>::WAVES_PER_
     int row, seg;            // current row and its segment
     int64_t u, end;          // units of all segments, in order: [u, end)
     int64_t base = 0;        // first unit of the current segment
+    int64_t share = 0;       // units a workgroup takes
     if (!a.split) {
         row = (int)(blockIdx.x / (uint32_t)a.head_tiles);
         seg = (int)(blockIdx.x % (uint32_t)a.head_tiles);
         u = 0;
         end = row_span(a, row).units;
     } else {
-        const int64_t total = units_before(a, a.rows) * a.head_tiles, share = share_of(total, (int)gridDim.x);
+        const int64_t total = units_before(a, a.rows) * a.head_tiles;
+        share = share_of(total, (int)gridDim.x);
         u = uniform64((int64_t)blockIdx.x * share);
         if (u >= total) return;
         end = u + share < total ? u + share : total;
@@ -780,36 +834,67 @@ __global__ __launch_bounds__(kAttendThreads, (AttendShape<D, KB, VB>::WAVES_PER_
         for (int i = 0; i < 2 * G; ++i) *reinterpret_cast<f4*>(&part_o[wave][col][16 * i + 4 * quad]) = W.o[i] * f;
         __syncthreads();
         const bool whole = u == base && stop == base + span.units;
-        const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
         const int hp = a.group < 16 ? a.group : 16;
-        float* ws = a.ws + slot * slot_floats(hp, D);
+        const size_t floats = slot_floats(hp, D);
+        float* slots = a.ws + kCounterBytes / sizeof(float);
+        auto finish = [&](int h, int d, const Joined& j) {
+            const bool empty = span.hi == 0 && !span.bad;
+            const float inv = empty ? 0.0f : 1.0f / j.sum;
+            u2v w;
+            w[0] = (uint32_t)f32_to_f16_bits(j.o[0] * inv) | ((uint32_t)f32_to_f16_bits(j.o[1] * inv) << 16);
+            w[1] = (uint32_t)f32_to_f16_bits(j.o[2] * inv) | ((uint32_t)f32_to_f16_bits(j.o[3] * inv) << 16);
+            *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)(h0 + h) * a.out_head + d) = w;
+            if (d == 0 && a.lse)
+                gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + h0 + h] =
+                    empty ? -__builtin_inff() : (j.top + __builtin_amdgcn_logf(j.sum)) * kLn2;
+        };
+        auto store = [&](float* p, int h, int d, const Joined& j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put(p + (size_t)h * D + d + e, j.o[e]);
+            if (d == 0) {
+                put(p + (size_t)hp * D + h, j.top);
+                put(p + (size_t)hp * (D + 1) + h, j.sum);
+            }
+        };
+        const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
         for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
             const int h = i / (D / 4), d = i % (D / 4) * 4;
-            float top = part_r[0][h], sum = 0.0f;
+            Joined j = {{0, 0, 0, 0}, part_r[0][h], 0.0f};
 #pragma unroll
-            for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, part_r[w][h]);
-            f4 o = {0, 0, 0, 0};
+            for (int w = 1; w < kAttendWaves; ++w) j.top = __builtin_fmaxf(j.top, part_r[w][h]);
 #pragma unroll
             for (int w = 0; w < kAttendWaves; ++w) {
-                sum += part_l[w][h] * __builtin_amdgcn_exp2f(part_r[w][h] - top);
-                o += *reinterpret_cast<const f4*>(&part_o[w][h][d]);
+                j.sum += part_l[w][h] * __builtin_amdgcn_exp2f(part_r[w][h] - j.top);
+                j.o += *reinterpret_cast<const f4*>(&part_o[w][h][d]);
             }
-            if (whole) {
-                const bool empty = span.hi == 0 && !span.bad;
-                const float inv = empty ? 0.0f : 1.0f / sum;
-                u2v w;
-                w[0] = (uint32_t)f32_to_f16_bits(o[0] * inv) | ((uint32_t)f32_to_f16_bits(o[1] * inv) << 16);
-                w[1] = (uint32_t)f32_to_f16_bits(o[2] * inv) | ((uint32_t)f32_to_f16_bits(o[3] * inv) << 16);
-                *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)(h0 + h) * a.out_head + d) = w;
-                if (d == 0 && a.lse)
-                    gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + h0 + h] =
-                        empty ? -__builtin_inff() : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-            } else {
-                *gptr_w<f4>(ws + (size_t)h * D + d) = o;
-                if (d == 0) {
-                    ws[(size_t)hp * D + h] = top;
-                    ws[(size_t)hp * (D + 1) + h] = sum;
+            if (whole) finish(h, d, j);
+            else store(slots + slot * floats, h, d, j);
+        }
+        if (!whole) {
+            // The segment's parts lie with workgroups w0 .. w1.  The last of a
+            // set of kJoinSet of them to finish joins the set, in order; where
+            // there are several sets, the last of those joins the sets.
+            const int w0 = (int)divide(base, share), w1 = (int)divide(base + span.units - 1, share);
+            const int n = w1 - w0 + 1, set = ((int)blockIdx.x - w0) / kJoinSet, sets = (n + kJoinSet - 1) / kJoinSet;
+            const int members = n - set * kJoinSet < kJoinSet ? n - set * kJoinSet : kJoinSet;
+            const int late = (int64_t)w0 * share == base ? 0 : 1;   // w0's first segment, or its last
+            auto slot_of = [&](int i) { return 2 * (w0 + i) + (i == 0 ? late : 0); };
+            uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws);
+            if (last_of(counters + slot_of(set * kJoinSet), (uint32_t)members, &last)) {
+                float* joined = slots + 2 * (size_t)gridDim.x * floats;
+                for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
+                    const int h = i / (D / 4), d = i % (D / 4) * 4;
+                    const Joined j = join_parts<D>(
+                        members, [&](int m) { return slots + (size_t)slot_of(set * kJoinSet + m) * floats; }, hp, h, d);
+                    if (sets == 1) finish(h, d, j);
+                    else store(joined + (size_t)slot_of(set * kJoinSet) * floats, h, d, j);
                 }
+                if (sets > 1 && last_of(counters + 2 * kAttendMaxWgs + slot_of(0), (uint32_t)sets, &last))
+                    for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
+                        const int h = i / (D / 4), d = i % (D / 4) * 4;
+                        finish(h, d, join_parts<D>(
+                            sets, [&](int m) { return joined + (size_t)slot_of(m * kJoinSet) * floats; }, hp, h, d));
+                    }
             }
         }
         __syncthreads();
@@ -821,71 +906,6 @@ __global__ __launch_bounds__(kAttendThreads, (AttendShape<D, KB, VB>::WAVES_PER_
             ++row;
         }
     }
-}
-
-// Joins the partial results of segments that several workgroups shared: one
-// workgroup per (row, query head).  Which workgroup of attend_kernel holds
-// which unit follows from the lengths alone.
-template <int D>
-__global__ __launch_bounds__(kAttendThreads) void attend_join_kernel(AttendArgs a, int grid) {
-    constexpr int LANES = D / 4, PARTS = kAttendThreads / LANES;
-    __shared__ __attribute__((aligned(16))) f4 red_o[PARTS][LANES];
-    __shared__ float red_l[PARTS > kAttendWaves ? PARTS : kAttendWaves];
-    const int tid = threadIdx.x, row = (int)(blockIdx.x / (uint32_t)a.q_heads), head = (int)(blockIdx.x % (uint32_t)a.q_heads);
-    const RowSpan span = row_span(a, row);
-    if (span.units == 0) return;
-    const int64_t before = units_before(a, row);
-    const int64_t total = units_before(a, a.rows) * a.head_tiles, share = share_of(total, grid);
-    const int tiles_per_kv = (a.group + 15) / 16, in_group = head % a.group;
-    const int seg = head / a.group * tiles_per_kv + in_group / 16, h = in_group % 16;
-    const int64_t base = before * a.head_tiles + (int64_t)seg * span.units;
-    const int64_t w0 = divide(base, share), w1 = divide(base + span.units - 1, share);
-    if (w0 == w1) return;   // written whole by one workgroup
-    const int hp = a.group < 16 ? a.group : 16;
-    const size_t floats = slot_floats(hp, D);
-    const int slot0 = w0 * share == base ? 0 : 1;   // the segment is its first workgroup's first, or its last
-    const int n = (int)(w1 - w0) + 1;
-    auto slot = [&](int i) -> const float* { return a.ws + (2 * (size_t)(w0 + i) + (i == 0 ? slot0 : 0)) * floats; };
-    // the parts' common reference, then their factors and sums, a chunk of parts at a time
-    float top = -3e38f;
-    for (int i = tid; i < n; i += kAttendThreads) top = __builtin_fmaxf(top, gptr<float>(slot(i))[(size_t)hp * D + h]);
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
-    if ((tid & 63) == 0) red_l[tid >> 6] = top;
-    __syncthreads();
-    top = red_l[0];
-#pragma unroll
-    for (int w = 1; w < kAttendWaves; ++w) top = __builtin_fmaxf(top, red_l[w]);
-    __syncthreads();
-    const int part = tid / LANES, d = tid % LANES * 4;
-    f4 o = {0, 0, 0, 0};
-    float l = 0.0f;
-    if (part < PARTS) {
-#pragma unroll 4
-        for (int i = part; i < n; i += PARTS) {
-            const float* s = slot(i);
-            const float f = __builtin_amdgcn_exp2f(gptr<float>(s)[(size_t)hp * D + h] - top);
-            l += gptr<float>(s)[(size_t)hp * (D + 1) + h] * f;
-            o += *gptr<f4>(s + (size_t)h * D + d) * f;
-        }
-        red_o[part][d / 4] = o;
-        if (d == 0) red_l[part] = l;
-    }
-    __syncthreads();
-    if (tid >= LANES) return;
-    o = red_o[0][tid];
-    l = red_l[0];
-    for (int p = 1; p < PARTS; ++p) {
-        o += red_o[p][tid];
-        l += red_l[p];
-    }
-    const float inv = 1.0f / l;
-    u2v w;
-    w[0] = (uint32_t)f32_to_f16_bits(o[0] * inv) | ((uint32_t)f32_to_f16_bits(o[1] * inv) << 16);
-    w[1] = (uint32_t)f32_to_f16_bits(o[2] * inv) | ((uint32_t)f32_to_f16_bits(o[3] * inv) << 16);
-    *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)head * a.out_head + d) = w;
-    if (d == 0 && a.lse)
-        gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + head] = (top + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 }  // namespace exq
@@ -1037,9 +1057,9 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     out->head_tiles = (int)tiles;
     out->split = units > kWholeUnits;
     // (a wide table times many rows may pass 64 bits' comfort, hence the early clamp)
-    out->wgs = out->split ? (int)std::min<int64_t>(kAttendMaxWgs, std::min<int64_t>(units, kAttendMaxWgs) * std::max<int64_t>(segments, 1))
-                          : (int)segments;
-    out->ws_bytes = out->split ? 2 * (size_t)out->wgs * 4 * (size_t)std::min(group, 16) * (size_t)(c->head_dim + 2) : 0;
+    const int64_t most = kCus * attend_waves_per_simd(c->head_dim, c->k_bits, c->v_bits);
+    out->wgs = out->split ? (int)std::min(most, std::min(units, most) * std::max<int64_t>(segments, 1)) : (int)segments;
+    out->ws_bytes = out->split ? kCounterBytes + 4 * (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
     return EXQ_OK;
 }
 
@@ -1182,8 +1202,6 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     const hipStream_t s = static_cast<hipStream_t>(stream);
     with_geometry(c, [&](auto D, auto KB, auto VB) {
         hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value>), dim3((unsigned)p.wgs), dim3(kAttendThreads), 0, s, a);
-        if (p.split)
-            hipLaunchKernelGGL((attend_join_kernel<D.value>), dim3((unsigned)rows * (unsigned)q_heads), dim3(kAttendThreads), 0, s, a, p.wgs);
     });
     return launched("attend launch");
 }

@@ -382,12 +382,33 @@ def test_guard_bands(exq):
     lbuf = torch.full((2 * 6 + 64,), 9.0, dtype=torch.float32, device="cuda")
     need = exq.exq_attend_workspace_bytes(c.cache.handle, 2, 6, c.dtable.shape[1])
     ws = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+    counters = ws[256:256 + exq.ATTEND_COUNTER_BYTES]
+    counters.zero_()
     out, lse = buf[64:-64].view(2, 6, 96), lbuf[32:-32].view(2, 6)
     c.cache.attend(q, c.dtable, i32([37, 600]), out=out, lse=lse, workspace=ws[256:256 + need])
     c.check(out, lse, q.cpu().numpy(), 96 ** -0.5)
+    assert torch.all(counters == 0)
     assert torch.all(buf[:64] == 9) and torch.all(buf[-64:] == 9) and torch.all(lbuf[:32] == 9) and torch.all(lbuf[-32:] == 9)
     assert torch.all(ws[:256] == 77) and torch.all(ws[-256:] == 77)
     np.testing.assert_array_equal(c.cache.pages.cpu().numpy().reshape(-1), c.pages)
+
+
+def test_calls_of_all_sizes_share_a_workspace(exq):
+    """Many workgroups to a segment (two levels of joining), few, and none, one after another through one workspace."""
+    lengths = [30000, 700]
+    c = Case(exq, 22, lengths, 64, 1, 64, (8, 8), spread=0.5, garbage=False)
+    ws = c.cache.workspace(2, 32, c.dtable.shape[1])
+    for heads in (1, 32, 7, 16):
+        q = values(c.rng, 2, heads, 64, spread=0.5)
+        for lens in ([30000, 700], [130, -1], [17000, 0], [-1, -1], [5, 700], [30000, -1]):
+            note("shared workspace heads=%d lengths=%s" % (heads, lens))
+            out, lse = c.cache.attend(to_dev(q), c.dtable, i32(lens), return_lse=True, workspace=ws)
+            if heads < 32:
+                one = Case.__new__(Case)
+                one.k, one.v, one.lengths = [x[:max(n, 0)] for x, n in zip(c.k, lens)], [
+                    x[:max(n, 0)] for x, n in zip(c.v, lens)], lens
+                one.check(out, lse, q, 0.125, what="%d heads %s" % (heads, lens))
+            assert torch.all(ws[:exq.ATTEND_COUNTER_BYTES] == 0)
 
 
 def test_other_streams_at_once(exq):
