@@ -5,6 +5,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
+#include <cstdio>
 #include <new>
 
 #include "exq_device_common.h"
@@ -76,24 +78,20 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t w) { return (w & 0x000F000F
 // their values: it would rather write a mask and the 0x6400 as literals of two
 // instructions than as registers of one v_and_or_b32.
 struct Nibbles {
-    uint32_t even, odd, one;
+    uint32_t even, odd, one_even, one_odd;
     __device__ __forceinline__ void init() {
         even = 0x000F000Fu;
         odd = 0x00F000F0u;
-        one = 0x64006400u;
-        asm volatile("" : "+v"(even), "+v"(odd), "+s"(one));
+        one_even = 0x64006400u;   // fp16 1024, whose bit 0 is worth 1
+        one_odd = 0x54005400u;    // fp16 64, whose bit 4 is worth 1
+        asm volatile("" : "+v"(even), "+v"(odd), "+s"(one_even), "+s"(one_odd));
     }
-    // The pair of codes at bits 4 e and 4 e + 16 of w, less 8, exactly: at bit
-    // 0 it reads 1024 + c, at bit 4 1024 + 16 c, and one shift by 8 serves the
-    // other two.
+    // The pair of codes at bits 4 e and 4 e + 16 of w, less 8, exactly; one
+    // shift by 8 serves e = 2 and 3.
     template <int E> __device__ __forceinline__ h2 pair(uint32_t w) const {
         const uint32_t x = E >= 2 ? w >> 8 : w;
-        if constexpr (E % 2 == 0) {
-            return as_h2((x & even) | one) - h2{1032, 1032};
-        } else {
-            const h2 sixteenth = {0.0625f, 0.0625f}, zero = {-72, -72};
-            return __builtin_elementwise_fma(as_h2((x & odd) | one), sixteenth, zero);
-        }
+        if constexpr (E % 2 == 0) return as_h2((x & even) | one_even) - h2{1032, 1032};
+        else return as_h2((x & odd) | one_odd) - h2{72, 72};
     }
 };
 
@@ -299,25 +297,22 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
 
 // ------------------------------------------------------------------ attend
 
-constexpr int kAttendWaves = 4;
-constexpr int kAttendThreads = 64 * kAttendWaves;
-constexpr int kUnitTokens = 32 * kAttendWaves;   // tokens a workgroup takes in one step: 32 a wave
-constexpr int kWholeUnits = 4;                   // sequences of at most this many units are not split
+constexpr int kCus = 256;
+constexpr int kAttendMaxSegments = 2048;   // more are not split: they load the card evenly enough
+constexpr int kAttendMaxParts = 32;        // parts of a segment
+constexpr int kAttendMaxWgs = kAttendMaxSegments + 2 * kCus;   // of a launch that splits
+constexpr int kJoinBatch = 8;              // parts whose loads a thread has in flight at once
 
 // Waves per SIMD a geometry's kernel is compiled for: as many as its raw data,
-// query and sums leave registers for.  A split launch has that many
-// workgroups (of one wave per SIMD) for each CU, all resident at once.
+// query and sums leave registers for.
 constexpr int attend_waves_per_simd(int D, int KB, int VB) {
     return D <= 96 ? 4 : D == 128 ? (KB + VB <= 8 ? 4 : 3) : KB + VB <= 16 ? 2 : 1;
 }
-constexpr int kCus = 256;
-constexpr int kAttendMaxWgs = 4 * kCus;          // workgroups of a split launch, at most
-constexpr int kJoinSet = 16;                     // parts that one workgroup joins at a time
 
-// The workspace starts with the arrival counters of sets of parts and of
-// segments, one for each slot (two slots a workgroup), zero between launches.
-constexpr size_t kCounterBytes = 2 * (2 * kAttendMaxWgs) * sizeof(uint32_t);
-static_assert(kCounterBytes == EXQ_ATTEND_COUNTER_BYTES, "documented size");
+// The workspace starts with the arrival counters of segments (at their first
+// workgroup's number), zero between launches.
+constexpr size_t kCounterBytes = EXQ_ATTEND_COUNTER_BYTES;
+static_assert(kCounterBytes >= kAttendMaxWgs * sizeof(uint32_t), "a counter for every workgroup");
 
 struct AttendArgs {
     CacheDev c;
@@ -333,24 +328,24 @@ struct AttendArgs {
     int window;
     int rows, q_heads, group;  // group: query heads per key-value head
     int head_tiles;            // kv_heads * ceil(group / 16): segments of a row
-    uint32_t tile_magic;       // floor(2^32 / tiles per page) + 1
-    bool split;
+    uint32_t tile_magic;       // floor(2^32 / tiles per page) + 1; 0 for one tile
+    int whole_units;           // rows of at most this many units are not split
+    int target;                // workgroups to split for; 0: a workgroup for each segment
 };
 
-// Tokens [lo, hi) that row r attends to, and its number of units of
-// kUnitTokens from the one that holds lo.  Rows left alone have no unit;
+// Tokens [lo, hi) that a row of length n attends to, and its number of units
+// of `unit` tokens from the one that holds lo.  Rows left alone have no unit;
 // empty rows and rows to be filled with NaN have one without tokens.
 struct RowSpan {
     int lo, hi, units;
     bool bad;
 };
-__device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int r) {
-    const int n = gptr<int32_t>(a.lengths)[r];
+__device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int n, int unit) {
     if (n < 0) return {0, 0, 0, false};
     const uint64_t cap = (uint64_t)a.t.width * a.c.page_size;
     if (n == 0 || (uint64_t)n > cap) return {0, 0, 1, n != 0};
     const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
-    return {lo, n, (n - 1) / kUnitTokens - lo / kUnitTokens + 1, false};
+    return {lo, n, (n - 1) / unit - lo / unit + 1, false};
 }
 
 // A value equal in all lanes, in scalar registers.
@@ -367,89 +362,162 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
     return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Units of rows [0, n), by one wave: 64 rows at a time.
-__device__ __forceinline__ int64_t units_before(const AttendArgs& a, int n) {
-    int64_t total = 0;
-    for (int r0 = 0; r0 < n; r0 += 64) {
-        const int r = r0 + (int)(threadIdx.x & 63);
-        int v = r < n ? row_span(a, r).units : 0;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-        total += uniform(v);
-    }
-    return total;
+// Inclusive prefix sum over a wave's lanes.
+__device__ __forceinline__ int wave_prefix(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // rows of 16: from 1, 2, 4, 8 lanes below
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row 0's sum to row 1, row 2's to row 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // the lower half's to the upper
+    return v;
 }
 
-// The row that holds unit `u` of all rows' (u in units of rows, not of
-// segments), and the units before it.
-__device__ __forceinline__ int row_of_unit(const AttendArgs& a, int64_t u, int64_t& before) {
-    before = 0;
-    for (int r0 = 0;; r0 += 64) {
-        const int lane = (int)(threadIdx.x & 63), r = r0 + lane;
-        const int mine = r < a.rows ? row_span(a, r).units : 0;
-        int v = mine;   // inclusive prefix sum over the lanes
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(v, d);
-            if (lane >= d) v += o;
+__device__ __forceinline__ int wave_max(int v) {
+    for (int m = 32; m >= 1; m >>= 1) {
+        const int o = __shfl_xor(v, m);
+        v = v > o ? v : o;
+    }
+    return uniform(v);
+}
+
+// One workgroup's work: chunk `chunk` of `chunks` of a segment (row, kv head,
+// 16 query heads), `size` units a chunk, and the number of the workgroup that
+// has the segment's first.
+struct Piece {
+    int row, seg, length;
+    int chunk, chunks, size, first;
+};
+
+// The piece of workgroup `w` of a launch that splits, counted from the lengths
+// by every wave for itself, 64 rows at a time (up to 64 rows are read once).
+// With U units in all segments, chunks have at least U / target units, so
+// there are at most target + segments of them, and a segment has at most
+// kAttendMaxParts.  False: there are fewer pieces.
+__device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w, Piece& p) {
+    int loaded = -1, mine = -1;
+    auto units_of = [&](int r0) {
+        if (r0 != loaded) {
+            const int r = r0 + (int)(threadIdx.x & 63);
+            mine = r < a.rows ? gptr<int32_t>(a.lengths)[r] : -1;
+            loaded = r0;
         }
+        return row_span(a, mine, unit).units;
+    };
+    int64_t total = 0;
+    int longest = 0;
+    for (int r0 = 0; r0 < a.rows; r0 += 64) {
+        const int units = units_of(r0);
+        total += __builtin_amdgcn_readlane(wave_prefix(units), 63);
+        const int most = wave_max(units);
+        longest = longest > most ? longest : most;
+    }
+    p.size = longest > 0 ? longest : 1;
+    if (longest > a.whole_units) {
+        const int even = (int)divide(total * a.head_tiles + a.target - 1, a.target);
+        const int least = (longest + kAttendMaxParts - 1) / kAttendMaxParts;
+        p.size = even > least ? even : least;
+    }
+    int before = 0;   // pieces of earlier rows
+    for (int r0 = 0; r0 < a.rows; r0 += 64) {
+        const int chunks = (units_of(r0) + p.size - 1) / p.size, v = wave_prefix(chunks * a.head_tiles);
         const int sum = __builtin_amdgcn_readlane(v, 63);
-        if (u < before + sum) {
-            const int at = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before + v <= u));   // rows that end at or before u
-            before += __builtin_amdgcn_readlane(v - mine, at);
-            return r0 + at;
+        if (w < before + sum) {
+            const int at = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before + v <= w));   // rows that end at or before w
+            p.row = r0 + at;
+            p.length = __builtin_amdgcn_readlane(mine, at);
+            p.chunks = __builtin_amdgcn_readlane(chunks, at);
+            before += __builtin_amdgcn_readlane(v, at) - p.chunks * a.head_tiles;
+            p.seg = (w - before) / p.chunks;
+            p.first = before + p.seg * p.chunks;
+            p.chunk = w - p.first;
+            return true;
         }
         before += sum;
     }
+    return false;
 }
 
-// Shares of a split launch: workgroup w of `grid` takes units [w c, (w + 1) c)
-// of all segments, c = ceil(total / grid).
-__device__ __forceinline__ int64_t share_of(int64_t total, int grid) { return divide(total + grid - 1, grid); }
-
-// Partial results follow the counters: slot s holds group rows of head_dim
-// sums, then the references and the sums of weights.  Workgroup w's first
-// segment uses slot 2 w, its last, if that is another, slot 2 w + 1 (those
-// between are whole); a set's joined result goes to its first part's slot in
-// a second array of slots.
+// Partial results follow the counters, a slot for each workgroup: the group's
+// rows of head_dim sums, then each row's reference and sum of weights.
 constexpr size_t slot_floats(int heads, int D) { return (size_t)heads * (D + 2); }
 
 // Workspace traffic between workgroups, which may run on XCDs with L2s of
-// their own: agent-scope accesses, ordered by the counters.
-__device__ __forceinline__ void put(float* p, float v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
-__device__ __forceinline__ float get(const float* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+// their own: agent-scope accesses only, which do not stop at an L2.  So a
+// store that has completed is seen by every later load, and no cache has to
+// be written back or invalidated.  (With release and acquire at the counters
+// instead, which do that to a whole L2 for every part, a 131072-token
+// sequence at 4 bits took twice as long: 113 us against 55.)
+typedef float f2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void put(float* p, f2 v) {
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f2 get(const float* p) {
+    return __builtin_bit_cast(f2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
 
 // Whether this workgroup is the last of `n` to arrive at a counter, which then
-// reads zero again.  What the workgroups put before is visible to the last.
+// reads zero again.  What the workgroups put before is there for the last.
 __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n, bool* flag) {
     // each thread's stores have completed (a workgroup barrier does not wait for them), then one count
     __builtin_amdgcn_s_waitcnt((0 & 15) | ((0 >> 4) << 14) | (7 << 4) | (15 << 8));   // vmcnt(0)
     __syncthreads();
     if (threadIdx.x == 0) {
-        *flag = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+        *flag = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
         if (*flag) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    if (*flag) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     return *flag;
 }
 
-// One head's four channels from d on, joined over `n` parts (part(i): its slot).
+// Four channels of one head, summed: the sums and the sum of weights against
+// the reference `top`.
 struct Joined {
     f4 o;
     float top, sum;
 };
-template <int D, class F>
-__device__ __forceinline__ Joined join_parts(int n, F&& part, int hp, int h, int d) {
+
+// out and lse of four channels.
+__device__ __forceinline__ void finish(const AttendArgs& a, int row, int head, int d, const Joined& j, bool empty) {
+    const float inv = empty ? 0.0f : 1.0f / j.sum;
+    u2v w;
+    w[0] = (uint32_t)f32_to_f16_bits(j.o[0] * inv) | ((uint32_t)f32_to_f16_bits(j.o[1] * inv) << 16);
+    w[1] = (uint32_t)f32_to_f16_bits(j.o[2] * inv) | ((uint32_t)f32_to_f16_bits(j.o[3] * inv) << 16);
+    *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)head * a.out_head + d) = w;
+    if (d == 0 && a.lse)
+        gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + head] =
+            empty ? -__builtin_inff() : (j.top + __builtin_amdgcn_logf(j.sum)) * kLn2;
+}
+
+// Slots first, first + step, .. below n of head h, channels d .. d + 3, joined
+// in that order.
+template <int D>
+__device__ __forceinline__ Joined join_parts(const float* slots, size_t floats, int first, int step, int n, int hp, int h, int d) {
     Joined j = {{0, 0, 0, 0}, -3e38f, 0.0f};
-    for (int i = 0; i < n; ++i) j.top = __builtin_fmaxf(j.top, get(part(i) + (size_t)hp * D + h));
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float* p = part(i);
-        const float f = __builtin_amdgcn_exp2f(get(p + (size_t)hp * D + h) - j.top);
-        j.sum += get(p + (size_t)hp * (D + 1) + h) * f;
-        const float* o = p + (size_t)h * D + d;
-        j.o += f4{get(o), get(o + 1), get(o + 2), get(o + 3)} * f;
+    for (int i0 = first; i0 < n; i0 += step * kJoinBatch) {
+        f2 rl[kJoinBatch], x[kJoinBatch], y[kJoinBatch];
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            const float* p = slots + (size_t)(i0 + i * step < n ? i0 + i * step : i0) * floats;
+            rl[i] = get(p + (size_t)hp * D + 2 * h);
+            x[i] = get(p + (size_t)h * D + d);
+            y[i] = get(p + (size_t)h * D + d + 2);
+        }
+        float top = j.top;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) top = __builtin_fmaxf(top, rl[i][0]);
+        const float keep = __builtin_amdgcn_exp2f(j.top - top);
+        j.sum *= keep;
+        j.o *= keep;
+        j.top = top;
+#pragma unroll
+        for (int i = 0; i < kJoinBatch; ++i) {
+            if (i0 + i * step < n) {
+                const float f = __builtin_amdgcn_exp2f(rl[i][0] - top);
+                j.sum += rl[i][1] * f;
+                j.o += f4{x[i][0], x[i][1], y[i][0], y[i][1]} * f;
+            }
+        }
     }
     return j;
 }
@@ -672,150 +740,131 @@ template <int D, int KB, int VB> struct AttendWave {
     }
 };
 
-template <int D, int KB, int VB>
-__global__ __launch_bounds__(kAttendThreads, (attend_waves_per_simd(D, KB, VB))) void attend_kernel(AttendArgs a) {
+// Attention over the cache: a workgroup of NW waves takes one chunk of a
+// segment, a unit of 32 NW tokens a step, each wave on 32 of them with a
+// softmax of its own; the waves join in LDS, and the last workgroup of a
+// segment to finish joins the parts of all, through the workspace.
+template <int D, int KB, int VB, int NW>
+__global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void attend_kernel(AttendArgs a) {
     using PK = CachePart<D, KB>;
     using PV = CachePart<D, VB>;
-    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
-    __shared__ __attribute__((aligned(16))) float part_o[kAttendWaves][16][D];
-    __shared__ float part_r[kAttendWaves][16], part_l[kAttendWaves][16];
+    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES, THREADS = 64 * NW, UNIT = 32 * NW;
+    __shared__ __attribute__((aligned(16))) float part_o[NW][16][D];
+    __shared__ float part_r[NW][16], part_l[NW][16];
     __shared__ bool last;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
 
-    // This workgroup's units: of one segment (row, kv head, 16 query heads),
-    // or its share of all of them.
-    int row, seg;            // current row and its segment
-    int64_t u, end;          // units of all segments, in order: [u, end)
-    int64_t base = 0;        // first unit of the current segment
-    int64_t share = 0;       // units a workgroup takes
-    if (!a.split) {
-        row = (int)(blockIdx.x / (uint32_t)a.head_tiles);
-        seg = (int)(blockIdx.x % (uint32_t)a.head_tiles);
-        u = 0;
-        end = row_span(a, row).units;
-    } else {
-        const int64_t total = units_before(a, a.rows) * a.head_tiles;
-        share = share_of(total, (int)gridDim.x);
-        u = uniform64((int64_t)blockIdx.x * share);
-        if (u >= total) return;
-        end = u + share < total ? u + share : total;
-        int64_t before;
-        row = row_of_unit(a, divide(u, a.head_tiles), before);
-        const int64_t in_row = u - before * a.head_tiles;
-        const int n = uniform(row_span(a, row).units);
-        seg = (int)divide(in_row, n);
-        base = u - (in_row - (int64_t)seg * n);
+    Piece p;
+    if (a.target == 0) {
+        p.row = (int)(blockIdx.x / (uint32_t)a.head_tiles);
+        p.seg = (int)(blockIdx.x % (uint32_t)a.head_tiles);
+        p.length = uniform(gptr<int32_t>(a.lengths)[p.row]);
+        p.chunk = 0;
+        p.chunks = 1;
+        p.size = 0x7FFFFFFF;
+        p.first = 0;
+    } else if (!find_piece(a, UNIT, (int)blockIdx.x, p)) {
+        return;
     }
-    bool first = true;
+    const RowSpan span = row_span(a, p.length, UNIT);
+    if (span.units == 0) return;   // a padding row
+    const int tiles_per_kv = (a.group + 15) / 16;
+    const int kvh = p.seg / tiles_per_kv, hs = p.seg % tiles_per_kv * 16;
+    const int h0 = kvh * a.group + hs, heads = a.group - hs < 16 ? a.group - hs : 16;
     AttendWave<D, KB, VB> W;
     W.nib.init();
-    while (u < end) {
-        row = uniform(row);
-        seg = uniform(seg);
-        RowSpan span = row_span(a, row);
-        span.lo = uniform(span.lo);
-        span.hi = uniform(span.hi);
-        span.units = uniform(span.units);
-        if (span.units == 0) {   // a padding row
-            ++row;
-            seg = 0;
-            continue;
-        }
-        const int head_tiles_per_kv = (a.group + 15) / 16;
-        const int kvh = seg / head_tiles_per_kv, h0 = kvh * a.group + seg % head_tiles_per_kv * 16;
-        const int heads = a.group - seg % head_tiles_per_kv * 16 < 16 ? a.group - seg % head_tiles_per_kv * 16 : 16;
-        const int64_t stop = base + span.units < end ? base + span.units : end;
-        // Query operand: channels 32 g + 8 q + (0..7) of head h0 + col.
-        const uint16_t* qsrc = a.q + (int64_t)row * a.q_row + (int64_t)(h0 + (col < heads ? col : 0)) * a.q_head + 8 * quad;
+    W.reset();
+    // Query operand: channels 32 g + 8 q + (0..7) of head h0 + col.
+    const uint16_t* qsrc = a.q + (int64_t)p.row * a.q_row + (int64_t)(h0 + (col < heads ? col : 0)) * a.q_head + 8 * quad;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            u4v w = *gptr<u4v>(qsrc + g * kCacheGroup);
-            w &= col < heads ? 0xFFFFFFFFu : 0u;
-            W.q[g] = __builtin_bit_cast(h8, w);
-        }
-        W.reset();
-        // The wave's steps: those of the units that hold a token of the span.
-        const int first_unit = span.lo / kUnitTokens, my = 32 * wave;
-        int i0 = (int)(u - base), i1 = (int)(stop - base);
-        {
-            const int lo_steps = (span.lo - my - 32 + kUnitTokens) / kUnitTokens - first_unit;      // first with a token >= lo
-            const int hi_steps = (span.hi - my + kUnitTokens - 1) / kUnitTokens - first_unit;       // past the last with one < hi
-            i0 = i0 > lo_steps ? i0 : lo_steps;
-            i1 = i1 < hi_steps ? i1 : hi_steps;
-        }
-        bool bad = span.bad;
-        const int32_t* pages = a.t.pages + (int64_t)row * a.t.stride;
-        // Lane j holds the numbers, among the cache's tiles, of the two tiles
-        // of step c0 + j, 64 steps at a time: one look at the page table per
-        // 64 steps.
-        const uint32_t page_tiles = a.c.tiles * a.c.kv_heads, head_tile = (uint32_t)kvh * a.c.tiles;
-        uint32_t tile_a = 0, tile_b = 0;
-        int c0 = 0;
-        auto look_up = [&](int from) {
-            c0 = from;
-            const int i = from + lane;
-            const int token = (first_unit + i) * kUnitTokens + my;
-            const bool live = i < i1;
-            const bool ina = live && token + 16 > span.lo, inb = live && token + 16 < span.hi;
-            auto number = [&](bool in, int tok, bool& odd) -> uint32_t {
-                const uint32_t tile = (uint32_t)tok / kCacheTile;
-                uint32_t pi = a.tile_magic ? __umulhi(tile, a.tile_magic) : tile;
-                if (pi * a.c.tiles > tile) --pi;
-                uint32_t page = in ? (uint32_t)gptr<int32_t>(pages)[pi] : 0u;
-                odd = page >= a.c.n_pages;
-                if (odd) page = 0;
-                return page * page_tiles + head_tile + (tile - pi * a.c.tiles);
-            };
-            bool odd_a, odd_b;
-            tile_a = number(ina, token, odd_a);
-            tile_b = number(inb, token + 16, odd_b);
-            if (!ina) tile_a = tile_b;   // tiles without a token of the span are not read
-            if (!inb) tile_b = tile_a;
-            bad |= __builtin_amdgcn_ballot_w64(odd_a || odd_b) != 0;
+    for (int g = 0; g < G; ++g) {
+        u4v w = *gptr<u4v>(qsrc + g * kCacheGroup);
+        w &= col < heads ? 0xFFFFFFFFu : 0u;
+        W.q[g] = __builtin_bit_cast(h8, w);
+    }
+    // The wave's steps: those of the chunk's units that hold a token of the span.
+    const int first_unit = span.lo / UNIT, my = 32 * wave;
+    int i0 = p.chunk * p.size, i1 = p.chunk + 1 < p.chunks ? i0 + p.size : span.units;
+    {
+        const int lo_steps = (span.lo - my - 32 + UNIT) / UNIT - first_unit;      // first with a token >= lo
+        const int hi_steps = (span.hi - my + UNIT - 1) / UNIT - first_unit;       // past the last with one < hi
+        i0 = i0 > lo_steps ? i0 : lo_steps;
+        i1 = i1 < hi_steps ? i1 : hi_steps;
+    }
+    bool bad = span.bad;
+    const int32_t* pages = a.t.pages + (int64_t)p.row * a.t.stride;
+    // Lane j holds the numbers, among the cache's tiles, of the two tiles
+    // of step c0 + j, 64 steps at a time: one look at the page table per
+    // 64 steps.
+    const uint32_t page_tiles = a.c.tiles * a.c.kv_heads, head_tile = (uint32_t)kvh * a.c.tiles;
+    uint32_t tile_a = 0, tile_b = 0;
+    int c0 = 0;
+    auto look_up = [&](int from) {
+        c0 = from;
+        const int i = from + lane;
+        const int token = (first_unit + i) * UNIT + my;
+        const bool live = i < i1;
+        const bool ina = live && token + 16 > span.lo, inb = live && token + 16 < span.hi;
+        auto number = [&](bool in, int tok, bool& odd) -> uint32_t {
+            const uint32_t tile = (uint32_t)tok / kCacheTile;
+            uint32_t pi = a.tile_magic ? __umulhi(tile, a.tile_magic) : tile;
+            if (pi * a.c.tiles > tile) --pi;
+            uint32_t page = in ? (uint32_t)gptr<int32_t>(pages)[pi] : 0u;
+            odd = page >= a.c.n_pages;
+            if (odd) page = 0;
+            return page * page_tiles + head_tile + (tile - pi * a.c.tiles);
         };
-        auto tile_at = [&](uint32_t number, int i) {
-            const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)number, i - c0);
-            return buffer_rsrc(a.c.pages + (uint64_t)n * TILE, (uint32_t)TILE);
-        };
-        // Keys and values of one step each in registers: a step's keys are
-        // asked for once the keys before are used up, under the second product,
-        // and its values under the next step's first.  Past the end the last
-        // step is loaded again, so that every wait knows what is in flight.
-        if (i0 < i1) {
-            RawKeys<D, KB> ka, kb;
-            RawValues<D, VB> va, vb;
-            look_up(i0);
-            __amdgpu_buffer_rsrc_t pa = tile_at(tile_a, i0), pb = tile_at(tile_b, i0);
+        bool odd_a, odd_b;
+        tile_a = number(ina, token, odd_a);
+        tile_b = number(inb, token + 16, odd_b);
+        if (!ina) tile_a = tile_b;   // tiles without a token of the span are not read
+        if (!inb) tile_b = tile_a;
+        bad |= __builtin_amdgcn_ballot_w64(odd_a || odd_b) != 0;
+    };
+    auto tile_at = [&](uint32_t number, int i) {
+        const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)number, i - c0);
+        return buffer_rsrc(a.c.pages + (uint64_t)n * TILE, (uint32_t)TILE);
+    };
+    // Keys and values of one step each in registers: a step's keys are
+    // asked for once the keys before are used up, under the second product,
+    // and its values under the next step's first.  Past the end the last
+    // step is loaded again, so that every wait knows what is in flight.
+    if (i0 < i1) {
+        RawKeys<D, KB> ka, kb;
+        RawValues<D, VB> va, vb;
+        look_up(i0);
+        __amdgpu_buffer_rsrc_t pa = tile_at(tile_a, i0), pb = tile_at(tile_b, i0);
+        load_keys(ka, pa, lane);
+        load_keys(kb, pb, lane);
+        load_values<D, KB>(va, pa, lane);
+        load_values<D, KB>(vb, pb, lane);
+        for (int i = i0; i < i1; ++i) {
+            const int next = i + 1 < i1 ? i + 1 : i;
+            if (next - c0 >= 64) look_up(next);
+            pa = tile_at(tile_a, next);
+            pb = tile_at(tile_b, next);
+            const int token = (first_unit + i) * UNIT + my;
+            const bool partial = token < span.lo || token + 32 > span.hi;
+            const h8 weights = W.weights(ka, kb, a.scale, partial, token + 4 * quad, token + 16 + 4 * quad, span.lo, span.hi);
+            __builtin_amdgcn_sched_barrier(0);   // not before the keys' registers are free
             load_keys(ka, pa, lane);
             load_keys(kb, pb, lane);
+            if (partial) {
+                clear_values(va, token + 4 * quad, span.lo, span.hi);
+                clear_values(vb, token + 16 + 4 * quad, span.lo, span.hi);
+            }
+            W.sums(va, vb, weights);
+            __builtin_amdgcn_sched_barrier(0);
             load_values<D, KB>(va, pa, lane);
             load_values<D, KB>(vb, pb, lane);
-            for (int i = i0; i < i1; ++i) {
-                const int next = i + 1 < i1 ? i + 1 : i;
-                if (next - c0 >= 64) look_up(next);
-                pa = tile_at(tile_a, next);
-                pb = tile_at(tile_b, next);
-                const int token = (first_unit + i) * kUnitTokens + my;
-                const bool partial = token < span.lo || token + 32 > span.hi;
-                const h8 p = W.weights(ka, kb, a.scale, partial, token + 4 * quad, token + 16 + 4 * quad, span.lo, span.hi);
-                __builtin_amdgcn_sched_barrier(0);   // not before the keys' registers are free
-                load_keys(ka, pa, lane);
-                load_keys(kb, pb, lane);
-                if (partial) {
-                    clear_values(va, token + 4 * quad, span.lo, span.hi);
-                    clear_values(vb, token + 16 + 4 * quad, span.lo, span.hi);
-                }
-                W.sums(va, vb, p);
-                __builtin_amdgcn_sched_barrier(0);
-                load_values<D, KB>(va, pa, lane);
-                load_values<D, KB>(vb, pb, lane);
-            }
         }
-        // Join the waves.  (The thread's index through a register the compiler
-        // does not see through: addresses made here stay out of the loop above.)
-        int id = tid;
-        asm volatile("" : "+v"(id));
+    }
+    // Join the waves.  (The thread's index through a register the compiler
+    // does not see through: addresses made here stay out of the loop above.)
+    int id = tid;
+    asm volatile("" : "+v"(id));
+    {
         const int quad = (id & 63) >> 4, col = id & 15;
         float l = W.l;
         l += __shfl_xor(l, 16);
@@ -828,84 +877,64 @@ __global__ __launch_bounds__(kAttendThreads, (attend_waves_per_simd(D, KB, VB)))
         __syncthreads();
         float ref = part_r[0][col];
 #pragma unroll
-        for (int w = 1; w < kAttendWaves; ++w) ref = __builtin_fmaxf(ref, part_r[w][col]);
+        for (int w = 1; w < NW; ++w) ref = __builtin_fmaxf(ref, part_r[w][col]);
         const float f = __builtin_amdgcn_exp2f(W.reference() - ref);
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) *reinterpret_cast<f4*>(&part_o[wave][col][16 * i + 4 * quad]) = W.o[i] * f;
         __syncthreads();
-        const bool whole = u == base && stop == base + span.units;
-        const int hp = a.group < 16 ? a.group : 16;
-        const size_t floats = slot_floats(hp, D);
-        float* slots = a.ws + kCounterBytes / sizeof(float);
-        auto finish = [&](int h, int d, const Joined& j) {
-            const bool empty = span.hi == 0 && !span.bad;
-            const float inv = empty ? 0.0f : 1.0f / j.sum;
-            u2v w;
-            w[0] = (uint32_t)f32_to_f16_bits(j.o[0] * inv) | ((uint32_t)f32_to_f16_bits(j.o[1] * inv) << 16);
-            w[1] = (uint32_t)f32_to_f16_bits(j.o[2] * inv) | ((uint32_t)f32_to_f16_bits(j.o[3] * inv) << 16);
-            *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)(h0 + h) * a.out_head + d) = w;
-            if (d == 0 && a.lse)
-                gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + h0 + h] =
-                    empty ? -__builtin_inff() : (j.top + __builtin_amdgcn_logf(j.sum)) * kLn2;
-        };
-        auto store = [&](float* p, int h, int d, const Joined& j) {
+    }
+    const int hp = a.group < 16 ? a.group : 16, items = heads * (D / 4);   // an item: four channels of a head
+    const size_t floats = slot_floats(hp, D);
+    float* slots = a.ws + kCounterBytes / sizeof(float);
+    for (int i = id; i < items; i += THREADS) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        Joined j = {{0, 0, 0, 0}, part_r[0][h], 0.0f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) put(p + (size_t)h * D + d + e, j.o[e]);
-            if (d == 0) {
-                put(p + (size_t)hp * D + h, j.top);
-                put(p + (size_t)hp * (D + 1) + h, j.sum);
-            }
-        };
-        const size_t slot = 2 * (size_t)blockIdx.x + (first ? 0 : 1);
-        for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
-            const int h = i / (D / 4), d = i % (D / 4) * 4;
-            Joined j = {{0, 0, 0, 0}, part_r[0][h], 0.0f};
+        for (int w = 1; w < NW; ++w) j.top = __builtin_fmaxf(j.top, part_r[w][h]);
 #pragma unroll
-            for (int w = 1; w < kAttendWaves; ++w) j.top = __builtin_fmaxf(j.top, part_r[w][h]);
-#pragma unroll
-            for (int w = 0; w < kAttendWaves; ++w) {
-                j.sum += part_l[w][h] * __builtin_amdgcn_exp2f(part_r[w][h] - j.top);
-                j.o += *reinterpret_cast<const f4*>(&part_o[w][h][d]);
-            }
-            if (whole) finish(h, d, j);
-            else store(slots + slot * floats, h, d, j);
+        for (int w = 0; w < NW; ++w) {
+            j.sum += part_l[w][h] * __builtin_amdgcn_exp2f(part_r[w][h] - j.top);
+            j.o += *reinterpret_cast<const f4*>(&part_o[w][h][d]);
         }
-        if (!whole) {
-            // The segment's parts lie with workgroups w0 .. w1.  The last of a
-            // set of kJoinSet of them to finish joins the set, in order; where
-            // there are several sets, the last of those joins the sets.
-            const int w0 = (int)divide(base, share), w1 = (int)divide(base + span.units - 1, share);
-            const int n = w1 - w0 + 1, set = ((int)blockIdx.x - w0) / kJoinSet, sets = (n + kJoinSet - 1) / kJoinSet;
-            const int members = n - set * kJoinSet < kJoinSet ? n - set * kJoinSet : kJoinSet;
-            const int late = (int64_t)w0 * share == base ? 0 : 1;   // w0's first segment, or its last
-            auto slot_of = [&](int i) { return 2 * (w0 + i) + (i == 0 ? late : 0); };
-            uint32_t* counters = reinterpret_cast<uint32_t*>(a.ws);
-            if (last_of(counters + slot_of(set * kJoinSet), (uint32_t)members, &last)) {
-                float* joined = slots + 2 * (size_t)gridDim.x * floats;
-                for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
-                    const int h = i / (D / 4), d = i % (D / 4) * 4;
-                    const Joined j = join_parts<D>(
-                        members, [&](int m) { return slots + (size_t)slot_of(set * kJoinSet + m) * floats; }, hp, h, d);
-                    if (sets == 1) finish(h, d, j);
-                    else store(joined + (size_t)slot_of(set * kJoinSet) * floats, h, d, j);
-                }
-                if (sets > 1 && last_of(counters + 2 * kAttendMaxWgs + slot_of(0), (uint32_t)sets, &last))
-                    for (int i = id; i < heads * (D / 4); i += kAttendThreads) {
-                        const int h = i / (D / 4), d = i % (D / 4) * 4;
-                        finish(h, d, join_parts<D>(
-                            sets, [&](int m) { return joined + (size_t)slot_of(m * kJoinSet) * floats; }, hp, h, d));
-                    }
-            }
-        }
-        __syncthreads();
-        first = false;
-        u = stop;
-        base += span.units;
-        if (++seg == a.head_tiles) {
-            seg = 0;
-            ++row;
+        if (p.chunks == 1) {
+            finish(a, p.row, h0 + h, d, j, span.hi == 0 && !span.bad);
+        } else {
+            float* slot = slots + (size_t)blockIdx.x * floats;
+            put(slot + (size_t)h * D + d, f2{j.o[0], j.o[1]});
+            put(slot + (size_t)h * D + d + 2, f2{j.o[2], j.o[3]});
+            if (d == 0) put(slot + (size_t)hp * D + 2 * h, f2{j.top, j.sum});
         }
     }
+    if (p.chunks == 1 || !last_of(reinterpret_cast<uint32_t*>(a.ws) + p.first, (uint32_t)p.chunks, &last)) return;
+    // The last to finish joins the parts, in order: threads by items, and where
+    // there are threads left over several of them on one item's parts.
+    const float* parts = slots + (size_t)p.first * floats;
+    const int ways = items < THREADS ? THREADS / items : 1;
+    if (ways == 1) {
+        for (int i = id; i < items; i += THREADS) {
+            const int h = i / (D / 4), d = i % (D / 4) * 4;
+            finish(a, p.row, h0 + h, d, join_parts<D>(parts, floats, 0, 1, p.chunks, hp, h, d), false);
+        }
+        return;
+    }
+    f4* way_o = reinterpret_cast<f4*>(&part_o[0][0][0]);                     // [THREADS]
+    f2* way_rl = reinterpret_cast<f2*>(&part_o[0][0][0]) + 2 * THREADS;      // [THREADS]
+    const int way = id / items, i = id % items, h = i / (D / 4), d = i % (D / 4) * 4;
+    Joined j = {{0, 0, 0, 0}, -3e38f, 0.0f};
+    if (way < ways) j = join_parts<D>(parts, floats, way, ways, p.chunks, hp, h, d);
+    way_o[id] = j.o;
+    way_rl[id] = f2{j.top, j.sum};
+    __syncthreads();
+    if (way != 0) return;
+    for (int w = 1; w < ways; ++w) {
+        const f2 rl = way_rl[w * items + i];
+        const float top = __builtin_fmaxf(j.top, rl[0]);
+        const float f = __builtin_amdgcn_exp2f(j.top - top), g = __builtin_amdgcn_exp2f(rl[0] - top);
+        j.o = j.o * f + way_o[w * items + i] * g;
+        j.sum = j.sum * f + rl[1] * g;
+        j.top = top;
+    }
+    finish(a, p.row, h0 + h, d, j, false);
 }
 
 }  // namespace exq
@@ -1037,10 +1066,10 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
     return EXQ_OK;
 }
 
-// Sizes of an exq_attend launch.
+// Shape of an exq_attend launch.
 struct AttendPlan {
-    int head_tiles, wgs;
-    bool split;
+    int head_tiles, wgs, waves;   // waves of a workgroup
+    int target, whole_units;
     size_t ws_bytes;
 };
 
@@ -1053,13 +1082,22 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     const int64_t tiles = (int64_t)c->kv_heads * ((group + 15) / 16), segments = tiles * rows;
     if (segments > 0x7FFFFFFFll || (int64_t)rows * q_heads > 0x7FFFFFFFll)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, q_heads);
-    const int64_t units = ((int64_t)table_width * c->page_size + kUnitTokens - 1) / kUnitTokens;   // of the longest row
+    const int64_t tokens = (int64_t)table_width * c->page_size;   // of the longest row
+    const char* e = getenv("EXQ_TUNE");   // "few_waves,few_target,few_whole_tokens,many_target,many_whole_tokens,many_from"
+    int few_waves = 8, few_target = 256, few_whole = 1024, many_target = 512, many_whole = 4096, many_from = 256;
+    if (e) sscanf(e, "%d,%d,%d,%d,%d,%d", &few_waves, &few_target, &few_whole, &many_target, &many_whole, &many_from);
+    const bool many = segments >= many_from;
+    const int per_simd = attend_waves_per_simd(c->head_dim, c->k_bits, c->v_bits);
+    out->waves = many || per_simd == 1 ? 4 : few_waves;
     out->head_tiles = (int)tiles;
-    out->split = units > kWholeUnits;
-    // (a wide table times many rows may pass 64 bits' comfort, hence the early clamp)
-    const int64_t most = kCus * attend_waves_per_simd(c->head_dim, c->k_bits, c->v_bits);
-    out->wgs = out->split ? (int)std::min(most, std::min(units, most) * std::max<int64_t>(segments, 1)) : (int)segments;
-    out->ws_bytes = out->split ? kCounterBytes + 4 * (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
+    const int unit = 32 * out->waves;
+    const int64_t units = (tokens - 1) / unit + 1;
+    out->whole_units = (many ? many_whole : few_whole) / unit;
+    const bool split = units > out->whole_units && segments <= kAttendMaxSegments;
+    out->target = split ? (many ? many_target : few_target) : 0;
+    out->wgs = split ? (int)std::min<int64_t>(out->target + segments, std::max<int64_t>(segments, 1) * std::min<int64_t>(units, kAttendMaxParts))
+                     : (int)segments;
+    out->ws_bytes = split ? kCounterBytes + (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
     return EXQ_OK;
 }
 
@@ -1198,10 +1236,15 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.group = q_heads / c->kv_heads;
     a.head_tiles = p.head_tiles;
     a.tile_magic = a.c.tiles == 1 ? 0u : (uint32_t)((1ull << 32) / a.c.tiles + 1);
-    a.split = p.split;
+    a.target = p.target;
+    a.whole_units = p.whole_units;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     with_geometry(c, [&](auto D, auto KB, auto VB) {
-        hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value>), dim3((unsigned)p.wgs), dim3(kAttendThreads), 0, s, a);
+        constexpr int FEW = attend_waves_per_simd(D.value, KB.value, VB.value) == 1 ? 4 : 8;
+        if (p.waves == FEW)
+            hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value, FEW>), dim3((unsigned)p.wgs), dim3(64 * FEW), 0, s, a);
+        else
+            hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value, 4>), dim3((unsigned)p.wgs), dim3(256), 0, s, a);
     });
     return launched("attend launch");
 }

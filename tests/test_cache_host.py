@@ -119,7 +119,7 @@ Q, O, L, W = FAKE + 2 * SIZE, FAKE + 4 * SIZE, FAKE + 6 * SIZE, 1 << 40
 
 
 def attend_args(**kw):
-    a = dict(q=Q, qs=(512, 64), rows=3, heads=8, table=T, width=40, tstride=40, lengths=S, scale=0.125, window=0, out=O,
+    a = dict(q=Q, qs=(512, 64), rows=3, heads=8, table=T, width=400, tstride=400, lengths=S, scale=0.125, window=0, out=O,
              os=(512, 64), lse=L, ws=W, wsb=1 << 30)
     a.update(kw)
     return [a["q"], a["qs"], a["rows"], a["heads"], a["table"], a["width"], a["tstride"], a["lengths"], a["scale"],
@@ -127,7 +127,7 @@ def attend_args(**kw):
 
 
 BAD_ATTEND = [dict(q=0), dict(q=Q + 4), dict(qs=(508, 64)), dict(qs=(512, -8)), dict(rows=-1), dict(heads=0), dict(heads=6),
-              dict(heads=-4), dict(table=0), dict(width=0), dict(tstride=39), dict(lengths=0), dict(lengths=S + 2),
+              dict(heads=-4), dict(table=0), dict(width=0), dict(tstride=399), dict(lengths=0), dict(lengths=S + 2),
               dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(out=0), dict(out=O + 2),
               dict(os=(0, 64)), dict(os=(512, 32)), dict(out=Q), dict(out=Q + 64), dict(out=FAKE), dict(lse=L + 2),
               dict(lse=O), dict(lse=Q), dict(lse=FAKE + 64), dict(ws=0), dict(ws=W + 8), dict(wsb=100), dict(ws=O), dict(ws=Q),
@@ -150,9 +150,11 @@ def test_attend_rejects_null_cache_and_too_many_rows(cache):
 def test_workspace_is_bounded_and_grows_with_the_split(cache):
     one = exq.exq_attend_workspace_bytes(cache, 1, 8, 1)        # 32 tokens: nothing to split
     assert one == 0
-    sizes = [exq.exq_attend_workspace_bytes(cache, r, 8, w) for r, w in ((1, 100), (16, 100), (4096, 1 << 20))]
+    sizes = [exq.exq_attend_workspace_bytes(cache, r, 8, w) for r, w in ((1, 1000), (16, 1000), (512, 1 << 20))]
     assert 0 < sizes[0] <= sizes[1] <= sizes[2] < 1 << 28
-    assert exq.exq_attend_workspace_bytes(cache, (1 << 31) // 64, 8, (1 << 31) - 1) < 1 << 28
+    assert exq.exq_attend_workspace_bytes(cache, 4096, 8, 1 << 20) == 0      # rows enough to load the card unsplit
+    for rows in (1, 16, 512, 513, (1 << 31) // 64):
+        assert exq.exq_attend_workspace_bytes(cache, rows, 8, (1 << 31) - 1) < 1 << 28
 
 
 def test_reference_reads_back_what_it_appends():

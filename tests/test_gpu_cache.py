@@ -375,7 +375,7 @@ def test_pages_beyond_32_bit_offsets(exq):
 # ------------------------------------------------- streams, graphs, guard bands, together
 
 def test_guard_bands(exq):
-    c = Case(exq, 18, [37, 600], 64, 2, 96, (4, 8))
+    c = Case(exq, 18, [37, 2600], 64, 2, 96, (4, 8))
     q = to_dev(values(c.rng, 2, 6, 96))
     note("guard bands")
     buf = torch.full((2 * 6 * 96 + 128,), 9.0, dtype=torch.float16, device="cuda")
@@ -385,7 +385,8 @@ def test_guard_bands(exq):
     counters = ws[256:256 + exq.ATTEND_COUNTER_BYTES]
     counters.zero_()
     out, lse = buf[64:-64].view(2, 6, 96), lbuf[32:-32].view(2, 6)
-    c.cache.attend(q, c.dtable, i32([37, 600]), out=out, lse=lse, workspace=ws[256:256 + need])
+    assert need > exq.ATTEND_COUNTER_BYTES
+    c.cache.attend(q, c.dtable, i32([37, 2600]), out=out, lse=lse, workspace=ws[256:256 + need])
     c.check(out, lse, q.cpu().numpy(), 96 ** -0.5)
     assert torch.all(counters == 0)
     assert torch.all(buf[:64] == 9) and torch.all(buf[-64:] == 9) and torch.all(lbuf[:32] == 9) and torch.all(lbuf[-32:] == 9)
