@@ -116,30 +116,95 @@ __device__ __forceinline__ RowPlace row_place(const CacheDev& c, const TableDev&
     return {(int64_t)page * c.page_bytes + (int64_t)(in / kCacheTile) * tile_bytes, (int)(in % kCacheTile)};
 }
 
-constexpr int kRowsThreads = 256;   // workgroup of the append and read kernels: 16 rows of one head
+// Append and read run one wave for 16 rows of one head: lane 16 q + t holds
+// channels 32 g + 8 q + (0..7) of every group g of row t, which is the keys'
+// own unit in the cache, so a lane moves its keys to or from wherever its row
+// lies, and 16 rows that fill a tile move as one contiguous run.  Values are
+// laid out by channel and have to change lanes: through LDS where the 16 rows
+// are a tile, by bytes where they are not.  Blocks of rows start where the
+// first row's tile starts, so that one sequence's rows (a prompt) make tiles
+// wherever the prompt starts.
+constexpr int kRowsThreads = 256;
 
-// The quantizer of one group of 32 values in LDS.
-__device__ __forceinline__ uint16_t group_scale_bits(const uint16_t* x, float top) {
-    float m = 0.0f;
-    bool odd = false;
-    for (int i = 0; i < kCacheGroup; ++i) {
-        const float a = __builtin_fabsf((float)__builtin_bit_cast(_Float16, x[i]));
-        odd |= !(a <= 65504.0f);
-        m = __builtin_fmaxf(m, a);
+// The rows of a lane and where they lie.
+struct RowsBlock {
+    int row, head;     // row < 0: none
+    RowPlace place;
+    bool tile;         // the wave's 16 rows are the 16 tokens of one tile, in order
+};
+
+__device__ __forceinline__ RowsBlock rows_block(const CacheDev& c, const TableDev& t, const int32_t* seqs,
+                                                const int32_t* positions, int rows, int tile_bytes) {
+    RowsBlock b;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t i = (int64_t)blockIdx.x * (kRowsThreads / 64) + wave;
+    b.head = (int)(i % c.kv_heads);
+    const int64_t r = i / c.kv_heads * kCacheTile - (gptr<int32_t>(positions)[0] & (kCacheTile - 1)) + (lane & 15);
+    b.row = r >= 0 && r < rows ? (int)r : -1;
+    b.place = b.row >= 0 ? row_place(c, t, seqs, positions, b.row, tile_bytes) : RowPlace{-1, 0};
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b.place.at);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)b.place.at >> 32));
+    const bool same = b.place.at >= 0 && b.place.token == (lane & 15) && (uint64_t)b.place.at == (((uint64_t)hi << 32) | lo);
+    b.tile = __builtin_amdgcn_ballot_w64(same) == ~0ull;
+    return b;
+}
+
+// max|x| of each group over the lane's 8 channels, then over the 4 lanes of
+// its row, as fp16 bits: ordered like integers, infinities and NaN on top.
+// Two groups to a dword.
+template <int G>
+__device__ __forceinline__ void group_max(const u4v (&x)[G], uint32_t (&m)[(G + 1) / 2]) {
+    typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+    auto top = [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
+    };
+    uint32_t h[G + 1];
+    h[G] = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint32_t a = x[g][0] & 0x7FFF7FFFu, b = x[g][1] & 0x7FFF7FFFu, c = x[g][2] & 0x7FFF7FFFu, d = x[g][3] & 0x7FFF7FFFu;
+        h[g] = top(top(a, b), top(c, d));
     }
-    return odd ? (uint16_t)0x7E00u : f32_to_f16_bits(m / top);
+#pragma unroll
+    for (int i = 0; i < (G + 1) / 2; ++i) {
+        // low halves of both groups against their high halves
+        const uint32_t a = h[2 * i], b = h[2 * i + 1];
+        uint32_t v = top((a & 0xFFFFu) | (b << 16), (a >> 16) | (b & 0xFFFF0000u));
+        v = top(v, (uint32_t)__shfl_xor((int)v, 16));
+        v = top(v, (uint32_t)__shfl_xor((int)v, 32));
+        m[i] = v;
+    }
 }
 
-template <int B>
-__device__ __forceinline__ uint32_t code_of(uint16_t x, uint16_t s) {
+// A group's scale from its max|x|: fp16 bits.
+template <int B> __device__ __forceinline__ uint32_t scale_bits(uint32_t max_bits) {
     constexpr float top = (float)((1 << (B - 1)) - 1);
-    const float f = (float)__builtin_bit_cast(_Float16, x), d = (float)__builtin_bit_cast(_Float16, s);
-    float c = 0.0f;
-    if (d > 0.0f) c = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(f / d), -top), top);   // NaN scale: zero point
-    return (uint32_t)((int)c + (1 << (B - 1)));
+    if (max_bits >= 0x7C00u) return 0x7E00u;
+    return f32_to_f16_bits((float)__builtin_bit_cast(_Float16, (uint16_t)max_bits) / top);
 }
 
-// One workgroup: 16 rows of one head.
+// Codes of eight values at scale s.  The quotient x / s: one Newton step on
+// x * (1 / s) leaves it within 2^-44 of itself before its rounding to fp32, so
+// a quotient that lies on a tie (k + 1/2, which fp32 holds) comes out exact,
+// and any other lies at least 2^-12 from a tie (s has 11 bits).  Adding 1.5 *
+// 2^23 + z rounds it to the nearest integer, ties to even, and leaves the code
+// in the sum's low bits.
+template <int B> __device__ __forceinline__ void codes_of(const u4v& x, uint32_t s_bits, uint32_t (&c)[8]) {
+    constexpr float top = (float)((1 << (B - 1)) - 1), magic = 12582912.0f + (float)(1 << (B - 1));
+    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)s_bits);
+    const bool live = s > 0.0f;   // not for zero or NaN scales: all codes are the zero point
+    const float inv = live ? __builtin_amdgcn_rcpf(s) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t w = x[e / 2];
+        const float f = (float)as_h2(w)[e % 2];
+        const float q0 = f * inv;
+        float q = __builtin_fmaf(__builtin_fmaf(-q0, s, f), inv, q0);
+        q = live ? q : 0.0f;
+        c[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(q, -top, top) + magic) & ((1u << B) - 1u);
+    }
+}
+
 template <int D, int KB, int VB>
 __global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableDev t, const uint16_t* __restrict__ k,
                                                               int64_t k_row, int64_t k_head,
@@ -150,83 +215,123 @@ __global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableD
     using PK = CachePart<D, KB>;
     using PV = CachePart<D, VB>;
     constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
-    __shared__ __attribute__((aligned(16))) uint16_t x[2][kCacheTile][D];
-    __shared__ uint16_t scale[2][kCacheTile][G];
-    __shared__ RowPlace place[kCacheTile];
-    const int tid = threadIdx.x, head = blockIdx.x % c.kv_heads, r0 = (int)(blockIdx.x / c.kv_heads) * kCacheTile;
-    if (tid < kCacheTile)
-        place[tid] = r0 + tid < rows ? row_place(c, t, seqs, positions, r0 + tid, TILE) : RowPlace{-1, 0};
-    for (int i = tid; i < 2 * kCacheTile * (D / 8); i += kRowsThreads) {
-        const int part = i / (kCacheTile * (D / 8)), r = i / (D / 8) % kCacheTile, d = i % (D / 8) * 8;
-        u4v w = {0, 0, 0, 0};
-        if (r0 + r < rows) {
-            const uint16_t* src = part ? v + (int64_t)(r0 + r) * v_row + head * v_head : k + (int64_t)(r0 + r) * k_row + head * k_head;
-            w = *gptr<u4v>(src + d);
-        }
-        *reinterpret_cast<u4v*>(&x[part][r][d]) = w;
-    }
-    __syncthreads();
-    for (int i = tid; i < 2 * kCacheTile * G; i += kRowsThreads) {
-        const int part = i / (kCacheTile * G), r = i / G % kCacheTile, g = i % G;
-        const int bits = part ? VB : KB;
-        if (bits < 16)
-            scale[part][r][g] = group_scale_bits(&x[part][r][g * kCacheGroup], (float)((1 << (bits - 1)) - 1));
-    }
-    __syncthreads();
-    uint8_t* head0 = c.pages + (int64_t)head * c.tiles * TILE;
-    // keys: one b-byte unit (8 channels) of one token at a time
-    for (int i = tid; i < kCacheTile * G * 4; i += kRowsThreads) {
-        const int r = i / (G * 4), g = i / 4 % G, q = i % 4;
-        const RowPlace p = place[r];
-        if (p.at < 0) continue;
-        uint8_t* tile = head0 + p.at;
-        uint8_t* dst = tile + PK::unit(16 * q + p.token, g);
-        const uint16_t* src = &x[0][r][g * kCacheGroup + 8 * q];
-        if constexpr (KB == 16) {
-            *gptr_w<u4v>(dst) = *reinterpret_cast<const u4v*>(src);
-        } else {
-            const uint16_t s = scale[0][r][g];
-            uint32_t w[KB / 4] = {};
+    __shared__ __attribute__((aligned(16))) uint8_t turned[kRowsThreads / 64][PV::CODES];
+    const RowsBlock b = rows_block(c, t, seqs, positions, rows, TILE);
+    if (__builtin_amdgcn_ballot_w64(b.place.at >= 0) == 0) return;
+    const int lane = (int)threadIdx.x & 63, q = lane >> 4;
+    uint8_t* buf = turned[threadIdx.x >> 6];
+    u4v kx[G], vx[G];
+    {
+        const int64_t r = b.place.at >= 0 ? b.row : 0;   // rows that go nowhere are not read
+        const uint16_t *ks = k + r * k_row + b.head * k_head + 8 * q, *vs = v + r * v_row + b.head * v_head + 8 * q;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t code = code_of<KB>(src[e], s);
-                if constexpr (KB == 4) w[0] |= code << (4 * (e / 2) + 16 * (e % 2));
-                else w[e / 4] |= code << (8 * (e % 4));
-            }
+        for (int g = 0; g < G; ++g) kx[g] = *gptr<u4v>(ks + g * kCacheGroup);
 #pragma unroll
-            for (int j = 0; j < KB / 4; ++j) gptr_w<uint32_t>(dst)[j] = w[j];
-            if (q == 0) *gptr_w<uint16_t>(tile + PK::CODES + 2 * (p.token * G + g)) = s;
-        }
+        for (int g = 0; g < G; ++g) vx[g] = *gptr<u4v>(vs + g * kCacheGroup);
     }
-    // values: the two channels 32 g + c and 32 g + 16 + c of one token at a time
-    for (int i = tid; i < kCacheTile * G * 16; i += kRowsThreads) {
-        const int r = i / (G * 16), g = i / 16 % G, col = i % 16;
-        const RowPlace p = place[r];
-        if (p.at < 0) continue;
-        uint8_t* part = head0 + p.at + PK::BYTES;
-        const int t4 = p.token % 4;
-        uint8_t* dst = part + PV::unit(16 * (p.token / 4) + col, g);
-        const uint16_t a = x[1][r][g * kCacheGroup + col], b = x[1][r][g * kCacheGroup + 16 + col];
-        if constexpr (VB == 16) {
-            gptr_w<uint16_t>(dst)[t4] = a;
-            gptr_w<uint16_t>(dst)[4 + t4] = b;
-        } else {
-            const uint16_t s = scale[1][r][g];
-            const uint32_t ca = code_of<VB>(a, s), cb = code_of<VB>(b, s);
-            if constexpr (VB == 4) {
-                gptr_w<uint8_t>(dst)[2 * (t4 % 2) + t4 / 2] = (uint8_t)(ca | (cb << 4));
+    uint8_t* tile = c.pages + (b.place.at >= 0 ? b.place.at : 0) + (int64_t)b.head * c.tiles * TILE;
+    const bool live = b.place.at >= 0;
+    const int tok = b.place.token;
+
+    // keys
+    if constexpr (KB == 16) {
+        if (live) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) *gptr_w<u4v>(tile + PK::unit(16 * q + tok, g)) = kx[g];
+        }
+    } else {
+        uint32_t m[(G + 1) / 2], w[G * KB / 4], s[G];
+        group_max<G>(kx, m);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            s[g] = scale_bits<KB>((m[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
+            uint32_t code[8];
+            codes_of<KB>(kx[g], s[g], code);
+            if constexpr (KB == 4) {
+                uint32_t x = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x |= code[e] << (4 * (e / 2) + 16 * (e % 2));
+                w[g] = x;
             } else {
-                gptr_w<uint8_t>(dst)[t4] = (uint8_t)ca;
-                gptr_w<uint8_t>(dst)[4 + t4] = (uint8_t)cb;
+                w[2 * g] = code[0] | (code[1] << 8) | (code[2] << 16) | (code[3] << 24);
+                w[2 * g + 1] = code[4] | (code[5] << 8) | (code[6] << 16) | (code[7] << 24);
             }
-            if (col == 0) *gptr_w<uint16_t>(part + PV::CODES + 8 * G * (p.token / 4) + 8 * g + 2 * t4) = s;
+        }
+        if (live) {
+            static_for<0, PK::CHUNKS>([&](auto jc) {
+                constexpr int j = jc, n = (G - j * PK::GPC < PK::GPC ? G - j * PK::GPC : PK::GPC) * KB / 4;
+                uint8_t* dst = tile + 1024 * j + (16 * q + tok) * (4 * n);
+                if constexpr (n == 4) *gptr_w<u4v>(dst) = u4v{w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
+                else {
+#pragma unroll
+                    for (int i = 0; i < n; ++i) gptr_w<uint32_t>(dst)[i] = w[4 * j + i];
+                }
+            });
+            if (q == 0) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) gptr_w<uint16_t>(tile + PK::CODES + 2 * tok * G)[g] = (uint16_t)s[g];
+            }
+        }
+    }
+
+    // values
+    uint8_t* part = tile + PK::BYTES;
+    uint32_t m[(G + 1) / 2];
+    if constexpr (VB < 16) group_max<G>(vx, m);
+    const int t4 = tok % 4, col0 = 8 * (q % 2), half = q / 2;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        uint32_t code[8], s = 0;
+        if constexpr (VB < 16) {
+            s = scale_bits<VB>((m[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
+            codes_of<VB>(vx[g], s, code);
+        }
+        if constexpr (VB == 4) {
+            // channels c and c + 16 share a byte: lanes q = 2, 3 hand theirs to q = 0, 1
+            uint32_t x = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x |= code[e] << (4 * e);
+            const uint32_t y = (uint32_t)__shfl_xor((int)x, 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) code[e] = ((x >> (4 * e)) & 15u) | (((y >> (4 * e)) & 15u) << 4);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int at = PV::unit(16 * (tok / 4) + col0 + e, g);
+            if constexpr (VB == 16) {
+                const uint32_t w = vx[g][e / 2];
+                const uint16_t x = (uint16_t)(e % 2 ? w >> 16 : w);
+                if (b.tile) *reinterpret_cast<uint16_t*>(buf + at + 8 * half + 2 * t4) = x;
+                else if (live) *gptr_w<uint16_t>(part + at + 8 * half + 2 * t4) = x;
+            } else {
+                const int inner = VB == 4 ? 2 * (t4 % 2) + t4 / 2 : 4 * half + t4;
+                const bool mine = VB == 8 || half == 0;
+                if (b.tile) {
+                    if (mine) buf[at + inner] = (uint8_t)code[e];
+                } else if (live && mine) {
+                    *gptr_w<uint8_t>(part + at + inner) = (uint8_t)code[e];
+                }
+            }
+        }
+        if constexpr (VB < 16) {
+            if (live && q == g % 4) *gptr_w<uint16_t>(part + PV::CODES + 8 * G * (tok / 4) + 8 * g + 2 * t4) = (uint16_t)s;
+        }
+    }
+    if (b.tile) {
+        // the wave's own LDS: its writes are done before its reads
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int i = 0; i < (PV::CODES + 1023) / 1024; ++i) {
+            const int at = 1024 * i + 16 * lane;
+            if (PV::CODES % 1024 == 0 || at < PV::CODES) *gptr_w<u4v>(part + at) = *reinterpret_cast<const u4v*>(buf + at);
         }
     }
 }
 
 // -------------------------------------------------------------------- read
 
-// One workgroup: 16 rows of one head, eight channels a thread at a time.
 template <int D, int KB, int VB>
 __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, TableDev t, uint16_t* __restrict__ k,
                                                                   int64_t k_row, int64_t k_head,
@@ -236,62 +341,128 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
                                                                   const int32_t* __restrict__ positions) {
     using PK = CachePart<D, KB>;
     using PV = CachePart<D, VB>;
-    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
-    __shared__ RowPlace place[kCacheTile];
-    const int tid = threadIdx.x, head = blockIdx.x % c.kv_heads, r0 = (int)(blockIdx.x / c.kv_heads) * kCacheTile;
-    if (tid < kCacheTile)
-        place[tid] = r0 + tid < rows ? row_place(c, t, seqs, positions, r0 + tid, TILE) : RowPlace{-1, 0};
-    __syncthreads();
-    const uint8_t* head0 = c.pages + (int64_t)head * c.tiles * TILE;
-    for (int i = tid; i < kCacheTile * G * 4; i += kRowsThreads) {
-        const int r = i / (G * 4), g = i / 4 % G, q = i % 4;
-        const RowPlace p = place[r];
-        if (p.at == -1) continue;
-        u4v kw = {0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u}, vw = kw;
-        if (p.at >= 0) {
-            const uint8_t* tile = head0 + p.at;
-            const uint8_t* ku = tile + PK::unit(16 * q + p.token, g);
-            if constexpr (KB == 16) {
-                kw = *gptr<u4v>(ku);
+    constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES, PITCH = D + 8;
+    __shared__ __attribute__((aligned(16))) uint16_t turned[kRowsThreads / 64][kCacheTile][PITCH];
+    const RowsBlock b = rows_block(c, t, seqs, positions, rows, TILE);
+    if (__builtin_amdgcn_ballot_w64(b.place.at != -1) == 0) return;
+    const int lane = (int)threadIdx.x & 63, q = lane >> 4;
+    const bool live = b.place.at >= 0, written = b.place.at != -1;
+    const int tok = live ? b.place.token : 0;
+    const uint8_t* tile = c.pages + (live ? b.place.at : 0) + (int64_t)b.head * c.tiles * TILE;   // rows outside read tile 0
+    const uint8_t* part = tile + PK::BYTES;
+    uint16_t (&buf)[kCacheTile][PITCH] = turned[threadIdx.x >> 6];
+    const u4v nan = {0x7E007E00u, 0x7E007E00u, 0x7E007E00u, 0x7E007E00u};
+
+    // what there is to load, all at once
+    uint32_t kw[G * KB / 4], ksc[(G + 1) / 2], vw[G * VB / 4], vsc[2 * G];
+    auto load_unit_words = [&](auto bits, uint32_t* w, const uint8_t* src, int unit_lane) {
+        constexpr int B = bits;
+        using P = CachePart<D, B>;
+        static_for<0, P::CHUNKS>([&](auto jc) {
+            constexpr int j = jc, n = (G - j * P::GPC < P::GPC ? G - j * P::GPC : P::GPC) * B / 4;
+            const uint8_t* at = src + 1024 * j + unit_lane * (4 * n);
+            if constexpr (n == 4) {
+                const u4v x = *gptr<u4v>(at);
+                w[4 * j] = x[0]; w[4 * j + 1] = x[1]; w[4 * j + 2] = x[2]; w[4 * j + 3] = x[3];
             } else {
-                const uint32_t s = (uint32_t)*gptr<uint16_t>(tile + PK::CODES + 2 * (p.token * G + g)) * 0x10001u;
-                if constexpr (KB == 4) {
-                    const uint32_t w = *gptr<uint32_t>(ku);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) kw[e] = scaled(nibbles(w >> (4 * e)), kBiasedZero<4>, s);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t w = gptr<uint16_t>(ku)[e];
-                        kw[e] = scaled((w & 0xFFu) | ((w & 0xFF00u) << 8) | 0x64006400u, kBiasedZero<8>, s);
-                    }
-                }
+                for (int i = 0; i < n; ++i) w[4 * j + i] = gptr<uint32_t>(at)[i];
             }
-            // channels 8 q .. 8 q + 7 of the group: half h = q / 2, c from 8 (q % 2)
-            const uint8_t* part = tile + PK::BYTES;
-            const int t4 = p.token % 4, h = q / 2;
-            uint32_t s = 0;
-            if constexpr (VB < 16)
-                s = (uint32_t)*gptr<uint16_t>(part + PV::CODES + 8 * G * (p.token / 4) + 8 * g + 2 * t4) * 0x10001u;
+        });
+    };
+    load_unit_words(IC<KB>{}, kw, tile, 16 * q + tok);
+    if constexpr (KB < 16) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const uint32_t s = gptr<uint16_t>(tile + PK::CODES + 2 * tok * G)[g];
+            ksc[g / 2] = g % 2 ? ksc[g / 2] | (s << 16) : s;
+        }
+    }
+    if (b.tile) {
+        load_unit_words(IC<VB>{}, vw, part, lane);
+        if constexpr (VB < 16) {
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) vsc[i] = gptr<uint32_t>(part + PV::CODES + 8 * G * q)[i];
+        }
+    }
+
+    // keys: the lane's own channels
+    uint16_t *kd = k + (int64_t)(written ? b.row : 0) * k_row + b.head * k_head + 8 * q;
+    uint16_t *vd = v + (int64_t)(written ? b.row : 0) * v_row + b.head * v_head + 8 * q;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        u4v o;
+        if constexpr (KB == 16) {
+            o = u4v{kw[4 * g], kw[4 * g + 1], kw[4 * g + 2], kw[4 * g + 3]};
+        } else {
+            const uint32_t s = ((ksc[g / 2] >> (16 * (g % 2))) & 0xFFFFu) * 0x10001u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                uint32_t half[2];
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const uint8_t* vu = part + PV::unit(16 * (p.token / 4) + 8 * (q % 2) + 2 * e + f, g);
-                    if constexpr (VB == 16) half[f] = gptr<uint16_t>(vu)[4 * h + t4];
-                    else if constexpr (VB == 8) half[f] = gptr<uint8_t>(vu)[4 * h + t4];
-                    else half[f] = ((uint32_t)gptr<uint8_t>(vu)[2 * (t4 % 2) + t4 / 2] >> (4 * h)) & 15u;
+                if constexpr (KB == 4) {
+                    o[e] = scaled(nibbles(kw[g] >> (4 * e)), kBiasedZero<4>, s);
+                } else {
+                    const uint32_t w = kw[2 * g + e / 2] >> (16 * (e % 2));
+                    o[e] = scaled((w & 0xFFu) | ((w & 0xFF00u) << 8) | 0x64006400u, kBiasedZero<8>, s);
                 }
-                const uint32_t w = half[0] | (half[1] << 16);
-                if constexpr (VB == 16) vw[e] = w;
-                else vw[e] = scaled(w | 0x64006400u, kBiasedZero<VB>, s);
             }
         }
-        const int64_t row = r0 + r;
-        const int d = g * kCacheGroup + 8 * q;
-        *gptr_w<u4v>(k + row * k_row + head * k_head + d) = kw;
-        *gptr_w<u4v>(v + row * v_row + head * v_head + d) = vw;
+        if (written) *gptr_w<u4v>(kd + g * kCacheGroup) = live ? o : nan;
+    }
+
+    // values
+    if (b.tile) {
+        // the lane's four tokens of channels 32 g + col and 32 g + 16 + col, turned in the wave's own LDS
+        const int col = lane & 15;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[2];   // tokens 4 q, 4 q + 1 and 4 q + 2, 4 q + 3
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (VB == 16) {
+                        x[i] = vw[4 * g + 2 * h + i];
+                    } else if constexpr (VB == 4) {
+                        x[i] = scaled(nibbles(vw[g] >> (4 * h + 8 * i)), kBiasedZero<4>, vsc[2 * g + i]);
+                    } else {
+                        const uint32_t w = vw[2 * g + h] >> (16 * i);
+                        x[i] = scaled((w & 0xFFu) | ((w & 0xFF00u) << 8) | 0x64006400u, kBiasedZero<8>, vsc[2 * g + i]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    buf[4 * q + i][kCacheGroup * g + 16 * h + col] = (uint16_t)(i % 2 ? x[i / 2] >> 16 : x[i / 2]);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            *gptr_w<u4v>(vd + g * kCacheGroup) = *reinterpret_cast<const u4v*>(&buf[lane & 15][kCacheGroup * g + 8 * q]);
+    } else if (written) {
+        const int t4 = tok % 4, col0 = 8 * (q % 2), half = q / 2;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            uint32_t s = 0;
+            if constexpr (VB < 16)
+                s = (uint32_t)*gptr<uint16_t>(part + PV::CODES + 8 * G * (tok / 4) + 8 * g + 2 * t4) * 0x10001u;
+            u4v o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t x[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const uint8_t* u = part + PV::unit(16 * (tok / 4) + col0 + 2 * e + f, g);
+                    if constexpr (VB == 16) x[f] = gptr<uint16_t>(u)[4 * half + t4];
+                    else if constexpr (VB == 8) x[f] = gptr<uint8_t>(u)[4 * half + t4];
+                    else x[f] = ((uint32_t)gptr<uint8_t>(u)[2 * (t4 % 2) + t4 / 2] >> (4 * half)) & 15u;
+                }
+                const uint32_t w = x[0] | (x[1] << 16);
+                if constexpr (VB == 16) o[e] = w;
+                else o[e] = scaled(w | 0x64006400u, kBiasedZero<VB>, s);
+            }
+            *gptr_w<u4v>(vd + g * kCacheGroup) = live ? o : nan;
+        }
     }
 }
 
@@ -1048,6 +1219,14 @@ exq_status launched(const char* what) {
     return e == hipSuccess ? EXQ_OK : fail(EXQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+// Waves of an append or read: a head of 16 rows each, and one block of rows
+// more than there are, for blocks that start at the first row's tile.
+int64_t rows_waves(const exq_cache* c, int rows) { return (((int64_t)rows + kCacheTile - 1) / kCacheTile + 1) * c->kv_heads; }
+unsigned rows_workgroups(const exq_cache* c, int rows) {
+    constexpr int per = kRowsThreads / 64;
+    return (unsigned)((rows_waves(c, rows) + per - 1) / per);
+}
+
 exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& v, int rows, const int32_t* table,
                            int table_rows, int table_width, int64_t table_stride, const int32_t* seqs,
                            const int32_t* positions) {
@@ -1061,7 +1240,7 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
     const size_t bytes = (size_t)c->n_pages * c->page_bytes;
     if (ranges_meet(k.p, extent(k), c->pages, bytes) || ranges_meet(v.p, extent(v), c->pages, bytes))
         return fail(EXQ_ERR_INVALID_ARG, "k or v overlaps the cache's pages");
-    if (((int64_t)rows + kCacheTile - 1) / kCacheTile * c->kv_heads > 0x7FFFFFFFll)
+    if (rows_waves(c, rows) > 0x7FFFFFFFll)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, c->kv_heads);
     return EXQ_OK;
 }
@@ -1144,7 +1323,7 @@ exq_status exq_cache_append(exq_cache_t c, const void* k, int64_t k_row_stride, 
     if (st != EXQ_OK || rows == 0) return st;
     const CacheDev d = cache_dev(c);
     const TableDev t{table, table_stride, (uint32_t)table_rows, (uint32_t)table_width};
-    const dim3 grid((unsigned)((rows + (int64_t)kCacheTile - 1) / kCacheTile * c->kv_heads));
+    const dim3 grid(rows_workgroups(c, rows));
     with_geometry(c, [&](auto D, auto KB, auto VB) {
         hipLaunchKernelGGL((append_kernel<D.value, KB.value, VB.value>), grid, dim3(kRowsThreads), 0,
                            static_cast<hipStream_t>(stream), d, t, static_cast<const uint16_t*>(k), k_row_stride,
@@ -1167,7 +1346,7 @@ exq_status exq_cache_read(exq_cache_t c, void* k, int64_t k_row_stride, int64_t 
     if (operands_meet(ko, vo)) return fail(EXQ_ERR_INVALID_ARG, "k and v overlap");
     const CacheDev d = cache_dev(c);
     const TableDev t{table, table_stride, (uint32_t)table_rows, (uint32_t)table_width};
-    const dim3 grid((unsigned)((rows + (int64_t)kCacheTile - 1) / kCacheTile * c->kv_heads));
+    const dim3 grid(rows_workgroups(c, rows));
     with_geometry(c, [&](auto D, auto KB, auto VB) {
         hipLaunchKernelGGL((cache_read_kernel<D.value, KB.value, VB.value>), grid, dim3(kRowsThreads), 0,
                            static_cast<hipStream_t>(stream), d, t, static_cast<uint16_t*>(k), k_row_stride, k_head_stride,
