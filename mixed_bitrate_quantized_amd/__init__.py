@@ -460,57 +460,59 @@ class KVCache:
         self.pages, self.n_pages, self.page_size, self.page_bytes = pages, n_pages, page_size, page_bytes
         self.kv_heads, self.head_dim, self.k_bits, self.v_bits = kv_heads, head_dim, k_bits, v_bits
         self.device, self._index = pages.device, pages.device.index
-        self._torch = torch
+        self._torch, self._C, self._empty = torch, torch._C, torch.empty_strided
+        self._f16, self._f32, self._i32 = torch.float16, torch.float32, torch.int32
+        self._scale = head_dim ** -0.5
+        self._needs = {}        # workspace bytes by (rows, q_heads, table width)
         self._workspaces = {}   # by stream: calls on one stream run one after another
         self.handle = exq_cache_create(pages.data_ptr(), n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
 
-    # Calls cost the host a few microseconds, as much as a small launch: the
-    # checks below are written for that.
+    # A call costs the host several microseconds, more than a small launch runs:
+    # the checks below are written for few operations on tensors.
 
-    def _is(self, x, dtype):
-        return x.dtype is dtype and x.get_device() == self._index
+    def _raw_stream(self):
+        """The raw current stream, or None if the cache's device is not the current one."""
+        C = self._C
+        return C._cuda_getCurrentRawStream(self._index) if C._cuda_getDevice() == self._index else None
 
     def _strides(self, name, x, shape):
         """(row, head) strides of an fp16 operand."""
-        if x.shape == shape and self._is(x, self._torch.float16):
+        if x.shape == shape and x.dtype is self._f16 and x.get_device() == self._index:
             row, head, channel = x.stride()
             if channel == 1:
                 return row, head
         _refuse("%s must be fp16 %s on %s with contiguous channels" % (name, list(shape), self.device))
 
-    def _check_indices(self, rows, **indices):
-        for name, x in indices.items():
-            if not (x.shape == (rows,) and self._is(x, self._torch.int32) and (rows < 2 or x.stride(0) == 1)):
-                _refuse("%s must be contiguous int32 [%d] on %s" % (name, rows, self.device))
+    def _index_vector(self, name, x, rows):
+        """Pointer of an int32 [rows] operand."""
+        if x.dtype is self._i32 and x.shape == (rows,) and x.get_device() == self._index and (
+                rows < 2 or x.stride() == (1,)):
+            return x.data_ptr()
+        _refuse("%s must be contiguous int32 [%d] on %s" % (name, rows, self.device))
 
     def _table(self, table):
         """(pointer, rows, width, stride) of a page table."""
-        if table.dim() == 2 and self._is(table, self._torch.int32):
+        if table.dtype is self._i32 and table.get_device() == self._index and table.dim() == 2:
             rows, width = table.shape
             stride, page = table.stride()
             if page == 1 or width == 1:
                 return table.data_ptr(), rows, width, stride
         _refuse("table must be int32 [sequences][pages] on %s with contiguous rows" % self.device)
 
-    def _current(self, stream):
-        """The raw current stream if a call can go straight to it, else None."""
-        C = self._torch._C
-        if stream is None and C._cuda_getDevice() == self._index:
-            return C._cuda_getCurrentRawStream(self._index)
-        return None
-
     def append(self, k, v, table, seqs, positions, stream=None):
         """Store rows k, v (fp16 [rows][kv_heads][head_dim]) at positions[r] of sequence seqs[r] (int32 [rows]; < 0: skipped)."""
-        raw = self._current(stream)
-        if raw is None:
+        raw = self._raw_stream()
+        if stream is not None or raw is None:
             with _on(stream, self.device):
                 return self.append(k, v, table, seqs, positions)
         rows = k.shape[0]
         shape = (rows, self.kv_heads, self.head_dim)
-        ks, vs = self._strides("k", k, shape), self._strides("v", v, shape)
-        self._check_indices(rows, seqs=seqs, positions=positions)
-        st = lib.exq_cache_append(self.handle, k.data_ptr(), *ks, v.data_ptr(), *vs, rows, *self._table(table),
-                                  seqs.data_ptr(), positions.data_ptr(), raw)
+        k_row, k_head = self._strides("k", k, shape)
+        v_row, v_head = self._strides("v", v, shape)
+        tab, table_rows, width, table_stride = self._table(table)
+        st = lib.exq_cache_append(self.handle, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head, rows, tab,
+                                  table_rows, width, table_stride, self._index_vector("seqs", seqs, rows),
+                                  self._index_vector("positions", positions, rows), raw)
         if st:
             _check(st, "exq_cache_append")
 
@@ -518,21 +520,24 @@ class KVCache:
         """The values held for positions[r] of sequence seqs[r]: fp16 k, v [rows][kv_heads][head_dim].
 
         Rows with seqs[r] < 0 are left as they were in k_out and v_out (in tensors allocated here: unspecified)."""
-        raw = self._current(stream)
-        if raw is None:
+        raw = self._raw_stream()
+        if stream is not None or raw is None:
             with _on(stream, self.device):
                 return self.read(table, seqs, positions, k_out, v_out)
-        rows = seqs.shape[0]
-        shape = (rows, self.kv_heads, self.head_dim)
-        self._check_indices(rows, seqs=seqs, positions=positions)
-        torch = self._torch
+        rows, heads, dim = seqs.shape[0], self.kv_heads, self.head_dim
+        shape = (rows, heads, dim)
         if k_out is None:
-            k_out = torch.empty(shape, dtype=torch.float16, device=self.device)
+            k_out, k_row, k_head = self._empty(shape, (heads * dim, dim, 1), dtype=self._f16, device=self.device), heads * dim, dim
+        else:
+            k_row, k_head = self._strides("k_out", k_out, shape)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=torch.float16, device=self.device)
-        ks, vs = self._strides("k_out", k_out, shape), self._strides("v_out", v_out, shape)
-        st = lib.exq_cache_read(self.handle, k_out.data_ptr(), *ks, v_out.data_ptr(), *vs, rows, *self._table(table),
-                                seqs.data_ptr(), positions.data_ptr(), raw)
+            v_out, v_row, v_head = self._empty(shape, (heads * dim, dim, 1), dtype=self._f16, device=self.device), heads * dim, dim
+        else:
+            v_row, v_head = self._strides("v_out", v_out, shape)
+        tab, table_rows, width, table_stride = self._table(table)
+        st = lib.exq_cache_read(self.handle, k_out.data_ptr(), k_row, k_head, v_out.data_ptr(), v_row, v_head, rows, tab,
+                                table_rows, width, table_stride, self._index_vector("seqs", seqs, rows),
+                                self._index_vector("positions", positions, rows), raw)
         if st:
             _check(st, "exq_cache_read")
         return k_out, v_out
@@ -554,44 +559,50 @@ class KVCache:
         scale: default head_dim ** -0.5.  lengths[r] == 0 gives zeros (lse -inf); < 0 leaves the row as it was.
         workspace: from workspace(); by default the cache keeps one for each stream, and a call under graph capture makes
         one that belongs to the graph."""
-        raw = self._current(stream)
-        if raw is None:
+        raw = self._raw_stream()
+        if stream is not None or raw is None:
             with _on(stream, self.device):
                 return self.attend(q, table, lengths, scale, window, out, return_lse, lse, workspace)
-        torch = self._torch
-        if q.dim() != 3:
+        shape = q.shape
+        if len(shape) != 3:
             _refuse("q must be [rows][q_heads][head_dim]")
-        rows, q_heads = q.shape[0], q.shape[1]
-        shape = (rows, q_heads, self.head_dim)
-        qs = self._strides("q", q, shape)
+        rows, q_heads, dim = shape
+        q_row, q_head = self._strides("q", q, (rows, q_heads, self.head_dim))
         tab, table_rows, width, table_stride = self._table(table)
         if table_rows != rows:
             _refuse("table must have q's %d rows" % rows)
-        self._check_indices(rows, lengths=lengths)
         if out is None:
-            out = torch.empty(shape, dtype=torch.float16, device=self.device)
-        os = self._strides("out", out, shape)
+            out, out_row, out_head = self._empty(shape, (q_heads * dim, dim, 1), dtype=self._f16, device=self.device), q_heads * dim, dim
+        else:
+            out_row, out_head = self._strides("out", out, shape)
         if lse is not None:
-            if not (lse.shape == (rows, q_heads) and self._is(lse, torch.float32) and lse.is_contiguous()):
+            if not (lse.dtype is self._f32 and lse.shape == (rows, q_heads) and lse.get_device() == self._index
+                    and lse.is_contiguous()):
                 _refuse("lse must be contiguous fp32 [%d][%d] on %s" % (rows, q_heads, self.device))
+            lse_ptr = lse.data_ptr()
         elif return_lse:
-            lse = torch.empty((rows, q_heads), dtype=torch.float32, device=self.device)
-        need = lib.exq_attend_workspace_bytes(self.handle, rows, q_heads, width)
+            lse = self._empty((rows, q_heads), (q_heads, 1), dtype=self._f32, device=self.device)
+            lse_ptr = lse.data_ptr()
+        else:
+            lse_ptr = None
+        need = self._needs.get((rows, q_heads, width))
+        if need is None:
+            need = self._needs[rows, q_heads, width] = lib.exq_attend_workspace_bytes(self.handle, rows, q_heads, width)
+        ws_ptr, ws_bytes = None, 0
         if need:
             if workspace is None:
-                workspace = self._workspaces.get(raw)
-                if torch._C._cuda_isCurrentStreamCapturing():
+                if self._C._cuda_isCurrentStreamCapturing():
                     workspace = self.workspace(rows, q_heads, width)
-                elif workspace is None or workspace.numel() < need:
-                    workspace = self._workspaces[raw] = self.workspace(rows, q_heads, width)
+                else:
+                    workspace = self._workspaces.get(raw)
+                    if workspace is None or workspace.numel() < need:
+                        workspace = self._workspaces[raw] = self.workspace(rows, q_heads, width)
             elif not (workspace.get_device() == self._index and workspace.is_contiguous()):
                 _refuse("workspace must be contiguous on %s" % self.device)
-            wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        else:
-            wp, wn = None, 0
-        st = lib.exq_attend(self.handle, q.data_ptr(), *qs, rows, q_heads, tab, width, table_stride, lengths.data_ptr(),
-                            self.head_dim ** -0.5 if scale is None else scale, window, out.data_ptr(), *os,
-                            None if lse is None else lse.data_ptr(), wp, wn, raw)
+            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        st = lib.exq_attend(self.handle, q.data_ptr(), q_row, q_head, rows, q_heads, tab, width, table_stride,
+                            self._index_vector("lengths", lengths, rows), self._scale if scale is None else scale, window,
+                            out.data_ptr(), out_row, out_head, lse_ptr, ws_ptr, ws_bytes, raw)
         if st:
             _check(st, "exq_attend")
         return (out, lse) if return_lse else out
