@@ -429,8 +429,8 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  *   table      device int32 [rows][table_width], rows table_stride apart
  *   lengths    device int32 [rows].  0: out is 0 and lse -infinity.  Negative:
  *              a padding row, out and lse left as they were.  Above
- *              table_width * page_size, or a page outside the cache among those
- *              read: out and lse are NaN.
+ *              table_width * page_size or 2^31 - 2^16, or a page outside the cache
+ *              among those read: out and lse are NaN.
  *   scale      finite;  window >= 0
  *   out        device fp16 with strides as for q, no element twice, no overlap
  *              with q or the pages

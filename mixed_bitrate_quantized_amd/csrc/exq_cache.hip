@@ -5,8 +5,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
-#include <cstdio>
 #include <new>
 
 #include "exq_device_common.h"
@@ -472,7 +470,7 @@ constexpr int kCus = 256;
 constexpr int kAttendMaxSegments = 2048;   // more are not split: they load the card evenly enough
 constexpr int kAttendMaxParts = 32;        // parts of a segment
 constexpr int kAttendMaxWgs = kAttendMaxSegments + 2 * kCus;   // of a launch that splits
-constexpr int kJoinBatch = 8;              // parts whose loads a thread has in flight at once
+constexpr int kJoinBatch = 16;             // parts whose loads a thread has in flight at once
 
 // Waves per SIMD a geometry's kernel is compiled for: as many as its raw data,
 // query and sums leave registers for.
@@ -504,6 +502,9 @@ struct AttendArgs {
     int target;                // workgroups to split for; 0: a workgroup for each segment
 };
 
+// Longest row: tokens are counted in 32 bits, up to a few units past the end.
+constexpr int kMaxLength = 0x7FFF0000;
+
 // Tokens [lo, hi) that a row of length n attends to, and its number of units
 // of `unit` tokens from the one that holds lo.  Rows left alone have no unit;
 // empty rows and rows to be filled with NaN have one without tokens.
@@ -513,7 +514,8 @@ struct RowSpan {
 };
 __device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int n, int unit) {
     if (n < 0) return {0, 0, 0, false};
-    const uint64_t cap = (uint64_t)a.t.width * a.c.page_size;
+    uint64_t cap = (uint64_t)a.t.width * a.c.page_size;
+    if (cap > (uint64_t)kMaxLength) cap = (uint64_t)kMaxLength;
     if (n == 0 || (uint64_t)n > cap) return {0, 0, 1, n != 0};
     const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
     return {lo, n, (n - 1) / unit - lo / unit + 1, false};
@@ -544,12 +546,16 @@ __device__ __forceinline__ int wave_prefix(int v) {
     return v;
 }
 
+// Maximum over a wave's lanes, moved like the prefix sum.
 __device__ __forceinline__ int wave_max(int v) {
-    for (int m = 32; m >= 1; m >>= 1) {
-        const int o = __shfl_xor(v, m);
-        v = v > o ? v : o;
-    }
-    return uniform(v);
+    auto top = [](int a, int b) { return a > b ? a : b; };
+    v = top(v, __builtin_amdgcn_update_dpp(v, v, 0x111, 0xF, 0xF, false));
+    v = top(v, __builtin_amdgcn_update_dpp(v, v, 0x112, 0xF, 0xF, false));
+    v = top(v, __builtin_amdgcn_update_dpp(v, v, 0x114, 0xF, 0xF, false));
+    v = top(v, __builtin_amdgcn_update_dpp(v, v, 0x118, 0xF, 0xF, false));
+    v = top(v, __builtin_amdgcn_update_dpp(v, v, 0x142, 0xA, 0xF, false));
+    v = top(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xC, 0xF, false));
+    return __builtin_amdgcn_readlane(v, 63);
 }
 
 // One workgroup's work: chunk `chunk` of `chunks` of a segment (row, kv head,
@@ -693,23 +699,27 @@ __device__ __forceinline__ Joined join_parts(const float* slots, size_t floats, 
     return j;
 }
 
+// Each tile is read once: non-temporal loads (32 x 4000 tokens in 16 bits 89.6
+// us, with ordinary ones 96.9; 16 x 8192 in 8 bits 54.3 and 59.1).
+constexpr int kStreamed = 2;
+
 // Reads go through one buffer descriptor a tile: its address in scalar
 // registers, a lane's place as a 32-bit offset from a compile-time start.
 template <int WORDS>
 __device__ __forceinline__ void load_words(uint32_t* dst, __amdgpu_buffer_rsrc_t tile, int at, int start) {
     if constexpr (WORDS >= 4) {
-        const u4v v = __builtin_amdgcn_raw_buffer_load_b128(tile, at, start, 0);
+        const u4v v = __builtin_amdgcn_raw_buffer_load_b128(tile, at, start, kStreamed);
         dst[0] = v[0]; dst[1] = v[1]; dst[2] = v[2]; dst[3] = v[3];
         load_words<WORDS - 4>(dst + 4, tile, at, start + 16);
     } else if constexpr (WORDS == 3) {
         typedef uint32_t u3v __attribute__((ext_vector_type(3)));
-        const u3v v = __builtin_amdgcn_raw_buffer_load_b96(tile, at, start, 0);
+        const u3v v = __builtin_amdgcn_raw_buffer_load_b96(tile, at, start, kStreamed);
         dst[0] = v[0]; dst[1] = v[1]; dst[2] = v[2];
     } else if constexpr (WORDS == 2) {
-        const u2v v = __builtin_amdgcn_raw_buffer_load_b64(tile, at, start, 0);
+        const u2v v = __builtin_amdgcn_raw_buffer_load_b64(tile, at, start, kStreamed);
         dst[0] = v[0]; dst[1] = v[1];
     } else if constexpr (WORDS == 1) {
-        dst[0] = __builtin_amdgcn_raw_buffer_load_b32(tile, at, start, 0);
+        dst[0] = __builtin_amdgcn_raw_buffer_load_b32(tile, at, start, kStreamed);
     }
 }
 
@@ -748,7 +758,7 @@ __device__ __forceinline__ void load_keys(RawKeys<D, B>& r, __amdgpu_buffer_rsrc
         if constexpr (G % 2) {   // a token's scales start at an even half: by halves
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(tile, at, S + 2 * g, 0);
+                const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(tile, at, S + 2 * g, kStreamed);
                 r.s[g / 2] = g % 2 ? r.s[g / 2] | (v << 16) : v;
             }
         } else {
@@ -771,15 +781,17 @@ __device__ __forceinline__ h8 key_operand(const RawKeys<D, KB>& r, int g, const 
     if constexpr (KB == 16) {
         o = u4v{r.k.w[4 * g], r.k.w[4 * g + 1], r.k.w[4 * g + 2], r.k.w[4 * g + 3]};
     } else {
-        const uint32_t sw = r.s[g / 2], s = __builtin_amdgcn_perm(sw, sw, g % 2 ? 0x03020302u : 0x01000100u);
+        const h2 both = as_h2(r.s[g / 2]);
+        const h2 s = g % 2 ? __builtin_shufflevector(both, both, 1, 1) : __builtin_shufflevector(both, both, 0, 0);
         if constexpr (KB == 4) {
             const uint32_t w = r.k.w[g];
-            static_for<0, 4>([&](auto e) { o[e.value] = __builtin_bit_cast(uint32_t, nib.pair<e.value>(w) * as_h2(s)); });
+            static_for<0, 4>([&](auto e) { o[e.value] = __builtin_bit_cast(uint32_t, nib.pair<e.value>(w) * s); });
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t w = r.k.w[2 * g + e / 2];
-                o[e] = scaled(__builtin_amdgcn_perm(w, 0x64006400u, e % 2 ? 0x01070106u : 0x01050104u), kBiasedZero<8>, s);
+                const uint32_t x = __builtin_amdgcn_perm(w, 0x64006400u, e % 2 ? 0x01070106u : 0x01050104u);
+                o[e] = __builtin_bit_cast(uint32_t, (as_h2(x) - as_h2(kBiasedZero<8>)) * s);
             }
         }
     }
@@ -846,10 +858,10 @@ template <int D, int KB, int VB> struct AttendWave {
     }
     __device__ __forceinline__ float reference() const { return limit < 0.0f ? -3e38f : r; }
 
-    // The first half of a step: weights of the 32 tokens of two tiles.  ta, tb:
-    // the lane's first token of each; partial: some lie outside [lo, hi).
+    // The first half of a step: weights of the 32 tokens of two tiles, one after
+    // the other.  ta: the lane's first token; partial: some lie outside [lo, hi).
     __device__ __forceinline__ h8 weights(const RawKeys<D, KB>& a, const RawKeys<D, KB>& b, float c, bool partial,
-                                          int ta, int tb, int lo, int hi) {
+                                          int ta, int lo, int hi) {
         f4 sa = {0, 0, 0, 0}, sb = {0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -863,10 +875,14 @@ template <int D, int KB, int VB> struct AttendWave {
             t[4 + i] = __builtin_fmaf(sb[i], c, -r);
         }
         if (partial) {
+            // token - lo, against the span's length: made here from a value the
+            // compiler does not see through, so that steps inside the span pay nothing
+            uint32_t at = (uint32_t)(ta - lo);
+            asm volatile("" : "+v"(at));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (ta + i < lo || ta + i >= hi) t[i] = -__builtin_inff();
-                if (tb + i < lo || tb + i >= hi) t[4 + i] = -__builtin_inff();
+                if (at + (uint32_t)i >= (uint32_t)(hi - lo)) t[i] = -__builtin_inff();
+                if (at + (uint32_t)(16 + i) >= (uint32_t)(hi - lo)) t[4 + i] = -__builtin_inff();
             }
         }
         float m = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(t[0], t[1]), __builtin_fmaxf(t[2], t[3])),
@@ -1017,7 +1033,7 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
             pb = tile_at(tile_b, next);
             const int token = (first_unit + i) * UNIT + my;
             const bool partial = token < span.lo || token + 32 > span.hi;
-            const h8 weights = W.weights(ka, kb, a.scale, partial, token + 4 * quad, token + 16 + 4 * quad, span.lo, span.hi);
+            const h8 weights = W.weights(ka, kb, a.scale, partial, token + 4 * quad, span.lo, span.hi);
             __builtin_amdgcn_sched_barrier(0);   // not before the keys' registers are free
             load_keys(ka, pa, lane);
             load_keys(kb, pb, lane);
@@ -1262,18 +1278,26 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     if (segments > 0x7FFFFFFFll || (int64_t)rows * q_heads > 0x7FFFFFFFll)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, q_heads);
     const int64_t tokens = (int64_t)table_width * c->page_size;   // of the longest row
-    const char* e = getenv("EXQ_TUNE");   // "few_waves,few_target,few_whole_tokens,many_target,many_whole_tokens,many_from"
-    int few_waves = 8, few_target = 256, few_whole = 1024, many_target = 512, many_whole = 4096, many_from = 256;
-    if (e) sscanf(e, "%d,%d,%d,%d,%d,%d", &few_waves, &few_target, &few_whole, &many_target, &many_whole, &many_from);
-    const bool many = segments >= many_from;
-    const int per_simd = attend_waves_per_simd(c->head_dim, c->k_bits, c->v_bits);
-    out->waves = many || per_simd == 1 ? 4 : few_waves;
+    // Few segments of long rows: workgroups of 8 waves, one a CU, so that a
+    // segment has half as many parts to join (131072 tokens of 8 heads at 4
+    // bits 40 us, with 4 waves 53; but 8192 tokens 13.8, with 4 waves 13.7,
+    // and 2 x 8192 15.6 against 14.0).  With 64 segments or more, twice as
+    // many workgroups as CUs balance rows of different lengths (16 ragged rows
+    // of up to 8192 tokens 27 us, with one a CU 36; equal rows of 4096 tokens
+    // 24.9 against 25.9); below that they only add parts (4 x 4096 tokens 15.1
+    // against 13.9).
+    const bool eight = segments < 64 && tokens >= 32768 && attend_waves_per_simd(c->head_dim, c->k_bits, c->v_bits) > 1;
+    out->waves = eight ? 8 : 4;
     out->head_tiles = (int)tiles;
     const int unit = 32 * out->waves;
     const int64_t units = (tokens - 1) / unit + 1;
-    out->whole_units = (many ? many_whole : few_whole) / unit;
+    // Rows that are not worth splitting: joining their parts costs what 1024
+    // tokens cost (one row of 1000 tokens 11.3 us whole, 16.1 split), and with
+    // a segment for each CU twice that (32 x 2000 tokens 21.8 us whole, 24.8
+    // split; at 16 x 2000 tokens 20.7 and 17.6).
+    out->whole_units = (segments >= kCus ? 2048 : 1024) / unit;
     const bool split = units > out->whole_units && segments <= kAttendMaxSegments;
-    out->target = split ? (many ? many_target : few_target) : 0;
+    out->target = split ? (segments >= 64 ? 2 * kCus : kCus) : 0;
     out->wgs = split ? (int)std::min<int64_t>(out->target + segments, std::max<int64_t>(segments, 1) * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
     out->ws_bytes = split ? kCounterBytes + (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
