@@ -398,7 +398,7 @@ void exq_cache_destroy(exq_cache_t cache);
  *              mixture of both.
  * Nothing but the bytes of those rows is written.  rows == 0 is a no-op.
  * Errors: INVALID_ARG (NULL, misaligned, bad size or stride, k or v overlapping
- * the pages), UNSUPPORTED (rows * heads beyond a launch's 2^31 - 1 workgroups), HIP. */
+ * the pages), UNSUPPORTED (rows * heads beyond a launch's 2^32 threads), HIP. */
 exq_status exq_cache_append(exq_cache_t cache, const void* k, int64_t k_row_stride, int64_t k_head_stride,
                             const void* v, int64_t v_row_stride, int64_t v_head_stride, int rows,
                             const int32_t* table, int table_rows, int table_width, int64_t table_stride,
@@ -431,7 +431,7 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  *              a padding row, out and lse left as they were.  Above
  *              table_width * page_size or 2^31 - 2^16, or a page outside the cache
  *              among those read: out and lse are NaN.
- *   scale      finite;  window >= 0
+ *   scale      finite, magnitude below 2^127;  window >= 0
  *   out        device fp16 with strides as for q, no element twice, no overlap
  *              with q or the pages
  *   lse        device fp32 [rows][q_heads] or NULL
@@ -445,10 +445,14 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  * reaches the result, NaN included.  Scores, softmax sums and output sums are
  * fp32; the weights e^{S_j - max} enter the second product rounded to fp16.
  * The order of summation depends on the sizes and lengths only: deterministic.
- * Accuracy, with S_j the exact scores, A = max_j |scale| sum_d |q_d K_hat_jd| and
- * P = sum_j e^{S_j} |V_hat_j| / sum_j e^{S_j} the average of the magnitudes:
- *   |out - out_ref| <= (2^-10 + 2^-14 + 2^-17 A) P + 2^-11 |out_ref| + 2^-24
- *   |lse - lse_ref| <= 2^-18 (1 + A) + 2^-22 |lse_ref|
+ * Accuracy for n tokens, with S_j the exact scores, A = max_j |scale| sum_d |q_d
+ * K_hat_jd| and P = sum_j e^{S_j} |V_hat_j| / sum_j e^{S_j} the average of the
+ * magnitudes:
+ *   |out - out_ref| <= (2^-11 + 2^-14 + n 2^-25 + (D + 8) 2^-23 A) P
+ *                      + 2^-32 sum_j |V_hat_j| + 2^-11 |out_ref| + 2^-24
+ *   |lse - lse_ref| <= (D + 8) 2^-24 A + n 2^-27 + 2^-19 + 2^-22 |lse_ref|
+ * (weights rounded to fp16, sums of n and of D = head_dim terms in fp32, weights
+ * below 2^-32 of the largest lost, the output's rounding).
  * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, HIP. */
 exq_status exq_attend(exq_cache_t cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int rows,
                       int q_heads, const int32_t* table, int table_width, int64_t table_stride,

@@ -43,6 +43,12 @@ template <int D, int B> struct CachePart {
     }
 };
 
+// Bytes of one token of one head.
+constexpr int row_bytes(int head_dim, int k_bits, int v_bits) {
+    const int scales = 2 * (head_dim / kCacheGroup);
+    return head_dim * k_bits / 8 + head_dim * v_bits / 8 + (k_bits < 16 ? scales : 0) + (v_bits < 16 ? scales : 0);
+}
+
 // What the kernels know about a cache.
 struct CacheDev {
     uint8_t* pages;
@@ -102,15 +108,17 @@ struct RowPlace {
     int token;
 };
 
+// Row r's place (r < 0: none); ahead(): loads to ask for once the page's is.
+template <class F>
 __device__ __forceinline__ RowPlace row_place(const CacheDev& c, const TableDev& t, const int32_t* seqs,
-                                              const int32_t* positions, int r, int tile_bytes) {
-    const int32_t s = gptr<int32_t>(seqs)[r], p = gptr<int32_t>(positions)[r];
-    if (s < 0) return {-1, 0};
-    if ((uint32_t)s >= t.rows || p < 0) return {-2, 0};
+                                              const int32_t* positions, int r, int tile_bytes, F&& ahead) {
+    const int32_t s = r >= 0 ? gptr<int32_t>(seqs)[r] : -1, p = r >= 0 ? gptr<int32_t>(positions)[r] : 0;
     const uint32_t pi = (uint32_t)p / c.page_size, in = (uint32_t)p % c.page_size;
-    if (pi >= t.width) return {-2, 0};
-    const uint32_t page = (uint32_t)gptr<int32_t>(t.pages)[(int64_t)s * t.stride + pi];
-    if (page >= c.n_pages) return {-2, 0};
+    const bool inside = s >= 0 && (uint32_t)s < t.rows && p >= 0 && pi < t.width;
+    const uint32_t page = inside ? (uint32_t)gptr<int32_t>(t.pages)[(int64_t)s * t.stride + pi] : 0u;
+    ahead();
+    if (s < 0) return {-1, 0};
+    if (!inside || page >= c.n_pages) return {-2, 0};
     return {(int64_t)page * c.page_bytes + (int64_t)(in / kCacheTile) * tile_bytes, (int)(in % kCacheTile)};
 }
 
@@ -124,6 +132,14 @@ __device__ __forceinline__ RowPlace row_place(const CacheDev& c, const TableDev&
 // wherever the prompt starts.
 constexpr int kRowsThreads = 256;
 
+// Orders a wave's own LDS writes before its reads, and its reads before its
+// next writes.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The rows of a lane and where they lie.
 struct RowsBlock {
     int row, head;     // row < 0: none
@@ -131,15 +147,17 @@ struct RowsBlock {
     bool tile;         // the wave's 16 rows are the 16 tokens of one tile, in order
 };
 
+// ahead(b): loads that do not wait for the rows' places.
+template <class F>
 __device__ __forceinline__ RowsBlock rows_block(const CacheDev& c, const TableDev& t, const int32_t* seqs,
-                                                const int32_t* positions, int rows, int tile_bytes) {
+                                                const int32_t* positions, int rows, int tile_bytes, F&& ahead) {
     RowsBlock b;
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int64_t i = (int64_t)blockIdx.x * (kRowsThreads / 64) + wave;
     b.head = (int)(i % c.kv_heads);
     const int64_t r = i / c.kv_heads * kCacheTile - (gptr<int32_t>(positions)[0] & (kCacheTile - 1)) + (lane & 15);
     b.row = r >= 0 && r < rows ? (int)r : -1;
-    b.place = b.row >= 0 ? row_place(c, t, seqs, positions, b.row, tile_bytes) : RowPlace{-1, 0};
+    b.place = row_place(c, t, seqs, positions, b.row, tile_bytes, [&] { ahead(b); });
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b.place.at);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)b.place.at >> 32));
     const bool same = b.place.at >= 0 && b.place.token == (lane & 15) && (uint64_t)b.place.at == (((uint64_t)hi << 32) | lo);
@@ -174,11 +192,14 @@ __device__ __forceinline__ void group_max(const u4v (&x)[G], uint32_t (&m)[(G + 
     }
 }
 
-// A group's scale from its max|x|: fp16 bits.
+// A group's scale from its max|x|: fp16 bits.  The quotient by 7 or 127 with
+// one Newton step, as below: no quotient of an 11-bit number by these lies
+// within 2^-46 of a tie of fp32, so it is the correctly rounded one.
 template <int B> __device__ __forceinline__ uint32_t scale_bits(uint32_t max_bits) {
-    constexpr float top = (float)((1 << (B - 1)) - 1);
-    if (max_bits >= 0x7C00u) return 0x7E00u;
-    return f32_to_f16_bits((float)__builtin_bit_cast(_Float16, (uint16_t)max_bits) / top);
+    constexpr float top = (float)((1 << (B - 1)) - 1), inv = 1.0f / top;
+    const float m = (float)__builtin_bit_cast(_Float16, (uint16_t)max_bits);
+    const float q0 = m * inv, q = __builtin_fmaf(__builtin_fmaf(-q0, top, m), inv, q0);
+    return max_bits >= 0x7C00u ? 0x7E00u : (uint32_t)f32_to_f16_bits(q);
 }
 
 // Codes of eight values at scale s.  The quotient x / s: one Newton step on
@@ -190,17 +211,22 @@ template <int B> __device__ __forceinline__ uint32_t scale_bits(uint32_t max_bit
 template <int B> __device__ __forceinline__ void codes_of(const u4v& x, uint32_t s_bits, uint32_t (&c)[8]) {
     constexpr float top = (float)((1 << (B - 1)) - 1), magic = 12582912.0f + (float)(1 << (B - 1));
     const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)s_bits);
-    const bool live = s > 0.0f;   // not for zero or NaN scales: all codes are the zero point
-    const float inv = live ? __builtin_amdgcn_rcpf(s) : 0.0f;
+    // zero scale: every quotient 0; NaN scale: codes that say nothing
+    const float inv = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const uint32_t w = x[e / 2];
         const float f = (float)as_h2(w)[e % 2];
-        const float q0 = f * inv;
-        float q = __builtin_fmaf(__builtin_fmaf(-q0, s, f), inv, q0);
-        q = live ? q : 0.0f;
+        const float q0 = f * inv, q = __builtin_fmaf(__builtin_fmaf(-q0, s, f), inv, q0);
         c[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(q, -top, top) + magic) & ((1u << B) - 1u);
     }
+}
+
+// Four nibbles of the low half of x, one to a byte.
+__device__ __forceinline__ uint32_t spread(uint32_t x) {
+    uint32_t t = x & 0xFFFFu;
+    t = (t | (t << 8)) & 0x00FF00FFu;
+    return (t | (t << 4)) & 0x0F0F0F0Fu;
 }
 
 template <int D, int KB, int VB>
@@ -214,19 +240,18 @@ __global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableD
     using PV = CachePart<D, VB>;
     constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES;
     __shared__ __attribute__((aligned(16))) uint8_t turned[kRowsThreads / 64][PV::CODES];
-    const RowsBlock b = rows_block(c, t, seqs, positions, rows, TILE);
-    if (__builtin_amdgcn_ballot_w64(b.place.at >= 0) == 0) return;
     const int lane = (int)threadIdx.x & 63, q = lane >> 4;
-    uint8_t* buf = turned[threadIdx.x >> 6];
     u4v kx[G], vx[G];
-    {
-        const int64_t r = b.place.at >= 0 ? b.row : 0;   // rows that go nowhere are not read
+    const RowsBlock b = rows_block(c, t, seqs, positions, rows, TILE, [&](const RowsBlock& b) {
+        const int64_t r = b.row >= 0 ? b.row : 0;
         const uint16_t *ks = k + r * k_row + b.head * k_head + 8 * q, *vs = v + r * v_row + b.head * v_head + 8 * q;
 #pragma unroll
         for (int g = 0; g < G; ++g) kx[g] = *gptr<u4v>(ks + g * kCacheGroup);
 #pragma unroll
         for (int g = 0; g < G; ++g) vx[g] = *gptr<u4v>(vs + g * kCacheGroup);
-    }
+    });
+    if (__builtin_amdgcn_ballot_w64(b.place.at >= 0) == 0) return;
+    uint8_t* buf = turned[threadIdx.x >> 6];
     uint8_t* tile = c.pages + (b.place.at >= 0 ? b.place.at : 0) + (int64_t)b.head * c.tiles * TILE;
     const bool live = b.place.at >= 0;
     const int tok = b.place.token;
@@ -272,59 +297,76 @@ __global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableD
         }
     }
 
-    // values
+    // values: the bytes (16 bits: halves) of the lane's channels, two (four)
+    // dwords a group
     uint8_t* part = tile + PK::BYTES;
-    uint32_t m[(G + 1) / 2];
-    if constexpr (VB < 16) group_max<G>(vx, m);
-    const int t4 = tok % 4, col0 = 8 * (q % 2), half = q / 2;
+    const int t4 = tok % 4, half = q / 2;
+    constexpr int WORDS = VB == 16 ? 4 : 2;
+    uint32_t w[G][WORDS];
+    if constexpr (VB == 16) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        uint32_t code[8], s = 0;
-        if constexpr (VB < 16) {
-            s = scale_bits<VB>((m[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
-            codes_of<VB>(vx[g], s, code);
-        }
-        if constexpr (VB == 4) {
-            // channels c and c + 16 share a byte: lanes q = 2, 3 hand theirs to q = 0, 1
-            uint32_t x = 0;
+        for (int g = 0; g < G; ++g)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x |= code[e] << (4 * e);
-            const uint32_t y = (uint32_t)__shfl_xor((int)x, 32);
+            for (int i = 0; i < 4; ++i) w[g][i] = vx[g][i];
+    } else {
+        uint32_t m[(G + 1) / 2], s[G];
+        group_max<G>(vx, m);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) code[e] = ((x >> (4 * e)) & 15u) | (((y >> (4 * e)) & 15u) << 4);
-        }
+        for (int g = 0; g < G; ++g) {
+            s[g] = scale_bits<VB>((m[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
+            uint32_t c8[8];
+            codes_of<VB>(vx[g], s[g], c8);
+            if constexpr (VB == 4) {
+                // channels c and c + 16 share a byte: lanes q = 2, 3 hand theirs to q = 0, 1
+                uint32_t x = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int at = PV::unit(16 * (tok / 4) + col0 + e, g);
-            if constexpr (VB == 16) {
-                const uint32_t w = vx[g][e / 2];
-                const uint16_t x = (uint16_t)(e % 2 ? w >> 16 : w);
-                if (b.tile) *reinterpret_cast<uint16_t*>(buf + at + 8 * half + 2 * t4) = x;
-                else if (live) *gptr_w<uint16_t>(part + at + 8 * half + 2 * t4) = x;
+                for (int e = 0; e < 8; ++e) x |= c8[e] << (4 * e);
+                const uint32_t y = (uint32_t)__shfl_xor((int)x, 32);
+                w[g][0] = spread(x) | (spread(y) << 4);
+                w[g][1] = spread(x >> 16) | (spread(y >> 16) << 4);
             } else {
-                const int inner = VB == 4 ? 2 * (t4 % 2) + t4 / 2 : 4 * half + t4;
-                const bool mine = VB == 8 || half == 0;
-                if (b.tile) {
-                    if (mine) buf[at + inner] = (uint8_t)code[e];
-                } else if (live && mine) {
-                    *gptr_w<uint8_t>(part + at + inner) = (uint8_t)code[e];
-                }
+                w[g][0] = c8[0] | (c8[1] << 8) | (c8[2] << 16) | (c8[3] << 24);
+                w[g][1] = c8[4] | (c8[5] << 8) | (c8[6] << 16) | (c8[7] << 24);
             }
         }
-        if constexpr (VB < 16) {
-            if (live && q == g % 4) *gptr_w<uint16_t>(part + PV::CODES + 8 * G * (tok / 4) + 8 * g + 2 * t4) = (uint16_t)s;
+        // (a row's four lanes hold the same scales: lane q = 0 stores them)
+        if (live && q == 0) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                gptr_w<uint16_t>(part + PV::CODES + 8 * G * (tok / 4) + 2 * t4)[4 * g] = (uint16_t)s[g];
         }
     }
+    // Element e of group g goes to the unit of lane 16 (tok / 4) + 8 (q % 2) + e.
+    const int unit_lane = 16 * (tok / 4) + 8 * (q % 2);
+    const int inner = VB == 4 ? 2 * (t4 % 2) + t4 / 2 : VB == 8 ? 4 * half + t4 : 8 * half + 2 * t4;
+    auto scatter = [&](auto put) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = PV::unit(unit_lane, g) + e * (PV::chunk_groups(g / PV::GPC) * VB) + inner;
+                put(at, VB == 16 ? w[g][e / 2] >> (16 * (e % 2)) : w[g][e / 4] >> (8 * (e % 4)));
+            }
+    };
+    const bool mine = live && (VB != 4 || half == 0);
     if (b.tile) {
-        // the wave's own LDS: its writes are done before its reads
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (mine) {
+            scatter([&](int at, uint32_t x) {
+                if constexpr (VB == 16) *reinterpret_cast<uint16_t*>(buf + at) = (uint16_t)x;
+                else buf[at] = (uint8_t)x;
+            });
+        }
+        wave_lds_fence();
 #pragma unroll
         for (int i = 0; i < (PV::CODES + 1023) / 1024; ++i) {
             const int at = 1024 * i + 16 * lane;
             if (PV::CODES % 1024 == 0 || at < PV::CODES) *gptr_w<u4v>(part + at) = *reinterpret_cast<const u4v*>(buf + at);
         }
+    } else if (mine) {
+        scatter([&](int at, uint32_t x) {
+            if constexpr (VB == 16) *gptr_w<uint16_t>(part + at) = (uint16_t)x;
+            else *gptr_w<uint8_t>(part + at) = (uint8_t)x;
+        });
     }
 }
 
@@ -341,7 +383,7 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
     using PV = CachePart<D, VB>;
     constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES, PITCH = D + 8;
     __shared__ __attribute__((aligned(16))) uint16_t turned[kRowsThreads / 64][kCacheTile][PITCH];
-    const RowsBlock b = rows_block(c, t, seqs, positions, rows, TILE);
+    const RowsBlock b = rows_block(c, t, seqs, positions, rows, TILE, [](const RowsBlock&) {});
     if (__builtin_amdgcn_ballot_w64(b.place.at != -1) == 0) return;
     const int lane = (int)threadIdx.x & 63, q = lane >> 4;
     const bool live = b.place.at >= 0, written = b.place.at != -1;
@@ -404,11 +446,27 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
                 }
             }
         }
-        if (written) *gptr_w<u4v>(kd + g * kCacheGroup) = live ? o : nan;
+        if (b.tile) *reinterpret_cast<u4v*>(&buf[lane & 15][kCacheGroup * g + 8 * q]) = o;
+        else if (written) *gptr_w<u4v>(kd + g * kCacheGroup) = live ? o : nan;
     }
+
+    // A tile's rows leave as whole rows, one after the other: written from the
+    // lanes that hold them, in runs of 64 bytes, 32768 rows at 4 bits took 45 us
+    // and now take 37.
+    auto store_tile = [&](uint16_t* dst, int64_t row_stride, int64_t head_stride) {
+        wave_lds_fence();
+        uint16_t* first = dst + (int64_t)(b.row - (lane & 15)) * row_stride + b.head * head_stride;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            const int at = 64 * i + lane, r = at / (D / 8), d = at % (D / 8) * 8;
+            *gptr_w<u4v>(first + r * row_stride + d) = *reinterpret_cast<const u4v*>(&buf[r][d]);
+        }
+        wave_lds_fence();
+    };
 
     // values
     if (b.tile) {
+        store_tile(k, k_row, k_head);
         // the lane's four tokens of channels 32 g + col and 32 g + 16 + col, turned in the wave's own LDS
         const int col = lane & 15;
 #pragma unroll
@@ -431,12 +489,7 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
                 for (int i = 0; i < 4; ++i)
                     buf[4 * q + i][kCacheGroup * g + 16 * h + col] = (uint16_t)(i % 2 ? x[i / 2] >> 16 : x[i / 2]);
             }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            *gptr_w<u4v>(vd + g * kCacheGroup) = *reinterpret_cast<const u4v*>(&buf[lane & 15][kCacheGroup * g + 8 * q]);
+        store_tile(v, v_row, v_head);
     } else if (written) {
         const int t4 = tok % 4, col0 = 8 * (q % 2), half = q / 2;
 #pragma unroll
@@ -468,6 +521,7 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
 
 constexpr int kCus = 256;
 constexpr int kAttendMaxSegments = 2048;   // more are not split: they load the card evenly enough
+constexpr int kAttendMaxRows = 256;        // likewise
 constexpr int kAttendMaxParts = 32;        // parts of a segment
 constexpr int kAttendMaxWgs = kAttendMaxSegments + 2 * kCus;   // of a launch that splits
 constexpr int kJoinBatch = 16;             // parts whose loads a thread has in flight at once
@@ -477,6 +531,9 @@ constexpr int kJoinBatch = 16;             // parts whose loads a thread has in 
 constexpr int attend_waves_per_simd(int D, int KB, int VB) {
     return D <= 96 ? 4 : D == 128 ? (KB + VB <= 8 ? 4 : 3) : KB + VB <= 16 ? 2 : 1;
 }
+
+// Geometries that have a kernel of 8 waves a workgroup beside the one of 4.
+constexpr bool attend_light(int D, int KB, int VB) { return row_bytes(D, KB, VB) <= 208; }
 
 // The workspace starts with the arrival counters of segments (at their first
 // workgroup's number), zero between launches.
@@ -1147,11 +1204,6 @@ exq_status check_geometry(int page_size, int kv_heads, int head_dim, int k_bits,
     return EXQ_OK;
 }
 
-int row_bytes(int head_dim, int k_bits, int v_bits) {
-    const int scales = 2 * (head_dim / kCacheGroup);
-    return head_dim * k_bits / 8 + head_dim * v_bits / 8 + (k_bits < 16 ? scales : 0) + (v_bits < 16 ? scales : 0);
-}
-
 CacheDev cache_dev(const exq_cache* c) {
     return CacheDev{c->pages, (int64_t)c->page_bytes, (uint32_t)c->n_pages, (uint32_t)c->page_size, (uint32_t)c->kv_heads,
                     (uint32_t)(c->page_size / kCacheTile)};
@@ -1230,6 +1282,8 @@ void with_geometry(const exq_cache* c, F&& f) {
     }
 }
 
+constexpr int64_t kMaxLaunchThreads = 0xFFFFFFFFll;
+
 exq_status launched(const char* what) {
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? EXQ_OK : fail(EXQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
@@ -1256,7 +1310,7 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
     const size_t bytes = (size_t)c->n_pages * c->page_bytes;
     if (ranges_meet(k.p, extent(k), c->pages, bytes) || ranges_meet(v.p, extent(v), c->pages, bytes))
         return fail(EXQ_ERR_INVALID_ARG, "k or v overlaps the cache's pages");
-    if (rows_waves(c, rows) > 0x7FFFFFFFll)
+    if (rows_waves(c, rows) > kMaxLaunchThreads / 64 - 8)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, c->kv_heads);
     return EXQ_OK;
 }
@@ -1275,18 +1329,14 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     if (table_width < 1) return fail(EXQ_ERR_INVALID_ARG, "table_width=%d", table_width);
     const int group = q_heads / c->kv_heads;
     const int64_t tiles = (int64_t)c->kv_heads * ((group + 15) / 16), segments = tiles * rows;
-    if (segments > 0x7FFFFFFFll || (int64_t)rows * q_heads > 0x7FFFFFFFll)
+    if (segments > kMaxLaunchThreads / 256)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, q_heads);
     const int64_t tokens = (int64_t)table_width * c->page_size;   // of the longest row
-    // Few segments of long rows: workgroups of 8 waves, one a CU, so that a
-    // segment has half as many parts to join (131072 tokens of 8 heads at 4
-    // bits 40 us, with 4 waves 53; but 8192 tokens 13.8, with 4 waves 13.7,
-    // and 2 x 8192 15.6 against 14.0).  With 64 segments or more, twice as
-    // many workgroups as CUs balance rows of different lengths (16 ragged rows
-    // of up to 8192 tokens 27 us, with one a CU 36; equal rows of 4096 tokens
-    // 24.9 against 25.9); below that they only add parts (4 x 4096 tokens 15.1
-    // against 13.9).
-    const bool eight = segments < 64 && tokens >= 32768 && attend_waves_per_simd(c->head_dim, c->k_bits, c->v_bits) > 1;
+    // Workgroups of 8 waves, one a CU, for few segments of long rows whose steps
+    // are light: a segment has half as many parts to join (at 4 bits, 131072
+    // tokens of 8 heads 38 us, with 4 waves 53; 4 x 16384 25.8 and 29.2; but 4
+    // x 4096 15.9 and 14.2; at 8 bits 4 x 16384 33.6 and 32.2).
+    const bool eight = segments < 64 && tokens >= 16384 && attend_light(c->head_dim, c->k_bits, c->v_bits);
     out->waves = eight ? 8 : 4;
     out->head_tiles = (int)tiles;
     const int unit = 32 * out->waves;
@@ -1294,9 +1344,15 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // Rows that are not worth splitting: joining their parts costs what 1024
     // tokens cost (one row of 1000 tokens 11.3 us whole, 16.1 split), and with
     // a segment for each CU twice that (32 x 2000 tokens 21.8 us whole, 24.8
-    // split; at 16 x 2000 tokens 20.7 and 17.6).
+    // split; at 16 x 2000 tokens 20.7 and 17.6).  Very many load the card
+    // evenly enough as they are, and every workgroup would look through all
+    // rows' lengths.
     out->whole_units = (segments >= kCus ? 2048 : 1024) / unit;
-    const bool split = units > out->whole_units && segments <= kAttendMaxSegments;
+    const bool split = units > out->whole_units && segments <= kAttendMaxSegments && rows <= kAttendMaxRows;
+    // With 64 segments or more, two workgroups a CU balance rows of different
+    // lengths (16 ragged rows of up to 8192 tokens 27 us, with one a CU 36;
+    // equal rows of 4096 tokens 24.9 against 25.9); below that they only add
+    // parts (4 x 4096 tokens 15.1 against 13.9).
     out->target = split ? (segments >= 64 ? 2 * kCus : kCus) : 0;
     out->wgs = split ? (int)std::min<int64_t>(out->target + segments, std::max<int64_t>(segments, 1) * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
@@ -1396,7 +1452,7 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     AttendPlan p;
     exq_status st = plan_attend(c, rows, q_heads, table_width, &p);
     if (st != EXQ_OK) return st;
-    if (!std::isfinite(scale)) return fail(EXQ_ERR_INVALID_ARG, "scale is not finite");
+    if (!std::isfinite(scale * kLog2e)) return fail(EXQ_ERR_INVALID_ARG, "scale=%g is not finite or too large", (double)scale);
     if (window < 0) return fail(EXQ_ERR_INVALID_ARG, "window=%d", window);
     if (rows == 0) return EXQ_OK;
     if ((st = check_table(table, rows, table_width, table_stride)) != EXQ_OK) return st;
@@ -1443,11 +1499,16 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.whole_units = p.whole_units;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     with_geometry(c, [&](auto D, auto KB, auto VB) {
-        constexpr int FEW = attend_waves_per_simd(D.value, KB.value, VB.value) == 1 ? 4 : 8;
-        if (p.waves == FEW)
-            hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value, FEW>), dim3((unsigned)p.wgs), dim3(64 * FEW), 0, s, a);
-        else
-            hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value, 4>), dim3((unsigned)p.wgs), dim3(256), 0, s, a);
+        auto launch = [&](auto NW) {
+            hipLaunchKernelGGL((attend_kernel<D.value, KB.value, VB.value, NW.value>), dim3((unsigned)p.wgs), dim3(64 * NW.value), 0, s, a);
+        };
+        if constexpr (attend_light(D.value, KB.value, VB.value)) {
+            if (p.waves == 8) {
+                launch(IC<8>{});
+                return;
+            }
+        }
+        launch(IC<4>{});
     });
     return launched("attend launch");
 }

@@ -163,6 +163,8 @@ def attend(q, k, v, scale):
             out[h] = w @ vh / l
             lse[h] = m + np.log(l)
             P = w @ np.abs(vh) / l
-            bo[h] = (2.0 ** -10 + 2.0 ** -14 + 2.0 ** -17 * A) * P + 2.0 ** -11 * np.abs(out[h]) + 2.0 ** -24
-            bl[h] = 2.0 ** -18 * (1 + A) + 2.0 ** -22 * np.abs(lse[h])
+            n = k.shape[0]
+            bo[h] = ((2.0 ** -11 + 2.0 ** -14 + n * 2.0 ** -25 + (dim + 8) * 2.0 ** -23 * A) * P
+                     + 2.0 ** -32 * np.abs(vh).sum(0) + 2.0 ** -11 * np.abs(out[h]) + 2.0 ** -24)
+            bl[h] = (dim + 8) * 2.0 ** -24 * A + n * 2.0 ** -27 + 2.0 ** -19 + 2.0 ** -22 * np.abs(lse[h])
     return out, lse, bo, bl

@@ -128,7 +128,7 @@ def attend_args(**kw):
 
 BAD_ATTEND = [dict(q=0), dict(q=Q + 4), dict(qs=(508, 64)), dict(qs=(512, -8)), dict(rows=-1), dict(heads=0), dict(heads=6),
               dict(heads=-4), dict(table=0), dict(width=0), dict(tstride=399), dict(lengths=0), dict(lengths=S + 2),
-              dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1), dict(out=0), dict(out=O + 2),
+              dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(window=-1), dict(out=0), dict(out=O + 2),
               dict(os=(0, 64)), dict(os=(512, 32)), dict(out=Q), dict(out=Q + 64), dict(out=FAKE), dict(lse=L + 2),
               dict(lse=O), dict(lse=Q), dict(lse=FAKE + 64), dict(ws=0), dict(ws=W + 8), dict(wsb=100), dict(ws=O), dict(ws=Q),
               dict(ws=FAKE), dict(ws=L)]
@@ -142,6 +142,7 @@ def test_attend_rejects(cache, bad):
 def test_attend_rejects_null_cache_and_too_many_rows(cache):
     expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_attend, None, *attend_args())
     expect(exq.EXQ_ERR_UNSUPPORTED, exq.exq_attend, cache, *attend_args(rows=(1 << 31) - 1, heads=64))
+    expect(exq.EXQ_ERR_UNSUPPORTED, exq.exq_attend, cache, *attend_args(rows=1 << 22, heads=4))    # 2^24 workgroups of 256
     assert exq.exq_attend_workspace_bytes(None, 1, 8, 4) == 0
     assert exq.exq_attend_workspace_bytes(cache, 1, 6, 4) == 0
     assert exq.exq_attend_workspace_bytes(cache, 1, 8, 0) == 0
@@ -150,10 +151,10 @@ def test_attend_rejects_null_cache_and_too_many_rows(cache):
 def test_workspace_is_bounded_and_grows_with_the_split(cache):
     one = exq.exq_attend_workspace_bytes(cache, 1, 8, 1)        # 32 tokens: nothing to split
     assert one == 0
-    sizes = [exq.exq_attend_workspace_bytes(cache, r, 8, w) for r, w in ((1, 1000), (16, 1000), (512, 1 << 20))]
+    sizes = [exq.exq_attend_workspace_bytes(cache, r, 8, w) for r, w in ((1, 1000), (16, 1000), (256, 1 << 20))]
     assert 0 < sizes[0] <= sizes[1] <= sizes[2] < 1 << 28
     assert exq.exq_attend_workspace_bytes(cache, 4096, 8, 1 << 20) == 0      # rows enough to load the card unsplit
-    for rows in (1, 16, 512, 513, (1 << 31) // 64):
+    for rows in (1, 16, 256, 257, 1 << 20):
         assert exq.exq_attend_workspace_bytes(cache, rows, 8, (1 << 31) - 1) < 1 << 28
 
 

@@ -103,6 +103,32 @@ def test_append_writes_exactly_the_references_bytes(exq, dim, kv_heads, page, bi
     np.testing.assert_array_equal(vo.cpu().numpy()[live].view(np.uint16), ref.held(v, bits[1])[live].view(np.uint16))
 
 
+@pytest.mark.parametrize("bits", [(4, 8), (8, 4)], ids=str)
+def test_every_fp16_magnitude_as_a_groups_largest_and_ties(exq, bits):
+    """Every finite fp16 as the largest of a group, beside the values nearest to the ties k + 1/2 of its scale (on the tie
+    where fp16 has it) and random ones: all read back as the reference quantizes them."""
+    rng = np.random.default_rng(11)
+    top16 = np.arange(0x7C00, dtype=np.uint16).view(np.float16)
+    n = top16.size
+    x = np.zeros((n, 1, 64), dtype=np.float16)
+    for g, b in enumerate((4, 8)):                      # the first group against 4-bit ties, the second against 8-bit ones
+        top = (1 << (b - 1)) - 1
+        s = (top16.astype(np.float32) / np.float32(top)).astype(np.float16).astype(np.float64)
+        k = rng.integers(-top, top, size=(n, 28)) + 0.5
+        ties = k * s[:, None]
+        x[:, 0, 32 * g:32 * g + 28] = np.clip(ties, -top16[:, None].astype(np.float64), top16[:, None].astype(np.float64))
+        x[:, 0, 32 * g + 28:32 * g + 31] = (rng.uniform(-1, 1, size=(n, 3)) * top16[:, None].astype(np.float64)).astype(np.float16)
+        x[:, 0, 32 * g + 31] = top16 * np.where(rng.integers(0, 2, n), -1, 1)
+    pages = -(-n // 256)
+    cache = exq.KVCache(pages, 256, 1, 64, *bits)
+    table, seqs, pos = i32(np.arange(pages)[None]), i32(np.zeros(n)), i32(np.arange(n))
+    note("every fp16 magnitude bits=%s" % (bits,))
+    cache.append(to_dev(x), to_dev(x), table, seqs, pos)
+    ko, vo = cache.read(table, seqs, pos)
+    np.testing.assert_array_equal(ko.cpu().numpy(), ref.held(x, bits[0]))
+    np.testing.assert_array_equal(vo.cpu().numpy(), ref.held(x, bits[1]))
+
+
 @pytest.mark.parametrize("bits", [(4, 4), (8, 8), (16, 16)], ids=str)
 def test_aligned_prompt_and_long_read(exq, bits):
     """Whole tiles in order, from position 0: 2 sequences of 200 and 64 tokens, written in one call and read in two orders."""
@@ -212,6 +238,23 @@ def test_attend_matches_reference(exq, dim, kv_heads, group, page, bits):
         one.check(o, l, q[r:r + 1], scale, what="alone")
 
 
+@pytest.mark.parametrize("bits", BITS, ids=str)
+@pytest.mark.parametrize("dim,kv_heads,group,page", [(64, 2, 5, 16), (96, 1, 3, 48), (128, 1, 8, 256), (256, 1, 2, 64)])
+def test_attend_split(exq, dim, kv_heads, group, page, bits):
+    """Rows long enough to be split and joined, in tables just wide enough and in ones of over 16384 tokens; with and
+    without a window."""
+    lengths = [1300, 5, 2100, 0, 1025]
+    c = Case(exq, dim + group + 1, lengths, page, kv_heads, dim, bits, spread=0.7)
+    wide = np.concatenate([c.table, np.full((5, -(-16384 // page)), -1, dtype=np.int32)], 1)
+    q = values(c.rng, 5, kv_heads * group, dim, spread=0.5)
+    for t in (c.table, wide):
+        for window in (0, 1200):
+            note("attend split dim=%d bits=%s width=%d window=%d" % (dim, bits, t.shape[1], window))
+            assert exq.exq_attend_workspace_bytes(c.cache.handle, 5, kv_heads * group, t.shape[1]) > 0
+            out, lse = c.cache.attend(to_dev(q), i32(t), i32(lengths), window=window, return_lse=True)
+            c.check(out, lse, q, dim ** -0.5, window, what="window %d" % window)
+
+
 @pytest.mark.parametrize("bits", [(4, 4), (16, 16)], ids=str)
 @pytest.mark.parametrize("window", [1, 16, 100, 129, 400, 1000])
 def test_window(exq, window, bits):
@@ -317,6 +360,55 @@ def test_infinite_and_nan_values_that_are_attended_to_show(exq, bits):
     rest = np.ones(64, bool)
     rest[bad] = False
     assert np.all(np.isfinite(o[0, 2:][:, rest])) and np.all(np.isfinite(o[1]))
+
+
+def test_scores_of_minus_infinity(exq):
+    """Keys whose score is -infinity weigh nothing, whole steps of them at the front included; a row of nothing else is NaN."""
+    n, dim = 2200, 64
+    c = Case(exq, 23, [n, 60, 1100], 64, 1, dim, (16, 16), garbage=False)
+    gone = [np.arange(n) < 900, np.ones(60, bool), np.arange(1100) >= 7]
+    for s in range(3):
+        c.k[s][gone[s], 0, 3] = -np.inf
+        ref.append(c.geo, c.pages, c.k[s], c.v[s], c.table, [s] * len(c.k[s]), range(len(c.k[s])))
+    c.cache.pages.copy_(to_dev(c.pages).view_as(c.cache.pages))
+    q = np.abs(values(c.rng, 3, 2, dim)) + np.float16(0.01)
+    note("scores of -infinity")
+    out, lse = c.cache.attend(to_dev(q), c.dtable, i32(c.lengths), return_lse=True)
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    assert np.all(np.isnan(out[1])) and np.all(np.isnan(lse[1]) | (lse[1] == -np.inf))
+    for s in (0, 2):
+        o, l, bo, bl = ref.attend(q[s], c.k[s][~gone[s]], c.v[s][~gone[s]], 0.125)
+        assert np.all(np.abs(out[s] - o) <= bo) and np.all(np.abs(lse[s] - l) <= bl)
+
+
+def test_shared_pages_and_expanded_tables(exq):
+    """Sequences that share a prefix's pages, through tables of their own and through one expanded table row."""
+    c = Case(exq, 24, [96, 96], 32, 2, 64, (4, 4), garbage=False)
+    t = c.table.copy()
+    t[1, :2] = t[0, :2]                                   # 64 shared tokens, then each its own
+    c.k[1][:64], c.v[1][:64] = c.k[0][:64], c.v[0][:64]
+    q = values(c.rng, 2, 4, 64)
+    note("shared pages")
+    out, lse = c.cache.attend(to_dev(q), i32(t), i32([96, 90]), return_lse=True)
+    c.check(out, lse, q, 0.125, lengths=[96, 90])
+    c.k[1], c.v[1] = c.k[0], c.v[0]
+    out, lse = c.cache.attend(to_dev(q), i32(t[:1]).expand(2, -1), i32([96, 40]), return_lse=True)
+    c.check(out, lse, q, 0.125, lengths=[96, 40])
+
+
+@pytest.mark.parametrize("rows", [65, 130, 257])
+def test_rows_beyond_a_waves_lanes_with_long_ones_among_them(exq, rows):
+    """More rows than a wave has lanes, most short, some long enough to be split (up to 256 rows), some padding."""
+    rng = np.random.default_rng(rows)
+    lengths = rng.integers(0, 40, rows)
+    lengths[[0, 63, 64, rows - 1]] = [2500, 1, 2900, 2777]
+    c = Case(exq, rows, list(lengths), 16, 1, 64, (8, 4), spare=0)
+    n = np.where(rng.integers(0, 5, rows) == 0, -1, lengths)
+    n[[0, 64, rows - 1]] = lengths[[0, 64, rows - 1]]
+    q = values(c.rng, rows, 3, 64)
+    note("%d rows, some long" % rows)
+    out, lse = c.cache.attend(to_dev(q), c.dtable, i32(n), return_lse=True)
+    c.check(out, lse, q, 0.125, lengths=list(n))
 
 
 def test_many_rows_and_heads(exq):
