@@ -321,9 +321,14 @@ def exq_attend(cache: int, q_ptr: int, q_strides, rows: int, q_heads: int, table
 
 # ------------------------------------------------------------ conveniences
 
-def _refuse(what: str):
-    """Argument checks of tensors, which the library never sees as such."""
-    raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", what)
+def _tensor_calls():
+    """The module of KVCache's calls, which checks their tensors and passes them to the library."""
+    if not os.path.exists(os.path.join(_PKG, "_exq_torch.so")):
+        from . import build as _b
+        _b.build()
+    from . import _exq_torch
+    _exq_torch.set_error(ExqError)
+    return _exq_torch
 
 
 def _on(stream, device):
@@ -456,97 +461,40 @@ class KVCache:
             pages = torch.zeros((n_pages, page_bytes), dtype=torch.uint8, device=device)
         if not (pages.dtype is torch.uint8 and pages.is_contiguous() and pages.is_cuda
                 and pages.numel() == n_pages * page_bytes):
-            _refuse("pages must be contiguous uint8 of %d x %d bytes on the GPU" % (n_pages, page_bytes))
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check",
+                           "pages must be contiguous uint8 of %d x %d bytes on the GPU" % (n_pages, page_bytes))
         self.pages, self.n_pages, self.page_size, self.page_bytes = pages, n_pages, page_size, page_bytes
         self.kv_heads, self.head_dim, self.k_bits, self.v_bits = kv_heads, head_dim, k_bits, v_bits
         self.device, self._index = pages.device, pages.device.index
-        self._torch, self._C, self._empty = torch, torch._C, torch.empty_strided
-        self._f16, self._f32, self._i32 = torch.float16, torch.float32, torch.int32
+        self._torch, self._C, self._calls = torch, torch._C, _tensor_calls()
         self._scale = head_dim ** -0.5
-        self._needs = {}        # workspace bytes by (rows, q_heads, table width)
         self._workspaces = {}   # by stream: calls on one stream run one after another
         self.handle = exq_cache_create(pages.data_ptr(), n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
 
-    # A call costs the host several microseconds, more than a small launch runs:
-    # the checks below are written for few operations on tensors.
-
-    def _raw_stream(self):
-        """The raw current stream, or None if the cache's device is not the current one."""
-        C = self._C
-        return C._cuda_getCurrentRawStream(self._index) if C._cuda_getDevice() == self._index else None
-
-    def _strides(self, name, x, shape):
-        """(row, head) strides of an fp16 operand."""
-        if x.shape == shape and x.dtype is self._f16 and x.get_device() == self._index:
-            row, head, channel = x.stride()
-            if channel == 1:
-                return row, head
-        _refuse("%s must be fp16 %s on %s with contiguous channels" % (name, list(shape), self.device))
-
-    def _index_vector(self, name, x, rows):
-        """Pointer of an int32 [rows] operand."""
-        if x.dtype is self._i32 and x.shape == (rows,) and x.get_device() == self._index and (
-                rows < 2 or x.stride() == (1,)):
-            return x.data_ptr()
-        _refuse("%s must be contiguous int32 [%d] on %s" % (name, rows, self.device))
-
-    def _table(self, table):
-        """(pointer, rows, width, stride) of a page table."""
-        if table.dtype is self._i32 and table.get_device() == self._index and table.dim() == 2:
-            rows, width = table.shape
-            stride, page = table.stride()
-            if page == 1 or width == 1:
-                return table.data_ptr(), rows, width, stride
-        _refuse("table must be int32 [sequences][pages] on %s with contiguous rows" % self.device)
-
     def append(self, k, v, table, seqs, positions, stream=None):
         """Store rows k, v (fp16 [rows][kv_heads][head_dim]) at positions[r] of sequence seqs[r] (int32 [rows]; < 0: skipped)."""
-        raw = self._raw_stream()
-        if stream is not None or raw is None:
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
             with _on(stream, self.device):
                 return self.append(k, v, table, seqs, positions)
-        rows = k.shape[0]
-        shape = (rows, self.kv_heads, self.head_dim)
-        k_row, k_head = self._strides("k", k, shape)
-        v_row, v_head = self._strides("v", v, shape)
-        tab, table_rows, width, table_stride = self._table(table)
-        st = lib.exq_cache_append(self.handle, k.data_ptr(), k_row, k_head, v.data_ptr(), v_row, v_head, rows, tab,
-                                  table_rows, width, table_stride, self._index_vector("seqs", seqs, rows),
-                                  self._index_vector("positions", positions, rows), raw)
-        if st:
-            _check(st, "exq_cache_append")
+        self._calls.append(self.handle, self.kv_heads, self.head_dim, index, C._cuda_getCurrentRawStream(index), k, v, table,
+                           seqs, positions)
 
     def read(self, table, seqs, positions, k_out=None, v_out=None, stream=None):
         """The values held for positions[r] of sequence seqs[r]: fp16 k, v [rows][kv_heads][head_dim].
 
         Rows with seqs[r] < 0 are left as they were in k_out and v_out (in tensors allocated here: unspecified)."""
-        raw = self._raw_stream()
-        if stream is not None or raw is None:
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
             with _on(stream, self.device):
                 return self.read(table, seqs, positions, k_out, v_out)
-        rows, heads, dim = seqs.shape[0], self.kv_heads, self.head_dim
-        shape = (rows, heads, dim)
-        if k_out is None:
-            k_out, k_row, k_head = self._empty(shape, (heads * dim, dim, 1), dtype=self._f16, device=self.device), heads * dim, dim
-        else:
-            k_row, k_head = self._strides("k_out", k_out, shape)
-        if v_out is None:
-            v_out, v_row, v_head = self._empty(shape, (heads * dim, dim, 1), dtype=self._f16, device=self.device), heads * dim, dim
-        else:
-            v_row, v_head = self._strides("v_out", v_out, shape)
-        tab, table_rows, width, table_stride = self._table(table)
-        st = lib.exq_cache_read(self.handle, k_out.data_ptr(), k_row, k_head, v_out.data_ptr(), v_row, v_head, rows, tab,
-                                table_rows, width, table_stride, self._index_vector("seqs", seqs, rows),
-                                self._index_vector("positions", positions, rows), raw)
-        if st:
-            _check(st, "exq_cache_read")
-        return k_out, v_out
+        return self._calls.read(self.handle, self.kv_heads, self.head_dim, index, C._cuda_getCurrentRawStream(index), table,
+                                seqs, positions, k_out, v_out)
 
-    def workspace(self, rows: int, q_heads: int, table_width: int):
-        """A workspace for attend calls of up to these sizes, to pass where calls must not share the cache's own: its
-        counters are zeroed on the current stream."""
+    def workspace(self, nbytes: int):
+        """A workspace for attend calls that need up to `nbytes` (exq_attend_workspace_bytes), to pass where calls must not
+        share the cache's own: its counters are zeroed on the current stream."""
         torch = self._torch
-        nbytes = exq_attend_workspace_bytes(self.handle, rows, q_heads, table_width)
         ws = torch.empty(max(nbytes, ATTEND_COUNTER_BYTES), dtype=torch.uint8, device=self.device)
         ws[:ATTEND_COUNTER_BYTES].view(torch.int32).zero_()
         return ws
@@ -559,53 +507,23 @@ class KVCache:
         scale: default head_dim ** -0.5.  lengths[r] == 0 gives zeros (lse -inf); < 0 leaves the row as it was.
         workspace: from workspace(); by default the cache keeps one for each stream, and a call under graph capture makes
         one that belongs to the graph."""
-        raw = self._raw_stream()
-        if stream is not None or raw is None:
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
             with _on(stream, self.device):
                 return self.attend(q, table, lengths, scale, window, out, return_lse, lse, workspace)
-        shape = q.shape
-        if len(shape) != 3:
-            _refuse("q must be [rows][q_heads][head_dim]")
-        rows, q_heads, dim = shape
-        q_row, q_head = self._strides("q", q, (rows, q_heads, self.head_dim))
-        tab, table_rows, width, table_stride = self._table(table)
-        if table_rows != rows:
-            _refuse("table must have q's %d rows" % rows)
-        if out is None:
-            out, out_row, out_head = self._empty(shape, (q_heads * dim, dim, 1), dtype=self._f16, device=self.device), q_heads * dim, dim
-        else:
-            out_row, out_head = self._strides("out", out, shape)
-        if lse is not None:
-            if not (lse.dtype is self._f32 and lse.shape == (rows, q_heads) and lse.get_device() == self._index
-                    and lse.is_contiguous()):
-                _refuse("lse must be contiguous fp32 [%d][%d] on %s" % (rows, q_heads, self.device))
-            lse_ptr = lse.data_ptr()
-        elif return_lse:
-            lse = self._empty((rows, q_heads), (q_heads, 1), dtype=self._f32, device=self.device)
-            lse_ptr = lse.data_ptr()
-        else:
-            lse_ptr = None
-        need = self._needs.get((rows, q_heads, width))
-        if need is None:
-            need = self._needs[rows, q_heads, width] = lib.exq_attend_workspace_bytes(self.handle, rows, q_heads, width)
-        ws_ptr, ws_bytes = None, 0
-        if need:
-            if workspace is None:
-                if self._C._cuda_isCurrentStreamCapturing():
-                    workspace = self.workspace(rows, q_heads, width)
-                else:
-                    workspace = self._workspaces.get(raw)
-                    if workspace is None or workspace.numel() < need:
-                        workspace = self._workspaces[raw] = self.workspace(rows, q_heads, width)
-            elif not (workspace.get_device() == self._index and workspace.is_contiguous()):
-                _refuse("workspace must be contiguous on %s" % self.device)
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        st = lib.exq_attend(self.handle, q.data_ptr(), q_row, q_head, rows, q_heads, tab, width, table_stride,
-                            self._index_vector("lengths", lengths, rows), self._scale if scale is None else scale, window,
-                            out.data_ptr(), out_row, out_head, lse_ptr, ws_ptr, ws_bytes, raw)
-        if st:
-            _check(st, "exq_attend")
-        return (out, lse) if return_lse else out
+        raw = C._cuda_getCurrentRawStream(index)
+        capturing = C._cuda_isCurrentStreamCapturing()
+        if scale is None:
+            scale = self._scale
+        result = self._calls.attend(self.handle, self.kv_heads, self.head_dim, index, raw, q, table, lengths, scale, window, out,
+                                    return_lse, lse, workspace, None if capturing else self._workspaces.get(raw))
+        if type(result) is int:   # a call that splits its rows, and no workspace of that many bytes yet
+            workspace = self.workspace(result)
+            if not capturing:
+                self._workspaces[raw] = workspace
+            result = self._calls.attend(self.handle, self.kv_heads, self.head_dim, index, raw, q, table, lengths, scale, window,
+                                        out, return_lse, lse, workspace, None)
+        return result
 
     def close(self):
         if self.handle:

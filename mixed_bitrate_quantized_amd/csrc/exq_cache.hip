@@ -1348,13 +1348,13 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // evenly enough as they are, and every workgroup would look through all
     // rows' lengths.
     out->whole_units = (segments >= kCus ? 2048 : 1024) / unit;
-    const bool split = units > out->whole_units && segments <= kAttendMaxSegments && rows <= kAttendMaxRows;
+    const bool split = units > out->whole_units && rows > 0 && segments <= kAttendMaxSegments && rows <= kAttendMaxRows;
     // With 64 segments or more, two workgroups a CU balance rows of different
     // lengths (16 ragged rows of up to 8192 tokens 27 us, with one a CU 36;
     // equal rows of 4096 tokens 24.9 against 25.9); below that they only add
     // parts (4 x 4096 tokens 15.1 against 13.9).
     out->target = split ? (segments >= 64 ? 2 * kCus : kCus) : 0;
-    out->wgs = split ? (int)std::min<int64_t>(out->target + segments, std::max<int64_t>(segments, 1) * std::min<int64_t>(units, kAttendMaxParts))
+    out->wgs = split ? (int)std::min<int64_t>(out->target + segments, segments * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
     out->ws_bytes = split ? kCounterBytes + (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
     return EXQ_OK;

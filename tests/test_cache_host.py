@@ -197,3 +197,35 @@ def test_kvcache_checks_tensors_before_the_library():
     with pytest.raises(exq.ExqError) as ei:
         exq.KVCache(4, 17, 2, 64, device="cpu")
     assert ei.value.status == exq.EXQ_ERR_INVALID_ARG
+
+
+def test_tensor_calls_refuse_before_the_library(cache):
+    """The checks of tensors (_exq_torch) with CPU tensors: every one is refused with the package's own error."""
+    torch = pytest.importorskip("torch")
+    calls = exq._tensor_calls()
+    head = (cache, 4, 64, 0, 0)
+    k = torch.zeros((3, 4, 64), dtype=torch.float16)
+    t = torch.zeros((3, 2), dtype=torch.int32)
+    n = torch.zeros(3, dtype=torch.int32)
+    I = exq.EXQ_ERR_INVALID_ARG
+    for bad in ((k, k, t, n, n), (k[0, 0, 0], k, t, n, n), (None, k, t, n, n), (k, 3, t, n, n)):
+        expect_call(I, calls.append, *head, *bad)
+    for bad in ((t, n, n, None, None), (t, t, n, None, None), (None, n, n, None, None), (t, "n", n, k, k)):
+        expect_call(I, calls.read, *head, *bad)
+    q = torch.zeros((3, 8, 64), dtype=torch.float16)
+    for bad in ((q, t, n), (q[0], t, n), (None, t, n), (q, n, n), (q, t, None)):
+        expect_call(I, calls.attend, *head, *bad, 0.125, 0, None, False, None, None, None)
+    expect_call(I, calls.attend, *head, q, t, n, 0.125, 1 << 40, None, False, None, None, None)
+    for wrong in ((calls.append, head), (calls.read, head + (t,)), (calls.attend, head + (q,))):
+        with pytest.raises(TypeError):
+            wrong[0](*wrong[1])
+    with pytest.raises(TypeError):
+        calls.append("cache", 4, 64, 0, 0, k, k, t, n, n)
+    with pytest.raises(TypeError):
+        calls.attend(*head, q, t, n, "scale", 0, None, False, None, None, None)
+
+
+def expect_call(status, fn, *args):
+    with pytest.raises(exq.ExqError) as ei:
+        fn(*args)
+    assert ei.value.status == status

@@ -490,7 +490,7 @@ def test_calls_of_all_sizes_share_a_workspace(exq):
     """Many workgroups to a segment (two levels of joining), few, and none, one after another through one workspace."""
     lengths = [30000, 700]
     c = Case(exq, 22, lengths, 64, 1, 64, (8, 8), spread=0.5, garbage=False)
-    ws = c.cache.workspace(2, 32, c.dtable.shape[1])
+    ws = c.cache.workspace(max(exq.exq_attend_workspace_bytes(c.cache.handle, 2, h, c.dtable.shape[1]) for h in (1, 7, 16, 32)))
     for heads in (1, 32, 7, 16):
         q = values(c.rng, 2, heads, 64, spread=0.5)
         for lens in ([30000, 700], [130, -1], [17000, 0], [-1, -1], [5, 700], [30000, -1]):
