@@ -519,7 +519,7 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
 
 // ------------------------------------------------------------------ attend
 
-constexpr int kCus = 256;
+constexpr int kCusLog2 = 8, kCus = 1 << kCusLog2;
 constexpr int kAttendMaxSegments = 2048;   // more are not split: they load the card evenly enough
 constexpr int kAttendMaxRows = 256;        // likewise
 constexpr int kAttendMaxParts = 32;        // parts of a segment
@@ -540,6 +540,17 @@ constexpr bool attend_light(int D, int KB, int VB) { return row_bytes(D, KB, VB)
 constexpr size_t kCounterBytes = EXQ_ATTEND_COUNTER_BYTES;
 static_assert(kCounterBytes >= kAttendMaxWgs * sizeof(uint32_t), "a counter for every workgroup");
 
+// Division of a 32-bit number by d with one product: m = floor(2^32 / d) + 1
+// gives a quotient that is at most one too high (m = 0 stands for d = 1).
+struct Divisor {
+    uint32_t d, m;
+    __host__ static Divisor of(uint32_t d) { return {d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
+    __device__ __forceinline__ uint32_t divide(uint32_t n) const {
+        const uint32_t q = m ? __umulhi(n, m) : n;
+        return q * d > n ? q - 1 : q;
+    }
+};
+
 struct AttendArgs {
     CacheDev c;
     TableDev t;
@@ -553,10 +564,11 @@ struct AttendArgs {
     float scale;               // scale * log2(e)
     int window;
     int rows, q_heads, group;  // group: query heads per key-value head
-    int head_tiles;            // kv_heads * ceil(group / 16): segments of a row
-    uint32_t tile_magic;       // floor(2^32 / tiles per page) + 1; 0 for one tile
+    Divisor head_tiles;        // kv_heads * ceil(group / 16): segments of a row
+    Divisor group_tiles;       // ceil(group / 16)
+    Divisor page_tiles;        // tiles of a page and head
     int whole_units;           // rows of at most this many units are not split
-    int target;                // workgroups to split for; 0: a workgroup for each segment
+    int target;                // log2 of the workgroups to split for; 0: a workgroup for each segment
 };
 
 // Longest row: tokens are counted in 32 bits, up to a few units past the end.
@@ -585,11 +597,6 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
     const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
     return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-// a / b, a >= 0 and b > 0, uniform: the 64-bit division only where 32 bits do not do.
-__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
-    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Inclusive prefix sum over a wave's lanes.
@@ -625,8 +632,8 @@ struct Piece {
 
 // The piece of workgroup `w` of a launch that splits, counted from the lengths
 // by every wave for itself, 64 rows at a time (up to 64 rows are read once).
-// With U units in all segments, chunks have at least U / target units, so
-// there are at most target + segments of them, and a segment has at most
+// With U units in all segments, chunks have at least U / 2^target units, so
+// there are at most 2^target + segments of them, and a segment has at most
 // kAttendMaxParts.  False: there are fewer pieces.
 __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w, Piece& p) {
     int loaded = -1, mine = -1;
@@ -648,21 +655,23 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
     }
     p.size = longest > 0 ? longest : 1;
     if (longest > a.whole_units) {
-        const int even = (int)divide(total * a.head_tiles + a.target - 1, a.target);
+        const int even = (int)((total * a.head_tiles.d + (1ll << a.target) - 1) >> a.target);
         const int least = (longest + kAttendMaxParts - 1) / kAttendMaxParts;
         p.size = even > least ? even : least;
     }
     int before = 0;   // pieces of earlier rows
     for (int r0 = 0; r0 < a.rows; r0 += 64) {
-        const int chunks = (units_of(r0) + p.size - 1) / p.size, v = wave_prefix(chunks * a.head_tiles);
+        const int units = units_of(r0);
+        const int chunks = longest <= a.whole_units ? (units > 0) : (units + p.size - 1) / p.size;
+        const int v = wave_prefix(chunks) * (int)a.head_tiles.d;
         const int sum = __builtin_amdgcn_readlane(v, 63);
         if (w < before + sum) {
             const int at = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before + v <= w));   // rows that end at or before w
             p.row = r0 + at;
             p.length = __builtin_amdgcn_readlane(mine, at);
             p.chunks = __builtin_amdgcn_readlane(chunks, at);
-            before += __builtin_amdgcn_readlane(v, at) - p.chunks * a.head_tiles;
-            p.seg = (w - before) / p.chunks;
+            before += __builtin_amdgcn_readlane(v, at) - p.chunks * (int)a.head_tiles.d;
+            p.seg = p.chunks == 1 ? w - before : (w - before) / p.chunks;
             p.first = before + p.seg * p.chunks;
             p.chunk = w - p.first;
             return true;
@@ -713,7 +722,7 @@ struct Joined {
 
 // out and lse of four channels.
 __device__ __forceinline__ void finish(const AttendArgs& a, int row, int head, int d, const Joined& j, bool empty) {
-    const float inv = empty ? 0.0f : 1.0f / j.sum;
+    const float inv = empty ? 0.0f : __builtin_amdgcn_rcpf(j.sum);
     u2v w;
     w[0] = (uint32_t)f32_to_f16_bits(j.o[0] * inv) | ((uint32_t)f32_to_f16_bits(j.o[1] * inv) << 16);
     w[1] = (uint32_t)f32_to_f16_bits(j.o[2] * inv) | ((uint32_t)f32_to_f16_bits(j.o[3] * inv) << 16);
@@ -993,16 +1002,17 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
     using PK = CachePart<D, KB>;
     using PV = CachePart<D, VB>;
     constexpr int G = D / kCacheGroup, TILE = PK::BYTES + PV::BYTES, THREADS = 64 * NW, UNIT = 32 * NW;
-    __shared__ __attribute__((aligned(16))) float part_o[NW][16][D];
-    __shared__ float part_r[NW][16], part_l[NW][16];
+    constexpr int PITCH = D + 4;   // heads' rows start four banks apart: 16 lanes store their head's sums side by side
+    __shared__ __attribute__((aligned(16))) float part_o[NW][16][PITCH];
+    __shared__ float part_r[NW][16], part_l[NW][16], part_f[NW][16];
     __shared__ bool last;
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
     const int quad = lane >> 4, col = lane & 15;
 
     Piece p;
     if (a.target == 0) {
-        p.row = (int)(blockIdx.x / (uint32_t)a.head_tiles);
-        p.seg = (int)(blockIdx.x % (uint32_t)a.head_tiles);
+        p.row = (int)a.head_tiles.divide(blockIdx.x);
+        p.seg = (int)(blockIdx.x - (uint32_t)p.row * a.head_tiles.d);
         p.length = uniform(gptr<int32_t>(a.lengths)[p.row]);
         p.chunk = 0;
         p.chunks = 1;
@@ -1013,8 +1023,7 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
     }
     const RowSpan span = row_span(a, p.length, UNIT);
     if (span.units == 0) return;   // a padding row
-    const int tiles_per_kv = (a.group + 15) / 16;
-    const int kvh = p.seg / tiles_per_kv, hs = p.seg % tiles_per_kv * 16;
+    const int kvh = (int)a.group_tiles.divide((uint32_t)p.seg), hs = (p.seg - kvh * (int)a.group_tiles.d) * 16;
     const int h0 = kvh * a.group + hs, heads = a.group - hs < 16 ? a.group - hs : 16;
     AttendWave<D, KB, VB> W;
     W.nib.init();
@@ -1038,10 +1047,9 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
     }
     bool bad = span.bad;
     const int32_t* pages = a.t.pages + (int64_t)p.row * a.t.stride;
-    // Lane j holds the numbers, among the cache's tiles, of the two tiles
-    // of step c0 + j, 64 steps at a time: one look at the page table per
-    // 64 steps.
-    const uint32_t page_tiles = a.c.tiles * a.c.kv_heads, head_tile = (uint32_t)kvh * a.c.tiles;
+    // Lane j holds the numbers, among the cache's tiles, of the two tiles of
+    // step c0 + j, 64 steps at a time: one look at the page table per 64 steps.
+    const uint32_t all_tiles = a.c.tiles * a.c.kv_heads, head_tile = (uint32_t)kvh * a.c.tiles;
     uint32_t tile_a = 0, tile_b = 0;
     int c0 = 0;
     auto look_up = [&](int from) {
@@ -1051,13 +1059,11 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
         const bool live = i < i1;
         const bool ina = live && token + 16 > span.lo, inb = live && token + 16 < span.hi;
         auto number = [&](bool in, int tok, bool& odd) -> uint32_t {
-            const uint32_t tile = (uint32_t)tok / kCacheTile;
-            uint32_t pi = a.tile_magic ? __umulhi(tile, a.tile_magic) : tile;
-            if (pi * a.c.tiles > tile) --pi;
+            const uint32_t tile = (uint32_t)tok / kCacheTile, pi = a.page_tiles.divide(tile);
             uint32_t page = in ? (uint32_t)gptr<int32_t>(pages)[pi] : 0u;
             odd = page >= a.c.n_pages;
             if (odd) page = 0;
-            return page * page_tiles + head_tile + (tile - pi * a.c.tiles);
+            return page * all_tiles + head_tile + (tile - pi * a.c.tiles);
         };
         bool odd_a, odd_b;
         tile_a = number(ina, token, odd_a);
@@ -1125,6 +1131,7 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
         const float f = __builtin_amdgcn_exp2f(W.reference() - ref);
 #pragma unroll
         for (int i = 0; i < 2 * G; ++i) *reinterpret_cast<f4*>(&part_o[wave][col][16 * i + 4 * quad]) = W.o[i] * f;
+        if (quad == 0) part_f[wave][col] = f;
         __syncthreads();
     }
     const int hp = a.group < 16 ? a.group : 16, items = heads * (D / 4);   // an item: four channels of a head
@@ -1137,7 +1144,7 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
         for (int w = 1; w < NW; ++w) j.top = __builtin_fmaxf(j.top, part_r[w][h]);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            j.sum += part_l[w][h] * __builtin_amdgcn_exp2f(part_r[w][h] - j.top);
+            j.sum += part_l[w][h] * part_f[w][h];
             j.o += *reinterpret_cast<const f4*>(&part_o[w][h][d]);
         }
         if (p.chunks == 1) {
@@ -1353,8 +1360,8 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // lengths (16 ragged rows of up to 8192 tokens 27 us, with one a CU 36;
     // equal rows of 4096 tokens 24.9 against 25.9); below that they only add
     // parts (4 x 4096 tokens 15.1 against 13.9).
-    out->target = split ? (segments >= 64 ? 2 * kCus : kCus) : 0;
-    out->wgs = split ? (int)std::min<int64_t>(out->target + segments, segments * std::min<int64_t>(units, kAttendMaxParts))
+    out->target = split ? (segments >= 64 ? kCusLog2 + 1 : kCusLog2) : 0;
+    out->wgs = split ? (int)std::min<int64_t>((1 << out->target) + segments, segments * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
     out->ws_bytes = split ? kCounterBytes + (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
     return EXQ_OK;
@@ -1493,8 +1500,9 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.rows = rows;
     a.q_heads = q_heads;
     a.group = q_heads / c->kv_heads;
-    a.head_tiles = p.head_tiles;
-    a.tile_magic = a.c.tiles == 1 ? 0u : (uint32_t)((1ull << 32) / a.c.tiles + 1);
+    a.head_tiles = Divisor::of((uint32_t)p.head_tiles);
+    a.group_tiles = Divisor::of((uint32_t)(a.group + 15) / 16);
+    a.page_tiles = Divisor::of(a.c.tiles);
     a.target = p.target;
     a.whole_units = p.whole_units;
     const hipStream_t s = static_cast<hipStream_t>(stream);
