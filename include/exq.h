@@ -331,7 +331,8 @@ void exq_plan_destroy(exq_plan_t plan);
  *
  * Quantizer: exq_pack's, over groups of 32 consecutive channels of one token
  * and head, for a width b of 4 or 8:
- *   s = fp16_RNE(fp32(max|x|) / fp32(2^(b-1)-1)), an fp32 division;
+ *   s = fp16_RNE(fp32(max|x|) / fp32(2^(b-1)-1)), an fp32 division, but at
+ *   most 9352 (b = 4) or 515.5 (b = 8), so that finite values stay finite;
  *   c = clamp(rint_even(fp32(x)/fp32(s)), -(2^(b-1)-1), 2^(b-1)-1) + 2^(b-1),
  *   2^(b-1) if s == 0;  the value held is x_hat = fp16_RNE((c - 2^(b-1)) * s).
  * A group that holds an infinity or a NaN gets a NaN scale: all of it reads

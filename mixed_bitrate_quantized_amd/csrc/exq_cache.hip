@@ -192,14 +192,16 @@ __device__ __forceinline__ void group_max(const u4v (&x)[G], uint32_t (&m)[(G + 
     }
 }
 
-// A group's scale from its max|x|: fp16 bits.  The quotient by 7 or 127 with
-// one Newton step, as below: no quotient of an 11-bit number by these lies
-// within 2^-46 of a tie of fp32, so it is the correctly rounded one.
+// A group's scale from its max|x|: fp16 bits.  The quotient by 7 or 127, one
+// Newton step on m * (1 / top): no quotient of an 11-bit number by these lies
+// within 2^-46 of a tie of fp32, so it is the correctly rounded one.  At most
+// the largest scale whose largest code's value, top * s, is finite in fp16
+// (the next ones give 65520 and 65532, which round to infinity).
 template <int B> __device__ __forceinline__ uint32_t scale_bits(uint32_t max_bits) {
-    constexpr float top = (float)((1 << (B - 1)) - 1), inv = 1.0f / top;
+    constexpr float top = (float)((1 << (B - 1)) - 1), inv = 1.0f / top, most = B == 4 ? 9352.0f : 515.5f;
     const float m = (float)__builtin_bit_cast(_Float16, (uint16_t)max_bits);
     const float q0 = m * inv, q = __builtin_fmaf(__builtin_fmaf(-q0, top, m), inv, q0);
-    return max_bits >= 0x7C00u ? 0x7E00u : (uint32_t)f32_to_f16_bits(q);
+    return max_bits >= 0x7C00u ? 0x7E00u : (uint32_t)f32_to_f16_bits(__builtin_fminf(q, most));
 }
 
 // Codes of eight values at scale s.  The quotient x / s: one Newton step on

@@ -56,6 +56,7 @@ def quantize(x, bits):
     f = x.astype(np.float32).reshape(*x.shape[:-1], -1, GROUP)
     with np.errstate(all="ignore"):
         s = (np.abs(f).max(-1) / top).astype(np.float16)
+        s = np.minimum(s, np.float16(9352 if bits == 4 else 515.5))   # top * s stays finite
         s = np.where(np.isfinite(f).all(-1), s, np.float16(np.nan))
         c = np.clip(np.rint(f / s.astype(np.float32)[..., None]), -top, top)
     c = np.where(s[..., None] > 0, c, 0).astype(np.int64) + (1 << (bits - 1))

@@ -190,6 +190,12 @@ def test_reference_quantizer_pins():
         assert np.max(np.abs(ref.held(y, b).astype(np.float64) - y.astype(np.float64))) <= s / 2 + 2 * 2.0 ** -11 * 2
 
 
+def test_reference_keeps_finite_values_finite():
+    x = np.repeat(np.arange(0x7C00, dtype=np.uint16).view(np.float16)[:, None], 32, 1)
+    for b in (4, 8):
+        assert np.all(np.isfinite(ref.held(x, b))) and np.all(ref.held(x, b)[-1] == 65472)
+
+
 def test_kvcache_checks_tensors_before_the_library():
     torch = pytest.importorskip("torch")
     with pytest.raises(exq.ExqError):

@@ -129,6 +129,18 @@ def test_every_fp16_magnitude_as_a_groups_largest_and_ties(exq, bits):
     np.testing.assert_array_equal(vo.cpu().numpy(), ref.held(x, bits[1]))
 
 
+@pytest.mark.parametrize("bits", [(4, 8), (8, 4), (16, 16)], ids=str)
+def test_the_largest_finite_values_stay_finite(exq, bits):
+    x = torch.full((16, 1, 64), 65504.0, dtype=torch.float16, device="cuda")
+    x[:, :, 1::2] = -65504.0
+    cache = exq.KVCache(1, 16, 1, 64, *bits)
+    table, seqs, pos = i32([[0]]), i32(np.zeros(16)), i32(np.arange(16))
+    note("largest finite values bits=%s" % (bits,))
+    cache.append(x, x, table, seqs, pos)
+    for got, b in zip(cache.read(table, seqs, pos), bits):
+        assert torch.all(got == torch.sign(x) * (65504 if b == 16 else 65472))   # 7 * 9352 and 127 * 515.5, in fp16
+
+
 @pytest.mark.parametrize("bits", [(4, 4), (8, 8), (16, 16)], ids=str)
 def test_aligned_prompt_and_long_read(exq, bits):
     """Whole tiles in order, from position 0: 2 sequences of 200 and 64 tokens, written in one call and read in two orders."""
