@@ -446,12 +446,14 @@ class KVCache:
 
     K and V are held in `k_bits` and `v_bits` bits (each 4 or 8, or both 16).  `table` is int32 [sequences][width] and
     names each sequence's pages; position p of sequence s lies in page table[s][p // page_size].  Every call runs on
-    `stream` (default: the current stream of the cache's device) and may be captured; all tensors are on that device.
+    `stream` (default: the current stream of the cache's device) and may be captured; all tensors are on that device.  Calls
+    on different streams run side by side: order a read or attend after the append that it needs, and drop the cache after
+    the last of them.
     """
 
     def __init__(self, n_pages: int, page_size: int, kv_heads: int, head_dim: int, k_bits: int = 4, v_bits: int = 4,
                  device="cuda", pages=None):
-        """`pages`: uint8 [n_pages][page_bytes], contiguous, any content (default: allocated and zeroed)."""
+        """`pages`: uint8 [n_pages][page_bytes], contiguous, any content (default: allocated and zeroed, which is waited for)."""
         import torch
         self.handle = None
         page_bytes = exq_cache_page_bytes(page_size, kv_heads, head_dim, k_bits, v_bits)
@@ -459,6 +461,8 @@ class KVCache:
             exq_cache_create(None, n_pages, page_size, kv_heads, head_dim, k_bits, v_bits)
         if pages is None:
             pages = torch.zeros((n_pages, page_bytes), dtype=torch.uint8, device=device)
+            if pages.is_cuda:   # the first append may come on any stream
+                torch.cuda.current_stream(pages.device).synchronize()
         if not (pages.dtype is torch.uint8 and pages.is_contiguous() and pages.is_cuda
                 and pages.numel() == n_pages * page_bytes):
             raise ExqError(EXQ_ERR_INVALID_ARG, "argument check",

@@ -722,12 +722,19 @@ struct Joined {
     float top, sum;
 };
 
+// One output in fp16.  The weights' roundings to fp16 can push an average of
+// values near 65504 past it: a finite one stays finite.
+__device__ __forceinline__ uint32_t output_bits(float x) {
+    const float kept = __builtin_amdgcn_fmed3f(x, -65504.0f, 65504.0f);
+    return (uint32_t)f32_to_f16_bits(__builtin_fabsf(x) < __builtin_inff() ? kept : x);
+}
+
 // out and lse of four channels.
 __device__ __forceinline__ void finish(const AttendArgs& a, int row, int head, int d, const Joined& j, bool empty) {
     const float inv = empty ? 0.0f : __builtin_amdgcn_rcpf(j.sum);
     u2v w;
-    w[0] = (uint32_t)f32_to_f16_bits(j.o[0] * inv) | ((uint32_t)f32_to_f16_bits(j.o[1] * inv) << 16);
-    w[1] = (uint32_t)f32_to_f16_bits(j.o[2] * inv) | ((uint32_t)f32_to_f16_bits(j.o[3] * inv) << 16);
+    w[0] = output_bits(j.o[0] * inv) | (output_bits(j.o[1] * inv) << 16);
+    w[1] = output_bits(j.o[2] * inv) | (output_bits(j.o[3] * inv) << 16);
     *gptr_w<u2v>(a.out + (int64_t)row * a.out_row + (int64_t)head * a.out_head + d) = w;
     if (d == 0 && a.lse)
         gptr_w<float>(a.lse)[(int64_t)row * a.q_heads + head] =

@@ -374,6 +374,21 @@ def test_infinite_and_nan_values_that_are_attended_to_show(exq, bits):
     assert np.all(np.isfinite(o[0, 2:][:, rest])) and np.all(np.isfinite(o[1]))
 
 
+def test_averages_of_the_largest_values_stay_finite(exq):
+    """Weights rounded to fp16 can sum to more than the sum they are divided by: an average of 65504s is still 65504."""
+    lengths = [1, 2, 3, 7, 40, 333, 1024, 2500]
+    c = Case(exq, 31, lengths, 64, 1, 64, (16, 16))
+    for s, n in enumerate(lengths):
+        c.v[s][:] = np.where(np.arange(64) % 2, np.float16(65504), np.float16(-65504))
+        ref.append(c.geo, c.pages, c.k[s], c.v[s], c.table, [s] * n, range(n))
+    c.cache.pages.copy_(to_dev(c.pages).view_as(c.cache.pages))
+    q = values(c.rng, len(lengths), 16, 64)
+    note("averages of the largest values")
+    out, lse = c.cache.attend(to_dev(q), c.dtable, i32(lengths), return_lse=True)
+    assert torch.all(torch.isfinite(out))
+    c.check(out, lse, q, 0.125)
+
+
 def test_scores_of_minus_infinity(exq):
     """Keys whose score is -infinity weigh nothing, whole steps of them at the front included; a row of nothing else is NaN."""
     n, dim = 2200, 64
@@ -514,6 +529,19 @@ def test_calls_of_all_sizes_share_a_workspace(exq):
                     x[:max(n, 0)] for x, n in zip(c.v, lens)], lens
                 one.check(out, lse, q, 0.125, what="%d heads %s" % (heads, lens))
             assert torch.all(ws[:exq.ATTEND_COUNTER_BYTES] == 0)
+
+
+def test_a_new_cache_is_ready_for_any_stream(exq):
+    x = to_dev(values(np.random.default_rng(32), 64, 8, 128))
+    table, seqs, pos = i32([[0]]), i32(np.zeros(64)), i32(np.arange(64))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    note("append on another stream than the cache's pages were zeroed on")
+    cache = exq.KVCache(4096, 256, 8, 128, 16, 16)    # 4 GiB of zeros
+    cache.append(x, x, table, seqs, pos, stream=other)
+    torch.cuda.synchronize()
+    k, v = cache.read(table, seqs, pos)
+    assert torch.equal(k, x) and torch.equal(v, x)
 
 
 def test_other_streams_at_once(exq):
