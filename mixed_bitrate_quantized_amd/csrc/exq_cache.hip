@@ -1085,6 +1085,13 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
         const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)number, i - c0);
         return buffer_rsrc(a.c.pages + (uint64_t)n * TILE, (uint32_t)TILE);
     };
+    // A wave's priority falls as its steps run out, at a half, a quarter and an
+    // eighth of a chunk: of two waves on a SIMD the older one would be served
+    // first and end when the younger still has a fifth to go, with nothing
+    // beside it to hide its waits (131072 tokens at 4 bits 35.4 us, without it
+    // 37.0; 64 ragged rows of up to 4096 41.2 and 45.2).  In 16 bits, where the
+    // memory alone sets the pace, it gains nothing (53.6 and 52.9).
+    constexpr bool kPaced = KB < 16;
     // Keys and values of one step each in registers: a step's keys are
     // asked for once the keys before are used up, under the second product,
     // and its values under the next step's first.  Past the end the last
@@ -1098,7 +1105,16 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
         load_keys(kb, pb, lane);
         load_values<D, KB>(va, pa, lane);
         load_values<D, KB>(vb, pb, lane);
+        if constexpr (kPaced) __builtin_amdgcn_s_setprio(3);
+        const int chunk_steps = p.size < span.units ? p.size : span.units;
+        int pace_mark = chunk_steps / 2, pace = 3;
         for (int i = i0; i < i1; ++i) {
+            if (kPaced && i1 - i <= pace_mark) {
+                pace_mark /= 2;
+                if (--pace == 2) __builtin_amdgcn_s_setprio(2);
+                else if (pace == 1) __builtin_amdgcn_s_setprio(1);
+                else __builtin_amdgcn_s_setprio(0);
+            }
             const int next = i + 1 < i1 ? i + 1 : i;
             if (next - c0 >= 64) look_up(next);
             pa = tile_at(tile_a, next);
