@@ -537,6 +537,9 @@ constexpr int attend_waves_per_simd(int D, int KB, int VB) {
 // Geometries that have a kernel of 8 waves a workgroup beside the one of 4.
 constexpr bool attend_light(int D, int KB, int VB) { return row_bytes(D, KB, VB) <= 208; }
 
+// Geometries of 4 bits for which four workgroups a CU may pay, and fit.
+constexpr bool attend_full(int D, int KB, int VB) { return D % 64 == 0 && KB + VB == 8 && attend_waves_per_simd(D, KB, VB) == 4; }
+
 // The workspace starts with the arrival counters of segments (at their first
 // workgroup's number), zero between launches.
 constexpr size_t kCounterBytes = EXQ_ATTEND_COUNTER_BYTES;
@@ -571,6 +574,8 @@ struct AttendArgs {
     Divisor page_tiles;        // tiles of a page and head
     int whole_units;           // rows of at most this many units are not split
     int target;                // log2 of the workgroups to split for; 0: a workgroup for each segment
+    int other;                 // log2 of another number of workgroups, for lengths that come out at no more; 0: none
+    int64_t other_units;       // from that many units on
 };
 
 // Longest row: tokens are counted in 32 bits, up to a few units past the end.
@@ -636,7 +641,8 @@ struct Piece {
 // by every wave for itself, 64 rows at a time (up to 64 rows are read once).
 // With U units in all segments, chunks have at least U / 2^target units, so
 // there are at most 2^target + segments of them, and a segment has at most
-// kAttendMaxParts.  False: there are fewer pieces.
+// kAttendMaxParts.  With `other` for `target` only where there are at most
+// 2^other: as many as fit side by side.  False: there are fewer pieces.
 __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w, Piece& p) {
     int loaded = -1, mine = -1;
     auto units_of = [&](int r0) {
@@ -657,14 +663,24 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
     }
     p.size = longest > 0 ? longest : 1;
     if (longest > a.whole_units) {
-        const int even = (int)((total * a.head_tiles.d + (1ll << a.target) - 1) >> a.target);
         const int least = (longest + kAttendMaxParts - 1) / kAttendMaxParts;
-        p.size = even > least ? even : least;
+        auto size_for = [&](int target) {
+            const int even = (int)((total * a.head_tiles.d + (1ll << target) - 1) >> target);
+            return even > least ? even : least;
+        };
+        p.size = size_for(a.target);
+        if (a.other && total * a.head_tiles.d >= a.other_units) {
+            const int size = size_for(a.other);
+            int pieces = 0;
+            for (int r0 = 0; r0 < a.rows; r0 += 64)
+                pieces += __builtin_amdgcn_readlane(wave_prefix((units_of(r0) + size - 1) / size), 63);
+            if (pieces * (int)a.head_tiles.d <= 1 << a.other) p.size = size;
+        }
     }
     int before = 0;   // pieces of earlier rows
     for (int r0 = 0; r0 < a.rows; r0 += 64) {
         const int units = units_of(r0);
-        const int chunks = longest <= a.whole_units ? (units > 0) : (units + p.size - 1) / p.size;
+        const int chunks = (units + p.size - 1) / p.size;
         const int v = wave_prefix(chunks) * (int)a.head_tiles.d;
         const int sum = __builtin_amdgcn_readlane(v, 63);
         if (w < before + sum) {
@@ -1347,10 +1363,16 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
     return EXQ_OK;
 }
 
+// Tokens of all segments from which on attend_full geometries take a workgroup
+// for every place the card has for one.
+constexpr int64_t kFullTokens = (int64_t)1 << 22;
+
 // Shape of an exq_attend launch.
 struct AttendPlan {
     int head_tiles, wgs, waves;   // waves of a workgroup
     int target, whole_units;
+    int other;
+    int64_t other_units;
     size_t ws_bytes;
 };
 
@@ -1386,7 +1408,19 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // equal rows of 4096 tokens 24.9 against 25.9); below that they only add
     // parts (4 x 4096 tokens 15.1 against 13.9).
     out->target = split ? (segments >= 64 ? kCusLog2 + 1 : kCusLog2) : 0;
-    out->wgs = split ? (int)std::min<int64_t>((1 << out->target) + segments, segments * std::min<int64_t>(units, kAttendMaxParts))
+    // Where the lengths divide evenly into another number, that one.  One a CU
+    // for heavy steps, whose loads fill the memory's queues by themselves (16 x
+    // 4096 tokens in 16 bits 47.6 us, with two 52.8; 16 x 8192 in 8 bits 51.8 and
+    // 52.3; head_dim 256, 16 x 4096 at 4 bits 32.5 and 36.4).  Four, all that fit,
+    // for very long rows at 4 bits, whose decoding waits for loads (32 x 16384
+    // 109 us, with two 114; head_dim 64, 64 x 16384 119 and 139; but 16 x 16384
+    // 61.4 and 60.9, and head_dim 96, 32 x 16384 108.4 and 105.8).
+    const bool heavy = !attend_light(c->head_dim, c->k_bits, c->v_bits);
+    const bool full = attend_full(c->head_dim, c->k_bits, c->v_bits) && segments * tokens >= kFullTokens;
+    out->other = !split || segments < 64 ? 0 : heavy ? kCusLog2 : full ? kCusLog2 + 2 : 0;
+    out->other_units = heavy ? 0 : kFullTokens / unit;
+    out->wgs = split ? (int)std::min<int64_t>(std::max<int64_t>((1 << out->target) + segments, out->other ? 1 << out->other : 0),
+                                              segments * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
     out->ws_bytes = split ? kCounterBytes + (size_t)out->wgs * sizeof(float) * slot_floats(std::min(group, 16), c->head_dim) : 0;
     return EXQ_OK;
@@ -1529,6 +1563,8 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.group_tiles = Divisor::of((uint32_t)(a.group + 15) / 16);
     a.page_tiles = Divisor::of(a.c.tiles);
     a.target = p.target;
+    a.other = p.other;
+    a.other_units = p.other_units;
     a.whole_units = p.whole_units;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     with_geometry(c, [&](auto D, auto KB, auto VB) {

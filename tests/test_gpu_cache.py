@@ -438,6 +438,37 @@ def test_rows_beyond_a_waves_lanes_with_long_ones_among_them(exq, rows):
     c.check(out, lse, q, 0.125, lengths=list(n))
 
 
+@pytest.mark.parametrize("dim,kv_heads,rows,bits", [(64, 4, 16, (16, 16)), (128, 8, 8, (8, 8)), (256, 1, 64, (4, 4)),
+                                                    (64, 1, 128, (16, 16)), (96, 4, 24, (16, 16))])
+def test_even_and_nearly_even_batches(exq, dim, kv_heads, rows, bits):
+    """Rows of one length, whose chunks come out at one a CU, and the same with a short, an empty and a padding row."""
+    c = Case(exq, 33, [1500], 32, kv_heads, dim, bits, spare=0)
+    c.k, c.v = c.k * rows, c.v * rows
+    table = c.dtable.expand(rows, -1)
+    q = values(c.rng, rows, kv_heads, dim)
+    for n in ([1500] * rows, [1400] * (rows - 1) + [130], [0, -1] + [1500] * (rows - 2)):
+        note("even batch dim=%d bits=%s lengths=%s.." % (dim, bits, n[:2]))
+        out, lse = c.cache.attend(to_dev(q), table, i32(n), return_lse=True)
+        c.check(out, lse, q, dim ** -0.5, lengths=n)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_four_million_tokens_of_a_batch(exq, dim):
+    """64 segments of over 2^16 tokens at 4 bits (a few pages over and over): even, and with one row short."""
+    page, times, rows, kv_heads = 64, 260, 32, 2
+    c = Case(exq, 34, [4 * page], page, kv_heads, dim, (4, 4), spare=0)
+    c.k, c.v = [np.tile(c.k[0], (times, 1, 1))] * rows, [np.tile(c.v[0], (times, 1, 1))] * rows
+    table = i32(np.tile(c.table, (1, times))).expand(rows, -1)
+    q = values(c.rng, rows, kv_heads, dim)
+    full = times * 4 * page
+    for n in ([full] * rows, [full - 17] * (rows - 1) + [777]):
+        note("four million tokens dim=%d last=%d" % (dim, n[-1]))
+        out, lse = c.cache.attend(to_dev(q), table, i32(n), return_lse=True)
+        keep = [n[r] if r in (0, 13, rows - 1) else -1 for r in range(rows)]
+        c.check(out, lse, q, dim ** -0.5, lengths=keep)
+        assert torch.all(torch.isfinite(out))
+
+
 def test_many_rows_and_heads(exq):
     """More rows than a workgroup has threads, in both split and whole launches."""
     for spare in (0, 40):
