@@ -231,6 +231,8 @@ __device__ __forceinline__ uint32_t spread(uint32_t x) {
     return (t | (t << 4)) & 0x0F0F0F0Fu;
 }
 
+// Bound by the bytes of k and v in and of the codes out: 16384 rows of 8 heads
+// of 128 at 4 bits (67 MB in, 19 out) 20-25 us, 3.4-4.3 TB/s of a copy's 4.8.
 template <int D, int KB, int VB>
 __global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableDev t, const uint16_t* __restrict__ k,
                                                               int64_t k_row, int64_t k_head,
@@ -374,6 +376,8 @@ __global__ __launch_bounds__(kRowsThreads) void append_kernel(CacheDev c, TableD
 
 // -------------------------------------------------------------------- read
 
+// Bound by the fp16 rows out: 32768 rows of 8 heads of 128 at 4 bits (38 MB in,
+// 134 out) 31-36 us, 4.8-5.6 TB/s of a copy's 4.8.
 template <int D, int KB, int VB>
 __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, TableDev t, uint16_t* __restrict__ k,
                                                                   int64_t k_row, int64_t k_head,
@@ -706,9 +710,9 @@ constexpr size_t slot_floats(int heads, int D) { return (size_t)heads * (D + 2);
 // Workspace traffic between workgroups, which may run on XCDs with L2s of
 // their own: agent-scope accesses only, which do not stop at an L2.  So a
 // store that has completed is seen by every later load, and no cache has to
-// be written back or invalidated.  (With release and acquire at the counters
-// instead, which do that to a whole L2 for every part, a 131072-token
-// sequence at 4 bits took twice as long: 113 us against 55.)
+// be written back or invalidated.  (Release and acquire at the counters, which
+// do that to a whole L2 for every part, took twice as long: 113 us against 55
+// for 131072 tokens at 4 bits when it was measured.)
 typedef float f2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ void put(float* p, f2 v) {
     __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -790,8 +794,11 @@ __device__ __forceinline__ Joined join_parts(const float* slots, size_t floats, 
     return j;
 }
 
-// Each tile is read once: non-temporal loads (32 x 4000 tokens in 16 bits 89.6
-// us, with ordinary ones 96.9; 16 x 8192 in 8 bits 54.3 and 59.1).
+// Each tile is read once: non-temporal loads (32 x 4000 tokens in 16 bits 89.2
+// us, with ordinary ones 96.1; 16 x 8192 in 8 bits 52.8 and 57.6).  A cache that
+// still lies in the 256 MB last-level cache would come faster with ordinary ones
+// (76 MB over and over 22.8 and 21.3), but between two steps of a sequence the
+// other layers' caches and weights pass through.
 constexpr int kStreamed = 2;
 
 // Reads go through one buffer descriptor a tile: its address in scalar
@@ -1022,6 +1029,12 @@ template <int D, int KB, int VB> struct AttendWave {
 // segment, a unit of 32 NW tokens a step, each wave on 32 of them with a
 // softmax of its own; the waves join in LDS, and the last workgroup of a
 // segment to finish joins the parts of all, through the workspace.
+//
+// Bound by the cache's bytes where there are many (32 x 16384 tokens at 4 bits:
+// 605 MB in 107 us, 5.7 TB/s, with the decoding of 4-bit codes, 200 of a step's
+// 240 vector instructions, close behind; 32 x 4000 in 16 bits: 525 MB in 81 us,
+// 6.5 TB/s of a plain read's 7.0), and by the chain of length, page number, first
+// tile and join where there are few (100 tokens 5.5 us, 2048 in parts 9).
 template <int D, int KB, int VB, int NW>
 __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void attend_kernel(AttendArgs a) {
     using PK = CachePart<D, KB>;
@@ -1388,25 +1401,26 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     const int64_t tokens = (int64_t)table_width * c->page_size;   // of the longest row
     // Workgroups of 8 waves, one a CU, for few segments of long rows whose steps
     // are light: a segment has half as many parts to join (at 4 bits, 131072
-    // tokens of 8 heads 38 us, with 4 waves 53; 4 x 16384 25.8 and 29.2; but 4
-    // x 4096 15.9 and 14.2; at 8 bits 4 x 16384 33.6 and 32.2).
+    // tokens of 8 heads 35.4 us, with 4 waves 47.8; 4 x 16384 22.7 and 26.9; but
+    // 4 x 4096 13.5 and 12.9; at 8 bits 4 x 16384 33.6 and 32.2).
     const bool eight = segments < 64 && tokens >= 16384 && attend_light(c->head_dim, c->k_bits, c->v_bits);
     out->waves = eight ? 8 : 4;
     out->head_tiles = (int)tiles;
     const int unit = 32 * out->waves;
     const int64_t units = (tokens - 1) / unit + 1;
-    // Rows that are not worth splitting: joining their parts costs what 1024
-    // tokens cost (one row of 1000 tokens 11.3 us whole, 16.1 split), and with
-    // a segment for each CU twice that (32 x 2000 tokens 21.8 us whole, 24.8
-    // split; at 16 x 2000 tokens 20.7 and 17.6).  Very many load the card
-    // evenly enough as they are, and every workgroup would look through all
-    // rows' lengths.
-    out->whole_units = (segments >= kCus ? 2048 : 1024) / unit;
+    // Rows that are not worth splitting: joining their parts costs what 640
+    // tokens cost where few workgroups run (one row of 800 tokens 10.9 us whole,
+    // 9.1 split; 600 tokens 8.9 and 9.2), 1024 where a quarter of the card does (8
+    // rows of 8 heads, 1000 tokens 11.6 whole, 12.6 split; 16 x 2000 22.1 and
+    // 16.7), and 2048 where all of it does (32 x 2000 23.4 and 23.2).  Very many
+    // load the card evenly enough as they are, and every workgroup would look
+    // through all rows' lengths.
+    out->whole_units = (segments >= kCus ? 2048 : segments >= 64 ? 1024 : 640) / unit;
     const bool split = units > out->whole_units && rows > 0 && segments <= kAttendMaxSegments && rows <= kAttendMaxRows;
     // With 64 segments or more, two workgroups a CU balance rows of different
-    // lengths (16 ragged rows of up to 8192 tokens 27 us, with one a CU 36;
-    // equal rows of 4096 tokens 24.9 against 25.9); below that they only add
-    // parts (4 x 4096 tokens 15.1 against 13.9).
+    // lengths (at 4 bits 16 ragged rows of up to 8192 tokens 23.2 us, with one a
+    // CU 30.8; equal rows of 4096 22.8 and 26.8); below that they only add parts
+    // (4 x 4096 tokens 13.4, with one a CU 12.9).
     out->target = split ? (segments >= 64 ? kCusLog2 + 1 : kCusLog2) : 0;
     // Where the lengths divide evenly into another number, that one.  One a CU
     // for heavy steps, whose loads fill the memory's queues by themselves (16 x
