@@ -580,6 +580,7 @@ struct AttendArgs {
     int target;                // log2 of the workgroups to split for; 0: a workgroup for each segment
     int other;                 // log2 of another number of workgroups, for lengths that come out at no more; 0: none
     int64_t other_units;       // from that many units on
+    int slack;                 // twelfths by which chunks may be longer for it
 };
 
 // Longest row: tokens are counted in 32 bits, up to a few units past the end.
@@ -674,11 +675,27 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
         };
         p.size = size_for(a.target);
         if (a.other && total * a.head_tiles.d >= a.other_units) {
-            const int size = size_for(a.other);
-            int pieces = 0;
-            for (int r0 = 0; r0 < a.rows; r0 += 64)
-                pieces += __builtin_amdgcn_readlane(wave_prefix((units_of(r0) + size - 1) / size), 63);
-            if (pieces * (int)a.head_tiles.d <= 1 << a.other) p.size = size;
+            // The first size, in twelfths from `size` on, that makes at most 2^limit
+            // pieces; 0: none.
+            auto fitting = [&](int size, int limit, int twelfths) {
+                for (int k = 0; k <= twelfths; ++k) {
+                    const int s = size + (size * k + 6) / 12;
+                    const float by = __builtin_amdgcn_rcpf((float)s);
+                    int pieces = 0;
+                    for (int r0 = 0; r0 < a.rows; r0 += 64) {
+                        const int units = units_of(r0), n = units + s - 1;   // a row's chunks: n / s, below 2^13
+                        int q = (int)((float)n * by);
+                        q -= q * s > n;
+                        q += (q + 1) * s <= n;
+                        pieces += __builtin_amdgcn_readlane(wave_prefix(q), 63);
+                    }
+                    if (pieces * (int)a.head_tiles.d <= 1 << limit) return s;
+                }
+                return 0;
+            };
+            int size = fitting(size_for(a.other), a.other, a.slack);
+            if (size == 0 && a.other < a.target) size = fitting(p.size, a.target, 6);
+            if (size > 0) p.size = size;
         }
     }
     int before = 0;   // pieces of earlier rows
@@ -1384,7 +1401,7 @@ constexpr int64_t kFullTokens = (int64_t)1 << 22;
 struct AttendPlan {
     int head_tiles, wgs, waves;   // waves of a workgroup
     int target, whole_units;
-    int other;
+    int other, slack;
     int64_t other_units;
     size_t ws_bytes;
 };
@@ -1422,16 +1439,23 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // CU 30.8; equal rows of 4096 22.8 and 26.8); below that they only add parts
     // (4 x 4096 tokens 13.4, with one a CU 12.9).
     out->target = split ? (segments >= 64 ? kCusLog2 + 1 : kCusLog2) : 0;
-    // Where the lengths divide evenly into another number, that one.  One a CU
-    // for heavy steps, whose loads fill the memory's queues by themselves (16 x
-    // 4096 tokens in 16 bits 47.6 us, with two 52.8; 16 x 8192 in 8 bits 51.8 and
-    // 52.3; head_dim 256, 16 x 4096 at 4 bits 32.5 and 36.4).  Four, all that fit,
-    // for very long rows at 4 bits, whose decoding waits for loads (32 x 16384
-    // 109 us, with two 114; head_dim 64, 64 x 16384 119 and 139; but 16 x 16384
-    // 61.4 and 60.9, and head_dim 96, 32 x 16384 108.4 and 105.8).
+    // Other numbers, where the lengths come out at no more than those with chunks
+    // that are little longer.  Heavy steps fill the memory's queues by themselves:
+    // one workgroup a CU (16 x 4096 tokens in 16 bits 48.2 us, with two 52.8; 24 x
+    // 4096 62.7 and 81.5; 16 x 8192 ragged 44.3 and 50.2; head_dim 256, 20 x 4096
+    // in 8 bits 40.0 and 50.5), with chunks up to a third longer where a token has
+    // 384 bytes or more, else of that size only (16 x 8192 ragged in 8 bits 33.4,
+    // with two 31.1); failing that exactly two, with chunks up to half longer (32
+    // x 4000 ragged in 8 bits 36.6 us, with what they come out at 39.4; 4-bit rows
+    // lose by it, 32 x 16384 ragged 85.8 and 77.7).  More segments than CUs have
+    // that many anyway.  Four, all that fit, for very long rows at 4 bits, whose
+    // decoding waits for loads (32 x 16384 109 us, with two 114; head_dim 64, 64 x
+    // 16384 119 and 139; but 16 x 16384 61.4 and 60.9, and head_dim 96, 32 x 16384
+    // 108.4 and 105.8).
     const bool heavy = !attend_light(c->head_dim, c->k_bits, c->v_bits);
     const bool full = attend_full(c->head_dim, c->k_bits, c->v_bits) && segments * tokens >= kFullTokens;
-    out->other = !split || segments < 64 ? 0 : heavy ? kCusLog2 : full ? kCusLog2 + 2 : 0;
+    out->other = !split || segments < 64 ? 0 : heavy ? (segments <= kCus ? kCusLog2 : 0) : full ? kCusLog2 + 2 : 0;
+    out->slack = row_bytes(c->head_dim, c->k_bits, c->v_bits) >= 384 ? 4 : 0;
     out->other_units = heavy ? 0 : kFullTokens / unit;
     out->wgs = split ? (int)std::min<int64_t>(std::max<int64_t>((1 << out->target) + segments, out->other ? 1 << out->other : 0),
                                               segments * std::min<int64_t>(units, kAttendMaxParts))
@@ -1579,6 +1603,7 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.target = p.target;
     a.other = p.other;
     a.other_units = p.other_units;
+    a.slack = p.slack;
     a.whole_units = p.whole_units;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     with_geometry(c, [&](auto D, auto KB, auto VB) {

@@ -441,12 +441,13 @@ def test_rows_beyond_a_waves_lanes_with_long_ones_among_them(exq, rows):
 @pytest.mark.parametrize("dim,kv_heads,rows,bits", [(64, 4, 16, (16, 16)), (128, 8, 8, (8, 8)), (256, 1, 64, (4, 4)),
                                                     (64, 1, 128, (16, 16)), (96, 4, 24, (16, 16))])
 def test_even_and_nearly_even_batches(exq, dim, kv_heads, rows, bits):
-    """Rows of one length, whose chunks come out at one a CU, and the same with a short, an empty and a padding row."""
+    """Rows of one length, whose chunks come out at one a CU, the same with a short, an empty and a padding row, and any."""
     c = Case(exq, 33, [1500], 32, kv_heads, dim, bits, spare=0)
     c.k, c.v = c.k * rows, c.v * rows
     table = c.dtable.expand(rows, -1)
     q = values(c.rng, rows, kv_heads, dim)
-    for n in ([1500] * rows, [1400] * (rows - 1) + [130], [0, -1] + [1500] * (rows - 2)):
+    ragged = [int(x) for x in c.rng.integers(1, 1501, rows)]
+    for n in ([1500] * rows, [1400] * (rows - 1) + [130], [0, -1] + [1500] * (rows - 2), ragged):
         note("even batch dim=%d bits=%s lengths=%s.." % (dim, bits, n[:2]))
         out, lse = c.cache.attend(to_dev(q), table, i32(n), return_lse=True)
         c.check(out, lse, q, dim ** -0.5, lengths=n)
