@@ -1454,9 +1454,16 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // 108.4 and 105.8).
     const bool heavy = !attend_light(c->head_dim, c->k_bits, c->v_bits);
     const bool full = attend_full(c->head_dim, c->k_bits, c->v_bits) && segments * tokens >= kFullTokens;
-    out->other = !split || segments < 64 ? 0 : heavy ? (segments <= kCus ? kCusLog2 : 0) : full ? kCusLog2 + 2 : 0;
-    out->slack = row_bytes(c->head_dim, c->k_bits, c->v_bits) >= 384 ? 4 : 0;
-    out->other_units = heavy ? 0 : kFullTokens / unit;
+    // Below 64 segments one a CU is the aim already, and a few workgroups more
+    // would double it for some: chunks up to a third longer if that makes them
+    // fit (5 x 16384 tokens at 4 bits 27.9 us, without 35.6; 6 x 8192 in 16 bits
+    // 38.9 and 51.6; 4 x 16384, which fit, 23.1 and 22.9).  8 segments have 256
+    // parts at most.
+    const bool few = segments < 64;
+    out->other = !split ? 0 : few ? (segments * kAttendMaxParts > kCus ? kCusLog2 : 0)
+                 : heavy ? (segments <= kCus ? kCusLog2 : 0) : full ? kCusLog2 + 2 : 0;
+    out->slack = few || row_bytes(c->head_dim, c->k_bits, c->v_bits) >= 384 ? 4 : 0;
+    out->other_units = few || heavy ? 0 : kFullTokens / unit;
     out->wgs = split ? (int)std::min<int64_t>(std::max<int64_t>((1 << out->target) + segments, out->other ? 1 << out->other : 0),
                                               segments * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
