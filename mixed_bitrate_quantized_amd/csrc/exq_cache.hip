@@ -579,7 +579,8 @@ struct AttendArgs {
     int whole_units;           // rows of at most this many units are not split
     int target;                // log2 of the workgroups to split for; 0: a workgroup for each segment
     int other;                 // log2 of another number of workgroups, for lengths that come out at no more; 0: none
-    int64_t other_units;       // from that many units on
+    int other_size;            // if chunks would have at least so many units then,
+    float other_rows;          // and the rows together are as long as so many of the longest
     int slack;                 // twelfths by which chunks may be longer for it
 };
 
@@ -647,7 +648,8 @@ struct Piece {
 // With U units in all segments, chunks have at least U / 2^target units, so
 // there are at most 2^target + segments of them, and a segment has at most
 // kAttendMaxParts.  With `other` for `target` only where there are at most
-// 2^other: as many as fit side by side.  False: there are fewer pieces.
+// 2^other: as many as fit side by side (of at most 64 rows).  False: there are
+// fewer pieces.
 __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w, Piece& p) {
     int loaded = -1, mine = -1;
     auto units_of = [&](int r0) {
@@ -658,59 +660,62 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
         }
         return row_span(a, mine, unit).units;
     };
-    int64_t total = 0;
+    uint32_t total = 0;   // fits: 256 rows of under 2^24 units
     int longest = 0;
     for (int r0 = 0; r0 < a.rows; r0 += 64) {
         const int units = units_of(r0);
-        total += __builtin_amdgcn_readlane(wave_prefix(units), 63);
+        total += (uint32_t)__builtin_amdgcn_readlane(wave_prefix(units), 63);
         const int most = wave_max(units);
         longest = longest > most ? longest : most;
     }
-    p.size = longest > 0 ? longest : 1;
+    const uint64_t all = (uint64_t)total * a.head_tiles.d;
+    const int least = (longest + kAttendMaxParts - 1) / kAttendMaxParts;
+    auto size_for = [&](int target) {
+        const int even = (int)((all + (1u << target) - 1) >> target);
+        return even > least ? even : least;
+    };
+    int size = longest > 0 ? longest : 1;
+    int limit = 0, k = 0, most_k = 0;   // pieces that may come out (0: any), the size's twelfths above `size`, and how many
     if (longest > a.whole_units) {
-        const int least = (longest + kAttendMaxParts - 1) / kAttendMaxParts;
-        auto size_for = [&](int target) {
-            const int even = (int)((total * a.head_tiles.d + (1ll << target) - 1) >> target);
-            return even > least ? even : least;
-        };
-        p.size = size_for(a.target);
-        if (a.other && total * a.head_tiles.d >= a.other_units) {
-            // The first size, in twelfths from `size` on, that makes at most 2^limit
-            // pieces; 0: none.
-            auto fitting = [&](int size, int limit, int twelfths) {
-                for (int k = 0; k <= twelfths; ++k) {
-                    const int s = size + (size * k + 6) / 12;
-                    const float by = __builtin_amdgcn_rcpf((float)s);
-                    int pieces = 0;
-                    for (int r0 = 0; r0 < a.rows; r0 += 64) {
-                        const int units = units_of(r0), n = units + s - 1;   // a row's chunks: n / s, below 2^13
-                        int q = (int)((float)n * by);
-                        q -= q * s > n;
-                        q += (q + 1) * s <= n;
-                        pieces += __builtin_amdgcn_readlane(wave_prefix(q), 63);
-                    }
-                    if (pieces * (int)a.head_tiles.d <= 1 << limit) return s;
-                }
-                return 0;
-            };
-            int size = fitting(size_for(a.other), a.other, a.slack);
-            if (size == 0 && a.other < a.target) size = fitting(p.size, a.target, 6);
-            if (size > 0) p.size = size;
+        size = size_for(a.target);
+        if (a.other) {
+            const int lone = size_for(a.other);
+            if (lone >= a.other_size && (float)total >= (float)longest * a.other_rows) {
+                size = lone;
+                limit = a.other;
+                most_k = a.slack;
+            }
         }
     }
     int before = 0;   // pieces of earlier rows
     for (int r0 = 0; r0 < a.rows; r0 += 64) {
         const int units = units_of(r0);
-        const int chunks = (units + p.size - 1) / p.size;
-        const int v = wave_prefix(chunks) * (int)a.head_tiles.d;
-        const int sum = __builtin_amdgcn_readlane(v, 63);
+        int chunks, v, sum;
+        for (;;) {
+            p.size = size + (size * k + 6) / 12;
+            // a row's chunks: n / p.size, at most 32, or 1 in whole rows
+            const int n = units + p.size - 1;
+            chunks = (int)((float)n * __builtin_amdgcn_rcpf((float)p.size));
+            chunks -= chunks * p.size > n;
+            chunks += (chunks + 1) * p.size <= n;
+            v = wave_prefix(chunks) * (int)a.head_tiles.d;
+            sum = __builtin_amdgcn_readlane(v, 63);
+            if (limit == 0 || sum <= 1 << limit) break;
+            if (++k > most_k) {   // up to `other`, then up to `target` if that is more, then as they come
+                k = 0;
+                most_k = 6;
+                size = size_for(a.target);
+                limit = limit < a.target ? a.target : 0;
+            }
+        }
         if (w < before + sum) {
             const int at = __builtin_popcountll(__builtin_amdgcn_ballot_w64(before + v <= w));   // rows that end at or before w
             p.row = r0 + at;
             p.length = __builtin_amdgcn_readlane(mine, at);
             p.chunks = __builtin_amdgcn_readlane(chunks, at);
             before += __builtin_amdgcn_readlane(v, at) - p.chunks * (int)a.head_tiles.d;
-            p.seg = p.chunks == 1 ? w - before : (w - before) / p.chunks;
+            // a quotient of numbers below 2^12, exact with half of one to spare
+            p.seg = uniform((int)(((float)(w - before) + 0.5f) * __builtin_amdgcn_rcpf((float)p.chunks)));
             p.first = before + p.seg * p.chunks;
             p.chunk = w - p.first;
             return true;
@@ -1401,8 +1406,8 @@ constexpr int64_t kFullTokens = (int64_t)1 << 22;
 struct AttendPlan {
     int head_tiles, wgs, waves;   // waves of a workgroup
     int target, whole_units;
-    int other, slack;
-    int64_t other_units;
+    int other, other_size, slack;
+    float other_rows;
     size_t ws_bytes;
 };
 
@@ -1446,9 +1451,11 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // in 8 bits 40.0 and 50.5), with chunks up to a third longer where a token has
     // 384 bytes or more, else of that size only (16 x 8192 ragged in 8 bits 33.4,
     // with two 31.1); failing that exactly two, with chunks up to half longer (32
-    // x 4000 ragged in 8 bits 36.6 us, with what they come out at 39.4; 4-bit rows
-    // lose by it, 32 x 16384 ragged 85.8 and 77.7).  More segments than CUs have
-    // that many anyway.  Four, all that fit, for very long rows at 4 bits, whose
+    // x 4000 ragged in 8 bits 36.6 us, with what they come out at 39.4).  Light
+    // ones: exactly two if the rows are about equally long (12 x 8192 at 4 bits
+    // 31.1 us, 34.2 without; 11 x 8192 in 4 and 8 bits 34.6 and 39.5; 16 x 4096,
+    // which come out at that, 23.7 and 23.1; ragged rows would lose, 32 x 16384
+    // 85.8 and 77.7).  More segments than CUs have that many anyway.  Four, all that fit, for very long rows at 4 bits, whose
     // decoding waits for loads (32 x 16384 109 us, with two 114; head_dim 64, 64 x
     // 16384 119 and 139; but 16 x 16384 61.4 and 60.9, and head_dim 96, 32 x 16384
     // 108.4 and 105.8).
@@ -1460,10 +1467,12 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // 38.9 and 51.6; 4 x 16384, which fit, 23.1 and 22.9).  8 segments have 256
     // parts at most.
     const bool few = segments < 64;
-    out->other = !split ? 0 : few ? (segments * kAttendMaxParts > kCus ? kCusLog2 : 0)
-                 : heavy ? (segments <= kCus ? kCusLog2 : 0) : full ? kCusLog2 + 2 : 0;
-    out->slack = few || row_bytes(c->head_dim, c->k_bits, c->v_bits) >= 384 ? 4 : 0;
-    out->other_units = few || heavy ? 0 : kFullTokens / unit;
+    const bool whole_card = !few && full;
+    out->other = !split || rows > 64 ? 0 : few ? (segments * kAttendMaxParts > kCus ? kCusLog2 : 0)
+                 : whole_card ? kCusLog2 + 2 : segments > kCus ? 0 : heavy ? kCusLog2 : kCusLog2 + 1;
+    out->slack = whole_card || (!few && heavy && row_bytes(c->head_dim, c->k_bits, c->v_bits) < 384) ? 0 : 4;
+    out->other_size = whole_card ? (int)(kFullTokens / unit >> out->other) : 2;   // chunks of one unit fit as they are
+    out->other_rows = few || heavy ? 0.0f : 0.875f * (float)rows;
     out->wgs = split ? (int)std::min<int64_t>(std::max<int64_t>((1 << out->target) + segments, out->other ? 1 << out->other : 0),
                                               segments * std::min<int64_t>(units, kAttendMaxParts))
                      : (int)segments;
@@ -1609,7 +1618,8 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.page_tiles = Divisor::of(a.c.tiles);
     a.target = p.target;
     a.other = p.other;
-    a.other_units = p.other_units;
+    a.other_size = p.other_size;
+    a.other_rows = p.other_rows;
     a.slack = p.slack;
     a.whole_units = p.whole_units;
     const hipStream_t s = static_cast<hipStream_t>(stream);

@@ -440,7 +440,8 @@ def test_rows_beyond_a_waves_lanes_with_long_ones_among_them(exq, rows):
 
 @pytest.mark.parametrize("dim,kv_heads,rows,bits", [(64, 4, 16, (16, 16)), (128, 8, 8, (8, 8)), (256, 1, 64, (4, 4)),
                                                     (64, 1, 128, (16, 16)), (96, 4, 24, (16, 16)),
-                                                    (128, 4, 5, (4, 4)), (64, 3, 7, (8, 4)), (128, 7, 6, (16, 16))])
+                                                    (128, 4, 5, (4, 4)), (64, 3, 7, (8, 4)), (128, 7, 6, (16, 16)),
+                                                    (128, 8, 11, (4, 8)), (64, 8, 12, (4, 4))])
 def test_even_and_nearly_even_batches(exq, dim, kv_heads, rows, bits):
     """Rows of one length, whose chunks come out at one a CU, the same with a short, an empty and a padding row, and any."""
     c = Case(exq, 33, [1500], 32, kv_heads, dim, bits, spare=0)
