@@ -560,6 +560,9 @@ struct Divisor {
     }
 };
 
+// Longest row: tokens are counted in 32 bits, up to a few units past the end.
+constexpr int kMaxLength = 0x7FFF0000;
+
 struct AttendArgs {
     CacheDev c;
     TableDev t;
@@ -572,6 +575,7 @@ struct AttendArgs {
     float* ws;
     float scale;               // scale * log2(e)
     int window;
+    int most;                  // longest row: what the table holds, kMaxLength at most
     int rows, q_heads, group;  // group: query heads per key-value head
     Divisor head_tiles;        // kv_heads * ceil(group / 16): segments of a row
     Divisor group_tiles;       // ceil(group / 16)
@@ -584,9 +588,6 @@ struct AttendArgs {
     int slack;                 // twelfths by which chunks may be longer for it
 };
 
-// Longest row: tokens are counted in 32 bits, up to a few units past the end.
-constexpr int kMaxLength = 0x7FFF0000;
-
 // Tokens [lo, hi) that a row of length n attends to, and its number of units
 // of `unit` tokens from the one that holds lo.  Rows left alone have no unit;
 // empty rows and rows to be filled with NaN have one without tokens.
@@ -596,9 +597,7 @@ struct RowSpan {
 };
 __device__ __forceinline__ RowSpan row_span(const AttendArgs& a, int n, int unit) {
     if (n < 0) return {0, 0, 0, false};
-    uint64_t cap = (uint64_t)a.t.width * a.c.page_size;
-    if (cap > (uint64_t)kMaxLength) cap = (uint64_t)kMaxLength;
-    if (n == 0 || (uint64_t)n > cap) return {0, 0, 1, n != 0};
+    if (n == 0 || n > a.most) return {0, 0, 1, n != 0};
     const int lo = a.window > 0 && n > a.window ? n - a.window : 0;
     return {lo, n, (n - 1) / unit - lo / unit + 1, false};
 }
@@ -651,19 +650,16 @@ struct Piece {
 // 2^other: as many as fit side by side (of at most 64 rows).  False: there are
 // fewer pieces.
 __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w, Piece& p) {
-    int loaded = -1, mine = -1;
-    auto units_of = [&](int r0) {
-        if (r0 != loaded) {
-            const int r = r0 + (int)(threadIdx.x & 63);
-            mine = r < a.rows ? gptr<int32_t>(a.lengths)[r] : -1;
-            loaded = r0;
-        }
-        return row_span(a, mine, unit).units;
-    };
+    int mine, units, longest = 0;
     uint32_t total = 0;   // fits: 256 rows of under 2^24 units
-    int longest = 0;
-    for (int r0 = 0; r0 < a.rows; r0 += 64) {
-        const int units = units_of(r0);
+    auto load = [&](int r0) {
+        const int r = r0 + (int)(threadIdx.x & 63);
+        mine = r < a.rows ? gptr<int32_t>(a.lengths)[r] : -1;
+        units = row_span(a, mine, unit).units;
+    };
+    // (backwards: the first 64 are there when the second pass starts)
+    for (int r0 = (a.rows - 1) & ~63; r0 >= 0; r0 -= 64) {
+        load(r0);
         total += (uint32_t)__builtin_amdgcn_readlane(wave_prefix(units), 63);
         const int most = wave_max(units);
         longest = longest > most ? longest : most;
@@ -688,8 +684,7 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
         }
     }
     int before = 0;   // pieces of earlier rows
-    for (int r0 = 0; r0 < a.rows; r0 += 64) {
-        const int units = units_of(r0);
+    for (int r0 = 0;;) {
         int chunks, v, sum;
         for (;;) {
             p.size = size + (size * k + 6) / 12;
@@ -721,8 +716,10 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
             return true;
         }
         before += sum;
+        r0 += 64;
+        if (r0 >= a.rows) return false;
+        load(r0);
     }
-    return false;
 }
 
 // Partial results follow the counters, a slot for each workgroup: the group's
@@ -1610,6 +1607,7 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     a.ws = static_cast<float*>(workspace);
     a.scale = scale * kLog2e;
     a.window = window;
+    a.most = (int)std::min<int64_t>(kMaxLength, (int64_t)table_width * c->page_size);
     a.rows = rows;
     a.q_heads = q_heads;
     a.group = q_heads / c->kv_heads;
