@@ -634,6 +634,13 @@ __device__ __forceinline__ int wave_max(int v) {
     return __builtin_amdgcn_readlane(v, 63);
 }
 
+// n / d of numbers below 2^12, d > 0: half of one to spare makes it exact.  A
+// few instructions, where the integer division has forty: code that runs once
+// costs its fetch, about 0.1 us for every 64 bytes.
+__device__ __forceinline__ int small_quotient(int n, int d) {
+    return (int)(((float)n + 0.5f) * __builtin_amdgcn_rcpf((float)d));
+}
+
 // One workgroup's work: chunk `chunk` of `chunks` of a segment (row, kv head,
 // 16 query heads), `size` units a chunk, and the number of the workgroup that
 // has the segment's first.
@@ -709,8 +716,7 @@ __device__ __forceinline__ bool find_piece(const AttendArgs& a, int unit, int w,
             p.length = __builtin_amdgcn_readlane(mine, at);
             p.chunks = __builtin_amdgcn_readlane(chunks, at);
             before += __builtin_amdgcn_readlane(v, at) - p.chunks * (int)a.head_tiles.d;
-            // a quotient of numbers below 2^12, exact with half of one to spare
-            p.seg = uniform((int)(((float)(w - before) + 0.5f) * __builtin_amdgcn_rcpf((float)p.chunks)));
+            p.seg = uniform(small_quotient(w - before, p.chunks));
             p.first = before + p.seg * p.chunks;
             p.chunk = w - p.first;
             return true;
@@ -1233,8 +1239,8 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
     // The last to finish joins the parts, in order: threads by items, and where
     // there are threads left over several of them on one item's parts.
     const float* parts = slots + (size_t)p.first * floats;
-    const int ways = items < THREADS ? THREADS / items : 1;
-    if (ways == 1) {
+    const int ways = uniform(small_quotient(THREADS, items));   // 0: more items than threads
+    if (ways <= 1) {
         for (int i = id; i < items; i += THREADS) {
             const int h = i / (D / 4), d = i % (D / 4) * 4;
             finish(a, p.row, h0 + h, d, join_parts<D>(parts, floats, 0, 1, p.chunks, hp, h, d), false);
@@ -1243,7 +1249,7 @@ __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void a
     }
     f4* way_o = reinterpret_cast<f4*>(&part_o[0][0][0]);                     // [THREADS]
     f2* way_rl = reinterpret_cast<f2*>(&part_o[0][0][0]) + 2 * THREADS;      // [THREADS]
-    const int way = id / items, i = id % items, h = i / (D / 4), d = i % (D / 4) * 4;
+    const int way = small_quotient(id, items), i = id - way * items, h = i / (D / 4), d = i % (D / 4) * 4;
     Joined j = {{0, 0, 0, 0}, -3e38f, 0.0f};
     if (way < ways) j = join_parts<D>(parts, floats, way, ways, p.chunks, hp, h, d);
     way_o[id] = j.o;
