@@ -1448,27 +1448,27 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // (4 x 4096 tokens 13.4, with one a CU 12.9).
     out->target = split ? (segments >= 64 ? kCusLog2 + 1 : kCusLog2) : 0;
     // Other numbers, where the lengths come out at no more than those with chunks
-    // that are little longer.  Heavy steps fill the memory's queues by themselves:
-    // one workgroup a CU (16 x 4096 tokens in 16 bits 48.2 us, with two 52.8; 24 x
-    // 4096 62.7 and 81.5; 16 x 8192 ragged 44.3 and 50.2; head_dim 256, 20 x 4096
-    // in 8 bits 40.0 and 50.5), with chunks up to a third longer where a token has
-    // 384 bytes or more, else of that size only (16 x 8192 ragged in 8 bits 33.4,
-    // with two 31.1); failing that exactly two, with chunks up to half longer (32
-    // x 4000 ragged in 8 bits 36.6 us, with what they come out at 39.4).  Light
-    // ones: exactly two if the rows are about equally long (12 x 8192 at 4 bits
-    // 31.1 us, 34.2 without; 11 x 8192 in 4 and 8 bits 34.6 and 39.5; 16 x 4096,
-    // which come out at that, 23.7 and 23.1; ragged rows would lose, 32 x 16384
-    // 85.8 and 77.7).  More segments than CUs have that many anyway.  Four, all that fit, for very long rows at 4 bits, whose
-    // decoding waits for loads (32 x 16384 109 us, with two 114; head_dim 64, 64 x
-    // 16384 119 and 139; but 16 x 16384 61.4 and 60.9, and head_dim 96, 32 x 16384
-    // 108.4 and 105.8).
+    // that are a little longer:
+    // - heavy steps fill the memory's queues by themselves.  One workgroup a CU (16
+    //   x 4096 tokens in 16 bits 47.9 us, with two 52.8; 24 x 4096 62.0 and 81.4; 16
+    //   x 8192 ragged 43.5 and 49.3; head_dim 256, 20 x 4096 in 8 bits 40.0 and
+    //   50.5), with chunks up to a third longer where a token has 384 bytes or more,
+    //   else of the equal size only (16 x 8192 ragged in 8 bits 33.4, with two
+    //   31.1); failing that exactly two, with chunks up to half longer (32 x 4000
+    //   ragged in 8 bits 35.5 us, with what they come out at 39.5).  More segments
+    //   than CUs make two of that kind anyway;
+    // - light ones: exactly two if the rows are about equally long (12 x 8192 at 4
+    //   bits 30.2 us, with what they come out at 33.8; 11 x 8192 in 4 and 8 bits
+    //   34.6 and 39.5; ragged rows would lose, 32 x 16384 85.8 and 77.7);
+    // - four, all that fit, for very long rows at 4 bits, whose decoding waits for
+    //   loads (32 x 16384 108 us, with two 114; head_dim 64, 64 x 16384 119 and 139;
+    //   but 16 x 16384 61.4 and 60.9, and head_dim 96, 32 x 16384 108.4 and 105.8).
     const bool heavy = !attend_light(c->head_dim, c->k_bits, c->v_bits);
     const bool full = attend_full(c->head_dim, c->k_bits, c->v_bits) && segments * tokens >= kFullTokens;
     // Below 64 segments one a CU is the aim already, and a few workgroups more
     // would double it for some: chunks up to a third longer if that makes them
-    // fit (5 x 16384 tokens at 4 bits 27.9 us, without 35.6; 6 x 8192 in 16 bits
-    // 38.9 and 51.6; 4 x 16384, which fit, 23.1 and 22.9).  8 segments have 256
-    // parts at most.
+    // fit (5 x 16384 tokens at 4 bits 27.2 us, without 35.2; 6 x 8192 in 16 bits
+    // 38.9 and 51.6).  8 segments have 256 parts at most.
     const bool few = segments < 64;
     const bool whole_card = !few && full;
     out->other = !split || rows > 64 ? 0 : few ? (segments * kAttendMaxParts > kCus ? kCusLog2 : 0)
