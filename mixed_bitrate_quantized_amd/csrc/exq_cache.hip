@@ -1387,9 +1387,10 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
                            int table_rows, int table_width, int64_t table_stride, const int32_t* seqs,
                            const int32_t* positions) {
     if (rows < 0) return fail(EXQ_ERR_INVALID_ARG, "rows=%d", rows);
+    if (table_rows < 0 || table_width < 0) return fail(EXQ_ERR_INVALID_ARG, "table of %d x %d", table_rows, table_width);
+    if (rows == 0) return EXQ_OK;   // a step without rows: the tensors may be empty, their pointers NULL
     exq_status st;
     if ((st = check_table(table, table_rows, table_width, table_stride)) != EXQ_OK) return st;
-    if (rows == 0) return EXQ_OK;
     if ((st = check_operand(k)) != EXQ_OK || (st = check_operand(v)) != EXQ_OK) return st;
     if (!seqs || !positions || !cache_aligned(seqs, 4) || !cache_aligned(positions, 4))
         return fail(EXQ_ERR_INVALID_ARG, "seqs or positions is NULL or misaligned");
@@ -1418,7 +1419,7 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     if (rows < 0) return fail(EXQ_ERR_INVALID_ARG, "rows=%d", rows);
     if (q_heads < 1 || q_heads % c->kv_heads)
         return fail(EXQ_ERR_INVALID_ARG, "q_heads=%d is not a positive multiple of kv_heads=%d", q_heads, c->kv_heads);
-    if (table_width < 1) return fail(EXQ_ERR_INVALID_ARG, "table_width=%d", table_width);
+    if (table_width < (rows > 0)) return fail(EXQ_ERR_INVALID_ARG, "table_width=%d", table_width);
     const int group = q_heads / c->kv_heads;
     const int64_t tiles = (int64_t)c->kv_heads * ((group + 15) / 16), segments = tiles * rows;
     if (segments > kMaxLaunchThreads / 256)

@@ -115,6 +115,25 @@ def test_no_rows_is_a_no_op(cache):
     exq.exq_attend(cache, *attend_args(rows=0)[:-1], stream=0)
 
 
+@pytest.mark.parametrize("table", [dict(table=0, trows=0, tstride=0), dict(table=0, trows=0, width=0, tstride=0), dict(trows=0),
+                                   dict(k=0, v=0, seqs=0, pos=0)], ids=str)
+def test_no_rows_is_a_no_op_with_an_empty_table_too(cache, table):
+    """A step without rows hands over empty tensors, whose pointers are NULL."""
+    exq.exq_cache_append(cache, *rows_args(rows=0, **table))
+    exq.exq_cache_read(cache, *rows_args(rows=0, **table))
+    for bad in (dict(trows=-1), dict(width=-1)):
+        expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_cache_append, cache, *rows_args(rows=0, **{**table, **bad}))
+        expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_cache_read, cache, *rows_args(rows=0, **{**table, **bad}))
+
+
+def test_attend_of_no_rows_with_an_empty_table(cache):
+    for width in (400, 0):
+        exq.exq_attend(cache, *attend_args(rows=0, table=0, width=width, tstride=0, q=0, out=0, lse=0, lengths=0, ws=0, wsb=0)[:-1],
+                       stream=0)
+        assert exq.exq_attend_workspace_bytes(cache, 0, 8, width) == 0
+    expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_attend, cache, *attend_args(rows=0, width=-1))
+
+
 Q, O, L, W = FAKE + 2 * SIZE, FAKE + 4 * SIZE, FAKE + 6 * SIZE, 1 << 40
 
 
