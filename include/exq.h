@@ -398,8 +398,8 @@ void exq_cache_destroy(exq_cache_t cache);
  *              differ: of two rows sent to one place either may be stored, or a
  *              mixture of both.
  * Nothing but the bytes of those rows is written.  rows == 0 is a no-op.
- * Errors: INVALID_ARG (NULL, misaligned, bad size or stride, k or v overlapping
- * the pages), UNSUPPORTED (rows * heads beyond a launch's 2^32 threads), HIP. */
+ * Errors: INVALID_ARG (NULL, misaligned, bad size or stride, k, v, table, seqs or
+ * positions overlapping the pages), UNSUPPORTED (rows * heads beyond a launch's 2^32 threads), HIP. */
 exq_status exq_cache_append(exq_cache_t cache, const void* k, int64_t k_row_stride, int64_t k_head_stride,
                             const void* v, int64_t v_row_stride, int64_t v_head_stride, int rows,
                             const int32_t* table, int table_rows, int table_width, int64_t table_stride,
@@ -407,7 +407,8 @@ exq_status exq_cache_append(exq_cache_t cache, const void* k, int64_t k_row_stri
 
 /* Read `rows` tokens back as the fp16 values the cache holds for them, bit for
  * bit x_hat.  Arguments as exq_cache_append, with k and v written (their rows
- * and heads must not overlap themselves or each other); positions may repeat.
+ * and heads must not overlap themselves, each other, the table, seqs or
+ * positions); positions may repeat.
  * A row with seqs[r] < 0 is left as it was; a row whose sequence, position or
  * page is outside the table or the cache is filled with NaN. */
 exq_status exq_cache_read(exq_cache_t cache, void* k, int64_t k_row_stride, int64_t k_head_stride, void* v,
@@ -433,8 +434,7 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  *              table_width * page_size or 2^31 - 2^16, or a page outside the cache
  *              among those read: out and lse are NaN.
  *   scale      finite, magnitude below 2^127;  window >= 0
- *   out        device fp16 with strides as for q, no element twice, no overlap
- *              with q or the pages
+ *   out        device fp16 with strides as for q, no element twice
  *   lse        device fp32 [rows][q_heads] or NULL
  *   workspace  device, 16-byte aligned, exq_attend_workspace_bytes() bytes; NULL if
  *              that is 0.  Its first EXQ_ATTEND_COUNTER_BYTES must be zero before the
@@ -442,6 +442,8 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  *              may hold anything.  Calls of any sizes may share one in stream
  *              order; calls that may run at the same time (other streams, replays
  *              of two graphs) need one each.
+ * out, lse and the workspace must not overlap each other, q, the table, lengths or
+ * the pages.
  * What a page holds behind a sequence's end, or before its window, never
  * reaches the result, NaN included.  Scores, softmax sums and output sums are
  * fp32; the weights e^{S_j - max} enter the second product rounded to fp16.

@@ -1350,6 +1350,11 @@ exq_status check_table(const int32_t* table, int rows, int width, int64_t stride
     return EXQ_OK;
 }
 
+// Bytes of a table from its first element to past its last.
+size_t table_extent(int rows, int width, int64_t stride) {
+    return 4 * ((size_t)(rows - 1) * (size_t)stride + (size_t)width);
+}
+
 // Calls f(IC<D>, IC<KB>, IC<VB>) for the cache's geometry.
 template <class F>
 void with_geometry(const exq_cache* c, F&& f) {
@@ -1400,6 +1405,14 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
     if (rows_waves(c, rows) > kMaxLaunchThreads / 64 - 8)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, c->kv_heads);
     return EXQ_OK;
+}
+
+// Whether [p, p + n), which a rows call writes, meets the table, seqs or
+// positions, which it reads.
+bool meets_indices(const void* p, size_t n, int rows, const int32_t* table, int table_rows, int table_width,
+                   int64_t table_stride, const int32_t* seqs, const int32_t* positions) {
+    return ranges_meet(p, n, table, table_extent(table_rows, table_width, table_stride)) ||
+           ranges_meet(p, n, seqs, 4 * (size_t)rows) || ranges_meet(p, n, positions, 4 * (size_t)rows);
 }
 
 // Tokens of all segments from which on attend_full geometries take a workgroup
@@ -1525,6 +1538,8 @@ exq_status exq_cache_append(exq_cache_t c, const void* k, int64_t k_row_stride, 
     const exq_status st =
         check_rows_call(c, ko, vo, rows, table, table_rows, table_width, table_stride, seqs, positions);
     if (st != EXQ_OK || rows == 0) return st;
+    if (meets_indices(c->pages, (size_t)c->n_pages * c->page_bytes, rows, table, table_rows, table_width, table_stride, seqs, positions))
+        return fail(EXQ_ERR_INVALID_ARG, "table, seqs or positions overlaps the cache's pages");
     const CacheDev d = cache_dev(c);
     const TableDev t{table, table_stride, (uint32_t)table_rows, (uint32_t)table_width};
     const dim3 grid(rows_workgroups(c, rows));
@@ -1548,6 +1563,9 @@ exq_status exq_cache_read(exq_cache_t c, void* k, int64_t k_row_stride, int64_t 
     if (st != EXQ_OK || rows == 0) return st;
     if (!distinct(ko) || !distinct(vo)) return fail(EXQ_ERR_INVALID_ARG, "rows or heads of k or v overlap themselves");
     if (operands_meet(ko, vo)) return fail(EXQ_ERR_INVALID_ARG, "k and v overlap");
+    if (meets_indices(k, extent(ko), rows, table, table_rows, table_width, table_stride, seqs, positions) ||
+        meets_indices(v, extent(vo), rows, table, table_rows, table_width, table_stride, seqs, positions))
+        return fail(EXQ_ERR_INVALID_ARG, "k or v overlaps table, seqs or positions");
     const CacheDev d = cache_dev(c);
     const TableDev t{table, table_stride, (uint32_t)table_rows, (uint32_t)table_width};
     const dim3 grid(rows_workgroups(c, rows));
@@ -1593,12 +1611,19 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     if (lse && (ranges_meet(lse, lse_bytes, out, extent(oo)) || ranges_meet(lse, lse_bytes, q, extent(qo)) ||
                 ranges_meet(lse, lse_bytes, c->pages, bytes)))
         return fail(EXQ_ERR_INVALID_ARG, "lse overlaps q, out or the cache's pages");
+    const size_t table_bytes = table_extent(rows, table_width, table_stride), lengths_bytes = 4 * (size_t)rows;
+    auto meets_read = [&](const void* x, size_t n) {   // of what every workgroup reads for itself
+        return ranges_meet(x, n, table, table_bytes) || ranges_meet(x, n, lengths, lengths_bytes);
+    };
+    if (meets_read(out, extent(oo)) || (lse && meets_read(lse, lse_bytes)))
+        return fail(EXQ_ERR_INVALID_ARG, "out or lse overlaps table or lengths");
     if (p.ws_bytes) {
         if (!workspace || !cache_aligned(workspace, 16) || workspace_bytes < p.ws_bytes)
             return fail(EXQ_ERR_INVALID_ARG, "workspace of %zu bytes: %zu 16-byte aligned ones are needed", workspace_bytes, p.ws_bytes);
         if (ranges_meet(workspace, p.ws_bytes, out, extent(oo)) || ranges_meet(workspace, p.ws_bytes, q, extent(qo)) ||
-            ranges_meet(workspace, p.ws_bytes, c->pages, bytes) || (lse && ranges_meet(workspace, p.ws_bytes, lse, lse_bytes)))
-            return fail(EXQ_ERR_INVALID_ARG, "workspace overlaps q, out, lse or the cache's pages");
+            ranges_meet(workspace, p.ws_bytes, c->pages, bytes) || (lse && ranges_meet(workspace, p.ws_bytes, lse, lse_bytes)) ||
+            meets_read(workspace, p.ws_bytes))
+            return fail(EXQ_ERR_INVALID_ARG, "workspace overlaps q, out, lse, table, lengths or the cache's pages");
     }
     AttendArgs a;
     a.c = cache_dev(c);

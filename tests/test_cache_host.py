@@ -134,6 +134,18 @@ def test_attend_of_no_rows_with_an_empty_table(cache):
     expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_attend, cache, *attend_args(rows=0, width=-1))
 
 
+@pytest.mark.parametrize("over", [dict(table=K), dict(table=V + 64), dict(table=K - 4), dict(seqs=K + 128), dict(pos=V), dict(pos=K - 16),
+                                  dict(table=K - 4 * 100, trows=2, tstride=100)], ids=str)
+def test_read_rejects_outputs_over_its_own_indices(cache, over):
+    expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_cache_read, cache, *rows_args(**over))
+
+
+@pytest.mark.parametrize("over", [dict(table=FAKE), dict(table=FAKE - 44), dict(seqs=FAKE + SIZE - 4), dict(pos=FAKE - 4),
+                                  dict(table=FAKE - 4 * 100, trows=2, tstride=100)], ids=str)
+def test_append_rejects_indices_in_the_pages(cache, over):
+    expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_cache_append, cache, *rows_args(**over))
+
+
 Q, O, L, W = FAKE + 2 * SIZE, FAKE + 4 * SIZE, FAKE + 6 * SIZE, 1 << 40
 
 
@@ -156,6 +168,14 @@ BAD_ATTEND = [dict(q=0), dict(q=Q + 4), dict(qs=(508, 64)), dict(qs=(512, -8)), 
 @pytest.mark.parametrize("bad", BAD_ATTEND, ids=str)
 def test_attend_rejects(cache, bad):
     expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_attend, cache, *attend_args(**bad))
+
+
+@pytest.mark.parametrize("over", [
+    dict(table=O), dict(table=O - 4796), dict(table=L), dict(table=W + 64), dict(table=O - 8000, tstride=2000), dict(lengths=O + 3064),
+    dict(lengths=O - 8), dict(lengths=L + 4), dict(lengths=W), dict(lengths=L - 8)], ids=str)
+def test_attend_rejects_outputs_and_a_workspace_over_its_table_or_lengths(cache, over):
+    """Workgroups of one launch read the lengths and the table while others write."""
+    expect(exq.EXQ_ERR_INVALID_ARG, exq.exq_attend, cache, *attend_args(**over))
 
 
 def test_attend_rejects_null_cache_and_too_many_rows(cache):
