@@ -216,6 +216,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double scale = PyFloat_AsDouble(a[8]);
         const long window = PyLong_AsLong(a[9]);
         if (PyErr_Occurred()) return nullptr;
+        const int want = PyObject_IsTrue(a[11]);
+        if (want < 0) return nullptr;
         if (window > INT32_MAX || window < INT32_MIN) return refuse("window=%ld", window);
         Rows q, out;
         Table t;
@@ -247,7 +249,6 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             Py_XDECREF(out_o);
             return nullptr;
         }
-        const bool want = PyObject_IsTrue(a[11]) == 1;
         PyObject* lse_o = nullptr;
         float* lse = nullptr;
         if (a[12] != Py_None || want) {

@@ -270,6 +270,16 @@ def test_tensor_calls_refuse_before_the_library(cache):
         calls.attend(*head, q, t, n, "scale", 0, None, False, None, None, None)
 
 
+def test_a_return_lse_without_a_truth_value_is_the_callers_error(cache):
+    """Its error reaches the caller before anything is looked at or launched."""
+    torch = pytest.importorskip("torch")
+    calls = exq._tensor_calls()
+    q = torch.zeros((3, 8, 64), dtype=torch.float16)
+    t = torch.zeros((3, 2), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        calls.attend(cache, 4, 64, 0, 0, q, t, t[:, 0], 0.125, 0, None, np.zeros(2), None, None, None)
+
+
 def expect_call(status, fn, *args):
     with pytest.raises(exq.ExqError) as ei:
         fn(*args)
