@@ -35,7 +35,12 @@ class ExqError(RuntimeError):
 def _load():
     if not os.path.exists(LIB_PATH):
         from . import build as _b
-        _b.build()
+        try:
+            _b.build()
+        except RuntimeError:
+            if not os.path.exists(LIB_PATH):
+                raise
+            # only the extension module failed: KVCache, which needs it, tries again and says why
     # PyTorch ships its own HIP runtime.  Importing it first makes libexq bind
     # to that already-loaded runtime instead of loading a second copy from
     # the ROCm install, so device pointers and streams from torch and from

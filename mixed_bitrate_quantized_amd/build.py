@@ -55,7 +55,9 @@ def _torch_flags():
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source (always, all at once) and link libexq.so and _exq_torch.so next to this file."""
+    """Compile every source (always, all at once) and link libexq.so and _exq_torch.so next to this file.
+
+    The library needs neither PyTorch nor Python's headers: if the extension fails, it is linked before the error is raised."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = []
     for src in HOST_SOURCES:
@@ -73,20 +75,26 @@ def build(verbose: bool = False) -> str:
                      ["-c", os.path.join(CSRC, TORCH_SOURCE), "-o", torch_obj]))
     procs = [(cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
              for _, cmd in jobs]
-    failed = None
-    for cmd, p in procs:
+    failed = {}   # by object: the command
+    for (obj, cmd), (_, p) in zip(jobs, procs):
         out = "\n".join(l for l in p.communicate()[0].splitlines() if "not a recognized feature" not in l)
         if p.returncode != 0:
             sys.stderr.write(out + "\n")
-            failed = failed or cmd
+            failed[obj] = cmd
         elif verbose and out.strip():
             print(out)
-    if failed:
-        raise RuntimeError("build step failed: " + " ".join(failed))
+
+    def check(objs):
+        for obj in objs:
+            if obj in failed:
+                raise RuntimeError("build step failed: " + " ".join(failed[obj]))
+
+    check(lib_objs)
     tmp = LIB + ".tmp%d" % os.getpid()
     _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + lib_objs + ["-lgomp"])
     os.replace(tmp, LIB)
     if torch_flags:
+        check([torch_obj])
         tmp = TORCH_LIB + ".tmp%d" % os.getpid()
         _run(["g++", "-shared", "-fPIC", "-o", tmp, torch_obj, "-L" + PKG, "-l:" + os.path.basename(LIB),
               "-Wl,-rpath,$ORIGIN"] + torch_flags[1])
