@@ -280,6 +280,16 @@ def test_a_return_lse_without_a_truth_value_is_the_callers_error(cache):
         calls.attend(cache, 4, 64, 0, 0, q, t, t[:, 0], 0.125, 0, None, np.zeros(2), None, None, None)
 
 
+def test_a_stream_of_another_device_is_refused():
+    """A call that names a stream runs on it or not at all."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream, device = 64, torch.device("cuda", 1)
+
+    expect(exq.EXQ_ERR_INVALID_ARG, exq._on, Stream(), torch.device("cuda", 0))
+
+
 def expect_call(status, fn, *args):
     with pytest.raises(exq.ExqError) as ei:
         fn(*args)
