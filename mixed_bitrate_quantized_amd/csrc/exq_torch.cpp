@@ -8,6 +8,7 @@
 
 #include <ATen/ATen.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 #include <cstdarg>
 #include <cstdio>
@@ -40,10 +41,8 @@ PyObject* refuse(const char* fmt, ...) {
     return raise(EXQ_ERR_INVALID_ARG, "argument check", text);
 }
 
-PyObject* status_or(exq_status st, const char* what, PyObject* value) {
-    if (st == EXQ_OK) return value;
-    Py_XDECREF(value);
-    return raise(st, what, exq_last_error());
+PyObject* status_or(exq_status st, const char* what, THPObjectPtr value) {
+    return st == EXQ_OK ? value.release() : raise(st, what, exq_last_error());
 }
 
 // The arguments every call starts with: what KVCache keeps, and the stream.
@@ -164,7 +163,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return nullptr;
         return status_or(exq_cache_append(c.cache, k.p, k.row, k.head, v.p, v.row, v.head, (int)rows, t.p, t.rows, t.width,
                                           t.stride, seqs, positions, c.stream),
-                         "exq_cache_append", Py_NewRef(Py_None));
+                         "exq_cache_append", THPObjectPtr(Py_NewRef(Py_None)));
     });
 }
 
@@ -182,24 +181,17 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!few_enough(rows) || !table_operand(a[5], c, t) || !index_operand("seqs", a[6], c, rows, seqs) ||
             !index_operand("positions", a[7], c, rows, positions))
             return nullptr;
-        PyObject* outs = PyTuple_New(2);
-        if (!outs) return nullptr;
+        THPObjectPtr out[2];
         Rows r[2];
         for (int i = 0; i < 2; ++i) {
-            PyObject* o = a[8 + i] == Py_None ? THPVariable_Wrap(empty(c, {rows, c.kv_heads, c.dim}, at::kHalf)) : Py_NewRef(a[8 + i]);
-            if (!o) {
-                Py_DECREF(outs);
-                return nullptr;
-            }
-            PyTuple_SET_ITEM(outs, i, o);
-            if (!rows_operand(i ? "v_out" : "k_out", o, c, rows, c.kv_heads, r[i])) {
-                Py_DECREF(outs);
-                return nullptr;
-            }
+            out[i] = a[8 + i] == Py_None ? THPVariable_Wrap(empty(c, {rows, c.kv_heads, c.dim}, at::kHalf)) : Py_NewRef(a[8 + i]);
+            if (!out[i] || !rows_operand(i ? "v_out" : "k_out", out[i], c, rows, c.kv_heads, r[i])) return nullptr;
         }
+        THPObjectPtr outs(PyTuple_Pack(2, out[0].get(), out[1].get()));
+        if (!outs) return nullptr;
         return status_or(exq_cache_read(c.cache, r[0].p, r[0].row, r[0].head, r[1].p, r[1].row, r[1].head, (int)rows, t.p, t.rows,
                                         t.width, t.stride, seqs, positions, c.stream),
-                         "exq_cache_read", outs);
+                         "exq_cache_read", std::move(outs));
     });
 }
 
@@ -244,33 +236,23 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             ws = w->data_ptr();
             ws_bytes = w->nbytes();
         }
-        PyObject* out_o = a[10] == Py_None ? THPVariable_Wrap(empty(c, {rows, heads, c.dim}, at::kHalf)) : Py_NewRef(a[10]);
-        if (!out_o || !rows_operand("out", out_o, c, rows, heads, out)) {
-            Py_XDECREF(out_o);
-            return nullptr;
-        }
-        PyObject* lse_o = nullptr;
+        THPObjectPtr out_o(a[10] == Py_None ? THPVariable_Wrap(empty(c, {rows, heads, c.dim}, at::kHalf)) : Py_NewRef(a[10]));
+        if (!out_o || !rows_operand("out", out_o, c, rows, heads, out)) return nullptr;
+        THPObjectPtr lse_o;
         float* lse = nullptr;
         if (a[12] != Py_None || want) {
             lse_o = a[12] == Py_None ? THPVariable_Wrap(empty(c, {rows, heads}, at::kFloat)) : Py_NewRef(a[12]);
             const at::Tensor* l = lse_o ? tensor("lse", lse_o) : nullptr;
-            if (l && !(here(*l, c, at::kFloat) && l->dim() == 2 && l->size(0) == rows && l->size(1) == heads && l->is_contiguous())) {
-                refuse("lse must be contiguous fp32 [%lld][%lld] on cuda:%d", (long long)rows, (long long)heads, c.index);
-                l = nullptr;
-            }
-            if (!l) {
-                Py_XDECREF(lse_o);
-                Py_DECREF(out_o);
-                return nullptr;
-            }
+            if (!l) return nullptr;
+            if (!(here(*l, c, at::kFloat) && l->dim() == 2 && l->size(0) == rows && l->size(1) == heads && l->is_contiguous()))
+                return refuse("lse must be contiguous fp32 [%lld][%lld] on cuda:%d", (long long)rows, (long long)heads, c.index);
             lse = static_cast<float*>(l->data_ptr());
         }
+        THPObjectPtr value(want ? PyTuple_Pack(2, out_o.get(), lse_o.get()) : Py_NewRef(out_o.get()));
+        if (!value) return nullptr;
         const exq_status st = exq_attend(c.cache, q.p, q.row, q.head, (int)rows, (int)heads, t.p, t.width, t.stride, lengths,
                                          (float)scale, (int)window, out.p, out.row, out.head, lse, ws, ws_bytes, c.stream);
-        PyObject* value = want ? PyTuple_Pack(2, out_o, lse_o) : Py_NewRef(out_o);
-        Py_DECREF(out_o);
-        Py_XDECREF(lse_o);
-        return status_or(st, "exq_attend", value);
+        return status_or(st, "exq_attend", std::move(value));
     });
 }
 

@@ -705,3 +705,39 @@ def test_binding_checks_tensors(exq):
     c.cache.close()
     with pytest.raises(exq.ExqError):
         c.cache.attend(q, c.dtable, n)
+
+
+class RoomFor:
+    """GPU memory that has room for so many bytes more, by the allocator's own limit."""
+
+    def __init__(self, nbytes):
+        self.nbytes = nbytes
+
+    def __enter__(self):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        total = torch.cuda.get_device_properties(0).total_memory
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + self.nbytes) / total)
+
+    def __exit__(self, *_):
+        torch.cuda.set_per_process_memory_fraction(1.0)
+
+
+def calls_without_room(exq):
+    """(what, room, call): a read and an attend whose first output of 1 GiB fits while the second does not."""
+    cache = exq.KVCache(1, 16, 8, 64, 4, 4)
+    rows = 1 << 20
+    out = rows * 8 * 64 * 2
+    table, zeros = i32([[0]]), i32(np.zeros(rows))
+    q = torch.zeros((1, 8, 64), dtype=torch.float16, device="cuda").expand(rows, 8, 64)
+    return [("read", 1.5 * out, lambda: cache.read(table, zeros, zeros)),
+            ("attend", out + out // 64, lambda: cache.attend(q, table.expand(rows, 1), zeros, return_lse=True))]
+
+
+def test_calls_that_run_out_of_memory_keep_nothing(exq):
+    for what, room, call in calls_without_room(exq):
+        before = torch.cuda.memory_allocated()
+        note("out of memory: %s" % what)
+        with RoomFor(room), pytest.raises(RuntimeError):
+            call()
+        assert torch.cuda.memory_allocated() <= before, what   # (less: what earlier tests left to the garbage collector)
