@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
@@ -129,12 +130,13 @@ at::Tensor empty(const Call& c, at::IntArrayRef shape, at::ScalarType type) {
     return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, (c10::DeviceIndex)c.index)));
 }
 
-// C++ exceptions (of PyTorch: out of memory, a tensor without storage) become Python's.
+// C++ exceptions (of PyTorch: out of memory, a tensor without storage) become
+// the Python exceptions that PyTorch raises for them.
 template <class F> PyObject* guarded(F&& f) {
     try {
         return f();
-    } catch (const std::exception& e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        if (!PyErr_Occurred()) torch::translate_exception_to_python(std::current_exception());
         return nullptr;
     }
 }

@@ -741,3 +741,11 @@ def test_calls_that_run_out_of_memory_keep_nothing(exq):
         with RoomFor(room), pytest.raises(RuntimeError):
             call()
         assert torch.cuda.memory_allocated() <= before, what   # (less: what earlier tests left to the garbage collector)
+
+
+def test_running_out_of_memory_is_pytorchs_own_error(exq):
+    """As from any other allocation: a program that frees something and tries again catches that type."""
+    for what, room, call in calls_without_room(exq):
+        note("out of memory: %s" % what)
+        with RoomFor(room), pytest.raises(torch.OutOfMemoryError):
+            call()
