@@ -351,6 +351,20 @@ def _on(stream, device):
     return scope
 
 
+def _call_on(stream, device, call, *args):
+    """call(*args) under `stream` and `device`.  The tensors among args may belong to another stream: they stay allocated until
+    the named one is through with the call, also if the caller drops them before.  (Not for the handle of a stream that is not
+    PyTorch's: its owner may destroy it before the tensors are dropped, and PyTorch would still wait for it then.)"""
+    import torch
+    with _on(stream, device):
+        result = call(*args)
+        if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
+            for x in args:
+                if isinstance(x, torch.Tensor) and x.device == device:
+                    x.record_stream(stream)
+    return result
+
+
 class Layer:
     """A packed layer resident on the GPU: owns its torch buffers and the handle."""
 
@@ -455,7 +469,8 @@ class KVCache:
     names each sequence's pages; position p of sequence s lies in page table[s][p // page_size].  Every call runs on
     `stream` (default: the current stream of the cache's device) and may be captured; all tensors are on that device.  Calls
     on different streams run side by side: order a read or attend after the append that it needs, and drop the cache after
-    the last of them.
+    the last of them.  A call that names a torch.cuda.Stream keeps its tensors' memory until that stream is through
+    with them (with another stream's handle the caller keeps them), and what it allocates belongs to that stream.
     """
 
     def __init__(self, n_pages: int, page_size: int, kv_heads: int, head_dim: int, k_bits: int = 4, v_bits: int = 4,
@@ -486,8 +501,7 @@ class KVCache:
         """Store rows k, v (fp16 [rows][kv_heads][head_dim]) at positions[r] of sequence seqs[r] (int32 [rows]; < 0: skipped)."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            with _on(stream, self.device):
-                return self.append(k, v, table, seqs, positions)
+            return _call_on(stream, self.device, self.append, k, v, table, seqs, positions)
         self._calls.append(self.handle, self.kv_heads, self.head_dim, index, C._cuda_getCurrentRawStream(index), k, v, table,
                            seqs, positions)
 
@@ -497,8 +511,7 @@ class KVCache:
         Rows with seqs[r] < 0 are left as they were in k_out and v_out (in tensors allocated here: unspecified)."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            with _on(stream, self.device):
-                return self.read(table, seqs, positions, k_out, v_out)
+            return _call_on(stream, self.device, self.read, table, seqs, positions, k_out, v_out)
         return self._calls.read(self.handle, self.kv_heads, self.head_dim, index, C._cuda_getCurrentRawStream(index), table,
                                 seqs, positions, k_out, v_out)
 
@@ -520,8 +533,7 @@ class KVCache:
         one that belongs to the graph."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            with _on(stream, self.device):
-                return self.attend(q, table, lengths, scale, window, out, return_lse, lse, workspace)
+            return _call_on(stream, self.device, self.attend, q, table, lengths, scale, window, out, return_lse, lse, workspace)
         raw = C._cuda_getCurrentRawStream(index)
         capturing = C._cuda_isCurrentStreamCapturing()
         if scale is None:

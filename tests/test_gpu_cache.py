@@ -749,3 +749,37 @@ def test_running_out_of_memory_is_pytorchs_own_error(exq):
         note("out of memory: %s" % what)
         with RoomFor(room), pytest.raises(torch.OutOfMemoryError):
             call()
+
+
+@pytest.mark.parametrize("call", ["append", "read", "attend"])
+def test_tensors_dropped_after_a_call_on_another_stream_stay_until_it_is_through(exq, call):
+    """Temporaries handed to a call that names a stream: their memory is not given out again while that stream has the call
+    still before it."""
+    c = Case(exq, 40, [2000, 700], 64, 2, 64, (4, 4))
+    side = torch.cuda.Stream()
+    half = lambda *shape: torch.ones(shape, dtype=torch.float16, device="cuda")
+    places = lambda: [c.dtable.clone(), i32(np.zeros(300)), i32(np.arange(300))]
+    need = exq.exq_attend_workspace_bytes(c.cache.handle, 2, 4, c.dtable.shape[1])
+    assert need > 0
+    if call == "append":
+        args = [half(300, 2, 64), half(300, 2, 64)] + places()
+        run = lambda x: c.cache.append(*x, stream=side)
+    elif call == "read":
+        args = places() + [half(300, 2, 64), half(300, 2, 64)]
+        run = lambda x: c.cache.read(*x, stream=side)
+    else:
+        args = [half(2, 4, 64), c.dtable.clone(), i32(c.lengths), half(2, 4, 64), torch.ones((2, 4), device="cuda"),
+                c.cache.workspace(need)]
+        run = lambda x: c.cache.attend(*x[:3], out=x[3], lse=x[4], workspace=x[5], stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    note("temporaries on another stream: %s" % call)
+    run(args)
+    before = {x.data_ptr() for x in args}
+    kinds = [(x.shape, x.dtype) for x in args]
+    del args
+    after = [torch.empty(shape, dtype=dtype, device="cuda").data_ptr() for shape, dtype in kinds]
+    waiting = not side.query()
+    torch.cuda.synchronize()
+    assert not (waiting and before & set(after))
