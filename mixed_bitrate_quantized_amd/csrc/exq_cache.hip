@@ -749,7 +749,9 @@ __device__ __forceinline__ f2 get(const float* p) {
 // Whether this workgroup is the last of `n` to arrive at a counter, which then
 // reads zero again.  What the workgroups put before is there for the last.
 __device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n, bool* flag) {
-    // each thread's stores have completed (a workgroup barrier does not wait for them), then one count
+    // each thread's stores have completed (a workgroup barrier does not wait for them), then one count.  To the compiler
+    // the wait touches no memory: the empty clobber in front of it keeps the stores there.
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((0 & 15) | ((0 >> 4) << 14) | (7 << 4) | (15 << 8));   // vmcnt(0)
     __syncthreads();
     if (threadIdx.x == 0) {

@@ -1,5 +1,7 @@
 """The build on the CPU: what the C library needs, and what only the extension module on PyTorch tensors does."""
 import os
+import re
+import subprocess
 
 import pytest
 
@@ -59,3 +61,27 @@ def test_a_library_that_does_not_compile_ends_the_build(small, monkeypatch):
     with pytest.raises(RuntimeError, match="broken_host.cpp"):
         build.build()
     assert not os.path.exists(build.LIB)
+
+
+def test_parts_are_stored_and_waited_for_before_they_are_counted(tmp_path):
+    """In every attention kernel as compiled: the stores of a part, the wait for them, the barrier, the one count."""
+    listing = str(tmp_path / "cache.s")
+    cmd = [build.hipcc()] + build.HIPCC_FLAGS + ["-S", "--cuda-device-only", "-o", listing, os.path.join(build.CSRC, "exq_cache.hip")]
+    subprocess.run(cmd, check=True, capture_output=True)
+    kernels, name = {}, None
+    with open(listing) as f:
+        for line in f:
+            label = re.match(r"(\w*attend_kernel\w*):", line)
+            if label:
+                name = label.group(1)
+            if line.startswith(".Lfunc_end"):
+                name = None
+            if name:
+                line = line.strip()
+                for letter, pattern in (("S", r"global_store\w* .*\bsc1\b"), ("W", r"s_waitcnt.*\bvmcnt\(0\)"), ("B", "s_barrier"),
+                                        ("C", "global_atomic_add")):
+                    if re.match(pattern, line):
+                        kernels[name] = kernels.get(name, "") + letter
+    assert len(kernels) >= 20
+    for name, order in kernels.items():
+        assert order.count("C") == 1 and re.search("S+W+BC", order), (name, order)
