@@ -783,3 +783,122 @@ def test_tensors_dropped_after_a_call_on_another_stream_stay_until_it_is_through
     waiting = not side.query()
     torch.cuda.synchronize()
     assert not (waiting and before & set(after))
+
+
+# ------------------------------------------------- long chunks, two tiles of heads, raw stream handles
+
+@pytest.mark.parametrize("bits", [(4, 4), (16, 16)], ids=str)
+def test_whole_rows_of_many_steps(exq, bits):
+    """More than 256 rows are not split: a wave takes 157 steps of the longest one, three looks at the page table.  A page
+    number that is none makes only the rows NaN that read it, past the second look too."""
+    rows, lengths = 257, {0: 20000, 5: 8193, 100: 8000, 256: 16500}
+    c = Case(exq, 41, [20000], 64, 1, 64, bits, spare=0)
+    n = np.full(rows, -1)
+    n[list(lengths)] = list(lengths.values())
+    c.k, c.v = c.k * rows, c.v * rows
+    q = values(c.rng, rows, 2, 64)
+    note("whole rows of many steps bits=%s" % (bits,))
+    out, lse = c.cache.attend(to_dev(q), c.dtable.expand(rows, -1), i32(n), return_lse=True)
+    c.check(out, lse, q, 0.125, lengths=list(n))
+    for bad in (8192 // 64, 16384 // 64 + 1, 19999 // 64):
+        t = c.table.copy()
+        t[0, bad] = c.cache.n_pages
+        out, lse = c.cache.attend(to_dev(q), i32(t).expand(rows, -1), i32(n), return_lse=True)
+        hit = [r for r, x in lengths.items() if x > 64 * bad]
+        assert hit and torch.all(torch.isnan(out[hit])) and torch.all(torch.isnan(lse[hit]))
+        c.check(out, lse, q, 0.125, lengths=[-1 if r in hit else x for r, x in enumerate(n)])
+
+
+@pytest.mark.parametrize("bits,unit", [((8, 8), 256), ((16, 16), 128)], ids=str)
+def test_chunks_of_more_steps_than_one_look_at_the_page_table(exq, bits, unit):
+    """One row so long that each of its 32 chunks has 66 units.  Seven pages over and over; all but a few places show the
+    five whose scores are near 0, those few, in the last two units of a chunk among others, the two whose scores are 16."""
+    page, dim = 48, 128 if bits[0] == 16 else 64
+    c = Case(exq, 42, [7 * page], page, 1, dim, bits, spare=0)
+    k = c.rng.standard_normal((7 * page, 1, dim)).astype(np.float16) * np.float16(0.05)
+    k[5 * page:] = 1
+    v = values(c.rng, 7 * page, 1, dim, spread=0.5)
+    ref.append(c.geo, c.pages, k, v, c.table, [0] * len(k), range(len(k)))
+    c.cache.pages.copy_(to_dev(c.pages).view_as(c.cache.pages))
+    k, v = ref.held(k, bits[0]).reshape(7, page, 1, dim), ref.held(v, bits[1]).reshape(7, page, 1, dim)
+    n = 32 * 66 * unit - 37
+    order = np.arange(-(-n // page)) % 5
+    chunk = 66 * unit
+    special = [3 * chunk + 64 * unit + 60, 20 * chunk + 65 * unit + 50, 31 * chunk + 65 * unit + 10, 9 * chunk + 100]
+    q = np.ones((1, 2, dim), dtype=np.float16)
+    q[0, 1, ::2] = 0.5
+    note("long chunks bits=%s" % (bits,))
+    for at in [special] + [[x] for x in special]:
+        here = order.copy()
+        here[[x // page for x in at]] = [5 + i % 2 for i in range(len(at))]
+        one = Case.__new__(Case)
+        one.k, one.v = [k[here].reshape(-1, 1, dim)], [v[here].reshape(-1, 1, dim)]
+        out, lse = c.cache.attend(to_dev(q), i32(c.table[:, here]), i32([n]), scale=16 / dim, return_lse=True)
+        one.check(out, lse, q, 16 / dim, lengths=[n], what="at %s" % at)
+
+
+def test_two_tiles_of_heads_through_a_shared_workspace(exq):
+    """17 to 32 query heads to a key-value head: two segments, each with parts of its own, between calls of one."""
+    c = Case(exq, 43, [2500, 700], 64, 1, 64, (8, 8), spread=0.5, garbage=False, spare=300)
+    ws = c.cache.workspace(exq.exq_attend_workspace_bytes(c.cache.handle, 2, 32, c.dtable.shape[1]))
+    for heads in (32, 5, 17, 32):
+        q = values(c.rng, 2, heads, 64, spread=0.5)
+        for lens in ([2500, 700], [2100, -1], [0, 650]):
+            note("two tiles of heads, heads=%d lengths=%s" % (heads, lens))
+            out, lse = c.cache.attend(to_dev(q), c.dtable, i32(lens), return_lse=True, workspace=ws)
+            one = Case.__new__(Case)
+            one.k, one.v = [x[:max(n, 0)] for x, n in zip(c.k, lens)], [x[:max(n, 0)] for x, n in zip(c.v, lens)]
+            one.check(out, lse, q, 0.125, lengths=lens, what="%d heads %s" % (heads, lens))
+            assert torch.all(ws[:exq.ATTEND_COUNTER_BYTES] == 0)
+
+
+def test_a_stream_may_be_a_raw_handle(exq):
+    """0, the default stream's, and another stream's, for all three calls."""
+    c = Case(exq, 44, [900], 64, 2, 64, (8, 4))
+    q, n = to_dev(values(c.rng, 1, 4, 64)), i32([900])
+    seqs, pos = i32(np.zeros(40)), i32(np.arange(40) + 3)
+    want = c.cache.attend(q, c.dtable, n)
+    k, v = c.cache.read(c.dtable, seqs, pos)
+    other = torch.cuda.Stream()
+    for handle in (0, other.cuda_stream):
+        torch.cuda.synchronize()
+        note("raw stream handle")
+        c.cache.append(k, v, c.dtable, seqs, pos, stream=handle)
+        got = c.cache.read(c.dtable, seqs, pos, stream=handle)
+        out = c.cache.attend(q, c.dtable, n, stream=handle)
+        torch.cuda.synchronize()
+        # (what was read back is written and read back again: a value's code and its group's scale may move by a rounding)
+        assert torch.equal(out, c.cache.attend(q, c.dtable, n))
+        assert all(torch.equal(a, b) for a, b in zip(got, c.cache.read(c.dtable, seqs, pos)))
+    assert want.shape == out.shape
+
+
+def test_a_captured_step_may_name_its_stream(exq):
+    """append, read and attend captured with the capturing stream named, temporaries among their arguments; two graphs in
+    turn, eager calls between."""
+    c = Case(exq, 45, [700, 1500], 64, 2, 64, (4, 8), spare=10)
+    q, k, v = (torch.zeros((2, h, 64), dtype=torch.float16, device="cuda") for h in (6, 2, 2))
+    seqs, pos, n = i32([0, 1]), i32([700, 1500]), i32([701, 1501])
+    assert exq.exq_attend_workspace_bytes(c.cache.handle, 2, 6, c.dtable.shape[1]) > 0
+
+    def step(stream=None):
+        c.cache.append(k.clone(), v.clone(), c.dtable, seqs, pos, stream=stream)
+        return c.cache.read(c.dtable, seqs, pos, stream=stream) + c.cache.attend(q.clone(), c.dtable, n, return_lse=True, stream=stream)
+
+    step()
+    torch.cuda.synchronize()
+    note("capture with a named stream")
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, step(torch.cuda.current_stream())))
+    for rep in range(6):
+        g, got = graphs[rep % 2]
+        for x, h in ((q, 6), (k, 2), (v, 2)):
+            x.copy_(to_dev(values(c.rng, 2, h, 64)))
+        g.replay()
+        torch.cuda.synchronize()
+        want = step()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), rep
+        torch.cuda.synchronize()
