@@ -455,7 +455,14 @@ size_t exq_attend_workspace_bytes(exq_cache_t cache, int rows, int q_heads, int 
  *                      + 2^-32 sum_j |V_hat_j| + 2^-11 |out_ref| + 2^-24
  *   |lse - lse_ref| <= (D + 8) 2^-24 A + n 2^-27 + 2^-19 + 2^-22 |lse_ref|
  * (weights rounded to fp16, sums of n and of D = head_dim terms in fp32, weights
- * below 2^-32 of the largest lost, the output's rounding).
+ * below 2^-32 of the largest lost, the output's rounding).  An infinite value
+ * makes out infinite or NaN; a score beyond fp32 (|S_j| log2(e) of 3e38 or more) may
+ * make it NaN.
+ * Speed: the shape of a launch is chosen from the sizes, not from the lengths.
+ * Hand over a table about as wide as the longest row (a slice of a wider one:
+ * table_stride stays), and rows much longer than the others in a call of their own
+ * where there are more than 256 rows or 2048 of (row, kv head, 16 query heads):
+ * such calls are not split along the length.
  * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED, HIP. */
 exq_status exq_attend(exq_cache_t cache, const void* q, int64_t q_row_stride, int64_t q_head_stride, int rows,
                       int q_heads, const int32_t* table, int table_width, int64_t table_stride,

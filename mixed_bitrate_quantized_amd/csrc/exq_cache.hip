@@ -129,7 +129,10 @@ __device__ __forceinline__ RowPlace row_place(const CacheDev& c, const TableDev&
 // laid out by channel and have to change lanes: through LDS where the 16 rows
 // are a tile, by bytes where they are not.  Blocks of rows start where the
 // first row's tile starts, so that one sequence's rows (a prompt) make tiles
-// wherever the prompt starts.
+// wherever the prompt starts.  A second sequence's rows make tiles only if they
+// happen to be in step with them: 8 prompts of 1001 tokens and 8 heads in one call
+// at 4 bits are appended in 16.3 us and read in 22, one of 8008 in 12 and 9 (in 16
+// bits 22.6 and 24, 10.6 and 12).
 constexpr int kRowsThreads = 256;
 
 // Orders a wave's own LDS writes before its reads, and its reads before its
@@ -526,9 +529,17 @@ __global__ __launch_bounds__(kRowsThreads) void cache_read_kernel(CacheDev c, Ta
 // ------------------------------------------------------------------ attend
 
 constexpr int kCusLog2 = 8, kCus = 1 << kCusLog2;
-constexpr int kAttendMaxSegments = 2048;   // more are not split: they load the card evenly enough
-constexpr int kAttendMaxRows = 256;        // likewise
-constexpr int kAttendMaxParts = 32;        // parts of a segment
+// Calls of more segments or rows are not split.  Equal rows load the card
+// evenly as they are (300 rows of 500 tokens and 8 heads at 4 bits 42 us), but
+// a long one among them runs alone in a workgroup a head: with one of 131072
+// tokens the 300 rows take 1106 us, where 255 with the same one, split, take
+// 70; 128 rows of 32 heads with one of 32768 take 294.
+constexpr int kAttendMaxSegments = 2048;
+constexpr int kAttendMaxRows = 256;
+// Parts of a segment: 8 segments have one for each CU.  Fewer leave CUs idle:
+// 131072 tokens at 4 bits take 34 us with 8 key-value heads, and 32, 30 and 28
+// with 4, 2 and 1.
+constexpr int kAttendMaxParts = 32;
 constexpr int kAttendMaxWgs = kAttendMaxSegments + 2 * kCus;   // of a launch that splits
 constexpr int kJoinBatch = 16;             // parts whose loads a thread has in flight at once
 
@@ -630,7 +641,8 @@ __device__ __forceinline__ int wave_max(int v) {
 
 // n / d of numbers below 2^12, d > 0: half of one to spare makes it exact.  A
 // few instructions, where the integer division has forty: code that runs once
-// costs its fetch, about 0.1 us for every 64 bytes.
+// waits for its fetch (these quotients in place of divisions: 1 x 8192 tokens
+// 12.75 -> 12.65 us, 1 x 131072 34.7 -> 34.4).
 __device__ __forceinline__ int small_quotient(int n, int d) {
     return (int)(((float)n + 0.5f) * __builtin_amdgcn_rcpf((float)d));
 }
@@ -961,6 +973,11 @@ __device__ __forceinline__ void clear_values(RawValues<D, VB>& r, int t0, int lo
 // transposed (rows: tokens, columns: heads), so the accumulator registers of
 // two tiles are, after the exponential, the lane's operand of the second
 // product as they stand: lane (q, head) holds tokens 4 q .. 4 q + 3 of each.
+// That operand is fp16, as the values are: a weight is off by 2^-11 of itself at
+// most, its sum l adds it unrounded.  Of the outputs' norm the error against 64
+// bits is 2.4e-4 to 2.9e-4, with weights of 32 bits 2.1e-4, the rounding of the
+// outputs.  Weights of 22 bits, in two operands, would take the second product
+// twice.
 template <int D, int KB, int VB> struct AttendWave {
     static constexpr int G = D / kCacheGroup;
     Nibbles nib;
@@ -1052,9 +1069,9 @@ template <int D, int KB, int VB> struct AttendWave {
 // segment to finish joins the parts of all, through the workspace.
 //
 // Bound by the cache's bytes where there are many (32 x 16384 tokens at 4 bits:
-// 605 MB in 107 us, 5.7 TB/s, with the decoding of 4-bit codes, 200 of a step's
-// 240 vector instructions, close behind; 32 x 4000 in 16 bits: 525 MB in 81 us,
-// 6.5 TB/s of a plain read's 7.0), and by the chain of length, page number, first
+// 605 MB in 107 us, 5.7 TB/s; with the codes used as they are, two instructions in
+// place of the decoding's 200 of a step's 240, 104; 32 x 4000 in 16 bits: 525 MB in
+// 81 us, 6.5 TB/s of a plain read's 7.0), and by the chain of length, page number, first
 // tile and join where there are few (100 tokens 5.5 us, 2048 in parts 9).
 template <int D, int KB, int VB, int NW>
 __global__ __launch_bounds__(64 * NW, (attend_waves_per_simd(D, KB, VB))) void attend_kernel(AttendArgs a) {
@@ -1412,7 +1429,13 @@ bool meets_indices(const void* p, size_t n, int rows, const int32_t* table, int 
 }
 
 // Tokens of all segments from which on attend_full geometries take a workgroup
-// for every place the card has for one.
+// for every place the card has for one.  Measured on rows of 16384 tokens and 8
+// heads, four workgroups a CU against one or two: head_dim 128, 8 rows 38 and 37
+// us, 12 57.6 and 50.3, 16 60.0 and 58.8, 20 90.5 and 79.2, 24 92.2 and 101.3, 28
+// 100 and 105, 32 104.7 and 107.2, 48 190 and 190; head_dim 64, 16 rows 37.7 and
+// 43.0, 24 62 and 74.7, 32 63 and 76, 48 124.6 and 124.6, 64 115 and 137.5.  So
+// the gain sets in at 3.1 million tokens of 128 channels and at 2.1 of 64 already;
+// the limit is above both, and calls between them and it do without.
 constexpr int64_t kFullTokens = (int64_t)1 << 22;
 
 // Shape of an exq_attend launch.
@@ -1433,7 +1456,13 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     const int64_t tiles = (int64_t)c->kv_heads * ((group + 15) / 16), segments = tiles * rows;
     if (segments > kMaxLaunchThreads / 256)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows of %d heads in one call", rows, q_heads);
-    const int64_t tokens = (int64_t)table_width * c->page_size;   // of the longest row
+    // Of the longest row there may be: the lengths are on the device.  The figures
+    // below are of tables about as wide as the rows.  In one for 131072 tokens the
+    // choices are those for long rows: 100 tokens take 5.4 us in place of 4.6, 2048
+    // 11.0 in place of 8.8, 4 x 4096 13.0 in place of 11.6, 16 x 900 10.9 in place of
+    // 10.1, 12 x 8192 33.8 in place of 30.0, 5 x 1999 of a window of 1023 in 8 bits
+    // 11.3 in place of 8.4.
+    const int64_t tokens = (int64_t)table_width * c->page_size;
     // Workgroups of 8 waves, one a CU, for few segments of long rows whose steps
     // are light: a segment has half as many parts to join (at 4 bits, 131072
     // tokens of 8 heads 35.4 us, with 4 waves 47.8; 4 x 16384 22.7 and 26.9; but
@@ -1448,7 +1477,7 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     // 9.1 split; 600 tokens 8.9 and 9.2), 1024 where a quarter of the card does (8
     // rows of 8 heads, 1000 tokens 11.6 whole, 12.6 split; 16 x 2000 22.1 and
     // 16.7), and 2048 where all of it does (32 x 2000 23.4 and 23.2).  Very many
-    // load the card evenly enough as they are, and every workgroup would look
+    // are not split at all (kAttendMaxSegments): every workgroup would look
     // through all rows' lengths.
     out->whole_units = (segments >= kCus ? 2048 : segments >= 64 ? 1024 : 640) / unit;
     const bool split = units > out->whole_units && rows > 0 && segments <= kAttendMaxSegments && rows <= kAttendMaxRows;
@@ -1471,8 +1500,8 @@ exq_status plan_attend(const exq_cache* c, int rows, int q_heads, int table_widt
     //   bits 30.2 us, with what they come out at 33.8; 11 x 8192 in 4 and 8 bits
     //   34.6 and 39.5; ragged rows would lose, 32 x 16384 85.8 and 77.7);
     // - four, all that fit, for very long rows at 4 bits, whose decoding waits for
-    //   loads (32 x 16384 108 us, with two 114; head_dim 64, 64 x 16384 119 and 139;
-    //   but 16 x 16384 61.4 and 60.9, and head_dim 96, 32 x 16384 108.4 and 105.8).
+    //   loads (32 x 16384 105 us, with two 107; head_dim 64, 64 x 16384 115 and 137;
+    //   but 16 x 16384 60.0 and 58.8, and head_dim 96, 32 x 16384 108.4 and 105.8).
     const bool heavy = !attend_light(c->head_dim, c->k_bits, c->v_bits);
     const bool full = attend_full(c->head_dim, c->k_bits, c->v_bits) && segments * tokens >= kFullTokens;
     // Below 64 segments one a CU is the aim already, and a few workgroups more
