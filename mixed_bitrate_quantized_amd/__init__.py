@@ -340,7 +340,7 @@ def _on(stream, device):
     """What a call runs under when it names a stream or its tensors' device is not the current one: that device and, for
     what the call allocates, that stream."""
     import torch
-    if getattr(stream, "device", device) != device:
+    if hasattr(stream, "cuda_stream") and getattr(stream, "device", device) != device:
         raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "a stream of %s for tensors on %s" % (stream.device, device))
     scope = contextlib.ExitStack()
     scope.enter_context(torch.cuda.device(device))

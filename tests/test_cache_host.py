@@ -290,6 +290,22 @@ def test_a_stream_of_another_device_is_refused():
     expect(exq.EXQ_ERR_INVALID_ARG, exq._on, Stream(), torch.device("cuda", 0))
 
 
+def test_a_stream_handle_may_be_any_integer(monkeypatch):
+    """numpy's integers have a device too, which is none of a stream's."""
+    torch = pytest.importorskip("torch")
+
+    class Reached(Exception):
+        pass
+
+    def device(_):
+        raise Reached
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for handle in (64, np.int64(64), np.uint64(64)):
+        with pytest.raises(Reached):
+            exq._on(handle, torch.device("cuda", 0))
+
+
 def expect_call(status, fn, *args):
     with pytest.raises(exq.ExqError) as ei:
         fn(*args)
