@@ -469,6 +469,168 @@ exq_status exq_attend(exq_cache_t cache, const void* q, int64_t q_row_stride, in
                       const int32_t* lengths, float scale, int window, void* out, int64_t out_row_stride,
                       int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- pages of sequences */
+
+/* Who owns which page of a key-value cache, kept on the GPU: a table (as the
+ * calls above read it), each sequence's length, and a list of free pages.  With
+ * P(n) = ceil(n / page_size) pages to n tokens, a sequence of n tokens owns the
+ * first P(n) entries of its row.  A decoding loop extends the sequences, appends
+ * the keys and values of the new rows and attends, with nothing read back.
+ *   table       device int32 [sequences][table_width], rows table_stride apart
+ *   lengths     device int32 [sequences]; a negative one marks a row that is not
+ *               in use: it is left alone and gets no rows
+ *   free_pages  device int32 [n_pages]: a stack whose first free_count[0] entries
+ *               are free pages; the others may hold anything
+ *   free_count  device int32 [1] (taken as within 0 .. n_pages)
+ *   workspace   device, exq_pages_workspace_bytes(sequences), any content
+ * No array may overlap another.  A page belongs to one sequence, or is shared by
+ * rows that never trim it.  Calls on one set of arrays are ordered by the caller.
+ * Nothing depends on timing: pages move in a stated order, so the same arrays
+ * give the same ones.  Errors: INVALID_ARG, UNSUPPORTED (a table of 2^31 entries
+ * or more), HIP. */
+size_t exq_pages_workspace_bytes(int sequences);
+
+/* Make room for counts[s] more tokens (<= 0: none) of every sequence s, in order:
+ *   - the i-th page that is missing, counted over the sequences and then along
+ *     the row, is free_pages[free_count - 1 - i]; free_count falls by their number;
+ *   - row offsets[s] + i, i < counts[s], is token lengths[s] + i of sequence s:
+ *     seqs and positions hold the two numbers, as exq_cache_append reads them; rows
+ *     behind the last one get sequence -1 and position 0;
+ *   - lengths[s] grows by counts[s].
+ * If the pages, the `rows` rows of the output or a row of the table do not
+ * suffice, the first sequence that they do not suffice for and all after it get
+ * nothing and keep their lengths.
+ *   seqs, positions   device int32 [rows], written; rows >= 0 (0: may be NULL)
+ *   offsets           device int32 [sequences + 1], written: each sequence's
+ *                     first row, and the number of rows
+ *   served            device int32 [1], written: how many sequences were served
+ *                     (all: `sequences`) */
+exq_status exq_pages_extend(int32_t* table, int sequences, int table_width, int64_t table_stride, int page_size,
+                            int32_t* lengths, const int32_t* counts, const int32_t* free_pages, int32_t* free_count,
+                            int n_pages, int32_t* seqs, int32_t* positions, int rows, int32_t* offsets, int32_t* served,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Cut every sequence s to its first keep[s] tokens (0: release it; negative, or
+ * lengths[s] or more: left as it is), for finished sequences and for drafted
+ * tokens that were not accepted.  Its pages behind P(keep[s]) go back: the i-th of
+ * F such pages, counted over the sequences and then along the row, to
+ * free_pages[free_count + F - 1 - i] (dropped where that is past n_pages, which
+ * a table whose pages came from the list never asks for), and their entries become
+ * -1; free_count grows by F.  So an extend by what a trim cut off restores the table. */
+exq_status exq_pages_trim(int32_t* table, int sequences, int table_width, int64_t table_stride, int page_size,
+                          int32_t* lengths, const int32_t* keep, int32_t* free_pages, int32_t* free_count, int n_pages,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------ rotary positions */
+
+/* Rotary positions of queries and keys, between a block's q/k linears and the
+ * cache.  For row r at position p = positions[r], every head, and the pair i <
+ * rotary_dim / 2 of channels (u, v) - channels i and i + rotary_dim / 2, or with
+ * `interleaved` 2 i and 2 i + 1:
+ *   u' = (u cos t - v sin t) factor,  v' = (u sin t + v cos t) factor,  t = p rates[i].
+ * Channels from rotary_dim on are copied.  A row with a negative position is
+ * padding: its outputs are left as they were.
+ *   q, k       device fp16 [rows][q_heads or k_heads][head_dim]; strides as for
+ *              exq_cache_append; either may have 0 heads (then NULL)
+ *   q_out, k_out   as q and k, no element twice; each may be its input itself
+ *              (same pointer and strides), else it must not overlap it.  Neither
+ *              may overlap the other, the other input, rates or positions
+ *   head_dim   a multiple of 8, 8 .. 65536;  rotary_dim   even, 2 .. head_dim
+ *   rates      device double [rotary_dim / 2], angles per token
+ *   factor     finite; multiplies the turned channels (1 but for stretched contexts)
+ *   positions  device int32 [rows]
+ * Accuracy: t in 64 bits (|p rates[i]| < 2^40), its sine and cosine and the products
+ * in fp32: |u' - u'_ref| <= 2^-11 |u'_ref| + 2^-20 |factor| (|u| + |v|) + 2^-24.  Fastest where
+ * rotary_dim is a multiple of 16.
+ * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED (rows * heads beyond a
+ * launch), HIP. */
+exq_status exq_rotate(const void* q, int64_t q_row_stride, int64_t q_head_stride, void* q_out,
+                      int64_t q_out_row_stride, int64_t q_out_head_stride, int q_heads, const void* k,
+                      int64_t k_row_stride, int64_t k_head_stride, void* k_out, int64_t k_out_row_stride,
+                      int64_t k_out_head_stride, int k_heads, int rows, int head_dim, int rotary_dim,
+                      int interleaved, const double* rates, float factor, const int32_t* positions, void* stream);
+
+/* --------------------------------------------------- low-rank adapters */
+
+/* A stack of low-rank adapters of one linear, for requests that each bring their
+ * own beside the shared weights.  The handle holds the geometry and the borrowed
+ * pointers, on the host only; any number of streams may use it at once.
+ *   count   adapters, 1 .. 8192
+ *   K, N    in and out features, multiples of 8, up to 2^20
+ *   rank    of the stack: a multiple of 8, 8 .. 256
+ *   a       device fp16 [count][rank][K], b  device fp16 [count][N][rank], 16-byte aligned
+ *   scales  device fp32 [count] or NULL (1)
+ *   ranks   device int32 [count] or NULL (rank): adapter i has ranks[i] (within 0 ..
+ *           rank); what a and b hold behind it never reaches a result, NaN included
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes above), OOM. */
+typedef struct exq_adapters* exq_adapters_t;
+exq_status exq_adapters_create(int count, int K, int N, int rank, const void* a, const void* b, const float* scales,
+                               const int32_t* ranks, exq_adapters_t* out);
+
+/* Release a handle (not the weights).  NULL is a no-op. */
+void exq_adapters_destroy(exq_adapters_t adapters);
+
+/* Bytes of workspace exq_lora_add needs for that many rows (0: none, or an
+ * argument is invalid). */
+size_t exq_lora_workspace_bytes(exq_adapters_t adapters, int rows);
+
+/* out[r] = y[r] + scales[i] * (x[r] a[i]^T) b[i]^T,  i = ids[r], for rows of any
+ * adapters in any order.
+ *   x        device fp16 [rows][K], y device fp16 [rows][N]: what exq_gemm reads and
+ *            writes; 16-byte aligned, row strides multiples of 8 elements, >= 0
+ *   ids      device int32 [rows].  Negative: no adapter, out[r] = y[r].  count or
+ *            more: out[r] is NaN
+ *   out      as y, no element twice; y itself (same pointer and stride) or apart
+ *            from it, and apart from x, ids and the handle's arrays
+ *   workspace   device, 16-byte aligned, any content; apart from all others.  Calls
+ *            that may run at the same time need one each
+ * Accuracy, with L_j = |x[r]| . |a[i][j]| the sum of magnitudes of one inner product
+ * and S = sum_j |b[n][j]| L_j:
+ *   |out - out_ref| <= 2^-11 |out_ref| + |scales[i]| S (K + rank + 64) 2^-23 + 2^-24
+ * (fp32 sums; the inner products enter the second product with 22 bits).  A row's
+ * result does not depend on the other rows' values or ids, but for its summation
+ * over K, which depends on the number of rows; deterministic.  x or y with an infinity or a NaN makes that row's
+ * results infinite or NaN.
+ * Capturable: no allocation, no wait.  rows == 0 is a no-op.  Errors: INVALID_ARG,
+ * UNSUPPORTED (rows beyond a launch), HIP. */
+exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_stride, int rows, const int32_t* ids,
+                        const void* y, int64_t y_row_stride, void* out, int64_t out_row_stride, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------ the next token */
+
+/* One token of every row of logits, from given random numbers.  With T the row's
+ * temperature, M its largest logit and w_i = e^{(l_i - M) / T}, tokens in order of
+ * falling logit, then rising index:
+ *   1. top_k > 0: the first top_k are left;
+ *   2. top_p < 1: of these the shortest run from the start whose weights reach
+ *      top_p times theirs is left, one token at least;
+ *   3. min_p > 0: those with w_i >= min_p are left, and the first one;
+ * and the token is the lowest index i whose running sum of the weights left, in
+ * order of the index, exceeds u times their sum.  T = 0: the first token.  The order of
+ * falling logit takes -0 and 0 as equal.  A logit of -infinity or NaN is never drawn.
+ * With a logit of +infinity only those are, all alike.
+ *   logits   device fp16 (bits 16) or fp32 (bits 32) [rows][vocab], rows row_stride
+ *            elements apart, aligned to their elements; vocab up to 2^21
+ *   u        device fp32 [rows], random numbers in [0, 1).  Negative: a padding row,
+ *            whose outputs are left as they were.  1 or more: as just below 1
+ *   temperatures, top_ks, top_ps, min_ps   device arrays [rows], or NULL: the value
+ *            that follows, for all rows
+ *   tokens   device int32 [rows], written
+ *   logprobs device fp32 [rows] or NULL: ln of the token's share of the weights left
+ * A row without a logit that may be drawn, or with a u, T, top_p or min_p that is
+ * NaN, or a negative T, gets token -1 and logprob NaN.
+ * Weights are computed in 64 bits and summed exactly, in units of 2^-42 (vocab of
+ * 2^21) to 2^-51 (4096 and fewer) of the largest: deterministic.  A logprob is
+ * within 2^-23 of its value relative, or 2^-30.
+ * rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, misaligned, a bad size, stride or
+ * setting, tokens or logprobs overlapping an input or each other), UNSUPPORTED
+ * (bits, vocab), HIP. */
+exq_status exq_sample(const void* logits, int bits, int rows, int vocab, int64_t row_stride, const float* u,
+                      const float* temperatures, float temperature, const int32_t* top_ks, int top_k,
+                      const float* top_ps, float top_p, const float* min_ps, float min_p, int32_t* tokens,
+                      float* logprobs, void* stream);
+
 /* ------------------------------------------------------------ diagnostic */
 
 /* A plain streaming read, the practical HBM read ceiling that the decode

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -91,7 +92,22 @@ def _load():
     lib.exq_attend_workspace_bytes.restype = u64
     lib.exq_attend.argtypes = [vp, vp, i64, i64, i32, i32, vp, i32, i64, vp, ctypes.c_float, i32, vp, i64, i64, vp, vp,
                                u64, vp]
-    for f in (lib.exq_pack, lib.exq_layer_create, lib.exq_gemm, lib.exq_gemm_noalloc, lib.exq_dequant, lib.exq_plan_create,
+    f32 = ctypes.c_float
+    pages = [vp, i32, i32, i64, i32, vp, vp, vp, vp, i32]
+    lib.exq_pages_workspace_bytes.argtypes = [i32]
+    lib.exq_pages_workspace_bytes.restype = u64
+    lib.exq_pages_extend.argtypes = pages + [vp, vp, i32, vp, vp, vp, u64, vp]
+    lib.exq_pages_trim.argtypes = pages + [vp, u64, vp]
+    lib.exq_rotate.argtypes = [vp, i64, i64, vp, i64, i64, i32] * 2 + [i32, i32, i32, i32, vp, f32, vp, vp]
+    lib.exq_adapters_create.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, ctypes.POINTER(vp)]
+    lib.exq_adapters_destroy.argtypes = [vp]
+    lib.exq_adapters_destroy.restype = None
+    lib.exq_lora_workspace_bytes.argtypes = [vp, i32]
+    lib.exq_lora_workspace_bytes.restype = u64
+    lib.exq_lora_add.argtypes = [vp, vp, i64, i32, vp, vp, i64, vp, i64, vp, u64, vp]
+    lib.exq_sample.argtypes = [vp, i32, i32, i32, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp]
+    for f in (lib.exq_pages_extend, lib.exq_pages_trim, lib.exq_rotate, lib.exq_adapters_create, lib.exq_lora_add, lib.exq_sample,
+              lib.exq_pack, lib.exq_layer_create, lib.exq_gemm, lib.exq_gemm_noalloc, lib.exq_dequant, lib.exq_plan_create,
               lib.exq_plan_run, lib.exq_stream_read, lib.exq_gemm_gated, lib.exq_group_errors,
               lib.exq_allocate_widths, lib.exq_autotune, lib.exq_set_variant, lib.exq_pack_qs,
               lib.exq_layer_create_qs, lib.exq_cache_create, lib.exq_cache_append, lib.exq_cache_read, lib.exq_attend):
@@ -108,7 +124,8 @@ EXPORTED = (
     "exq_stream_read", "exq_gemm_gated", "exq_group_errors", "exq_allocate_widths", "exq_trimmed_mean",
     "exq_autotune", "exq_set_variant", "exq_pack_qs", "exq_layer_create_qs", "exq_gemm_noalloc",
     "exq_cache_page_bytes", "exq_cache_create", "exq_cache_destroy", "exq_cache_append", "exq_cache_read",
-    "exq_attend_workspace_bytes", "exq_attend",
+    "exq_attend_workspace_bytes", "exq_attend", "exq_pages_workspace_bytes", "exq_pages_extend", "exq_pages_trim", "exq_rotate",
+    "exq_adapters_create", "exq_adapters_destroy", "exq_lora_workspace_bytes", "exq_lora_add", "exq_sample",
 )
 
 VARIANT_DEFAULT, VARIANT_DECODE16, VARIANT_DECODE64, VARIANT_PREFILL = 0, 1, 2, 3
@@ -324,10 +341,66 @@ def exq_attend(cache: int, q_ptr: int, q_strides, rows: int, q_heads: int, table
                           workspace_bytes, _stream_ptr(stream)), "exq_attend")
 
 
+def exq_pages_workspace_bytes(sequences: int) -> int:
+    return int(lib.exq_pages_workspace_bytes(sequences))
+
+
+def exq_pages_extend(table_ptr: int, sequences: int, table_width: int, table_stride: int, page_size: int, lengths_ptr: int,
+                     counts_ptr: int, free_ptr: int, free_count_ptr: int, n_pages: int, seqs_ptr: int, positions_ptr: int,
+                     rows: int, offsets_ptr: int, served_ptr: int, workspace_ptr: int, workspace_bytes: int, stream=None) -> None:
+    _check(lib.exq_pages_extend(table_ptr, sequences, table_width, table_stride, page_size, lengths_ptr, counts_ptr, free_ptr,
+                                free_count_ptr, n_pages, seqs_ptr, positions_ptr, rows, offsets_ptr, served_ptr, workspace_ptr,
+                                workspace_bytes, _stream_ptr(stream)), "exq_pages_extend")
+
+
+def exq_pages_trim(table_ptr: int, sequences: int, table_width: int, table_stride: int, page_size: int, lengths_ptr: int,
+                   keep_ptr: int, free_ptr: int, free_count_ptr: int, n_pages: int, workspace_ptr: int, workspace_bytes: int,
+                   stream=None) -> None:
+    _check(lib.exq_pages_trim(table_ptr, sequences, table_width, table_stride, page_size, lengths_ptr, keep_ptr, free_ptr,
+                              free_count_ptr, n_pages, workspace_ptr, workspace_bytes, _stream_ptr(stream)), "exq_pages_trim")
+
+
+def exq_rotate(q_ptr, q_strides, q_out_ptr, q_out_strides, q_heads: int, k_ptr, k_strides, k_out_ptr, k_out_strides,
+               k_heads: int, rows: int, head_dim: int, rotary_dim: int, interleaved: bool, rates_ptr: int, factor: float,
+               positions_ptr: int, stream=None) -> None:
+    """Strides: (row, head) in elements."""
+    _check(lib.exq_rotate(q_ptr, q_strides[0], q_strides[1], q_out_ptr, q_out_strides[0], q_out_strides[1], q_heads, k_ptr,
+                          k_strides[0], k_strides[1], k_out_ptr, k_out_strides[0], k_out_strides[1], k_heads, rows, head_dim,
+                          rotary_dim, int(interleaved), rates_ptr, factor, positions_ptr, _stream_ptr(stream)), "exq_rotate")
+
+
+def exq_adapters_create(count: int, K: int, N: int, rank: int, a_ptr: int, b_ptr: int, scales_ptr=None, ranks_ptr=None) -> int:
+    h = ctypes.c_void_p()
+    _check(lib.exq_adapters_create(count, K, N, rank, a_ptr, b_ptr, scales_ptr, ranks_ptr, ctypes.byref(h)),
+           "exq_adapters_create")
+    return h.value
+
+
+def exq_adapters_destroy(adapters: int) -> None:
+    lib.exq_adapters_destroy(adapters)
+
+
+def exq_lora_workspace_bytes(adapters: int, rows: int) -> int:
+    return int(lib.exq_lora_workspace_bytes(adapters, rows))
+
+
+def exq_lora_add(adapters: int, x_ptr: int, x_stride: int, rows: int, ids_ptr: int, y_ptr: int, y_stride: int, out_ptr: int,
+                 out_stride: int, workspace_ptr: int, workspace_bytes: int, stream=None) -> None:
+    _check(lib.exq_lora_add(adapters, x_ptr, x_stride, rows, ids_ptr, y_ptr, y_stride, out_ptr, out_stride, workspace_ptr,
+                            workspace_bytes, _stream_ptr(stream)), "exq_lora_add")
+
+
+def exq_sample(logits_ptr: int, bits: int, rows: int, vocab: int, row_stride: int, u_ptr: int, temperatures_ptr,
+               temperature: float, top_ks_ptr, top_k: int, top_ps_ptr, top_p: float, min_ps_ptr, min_p: float, tokens_ptr: int,
+               logprobs_ptr=None, stream=None) -> None:
+    _check(lib.exq_sample(logits_ptr, bits, rows, vocab, row_stride, u_ptr, temperatures_ptr, temperature, top_ks_ptr, top_k,
+                          top_ps_ptr, top_p, min_ps_ptr, min_p, tokens_ptr, logprobs_ptr, _stream_ptr(stream)), "exq_sample")
+
+
 # ------------------------------------------------------------ conveniences
 
 def _tensor_calls():
-    """The module of KVCache's calls, which checks their tensors and passes them to the library."""
+    """The module of the calls on tensors, which checks them and passes them to the library."""
     if not os.path.exists(os.path.join(_PKG, "_exq_torch.so")):
         from . import build as _b
         _b.build()
@@ -558,3 +631,194 @@ class KVCache:
             self.close()
         except Exception:
             pass
+
+
+class PagePool:
+    """The pages of a KVCache, handed out to sequences and taken back on the GPU.
+
+    Owns `table` (int32 [sequences][width], -1 where there is no page), `lengths` (int32 [sequences]), and the list of free
+    pages (`free`, `free_count`).  extend() makes room for new tokens and says where they go; trim() cuts sequences; nothing is
+    read back.  table and lengths are what KVCache's calls take.  Every call runs on `stream` (default: the current stream of
+    the pool's device) and may be captured; calls on one pool, and what reads its tensors, are ordered by the caller.
+    """
+
+    def __init__(self, n_pages: int, page_size: int, sequences: int, width: int, device="cuda"):
+        import torch
+        if not (0 < n_pages < 1 << 31 and 0 < page_size <= 65536 and 0 < sequences and 0 < width
+                and sequences * width < 1 << 31):
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "%d pages of %d tokens for %d sequences of %d pages"
+                           % (n_pages, page_size, sequences, width))
+        self.n_pages, self.page_size, self.sequences, self.width = n_pages, page_size, sequences, width
+        self.table = torch.full((sequences, width), -1, dtype=torch.int32, device=device)
+        self.lengths = torch.zeros(sequences, dtype=torch.int32, device=device)
+        self.free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = torch.full((1,), n_pages, dtype=torch.int32, device=device)
+        self.served = torch.full((1,), sequences, dtype=torch.int32, device=device)
+        self._workspace = torch.empty(exq_pages_workspace_bytes(sequences) // 4, dtype=torch.int32, device=device)
+        self.device, self._index = self.table.device, self.table.device.index
+        self._C, self._calls = torch._C, _tensor_calls()
+        if self.table.is_cuda:   # the first call may come on any stream
+            torch.cuda.current_stream(self.device).synchronize()
+
+    def extend(self, counts, rows: int, seqs=None, positions=None, offsets=None, stream=None):
+        """Make room for counts[s] (int32 [sequences]) more tokens of every sequence -> (seqs, positions, offsets): for row r of
+        `rows` its sequence (-1 behind the last) and position, and for sequence s its first row offsets[s].
+
+        Where pages, rows or the table's width do not suffice, the first sequence concerned and all after it get nothing;
+        `served` (int32 [1]) tells how many were served."""
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
+            return _call_on(stream, self.device, self.extend, counts, rows, seqs, positions, offsets)
+        return self._calls.extend(index, C._cuda_getCurrentRawStream(index), self.page_size, self.table, self.lengths, self.free,
+                                  self.free_count, self.served, self._workspace, counts, rows, seqs, positions, offsets)
+
+    def trim(self, keep, stream=None):
+        """Cut every sequence s to its first keep[s] tokens (int32 [sequences]; 0 releases it, negative leaves it as it is)."""
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
+            return _call_on(stream, self.device, self.trim, keep)
+        self._calls.trim(index, C._cuda_getCurrentRawStream(index), self.page_size, self.table, self.lengths, self.free,
+                         self.free_count, self._workspace, keep)
+
+
+def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling=None):
+    """(angles per token of each pair as a list of rotary_dim / 2, factor of the turned channels).
+
+    Pair i turns by base ** (-2 i / rotary_dim) a token.  `scaling` stretches that for contexts longer than the trained one:
+      {"kind": "linear", "factor": s}   positions divided by s;
+      {"kind": "base", "factor": s}     the base times s ** (d / (d - 2)), d = rotary_dim: the slowest pair is stretched by s;
+      {"kind": "parts", "factor": s, "context": c, "low": 1, "high": 32, "attention": None}
+          pairs by the number of turns they make in the trained context of c tokens: below `low` divided by s, above
+          `high` as they are, a mixture between; and the channels times `attention` (None: 0.1 ln s + 1).
+    """
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 0:
+        raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "rotary_dim=%d base=%r" % (rotary_dim, base))
+    given = dict(scaling or {"kind": "none"})
+    kind = given.pop("kind", None)
+    allowed = {"none": (), "linear": ("factor",), "base": ("factor",), "parts": ("factor", "context", "low", "high", "attention")}
+    if kind not in allowed or not set(given) <= set(allowed[kind]):
+        raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "scaling %r" % (scaling,))
+    s, factor = float(given.get("factor", 1.0)), 1.0
+    if not 0 < s < math.inf:
+        raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "scaling factor %r" % s)
+    if kind == "base" and rotary_dim > 2:
+        base = base * s ** (rotary_dim / (rotary_dim - 2))
+    rates = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if kind == "linear" or (kind == "base" and rotary_dim == 2):
+        rates = [f / s for f in rates]
+    elif kind == "parts":
+        if "context" not in given:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "scaling by parts needs the trained context")
+        low, high = float(given.get("low", 1.0)), float(given.get("high", 32.0))
+        if not low < high:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "low=%r high=%r" % (low, high))
+        keep = [min(1.0, max(0.0, (given["context"] * f / (2 * math.pi) - low) / (high - low))) for f in rates]
+        rates = [(1 - g) * f / s + g * f for f, g in zip(rates, keep)]
+        attention = given.get("attention")
+        factor = 0.1 * math.log(s) + 1.0 if attention is None else float(attention)
+    return rates, factor
+
+
+class Rotary:
+    """Rotary positions of a model's heads: the angles of its pairs of channels on the GPU.
+
+    rotary_dim: the channels that turn (default: all); interleaved: pairs are neighbours, else halves apart; base and
+    scaling: rotary_rates.  Or `rates` (angles per token, one a pair) and `factor` directly."""
+
+    def __init__(self, head_dim: int, rotary_dim=None, base: float = 10000.0, interleaved: bool = False, scaling=None, rates=None,
+                 factor=None, device="cuda"):
+        import torch
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if rates is None:
+            rates, scaled = rotary_rates(rotary_dim, base, scaling)
+            factor = scaled if factor is None else factor
+        elif scaling is not None:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "rates and scaling")
+        rates = torch.as_tensor(rates, dtype=torch.float64).to(device).contiguous().clone()
+        if rates.dim() != 1 or 2 * rates.numel() != rotary_dim:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "%d rates for %d channels" % (rates.numel(), rotary_dim))
+        self.head_dim, self.rotary_dim, self.interleaved = head_dim, rotary_dim, bool(interleaved)
+        self.rates, self.factor = rates, float(1.0 if factor is None else factor)
+        self.device, self._index = rates.device, rates.device.index
+        self._C, self._calls = torch._C, _tensor_calls()
+        if rates.is_cuda:   # the first call may come on any stream
+            torch.cuda.current_stream(self.device).synchronize()
+
+    def rotate(self, q, positions, k=None, q_out=None, k_out=None, stream=None):
+        """q (fp16 [rows][heads][head_dim]), and k if given, turned by positions (int32 [rows]; < 0: left as it was in the
+        output) -> q_out, or (q_out, k_out).  An output may be its input."""
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
+            return _call_on(stream, self.device, self.rotate, q, positions, k, q_out, k_out)
+        return self._calls.rotate(index, C._cuda_getCurrentRawStream(index), self.head_dim, self.rotary_dim, self.interleaved,
+                                  self.rates, self.factor, q, positions, k, q_out, k_out)
+
+
+class Adapters:
+    """Low-rank adapters of one linear: a fp16 [count][rank][K], b fp16 [count][N][rank], contiguous on the GPU (kept, not
+    copied).  scales: fp32 [count]; ranks: int32 [count], where adapters have fewer than the stack's."""
+
+    def __init__(self, a, b, scales=None, ranks=None):
+        import torch
+        self.handle = None
+        count = a.shape[0] if a.dim() == 3 else 0
+        fits = (a.dim() == 3 and b.dim() == 3 and b.shape[0] == count and b.shape[2] == a.shape[1]
+                and all(x.is_cuda and x.is_contiguous() and x.device == a.device for x in (a, b, scales, ranks) if x is not None)
+                and a.dtype is torch.float16 and b.dtype is torch.float16
+                and (scales is None or (scales.dtype is torch.float32 and tuple(scales.shape) == (count,)))
+                and (ranks is None or (ranks.dtype is torch.int32 and tuple(ranks.shape) == (count,))))
+        if not fits:
+            raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "a must be fp16 [count][rank][K], b fp16 [count][N][rank], scales "
+                           "fp32 [count] and ranks int32 [count], contiguous on one GPU")
+        self.a, self.b, self.scales, self.ranks = a, b, scales, ranks
+        self.count, self.rank, self.K = a.shape
+        self.N = b.shape[1]
+        self.device, self._index = a.device, a.device.index
+        self._C, self._calls = torch._C, _tensor_calls()
+        self.handle = exq_adapters_create(self.count, self.K, self.N, self.rank, a.data_ptr(), b.data_ptr(),
+                                          None if scales is None else scales.data_ptr(), None if ranks is None else ranks.data_ptr())
+
+    def add(self, x, ids, y, out=None, workspace=None, stream=None):
+        """out = y + scales[i] (x a[i]^T) b[i]^T with i = ids[row] (int32 [rows]; < 0: none): x fp16 [rows][K], y fp16
+        [rows][N].  `out` may be y.  workspace: uint8, exq_lora_workspace_bytes() of them (default: allocated)."""
+        index, C = self._index, self._C
+        if stream is not None or C._cuda_getDevice() != index:
+            return _call_on(stream, self.device, self.add, x, ids, y, out, workspace)
+        return self._calls.lora_add(index, C._cuda_getCurrentRawStream(index), self.handle, self.K, self.N, x, ids, y, out,
+                                    workspace)
+
+    def close(self):
+        if self.handle:
+            exq_adapters_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_sample = None
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, return_logprobs: bool = False, logprobs=None,
+           stream=None):
+    """One token of every row of logits (fp16 or fp32 [rows][vocab]) from random numbers u (fp32 [rows], in [0, 1)).
+
+    temperature, top_p, min_p: a number, or fp32 [rows]; top_k: a number, or int32 [rows] (0: off).  Filters apply in the
+    order top-k, top-p, min-p (include/exq.h) -> tokens int32 [rows], or (tokens, logprobs fp32 [rows]) with the logarithm of
+    the probability each was drawn with.  A row with u < 0 is left as it was; one without a token to draw gets -1.  Runs on
+    `stream` (default: the current stream of the logits' device) and may be captured."""
+    global _sample
+    if _sample is None:
+        import torch
+        _sample = (torch, torch._C, _tensor_calls())
+    torch, C, calls = _sample
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "logits must be a tensor on the GPU")
+    index = logits.get_device()
+    if stream is not None or C._cuda_getDevice() != index:
+        return _call_on(stream, logits.device, sample, logits, u, temperature, top_k, top_p, min_p, out, return_logprobs, logprobs)
+    return calls.sample(index, C._cuda_getCurrentRawStream(index), logits, u, temperature, top_k, top_p, min_p, out,
+                        return_logprobs, logprobs)

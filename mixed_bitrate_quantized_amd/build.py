@@ -13,7 +13,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libexq.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-HIP_SOURCES = ("exq_device.hip", "exq_prefill.hip", "exq_cache.hip")
+HIP_SOURCES = ("exq_device.hip", "exq_prefill.hip", "exq_cache.hip", "exq_pages.hip", "exq_rotate.hip", "exq_lora.hip",
+               "exq_sample.hip")
 HOST_SOURCES = ("exq_host.cpp",)
 TORCH_SOURCE = "exq_torch.cpp"
 TORCH_LIB = os.path.join(PKG, "_exq_torch.so")

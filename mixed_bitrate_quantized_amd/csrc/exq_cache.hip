@@ -9,6 +9,7 @@
 
 #include "exq_device_common.h"
 #include "exq_internal.h"
+#include "exq_operand.h"
 
 // Geometry of a cache and its borrowed pages (the exq_cache_t handle).
 struct exq_cache {
@@ -1288,8 +1289,6 @@ using namespace exq;
 
 namespace {
 
-bool cache_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
 exq_status check_geometry(int page_size, int kv_heads, int head_dim, int k_bits, int v_bits) {
     if (page_size < 16 || page_size > 65536 || page_size % 16)
         return fail(EXQ_ERR_INVALID_ARG, "page_size=%d is not a multiple of 16 in 16..65536", page_size);
@@ -1306,66 +1305,6 @@ exq_status check_geometry(int page_size, int kv_heads, int head_dim, int k_bits,
 CacheDev cache_dev(const exq_cache* c) {
     return CacheDev{c->pages, (int64_t)c->page_bytes, (uint32_t)c->n_pages, (uint32_t)c->page_size, (uint32_t)c->kv_heads,
                     (uint32_t)(c->page_size / kCacheTile)};
-}
-
-// An fp16 operand of (rows, heads, head_dim) with element strides.
-struct Operand {
-    const char* name;
-    const void* p;
-    int64_t row, head;
-    int rows, heads, dim;
-};
-
-constexpr int64_t kMaxStride = (int64_t)1 << 30;   // elements: with 2^31 rows and heads extents stay inside 64 bits
-
-exq_status check_operand(const Operand& x) {
-    if (!x.p) return fail(EXQ_ERR_INVALID_ARG, "%s is NULL", x.name);
-    if (!cache_aligned(x.p, 16)) return fail(EXQ_ERR_INVALID_ARG, "%s must be 16-byte aligned", x.name);
-    if (x.row < 0 || x.head < 0 || x.row % 8 || x.head % 8 || x.row > kMaxStride || x.head > kMaxStride)
-        return fail(EXQ_ERR_INVALID_ARG, "%s: strides (%lld, %lld) must be multiples of 8 in 0..2^30", x.name,
-                    (long long)x.row, (long long)x.head);
-    return EXQ_OK;
-}
-
-size_t extent(const Operand& x) {   // bytes from its first element to past its last
-    return 2 * ((size_t)(x.rows - 1) * (size_t)x.row + (size_t)(x.heads - 1) * (size_t)x.head + (size_t)x.dim);
-}
-
-bool ranges_meet(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
-// Whether no element of x is written twice.
-bool distinct(const Operand& x) {
-    const int64_t rows = x.rows, heads = x.heads, dim = x.dim;
-    const bool rows_outer = (heads == 1 || x.head >= dim) && (rows == 1 || x.row >= (heads - 1) * x.head + dim);
-    const bool heads_outer = (rows == 1 || x.row >= dim) && (heads == 1 || x.head >= (rows - 1) * x.row + dim);
-    return rows_outer || heads_outer;
-}
-
-// Whether two operands may share memory.  Slices of one buffer's rows (equal
-// row strides, disjoint within the row) do not, although their extents meet.
-bool operands_meet(const Operand& a, const Operand& b) {
-    if (!ranges_meet(a.p, extent(a), b.p, extent(b))) return false;
-    if (a.row != b.row || a.row == 0) return true;
-    const int64_t stride = 2 * a.row, na = 2 * ((a.heads - 1) * a.head + a.dim), nb = 2 * ((b.heads - 1) * b.head + b.dim);
-    const int64_t diff = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
-    const int64_t at = ((diff % stride) + stride) % stride;   // where b's rows start within a's stride
-    return !(na <= at && at + nb <= stride);
-}
-
-exq_status check_table(const int32_t* table, int rows, int width, int64_t stride) {
-    if (!table || !cache_aligned(table, 4)) return fail(EXQ_ERR_INVALID_ARG, "table is NULL or misaligned");
-    if (rows < 1 || width < 1) return fail(EXQ_ERR_INVALID_ARG, "table of %d x %d", rows, width);
-    if (stride < 0 || stride > kMaxStride || (rows > 1 && stride != 0 && stride < width))
-        return fail(EXQ_ERR_INVALID_ARG, "table_stride=%lld", (long long)stride);
-    return EXQ_OK;
-}
-
-// Bytes of a table from its first element to past its last.
-size_t table_extent(int rows, int width, int64_t stride) {
-    return 4 * ((size_t)(rows - 1) * (size_t)stride + (size_t)width);
 }
 
 // Calls f(IC<D>, IC<KB>, IC<VB>) for the cache's geometry.
@@ -1386,13 +1325,6 @@ void with_geometry(const exq_cache* c, F&& f) {
     }
 }
 
-constexpr int64_t kMaxLaunchThreads = 0xFFFFFFFFll;
-
-exq_status launched(const char* what) {
-    const hipError_t e = hipGetLastError();
-    return e == hipSuccess ? EXQ_OK : fail(EXQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
 // Waves of an append or read: a head of 16 rows each, and one block of rows
 // more than there are, for blocks that start at the first row's tile.
 int64_t rows_waves(const exq_cache* c, int rows) { return (((int64_t)rows + kCacheTile - 1) / kCacheTile + 1) * c->kv_heads; }
@@ -1410,7 +1342,7 @@ exq_status check_rows_call(const exq_cache* c, const Operand& k, const Operand& 
     exq_status st;
     if ((st = check_table(table, table_rows, table_width, table_stride)) != EXQ_OK) return st;
     if ((st = check_operand(k)) != EXQ_OK || (st = check_operand(v)) != EXQ_OK) return st;
-    if (!seqs || !positions || !cache_aligned(seqs, 4) || !cache_aligned(positions, 4))
+    if (!seqs || !positions || !aligned(seqs, 4) || !aligned(positions, 4))
         return fail(EXQ_ERR_INVALID_ARG, "seqs or positions is NULL or misaligned");
     const size_t bytes = (size_t)c->n_pages * c->page_bytes;
     if (ranges_meet(k.p, extent(k), c->pages, bytes) || ranges_meet(v.p, extent(v), c->pages, bytes))
@@ -1537,7 +1469,7 @@ exq_status exq_cache_create(void* pages, int64_t n_pages, int page_size, int kv_
     *out = nullptr;
     const exq_status st = check_geometry(page_size, kv_heads, head_dim, k_bits, v_bits);
     if (st != EXQ_OK) return st;
-    if (!pages || !cache_aligned(pages, 16)) return fail(EXQ_ERR_INVALID_ARG, "pages is NULL or not 16-byte aligned");
+    if (!pages || !aligned(pages, 16)) return fail(EXQ_ERR_INVALID_ARG, "pages is NULL or not 16-byte aligned");
     if (n_pages < 1 || n_pages > 0x7FFFFFFFll)
         return fail(EXQ_ERR_INVALID_ARG, "n_pages=%lld outside 1..2^31-1", (long long)n_pages);
     if (n_pages * kv_heads > 0xFFFFFFFFll / (page_size / kCacheTile))   // tiles are numbered in 32 bits
@@ -1626,7 +1558,7 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     const Operand qo{"q", q, q_row_stride, q_head_stride, rows, q_heads, c->head_dim};
     const Operand oo{"out", out, out_row_stride, out_head_stride, rows, q_heads, c->head_dim};
     if ((st = check_operand(qo)) != EXQ_OK || (st = check_operand(oo)) != EXQ_OK) return st;
-    if (!lengths || !cache_aligned(lengths, 4) || !cache_aligned(lse, 4))
+    if (!lengths || !aligned(lengths, 4) || !aligned(lse, 4))
         return fail(EXQ_ERR_INVALID_ARG, "lengths is NULL, or lengths or lse misaligned");
     if (!distinct(oo)) return fail(EXQ_ERR_INVALID_ARG, "rows or heads of out overlap themselves");
     const size_t bytes = (size_t)c->n_pages * c->page_bytes;
@@ -1643,7 +1575,7 @@ exq_status exq_attend(exq_cache_t c, const void* q, int64_t q_row_stride, int64_
     if (meets_read(out, extent(oo)) || (lse && meets_read(lse, lse_bytes)))
         return fail(EXQ_ERR_INVALID_ARG, "out or lse overlaps table or lengths");
     if (p.ws_bytes) {
-        if (!workspace || !cache_aligned(workspace, 16) || workspace_bytes < p.ws_bytes)
+        if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.ws_bytes)
             return fail(EXQ_ERR_INVALID_ARG, "workspace of %zu bytes: %zu 16-byte aligned ones are needed", workspace_bytes, p.ws_bytes);
         if (ranges_meet(workspace, p.ws_bytes, out, extent(oo)) || ranges_meet(workspace, p.ws_bytes, q, extent(qo)) ||
             ranges_meet(workspace, p.ws_bytes, c->pages, bytes) || (lse && ranges_meet(workspace, p.ws_bytes, lse, lse_bytes)) ||
