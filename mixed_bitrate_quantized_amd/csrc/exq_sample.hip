@@ -14,8 +14,8 @@
 // that at least j logits reach and, with the row dealt out over 1024 threads, not
 // many more.  These go to LDS, where the cut is found digit by digit of their
 // values (a histogram of weights or counts for each digit), and the draw digit
-// by digit of their indices.  Only where the cut lies below them (nearly flat
-// rows, or a top-k in the thousands) is the whole row histogrammed.
+// by digit of their indices.  Where the cut lies below them (nearly flat rows, or a
+// top-k in the thousands), a histogram of the whole row narrows it to one bin.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -29,10 +29,13 @@ namespace exq {
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
-constexpr int kSampleList = 8192;             // candidates that LDS holds
+constexpr int kSampleList = 4096;             // candidates that LDS holds
+constexpr int kSampleWant = 900;               // threads' largest logits that bound top-p's candidates
 constexpr int kSampleEach = kSampleList / kSampleThreads;
-constexpr int kSampleBins = 2048;             // of a digit of 11 bits
+constexpr int kDigit = 9;                     // bits looked at together
+constexpr int kSampleBins = 2048;             // of a row's histogram
 constexpr int kSampleMaxVocabLog2 = 21;
+constexpr int kPowers = 256;                  // 2^(i / 256) in LDS
 
 // A setting of every row: from memory, or the same for all.
 template <class T> struct PerRow {
@@ -53,26 +56,25 @@ struct SampleArgs {
     float* logprobs;
 };
 
-// Ordered keys: larger for larger logits, the value in the upper bits; 0 for a
-// NaN or -infinity, which are never drawn.  -0 and 0 have one key.
+// Ordered keys: larger for larger logits; 0 for a NaN or -infinity, which are
+// never drawn.  -0 and 0 have one key.
 template <class T> struct Logit;
 template <> struct Logit<_Float16> {
     typedef h8 vec;
-    static constexpr int VEC = 8, LEVELS = 2;   // digits of 11 bits that tell keys apart
+    static constexpr int VEC = 8, BITS = 16, COARSE = 4;   // COARSE: bits of a key below 1/64 of a power of two
     __device__ static uint32_t key(_Float16 x) {
         uint32_t b = __builtin_bit_cast(uint16_t, x);
         if (b == 0x8000u) b = 0;
         const uint32_t k = b ^ (b & 0x8000u ? 0xFFFFu : 0x8000u);
-        return (float)x > -__builtin_huge_valf() ? k << 16 : 0u;
+        return (float)x > -__builtin_huge_valf() ? k : 0u;
     }
-    __device__ static float value(uint32_t key) {
-        const uint32_t k = key >> 16;
+    __device__ static float value(uint32_t k) {
         return (float)__builtin_bit_cast(_Float16, (uint16_t)(k ^ (k & 0x8000u ? 0x8000u : 0xFFFFu)));
     }
 };
 template <> struct Logit<float> {
     typedef f4 vec;
-    static constexpr int VEC = 4, LEVELS = 3;
+    static constexpr int VEC = 4, BITS = 32, COARSE = 17;
     __device__ static uint32_t key(float x) {
         const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
         return x > -__builtin_huge_valf() ? b ^ (b & 0x80000000u ? 0xFFFFFFFFu : 0x80000000u) : 0u;
@@ -80,158 +82,202 @@ template <> struct Logit<float> {
     __device__ static float value(uint32_t k) { return __builtin_bit_cast(float, k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
 };
 
-// Weights of a row.  2^f for |f| <= 1/2 from its series: the first term left
-// out, (f ln 2)^13 / 13!, is below 2^-52.
+constexpr double kLn2d = 0.69314718055994530942;
+
+// 2^f for |f| <= 1 from its series; the first term left out is below 2^-53 of it
+// at 1/2, and 2^-40 at 1.
+__device__ __forceinline__ double exp2_series(double f) {
+    double p = 1.0;
+#pragma unroll
+    for (int i = 13; i >= 1; --i) p = __builtin_fma(p, f * (kLn2d / i), 1.0);
+    return p;
+}
+
+// Weights of a row: 2^(j / 256) from LDS times 2^r, |r| <= 1/512, whose series is cut
+// behind r^3: within 2^-45.
 struct Weights {
-    double top, c;   // largest logit, log2(e) / T
     float topf;
+    double top, c;   // largest logit, 256 log2(e) / T; beside an infinity all else weighs nothing
     double scale;    // 2^shift
-    double least;    // min-p, 0 for none
+    double least;    // min-p
+    const double* powers;
     __device__ double real(float l) const {
 #pragma clang fp contract(off)   // the same bits wherever the compiler puts it
-        double t = l == topf ? 0.0 : ((double)l - top) * c;
-        t = __builtin_fmax(t, -1100.0);
-        const double n = __builtin_rint(t), f = (t - n) * 0.69314718055994530942;
-        double p = 1.0 / 479001600;
-        p = __builtin_fma(p, f, 1.0 / 39916800);
-        p = __builtin_fma(p, f, 1.0 / 3628800);
-        p = __builtin_fma(p, f, 1.0 / 362880);
-        p = __builtin_fma(p, f, 1.0 / 40320);
-        p = __builtin_fma(p, f, 1.0 / 5040);
-        p = __builtin_fma(p, f, 1.0 / 720);
-        p = __builtin_fma(p, f, 1.0 / 120);
-        p = __builtin_fma(p, f, 1.0 / 24);
-        p = __builtin_fma(p, f, 1.0 / 6);
-        p = __builtin_fma(p, f, 0.5);
-        p = __builtin_fma(p, f, 1.0);
-        p = __builtin_fma(p, f, 1.0);
-        return __builtin_ldexp(p, (int)n);
+        constexpr double a = kLn2d / kPowers;
+        const double t = __builtin_fmax(((double)__builtin_fminf(l, __FLT_MAX__) - top) * c, -256.0 * 1000);
+        const double n = t + 6755399441055744.0;   // 1.5 * 2^52: rounds t, and leaves it in the sum's low bits
+        const double f = t - (n - 6755399441055744.0);
+        const int j = (int)(uint32_t)__builtin_bit_cast(uint64_t, n);
+        const double power = powers[j & (kPowers - 1)];
+        const double q = __builtin_fma(f, __builtin_fma(f, a * a * a / 6, a * a / 2), a);
+        const double w = __builtin_fma(power * f, q, power);
+        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, w) + ((uint64_t)(uint32_t)((j >> 8) << 20) << 32));
     }
     // In units, rounded: 2^52 + w * 2^shift has the whole number in its lower bits.
     __device__ uint64_t units(double w) const {
         return __builtin_bit_cast(uint64_t, __builtin_fma(w, scale, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
     }
     __device__ uint64_t of(float l) const { return units(real(l)); }
+    // Zero below min-p.
+    __device__ uint64_t kept(float l) const {
+        const double w = real(l);
+        return w >= least ? units(w) : 0;
+    }
     // ln of its probability among weights of `sum` units
     __device__ float log_of(float l, float temperature, uint64_t sum) const {
         const double z = l == topf ? 0.0 : ((double)l - top) / (double)temperature;
         return (float)(z - log((double)sum / scale));
     }
-    // Zero below min-p.
-    __device__ uint64_t kept(float l) const {
-        const double w = real(l);
-        return w >= least || l == topf ? units(w) : 0;
-    }
 };
 
 struct SampleShared {
     union {
-        uint64_t list[kSampleList];                          // key and index of a candidate
+        uint64_t list[kSampleList];                             // key and index of a candidate
         uint64_t tiles[(1 << kSampleMaxVocabLog2) / 256 + 2];   // sums of weights
     };
     uint64_t bins[kSampleBins];
+    double powers[kPowers];
     uint64_t wave[kSampleWaves];
-    uint64_t above;
+    uint64_t below;
     uint32_t bin, count;
 };
 
-__device__ __forceinline__ uint64_t wave_sum_before(uint64_t x, uint64_t& total) {   // exclusive
-    const int lane = threadIdx.x & 63;
-    uint64_t s = x;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const uint64_t y = __shfl_up(s, d);
-        if (lane >= d) s += y;
-    }
-    total = __shfl(s, 63);
-    return s - x;
+// Moves a value within a wave: lanes without a source get 0.
+template <int HOW, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t x) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, HOW, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), HOW, ROWS, 0xF, false);
+    return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t lane_value(uint64_t x, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane);
+    return (uint64_t)hi << 32 | lo;
+}
+struct Sum {
+    __device__ static uint64_t of(uint64_t a, uint64_t b) { return a + b; }
+};
+struct Larger {
+    __device__ static uint64_t of(uint64_t a, uint64_t b) { return a > b ? a : b; }
+};
+// Sums (or largest values) over the lanes up to each one, of 16 and of 64.
+template <class Op = Sum> __device__ __forceinline__ uint64_t prefix16(uint64_t x) {
+    x = Op::of(x, moved<0x111, 0xF>(x));
+    x = Op::of(x, moved<0x112, 0xF>(x));
+    x = Op::of(x, moved<0x114, 0xF>(x));
+    return Op::of(x, moved<0x118, 0xF>(x));
+}
+template <class Op = Sum> __device__ __forceinline__ uint64_t prefix64(uint64_t x) {
+    x = prefix16<Op>(x);
+    x = Op::of(x, moved<0x142, 0xA>(x));   // row 0's to row 1, row 2's to row 3
+    return Op::of(x, moved<0x143, 0xC>(x));   // the lower half's to the upper
 }
 
-// Sum over the workgroup, and of the threads before.
-__device__ __forceinline__ uint64_t block_sum_before(SampleShared& s, uint64_t x, uint64_t& total) {
-    const int wave = threadIdx.x / 64;
-    uint64_t mine;
-    uint64_t before = wave_sum_before(x, mine);
+// Over the workgroup: the sum of the threads before (with BEFORE), and of all.
+template <class Op = Sum, bool BEFORE = false>
+__device__ __forceinline__ uint64_t block_reduce(SampleShared& s, uint64_t x, uint64_t* before = nullptr) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
+    const uint64_t sums = prefix64<Op>(x);
     __syncthreads();
-    if (threadIdx.x % 64 == 0) s.wave[wave] = mine;
+    if (lane == 63) s.wave[wave] = sums;
     __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kSampleWaves; ++w) {
-        before += w < wave ? s.wave[w] : 0;
-        total += s.wave[w];
-    }
-    return before;
+    const uint64_t waves = prefix16<Op>(s.wave[lane & 15]);
+    if (BEFORE) *before = sums - x + (wave ? lane_value(waves, wave - 1) : 0);
+    return lane_value(waves, 15);
 }
-__device__ __forceinline__ uint64_t block_sum(SampleShared& s, uint64_t x) {
-    uint64_t total;
-    block_sum_before(s, x, total);
-    return total;
-}
+static_assert(kSampleWaves == 16, "a row of lanes adds up the waves");
 
-// The largest key K with sum of amounts of keys >= K at least `need` (which
-// all reach), from LEVELS digits of 11 bits below bit TOP, to the last one looked
-// at; `above`: the sum of amounts of larger ones.  source(f) calls
-// f(key, amount) for the thread's elements.
-template <int TOP, int LEVELS, class S>
-__device__ __forceinline__ uint32_t select_key(SampleShared& s, uint64_t need, uint64_t& above, S&& source) {
-    const int t = threadIdx.x;
-    uint32_t key = 0;
-    above = 0;
+// The bin of 64 PER that takes the running sum from the first one to `need`
+// or more, and the sum below it; by one wave, for all after a barrier.
+template <int PER> __device__ __forceinline__ void find_bin(SampleShared& s, uint64_t need) {
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        uint64_t x[PER], sum = 0;
 #pragma unroll
-    for (int level = 0; level < LEVELS; ++level) {
-        const int low = TOP - 11 * (level + 1) > 0 ? TOP - 11 * (level + 1) : 0;   // of this digit
-        const int high = TOP - 11 * level;
-        __syncthreads();
-        s.bins[t] = s.bins[t + kSampleThreads] = 0;
-        __syncthreads();
-        source([&](uint32_t k, uint64_t amount) {
-            const bool match = level == 0 || ((k ^ key) >> high) == 0;
-            if (match && amount)
-                atomicAdd(reinterpret_cast<unsigned long long*>(&s.bins[(k >> low) & (kSampleBins - 1) & ((1u << (high - low)) - 1)]),
-                          (unsigned long long)amount);
-        });
-        __syncthreads();
-        // bins from the top, two a thread
-        const int b = kSampleBins - 1 - 2 * t;
-        const uint64_t x = s.bins[b], y = s.bins[b - 1];
-        uint64_t total;
-        const uint64_t before = above + block_sum_before(s, x + y, total);
-        if (before < need && need <= before + x + y) {
-            const bool first = need <= before + x;
-            s.bin = first ? b : b - 1;
-            s.above = first ? before : before + x;
+        for (int i = 0; i < PER; ++i) {
+            x[i] = s.bins[PER * threadIdx.x + i];
+            sum += x[i];
         }
-        __syncthreads();
-        key |= s.bin << low;
-        above = s.above;
+        uint64_t before = prefix64(sum) - sum;
+        if (before < need && need <= before + sum) {
+            int bin = 0;
+#pragma unroll
+            for (int i = 0; i < PER - 1; ++i) {
+                const bool past = need > before + x[i];
+                if (!past) break;
+                before += x[i];
+                bin = i + 1;
+            }
+            s.bin = PER * threadIdx.x + bin;
+            s.below = before;
+        }
     }
-    return key;
+    __syncthreads();
 }
+
+__device__ __forceinline__ void add_to_bin(SampleShared& s, uint32_t bin, uint64_t amount) {
+    atomicAdd(reinterpret_cast<unsigned long long*>(&s.bins[bin]), (unsigned long long)amount);
+}
+
+// The smallest D below 2^bits with a sum of amounts of d <= D of `need` or more
+// (which all d reach), digit by digit; `below`: the sum of the smaller ones.
+// source(f) calls f(d, amount) for the thread's elements.
+template <class S>
+__device__ __forceinline__ uint32_t select(SampleShared& s, int bits, uint64_t need, uint64_t& below, S&& source) {
+    uint32_t value = 0;
+    below = 0;
+    for (int high = bits, low; high > 0; high = low) {
+        low = max(high - kDigit, 0);
+        __syncthreads();
+        if (threadIdx.x < 1 << kDigit) s.bins[threadIdx.x] = 0;
+        __syncthreads();
+        const bool first = high == bits;
+        source([&](uint32_t d, uint64_t amount) {
+            const uint32_t digit = d >> low;
+            if ((first || (digit ^ (value >> low)) >> (high - low) == 0) && amount)
+                add_to_bin(s, digit & ((1u << (high - low)) - 1), amount);
+        });
+        find_bin<(1 << kDigit) / 64>(s, need - below);
+        value |= s.bin << low;
+        below += s.below;
+    }
+    return value;
+}
+__device__ __forceinline__ int bits_of(uint32_t x) { return x ? 32 - __builtin_clz(x) : 0; }
 
 template <class T> __device__ __forceinline__ int head_elements(const T* row, int vocab) {
     return min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
 }
 
-// f(index, value) for the thread's elements of the row, in ascending order.
-template <class T, class F> __device__ __forceinline__ void for_row(const T* row, int vocab, F&& f) {
+// f(index, value) for the thread's elements of the row, AHEAD vectors loaded at
+// a time.
+template <class T, int AHEAD, class F> __device__ __forceinline__ void for_row(const T* row, int vocab, F&& f) {
     typedef typename Logit<T>::vec vec;
     constexpr int VEC = Logit<T>::VEC;
     const int t = threadIdx.x, head = head_elements(row, vocab), vecs = (vocab - head) / VEC, tail = head + vecs * VEC;
-    if (t < head) f(t, row[t]);
     const EXQ_GLOBAL vec* body = gptr<vec>(row + head);
-    for (int j = t; j < vecs; j += 4 * kSampleThreads) {
-        vec x[4];
+    for (int j = t; j < vecs; j += AHEAD * kSampleThreads) {
+        vec x[AHEAD];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = j + i * kSampleThreads < vecs ? body[j + i * kSampleThreads] : vec{};
+        for (int i = 0; i < AHEAD; ++i) x[i] = j + i * kSampleThreads < vecs ? body[j + i * kSampleThreads] : vec{};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < AHEAD; ++i)
             if (j + i * kSampleThreads < vecs)
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) f(head + (j + i * kSampleThreads) * VEC + e, x[i][e]);
     }
-    if (t < vocab - tail) f(tail + t, row[tail + t]);
+    // the row's ends, fewer than a vector each
+    const int ends = head + vocab - tail;
+    if (t < ends) {
+        const int i = t < head ? t : tail + t - head;
+        f(i, row[i]);
+    }
 }
+
+// What the filters left: keys above `key`, and of those equal the indices up to
+// `index`.
+struct Cut {
+    uint32_t key, index;
+    __device__ bool keeps(uint32_t k, uint32_t i) const { return k > key || (k == key && i <= index); }
+};
 
 template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
     __shared__ SampleShared s;
@@ -253,18 +299,14 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
 
     // the largest logit, at its lowest index
     uint64_t best = 0;
-    for_row<T>(row, a.vocab, [&](int i, T x) {
-        const uint32_t k = L::key(x);
-        if (k > (uint32_t)(best >> 32)) best = (uint64_t)k << 32 | (uint32_t)~i;
+    for_row<T, 4>(row, a.vocab, [&](int i, T x) {
+        const uint64_t it = (uint64_t)L::key(x) << 32 | (uint32_t)~i;
+        if (it >> 32) best = std::max(best, it);
     });
     const uint32_t mine = (uint32_t)(best >> 32);
-#pragma unroll
-    for (int d = 32; d; d /= 2) best = std::max<uint64_t>(best, __shfl_xor((unsigned long long)best, d));
-    if (lane == 0) s.wave[t / 64] = best;
-    if (t == 0) s.count = s.bin = 0;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSampleWaves; ++w) best = std::max<uint64_t>(best, s.wave[w]);
+    if (t < kPowers) s.powers[t] = exp2_series((double)t / kPowers);
+    if (t == 0) s.bin = s.below = 0;
+    best = block_reduce<Larger>(s, best);
     if (best == 0) {   // nothing that may be drawn
         if (t == 0) answer(-1, __builtin_nanf(""));
         return;
@@ -273,132 +315,188 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
         if (t == 0) answer((int)~(uint32_t)best, 0.0f);
         return;
     }
-    Weights w;
-    w.topf = L::value((uint32_t)(best >> 32));
-    w.top = w.topf;
-    w.c = 1.4426950408889634074 / (double)temperature;
-    w.scale = (double)(1ull << a.shift);
-    w.least = min_p;
+    const uint32_t top_key = (uint32_t)(best >> 32);
+    const float topf = L::value(top_key), finite_top = __builtin_fminf(topf, __FLT_MAX__);
+    const Weights w{topf, (double)finite_top, topf > __FLT_MAX__ ? 1e300 : kPowers * 1.4426950408889634074 / (double)temperature,
+                    (double)(1ull << a.shift), min_p, s.powers};
+    const int index_bits = a.vocab > 1 << 2 * kDigit ? kSampleMaxVocabLog2 : 2 * kDigit;
+    Cut cut{0, 0xFFFFFFFFu};
 
-    const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
-    uint32_t cut = 1;             // kept: keys above it, and of those equal the ones up to index cut_index
-    uint32_t cut_index = 0xFFFFFFFFu;
-    if (by_k || by_p) {
-        // candidates: at least as many as threads' maxima reach the threshold
-        uint64_t above;
-        const uint64_t threads = block_sum(s, mine ? 1 : 0);
-        const uint64_t want = std::min<uint64_t>(by_k ? (uint64_t)top_k : 1000, threads);
-        const uint32_t least = std::max(1u, select_key<32, 1>(s, want, above, [&](auto&& f) {
-            if (mine) f(mine, 1);
-        }));
-        uint64_t sum = 0;
-        for_row<T>(row, a.vocab, [&](int i, T x) {
+    // Elements that want(key, value) asks for, and the cut keeps, into the list.
+    const auto collect = [&](auto&& want) {
+        __syncthreads();
+        if (t == 0) s.count = 0;
+        __syncthreads();
+        for_row<T, 2>(row, a.vocab, [&](int i, T x) {
             const uint32_t k = L::key(x);
-            if (!by_k && k) sum += w.of(L::value(k));
-            if (k >= least) {
+            if (k && want(k, x) && cut.keeps(k, (uint32_t)i)) {
                 const uint32_t at = atomicAdd(&s.count, 1u);
                 if (at < kSampleList) s.list[at] = (uint64_t)k << 32 | (uint32_t)i;
             }
         });
-        uint64_t total = by_k ? 0 : block_sum(s, sum);   // of what top-p is a share of, if it is the whole row
         __syncthreads();
-        const uint32_t count = s.count;
+        return (int)std::min<uint32_t>(s.count, 0x7FFFFFFFu);
+    };
+
+    const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
+    if (by_k || by_p) {
+        uint64_t below;
+        // a threshold that `want` threads' largest logits reach, to 1/64 of a power of two
+        const auto coarse = [&](uint32_t k) { return min((top_key >> L::COARSE) - (k >> L::COARSE), (1u << kDigit) - 1); };
+        const uint64_t threads = block_reduce(s, mine ? 1 : 0);
+        const uint64_t want = std::min<uint64_t>(by_k ? (uint64_t)top_k : kSampleWant, threads);
+        const uint32_t least = select(s, kDigit, want, below, [&](auto&& f) {
+            if (mine) f(coarse(mine), 1);
+        });
+        double thread_sum = 0;
+        int count = collect([&](uint32_t k, T l) {
+            if (!by_k) thread_sum += w.real((float)l);
+            return coarse(k) <= least;
+        });
+        const auto share = [&](uint64_t total) {   // what top-p needs of it
+            return std::min<uint64_t>(std::max<uint64_t>((uint64_t)__builtin_ceil((double)top_p * (double)total), 1), total);
+        };
+        // top-p's share of the whole row
+        const uint64_t row_share = by_k ? 0 : share(block_reduce(s, (uint64_t)__builtin_rint(thread_sum * w.scale)));
+
+        // the thread's candidates
         uint32_t keys[kSampleEach], at[kSampleEach];
         uint64_t ws[kSampleEach];
-        bool held = count <= kSampleList && (!by_k || count >= (uint32_t)top_k);
-        if (held) {
-            uint64_t here = 0;
+        const auto load = [&] {
 #pragma unroll
             for (int i = 0; i < kSampleEach; ++i) {
-                const bool in = t + i * kSampleThreads < (int)count;
-                const uint64_t x = in ? s.list[t + i * kSampleThreads] : 0;
-                keys[i] = (uint32_t)(x >> 32);
-                at[i] = (uint32_t)x;
-                ws[i] = in ? w.of(L::value(keys[i])) : 0;
-                here += ws[i];
+                keys[i] = at[i] = 0;
+                ws[i] = 0;
+                if (t + i * kSampleThreads < count) {
+                    const uint64_t x = s.list[t + i * kSampleThreads];
+                    keys[i] = (uint32_t)(x >> 32);
+                    at[i] = (uint32_t)x;
+                    ws[i] = w.of(L::value(keys[i]));
+                }
             }
-            const uint64_t sum_here = block_sum(s, here);
-            if (!by_k) held = (double)sum_here >= (double)top_p * (double)total;
-        }
+        };
         const auto each = [&](auto&& f) {
 #pragma unroll
             for (int i = 0; i < kSampleEach; ++i)
-                if (keys[i]) f(keys[i], at[i], ws[i]);
+                if (i * kSampleThreads < count && keys[i]) f(keys[i], at[i], ws[i]);
         };
-        const auto every = [&](auto&& f) {
-            for_row<T>(row, a.vocab, [&](int i, T x) {
-                const uint32_t k = L::key(x);
-                if (k) f(k, (uint32_t)i, k);
-            });
-        };
-        // Narrows the cut by one filter: `from(f)` calls f(key, index, what weighs it).
-        const auto narrow = [&](auto&& from, auto&& weigh, bool counts, uint64_t need) {
-            const uint32_t old = cut, old_index = cut_index;
-            const auto source = [&](auto&& f) {
-                from([&](uint32_t k, uint32_t i, auto x) {
-                    if (k > old || (k == old && i <= old_index)) f(k, i, counts ? 1 : weigh(k, x));
-                });
-            };
-            cut = select_key<32, L::LEVELS>(s, need, above, [&](auto&& f) { source([&](uint32_t k, uint32_t, uint64_t x) { f(k, x); }); });
-            // of equal ones the first: their amounts are equal
-            const uint64_t one = counts ? 1 : w.of(L::value(cut));
-            const uint64_t ties = (need - above + one - 1) / one;
-            uint64_t skipped;
-            const uint32_t last = select_key<22, 2>(s, ties, skipped, [&](auto&& f) {
-                source([&](uint32_t k, uint32_t i, uint64_t) {
-                    if (k == cut) f(~i & 0x3FFFFFu, 1);
-                });
-            });
-            cut_index = ~last & 0x3FFFFFu;
-        };
-        const auto filters = [&](auto&& from, auto&& weigh) {
-            if (by_k) {
-                uint64_t n = 0;
-                from([&](uint32_t, uint32_t, auto) { ++n; });
-                n = block_sum(s, n);
-                narrow(from, weigh, true, std::min<uint64_t>(n, top_k));
-                if (by_p) {
-                    uint64_t x = 0;
-                    from([&](uint32_t k, uint32_t i, auto y) {
-                        if (k > cut || (k == cut && i <= cut_index)) x += weigh(k, y);
-                    });
-                    total = block_sum(s, x);
-                }
-            }
-            if (by_p) {
-                const double share = (double)top_p * (double)total;
-                narrow(from, weigh, false, std::min<uint64_t>(std::max<uint64_t>((uint64_t)__builtin_ceil(share), 1), total));
-            }
-        };
+        // Whether the candidates hold what the filters leave: else they are found anew, around each filter's cut.
+        bool held = count <= kSampleList && (!by_k || count >= top_k);
         if (held) {
-            filters(each, [](uint32_t, uint64_t x) { return x; });
-            uint64_t sum = 0;
-#pragma unroll
-            for (int i = 0; i < kSampleEach; ++i) {
-                const bool in = keys[i] > cut || (keys[i] == cut && at[i] <= cut_index);
-                ws[i] = in ? w.kept(L::value(keys[i])) : 0;
-                sum += ws[i];
+            load();
+            if (!by_k) {
+                uint64_t here = 0;
+                each([&](uint32_t, uint32_t, uint64_t x) { here += x; });
+                held = block_reduce(s, here) >= row_share;
             }
-            sum = block_sum(s, sum);
+        }
+        // their keys lie that near the top, or anywhere from the last bin on
+        const int held_bits = least < (1u << kDigit) - 1 ? L::COARSE + kDigit : L::BITS;
+
+#pragma unroll 1
+        for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
+            const bool counts = filter == 0;
+            uint64_t need, all = 0;   // of those in the cut (or in the bin that holds the next one)
+            int bits = held_bits;
+            if (held) {
+                each([&](uint32_t k, uint32_t i, uint64_t x) { all += !cut.keeps(k, i) ? 0 : counts ? 1 : x; });
+                all = block_reduce(s, all);
+                need = counts ? (uint64_t)top_k : by_k ? share(all) : row_share;
+                if (need >= all) continue;
+            } else {
+                // 64 bins for one of the logits, or for a power of two of the weights
+                const float rate = counts ? 64.0f : __builtin_fminf((float)(w.c * (64.0 / kPowers)), 1e30f);
+                const auto bin_of = [&](float l) {
+                    const float d = (finite_top - __builtin_fminf(l, __FLT_MAX__)) * rate;
+                    return d < (float)(kSampleBins - 1) ? (int)d : kSampleBins - 1;
+                };
+                __syncthreads();
+                for (int i = t; i < kSampleBins; i += kSampleThreads) s.bins[i] = 0;
+                __syncthreads();
+                for_row<T, 2>(row, a.vocab, [&](int i, T x) {
+                    const uint32_t k = L::key(x);
+                    if (k && cut.keeps(k, (uint32_t)i)) {
+                        const uint64_t amount = counts ? 1 : w.of((float)x);
+                        if (amount) add_to_bin(s, (uint32_t)bin_of((float)x), amount);
+                    }
+                });
+                __syncthreads();
+                for (int i = t; i < kSampleBins; i += kSampleThreads) all += s.bins[i];
+                all = block_reduce(s, all);
+                need = counts ? (uint64_t)top_k : share(all);
+                if (need >= all) continue;
+                find_bin<kSampleBins / 64>(s, need);
+                const int bin = (int)s.bin;
+                below = s.below;
+                count = collect([&](uint32_t, T x) { return bin_of((float)x) == bin; });
+                bits = L::BITS;
+                if (count > kSampleList) {   // of equal or nearly equal ones: over the row again, by key and then by index
+                    uint32_t key = 0;
+                    uint64_t left = need;
+#pragma unroll 1
+                    for (int by_index = 0; by_index < 2; ++by_index) {
+                        const uint32_t d = select(s, by_index ? index_bits : L::BITS, left, below, [&](auto&& f) {
+                            for_row<T, 1>(row, a.vocab, [&](int i, T x) {
+                                const uint32_t k = L::key(x);
+                                if (k && cut.keeps(k, (uint32_t)i) && (!by_index || k == key))
+                                    f(by_index ? (uint32_t)i : top_key - k, counts || by_index ? 1 : w.of((float)x));
+                            });
+                        });
+                        if (by_index) {
+                            cut = Cut{key, d};
+                        } else {
+                            key = top_key - d;
+                            const uint64_t one = counts ? 1 : w.of(L::value(key));
+                            left = (left - below + one - 1) / one;
+                        }
+                    }
+                    continue;
+                }
+                load();
+                need -= below;
+            }
+            // the key whose elements take the sum to `need`; of those, whose amounts are equal, the first ones
+            const uint32_t key = top_key - select(s, bits, need, below, [&](auto&& f) {
+                each([&](uint32_t k, uint32_t i, uint64_t x) {
+                    if (cut.keeps(k, i)) f(top_key - k, counts ? 1 : x);
+                });
+            });
+            const uint64_t one = counts ? 1 : w.of(L::value(key)), ties = (need - below + one - 1) / one;
+            uint64_t equal = 0;
+            each([&](uint32_t k, uint32_t i, uint64_t) { equal += k == key && cut.keeps(k, i); });
+            uint32_t index = cut.key == key ? cut.index : 0xFFFFFFFFu;
+            if (block_reduce(s, equal) > ties)
+                index = select(s, index_bits, ties, below, [&](auto&& f) {
+                    each([&](uint32_t k, uint32_t i, uint64_t) {
+                        if (k == key && cut.keeps(k, i)) f(i, 1);
+                    });
+                });
+            cut = Cut{key, index};
+        }
+        if (held) {
+            uint64_t sum = 0;
+            each([&](uint32_t k, uint32_t i, uint64_t& x) {
+                x = cut.keeps(k, i) ? w.kept(L::value(k)) : 0;
+                sum += x;
+            });
+            sum = block_reduce(s, sum);
             // the draw: indices in ascending order
             const uint64_t target = std::min<uint64_t>((uint64_t)((double)u * (double)sum), sum - 1);
-            const uint32_t token = ~select_key<22, 2>(s, target + 1, above, [&](auto&& f) {
-                each([&](uint32_t, uint32_t i, uint64_t x) { f(~i & 0x3FFFFFu, x); });
-            }) & 0x3FFFFFu;
-#pragma unroll
-            for (int i = 0; i < kSampleEach; ++i)
-                if (keys[i] && at[i] == token)
-                    answer((int)token, w.log_of(L::value(keys[i]), temperature, sum));
+            const uint32_t token = select(s, index_bits, target + 1, below, [&](auto&& f) {
+                each([&](uint32_t, uint32_t i, uint64_t x) { f(i, x); });
+            });
+            each([&](uint32_t k, uint32_t i, uint64_t) {
+                if (i == token) answer((int)token, w.log_of(L::value(k), temperature, sum));
+            });
             return;
         }
-        filters(every, [&](uint32_t k, uint32_t) { return w.of(L::value(k)); });
         __syncthreads();
     }
 
     // the draw over the whole row: sums of tiles, then the tile that holds it
-    const auto weight = [&](T x, int i) -> uint64_t {
-        const uint32_t k = L::key(x);
-        return k > cut || (k == cut && (uint32_t)i <= cut_index) ? w.kept(L::value(k)) : 0;
+    const auto weight = [&](T l, int i) -> uint64_t {
+        const uint32_t k = L::key(l);
+        return k && cut.keeps(k, (uint32_t)i) ? w.kept((float)l) : 0;
     };
     const int head = head_elements(row, a.vocab), vecs = (a.vocab - head) / L::VEC, tail = head + vecs * L::VEC;
     const int tiles = 2 + (vecs + 63) / 64;
@@ -413,29 +511,29 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
         return {head + j * L::VEC, j < vecs ? L::VEC : 0};
     };
     for (int tile = t / 64; tile < tiles; tile += kSampleWaves) {
-        const Span x = span(tile);
-        uint64_t sum = 0, tile_sum;
-        if (x.n == L::VEC) {
-            const typename L::vec v = *gptr<typename L::vec>(row + x.first);
+        const Span at = span(tile);
+        uint64_t sum = 0;
+        if (at.n == L::VEC) {
+            const typename L::vec v = *gptr<typename L::vec>(row + at.first);
 #pragma unroll
-            for (int e = 0; e < L::VEC; ++e) sum += weight(v[e], x.first + e);
-        } else {
-            for (int e = 0; e < x.n; ++e) sum += weight(row[x.first + e], x.first + e);
+            for (int e = 0; e < L::VEC; ++e) sum += weight(v[e], at.first + e);
+        } else if (at.n) {
+            sum = weight(row[at.first], at.first);
         }
-        wave_sum_before(sum, tile_sum);
-        if (lane == 0) s.tiles[tile] = tile_sum;
+        sum = prefix64(sum);
+        if (lane == 63) s.tiles[tile] = sum;
     }
     __syncthreads();
     const int per = (tiles + kSampleThreads - 1) / kSampleThreads;
-    uint64_t sum = 0, total;
+    uint64_t sum = 0, before;
     for (int i = t * per; i < std::min(tiles, (t + 1) * per); ++i) sum += s.tiles[i];
-    uint64_t before = block_sum_before(s, sum, total);
+    const uint64_t total = block_reduce<Sum, true>(s, sum, &before);
     const uint64_t target = std::min<uint64_t>((uint64_t)((double)u * (double)total), total - 1);
     if (before <= target && target < before + sum) {
         for (int i = t * per; i < tiles; ++i) {
             if (target < before + s.tiles[i]) {
                 s.bin = i;
-                s.above = before;
+                s.below = before;
                 break;
             }
             before += s.tiles[i];
@@ -443,17 +541,19 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
     }
     __syncthreads();
     if (t >= 64) return;
-    const int tile = (int)s.bin;
-    const Span x = span(tile);
-    uint64_t lane_sum = 0, tile_sum;
-    for (int e = 0; e < x.n; ++e) lane_sum += weight(row[x.first + e], x.first + e);
-    uint64_t at = s.above + wave_sum_before(lane_sum, tile_sum);
-    if (at <= target && target < at + lane_sum) {
-        for (int e = 0; e < x.n; ++e) {
-            const int i = x.first + e;
-            at += weight(row[i], i);
-            if (target < at) {
-                answer(i, w.log_of(L::value(L::key(row[i])), temperature, total));
+    // its elements one by one: 64 neighbours at a time
+    const Span at = span((int)s.bin);
+    uint64_t lane_sum = 0;
+#pragma unroll 1
+    for (int e = 0; e < at.n; ++e) lane_sum += weight(row[at.first + e], at.first + e);
+    uint64_t reached = s.below + prefix64(lane_sum) - lane_sum;
+    if (reached <= target && target < reached + lane_sum) {
+#pragma unroll 1
+        for (int e = 0; e < at.n; ++e) {
+            const int i = at.first + e;
+            reached += weight(row[i], i);
+            if (target < reached) {
+                answer(i, w.log_of((float)row[i], temperature, total));
                 break;
             }
         }
