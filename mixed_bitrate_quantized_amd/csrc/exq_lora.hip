@@ -4,10 +4,10 @@
 // for any mix of adapters in one call.
 //
 // Bound by the bytes of x, y, out and the adapters in use; for a few rows by
-// the launches.  Three of them:
-//   group   rows of one adapter are gathered into tiles, so that an adapter in
-//           use is read once for a tile of its rows, in whatever order they come;
-//   shrink  low = x A^T for a tile, K cut over waves and workgroups;
+// the launches.  Rows of one adapter are gathered into tiles, so that an adapter
+// in use is read once for a tile of its rows, in whatever order they come:
+//   group   the rows sorted by adapter (up to 64 rows every wave does that for itself);
+//   shrink  low = x A^T for 16 rows, K cut over waves and workgroups;
 //   expand  out = y + s low B^T for a tile and a block of columns.
 // Products run on v_mfma_f32_16x16x32_f16, sums are fp32.  low enters the second
 // product as two fp16 numbers whose sum has 22 bits, scaled by a power of two
@@ -35,10 +35,11 @@ namespace exq {
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
-// A tile: rows perm[start], .. perm[start + count - 1] of one adapter; adapter
-// -1: rows without one, -2: rows whose number is out of range.
+// A tile: up to 16 or 64 rows of one adapter, its rank and scale; adapter -1:
+// rows without one, -2: rows whose number is out of range.  count 0: none.
 struct LoraTile {
-    int32_t adapter, start, count, pad;
+    int32_t adapter, count, rank;
+    float scale;
 };
 
 struct LoraArgs {
@@ -49,97 +50,172 @@ struct LoraArgs {
     const float* scales;
     const int32_t *ranks, *ids;
     // workspace
-    int32_t* tile_count;
     LoraTile* tiles;
-    int32_t* perm;
-    float* low;        // [splits][rows][rank]: parts of x A^T, rows in tiles' order
+    int32_t* tile_rows;   // of each tile
+    int32_t* place;       // of each row among its adapter's
+    float* low;           // [splits][rows][rank]: parts of x A^T
     int splits, slice;   // parts of K, and channels of one
-    int columns;         // of an expanding workgroup
+    int blocks, columns;   // expanding workgroups of a tile, and columns of one
     bool in_place;
 };
 
+constexpr int kLoraFew = 64;     // rows that a wave groups by itself
+constexpr int kLoraSplits = 8;   // parts of K at most
+
+__device__ __forceinline__ int lora_rank(const LoraArgs& a, int adapter) {
+    return adapter < 0 ? 0 : a.ranks ? min(max(a.ranks[adapter], 0), a.rank) : a.rank;
+}
+__device__ __forceinline__ float lora_scale(const LoraArgs& a, int adapter) {
+    return a.scales && adapter >= 0 ? a.scales[adapter] : 1.0f;
+}
+
+// Tile `no` of tiles of T rows, lane i with the row of slot i.
+template <int T> __device__ __forceinline__ LoraTile lora_tile(const LoraArgs& a, int no, int& row) {
+    const int lane = threadIdx.x & 63;
+    const LoraTile tile = a.tiles[no];
+    row = a.tile_rows[(int64_t)no * T + lane % T];
+    if (lane >= tile.count) row = 0;
+    return tile;
+}
+
+// The same for up to 64 rows without the table: every wave groups them for
+// itself, an adapter at a time, in order of its first row.
+template <int T> __device__ __forceinline__ LoraTile lora_tile_of_few(const LoraArgs& a, int no, int& row) {
+    const int lane = threadIdx.x & 63;
+    int id = lane < a.rows ? a.ids[lane] : -1;
+    id = id < 0 ? -1 : id < a.adapters ? id : -2;
+    // rows without an adapter need nothing where out is y
+    uint64_t left = __ballot(lane < a.rows && !(a.in_place && id == -1));
+    row = 0;
+    while (left) {
+        const int one = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t same = __ballot(id == one) & left;
+        const int n = __builtin_popcountll(same), tiles = (n + T - 1) / T;
+        if (no < tiles) {
+            // the place of the bit that is the lane's in `same`
+            int nth = no * T + lane;
+#pragma unroll
+            for (int w = 32; w; w /= 2) {
+                const int below = __builtin_popcountll(same >> row & ((1ull << w) - 1));
+                if (nth >= below) {
+                    nth -= below;
+                    row += w;
+                }
+            }
+            const int count = min(T, n - no * T);
+            if (lane >= count) row = 0;
+            return LoraTile{one, count, lora_rank(a, one), lora_scale(a, one)};
+        }
+        no -= tiles;
+        left &= ~same;
+    }
+    return LoraTile{-1, 0, 0, 0.0f};
+}
+
 constexpr int kLoraGroupThreads = 1024;
+constexpr int kLoraGroupEach = 8;   // rows whose places a thread keeps in registers
 constexpr int kLoraMaxAdapters = 8192;
 
 // Counting sort of the rows by adapter.  Which of an adapter's rows share a tile
 // depends on the order of atomics; a row's result does not depend on that.
-__global__ __launch_bounds__(kLoraGroupThreads) void lora_group_kernel(LoraArgs a, int tile_rows) {
-    __shared__ int32_t next[kLoraMaxAdapters + 2];
-    __shared__ int32_t wave_rows[kLoraGroupThreads / 64], wave_tiles[kLoraGroupThreads / 64];
+// One workgroup, a chain of look-ups: 2048 rows of 6 adapters take 4 us of a
+// call's 45.
+__global__ __launch_bounds__(kLoraGroupThreads) void lora_group_kernel(LoraArgs a, int T, int most_tiles) {
+    __shared__ int32_t bin_rows[kLoraMaxAdapters + 2], first_tile[kLoraMaxAdapters + 2];
+    __shared__ int32_t wave_tiles[kLoraGroupThreads / 64];
     const int t = threadIdx.x, lane = t % 64, wave = t / 64, bins = a.adapters + 2;
-    for (int i = t; i < bins; i += kLoraGroupThreads) next[i] = 0;
+    int id[kLoraGroupEach], place[kLoraGroupEach];
+    const auto bin_of = [&](int i) { return i < 0 ? a.adapters : i < a.adapters ? i : a.adapters + 1; };
+#pragma unroll
+    for (int i = 0; i < kLoraGroupEach; ++i) id[i] = t + i * kLoraGroupThreads < a.rows ? a.ids[t + i * kLoraGroupThreads] : 0;
+    for (int i = t; i < bins; i += kLoraGroupThreads) bin_rows[i] = 0;
     __syncthreads();
-    const auto bin_of = [&](int id) { return id < 0 ? a.adapters : id < a.adapters ? id : a.adapters + 1; };
-    for (int r = t; r < a.rows; r += kLoraGroupThreads) atomicAdd(&next[bin_of(a.ids[r])], 1);
+#pragma unroll
+    for (int i = 0; i < kLoraGroupEach; ++i)
+        if (t + i * kLoraGroupThreads < a.rows) place[i] = atomicAdd(&bin_rows[bin_of(id[i])], 1);
+    for (int r = t + kLoraGroupEach * kLoraGroupThreads; r < a.rows; r += kLoraGroupThreads)
+        a.place[r] = atomicAdd(&bin_rows[bin_of(a.ids[r])], 1);
     __syncthreads();
-    int rows_before = 0, tiles_before = 0;
+    int tiles_before = 0;
     for (int base = 0; base < bins; base += kLoraGroupThreads) {
-        const int bin = base + t;
-        const int n = bin < bins ? next[bin] : 0;
+        const int bin = base + t, adapter = bin < a.adapters ? bin : bin == a.adapters ? -1 : -2;
+        const int n = bin < bins ? bin_rows[bin] : 0;
         // rows without an adapter need nothing where out is y
-        const int tiles = bin == a.adapters && a.in_place ? 0 : (n + tile_rows - 1) / tile_rows;
-        int rs = n, ts = tiles;
+        const int tiles = adapter == -1 && a.in_place ? 0 : (n + T - 1) / T;
+        const int rank = n ? lora_rank(a, adapter) : 0;
+        const float scale = n ? lora_scale(a, adapter) : 0.0f;
+        int sum = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) {
-            const int u = __shfl_up(rs, d), v = __shfl_up(ts, d);
-            if (lane >= d) rs += u, ts += v;
+            const int u = __shfl_up(sum, d);
+            if (lane >= d) sum += u;
         }
-        if (lane == 63) {
-            wave_rows[wave] = rs;
-            wave_tiles[wave] = ts;
-        }
+        if (lane == 63) wave_tiles[wave] = sum;
         __syncthreads();
-        int row = rows_before + rs - n, tile = tiles_before + ts - tiles;
+        int tile = tiles_before + sum - tiles;
         for (int w = 0; w < kLoraGroupThreads / 64; ++w) {
-            row += w < wave ? wave_rows[w] : 0;
             tile += w < wave ? wave_tiles[w] : 0;
-            rows_before += wave_rows[w];
             tiles_before += wave_tiles[w];
         }
         if (bin < bins) {
-            next[bin] = row;
-            const int adapter = bin < a.adapters ? bin : bin == a.adapters ? -1 : -2;
-            for (int i = 0; i < tiles; ++i)
-                a.tiles[tile + i] = LoraTile{adapter, row + i * tile_rows, min(tile_rows, n - i * tile_rows), 0};
+            first_tile[bin] = tiles ? tile : -1;
+            for (int i = 0; i < tiles; ++i) a.tiles[tile + i] = LoraTile{adapter, min(T, n - i * T), rank, scale};
         }
         __syncthreads();
     }
-    if (t == 0) *a.tile_count = tiles_before;
-    for (int r = t; r < a.rows; r += kLoraGroupThreads) a.perm[atomicAdd(&next[bin_of(a.ids[r])], 1)] = r;
+    for (int i = tiles_before + t; i < most_tiles; i += kLoraGroupThreads) a.tiles[i] = LoraTile{-1, 0, 0, 0.0f};
+    const auto put = [&](int r, int i, int at) {
+        const int first = first_tile[bin_of(i)];
+        if (first >= 0) a.tile_rows[(int64_t)first * T + at] = r;
+    };
+#pragma unroll
+    for (int i = 0; i < kLoraGroupEach; ++i)
+        if (t + i * kLoraGroupThreads < a.rows) put(t + i * kLoraGroupThreads, id[i], place[i]);
+    for (int r = t + kLoraGroupEach * kLoraGroupThreads; r < a.rows; r += kLoraGroupThreads) put(r, a.ids[r], a.place[r]);
 }
 
-__device__ __forceinline__ h8 zero8() { return h8{}; }
+// A wave's part of low^T = A x^T: 16 RT ranks by 16 TT rows (of a tile of T), K
+// cut over W waves.  Lane 16 q + i holds channels 8 q .. + 7 of rank i and of row i
+// for each step of 32 channels, so both operands are loads of a row's neighbours.
+// All of a wave's STEPS steps are in flight at once where K is cut that fine.
+// Tiles of 64 rows are shrunk 32 at a time, to read A half as often: x from
+// memory and A from L2 add up (2048 rows of 8192 at rank 32 took 21 us by 16,
+// 12 of them without A, 13 without x).
+constexpr int shrink_waves(int T) { return T == 64 ? 16 : 8; }
+constexpr int shrink_rows(int T) { return T == 64 ? 2 : 1; }   // in units of 16
+template <int TT, int RT> constexpr int kShrinkSteps = RT == 4 && TT == 2 ? 2 : 4;
 
-constexpr int kShrinkWaves = 8;
-
-// A wave's part of low^T = A x^T: 16 RT ranks by 16 TT rows.  Lane 16 q + i holds
-// channels 8 q .. + 7 of rank i and of row i for each step of 32 channels, so
-// both operands are loads of a row's neighbours.
-template <int TT, int RT>
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs a) {
-    __shared__ f4 parts[kShrinkWaves / 2][RT * TT][64];
-    const int tile_no = blockIdx.x / a.splits, split = blockIdx.x - tile_no * a.splits;
-    if (tile_no >= *a.tile_count) return;
-    const LoraTile tile = a.tiles[tile_no];
-    if (tile.adapter < 0) return;
+template <bool FEW, int T, int RT>
+__global__ __launch_bounds__(64 * shrink_waves(T)) void lora_shrink_kernel(LoraArgs a) {
+    constexpr int TT = shrink_rows(T), W = shrink_waves(T);
+    __shared__ f4 parts[W / 2][RT * TT][64];
+    constexpr int SUBS = T / (16 * TT);
+    const int split = blockIdx.x % a.splits, no = blockIdx.x / a.splits / SUBS, slot0 = blockIdx.x / a.splits % SUBS * 16 * TT;
     const int t = threadIdx.x, wave = t / 64, lane = t % 64, i16 = lane % 16, q = lane / 16;
+    int rows_of_tile;
+    const LoraTile tile = FEW ? lora_tile_of_few<T>(a, no, rows_of_tile) : lora_tile<T>(a, no, rows_of_tile);
+    if (FEW && split == 0 && blockIdx.y == 0 && wave == 0) {   // for lora_expand_kernel
+        if (lane == 0) a.tiles[no] = tile;
+        if (lane < T) a.tile_rows[no * T + lane] = rows_of_tile;
+    }
+    if (tile.adapter < 0 || slot0 >= tile.count) return;
     const int rank0 = blockIdx.y * 16 * RT;
-    const int rank = a.ranks ? min(max(a.ranks[tile.adapter], 0), a.rank) : a.rank;
     // the wave's channels
-    const int per = a.slice / kShrinkWaves;
+    const int per = a.slice / W;
     const int k_begin = split * a.slice + wave * per, k_end = min(a.K, k_begin + per);
     const EXQ_GLOBAL uint16_t *xp[TT], *ap[RT];
+    int row[TT];
     bool x_in[TT], a_in[RT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        x_in[j] = 16 * j + i16 < tile.count;
-        const int row = x_in[j] ? a.perm[tile.start + 16 * j + i16] : 0;
-        xp[j] = gptr<uint16_t>(a.x + (int64_t)row * a.x_row);
+    for (int m = 0; m < TT; ++m) {
+        x_in[m] = slot0 + 16 * m + i16 < tile.count;
+        row[m] = __shfl(rows_of_tile, slot0 + 16 * m + i16);
+        xp[m] = gptr<uint16_t>(a.x + (int64_t)row[m] * a.x_row);
     }
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
         const int r = rank0 + 16 * j + i16;
-        a_in[j] = r < rank;
+        a_in[j] = r < tile.rank;
         ap[j] = gptr<uint16_t>(a.a + ((int64_t)tile.adapter * a.rank + (a_in[j] ? r : 0)) * a.K);
     }
     f4 acc[RT][TT];
@@ -147,7 +223,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
     for (int j = 0; j < RT; ++j)
 #pragma unroll
         for (int m = 0; m < TT; ++m) acc[j][m] = f4{};
-    constexpr int STEPS = TT + RT <= 4 ? 4 : 2;   // in flight
+    constexpr int STEPS = kShrinkSteps<TT, RT>;
     for (int k0 = k_begin; k0 < k_end; k0 += 32 * STEPS) {
         h8 xs[STEPS][TT], as[STEPS][RT];
 #pragma unroll
@@ -155,9 +231,9 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
             const int k = k0 + 32 * s + 8 * q;
             const bool in = k < k_end;   // K and slices are multiples of 8
 #pragma unroll
-            for (int m = 0; m < TT; ++m) xs[s][m] = in && x_in[m] ? *(const EXQ_GLOBAL h8*)(xp[m] + k) : zero8();
+            for (int m = 0; m < TT; ++m) xs[s][m] = in && x_in[m] ? *(const EXQ_GLOBAL h8*)(xp[m] + k) : h8{};
 #pragma unroll
-            for (int j = 0; j < RT; ++j) as[s][j] = in && a_in[j] ? *(const EXQ_GLOBAL h8*)(ap[j] + k) : zero8();
+            for (int j = 0; j < RT; ++j) as[s][j] = in && a_in[j] ? *(const EXQ_GLOBAL h8*)(ap[j] + k) : h8{};
         }
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
@@ -168,7 +244,7 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
     }
     // the waves' sums, in a fixed order
 #pragma unroll
-    for (int half = kShrinkWaves / 2; half; half /= 2) {
+    for (int half = W / 2; half; half /= 2) {
         if (wave >= half && wave < 2 * half)
 #pragma unroll
             for (int j = 0; j < RT; ++j)
@@ -190,123 +266,172 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(LoraArgs
         for (int j = 0; j < RT; ++j) {
             const int r = rank0 + 16 * j + 4 * q;
             if (x_in[m] && r < a.rank)   // a.rank is a multiple of 8
-                *gptr_w<f4>(a.low + ((int64_t)split * a.rows + tile.start + 16 * m + i16) * a.rank + r) = acc[j][m];
+                *gptr_w<f4>(a.low + ((int64_t)split * a.rows + row[m]) * a.rank + r) = acc[j][m];
         }
 }
 
 constexpr int kExpandWaves = 4;
 constexpr int kLowPad = 8;   // fp16 after each row of low in LDS, against bank conflicts
+constexpr int kExpandRank16 = 256, kExpandRank64 = 128;   // largest ranks of tiles of 16 and of 64 rows
 
-// A wave takes 64 columns at a time: four products whose rows are columns 16 q +
-// 4 m + i, so that a lane ends up with 16 neighbouring columns of one row.
-template <int TT>
-__global__ __launch_bounds__(64 * kExpandWaves) void lora_expand_kernel(LoraArgs a) {
+// A wave takes 16 NT columns at a time: NT products whose rows are columns 4 NT q
+// + 4 m + i, so that a lane ends up with 4 NT neighbouring columns of one row.
+template <int T>
+__global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
-    __shared__ float unscale[16 * TT];
-    const int blocks = (a.N + a.columns - 1) / a.columns;
-    const int tile_no = blockIdx.x / blocks, block = blockIdx.x - tile_no * blocks;
-    if (tile_no >= *a.tile_count) return;
-    const LoraTile tile = a.tiles[tile_no];
+    __shared__ float unscale[T];
+    constexpr int TT = T / 16, NT = T == 64 ? 2 : 4, COLS = 16 * NT;
+    const int block = blockIdx.x % a.blocks;
+    int rows_of_tile;
+    const LoraTile tile = lora_tile<T>(a, blockIdx.x / a.blocks, rows_of_tile);
+    if (tile.count == 0) return;
     const int t = threadIdx.x, lane = t % 64, wave = t / 64, i16 = lane % 16, q = lane / 16;
     const int n_begin = block * a.columns, n_end = min(a.N, n_begin + a.columns);
     if (tile.adapter < 0) {   // copied, or refused
-        const uint16_t nan = 0x7E00;
-        const h8 nans = {__builtin_bit_cast(_Float16, nan), __builtin_bit_cast(_Float16, nan), __builtin_bit_cast(_Float16, nan),
-                         __builtin_bit_cast(_Float16, nan), __builtin_bit_cast(_Float16, nan), __builtin_bit_cast(_Float16, nan),
-                         __builtin_bit_cast(_Float16, nan), __builtin_bit_cast(_Float16, nan)};
+        const _Float16 nan = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
+        const h8 nans = {nan, nan, nan, nan, nan, nan, nan, nan};
         for (int r = 0; r < tile.count; ++r) {
-            const int64_t row = a.perm[tile.start + r];
+            const int64_t row = __shfl(rows_of_tile, r);
             for (int n = n_begin + 8 * t; n < n_end; n += 8 * 64 * kExpandWaves)
                 *gptr_w<h8>(a.out + row * a.out_row + n) = tile.adapter == -1 ? *gptr<h8>(a.y + row * a.y_row + n) : nans;
         }
         return;
     }
-    const int rank = a.ranks ? min(max(a.ranks[tile.adapter], 0), a.rank) : a.rank;
     const int padded = (a.rank + 31) / 32 * 32, pitch = padded + kLowPad;
-    uint16_t *hi = lds, *lo = lds + 16 * TT * pitch;
-    const float scale = a.scales ? a.scales[tile.adapter] : 1.0f;
-    // low: four lanes a row add up its parts, find its largest and cut it in two
-    {
-        constexpr int LANES = 64 * kExpandWaves / (16 * TT);   // of a row: 16 or 4
-        const int r = t / LANES, first = t % LANES;
-        const float* from = a.low + (int64_t)(tile.start + r) * a.rank;
-        const auto value = [&](int j) {
-            float v = 0.0f;
-            if (r < tile.count && j < rank)
-                for (int s = 0; s < a.splits; ++s) v += from[(int64_t)s * a.rows * a.rank + j];
-            return v;
-        };
-        float most = 0.0f;
-        for (int j = first; j < rank; j += LANES) {
-            const float v = __builtin_fabsf(value(j));
-            most = v < __builtin_huge_valf() ? __builtin_fmaxf(most, v) : most;
-        }
+    uint16_t *hi = lds, *lo = lds + T * pitch;
+    // low: a few lanes a row add up its parts, all asked for at once
+    constexpr int LANES = 64 * kExpandWaves / T;   // of a row: 16 or 4
+    constexpr int MOST = (T == 64 ? kExpandRank64 : kExpandRank16) / (4 * LANES);
+    const int low_row = t / LANES, first = 4 * (t % LANES);
+    const float* from = a.low + (int64_t)__shfl(rows_of_tile, low_row) * a.rank;
+    const int64_t part = (int64_t)a.rows * a.rank;
+    f4 v[MOST];
 #pragma unroll
-        for (int d = 1; d < LANES; d *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, d));
-        // |low| * 2^e below 2^15
-        int e = 0;
-        if (most > 0.0f) e = 15 - (__builtin_amdgcn_frexp_expf(most));
-        e = min(e, 126);
-        for (int j = first; j < padded; j += LANES) {
-            const float v = __builtin_ldexpf(value(j), e);
-            const _Float16 h = (_Float16)v;
-            hi[r * pitch + j] = __builtin_bit_cast(uint16_t, h);
-            lo[r * pitch + j] = f32_to_f16_bits(v - (float)h);
-        }
-        if (first == 0) unscale[r] = __builtin_ldexpf(scale, -e);
+    for (int m = 0; m < MOST; ++m) {
+        const int j = first + 4 * LANES * m;
+        v[m] = f4{};
+        if (4 * LANES * m >= padded) continue;
+        f4 parts[kLoraSplits];
+#pragma unroll
+        for (int s = 0; s < kLoraSplits; ++s)   // zero behind the adapter's own rank; a.rank is a multiple of 8
+            parts[s] = s < a.splits && low_row < tile.count && j < a.rank ? *gptr<f4>(from + s * part + j) : f4{};
+#pragma unroll
+        for (int s = 0; s < kLoraSplits; ++s) v[m] += parts[s];
     }
-    __syncthreads();
+    // the wave's first y and B, asked for ahead of their use
     int64_t row[TT];
     bool in[TT];
-    float f[TT];
 #pragma unroll
-    for (int m = 0; m < TT; ++m) {
-        in[m] = 16 * m + i16 < tile.count;
-        row[m] = in[m] ? a.perm[tile.start + 16 * m + i16] : 0;
-        f[m] = unscale[16 * m + i16];
+    for (int j = 0; j < TT; ++j) {
+        in[j] = 16 * j + i16 < tile.count;
+        row[j] = __shfl(rows_of_tile, 16 * j + i16);
     }
     const uint16_t* b = a.b + (int64_t)tile.adapter * a.N * a.rank;
-    for (int n0 = n_begin + 64 * wave; n0 < n_end; n0 += 64 * kExpandWaves) {
-        f4 acc[4][TT];
+    struct Loaded {   // for a step of columns
+        h8 y[TT][NT / 2], b[2][NT];
+    };
+    const auto load_b = [&](Loaded& x, int n0, int k) {   // 64 ranks: whole lines of B where it has as many
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < NT; ++m) {
+                const int c = n0 + 4 * NT * (i16 / 4) + 4 * m + i16 % 4, j = k + 32 * h + 8 * q;
+                x.b[h][m] = c < n_end && j < tile.rank ? *gptr<h8>(b + (int64_t)c * a.rank + j) : h8{};
+            }
+    };
+    const auto load = [&](Loaded& x, int n0) {
+        load_b(x, n0, 0);
+#pragma unroll
+        for (int j = 0; j < TT; ++j)
+#pragma unroll
+            for (int half = 0; half < NT / 2; ++half) {   // N and blocks are multiples of 8
+                const int n = n0 + 4 * NT * q + 8 * half;
+                x.y[j][half] = in[j] && n < n_end ? *gptr<h8>(a.y + row[j] * a.y_row + n) : h8{};
+            }
+    };
+    Loaded l0, l1;
+    load(l0, n_begin + COLS * wave);
+    // its largest, and the cut in two: |low| * 2^e below 2^15
+    {
+        float most = 0.0f;
+#pragma unroll
+        for (int m = 0; m < MOST; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = __builtin_fabsf(v[m][e]);
+                most = x < __builtin_huge_valf() ? __builtin_fmaxf(most, x) : most;
+            }
+#pragma unroll
+        for (int d = 1; d < LANES; d *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, d));
+        const int e2 = most > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(most), 126) : 0;
+#pragma unroll
+        for (int m = 0; m < MOST; ++m) {
+            const int j = first + 4 * LANES * m;
+            if (j >= padded) continue;
+            h4 h, l;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = __builtin_ldexpf(v[m][e], e2);
+                h[e] = (_Float16)x;
+                l[e] = (_Float16)(x - (float)h[e]);
+            }
+            *reinterpret_cast<h4*>(hi + low_row * pitch + j) = h;
+            *reinterpret_cast<h4*>(lo + low_row * pitch + j) = l;
+        }
+        if (first == 0) unscale[low_row] = __builtin_ldexpf(tile.scale, -e2);
+    }
+    __syncthreads();
+    float f[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) f[j] = unscale[16 * j + i16];
+    const auto step = [&](Loaded& x, int n0) {
+        f4 acc[NT][TT];
+#pragma unroll
+        for (int m = 0; m < NT; ++m)
 #pragma unroll
             for (int j = 0; j < TT; ++j) acc[m][j] = f4{};
-        for (int k = 0; k < rank; k += 32) {
-            h8 bs[4];
+        for (int k = 0; k < tile.rank; k += 64) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int n = n0 + 16 * (i16 / 4) + 4 * m + i16 % 4, j = k + 8 * q;
-                h8 v = n < n_end && j < rank ? *gptr<h8>(b + (int64_t)n * a.rank + j) : zero8();
-                if (j + 8 > rank)   // what lies behind the adapter's own rank may be anything
+            for (int h = 0; h < 2; ++h) {
+                const int k8 = k + 32 * h + 8 * q;
+                if (k + 32 * h >= tile.rank) continue;
+                if (k8 + 8 > tile.rank)   // what lies behind the adapter's own rank may be anything
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = j + e < rank ? v[e] : (_Float16)0.0f;
-                bs[m] = v;
-            }
+                    for (int m = 0; m < NT; ++m)
 #pragma unroll
-            for (int j = 0; j < TT; ++j) {
-                const h8 h = *reinterpret_cast<const h8*>(hi + (16 * j + i16) * pitch + k + 8 * q);
-                const h8 l = *reinterpret_cast<const h8*>(lo + (16 * j + i16) * pitch + k + 8 * q);
+                        for (int e = 0; e < 8; ++e) x.b[h][m][e] = k8 + e < tile.rank ? x.b[h][m][e] : (_Float16)0.0f;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bs[m], h, acc[m][j], 0, 0, 0);
-                    acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(bs[m], l, acc[m][j], 0, 0, 0);
+                for (int j = 0; j < TT; ++j) {
+                    const h8 high = *reinterpret_cast<const h8*>(hi + (16 * j + i16) * pitch + k8);
+                    const h8 rest = *reinterpret_cast<const h8*>(lo + (16 * j + i16) * pitch + k8);
+#pragma unroll
+                    for (int m = 0; m < NT; ++m) {
+                        acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.b[h][m], high, acc[m][j], 0, 0, 0);
+                        acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.b[h][m], rest, acc[m][j], 0, 0, 0);
+                    }
                 }
             }
+            if (k + 64 < tile.rank) load_b(x, n0, k + 64);
         }
-        const int n = n0 + 16 * q;
+        const int n = n0 + 4 * NT * q;
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-            if (!in[j]) continue;
+        for (int j = 0; j < TT; ++j)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (n + 8 * half >= n_end) continue;   // N and blocks are multiples of 8
-                h8 v = *gptr<h8>(a.y + row[j] * a.y_row + n + 8 * half);
+            for (int half = 0; half < NT / 2; ++half) {
+                h8 o;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = (_Float16)__builtin_fmaf(acc[2 * half + e / 4][j][e % 4], f[j], (float)v[e]);
-                *gptr_w<h8>(a.out + row[j] * a.out_row + n + 8 * half) = v;
+                for (int e = 0; e < 8; ++e) o[e] = (_Float16)__builtin_fmaf(acc[2 * half + e / 4][j][e % 4], f[j], (float)x.y[j][half][e]);
+                if (in[j] && n + 8 * half < n_end) *gptr_w<h8>(a.out + row[j] * a.out_row + n + 8 * half) = o;
             }
-        }
+    };
+    // the next step's loads are in flight under this one's products
+    constexpr int STEP = COLS * kExpandWaves;
+    for (int n0 = n_begin + COLS * wave; n0 < n_end; n0 += 2 * STEP) {
+        if (n0 + STEP < n_end) load(l1, n0 + STEP);
+        step(l0, n0);
+        if (n0 + STEP >= n_end) break;
+        if (n0 + 2 * STEP < n_end) load(l0, n0 + 2 * STEP);
+        step(l1, n0 + STEP);
     }
 }
 
@@ -320,28 +445,55 @@ namespace {
 
 // Shape of a call.
 struct LoraPlan {
-    int tile_rows, tiles, splits, slice;
-    size_t tiles_at, perm_at, low_at, bytes;   // of the workspace
+    bool few;
+    int tile_rows, tiles, splits, slice, rank_tiles;
+    size_t rows_at, place_at, low_at, bytes;   // of the workspace
 };
 
 exq_status plan_lora(const exq_adapters* h, int rows, LoraPlan* p) {
     if (!h) return fail(EXQ_ERR_INVALID_ARG, "adapters is NULL");
     if (rows < 0) return fail(EXQ_ERR_INVALID_ARG, "rows=%d", rows);
-    p->tile_rows = rows >= 512 && h->rank <= 128 ? 64 : 16;
+    *p = LoraPlan{};
+    if (rows == 0) return EXQ_OK;
+    p->few = rows <= kLoraFew;
+    p->tile_rows = rows >= 512 && h->rank <= kExpandRank64 ? 64 : 16;
     p->tiles = (int)std::min<int64_t>(rows, (int64_t)rows / p->tile_rows + h->count + 2);
-    // a wave has 128 channels at least; about 512 workgroups
-    const int rank_blocks = (h->rank + 31) / 32;
-    const int most = std::max(1, (h->K + 128 * kShrinkWaves - 1) / (128 * kShrinkWaves));
-    const int busy = std::max(1, std::min(p->tiles, rows / p->tile_rows + 1)) * rank_blocks;
-    p->splits = std::max(1, std::min(most, 512 / busy));
-    const int unit = 32 * kShrinkWaves;
+    p->rank_tiles = h->rank <= 16 ? 1 : h->rank <= 32 || p->few ? 2 : 4;
+    // a wave's channels are all in flight at once, or there are four waves a SIMD
+    // already: workgroups that wait for a place would double the time (2048 rows of
+    // 8192 in 4 parts, 280 workgroups, 21 us, in 3 parts 18.5)
+    const int rank_blocks = (h->rank + 16 * p->rank_tiles - 1) / (16 * p->rank_tiles);
+    const int W = shrink_waves(p->tile_rows), TT = shrink_rows(p->tile_rows);
+    const int channels = 32 * W * (p->rank_tiles == 4 && TT == 2 ? kShrinkSteps<2, 4> : kShrinkSteps<1, 1>);
+    const int most = std::min(kLoraSplits, (h->K + channels - 1) / channels);
+    const int64_t part_tiles = ((int64_t)rows + 16 * TT - 1) / (16 * TT) + (TT > 1 ? std::min(h->count, rows / 64) : 0);   // half of them filled
+    p->splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 4096 / W / (part_tiles * rank_blocks)));
+    const int unit = 32 * W;
     p->slice = ((h->K + p->splits - 1) / p->splits + unit - 1) / unit * unit;
     p->splits = (h->K + p->slice - 1) / p->slice;
-    p->tiles_at = 16;
-    p->perm_at = p->tiles_at + sizeof(LoraTile) * (size_t)p->tiles;
-    p->low_at = (p->perm_at + 4 * (size_t)rows + 15) / 16 * 16;
-    p->bytes = rows ? p->low_at + 4 * (size_t)p->splits * rows * h->rank : 0;
+    p->rows_at = sizeof(LoraTile) * (size_t)p->tiles;
+    p->place_at = p->rows_at + 4 * (size_t)p->tiles * p->tile_rows;
+    p->low_at = (p->place_at + (rows > kLoraGroupThreads * kLoraGroupEach ? 4 * (size_t)rows : 0) + 15) / 16 * 16;
+    p->bytes = p->low_at + 4 * (size_t)p->splits * rows * h->rank;
     return EXQ_OK;
+}
+
+template <bool FEW, int T> exq_status launch_lora(const LoraArgs& a, const LoraPlan& p, hipStream_t s) {
+    exq_status st;
+    if (!FEW) {
+        hipLaunchKernelGGL(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 0, s, a, T, p.tiles);
+        if ((st = launched("adapters group launch")) != EXQ_OK) return st;
+    }
+    const int ranks = 16 * p.rank_tiles;
+    const dim3 grid((unsigned)(p.tiles * (T / 16 / shrink_rows(T)) * p.splits), (unsigned)((a.rank + ranks - 1) / ranks));
+    const dim3 block(64 * shrink_waves(T));
+    if (p.rank_tiles == 1) hipLaunchKernelGGL((lora_shrink_kernel<FEW, T, 1>), grid, block, 0, s, a);
+    else if (FEW || p.rank_tiles == 2) hipLaunchKernelGGL((lora_shrink_kernel<FEW, T, 2>), grid, block, 0, s, a);
+    else if constexpr (!FEW) hipLaunchKernelGGL((lora_shrink_kernel<FEW, T, 4>), grid, block, 0, s, a);
+    if ((st = launched("adapters shrink launch")) != EXQ_OK) return st;
+    const int pitch = (a.rank + 31) / 32 * 32 + kLowPad;
+    hipLaunchKernelGGL((lora_expand_kernel<T>), dim3((unsigned)(p.tiles * a.blocks)), dim3(64 * kExpandWaves), 2u * 2u * T * pitch, s, a);
+    return launched("adapters expand launch");
 }
 
 }  // namespace
@@ -422,37 +574,22 @@ exq_status exq_lora_add(exq_adapters_t h, const void* x, int64_t x_row_stride, i
     a.scales = h->scales;
     a.ranks = h->ranks;
     a.ids = ids;
-    a.tile_count = reinterpret_cast<int32_t*>(ws);
-    a.tiles = reinterpret_cast<LoraTile*>(ws + p.tiles_at);
-    a.perm = reinterpret_cast<int32_t*>(ws + p.perm_at);
+    a.tiles = reinterpret_cast<LoraTile*>(ws);
+    a.tile_rows = reinterpret_cast<int32_t*>(ws + p.rows_at);
+    a.place = reinterpret_cast<int32_t*>(ws + p.place_at);
     a.low = reinterpret_cast<float*>(ws + p.low_at);
     a.splits = p.splits;
     a.slice = p.slice;
     a.in_place = in_place;
-    // a wave's 64 columns at a time, blocks that make about 1024 workgroups
-    const int unit = 64 * kExpandWaves, units = (h->N + unit - 1) / unit;
-    const int busy = std::min(p.tiles, rows / p.tile_rows + 1);
-    a.columns = unit * std::max<int>(1, (int)std::min<int64_t>(units, (int64_t)units * busy / 1024));
-    const int blocks = (h->N + a.columns - 1) / a.columns, rank_blocks = (h->rank + 31) / 32;
-    if ((int64_t)p.tiles * std::max(blocks, p.splits * rank_blocks) > kMaxLaunchThreads / 1024)
+    // blocks that make at most about 750 workgroups, which run side by side
+    const int unit = 16 * (p.tile_rows == 64 ? 2 : 4) * kExpandWaves, units = (h->N + unit - 1) / unit;
+    const int busy = p.few ? std::min(rows, h->count + 1) : std::min(p.tiles, rows / p.tile_rows + 1);
+    a.columns = unit * (int)std::min<int64_t>(units, ((int64_t)units * busy + 749) / 750);
+    a.blocks = (h->N + a.columns - 1) / a.columns;
+    if ((int64_t)p.tiles * std::max(a.blocks, p.splits * (p.tile_rows / 16)) > kMaxLaunchThreads / 512)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows in one call", rows);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    hipLaunchKernelGGL(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 0, s, a, p.tile_rows);
-    if ((st = launched("adapters group launch")) != EXQ_OK) return st;
-    const dim3 shrink_grid((unsigned)(p.tiles * p.splits), (unsigned)rank_blocks), shrink_block(64 * kShrinkWaves);
-    const dim3 expand_grid((unsigned)(p.tiles * blocks)), expand_block(64 * kExpandWaves);
-    const int pitch = (h->rank + 31) / 32 * 32 + kLowPad;
-    const unsigned lds = 2u * 2u * p.tile_rows * pitch;
-    if (p.tile_rows == 64) {
-        hipLaunchKernelGGL((lora_shrink_kernel<4, 2>), shrink_grid, shrink_block, 0, s, a);
-        if ((st = launched("adapters shrink launch")) != EXQ_OK) return st;
-        hipLaunchKernelGGL((lora_expand_kernel<4>), expand_grid, expand_block, lds, s, a);
-    } else {
-        hipLaunchKernelGGL((lora_shrink_kernel<1, 2>), shrink_grid, shrink_block, 0, s, a);
-        if ((st = launched("adapters shrink launch")) != EXQ_OK) return st;
-        hipLaunchKernelGGL((lora_expand_kernel<1>), expand_grid, expand_block, lds, s, a);
-    }
-    return launched("adapters expand launch");
+    return p.few ? launch_lora<true, 16>(a, p, s) : p.tile_rows == 64 ? launch_lora<false, 64>(a, p, s) : launch_lora<false, 16>(a, p, s);
 }
 
 }  // extern "C"
