@@ -35,7 +35,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
 constexpr int kSampleList = 4096;             // candidates that LDS holds
-constexpr int kSampleEach = kSampleList / kSampleThreads;
+constexpr int kSampleNear = 900;              // a top-k that is looked for from the threads' largest logits
 constexpr int kDigit = 9;                     // bits looked at together
 constexpr int kSampleBins = 2048;             // of a row's histogram
 constexpr int kSampleMaxVocabLog2 = 21;
@@ -74,6 +74,23 @@ template <> struct Logit<_Float16> {
         const uint32_t k = b ^ (b & 0x8000u ? 0xFFFFu : 0x8000u);
         return (float)x > -__builtin_huge_valf() ? k : 0u;
     }
+    __device__ static float largest(const h8& x) {   // NaN aside
+        const h4 a = __builtin_elementwise_max(__builtin_shufflevector(x, x, 0, 1, 2, 3), __builtin_shufflevector(x, x, 4, 5, 6, 7));
+        const h2 b = __builtin_elementwise_max(__builtin_shufflevector(a, a, 0, 1), __builtin_shufflevector(a, a, 2, 3));
+        return (float)__builtin_elementwise_max(b[0], b[1]);
+    }
+    __device__ static _Float16 at(const h8& x, int e) {
+        const u4v y = __builtin_bit_cast(u4v, x);
+        const uint32_t pair = e < 4 ? (e < 2 ? y[0] : y[1]) : (e < 6 ? y[2] : y[3]);
+        return __builtin_bit_cast(_Float16, (uint16_t)(pair >> (16 * (e & 1))));
+    }
+    // Key of the smallest value that is x or more (0: any).
+    __device__ static uint32_t first_from(double x) {
+        if (!(x > -65504.0)) return 0;
+        if (x > 65504.0) return 0xFC00u;
+        const _Float16 near = (_Float16)(float)x;
+        return key(near) + ((double)near < x);
+    }
     __device__ static float value(uint32_t k) {
         return (float)__builtin_bit_cast(_Float16, (uint16_t)(k ^ (k & 0x8000u ? 0x8000u : 0xFFFFu)));
     }
@@ -85,6 +102,16 @@ template <> struct Logit<float> {
     __device__ static uint32_t key(float x) {
         const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
         return x > -__builtin_huge_valf() ? b ^ (b & 0x80000000u ? 0xFFFFFFFFu : 0x80000000u) : 0u;
+    }
+    __device__ static float largest(const f4& x) {
+        return __builtin_fmaxf(__builtin_fmaxf(x[0], x[1]), __builtin_fmaxf(x[2], x[3]));
+    }
+    __device__ static float at(const f4& x, int e) { return e < 2 ? (e ? x[1] : x[0]) : (e < 3 ? x[2] : x[3]); }
+    __device__ static uint32_t first_from(double x) {
+        if (!(x > -(double)__FLT_MAX__)) return 0;
+        if (x > (double)__FLT_MAX__) return 0xFF800000u;
+        const float near = (float)x;
+        return key(near) + ((double)near < x);
     }
     __device__ static float value(uint32_t k) { return __builtin_bit_cast(float, k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
 };
@@ -106,7 +133,6 @@ struct Weights {
     float topf;
     double top, c;   // largest logit, 256 log2(e) / T; beside an infinity all else weighs nothing
     double scale;    // 2^shift
-    double least;    // min-p
     const double* powers;
     __device__ double power(double t) const {   // 2^(t / 256)
 #pragma clang fp contract(off)   // the same bits wherever the compiler puts it
@@ -129,11 +155,6 @@ struct Weights {
         return __builtin_bit_cast(uint64_t, __builtin_fma(w, scale, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
     }
     __device__ uint64_t of(float l) const { return units(real(l)); }
-    // Zero below min-p.
-    __device__ uint64_t kept(float l) const {
-        const double w = real(l);
-        return w >= least ? units(w) : 0;
-    }
     // ln of its probability among weights of `sum` units
     __device__ float log_of(float l, float temperature, uint64_t sum) const {
         const double z = l == topf ? 0.0 : ((double)l - top) / (double)temperature;
@@ -141,29 +162,35 @@ struct Weights {
     }
 };
 
-constexpr int kSampleTiles = (1 << kSampleMaxVocabLog2) / 256 + 2;   // at most
+constexpr int kSampleTiles = 2048;
 
 struct SampleShared {
     union {
         uint32_t counts[kCounters];      // of magnitude m: positive in the lower half, negative in the upper
-        uint64_t list[kSampleList];      // key and index of a candidate
         struct {
-            uint64_t sums[kSampleTiles];     // of weights above the cut
-            uint32_t equals[kSampleTiles];   // elements at it
-        } tile;
+            uint64_t list[kSampleList], weights[kSampleList];   // of candidates: key and index, weight
+            uint32_t vectors[kSampleList];                      // of the row, that hold candidates
+            uint64_t tile_sum[kSampleTiles];                    // weights left, above the cut
+            uint32_t tile_equal[kSampleTiles];                  // elements at it
+        };
     };
     uint64_t bins[kSampleBins];
     double powers[kPowers];
     uint64_t wave[kSampleWaves];
     uint64_t below;
-    uint32_t bin, count;
+    uint32_t bin, count, vector_count;
     // counters' sums: for each power of two (and sign), the largest values first
     double block_weight[64];
     uint32_t block_count[64];
-    double steps[32][3];   // weights 1, 2, 3 magnitudes behind one, for each power of two
+    double steps[32][4];   // weights 0, 1, 2, 3 magnitudes behind one, to its own, for each power of two
+    double part_count[4], part_weight[4];
     // a cut found among them
     uint32_t cut_key, cut_above, cut_equal;
     double cut_weight_above, cut_weight, cut_need;
+    double log_min_p;
+    // of up to 128 candidates: their places among the others
+    uint32_t rank[128];
+    uint64_t before[128];
 };
 
 // Moves a value within a wave: lanes without a source get 0.
@@ -203,28 +230,12 @@ __device__ __forceinline__ double prefix64(double x) {
     return __builtin_bit_cast(double, prefix64<SumReal>(__builtin_bit_cast(uint64_t, x)));
 }
 
-// Orders LDS accesses of WAVES waves: all of the workgroup, or one for itself.
-template <int WAVES> __device__ __forceinline__ void team_sync() {
-    if (WAVES == kSampleWaves) {
-        __syncthreads();
-    } else {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    }
-}
-
-// Over WAVES waves (all of the workgroup, or the one that is left of it): the sum
-// of the threads before (with BEFORE), and of all.
-template <int WAVES, class Op = Sum, bool BEFORE = false>
+// Over the workgroup: the sum of the threads before (with BEFORE), and of all.
+template <class Op = Sum, bool BEFORE = false>
 __device__ __forceinline__ uint64_t reduce(SampleShared& s, uint64_t x, uint64_t* before = nullptr) {
-    static_assert(WAVES == 1 || WAVES == 16, "a row of lanes adds up the waves");
+    static_assert(kSampleWaves == 16, "a row of lanes adds up the waves");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x & 63;
     const uint64_t sums = prefix64<Op>(x);
-    if (WAVES == 1) {
-        if (BEFORE) *before = sums - x;
-        return lane_value(sums, 63);
-    }
     __syncthreads();
     if (lane == 63) s.wave[wave] = sums;
     __syncthreads();
@@ -235,13 +246,13 @@ __device__ __forceinline__ uint64_t reduce(SampleShared& s, uint64_t x, uint64_t
 
 // The bin of 64 PER that takes the running sum from the first one to `need`
 // or more, and the sum below it; by one wave, for all after a barrier.
-template <int WAVES, int PER> __device__ __forceinline__ void find_bin(SampleShared& s, uint64_t need) {
-    team_sync<WAVES>();
+template <int PER, class F> __device__ __forceinline__ void find_bin(SampleShared& s, uint64_t need, F&& bin_at) {
+    __syncthreads();
     if (threadIdx.x < 64) {
         uint64_t x[PER], sum = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            x[i] = s.bins[PER * threadIdx.x + i];
+            x[i] = s.bins[bin_at(threadIdx.x, i)];
             sum += x[i];
         }
         uint64_t before = prefix64(sum) - sum;
@@ -258,7 +269,7 @@ template <int WAVES, int PER> __device__ __forceinline__ void find_bin(SampleSha
             s.below = before;
         }
     }
-    team_sync<WAVES>();
+    __syncthreads();
 }
 
 __device__ __forceinline__ void add_to_bin(SampleShared& s, uint32_t bin, uint64_t amount) {
@@ -268,26 +279,28 @@ __device__ __forceinline__ void add_to_bin(SampleShared& s, uint32_t bin, uint64
 // The smallest D below 2^bits with a sum of amounts of d <= D of `need` or more
 // (which all d reach), digit by digit; `below`: the sum of the smaller ones.
 // source(f) calls f(d, amount) for the thread's elements.
-template <int WAVES, class S>
+template <class S>
 __device__ __forceinline__ uint32_t select(SampleShared& s, int bits, uint64_t need, uint64_t& below, S&& source) {
-    uint32_t value = 0;
+    static_assert(kDigit == 9 && kSampleThreads >= 2 << kDigit, "two sets of bins, cleared by a thread each");
+    uint32_t value = 0, set = 0;   // the other set is cleared under a digit's search
     below = 0;
+    __syncthreads();
+    s.bins[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll 1
     for (int high = bits, low; high > 0; high = low) {
         low = max(high - kDigit, 0);
-        team_sync<WAVES>();
-#pragma unroll
-        for (int i = 0; i < 1 << kDigit; i += 64 * WAVES)
-            if (WAVES == 1 || threadIdx.x < 1 << kDigit) s.bins[threadIdx.x + i] = 0;
-        team_sync<WAVES>();
         const bool first = high == bits;
         source([&](uint32_t d, uint64_t amount) {
-            const uint32_t digit = d >> low;
-            if ((first || (digit ^ (value >> low)) >> (high - low) == 0) && amount)
-                add_to_bin(s, digit & ((1u << (high - low)) - 1), amount);
+            const uint32_t digit = d >> low, bin = digit & ((1u << (high - low)) - 1);
+            // a lane's 8 neighbours lie 64 apart: no bank conflicts
+            if ((first || (digit ^ (value >> low)) >> (high - low) == 0) && amount) add_to_bin(s, set + ((bin & 7) << 6 | bin >> 3), amount);
         });
-        find_bin<WAVES, (1 << kDigit) / 64>(s, need - below);
+        find_bin<8>(s, need - below, [&](int lane, int i) { return (int)set + 64 * i + lane; });
         value |= s.bin << low;
         below += s.below;
+        if (threadIdx.x < 1 << kDigit) s.bins[set + threadIdx.x] = 0;
+        set ^= 1 << kDigit;
     }
     return value;
 }
@@ -296,21 +309,40 @@ template <class T> __device__ __forceinline__ int head_elements(const T* row, in
     return min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (int)sizeof(T));
 }
 
-// each(vector, index) for the thread's vectors of the row, AHEAD loaded at a time,
-// and one(value, index) for the ends of the row, fewer than a vector each.
-template <class T, int AHEAD, class F, class G>
+// each(vector, index, in) for the thread's vectors of the row, AHEAD in flight (in:
+// whether it has one, all lanes of a wave together), and one(value, index) for the
+// ends of the row, fewer than a vector each.  Later looks at a row go BACK, from what
+// the last one left in the L2.
+template <class T, int AHEAD, bool BACK, class F, class G>
 __device__ __forceinline__ void for_vectors(const T* row, int vocab, F&& each, G&& one) {
     typedef typename Logit<T>::vec vec;
     constexpr int VEC = Logit<T>::VEC;
     const int t = threadIdx.x, head = head_elements(row, vocab), vecs = (vocab - head) / VEC, tail = head + vecs * VEC;
     const EXQ_GLOBAL vec* body = gptr<vec>(row + head);
-    for (int j = t; j < vecs; j += AHEAD * kSampleThreads) {
+    const int rounds = (vecs + kSampleThreads - 1) / kSampleThreads;
+    const auto place = [&](int round) { return t + (BACK ? rounds - 1 - round : round) * kSampleThreads; };
+    const auto load = [&](int round) { return round < rounds && place(round) < vecs ? body[place(round)] : vec{}; };
+    if constexpr (AHEAD > 4) {   // a small body: unrolled
+        for (int round = 0; round < rounds; round += AHEAD) {
+            vec x[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) x[i] = load(round + i);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (round + i < rounds) each(x[i], head + place(round + i) * VEC, place(round + i) < vecs);
+        }
+    } else {   // a large one: there once
         vec x[AHEAD];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) x[i] = j + i * kSampleThreads < vecs ? body[j + i * kSampleThreads] : vec{};
+        for (int i = 0; i < AHEAD; ++i) x[i] = load(i);
+#pragma unroll 1
+        for (int round = 0; round < rounds; ++round) {
+            const vec now = x[0];
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (j + i * kSampleThreads < vecs) each(x[i], head + (j + i * kSampleThreads) * VEC);
+            for (int i = 0; i + 1 < AHEAD; ++i) x[i] = x[i + 1];
+            x[AHEAD - 1] = load(round + AHEAD);
+            each(now, head + place(round) * VEC, place(round) < vecs);
+        }
     }
     const int ends = head + vocab - tail;
     if (t < ends) {
@@ -319,48 +351,54 @@ __device__ __forceinline__ void for_vectors(const T* row, int vocab, F&& each, G
     }
 }
 
-// f(index, value) for the thread's elements of the row.
-template <class T, int AHEAD, class F> __device__ __forceinline__ void for_row(const T* row, int vocab, F&& f) {
-    for_vectors<T, AHEAD>(row, vocab, [&](const typename Logit<T>::vec& x, int i) {
-#pragma unroll
-        for (int e = 0; e < Logit<T>::VEC; ++e) f(i + e, x[e]);
-    }, [&](T x, int i) { f(i, x); });
+// f(value, index) for a vector's elements, the body there once or twice.
+template <class F> __device__ __forceinline__ void for_elements(const f4& x, int i, F&& f) {
+    f4 y = x;
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+        f(y[0], i + e);
+        y = __builtin_shufflevector(y, y, 1, 2, 3, 0);
+    }
+}
+template <class F> __device__ __forceinline__ void for_elements(const h8& x, int i, F&& f) {
+    u4v y = __builtin_bit_cast(u4v, x);
+#pragma unroll 1
+    for (int e = 0; e < 8; e += 2) {
+        const uint32_t pair = y[0];
+        const h2 z = as_h2(pair);
+        f(z[0], i + e);
+        f(z[1], i + e + 1);
+        y = __builtin_shufflevector(y, y, 1, 2, 3, 0);
+    }
+}
+
+// f(value, index) for the thread's elements of the row.
+template <class T, int AHEAD, bool BACK, class F> __device__ __forceinline__ void for_row(const T* row, int vocab, F&& f) {
+    for_vectors<T, AHEAD, BACK>(row, vocab, [&](const typename Logit<T>::vec& x, int i, bool in) {
+        if (in) for_elements(x, i, f);
+    }, [&](T x, int i) { f(x, i); });
 }
 
 // What the filters left: keys above `key`, and of those with it the first `quota`.
 struct Cut {
     uint32_t key, quota;
 };
+// And keys from `least` on.  (The key below 0's would be -0's, which has none.)
+template <class T> __device__ __forceinline__ Cut with_least(Cut cut, uint32_t least) {
+    constexpr uint32_t zero = 1u << (Logit<T>::BITS - 1);
+    return least > cut.key ? Cut{least - 1 - (least == zero), 0} : cut;
+}
 
 // ------------------------------------------------------- counters of fp16 keys
 
-// Counts a row and returns the thread's largest logit.
-__device__ __forceinline__ float count_row(SampleShared& s, const _Float16* row, int vocab) {
+__device__ __forceinline__ void clear_counters(SampleShared& s) {
     u4v* zero = reinterpret_cast<u4v*>(s.counts);
 #pragma unroll
     for (int i = 0; i < kCounters / 4; i += kSampleThreads) zero[threadIdx.x + i] = u4v{0, 0, 0, 0};
     __syncthreads();
-    const _Float16 lowest = -(_Float16)__builtin_huge_valf();
-    h8 most = {lowest, lowest, lowest, lowest, lowest, lowest, lowest, lowest};
-    const auto count = [&](uint32_t bits) {   // of the lower half
-        atomicAdd(&s.counts[bits & 0x7FFFu], bits & 0x8000u ? 0x10000u : 1u);
-    };
-    for_vectors<_Float16, 8>(row, vocab, [&](const h8& x, int) {
-        most = __builtin_elementwise_max(most, x);
-        const u4v bits = __builtin_bit_cast(u4v, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            count(bits[i]);
-            count(bits[i] >> 16);
-        }
-    }, [&](_Float16 x, int) {
-        most[0] = __builtin_elementwise_max(most[0], x);
-        count(__builtin_bit_cast(uint16_t, x));
-    });
-    float top = (float)most[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, (float)most[i]);
-    return top;
+}
+__device__ __forceinline__ void count(SampleShared& s, uint32_t bits) {   // of the lower half
+    atomicAdd(&s.counts[bits & 0x7FFFu], bits & 0x8000u ? 0x10000u : 1u);
 }
 
 // Four neighbouring magnitudes of one sign, from the largest logit to the smallest.
@@ -369,11 +407,8 @@ struct Four {
     double w[4];
 };
 
-// The lane's of 256: magnitudes of power of two `block`, part `part` of 4.  Largest
-// logits come first: with positive ones the upper lanes' magnitudes in turn.
-template <bool NEGATIVE> __device__ __forceinline__ Four four_of(const SampleShared& s, int block, int part) {
-    const int lane = threadIdx.x & 63, m0 = 1024 * block + 256 * (NEGATIVE ? part : 3 - part) + 4 * (NEGATIVE ? lane : 63 - lane);
-    const u4v c = *reinterpret_cast<const u4v*>(&s.counts[m0]);
+// From the counters `c` of magnitudes m0 .. m0 + 3.
+template <bool NEGATIVE> __device__ __forceinline__ Four four_from(const u4v& c, uint32_t m0) {
     Four x;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -388,29 +423,38 @@ template <bool NEGATIVE> __device__ __forceinline__ Four four_of(const SampleSha
     return x;
 }
 
+// The lane's of 256 magnitudes, part `part` of 4 of power of two `block`, the
+// largest logits in the first lanes.
+__device__ __forceinline__ Four four_of(const SampleShared& s, bool negative, int block, int part) {
+    const int lane = threadIdx.x & 63, m0 = 1024 * block + 256 * (negative ? part : 3 - part) + 4 * (negative ? lane : 63 - lane);
+    const u4v c = *reinterpret_cast<const u4v*>(&s.counts[m0]);
+    return negative ? four_from<true>(c, m0) : four_from<false>(c, m0);
+}
+
 // Their weights, and what the counted ones add up to.  Neighbours' weights have
 // one ratio within a power of two.
 __device__ __forceinline__ double weigh(const SampleShared& s, const Weights& w, uint32_t top_key, int block, Four& x) {
     x.w[0] = x.w[1] = x.w[2] = x.w[3] = 0;
     if (x.all == 0) return 0.0;
-    if (x.key[0] <= top_key) {
-        x.w[0] = w.real(Logit<_Float16>::value(x.key[0]));
+    // (the first ones may lie above the largest logit, uncounted)
+    const uint32_t first = std::min(x.key[0], top_key);
+    const int skip = (int)(x.key[0] - first);
+    const double base = w.real(Logit<_Float16>::value(first));
+    double sum = 0;
 #pragma unroll
-        for (int e = 1; e < 4; ++e) x.w[e] = x.w[0] * s.steps[block][e - 1];
-    } else {   // some, not counted, lie above the largest logit
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (x.key[e] <= top_key) x.w[e] = w.real(Logit<_Float16>::value(x.key[e]));
+    for (int e = 0; e < 4; ++e) {
+        x.w[e] = x.n[e] ? base * s.steps[block][max(e - skip, 0)] : 0.0;
+        sum = __builtin_fma((double)x.n[e], x.w[e], sum);
     }
-    return __builtin_fma(x.n[3], x.w[3], __builtin_fma(x.n[2], x.w[2], __builtin_fma(x.n[1], x.w[1], x.n[0] * x.w[0])));
+    return sum;
 }
 
 // Adds the counters up by power of two and sign, their weights too if asked for.
 // The number of logits that may be drawn; -1: a counter overflowed (65536 equal ones).
 __device__ __forceinline__ int sum_counters(SampleShared& s, const Weights& w, uint32_t top_key, bool weights, int vocab) {
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64), lane = t & 63;
-    if (weights && t < 32 * 3)   // neighbours of a power of two lie 2^(block - 25) apart
-        s.steps[t / 3][t % 3] = w.power(-(1 + t % 3) * __builtin_ldexp(w.c, max(t / 3, 1) - 25));
+    if (weights && t < 32 * 4)   // neighbours of a power of two lie 2^(block - 25) apart
+        s.steps[t / 4][t % 4] = w.power(-(t % 4) * __builtin_ldexp(w.c, max(t / 4, 1) - 25));
     __syncthreads();
     uint64_t all = 0;
 #pragma unroll 1
@@ -419,93 +463,101 @@ __device__ __forceinline__ int sum_counters(SampleShared& s, const Weights& w, u
         double sum[2] = {0, 0};
 #pragma unroll 1
         for (int part = 0; part < 4; ++part) {
-            Four x = four_of<false>(s, block, part);
+            const uint32_t m0 = 1024 * block + 256 * part + 4 * lane;
+            const u4v c = *reinterpret_cast<const u4v*>(&s.counts[m0]);
+            if (__ballot((c[0] | c[1] | c[2] | c[3]) != 0) == 0) continue;
+            Four x = four_from<false>(c, m0);
             n[0] += x.all;
             if (weights) sum[0] += weigh(s, w, top_key, block, x);
-            x = four_of<true>(s, block, part);
+            x = four_from<true>(c, m0);
             n[1] += x.all;
             if (weights) sum[1] += weigh(s, w, top_key, block, x);
         }
+        const uint64_t both = prefix64((uint64_t)n[1] << 32 | n[0]);
         all += n[0] + n[1];
-#pragma unroll
-        for (int sign = 0; sign < 2; ++sign) {
-            const uint32_t count = (uint32_t)prefix64((uint64_t)n[sign]);
-            const double weight = weights ? prefix64(sum[sign]) : 0.0;
-            if (lane == 63) {
-                s.block_count[sign ? 32 + block : 31 - block] = count;
-                s.block_weight[sign ? 32 + block : 31 - block] = weight;
-            }
+        const double up = weights ? prefix64(sum[0]) : 0.0, down = weights ? prefix64(sum[1]) : 0.0;
+        if (lane == 63) {
+            s.block_count[31 - block] = (uint32_t)both;
+            s.block_count[32 + block] = (uint32_t)(both >> 32);
+            s.block_weight[31 - block] = up;
+            s.block_weight[32 + block] = down;
         }
     }
     // -infinity and NaN were not counted above
     uint64_t rest = 0;
     for (int m = 0x7C00 + t; m < kCounters; m += kSampleThreads) rest += (s.counts[m] >> 16) + (m > 0x7C00 ? s.counts[m] & 0xFFFFu : 0);
-    const uint64_t both = reduce<kSampleWaves>(s, all | rest << 32);
+    const uint64_t both = reduce(s, all | rest << 32);
     return (both & 0xFFFFFFFFu) + (both >> 32) == (uint64_t)vocab ? (int)(uint32_t)both : -1;
 }
 
 // Where the running sum of counts, or weights, reaches `need` (with `share`: that
-// share of all weights): into s.cut_*.
+// share of all weights): into s.cut_*.  Four waves take a part each of the power of
+// two that holds it.
 __device__ __forceinline__ void find_key(SampleShared& s, const Weights& w, uint32_t top_key, bool counts, double need, bool weights,
                                          bool share) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const auto at_lane = [](double x, int i) { return __builtin_bit_cast(double, lane_value(__builtin_bit_cast(uint64_t, x), i)); };
+    double n_before = 0, w_before = 0, here = 0, here_w = 0, here_to = 0, here_w_to = 0;
+    Four x{};
     __syncthreads();
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        const auto at_lane = [](double x, int i) { return __builtin_bit_cast(double, lane_value(__builtin_bit_cast(uint64_t, x), i)); };
+    if (wave < 4) {
         const double n = s.block_count[lane], weight = s.block_weight[lane];
         const double n_to = prefix64(n), w_to = prefix64(weight);
         if (share) need *= at_lane(w_to, 63);
         // (the last block that holds anything, if rounding kept the sum below)
         const uint64_t reach = __ballot((counts ? n_to : w_to) >= need && n > 0), any = __ballot(n > 0);
         const int at = reach ? __builtin_ctzll(reach) : 63 - __builtin_clzll(any);
-        double n_before = at_lane(n_to - n, at), w_before = at_lane(w_to - weight, at);
+        n_before = at_lane(n_to - n, at);
+        w_before = at_lane(w_to - weight, at);
         const int block = at >= 32 ? at - 32 : 31 - at;
-#pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
-            Four x = at >= 32 ? four_of<true>(s, block, part) : four_of<false>(s, block, part);
-            const double here = x.all, here_w = weights ? weigh(s, w, top_key, block, x) : 0.0;
-            const double here_to = prefix64(here), here_w_to = prefix64(here_w);
-            const uint64_t some = __ballot(x.all != 0);
-            const uint64_t found = __ballot(x.all != 0 && (counts ? n_before + here_to : w_before + here_w_to) >= need);
-            // the lane that reaches it; so far, the last one that holds anything
-            if (some && lane == (found ? __builtin_ctzll(found) : 63 - __builtin_clzll(some))) {
-                double nb = n_before + (here_to - here), wb = w_before + (here_w_to - here_w);
-                bool done = false;
+        x = four_of(s, at >= 32, block, wave);
+        here = x.all;
+        here_w = weights ? weigh(s, w, top_key, block, x) : 0.0;
+        here_to = prefix64(here);
+        here_w_to = prefix64(here_w);
+        if (lane == 63) {
+            s.part_count[wave] = here_to;
+            s.part_weight[wave] = here_w_to;
+        }
+    }
+    __syncthreads();
+    if (wave < 4) {
+        double n = n_before, weight = w_before;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (!x.n[e] || done) continue;
-                    s.cut_key = x.key[e];
-                    s.cut_above = (uint32_t)nb;
-                    s.cut_equal = x.n[e];
-                    s.cut_weight_above = wb;
-                    s.cut_weight = weights ? x.w[e] : 0.0;
-                    nb += x.n[e];
-                    if (weights) wb += x.n[e] * x.w[e];
-                    done = (counts ? nb : wb) >= need;
-                }
+        for (int part = 0; part < 4; ++part) {
+            if (part == wave) {
+                n_before = n;
+                w_before = weight;
             }
-            if (lane == 0) s.cut_need = need;
-            if (found) break;
-            n_before += at_lane(here_to, 63);
-            w_before += at_lane(here_w_to, 63);
+            n += s.part_count[part];
+            weight += s.part_weight[part];
+        }
+        if (wave == 0 && lane == 0) s.cut_need = need;
+        need = __builtin_fmin(need, counts ? n : weight);
+        const double from = counts ? n_before : w_before, own = counts ? here_to : here_w_to;
+        // the first part, and its first lane, that reach it and hold something
+        const uint64_t found = __ballot(x.all != 0 && from + own >= need);
+        if (from < need && found && lane == __builtin_ctzll(found)) {
+            double nb = n_before + (here_to - here), wb = w_before + (here_w_to - here_w);
+            bool done = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!x.n[e] || done) continue;
+                s.cut_key = x.key[e];
+                s.cut_above = (uint32_t)nb;
+                s.cut_equal = x.n[e];
+                s.cut_weight_above = wb;
+                s.cut_weight = weights ? x.w[e] : 0.0;
+                nb += x.n[e];
+                if (weights) wb += x.n[e] * x.w[e];
+                done = (counts ? nb : wb) >= need;
+            }
         }
     }
     __syncthreads();
 }
 
 // ---------------------------------------------------------------- candidates
-
-// What ends a row on its list of `count` candidates, by WAVES waves.
-struct Finish {
-    int count, vocab;
-    uint32_t top_key;
-    int key_bits, index_bits;
-    int top_k;           // 0: done
-    float top_p;         // 1 or more: done
-    uint64_t share;      // what top-p needs, if it is of more than the list; else 0
-    Cut cut;
-    float u, temperature;
-};
 
 __device__ __forceinline__ uint64_t share_of(float top_p, uint64_t total) {   // what top-p needs of it
     return std::min<uint64_t>(std::max<uint64_t>((uint64_t)__builtin_ceil((double)top_p * (double)total), 1), total);
@@ -514,77 +566,127 @@ __device__ __forceinline__ uint64_t target_of(float u, uint64_t total) {
     return std::min<uint64_t>((uint64_t)((double)u * (double)total), total - 1);
 }
 
-template <class T, int WAVES, class A>
-__device__ __forceinline__ void finish(SampleShared& s, const Weights& w, Finish f, A&& answer) {
+// What is known of a row, and what is left to do on its list of candidates.
+struct Row {
+    int count;           // of candidates
+    int vocab;
+    uint32_t top_key;
+    int key_bits;        // candidates' keys lie within 2^key_bits of the top
+    int top_k;           // 0: done
+    float top_p;         // 1 or more: done
+    uint64_t share;      // what top-p needs, if that is known; else 0
+    Cut cut;
+    uint32_t least;      // the smallest key that min-p leaves
+    float u, temperature;
+};
+
+// Up to 128 candidates: every one is compared with every other, by all threads.
+template <class T, class A>
+__device__ __forceinline__ void finish_few(SampleShared& s, const Weights& w, const Row& f, A&& answer) {
     typedef Logit<T> L;
-    constexpr int N = 64 * WAVES;
-    uint32_t keys[kSampleEach], at[kSampleEach];
-    uint64_t ws[kSampleEach];
-#pragma unroll
-    for (int i = 0; i < kSampleEach; ++i) {
-        keys[i] = at[i] = 0;
-        ws[i] = 0;
-        if ((int)threadIdx.x + i * N < f.count) {
-            const uint64_t x = s.list[threadIdx.x + i * N];
-            keys[i] = (uint32_t)(x >> 32);
-            at[i] = (uint32_t)x;
-            ws[i] = w.of(L::value(keys[i]));
-        }
+    const int t = threadIdx.x, n = f.count <= 64 ? 64 : 128, i = t & (n - 1), group = t / n, per = n * n / kSampleThreads;
+    const uint64_t x = i < f.count ? s.list[i] : 0;
+    const uint32_t key = (uint32_t)(x >> 32), index = (uint32_t)x;
+    const uint64_t weight = key ? w.of(L::value(key)) : 0;
+    if (t < n) {
+        s.weights[t] = weight;
+        s.rank[t] = 0;
+        s.before[t] = 0;
     }
+    __syncthreads();
+    // those before it in the filters' order, their number and weights, and those of its key
+    const int first_j = group * per, last_j = std::min(f.count, first_j + per);
+    uint32_t rank = 0;
+    uint64_t before = 0;
+#pragma unroll 1
+    for (int j = first_j; j < last_j; ++j) {
+        const uint64_t y = s.list[j];
+        const uint32_t k = (uint32_t)(y >> 32);
+        const bool tie = k == key && (uint32_t)y < index;
+        rank += (k > key || tie ? 1 : 0) + (tie ? 0x10000 : 0);
+        before += k > key || tie ? s.weights[j] : 0;
+    }
+    if (rank) atomicAdd(&s.rank[i], rank);
+    if (before) atomicAdd(reinterpret_cast<unsigned long long*>(&s.before[i]), (unsigned long long)before);
+    __syncthreads();
+    rank = s.rank[i] & 0xFFFFu;
+    before = s.before[i];
+    bool in = key && (key > f.cut.key || (key == f.cut.key && s.rank[i] >> 16 < f.cut.quota));
+    if (f.top_k) in = in && rank < (uint32_t)f.top_k;
+    if (f.top_p < 1.0f) {
+        const uint64_t need = f.share ? f.share : share_of(f.top_p, reduce(s, in && t < n ? weight : 0));
+        in = in && before < need;
+    }
+    in = in && key >= f.least;
+    const uint64_t mine = in ? weight : 0, sum = reduce(s, t < n ? mine : 0), target = target_of(f.u, sum);
+    if (t < n) {
+        s.weights[t] = mine;
+        s.before[t] = 0;
+    }
+    __syncthreads();
+    uint64_t lower = 0;   // of those left, with lower indices
+#pragma unroll 1
+    for (int j = first_j; j < last_j; ++j) lower += (uint32_t)s.list[j] < index ? s.weights[j] : 0;
+    if (lower) atomicAdd(reinterpret_cast<unsigned long long*>(&s.before[i]), (unsigned long long)lower);
+    __syncthreads();
+    lower = s.before[i];
+    if (t < n && mine && lower <= target && target < lower + mine) answer((int)index, w.log_of(L::value(key), f.temperature, sum));
+}
+
+// The cut of a longer list, from the filters that are left to do.
+template <class T> __device__ __forceinline__ void filter_list(SampleShared& s, const Weights& w, Row& f) {
+    typedef Logit<T> L;
+    // a thread's own candidates, which no other looks at
     const auto each = [&](auto&& g) {
-#pragma unroll
-        for (int i = 0; i < kSampleEach; ++i)
-            if (i * N < f.count && keys[i]) g(keys[i], at[i], ws[i]);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < f.count; i += kSampleThreads) g((uint32_t)(s.list[i] >> 32), s.weights[i]);
     };
+    each([&](uint32_t k, uint64_t& x) { x = w.of(L::value(k)); });
     uint64_t below;
 #pragma unroll 1
     for (int filter = f.top_k ? 0 : 1; filter < (f.top_p < 1.0f ? 2 : 1); ++filter) {
         const bool counts = filter == 0;
         uint64_t all = 0;
-        each([&](uint32_t k, uint32_t, uint64_t x) { all += k < f.cut.key ? 0 : counts ? 1 : k > f.cut.key ? x : 0; });
-        all = reduce<WAVES>(s, all);
+        each([&](uint32_t k, uint64_t x) { all += k < f.cut.key ? 0 : counts ? 1 : k > f.cut.key ? x : 0; });
+        all = reduce(s, all);
         if (!counts && f.cut.key) all += f.cut.quota * w.of(L::value(f.cut.key));
         const uint64_t need = counts ? (uint64_t)f.top_k : f.share ? f.share : share_of(f.top_p, all);
         if (need >= all) continue;
-        const uint32_t key = f.top_key - select<WAVES>(s, f.key_bits, need, below, [&](auto&& g) {
-            each([&](uint32_t k, uint32_t, uint64_t x) {
+        const uint32_t key = f.top_key - select(s, f.key_bits, need, below, [&](auto&& g) {
+            each([&](uint32_t k, uint64_t x) {
                 if (k >= f.cut.key) g(f.top_key - k, counts ? 1 : x);
             });
         });
         const uint64_t one = counts ? 1 : w.of(L::value(key));
         f.cut = Cut{key, (uint32_t)((need - below + one - 1) / one)};
     }
-    // of those at the cut the first ones
-    uint32_t last = 0xFFFFFFFFu;
-    uint64_t equal = 0;
-    each([&](uint32_t k, uint32_t, uint64_t) { equal += k == f.cut.key; });
-    if (reduce<WAVES>(s, equal) > f.cut.quota)
-        last = select<WAVES>(s, f.index_bits, f.cut.quota, below, [&](auto&& g) {
-            each([&](uint32_t k, uint32_t i, uint64_t) {
-                if (k == f.cut.key) g(i, 1);
-            });
-        });
-    uint64_t sum = 0;
-    each([&](uint32_t k, uint32_t i, uint64_t& x) {
-        const bool in = k > f.cut.key || (k == f.cut.key && i <= last);
-        x = in ? w.kept(L::value(k)) : 0;
-        sum += x;
-    });
-    sum = reduce<WAVES>(s, sum);
-    // the draw: indices in ascending order
-    const uint32_t token = select<WAVES>(s, f.index_bits, target_of(f.u, sum) + 1, below, [&](auto&& g) {
-        each([&](uint32_t, uint32_t i, uint64_t x) { g(i, x); });
-    });
-    each([&](uint32_t k, uint32_t i, uint64_t) {
-        if (i == token) answer((int)token, w.log_of(L::value(k), f.temperature, sum));
-    });
 }
+
+// The row in tiles: its head, groups of 64 vectors (a wave's look), its tail.
+template <class T> struct Tiles {
+    int head, vecs, tail, vocab, groups, per, count;   // per: groups of a tile
+    __device__ Tiles(const T* row, int n) {
+        constexpr int VEC = Logit<T>::VEC;
+        vocab = n;
+        head = head_elements(row, n);
+        vecs = (n - head) / VEC;
+        tail = head + vecs * VEC;
+        groups = (vecs + 63) / 64;
+        per = groups <= kSampleTiles - 2 ? 1 : (groups + kSampleTiles - 3) / (kSampleTiles - 2);
+        count = 2 + (groups + per - 1) / per;
+    }
+    __device__ int of(int i) const {   // of index i
+        if (i < head) return 0;
+        return i >= tail ? count - 1 : 1 + (i - head) / (64 * Logit<T>::VEC) / per;
+    }
+};
 
 // -------------------------------------------------------------------- kernel
 
 template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
     __shared__ SampleShared s;
     typedef Logit<T> L;
+    typedef typename L::vec vec;
     const int t = threadIdx.x, r = blockIdx.x, lane = t % 64;
     const float u = a.u[r];
     if (u < 0.0f) return;
@@ -601,68 +703,154 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
     }
     const bool first_only = temperature == 0.0f || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
+    const bool near = by_k && top_k <= kSampleNear;   // top-k from the threads' largest logits
+    bool counted = L::COUNTED && !first_only && !near && (by_k || by_p);
     if (t < kPowers) s.powers[t] = exp2_series((double)t / kPowers);
     if (t == 0) s.bin = s.below = 0;
+    if (t == kPowers && min_p > 0.0f) s.log_min_p = log((double)min_p);
+    if (counted) clear_counters(s);
 
-    // the largest logit
-    bool counted = L::COUNTED && !first_only && (by_k || by_p);
-    uint64_t best = 0;
-    uint32_t mine = 0;   // the thread's own
-    if constexpr (L::COUNTED) {
-        if (counted) best = (uint64_t)L::key((_Float16)count_row(s, row, a.vocab)) << 32;
-    }
-    if (!counted) {   // and its lowest index
-        for_row<T, 4>(row, a.vocab, [&](int i, T x) {
-            const uint64_t it = (uint64_t)L::key(x) << 32 | (uint32_t)~i;
-            if (it >> 32) best = std::max(best, it);
-        });
-        mine = (uint32_t)(best >> 32);
-    }
-    best = reduce<kSampleWaves, Larger>(s, best);
+    // the largest logit, in which vector it comes first
+    float mine = -__builtin_huge_valf();   // the thread's
+    int mine_at = 0;
+    const auto look = [&](float x, int i) {
+        if (x > mine) {
+            mine = x;
+            mine_at = i;
+        }
+    };
+    for_vectors<T, 6, false>(row, a.vocab, [&](const vec& x, int i, bool in) {
+        if (!in) return;
+        look(L::largest(x), i);
+        if constexpr (L::COUNTED) {
+            if (counted) {
+                const u4v bits = __builtin_bit_cast(u4v, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    count(s, bits[e]);
+                    count(s, bits[e] >> 16);
+                }
+            }
+        }
+    }, [&](T x, int i) {
+        look((float)x, i);
+        if constexpr (L::COUNTED) {
+            if (counted) count(s, __builtin_bit_cast(uint16_t, x));
+        }
+    });
+    const uint32_t mine_key = L::key((T)mine);
+    const uint64_t best = reduce<Larger>(s, mine_key ? (uint64_t)mine_key << 32 | (uint32_t)~mine_at : 0);
     if (best == 0) {   // nothing that may be drawn
         if (t == 0) answer(-1, __builtin_nanf(""));
         return;
     }
+    const uint32_t top_key = (uint32_t)(best >> 32);
     if (first_only) {
-        if (t == 0) answer((int)~(uint32_t)best, 0.0f);
+        const int i = (int)~(uint32_t)best + t;
+        if (t < 64) {
+            const uint64_t is = __ballot(t < L::VEC && i < a.vocab && L::key(row[min(i, a.vocab - 1)]) == top_key);
+            if (t == 0) answer(i + __builtin_ctzll(is), 0.0f);
+        }
         return;
     }
-    const uint32_t top_key = (uint32_t)(best >> 32);
     const float topf = L::value(top_key), finite_top = __builtin_fminf(topf, __FLT_MAX__);
     const Weights w{topf, (double)finite_top, topf > __FLT_MAX__ ? 1e300 : kPowers * 1.4426950408889634074 / (double)temperature,
-                    (double)(1ull << a.shift), min_p, s.powers};
-    Finish f{0, a.vocab, top_key, L::BITS, a.vocab > 1 << 2 * kDigit ? kSampleMaxVocabLog2 : 2 * kDigit, 0, 1.0f, 0,
-             Cut{0, 0xFFFFFFFFu}, u, temperature};
+                    (double)(1ull << a.shift), s.powers};
+    Row f{0, a.vocab, top_key, L::BITS, 0, 1.0f, 0, Cut{0, 0xFFFFFFFFu}, 0, u, temperature};
+    if (min_p > 0.0f) {   // w >= min-p where the logit is M + T ln(min-p) or more
+        const double least = min_p == 1.0f ? (double)topf : (double)topf + (double)temperature * s.log_min_p;
+        f.least = L::first_from(least);
+    }
 
-    // Elements that want(key, value) asks for, into the list.
-    const auto collect = [&](auto&& want) {
+    // Elements that want(value) asks for, which no NaN or -infinity passes, into the
+    // list: first the vectors that hold one (any(vector) tells, or may), then their elements.
+    const auto collect = [&](auto&& any, auto&& want) __attribute__((always_inline)) {
         __syncthreads();
-        if (t == 0) s.count = 0;
+        if (t == 0) s.count = s.vector_count = 0;
         __syncthreads();
-        for_row<T, 4>(row, a.vocab, [&](int i, T x) {
-            const uint32_t k = L::key(x);
-            if (k && want(k, x)) {
-                const uint32_t at = atomicAdd(&s.count, 1u);
-                if (at < kSampleList) s.list[at] = (uint64_t)k << 32 | (uint32_t)i;
+        // places for all of a wave's at once
+        const auto places = [&](uint32_t* counter) {
+            const uint64_t all = __ballot(true);
+            const uint32_t before = __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+            uint32_t at = 0;
+            if (before == 0) at = atomicAdd(counter, (uint32_t)__builtin_popcountll(all));
+            return __builtin_amdgcn_readfirstlane(at) + before;
+        };
+        const auto put = [&](T x, int i) {
+            const uint32_t at = places(&s.count);
+            if (at < kSampleList) s.list[at] = (uint64_t)L::key(x) << 32 | (uint32_t)i;
+        };
+        for_vectors<T, 6, true>(row, a.vocab, [&](const vec& x, int i, bool in) {
+            if (in && any(x)) {
+                const uint32_t at = places(&s.vector_count);
+                if (at < kSampleList) s.vectors[at] = (uint32_t)i;
             }
+        }, [&](T x, int i) {
+            if (want(x)) put(x, i);
         });
+        __syncthreads();
+        const int n = (int)std::min<uint32_t>(s.vector_count, 0x7FFFFFFFu);
+        if (n > kSampleList) return n;
+#pragma unroll 1
+        for (int j = t; j < n; j += kSampleThreads) {
+            const int i = (int)s.vectors[j];
+            const vec x = *gptr<vec>(row + i);
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < L::VEC; ++e) hits |= want(x[e]) ? 1u << e : 0;
+            while (hits) {
+                const int e = __builtin_ctz(hits);
+                put(L::at(x, e), i + e);
+                hits &= hits - 1;
+            }
+        }
         __syncthreads();
         return (int)std::min<uint32_t>(s.count, 0x7FFFFFFFu);
     };
+    const T nothing = (T)-__builtin_huge_valf();
+    const auto collect_from = [&](uint32_t key) __attribute__((always_inline)) {   // 0: all
+        const T from = key ? (T)L::value(key) : nothing;
+        return collect([&](const vec& x) { return key ? L::largest(x) >= (float)from : L::largest(x) > (float)from; },
+                       [&](T x) { return key ? x >= from : x > from; });
+    };
 
+    bool held = false;   // whether the list holds all that the filters can leave
     if (by_k || by_p) {
-        bool held = false;   // whether the list holds all that the filters can leave
+        if (near) {
+            // a threshold that top_k threads' largest logits reach, to 1/64 of a power of two
+            const auto coarse = [&](uint32_t k) { return min((top_key >> L::COARSE) - (k >> L::COARSE), (1u << kDigit) - 1); };
+            const uint64_t want = std::min<uint64_t>(top_k, reduce(s, mine_key ? 1 : 0));
+            uint64_t below;
+            const uint32_t least = select(s, kDigit, want, below, [&](auto&& g) {
+                if (mine_key) g(coarse(mine_key), 1);
+            });
+            const bool any = least == (1u << kDigit) - 1;
+            f.count = collect_from(any ? 0 : ((top_key >> L::COARSE) - least) << L::COARSE);
+            held = f.count <= kSampleList && (any || f.count >= top_k);
+            f.top_k = top_k;
+            f.top_p = top_p;
+            if (!any) f.key_bits = L::COARSE + kDigit;
+        }
         if constexpr (L::COUNTED) {
-            const int some = counted ? sum_counters(s, w, top_key, by_p, a.vocab) : -1;
-            counted = some >= 0;
-            if (counted) {
-                uint32_t kept = 0;   // at the cut or above
+            // With top-k, top-p is left to the list if that can hold what top-k leaves.
+            bool weights = by_p && !(by_k && top_k <= kSampleList / 2);
+            uint32_t kept = 0;   // at the cut or above
+#pragma unroll 1
+            while (counted) {
+                const int some = sum_counters(s, w, top_key, weights, a.vocab);
+                counted = some >= 0;
+                if (!counted) break;
+                kept = (uint32_t)some;
                 if (by_k && some > top_k) {
-                    find_key(s, w, top_key, true, (double)top_k, by_p, false);
+                    find_key(s, w, top_key, true, (double)top_k, weights, false);
                     f.cut = Cut{s.cut_key, (uint32_t)top_k - s.cut_above};
                     kept = s.cut_above + s.cut_equal;
                 }
-                if (by_p) {
+                if (weights || !by_p || kept <= kSampleList) break;
+                weights = true;
+            }
+            if (counted) {
+                if (weights) {
                     const bool cut = f.cut.key != 0;
                     find_key(s, w, top_key, false, (double)top_p * (cut ? s.cut_weight_above + f.cut.quota * s.cut_weight : 1.0), true, !cut);
                     const double ties = __builtin_ceil((s.cut_need - s.cut_weight_above) / s.cut_weight);
@@ -671,32 +859,20 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
                     f.cut = Cut{s.cut_key, quota};
                     kept = s.cut_above + s.cut_equal;
                 }
-                if (f.cut.key && kept <= kSampleList) {
-                    f.count = collect([&](uint32_t k, T) { return k >= f.cut.key; });
+                if (kept <= kSampleList) {
+                    // (what top-p is a share of includes what min-p drops)
+                    const bool later = by_p && !weights;
+                    f.count = collect_from(later ? f.cut.key : std::max(f.cut.key, f.least));
+                    if (later) f.top_p = top_p;
                     held = true;
                 }
-            } else {   // an overflow: the threads' largest logits for what follows
-                for_row<T, 4>(row, a.vocab, [&](int, T x) { mine = std::max(mine, L::key(x)); });
             }
         }
-        if (!counted) {
-            uint64_t below;
-            if (by_k) {
-                // a threshold that top_k threads' largest logits reach, to 1/64 of a power of two
-                const auto coarse = [&](uint32_t k) { return min((top_key >> L::COARSE) - (k >> L::COARSE), (1u << kDigit) - 1); };
-                const uint64_t want = std::min<uint64_t>(top_k, reduce<kSampleWaves>(s, mine ? 1 : 0));
-                const uint32_t least = select<kSampleWaves>(s, kDigit, want, below, [&](auto&& g) {
-                    if (mine) g(coarse(mine), 1);
-                });
-                f.count = collect([&](uint32_t k, T) { return coarse(k) <= least; });
-                held = f.count <= kSampleList && f.count >= top_k;
-                f.top_k = top_k;
-                f.top_p = top_p;
-                // the keys lie that near the top, or anywhere from the last bin on
-                if (least < (1u << kDigit) - 1) f.key_bits = L::COARSE + kDigit;
-            }
+        if (!counted && !held) {
+            f.top_k = 0;
+            f.top_p = 1.0f;
 #pragma unroll 1
-            for (int filter = by_k ? 0 : 1; !held && filter < (by_p ? 2 : 1); ++filter) {
+            for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
                 const bool counts = filter == 0;
                 // 64 bins for one of the logits, or for a power of two of the weights
                 const float rate = counts ? 64.0f : __builtin_fminf((float)(w.c * (64.0 / kPowers)), 1e30f);
@@ -707,54 +883,58 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
                 __syncthreads();
                 for (int i = t; i < kSampleBins; i += kSampleThreads) s.bins[i] = 0;
                 __syncthreads();
-                for_row<T, 2>(row, a.vocab, [&](int, T x) {
-                    const uint32_t k = L::key(x);
-                    if (k && k >= f.cut.key) {
-                        const uint64_t amount = counts ? 1 : k > f.cut.key ? w.of((float)x) : 0;
+                const bool none = f.cut.key == 0;
+                const T cut = none ? nothing : (T)L::value(f.cut.key);
+                const auto left = [&](T x) { return none ? x > cut : x >= cut; };
+                for_row<T, 4, true>(row, a.vocab, [&](T x, int) {
+                    if (x > cut) {
+                        const uint64_t amount = counts ? 1 : w.of((float)x);
                         if (amount) add_to_bin(s, (uint32_t)bin_of((float)x), amount);
                     }
                 });
-                if (!counts && f.cut.key && t == 0) {
-                    const float l = L::value(f.cut.key);
-                    add_to_bin(s, (uint32_t)bin_of(l), f.cut.quota * w.of(l));
-                }
+                if (!counts && !none && t == 0) add_to_bin(s, (uint32_t)bin_of((float)cut), f.cut.quota * w.of((float)cut));
                 __syncthreads();
                 uint64_t all = 0;
                 for (int i = t; i < kSampleBins; i += kSampleThreads) all += s.bins[i];
-                all = reduce<kSampleWaves>(s, all);
+                all = reduce(s, all);
                 const uint64_t need = counts ? (uint64_t)top_k : share_of(top_p, all);
                 if (need >= all) continue;
-                find_bin<kSampleWaves, kSampleBins / 64>(s, need);
+                find_bin<kSampleBins / 64>(s, need, [](int i, int e) { return kSampleBins / 64 * i + e; });
                 const int bin = (int)s.bin;
                 const uint64_t before = s.below;
-                if (!counts) {   // all that is left fits the list?
-                    f.count = collect([&](uint32_t k, T x) { return k >= f.cut.key && bin_of((float)x) <= bin; });
-                    if (f.count <= kSampleList) {
-                        held = true;
-                        f.top_k = 0;
-                        f.top_p = top_p;
-                        f.share = need;
-                        f.key_bits = L::BITS;
-                        break;
-                    }
+                // all that is left, if it fits the list; else the bin that holds the cut
+                int count = 0, from = 0;
+#pragma unroll 1
+                for (; from <= bin; from = from < bin ? bin : bin + 1) {
+                    const auto in = [&](T x) { return left(x) && bin_of((float)x) >= from && bin_of((float)x) <= bin; };
+                    count = collect([&](const vec& x) {
+                        bool some = false;
+#pragma unroll
+                        for (int e = 0; e < L::VEC; ++e) some = some || in(x[e]);
+                        return some;
+                    }, in);
+                    if (count <= kSampleList) break;
                 }
-                const int count = collect([&](uint32_t k, T x) { return k >= f.cut.key && bin_of((float)x) == bin; });
                 uint64_t skipped;
                 uint32_t d;
                 if (count <= kSampleList) {
-                    d = select<kSampleWaves>(s, L::BITS, need - before, skipped, [&](auto&& g) {
+                    if (from == 0 && filter == (by_p ? 1 : 0)) {   // the last filter
+                        held = true;
+                        f.count = count;
+                    }
+                    const uint64_t behind = from ? before : 0;
+                    d = select(s, L::BITS, need - behind, skipped, [&](auto&& g) {
 #pragma unroll 1
                         for (int i = t; i < count; i += kSampleThreads) {
                             const uint32_t k = (uint32_t)(s.list[i] >> 32);
                             g(top_key - k, counts ? 1 : w.of(L::value(k)));
                         }
                     });
-                    skipped += before;
+                    skipped += behind;
                 } else {   // equal or nearly equal ones: over the row again
-                    d = select<kSampleWaves>(s, L::BITS, need, skipped, [&](auto&& g) {
-                        for_row<T, 1>(row, a.vocab, [&](int, T x) {
-                            const uint32_t k = L::key(x);
-                            if (k && k >= f.cut.key) g(top_key - k, counts ? 1 : w.of((float)x));
+                    d = select(s, L::BITS, need, skipped, [&](auto&& g) {
+                        for_row<T, 4, true>(row, a.vocab, [&](T x, int) {
+                            if (left(x)) g(top_key - L::key(x), counts ? 1 : w.of((float)x));
                         });
                     });
                 }
@@ -762,112 +942,137 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
                 f.cut = Cut{top_key - d, (uint32_t)((need - skipped + one - 1) / one)};
             }
         }
-        if (held) {
-            if (f.count > 64 * kSampleEach) {
-                finish<T, kSampleWaves>(s, w, f, answer);
-            } else if (t < 64) {
-                finish<T, 1>(s, w, f, answer);
-            }
+        if (held && f.count <= 128) {
+            finish_few<T>(s, w, f, answer);
             return;
         }
+        if (held) filter_list<T>(s, w, f);
         __syncthreads();
     }
 
-    // the draw over the whole row: sums of tiles, then the tile that holds it
-    const int head = head_elements(row, a.vocab), vecs = (a.vocab - head) / L::VEC, tail = head + vecs * L::VEC;
-    const int tiles = 2 + (vecs + 63) / 64;
-    // a lane's elements of a tile: VEC neighbours, or one at the row's ends
-    struct Span {
-        int first, n;
-    };
-    const auto span = [&](int tile) -> Span {
-        const int j = (tile - 1) * 64 + lane;
-        if (tile == 0) return {lane, lane < head};
-        if (tile == tiles - 1) return {tail + lane, lane < a.vocab - tail};
-        return {head + j * L::VEC, j < vecs ? L::VEC : 0};
-    };
-    const uint64_t one = f.cut.key ? w.kept(L::value(f.cut.key)) : 0;   // of those at the cut
-    for (int tile = t / 64; tile < tiles; tile += kSampleWaves) {
-        const Span at = span(tile);
-        uint64_t sum = 0;
-        uint32_t equal = 0;
-        const auto add = [&](T l) {
-            const uint32_t k = L::key(l);
-            equal += k && k == f.cut.key;
-            if (k > f.cut.key) sum += w.kept((float)l);
-        };
-        if (at.n == L::VEC) {
-            const typename L::vec v = *gptr<typename L::vec>(row + at.first);
-#pragma unroll
-            for (int e = 0; e < L::VEC; ++e) add(v[e]);
-        } else if (at.n) {
-            add(row[at.first]);
-        }
-        sum = prefix64(sum);
-        const uint32_t equals = (uint32_t)prefix64((uint64_t)equal);
-        if (lane == 63) {
-            s.tile.sums[tile] = sum;
-            s.tile.equals[tile] = equals;
-        }
+    // the draw: weights left, tile by tile of the row, then the tile that holds it
+    const Tiles<T> tiles(row, a.vocab);
+    f.cut = with_least<T>(f.cut, f.least);
+    const T cut = f.cut.key ? (T)L::value(f.cut.key) : nothing;
+    const uint64_t one = f.cut.key ? w.of((float)cut) : 0;   // of each of those at the cut
+    for (int i = t; i < tiles.count; i += kSampleThreads) {
+        s.tile_sum[i] = 0;
+        s.tile_equal[i] = 0;
     }
     __syncthreads();
-    const int per = (tiles + kSampleThreads - 1) / kSampleThreads, begin = std::min(tiles, t * per), end = std::min(tiles, (t + 1) * per);
-    uint64_t equal = 0, equal_before, sum = 0, before;
-    for (int i = begin; i < end; ++i) equal += s.tile.equals[i];
-    reduce<kSampleWaves, Sum, true>(s, equal, &equal_before);
-    const auto taken = [&](uint64_t from, uint64_t n) {   // of n at the cut behind `from` others
-        return from >= f.cut.quota ? 0 : std::min<uint64_t>(n, f.cut.quota - from);
-    };
-    equal = equal_before;
-    for (int i = begin; i < end; ++i) {
-        sum += s.tile.sums[i] + taken(equal, s.tile.equals[i]) * one;
-        equal += s.tile.equals[i];
-    }
-    const uint64_t total = reduce<kSampleWaves, Sum, true>(s, sum, &before), target = target_of(u, total);
-    if (before <= target && target < before + sum) {
-        equal = equal_before;
-        for (int i = begin; i < end; ++i) {
-            const uint64_t here = s.tile.sums[i] + taken(equal, s.tile.equals[i]) * one;
-            if (target < before + here) {
-                s.bin = i;
-                s.below = before;
-                s.count = (uint32_t)equal;
-                break;
+    if (held) {
+#pragma unroll 1
+        for (int i = t; i < f.count; i += kSampleThreads) {
+            const uint32_t k = (uint32_t)(s.list[i] >> 32);
+            const int tile = tiles.of((int)(uint32_t)s.list[i]);
+            if (k > f.cut.key) atomicAdd(reinterpret_cast<unsigned long long*>(&s.tile_sum[tile]), (unsigned long long)w.of(L::value(k)));
+            else if (k == f.cut.key) atomicAdd(&s.tile_equal[tile], 1u);
+        }
+    } else {
+        uint64_t sum = 0;
+        uint32_t equal = 0;
+        const auto add = [&](T l, int) {
+            equal += l == cut;   // (without a cut: -infinities, of which none counts)
+            if (l > cut) sum += w.of((float)l);
+        };
+        const auto put = [&](int tile) {
+            if (__ballot(sum != 0)) {
+                sum = prefix64(sum);
+                if (lane == 63) atomicAdd(reinterpret_cast<unsigned long long*>(&s.tile_sum[tile]), (unsigned long long)sum);
             }
-            before += here;
-            equal += s.tile.equals[i];
+            if (__ballot(equal != 0)) {
+                equal = (uint32_t)prefix64((uint64_t)equal);
+                if (lane == 63) atomicAdd(&s.tile_equal[tile], equal);
+            }
+            sum = equal = 0;
+        };
+        for_vectors<T, 4, true>(row, a.vocab, [&](const vec& x, int i, bool in) {
+            if (in) for_elements(x, i, add);
+            if (__ballot(in)) put(tiles.of(__builtin_amdgcn_readfirstlane(i)));
+        }, [](T, int) {});
+        if (t < 64) {   // the row's ends
+            if (t < tiles.head) add(row[t], t);
+            put(0);
+            if (t < a.vocab - tiles.tail) add(row[tiles.tail + t], tiles.tail + t);
+            put(tiles.count - 1);
         }
     }
     __syncthreads();
     if (t >= 64) return;
-    const Span at = span((int)s.bin);
-    uint32_t lane_equal = 0;
+
+    // one wave: neighbouring tiles to a lane
+    const int per = (tiles.count + 63) / 64, begin = std::min(tiles.count, lane * per), end = std::min(tiles.count, begin + per);
+    const auto taken = [&](uint64_t from, uint64_t n) {   // of n at the cut behind `from` others
+        return from >= f.cut.quota ? 0 : std::min<uint64_t>(n, f.cut.quota - from);
+    };
+    uint64_t equal = 0, sum = 0;
+    for (int i = begin; i < end; ++i) equal += s.tile_equal[i];
+    equal = prefix64(equal) - equal;
+    const uint64_t equal_first = equal;
+    for (int i = begin; i < end; ++i) {
+        sum += s.tile_sum[i] + taken(equal, s.tile_equal[i]) * one;
+        equal += s.tile_equal[i];
+    }
+    uint64_t upto = prefix64(sum);
+    const uint64_t total = lane_value(upto, 63), target = target_of(u, total);
+    const uint64_t reach = __ballot(target < upto);
+    int tile = begin;
+    uint64_t before = upto - sum;
+    equal = equal_first;
+    for (; tile < end - 1; ++tile) {
+        const uint64_t here = s.tile_sum[tile] + taken(equal, s.tile_equal[tile]) * one;
+        if (target < before + here) break;
+        before += here;
+        equal += s.tile_equal[tile];
+    }
+    const int owner = reach ? __builtin_ctzll(reach) : 63;
+    tile = __builtin_amdgcn_readlane(tile, owner);
+    before = lane_value(before, owner);
+    equal = lane_value(equal, owner);
+    // the tile's elements, 64 vectors at a time: a lane has neighbours, or one at the row's ends
+    const int groups = tile == 0 || tile == tiles.count - 1 ? 1 : tiles.per;
 #pragma unroll 1
-    for (int e = 0; e < at.n; ++e) lane_equal += L::key(row[at.first + e]) == f.cut.key && f.cut.key;
-    const uint32_t equal_first = s.count + (uint32_t)prefix64((uint64_t)lane_equal) - lane_equal;
-    uint64_t lane_sum = 0, reached = 0;
-    // once for the lane's sum, and once for the element
-#pragma unroll 1
-    for (int round = 0; round < 2; ++round) {
-        uint32_t seen = equal_first;
-        uint64_t sums = 0;
-#pragma unroll 1
-        for (int e = 0; e < at.n; ++e) {
-            const T l = row[at.first + e];
-            const uint32_t k = L::key(l);
-            uint64_t x = 0;
-            if (k > f.cut.key) x = w.kept((float)l);
-            else if (k && k == f.cut.key) x = seen++ < f.cut.quota ? one : 0;
-            sums += x;
-            if (round && target < reached + sums) {
-                answer(at.first + e, w.log_of((float)l, temperature, total));
-                break;
-            }
+    for (int g = 0; g < groups; ++g) {
+        int first, n;
+        if (tile == 0) {
+            first = lane;
+            n = lane < tiles.head;
+        } else if (tile == tiles.count - 1) {
+            first = tiles.tail + lane;
+            n = first < a.vocab;
+        } else {
+            const int j = ((tile - 1) * tiles.per + g) * 64 + lane;
+            first = tiles.head + j * L::VEC;
+            n = j < tiles.vecs ? L::VEC : 0;
         }
-        if (round) break;
-        lane_sum = sums;
-        reached = s.below + prefix64(lane_sum) - lane_sum;
-        if (!(reached <= target && target < reached + lane_sum)) break;
+        vec x{};
+        if (n == L::VEC) x = *gptr<vec>(row + first);
+        else if (n) x[0] = row[first];
+        uint32_t lane_equal = 0;
+#pragma unroll
+        for (int e = 0; e < L::VEC; ++e) lane_equal += e < n && x[e] == cut;
+        const uint32_t equal_to = (uint32_t)prefix64((uint64_t)lane_equal);
+        uint64_t seen = equal + equal_to - lane_equal, to[L::VEC], lane_sum = 0;   // the weights up to each of the lane's
+#pragma unroll
+        for (int e = 0; e < L::VEC; ++e) {
+            if (e < n && x[e] > cut) lane_sum += w.of((float)x[e]);
+            else if (e < n && x[e] == cut) lane_sum += seen++ < f.cut.quota ? one : 0;
+            to[e] = lane_sum;
+        }
+        const uint64_t sums = prefix64(lane_sum), from = before + sums - lane_sum;
+        if (from <= target && target < from + lane_sum) {
+            int e = 0;
+            float l = (float)x[0];
+#pragma unroll
+            for (int i = 1; i < L::VEC; ++i)
+                if (target >= from + to[i - 1]) {
+                    e = i;
+                    l = (float)x[i];
+                }
+            answer(first + e, w.log_of(l, temperature, total));
+        }
+        before += lane_value(sums, 63);
+        equal += (uint32_t)__builtin_amdgcn_readlane((int)equal_to, 63);
     }
 }
 
