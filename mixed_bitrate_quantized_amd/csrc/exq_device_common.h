@@ -121,6 +121,43 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 // been seen to read element 0 whatever i is.
 __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
 
+// Moves a value within a wave: lanes without a source get 0.
+template <int HOW, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t x) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, HOW, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), HOW, ROWS, 0xF, false);
+    return (uint64_t)hi << 32 | lo;
+}
+__device__ __forceinline__ uint64_t lane_value(uint64_t x, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane);
+    return (uint64_t)hi << 32 | lo;
+}
+struct Sum {
+    __device__ __forceinline__ static uint64_t of(uint64_t a, uint64_t b) { return a + b; }
+};
+struct SumReal {
+    __device__ __forceinline__ static uint64_t of(uint64_t a, uint64_t b) {
+        return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b));
+    }
+};
+struct Larger {
+    __device__ __forceinline__ static uint64_t of(uint64_t a, uint64_t b) { return a > b ? a : b; }
+};
+// Sums (or largest values) over the lanes up to each one, of 16 and of 64.
+template <class Op = Sum> __device__ __forceinline__ uint64_t prefix16(uint64_t x) {
+    x = Op::of(x, moved<0x111, 0xF>(x));
+    x = Op::of(x, moved<0x112, 0xF>(x));
+    x = Op::of(x, moved<0x114, 0xF>(x));
+    return Op::of(x, moved<0x118, 0xF>(x));
+}
+template <class Op = Sum> __device__ __forceinline__ uint64_t prefix64(uint64_t x) {
+    x = prefix16<Op>(x);
+    x = Op::of(x, moved<0x142, 0xA>(x));   // row 0's to row 1, row 2's to row 3
+    return Op::of(x, moved<0x143, 0xC>(x));   // the lower half's to the upper
+}
+__device__ __forceinline__ double prefix64(double x) {
+    return __builtin_bit_cast(double, prefix64<SumReal>(__builtin_bit_cast(uint64_t, x)));
+}
+
 // Descriptor of `layer` bound to x and y (device pointers).
 LinearDev linear_dev(const exq_layer* layer, const void* x, void* y);
 

@@ -46,7 +46,7 @@ constexpr int kCounters = 1 << 15;            // of 16 bits for each sign
 template <class T> struct PerRow {
     const T* p;
     T all;
-    __device__ T of(int row) const { return p ? p[row] : all; }
+    __device__ __forceinline__ T of(int row) const { return p ? p[row] : all; }
 };
 
 struct SampleArgs {
@@ -68,30 +68,30 @@ template <> struct Logit<_Float16> {
     typedef h8 vec;
     static constexpr int VEC = 8, BITS = 16, COARSE = 4;   // COARSE: bits of a key below 1/64 of a power of two
     static constexpr bool COUNTED = true;                  // a counter for every key fits LDS
-    __device__ static uint32_t key(_Float16 x) {
+    __device__ __forceinline__ static uint32_t key(_Float16 x) {
         uint32_t b = __builtin_bit_cast(uint16_t, x);
         if (b == 0x8000u) b = 0;
         const uint32_t k = b ^ (b & 0x8000u ? 0xFFFFu : 0x8000u);
         return (float)x > -__builtin_huge_valf() ? k : 0u;
     }
-    __device__ static float largest(const h8& x) {   // NaN aside
+    __device__ __forceinline__ static float largest(const h8& x) {   // NaN aside
         const h4 a = __builtin_elementwise_max(__builtin_shufflevector(x, x, 0, 1, 2, 3), __builtin_shufflevector(x, x, 4, 5, 6, 7));
         const h2 b = __builtin_elementwise_max(__builtin_shufflevector(a, a, 0, 1), __builtin_shufflevector(a, a, 2, 3));
         return (float)__builtin_elementwise_max(b[0], b[1]);
     }
-    __device__ static _Float16 at(const h8& x, int e) {
+    __device__ __forceinline__ static _Float16 at(const h8& x, int e) {
         const u4v y = __builtin_bit_cast(u4v, x);
         const uint32_t pair = e < 4 ? (e < 2 ? y[0] : y[1]) : (e < 6 ? y[2] : y[3]);
         return __builtin_bit_cast(_Float16, (uint16_t)(pair >> (16 * (e & 1))));
     }
     // Key of the smallest value that is x or more (0: any).
-    __device__ static uint32_t first_from(double x) {
+    __device__ __forceinline__ static uint32_t first_from(double x) {
         if (!(x > -65504.0)) return 0;
         if (x > 65504.0) return 0xFC00u;
         const _Float16 near = (_Float16)(float)x;
         return key(near) + ((double)near < x);
     }
-    __device__ static float value(uint32_t k) {
+    __device__ __forceinline__ static float value(uint32_t k) {
         return (float)__builtin_bit_cast(_Float16, (uint16_t)(k ^ (k & 0x8000u ? 0x8000u : 0xFFFFu)));
     }
 };
@@ -99,21 +99,21 @@ template <> struct Logit<float> {
     typedef f4 vec;
     static constexpr int VEC = 4, BITS = 32, COARSE = 17;
     static constexpr bool COUNTED = false;
-    __device__ static uint32_t key(float x) {
+    __device__ __forceinline__ static uint32_t key(float x) {
         const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
         return x > -__builtin_huge_valf() ? b ^ (b & 0x80000000u ? 0xFFFFFFFFu : 0x80000000u) : 0u;
     }
-    __device__ static float largest(const f4& x) {
+    __device__ __forceinline__ static float largest(const f4& x) {
         return __builtin_fmaxf(__builtin_fmaxf(x[0], x[1]), __builtin_fmaxf(x[2], x[3]));
     }
-    __device__ static float at(const f4& x, int e) { return e < 2 ? (e ? x[1] : x[0]) : (e < 3 ? x[2] : x[3]); }
-    __device__ static uint32_t first_from(double x) {
+    __device__ __forceinline__ static float at(const f4& x, int e) { return e < 2 ? (e ? x[1] : x[0]) : (e < 3 ? x[2] : x[3]); }
+    __device__ __forceinline__ static uint32_t first_from(double x) {
         if (!(x > -(double)__FLT_MAX__)) return 0;
         if (x > (double)__FLT_MAX__) return 0xFF800000u;
         const float near = (float)x;
         return key(near) + ((double)near < x);
     }
-    __device__ static float value(uint32_t k) { return __builtin_bit_cast(float, k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
+    __device__ __forceinline__ static float value(uint32_t k) { return __builtin_bit_cast(float, k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
 };
 
 constexpr double kLn2d = 0.69314718055994530942;
@@ -134,7 +134,7 @@ struct Weights {
     double top, c;   // largest logit, 256 log2(e) / T; beside an infinity all else weighs nothing
     double scale;    // 2^shift
     const double* powers;
-    __device__ double power(double t) const {   // 2^(t / 256)
+    __device__ __forceinline__ double power(double t) const {   // 2^(t / 256)
 #pragma clang fp contract(off)   // the same bits wherever the compiler puts it
         constexpr double a = kLn2d / kPowers;
         t = __builtin_fmax(t, -256.0 * 1000);
@@ -146,17 +146,17 @@ struct Weights {
         const double w = __builtin_fma(near * f, q, near);
         return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, w) + ((uint64_t)(uint32_t)((j >> 8) << 20) << 32));
     }
-    __device__ double real(float l) const {   // l: at most the largest
+    __device__ __forceinline__ double real(float l) const {   // l: at most the largest
 #pragma clang fp contract(off)
         return power(((double)__builtin_fminf(l, __FLT_MAX__) - top) * c);
     }
     // In units, rounded: 2^52 + w * 2^shift has the whole number in its lower bits.
-    __device__ uint64_t units(double w) const {
+    __device__ __forceinline__ uint64_t units(double w) const {
         return __builtin_bit_cast(uint64_t, __builtin_fma(w, scale, 4503599627370496.0)) & 0xFFFFFFFFFFFFFull;
     }
-    __device__ uint64_t of(float l) const { return units(real(l)); }
+    __device__ __forceinline__ uint64_t of(float l) const { return units(real(l)); }
     // ln of its probability among weights of `sum` units
-    __device__ float log_of(float l, float temperature, uint64_t sum) const {
+    __device__ __forceinline__ float log_of(float l, float temperature, uint64_t sum) const {
         const double z = l == topf ? 0.0 : ((double)l - top) / (double)temperature;
         return (float)(z - log((double)sum / scale));
     }
@@ -192,43 +192,6 @@ struct SampleShared {
     uint32_t rank[128];
     uint64_t before[128];
 };
-
-// Moves a value within a wave: lanes without a source get 0.
-template <int HOW, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t x) {
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, HOW, ROWS, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), HOW, ROWS, 0xF, false);
-    return (uint64_t)hi << 32 | lo;
-}
-__device__ __forceinline__ uint64_t lane_value(uint64_t x, int lane) {
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane);
-    return (uint64_t)hi << 32 | lo;
-}
-struct Sum {
-    __device__ static uint64_t of(uint64_t a, uint64_t b) { return a + b; }
-};
-struct SumReal {
-    __device__ static uint64_t of(uint64_t a, uint64_t b) {
-        return __builtin_bit_cast(uint64_t, __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b));
-    }
-};
-struct Larger {
-    __device__ static uint64_t of(uint64_t a, uint64_t b) { return a > b ? a : b; }
-};
-// Sums (or largest values) over the lanes up to each one, of 16 and of 64.
-template <class Op = Sum> __device__ __forceinline__ uint64_t prefix16(uint64_t x) {
-    x = Op::of(x, moved<0x111, 0xF>(x));
-    x = Op::of(x, moved<0x112, 0xF>(x));
-    x = Op::of(x, moved<0x114, 0xF>(x));
-    return Op::of(x, moved<0x118, 0xF>(x));
-}
-template <class Op = Sum> __device__ __forceinline__ uint64_t prefix64(uint64_t x) {
-    x = prefix16<Op>(x);
-    x = Op::of(x, moved<0x142, 0xA>(x));   // row 0's to row 1, row 2's to row 3
-    return Op::of(x, moved<0x143, 0xC>(x));   // the lower half's to the upper
-}
-__device__ __forceinline__ double prefix64(double x) {
-    return __builtin_bit_cast(double, prefix64<SumReal>(__builtin_bit_cast(uint64_t, x)));
-}
 
 // Over the workgroup: the sum of the threads before (with BEFORE), and of all.
 template <class Op = Sum, bool BEFORE = false>
@@ -665,7 +628,7 @@ template <class T> __device__ __forceinline__ void filter_list(SampleShared& s, 
 // The row in tiles: its head, groups of 64 vectors (a wave's look), its tail.
 template <class T> struct Tiles {
     int head, vecs, tail, vocab, groups, per, count;   // per: groups of a tile
-    __device__ Tiles(const T* row, int n) {
+    __device__ __forceinline__ Tiles(const T* row, int n) {
         constexpr int VEC = Logit<T>::VEC;
         vocab = n;
         head = head_elements(row, n);
@@ -675,9 +638,10 @@ template <class T> struct Tiles {
         per = groups <= kSampleTiles - 2 ? 1 : (groups + kSampleTiles - 3) / (kSampleTiles - 2);
         count = 2 + (groups + per - 1) / per;
     }
-    __device__ int of(int i) const {   // of index i
+    __device__ __forceinline__ int of(int i) const {   // of index i
         if (i < head) return 0;
-        return i >= tail ? count - 1 : 1 + (i - head) / (64 * Logit<T>::VEC) / per;
+        const int group = (i - head) / (64 * Logit<T>::VEC);
+        return i >= tail ? count - 1 : 1 + (per == 1 ? group : group / per);
     }
 };
 
@@ -815,7 +779,11 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
     };
 
     bool held = false;   // whether the list holds all that the filters can leave
-    if (by_k || by_p) {
+    if (by_k || by_p || f.least) {
+        if (!by_k && !by_p) {
+            f.count = collect_from(f.least);
+            held = f.count <= kSampleList;
+        }
         if (near) {
             // a threshold that top_k threads' largest logits reach, to 1/64 of a power of two
             const auto coarse = [&](uint32_t k) { return min((top_key >> L::COARSE) - (k >> L::COARSE), (1u << kDigit) - 1); };
@@ -868,7 +836,7 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
                 }
             }
         }
-        if (!counted && !held) {
+        if (!counted && !held && (by_k || by_p)) {
             f.top_k = 0;
             f.top_p = 1.0f;
 #pragma unroll 1
@@ -987,8 +955,10 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
             sum = equal = 0;
         };
         for_vectors<T, 4, true>(row, a.vocab, [&](const vec& x, int i, bool in) {
+            // (cut or not, what is below it adds nothing)
+            if (__ballot(in && L::largest(x) >= (float)cut) == 0) return;
             if (in) for_elements(x, i, add);
-            if (__ballot(in)) put(tiles.of(__builtin_amdgcn_readfirstlane(i)));
+            put(tiles.of(__builtin_amdgcn_readfirstlane(i)));
         }, [](T, int) {});
         if (t < 64) {   // the row's ends
             if (t < tiles.head) add(row[t], t);
