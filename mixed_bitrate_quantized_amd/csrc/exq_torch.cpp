@@ -271,6 +271,32 @@ PyObject* given_or_empty(PyObject* o, const Call& c, at::IntArrayRef shape, at::
     return o == Py_None ? THPVariable_Wrap(empty(c, shape, type)) : Py_NewRef(o);
 }
 
+// New outputs of a call, contiguous, in one allocation: one of them costs the host a
+// microsecond, a tensor on it a tenth of that.
+struct Output {
+    at::IntArrayRef shape;
+    at::ScalarType type;
+    size_t bytes() const {
+        int64_t n = (int64_t)at::elementSize(type);
+        for (const int64_t x : shape) n *= x;
+        return ((size_t)n + 255) / 256 * 256;
+    }
+};
+template <size_t N> void empties(const Call& c, const Output (&x)[N], THPObjectPtr (&out)[N]) {
+    size_t total = 0;
+    for (const Output& o : x) total += o.bytes();
+    const at::Tensor all = empty(c, {(int64_t)total}, at::kByte);
+    size_t at = 0;
+    for (size_t i = 0; i < N; ++i) {
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                                c10::scalarTypeToTypeMeta(x[i].type));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(x[i].shape);
+        t.unsafeGetTensorImpl()->set_storage_offset((int64_t)(at / at::elementSize(x[i].type)));
+        at += x[i].bytes();
+        out[i] = THPVariable_Wrap(t);
+    }
+}
+
 // A pool's own arrays.
 struct Pool {
     Table t;
@@ -311,9 +337,12 @@ PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return nullptr;
         const char* names[3] = {"seqs", "positions", "offsets"};
         THPObjectPtr o[3];
+        const int64_t sizes[3] = {rows, rows, (int64_t)p.t.rows + 1};
+        if (a[11] == Py_None && a[12] == Py_None && a[13] == Py_None)
+            empties(c, {Output{sizes[0], at::kInt}, Output{sizes[1], at::kInt}, Output{sizes[2], at::kInt}}, o);
         for (int i = 0; i < 3; ++i) {
-            const int64_t size = i < 2 ? rows : (int64_t)p.t.rows + 1;
-            o[i] = given_or_empty(a[11 + i], c, {size}, at::kInt);
+            const int64_t size = sizes[i];
+            if (!o[i]) o[i] = given_or_empty(a[11 + i], c, {size}, at::kInt);
             if (!o[i] || !index_operand(names[i], o[i], c, size, out[i])) return nullptr;
         }
         THPObjectPtr outs(PyTuple_Pack(3, o[0].get(), o[1].get(), o[2].get()));
@@ -373,9 +402,14 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
         THPObjectPtr o[2];
         if (!few_enough(rows) || !few_enough(heads[0]) || !few_enough(heads[1]) || !index_operand("positions", a[8], c, rows, positions))
             return nullptr;
-        for (int i = 0; i < (both ? 2 : 1); ++i) {
+        for (int i = 0; i < (both ? 2 : 1); ++i)
             if (!rows_operand(i ? "k" : "q", a[i ? 9 : 7], c, rows, heads[i], in[i])) return nullptr;
-            o[i] = given_or_empty(a[10 + i], c, {rows, heads[i], c.dim}, at::kHalf);
+        if (both && a[10] == Py_None && a[11] == Py_None) {
+            const int64_t q_shape[3] = {rows, heads[0], c.dim}, k_shape[3] = {rows, heads[1], c.dim};
+            empties(c, {Output{q_shape, at::kHalf}, Output{k_shape, at::kHalf}}, o);
+        }
+        for (int i = 0; i < (both ? 2 : 1); ++i) {
+            if (!o[i]) o[i] = given_or_empty(a[10 + i], c, {rows, heads[i], c.dim}, at::kHalf);
             if (!o[i] || !rows_operand(i ? "k_out" : "q_out", o[i], c, rows, heads[i], out[i])) return nullptr;
         }
         THPObjectPtr value(both ? PyTuple_Pack(2, o[0].get(), o[1].get()) : Py_NewRef(o[0].get()));
@@ -482,12 +516,20 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
             !setting("top_k", a[5], c, rows, top_k) || !setting("top_p", a[6], c, rows, top_p) ||
             !setting("min_p", a[7], c, rows, min_p))
             return nullptr;
-        THPObjectPtr tokens(given_or_empty(a[8], c, {rows}, at::kInt)), logs;
+        THPObjectPtr tokens, logs;
+        if (want && a[8] == Py_None && a[10] == Py_None) {
+            THPObjectPtr o[2];
+            empties(c, {Output{rows, at::kInt}, Output{rows, at::kFloat}}, o);
+            tokens = std::move(o[0]);
+            logs = std::move(o[1]);
+        } else {
+            tokens = given_or_empty(a[8], c, {rows}, at::kInt);
+        }
         const int32_t* tokens_p;
         if (!tokens || !index_operand("out", tokens, c, rows, tokens_p)) return nullptr;
         float* logs_p = nullptr;
         if (want || a[10] != Py_None) {
-            logs = given_or_empty(a[10], c, {rows}, at::kFloat);
+            if (!logs) logs = given_or_empty(a[10], c, {rows}, at::kFloat);
             const at::Tensor* t = logs ? tensor("logprobs", logs) : nullptr;
             if (!t) return nullptr;
             if (!here(*t, c, at::kFloat) || t->dim() != 1 || t->size(0) != rows || (rows > 1 && t->stride(0) != 1))
