@@ -618,6 +618,9 @@ exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_st
  *            that follows, for all rows
  *   tokens   device int32 [rows], written
  *   logprobs device fp32 [rows] or NULL: ln of the token's share of the weights left
+ *   workspace  device, 16-byte aligned, exq_sample_workspace_bytes(rows, vocab) bytes,
+ *            written, or NULL.  With it, few rows of many logits are shared out over
+ *            the GPU (1 x 131072 fp32 logits drawn from all: XX us, without YY)
  * A row without a logit that may be drawn, or with a u, T, top_p or min_p that is
  * NaN, or a negative T, gets token -1 and logprob NaN.
  * Weights are computed in 64 bits and summed exactly, in units of 2^-42 (vocab of
@@ -626,10 +629,11 @@ exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_st
  * rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, misaligned, a bad size, stride or
  * setting, tokens or logprobs overlapping an input or each other), UNSUPPORTED
  * (bits, vocab), HIP. */
+size_t exq_sample_workspace_bytes(int rows, int vocab);   /* 0: none is needed */
 exq_status exq_sample(const void* logits, int bits, int rows, int vocab, int64_t row_stride, const float* u,
                       const float* temperatures, float temperature, const int32_t* top_ks, int top_k,
                       const float* top_ps, float top_p, const float* min_ps, float min_p, int32_t* tokens,
-                      float* logprobs, void* stream);
+                      float* logprobs, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------ diagnostic */
 

@@ -105,7 +105,9 @@ def _load():
     lib.exq_lora_workspace_bytes.argtypes = [vp, i32]
     lib.exq_lora_workspace_bytes.restype = u64
     lib.exq_lora_add.argtypes = [vp, vp, i64, i32, vp, vp, i64, vp, i64, vp, u64, vp]
-    lib.exq_sample.argtypes = [vp, i32, i32, i32, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp]
+    lib.exq_sample_workspace_bytes.argtypes = [i32, i32]
+    lib.exq_sample_workspace_bytes.restype = u64
+    lib.exq_sample.argtypes = [vp, i32, i32, i32, i64, vp, vp, f32, vp, i32, vp, f32, vp, f32, vp, vp, vp, u64, vp]
     for f in (lib.exq_pages_extend, lib.exq_pages_trim, lib.exq_rotate, lib.exq_adapters_create, lib.exq_lora_add, lib.exq_sample,
               lib.exq_pack, lib.exq_layer_create, lib.exq_gemm, lib.exq_gemm_noalloc, lib.exq_dequant, lib.exq_plan_create,
               lib.exq_plan_run, lib.exq_stream_read, lib.exq_gemm_gated, lib.exq_group_errors,
@@ -125,7 +127,8 @@ EXPORTED = (
     "exq_autotune", "exq_set_variant", "exq_pack_qs", "exq_layer_create_qs", "exq_gemm_noalloc",
     "exq_cache_page_bytes", "exq_cache_create", "exq_cache_destroy", "exq_cache_append", "exq_cache_read",
     "exq_attend_workspace_bytes", "exq_attend", "exq_pages_workspace_bytes", "exq_pages_extend", "exq_pages_trim", "exq_rotate",
-    "exq_adapters_create", "exq_adapters_destroy", "exq_lora_workspace_bytes", "exq_lora_add", "exq_sample",
+    "exq_adapters_create", "exq_adapters_destroy", "exq_lora_workspace_bytes", "exq_lora_add", "exq_sample_workspace_bytes",
+    "exq_sample",
 )
 
 VARIANT_DEFAULT, VARIANT_DECODE16, VARIANT_DECODE64, VARIANT_PREFILL = 0, 1, 2, 3
@@ -390,11 +393,16 @@ def exq_lora_add(adapters: int, x_ptr: int, x_stride: int, rows: int, ids_ptr: i
                             workspace_bytes, _stream_ptr(stream)), "exq_lora_add")
 
 
+def exq_sample_workspace_bytes(rows: int, vocab: int) -> int:
+    return int(lib.exq_sample_workspace_bytes(rows, vocab))
+
+
 def exq_sample(logits_ptr: int, bits: int, rows: int, vocab: int, row_stride: int, u_ptr: int, temperatures_ptr,
                temperature: float, top_ks_ptr, top_k: int, top_ps_ptr, top_p: float, min_ps_ptr, min_p: float, tokens_ptr: int,
-               logprobs_ptr=None, stream=None) -> None:
+               logprobs_ptr=None, workspace_ptr=None, workspace_bytes: int = 0, stream=None) -> None:
     _check(lib.exq_sample(logits_ptr, bits, rows, vocab, row_stride, u_ptr, temperatures_ptr, temperature, top_ks_ptr, top_k,
-                          top_ps_ptr, top_p, min_ps_ptr, min_p, tokens_ptr, logprobs_ptr, _stream_ptr(stream)), "exq_sample")
+                          top_ps_ptr, top_p, min_ps_ptr, min_p, tokens_ptr, logprobs_ptr, workspace_ptr, workspace_bytes,
+                          _stream_ptr(stream)), "exq_sample")
 
 
 # ------------------------------------------------------------ conveniences

@@ -38,6 +38,8 @@ constexpr int kSampleList = 4096;             // candidates that LDS holds
 constexpr int kSampleNear = 900;              // a top-k that is looked for from the threads' largest logits
 constexpr int kDigit = 9;                     // bits looked at together
 constexpr int kSampleBins = 2048;             // of a row's histogram
+constexpr int kSampleParts = 16;              // of a row, at most
+constexpr int kSamplePartList = 1024;         // candidates of a part
 constexpr int kSampleMaxVocabLog2 = 21;
 constexpr int kPowers = 256;                  // 2^(i / 256) in LDS
 constexpr int kCounters = 1 << 15;            // of 16 bits for each sign
@@ -47,6 +49,29 @@ template <class T> struct PerRow {
     const T* p;
     T all;
     __device__ __forceinline__ T of(int row) const { return p ? p[row] : all; }
+};
+
+// Words that workgroups of one launch leave for one another go past the caches of
+// their XCDs.  (A fence of all waves, which writes back and drops those, took 100 us
+// in 256 workgroups.)
+__device__ __forceinline__ void leave(uint64_t* p, uint64_t x) { __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint64_t left_at(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// Rows shared out over `parts` workgroups each: what these leave for one another, 64
+// bits each.
+struct SampleSplit {
+    uint64_t* p;
+    int rows, parts;
+    __host__ __device__ int64_t head() const { return ((int64_t)rows * (2 + parts) + 1) & ~1; }
+    __device__ uint64_t* best(int r) const { return p + r; }                  // largest key, and where
+    __device__ uint64_t* done(int r) const { return p + rows + r; }           // parts that are
+    __device__ uint64_t* counts(int r) const { return p + 2 * rows + (int64_t)r * parts; }   // of the parts' lists
+    __device__ uint64_t* bins(int r, int part) const { return p + head() + ((int64_t)r * parts + part) * kSampleBins; }
+    __device__ uint64_t* tiles(int r) const { return p + head() + ((int64_t)rows * parts + r) * kSampleBins; }
+    __device__ uint64_t* list(int r, int part) const {
+        return p + head() + (int64_t)rows * (parts + 1) * kSampleBins + ((int64_t)r * parts + part) * kSamplePartList;
+    }
+    size_t bytes() const { return 8 * (size_t)(head() + (int64_t)rows * ((parts + 1) * kSampleBins + parts * kSamplePartList)); }
 };
 
 struct SampleArgs {
@@ -59,6 +84,7 @@ struct SampleArgs {
     PerRow<float> top_p, min_p;
     int32_t* tokens;
     float* logprobs;
+    SampleSplit split;
 };
 
 // Ordered keys: larger for larger logits; 0 for a NaN or -infinity, which are
@@ -162,7 +188,8 @@ struct Weights {
     }
 };
 
-constexpr int kSampleTiles = 2048;
+constexpr int kSampleTiles = 2048;   // of a row, at most
+static_assert(kSampleTiles == kSampleBins, "either fills a part's sums");
 
 struct SampleShared {
     union {
@@ -237,6 +264,20 @@ template <int PER, class F> __device__ __forceinline__ void find_bin(SampleShare
 
 __device__ __forceinline__ void add_to_bin(SampleShared& s, uint32_t bin, uint64_t amount) {
     atomicAdd(reinterpret_cast<unsigned long long*>(&s.bins[bin]), (unsigned long long)amount);
+}
+
+// The same of a row's histogram, two bins to a thread, with need(sum of all).
+template <class F> __device__ __forceinline__ uint64_t find_row_bin(SampleShared& s, uint64_t x0, uint64_t x1, F&& need_of) {
+    static_assert(kSampleBins == 2 * kSampleThreads, "two bins to a thread");
+    uint64_t before;
+    const uint64_t all = reduce<Sum, true>(s, x0 + x1, &before), need = need_of(all);
+    if (before < need && need <= before + x0 + x1) {
+        const bool second = need > before + x0;
+        s.bin = 2 * threadIdx.x + second;
+        s.below = before + (second ? x0 : 0);
+    }
+    __syncthreads();
+    return need;
 }
 
 // The smallest D below 2^bits with a sum of amounts of d <= D of `need` or more
@@ -647,11 +688,163 @@ template <class T> struct Tiles {
 
 // -------------------------------------------------------------------- kernel
 
-template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
+// The tiles of a row's body that a part of it has, and each(value, index) for their
+// elements and, for the first part, the row's ends; put(tile) behind a wave's
+// elements of a tile.
+template <class T> struct Part {
+    int first, last;   // tiles of the body, from 0
+    __device__ __forceinline__ Part(const Tiles<T>& tiles, int part, int parts) {
+        const int body = tiles.count - 2, each = (body + parts - 1) / parts;
+        first = std::min(body, part * each);
+        last = std::min(body, first + each);
+    }
+    template <class F, class G>
+    __device__ __forceinline__ void each(const Tiles<T>& tiles, const T* row, int part, F&& f, G&& put) const {
+        typedef typename Logit<T>::vec vec;
+        constexpr int VEC = Logit<T>::VEC;
+        const int t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
+        const EXQ_GLOBAL vec* body = gptr<vec>(row + tiles.head);
+        const int end = std::min(last * tiles.per, tiles.groups);
+        // the next group's load is under way while one is worked on
+        const auto load = [&](int group) { return group < end && group * 64 + lane < tiles.vecs ? body[group * 64 + lane] : vec{}; };
+        int group = first * tiles.per + wave;
+        vec next = load(group);
+#pragma unroll 1
+        for (; group < end; group += kSampleWaves) {
+            const vec x = next;
+            next = load(group + kSampleWaves);
+            const int j = group * 64 + lane;
+            if (j < tiles.vecs) for_elements(x, tiles.head + j * VEC, f);
+            put(1 + (tiles.per == 1 ? group : group / tiles.per));
+        }
+        if (part == 0 && t < 64) {
+            if (t < tiles.head) f(row[t], t);
+            put(0);
+            if (t < tiles.vocab - tiles.tail) f(row[tiles.tail + t], tiles.tail + t);
+            put(tiles.count - 1);
+        }
+    }
+    // s.tile_sum of them, and of the row's ends
+    __device__ __forceinline__ void clear(SampleShared& s, const Tiles<T>& tiles) const {
+        for (int i = 1 + first + threadIdx.x; i < 1 + last; i += kSampleThreads) s.tile_sum[i] = 0;
+        if (threadIdx.x < 2) s.tile_sum[threadIdx.x ? tiles.count - 1 : 0] = 0;
+    }
+    __device__ __forceinline__ void store(const SampleShared& s, const Tiles<T>& tiles, int part, uint64_t* out) const {
+        for (int i = 1 + first + threadIdx.x; i < 1 + last; i += kSampleThreads) leave(out + i, s.tile_sum[i]);
+        if (part == 0 && threadIdx.x < 2) {
+            const int i = threadIdx.x ? tiles.count - 1 : 0;
+            leave(out + i, s.tile_sum[i]);
+        }
+    }
+};
+// A wave's sum, to its tile.
+__device__ __forceinline__ void put_sum(SampleShared& s, uint64_t& sum, int tile) {
+    if (__ballot(sum != 0)) {
+        sum = prefix64(sum);
+        if (threadIdx.x % 64 == 63) atomicAdd(reinterpret_cast<unsigned long long*>(&s.tile_sum[tile]), (unsigned long long)sum);
+    }
+    sum = 0;
+}
+
+// A part's share of the first look: the weights of its tiles, by tile, or with
+// BINS by bin_of(logit).
+template <class T, bool BINS, class B>
+__device__ __forceinline__ void sum_part(SampleShared& s, const SampleSplit& split, const T* row, int vocab, int r, int part,
+                                         const Weights& w, B&& bin_of) {
+    const Tiles<T> tiles(row, vocab);
+    const Part<T> mine(tiles, part, split.parts);
+    __syncthreads();
+    if (BINS) s.bins[threadIdx.x] = s.bins[threadIdx.x + kSampleThreads] = 0;
+    else mine.clear(s, tiles);
+    __syncthreads();
+    uint64_t sum = 0;
+    mine.each(tiles, row, part, [&](T x, int) {
+        if ((float)x > -__builtin_huge_valf()) {
+            const uint64_t amount = w.of((float)x);
+            if (!BINS) sum += amount;
+            else if (amount) add_to_bin(s, (uint32_t)bin_of((float)x), amount);
+        }
+    }, [&](int tile) {
+        if (!BINS) put_sum(s, sum, tile);
+    });
+    __syncthreads();
+    if (BINS) {
+        uint64_t* out = split.bins(r, part);
+        for (int i = threadIdx.x; i < kSampleBins; i += kSampleThreads) *gptr_w<uint64_t>(out + i) = s.bins[i];
+    } else {
+        mine.store(s, tiles, part, split.tiles(r));
+    }
+}
+
+// A part's share of the second: the weights of its tiles' logits of smaller bins than
+// `bin`, where top-p ends, that min-p leaves (from `least`), and a list of those
+// of that bin.  Whether all other parts were done before, with theirs.
+template <class T, class B>
+__device__ __forceinline__ bool cut_part(SampleShared& s, const SampleSplit& split, const T* row, int vocab, int r, int part,
+                                         const Weights& w, B&& bin_of, int bin, uint32_t least) {
+    typedef Logit<T> L;
+    const int t = threadIdx.x;
+    const Tiles<T> tiles(row, vocab);
+    const Part<T> mine(tiles, part, split.parts);
+    mine.clear(s, tiles);
+    if (t == 0) s.count = 0;
+    __syncthreads();
+    uint64_t sum = 0;
+    mine.each(tiles, row, part, [&](T x, int i) {
+        if (!((float)x > -__builtin_huge_valf())) return;
+        const int b = bin_of((float)x);
+        if (b > bin) return;
+        if (b < bin) {
+            if (L::key(x) >= least) sum += w.of((float)x);
+        } else {
+            const uint32_t at = atomicAdd(&s.count, 1u);
+            if (at < kSamplePartList) s.list[at] = (uint64_t)L::key(x) << 32 | (uint32_t)i;
+        }
+    }, [&](int tile) { put_sum(s, sum, tile); });
+    __syncthreads();
+    mine.store(s, tiles, part, split.tiles(r));
+    const int n = (int)s.count;
+    uint64_t* out = split.list(r, part);
+    for (int i = t; i < std::min(n, kSamplePartList); i += kSampleThreads) leave(out + i, s.list[i]);
+    if (t == 0) leave(split.counts(r) + part, (uint64_t)n);
+    // The last one goes on.  What a part leaves has arrived before its one in `done`, and
+    // is read behind the last one's.
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (t == 0) s.count = (uint32_t)__hip_atomic_fetch_add(split.done(r), 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    return (int)s.count == split.parts - 1;
+}
+
+// The parts' lists as one; whether they are whole and fit it.
+__device__ __forceinline__ bool join_lists(SampleShared& s, const SampleSplit& split, int r, int& count) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t n = lane < split.parts ? left_at(split.counts(r) + lane) : 0;
+    const uint64_t upto = prefix64(n);
+    if (__ballot(n > kSamplePartList) || lane_value(upto, 63) > kSampleList) return false;
+    count = (int)lane_value(upto, 63);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    static_assert(kSampleParts <= kSampleWaves, "a wave to a part");
+    if (wave < split.parts) {
+        const int from = (int)(lane_value(upto, wave) - lane_value(n, wave)), own = (int)lane_value(n, wave);
+        const uint64_t* x = split.list(r, wave);
+        for (int i = lane; i < own; i += 64) s.list[from + i] = left_at(x + i);
+    }
+    __syncthreads();
+    return true;
+}
+
+// A workgroup to a row.  Rows whose every logit has to be weighed are shared out over
+// split.parts of them if there are: all look for the largest logit and each weighs a
+// part.  A second launch (REST) does what then is left: the draw, or, with top-p,
+// each part that of its logits at and above the end of it and the last one the draw.
+template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
     __shared__ SampleShared s;
     typedef Logit<T> L;
     typedef typename L::vec vec;
-    const int t = threadIdx.x, r = blockIdx.x, lane = t % 64;
+    const int t = threadIdx.x, lane = t % 64, part = blockIdx.x / a.rows, r = blockIdx.x - part * a.rows;
     const float u = a.u[r];
     if (u < 0.0f) return;
     const T* row = static_cast<const T*>(a.logits) + (int64_t)r * a.stride;
@@ -662,51 +855,64 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
         if (a.logprobs) a.logprobs[r] = logprob;
     };
     if (!(temperature >= 0.0f) || u != u || top_p != top_p || min_p != min_p) {
-        if (t == 0) answer(-1, __builtin_nanf(""));
+        if (!REST && part == 0 && t == 0) answer(-1, __builtin_nanf(""));
         return;
     }
     const bool first_only = temperature == 0.0f || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
     const bool near = by_k && top_k <= kSampleNear;   // top-k from the threads' largest logits
-    bool counted = L::COUNTED && !first_only && !near && (by_k || by_p);
+    const bool split = a.split.parts > 1 && !first_only && !by_k && (by_p || !(min_p > 0.0f));
+    if (split ? REST && !by_p && part : REST || part) return;   // what one workgroup, or the first launch's, has all of
+    bool counted = L::COUNTED && !split && !first_only && !near && (by_k || by_p);
     if (t < kPowers) s.powers[t] = exp2_series((double)t / kPowers);
     if (t == 0) s.bin = s.below = 0;
     if (t == kPowers && min_p > 0.0f) s.log_min_p = log((double)min_p);
     if (counted) clear_counters(s);
 
-    // the largest logit, in which vector it comes first
-    float mine = -__builtin_huge_valf();   // the thread's
+    float mine = -__builtin_huge_valf();   // the thread's largest logit, in which vector it comes first
     int mine_at = 0;
-    const auto look = [&](float x, int i) {
-        if (x > mine) {
-            mine = x;
-            mine_at = i;
-        }
-    };
-    for_vectors<T, 6, false>(row, a.vocab, [&](const vec& x, int i, bool in) {
-        if (!in) return;
-        look(L::largest(x), i);
-        if constexpr (L::COUNTED) {
-            if (counted) {
-                const u4v bits = __builtin_bit_cast(u4v, x);
+    uint32_t mine_key = 0;
+    uint64_t best;
+    if constexpr (REST) {
+        best = *a.split.best(r);
+        __syncthreads();
+        if (best == 0) return;
+    } else {
+        const auto look = [&](float x, int i) {
+            if (x > mine) {
+                mine = x;
+                mine_at = i;
+            }
+        };
+        for_vectors<T, 6, false>(row, a.vocab, [&](const vec& x, int i, bool in) {
+            if (!in) return;
+            look(L::largest(x), i);
+            if constexpr (L::COUNTED) {
+                if (counted) {
+                    const u4v bits = __builtin_bit_cast(u4v, x);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    count(s, bits[e]);
-                    count(s, bits[e] >> 16);
+                    for (int e = 0; e < 4; ++e) {
+                        count(s, bits[e]);
+                        count(s, bits[e] >> 16);
+                    }
                 }
             }
+        }, [&](T x, int i) {
+            look((float)x, i);
+            if constexpr (L::COUNTED) {
+                if (counted) count(s, __builtin_bit_cast(uint16_t, x));
+            }
+        });
+        mine_key = L::key((T)mine);
+        best = reduce<Larger>(s, mine_key ? (uint64_t)mine_key << 32 | (uint32_t)~mine_at : 0);
+        if (split && part == 0 && t == 0) {
+            *a.split.best(r) = best;
+            *a.split.done(r) = 0;
         }
-    }, [&](T x, int i) {
-        look((float)x, i);
-        if constexpr (L::COUNTED) {
-            if (counted) count(s, __builtin_bit_cast(uint16_t, x));
+        if (best == 0) {   // nothing that may be drawn
+            if (part == 0 && t == 0) answer(-1, __builtin_nanf(""));
+            return;
         }
-    });
-    const uint32_t mine_key = L::key((T)mine);
-    const uint64_t best = reduce<Larger>(s, mine_key ? (uint64_t)mine_key << 32 | (uint32_t)~mine_at : 0);
-    if (best == 0) {   // nothing that may be drawn
-        if (t == 0) answer(-1, __builtin_nanf(""));
-        return;
     }
     const uint32_t top_key = (uint32_t)(best >> 32);
     if (first_only) {
@@ -724,6 +930,22 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
     if (min_p > 0.0f) {   // w >= min-p where the logit is M + T ln(min-p) or more
         const double least = min_p == 1.0f ? (double)topf : (double)topf + (double)temperature * s.log_min_p;
         f.least = L::first_from(least);
+    }
+
+    // 64 bins for one of the logits, or for a power of two of the weights
+    const auto bins_of = [&](bool counts) {
+        const float rate = counts ? 64.0f : __builtin_fminf((float)(w.c * (64.0 / kPowers)), 1e30f);
+        return [=](float l) {
+            const float d = (finite_top - __builtin_fminf(l, __FLT_MAX__)) * rate;
+            return d < (float)(kSampleBins - 1) ? (int)d : kSampleBins - 1;
+        };
+    };
+    if constexpr (!REST) {
+        if (split) {
+            if (by_p) sum_part<T, true>(s, a.split, row, a.vocab, r, part, w, bins_of(false));
+            else sum_part<T, false>(s, a.split, row, a.vocab, r, part, w, bins_of(false));
+            return;
+        }
     }
 
     // Elements that want(value) asks for, which no NaN or -infinity passes, into the
@@ -778,13 +1000,51 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
                        [&](T x) { return key ? x >= from : x > from; });
     };
 
+    uint64_t bins[2] = {0, 0};   // of the row's histogram, the thread's two
+    bool summed = REST && !by_p;   // whether the parts' sums of tiles hold what is left
+    if constexpr (REST) {
+        if (by_p) {
+            typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+#pragma unroll 8
+            for (int p = 0; p < a.split.parts; ++p) {
+                const u64x2 x = *gptr<u64x2>(a.split.bins(r, p) + 2 * t);
+                bins[0] += x[0];
+                bins[1] += x[1];
+            }
+            const uint64_t need = find_row_bin(s, bins[0], bins[1], [&](uint64_t all) { return share_of(top_p, all); });
+            const int bin = (int)s.bin;
+            const uint64_t behind = need - s.below;
+            if (!cut_part<T>(s, a.split, row, a.vocab, r, part, w, bins_of(false), bin, f.least)) return;
+            summed = join_lists(s, a.split, r, f.count);
+            if (summed) {
+                // the bin's keys lie close together
+                uint32_t most = 0, rest = 0;
+                for (int i = t; i < f.count; i += kSampleThreads) {
+                    const uint32_t k = (uint32_t)(s.list[i] >> 32);
+                    most = std::max(most, k);
+                    rest = std::max(rest, ~k);
+                }
+                most = (uint32_t)reduce<Larger>(s, most);
+                rest = most - ~(uint32_t)reduce<Larger>(s, rest);
+                uint64_t skipped;
+                const uint32_t key = most - select(s, rest ? 32 - __builtin_clz(rest) : 0, behind, skipped, [&](auto&& g) {
+                    for (int i = t; i < f.count; i += kSampleThreads) {
+                        const uint32_t k = (uint32_t)(s.list[i] >> 32);
+                        g(most - k, w.of(L::value(k)));
+                    }
+                });
+                const uint64_t one = w.of(L::value(key));
+                f.cut = Cut{key, (uint32_t)((behind - skipped + one - 1) / one)};
+            }
+        }
+    }
     bool held = false;   // whether the list holds all that the filters can leave
-    if (by_k || by_p || f.least) {
-        if (!by_k && !by_p) {
+    if (!summed && (by_k || by_p || f.least)) {
+        if (!REST && !by_k && !by_p) {
             f.count = collect_from(f.least);
             held = f.count <= kSampleList;
         }
-        if (near) {
+        if (!REST && near) {
             // a threshold that top_k threads' largest logits reach, to 1/64 of a power of two
             const auto coarse = [&](uint32_t k) { return min((top_key >> L::COARSE) - (k >> L::COARSE), (1u << kDigit) - 1); };
             const uint64_t want = std::min<uint64_t>(top_k, reduce(s, mine_key ? 1 : 0));
@@ -799,7 +1059,7 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
             f.top_p = top_p;
             if (!any) f.key_bits = L::COARSE + kDigit;
         }
-        if constexpr (L::COUNTED) {
+        if constexpr (L::COUNTED && !REST) {
             // With top-k, top-p is left to the list if that can hold what top-k leaves.
             bool weights = by_p && !(by_k && top_k <= kSampleList / 2);
             uint32_t kept = 0;   // at the cut or above
@@ -840,34 +1100,33 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
             f.top_k = 0;
             f.top_p = 1.0f;
 #pragma unroll 1
-            for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
-                const bool counts = filter == 0;
-                // 64 bins for one of the logits, or for a power of two of the weights
-                const float rate = counts ? 64.0f : __builtin_fminf((float)(w.c * (64.0 / kPowers)), 1e30f);
-                const auto bin_of = [&](float l) {
-                    const float d = (finite_top - __builtin_fminf(l, __FLT_MAX__)) * rate;
-                    return d < (float)(kSampleBins - 1) ? (int)d : kSampleBins - 1;
-                };
-                __syncthreads();
-                for (int i = t; i < kSampleBins; i += kSampleThreads) s.bins[i] = 0;
-                __syncthreads();
+            for (int filter = !REST && by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
+                const bool counts = !REST && filter == 0;
+                const auto bin_of = bins_of(counts);
                 const bool none = f.cut.key == 0;
                 const T cut = none ? nothing : (T)L::value(f.cut.key);
                 const auto left = [&](T x) { return none ? x > cut : x >= cut; };
-                for_row<T, 4, true>(row, a.vocab, [&](T x, int) {
-                    if (x > cut) {
-                        const uint64_t amount = counts ? 1 : w.of((float)x);
-                        if (amount) add_to_bin(s, (uint32_t)bin_of((float)x), amount);
-                    }
-                });
-                if (!counts && !none && t == 0) add_to_bin(s, (uint32_t)bin_of((float)cut), f.cut.quota * w.of((float)cut));
-                __syncthreads();
+                if constexpr (!REST) {
+                    __syncthreads();
+                    s.bins[t] = s.bins[t + kSampleThreads] = 0;
+                    __syncthreads();
+                    for_row<T, 4, true>(row, a.vocab, [&](T x, int) {
+                        if (x > cut) {
+                            const uint64_t amount = counts ? 1 : w.of((float)x);
+                            if (amount) add_to_bin(s, (uint32_t)bin_of((float)x), amount);
+                        }
+                    });
+                    if (!counts && !none && t == 0) add_to_bin(s, (uint32_t)bin_of((float)cut), f.cut.quota * w.of((float)cut));
+                    __syncthreads();
+                    bins[0] = s.bins[2 * t];
+                    bins[1] = s.bins[2 * t + 1];
+                }
                 uint64_t all = 0;
-                for (int i = t; i < kSampleBins; i += kSampleThreads) all += s.bins[i];
-                all = reduce(s, all);
-                const uint64_t need = counts ? (uint64_t)top_k : share_of(top_p, all);
+                const uint64_t need = find_row_bin(s, bins[0], bins[1], [&](uint64_t sum) {
+                    all = sum;
+                    return counts ? (uint64_t)top_k : share_of(top_p, sum);
+                });
                 if (need >= all) continue;
-                find_bin<kSampleBins / 64>(s, need, [](int i, int e) { return kSampleBins / 64 * i + e; });
                 const int bin = (int)s.bin;
                 const uint64_t before = s.below;
                 // all that is left, if it fits the list; else the bin that holds the cut
@@ -924,11 +1183,11 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
     const T cut = f.cut.key ? (T)L::value(f.cut.key) : nothing;
     const uint64_t one = f.cut.key ? w.of((float)cut) : 0;   // of each of those at the cut
     for (int i = t; i < tiles.count; i += kSampleThreads) {
-        s.tile_sum[i] = 0;
+        s.tile_sum[i] = summed ? left_at(a.split.tiles(r) + i) : 0;
         s.tile_equal[i] = 0;
     }
     __syncthreads();
-    if (held) {
+    if (summed || held) {
 #pragma unroll 1
         for (int i = t; i < f.count; i += kSampleThreads) {
             const uint32_t k = (uint32_t)(s.list[i] >> 32);
@@ -1052,10 +1311,34 @@ template <class T> __global__ __launch_bounds__(kSampleThreads) void sample_kern
 
 using namespace exq;
 
+namespace {
+
+constexpr int kSampleWorkgroups = 256;   // of a call whose rows are split
+constexpr int kSampleSplit = 16384;      // vocabularies that are
+
+int sample_parts(int rows, int vocab) {
+    return vocab < kSampleSplit ? 1 : std::max(1, std::min(kSampleParts, kSampleWorkgroups / rows));
+}
+
+template <bool REST> exq_status sample_call(int bits, const SampleArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.rows * a.split.parts));
+    if (bits == 16) hipLaunchKernelGGL((sample_kernel<_Float16, REST>), grid, dim3(kSampleThreads), 0, s, a);
+    else hipLaunchKernelGGL((sample_kernel<float, REST>), grid, dim3(kSampleThreads), 0, s, a);
+    return launched("sample launch");
+}
+
+}  // namespace
+
+extern "C" size_t exq_sample_workspace_bytes(int rows, int vocab) {
+    if (rows < 1 || vocab < 1) return 0;
+    const int parts = sample_parts(rows, vocab);
+    return parts > 1 ? SampleSplit{nullptr, rows, parts}.bytes() : 0;
+}
+
 extern "C" exq_status exq_sample(const void* logits, int bits, int rows, int vocab, int64_t row_stride, const float* u,
                                  const float* temperatures, float temperature, const int32_t* top_ks, int top_k,
                                  const float* top_ps, float top_p, const float* min_ps, float min_p, int32_t* tokens,
-                                 float* logprobs, void* stream) {
+                                 float* logprobs, void* workspace, size_t workspace_bytes, void* stream) {
     if (rows < 0 || vocab < 1) return fail(EXQ_ERR_INVALID_ARG, "rows=%d vocab=%d", rows, vocab);
     if (bits != 16 && bits != 32) return fail(EXQ_ERR_UNSUPPORTED, "logits of %d bits (16 or 32)", bits);
     if (vocab > 1 << kSampleMaxVocabLog2) return fail(EXQ_ERR_UNSUPPORTED, "vocab=%d over 2^%d", vocab, kSampleMaxVocabLog2);
@@ -1085,12 +1368,28 @@ extern "C" exq_status exq_sample(const void* logits, int bits, int rows, int voc
             if (y.p && ranges_meet(x.p, n, y.p, n)) return fail(EXQ_ERR_INVALID_ARG, "%s overlaps %s", x.name, y.name);
     }
     if (logprobs && ranges_meet(tokens, n, logprobs, n)) return fail(EXQ_ERR_INVALID_ARG, "tokens overlaps logprobs");
+    int parts = 1;
+    if (workspace) {
+        const size_t need = exq_sample_workspace_bytes(rows, vocab);
+        if (!aligned(workspace, 16)) return fail(EXQ_ERR_INVALID_ARG, "workspace is misaligned");
+        if (workspace_bytes < need) return fail(EXQ_ERR_INVALID_ARG, "workspace of %zu bytes: %zu are needed", workspace_bytes, need);
+        if (need && ranges_meet(workspace, need, logits, logits_bytes)) return fail(EXQ_ERR_INVALID_ARG, "workspace overlaps logits");
+        for (const auto& x : read)
+            if (need && x.p && ranges_meet(workspace, need, x.p, n)) return fail(EXQ_ERR_INVALID_ARG, "workspace overlaps %s", x.name);
+        for (const auto& x : written)
+            if (need && x.p && ranges_meet(workspace, need, x.p, n)) return fail(EXQ_ERR_INVALID_ARG, "workspace overlaps %s", x.name);
+        // (settings for all rows that leave no row to split)
+        const bool no_row = (!temperatures && temperature == 0) || (!top_ks && top_k > 0 && top_k < vocab) || (!top_ps && top_p <= 0) ||
+                            (!min_ps && min_p > 0 && !top_ps && top_p >= 1);
+        if (need && !no_row) parts = sample_parts(rows, vocab);
+    }
     int log2 = 0;
     while ((1 << log2) < vocab) ++log2;
     const SampleArgs a{logits, row_stride, rows, vocab, std::min(51, 63 - log2), u, {temperatures, temperature},
-                       {top_ks, top_k}, {top_ps, top_p}, {min_ps, min_p}, tokens, logprobs};
+                       {top_ks, top_k}, {top_ps, top_p}, {min_ps, min_p}, tokens, logprobs,
+                       {static_cast<uint64_t*>(workspace), rows, parts}};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (bits == 16) hipLaunchKernelGGL((sample_kernel<_Float16>), dim3((unsigned)rows), dim3(kSampleThreads), 0, s, a);
-    else hipLaunchKernelGGL((sample_kernel<float>), dim3((unsigned)rows), dim3(kSampleThreads), 0, s, a);
-    return launched("sample launch");
+    exq_status st;
+    if ((st = sample_call<false>(bits, a, s)) != EXQ_OK || parts == 1) return st;
+    return sample_call<true>(bits, a, s);
 }

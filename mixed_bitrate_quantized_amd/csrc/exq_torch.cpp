@@ -538,9 +538,12 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         THPObjectPtr value(want ? PyTuple_Pack(2, tokens.get(), logs.get()) : Py_NewRef(tokens.get()));
         if (!value) return nullptr;
+        const size_t bytes = exq_sample_workspace_bytes((int)rows, (int)vocab);
+        at::Tensor workspace;
+        if (bytes) workspace = empty(c, {(int64_t)bytes}, at::kByte);
         return status_or(exq_sample(l->data_ptr(), wide ? 32 : 16, (int)rows, (int)vocab, rows > 1 ? l->stride(0) : 0, u.p,
                                     temperature.p, temperature.all, top_k.p, top_k.all, top_p.p, top_p.all, min_p.p, min_p.all,
-                                    const_cast<int32_t*>(tokens_p), logs_p, c.stream),
+                                    const_cast<int32_t*>(tokens_p), logs_p, bytes ? workspace.data_ptr() : nullptr, bytes, c.stream),
                          "exq_sample", std::move(value));
     });
 }

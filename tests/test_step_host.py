@@ -176,10 +176,13 @@ def test_lora_without_rows_or_adapters(adapters):
 
 def sample_args(**kw):
     a = dict(logits=at(0), bits=16, rows=4, vocab=1000, stride=1000, u=at(1), ts=None, t=1.0, ks=None, k=0, ps=None, p=1.0, ms=None,
-             m=0.0, tokens=at(2), logs=at(3))
+             m=0.0, tokens=at(2), logs=at(3), ws=None, bytes=0)
     a.update(kw)
     return [a[x] for x in ("logits", "bits", "rows", "vocab", "stride", "u", "ts", "t", "ks", "k", "ps", "p", "ms", "m", "tokens",
-                           "logs")] + [0]
+                           "logs", "ws", "bytes")] + [0]
+
+
+SPLIT = dict(rows=2, vocab=32000, stride=32000, ws=at(5), bytes=1 << 20)   # rows that a workspace shares out
 
 
 NAN = float("nan")
@@ -190,7 +193,9 @@ NAN = float("nan")
     (I, dict(vocab=0)), (U, dict(vocab=(1 << 21) + 1)), (I, dict(stride=999)), (I, dict(stride=-1)), (I, dict(u=0)),
     (I, dict(u=at(1) + 2)), (I, dict(t=-1.0)), (I, dict(t=NAN)), (I, dict(p=NAN)), (I, dict(m=NAN)), (I, dict(ts=at(4) + 1)),
     (I, dict(ks=at(4) + 2)), (I, dict(tokens=0)), (I, dict(logs=at(3) + 2)), (I, dict(tokens=at(0) + 7996)), (I, dict(tokens=at(1))),
-    (I, dict(logs=at(2) + 12)), (I, dict(ms=at(2) - 12)), (I, dict(ps=at(3)))], ids=str)
+    (I, dict(logs=at(2) + 12)), (I, dict(ms=at(2) - 12)), (I, dict(ps=at(3))),
+    (I, dict(SPLIT, ws=at(5) + 4)), (I, dict(SPLIT, bytes=1000)), (I, dict(SPLIT, ws=at(0) + 64)), (I, dict(SPLIT, ws=at(1))),
+    (I, dict(SPLIT, ws=at(2) - 64)), (I, dict(SPLIT, ts=at(5) + 800))], ids=str)
 def test_sample_rejects(status, bad):
     expect(status, exq.exq_sample, *sample_args(**bad))
 
