@@ -1313,11 +1313,17 @@ using namespace exq;
 
 namespace {
 
-constexpr int kSampleWorkgroups = 256;   // of a call whose rows are split
-constexpr int kSampleSplit = 16384;      // vocabularies that are
+constexpr int kSampleWorkgroups = 256;   // of a call whose rows are split: one to a CU
+constexpr int kSampleSplit = 16384;      // smallest vocabulary that is
+constexpr int kSampleShare = 4096;       // logits of a part, at least
 
+// The second launch and what parts leave for one another cost 6 us.  Without and with
+// it (us; drawn from all, and from a nucleus of 0.9):
+//   1 x 8192 fp32    9.1, 10.6   19.5, 22.6       1 x 131072 fp16   47, 16.5   39, 30
+//   1 x 16384 fp32   12.5, 11.2  25.1, 22.0       128 x 50001 fp16  23.8, 19.2   34.6, 36.2
+//   1 x 32000 fp16   16.9, 12.3  23.7, 23.5       128 x 50001 fp32  28.9, 22.4   53, 40
 int sample_parts(int rows, int vocab) {
-    return vocab < kSampleSplit ? 1 : std::max(1, std::min(kSampleParts, kSampleWorkgroups / rows));
+    return vocab < kSampleSplit ? 1 : std::max(1, std::min(std::min(kSampleParts, vocab / kSampleShare), kSampleWorkgroups / rows));
 }
 
 template <bool REST> exq_status sample_call(int bits, const SampleArgs& a, hipStream_t s) {
