@@ -567,7 +567,7 @@ __device__ __forceinline__ uint64_t share_of(float top_p, uint64_t total) {   //
     return std::min<uint64_t>(std::max<uint64_t>((uint64_t)__builtin_ceil((double)top_p * (double)total), 1), total);
 }
 __device__ __forceinline__ uint64_t target_of(float u, uint64_t total) {
-    return std::min<uint64_t>((uint64_t)((double)u * (double)total), total - 1);
+    return std::min<uint64_t>((uint64_t)((double)__builtin_fminf(u, 1.0f) * (double)total), total - 1);
 }
 
 // What is known of a row, and what is left to do on its list of candidates.

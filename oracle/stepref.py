@@ -65,8 +65,9 @@ def rotate(x, positions, rates, factor, rotary_dim, interleaved):
             a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
             t = float(p) * float(rates[i])
             c, s = np.cos(t) * factor, np.sin(t) * factor
-            out[r, :, a] = x[r, :, a] * c - x[r, :, b] * s
-            out[r, :, b] = x[r, :, a] * s + x[r, :, b] * c
+            with np.errstate(invalid="ignore"):   # infinities among the channels
+                out[r, :, a] = x[r, :, a] * c - x[r, :, b] * s
+                out[r, :, b] = x[r, :, a] * s + x[r, :, b] * c
     return out
 
 
@@ -93,11 +94,10 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     l = np.asarray(logits, dtype=np.float64)
     if any(np.isnan(v) for v in (u, temperature, top_p, min_p)) or temperature < 0:
         return -1, np.nan, 1.0
-    order = [i for i in np.lexsort((np.arange(l.size), -np.where(np.isnan(l), -np.inf, l)))
-             if not np.isnan(l[i]) and l[i] != -np.inf]
-    if not order:
+    order = np.lexsort((np.arange(l.size), -np.where(np.isnan(l), -np.inf, l)))
+    order = order[~np.isnan(l[order]) & (l[order] != -np.inf)]
+    if not order.size:
         return -1, np.nan, 1.0
-    order = np.array(order)
     if temperature == 0:
         return int(order[0]), 0.0, 1.0
     top = l[order[0]]

@@ -60,7 +60,7 @@ def extend_both(pool, want, counts, rows, what=""):
 
 # one workgroup does all of a call, a second launch the rest of it, sequences in several passes
 @pytest.mark.parametrize("sequences,page,width,most", [(1, 16, 8, 40), (3, 1, 50, 20), (64, 48, 9, 100), (255, 16, 6, 30),
-                                                       (257, 16, 20, 90), (1100, 32, 4, 9), (5000, 16, 3, 12), (9000, 64, 2, 3)])
+                                                       (257, 16, 20, 90), (1100, 32, 4, 9), (1100, 16, 20, 40), (5000, 16, 3, 12), (9000, 64, 2, 3)])
 def test_pages_of_a_changing_batch(exq, sequences, page, width, most):
     note("pages: %d sequences" % sequences)
     rng = np.random.default_rng(sequences)
@@ -275,6 +275,20 @@ def test_lora_of_few_distinct_rows_and_one_adapter(exq):
         check_lora(dy, x, ids, y, a, b, None, None, "%d rows in place" % rows)
 
 
+@pytest.mark.parametrize("rows,count", [(64, 64), (65, 64), (511, 3), (512, 3), (9000, 5000), (20000, 2)])
+def test_lora_of_many_rows_and_adapters(exq, rows, count):
+    """On both sides of where rows are grouped and tiled otherwise; more rows than a thread keeps, more adapters than threads."""
+    rng = np.random.default_rng(rows + count)
+    K, N, rank = 72, 88, 8
+    a, b, scales, ranks = stack(rng, count, K, N, rank)
+    adapters = exq.Adapters(to_dev(a), to_dev(b), f32(scales), i32(ranks))
+    x, y = (rng.standard_normal((rows, n)).astype(np.float16) for n in (K, N))
+    for ids in (rng.permutation(np.arange(rows) % (count + 1) - 1), rng.integers(-1, count + 1, rows)):
+        out = adapters.add(to_dev(x), i32(ids), to_dev(y))
+        pick = np.unique(np.concatenate([np.arange(min(rows, 300)), rng.integers(0, rows, 700), np.arange(rows - 40, rows)]))
+        check_lora(out[torch.tensor(pick, device="cuda")], x[pick], ids[pick], y[pick], a, b, scales, ranks, "%d rows of %d" % (rows, count))
+
+
 def test_lora_large_small_and_non_finite_values(exq):
     """Inner products far beyond fp16, and far below; a row with an infinity leaves its neighbours alone."""
     rng = np.random.default_rng(9)
@@ -420,7 +434,7 @@ def test_sample_settings_of_each_row_and_padding_rows(exq):
                     top_p=rng.choice([-1.0, 0.3, 0.95, 1.0, 7.0], rows).astype(np.float32), min_p=rng.choice([-1.0, 0.0, 0.02, 3.0], rows).astype(np.float32))
     settings["temperature"][3], settings["top_p"][5], settings["min_p"][6], settings["temperature"][7] = np.nan, np.nan, np.nan, -1.0
     u = rng.random(rows).astype(np.float32)
-    u[8], u[9], u[10] = np.nan, 1.0, 5.0
+    u[8], u[9], u[10], u[11] = np.nan, 1.0, 5.0, np.inf
     check_sample(exq, logits, u, "each", **settings)
     u[::3] = -1.0
     tokens = torch.full((rows,), 99, dtype=torch.int32, device="cuda")
@@ -459,6 +473,68 @@ def test_sample_many_rows_and_the_largest_vocabulary(exq):
     big = likely(rng, 1, 1 << 21)
     for settings in (dict(), dict(top_p=0.9), dict(top_k=50), dict(top_k=1 << 20)):
         check_sample(exq, big, rng.random(1), "2^21 %s" % settings, True, **settings)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_sample_of_more_rows_than_are_shared_out(exq, wide):
+    """Long rows that a workgroup has to itself."""
+    rng = np.random.default_rng(18)
+    x = likely(rng, 260, 20011)
+    x[3, rng.random(20011) < 0.5] = -np.inf
+    for settings in (dict(), dict(top_p=0.9), dict(temperature=3.0, top_p=0.98, min_p=0.01), dict(top_k=7000, top_p=0.95)):
+        check_sample(exq, x, rng.random(260), "260 rows %s" % settings, wide, **settings)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("rows,vocab", [(1, 16384), (2, 16391), (3, 70001), (17, 50001), (51, 16400), (85, 20001), (128, 16385), (129, 16385)])
+def test_sample_rows_shared_out(exq, rows, vocab, wide):
+    """Every number of parts, with rows that begin and end anywhere, masked ones and flat ones."""
+    rng = np.random.default_rng(rows + vocab)
+    x = likely(rng, rows, vocab)
+    x[rng.integers(0, rows), :] *= 0.01
+    x[rng.integers(0, rows), rng.random(vocab) < 0.99] = -np.inf
+    x = x.astype(np.float32 if wide else np.float16)
+    d = torch.full((rows, vocab + 5), float("nan"), dtype=torch.float32 if wide else torch.float16, device="cuda")
+    for settings in (dict(), dict(top_p=0.9), dict(temperature=2.0, top_p=0.5, min_p=0.02)):
+        u = rng.random(rows)
+        want = check_sample(exq, x, u, "%d rows %s" % (rows, settings), wide, **settings)
+        for offset in (1, 5):
+            d[:, offset:offset + vocab] = to_dev(x)
+            np.testing.assert_array_equal(host(exq.sample(d[:, offset:offset + vocab], f32(u), **settings)), want)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_sample_equal_logits_beyond_any_counter_and_list(exq, wide):
+    """131072 equal logits: more than 16 bits count, than a list of candidates holds and than one power of two of bins tells apart."""
+    rng = np.random.default_rng(19)
+    same = np.zeros((3, 131072))
+    same[1, :70000] = 1.0
+    same[2, 5::2] = -np.inf
+    u = np.array([0.1, 0.7, 0.999])
+    for settings in (dict(), dict(top_p=0.5), dict(top_k=100000), dict(top_k=69999, top_p=0.9), dict(top_k=20), dict(top_k=901, top_p=0.5),
+                     dict(top_p=0.9, min_p=0.5), dict(min_p=0.99)):
+        check_sample(exq, same, u, "equal %s" % settings, wide, **settings)
+    many = np.zeros((130, 131072), dtype=np.float16)      # a workgroup to a row
+    many[:, 100000:] = rng.integers(-2, 1, (130, 31072))
+    d = to_dev(many.astype(np.float32) if wide else many)
+    for settings in (dict(top_p=0.5), dict()):
+        got = host(exq.sample(d, f32([0.37] * 130), **settings))
+        for r in (0, 64, 129):
+            assert got[r] == ref.sample_row(many[r], np.float32(0.37), **{k: np.float32(v) for k, v in settings.items()})[0], (r, settings)
+
+
+@pytest.mark.parametrize("vocab", [9000, 40000])
+def test_sample_between_its_ways_to_find_the_top(exq, vocab):
+    """A top-k on both sides of each way's limits, with ties at the end of it, nuclei that leave a list of any length, and min-p
+    alone from one token to all."""
+    rng = np.random.default_rng(vocab)
+    x = likely(rng, 3, vocab)
+    x[1] = np.round(x[1] * 4) / 4          # many ties
+    x[2] = 0.02 * x[2]                     # flat
+    for wide in (False, True):
+        for settings in ([dict(top_k=k, top_p=p) for k in (127, 129, 899, 900, 901, 2048, 2049, 4096, 4097, 6000) for p in (1.0, 0.9)]
+                         + [dict(min_p=p) for p in (1e-30, 1e-6, 1e-3, 0.3, 0.97, 1.0)] + [dict(temperature=2.0, top_k=3000, top_p=0.9, min_p=0.3)]):
+            check_sample(exq, x, rng.random(3), "%d %s" % (vocab, settings), wide, **settings)
 
 
 def test_sample_draws_the_shares(exq):
@@ -540,6 +616,37 @@ def test_graphs_replay_with_new_values(exq):
         torch.cuda.synchronize()
         for i, (x, y) in enumerate(zip(got, want)):
             assert torch.equal(x, y), (rep, i)
+
+
+def test_shared_out_draws_on_two_streams_and_in_graphs(exq):
+    """Long rows on two streams at a time, eager and replayed: each call has a workspace of its own."""
+    rng = np.random.default_rng(25)
+    logits = [to_dev(likely(rng, 4, 50001).astype(np.float16)) for _ in range(2)]
+    u = [f32(rng.random(4)) for _ in range(2)]
+    note("graph capture of draws")
+    draw = lambda i: exq.sample(logits[i], u[i], top_p=0.9, return_logprobs=True)
+    streams, graphs = [torch.cuda.Stream() for _ in range(2)], []
+    for i in range(2):
+        draw(i)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, draw(i)))
+    for rep in range(5):
+        for i in range(2):
+            logits[i].copy_(to_dev(likely(rng, 4, 50001).astype(np.float16)))
+            u[i].copy_(f32(rng.random(4)))
+        want = [draw(i) for i in range(2)]
+        torch.cuda.synchronize()
+        got = []
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got.append([draw(i) for _ in range(8)])
+                graphs[i][0].replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for tokens, logs in got[i] + [graphs[i][1]]:
+                assert torch.equal(tokens, want[i][0]) and torch.equal(logs, want[i][1]), (rep, i)
+            assert host(want[i][0]).tolist() == [ref.sample_row(l, x, top_p=np.float32(0.9))[0] for l, x in zip(host(logits[i]), host(u[i]))]
 
 
 def test_calls_are_deterministic(exq):
