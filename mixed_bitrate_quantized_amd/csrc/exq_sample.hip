@@ -36,6 +36,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
 constexpr int kSampleList = 4096;             // candidates that LDS holds
 constexpr int kSampleNear = 900;              // a top-k that is looked for from the threads' largest logits
+constexpr int kSampleFew = 256;               // candidates that are compared one by one
 constexpr int kDigit = 9;                     // bits looked at together
 constexpr int kSampleBins = 2048;             // of a row's histogram
 constexpr int kSampleParts = 16;              // of a row, at most
@@ -215,9 +216,9 @@ struct SampleShared {
     uint32_t cut_key, cut_above, cut_equal;
     double cut_weight_above, cut_weight, cut_need;
     double log_min_p;
-    // of up to 128 candidates: their places among the others
-    uint32_t rank[128];
-    uint64_t before[128];
+    // of few candidates: their places among the others, weights before them
+    uint32_t rank[kSampleFew];
+    uint64_t before[kSampleFew];
 };
 
 // Over the workgroup: the sum of the threads before (with BEFORE), and of all.
@@ -578,63 +579,60 @@ struct Row {
     int key_bits;        // candidates' keys lie within 2^key_bits of the top
     int top_k;           // 0: done
     float top_p;         // 1 or more: done
-    uint64_t share;      // what top-p needs, if that is known; else 0
     Cut cut;
     uint32_t least;      // the smallest key that min-p leaves
     float u, temperature;
 };
 
-// Up to 128 candidates: every one is compared with every other, by all threads.
+// Up to kSampleFew candidates: every one is compared with every other, by all
+// threads, which gives each its place in the filters' order and in the index's.
+// Weights put there leave a sum over the threads before for either.
 template <class T, class A>
 __device__ __forceinline__ void finish_few(SampleShared& s, const Weights& w, const Row& f, A&& answer) {
     typedef Logit<T> L;
-    const int t = threadIdx.x, n = f.count <= 64 ? 64 : 128, i = t & (n - 1), group = t / n, per = n * n / kSampleThreads;
+    const int t = threadIdx.x, n = f.count <= 64 ? 64 : f.count <= 128 ? 128 : kSampleFew;
+    const int i = t & (n - 1), group = t / n, per = n * n / kSampleThreads;
+    const bool one = t < f.count;   // the thread has the list's t-th
     const uint64_t x = i < f.count ? s.list[i] : 0;
     const uint32_t key = (uint32_t)(x >> 32), index = (uint32_t)x;
-    const uint64_t weight = key ? w.of(L::value(key)) : 0;
-    if (t < n) {
-        s.weights[t] = weight;
-        s.rank[t] = 0;
-        s.before[t] = 0;
-    }
+    const uint64_t weight = one ? w.of(L::value(key)) : 0;
+    if (t < n) s.rank[t] = 0;
     __syncthreads();
-    // those before it in the filters' order, their number and weights, and those of its key
     const int first_j = group * per, last_j = std::min(f.count, first_j + per);
     uint32_t rank = 0;
-    uint64_t before = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int j = first_j; j < last_j; ++j) {
         const uint64_t y = s.list[j];
-        const uint32_t k = (uint32_t)(y >> 32);
-        const bool tie = k == key && (uint32_t)y < index;
-        rank += (k > key || tie ? 1 : 0) + (tie ? 0x10000 : 0);
-        before += k > key || tie ? s.weights[j] : 0;
+        rank += ((y ^ 0xFFFFFFFFu) > (x ^ 0xFFFFFFFFu) ? 1u : 0u) + ((uint32_t)y < index ? 0x10000u : 0u);
     }
-    if (rank) atomicAdd(&s.rank[i], rank);
-    if (before) atomicAdd(reinterpret_cast<unsigned long long*>(&s.before[i]), (unsigned long long)before);
+    if (rank && i < f.count) atomicAdd(&s.rank[i], rank);
     __syncthreads();
-    rank = s.rank[i] & 0xFFFFu;
-    before = s.before[i];
-    bool in = key && (key > f.cut.key || (key == f.cut.key && s.rank[i] >> 16 < f.cut.quota));
-    if (f.top_k) in = in && rank < (uint32_t)f.top_k;
+    const uint32_t place = one ? s.rank[t] & 0xFFFFu : 0, at = one ? s.rank[t] >> 16 : 0;
+    uint32_t limit = f.top_k ? std::min(f.top_k, f.count) : f.count;   // places left
+    if (f.cut.key) limit = (uint32_t)std::min<uint64_t>(limit, reduce(s, one && key > f.cut.key) + f.cut.quota);
+    bool in = one && place < limit;
     if (f.top_p < 1.0f) {
-        const uint64_t need = f.share ? f.share : share_of(f.top_p, reduce(s, in && t < n ? weight : 0));
-        in = in && before < need;
+        if (one) s.before[place] = in ? weight : 0;
+        __syncthreads();
+        const uint64_t here = one ? s.before[t] : 0;
+        uint64_t before;
+        const uint64_t need = share_of(f.top_p, reduce<Sum, true>(s, here, &before));
+        if (one) s.before[t] = before;
+        __syncthreads();
+        in = in && s.before[place] < need;
     }
-    in = in && key >= f.least;
-    const uint64_t mine = in ? weight : 0, sum = reduce(s, t < n ? mine : 0), target = target_of(f.u, sum);
-    if (t < n) {
-        s.weights[t] = mine;
-        s.before[t] = 0;
+    if (one) {
+        s.list[at] = x;
+        s.weights[at] = in && key >= f.least ? weight : 0;
     }
     __syncthreads();
-    uint64_t lower = 0;   // of those left, with lower indices
-#pragma unroll 1
-    for (int j = first_j; j < last_j; ++j) lower += (uint32_t)s.list[j] < index ? s.weights[j] : 0;
-    if (lower) atomicAdd(reinterpret_cast<unsigned long long*>(&s.before[i]), (unsigned long long)lower);
-    __syncthreads();
-    lower = s.before[i];
-    if (t < n && mine && lower <= target && target < lower + mine) answer((int)index, w.log_of(L::value(key), f.temperature, sum));
+    const uint64_t mine = one ? s.weights[t] : 0;
+    uint64_t lower;
+    const uint64_t sum = reduce<Sum, true>(s, mine, &lower), target = target_of(f.u, sum);
+    if (mine && lower <= target && target < lower + mine) {
+        const uint64_t y = s.list[t];
+        answer((int)(uint32_t)y, w.log_of(L::value((uint32_t)(y >> 32)), f.temperature, sum));
+    }
 }
 
 // The cut of a longer list, from the filters that are left to do.
@@ -654,7 +652,7 @@ template <class T> __device__ __forceinline__ void filter_list(SampleShared& s, 
         each([&](uint32_t k, uint64_t x) { all += k < f.cut.key ? 0 : counts ? 1 : k > f.cut.key ? x : 0; });
         all = reduce(s, all);
         if (!counts && f.cut.key) all += f.cut.quota * w.of(L::value(f.cut.key));
-        const uint64_t need = counts ? (uint64_t)f.top_k : f.share ? f.share : share_of(f.top_p, all);
+        const uint64_t need = counts ? (uint64_t)f.top_k : share_of(f.top_p, all);
         if (need >= all) continue;
         const uint32_t key = f.top_key - select(s, f.key_bits, need, below, [&](auto&& g) {
             each([&](uint32_t k, uint64_t x) {
@@ -837,10 +835,11 @@ __device__ __forceinline__ bool join_lists(SampleShared& s, const SampleSplit& s
 }
 
 // A workgroup to a row.  Rows whose every logit has to be weighed are shared out over
-// split.parts of them if there are: all look for the largest logit and each weighs a
-// part.  A second launch (REST) does what then is left: the draw, or, with top-p,
-// each part that of its logits at and above the end of it and the last one the draw.
-template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
+// split.parts of them if there are.  A launch before (FIRST) has all of them look for
+// the largest logit and each weigh a part.  Then one of them draws, or, with top-p,
+// each does that part's logits at and above the end of it and the last one draws.
+// Rows that are not split have their one workgroup beside these.
+template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void sample_kernel(SampleArgs a) {
     __shared__ SampleShared s;
     typedef Logit<T> L;
     typedef typename L::vec vec;
@@ -855,14 +854,14 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
         if (a.logprobs) a.logprobs[r] = logprob;
     };
     if (!(temperature >= 0.0f) || u != u || top_p != top_p || min_p != min_p) {
-        if (!REST && part == 0 && t == 0) answer(-1, __builtin_nanf(""));
+        if (!FIRST && part == 0 && t == 0) answer(-1, __builtin_nanf(""));
         return;
     }
     const bool first_only = temperature == 0.0f || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
     const bool near = by_k && top_k <= kSampleNear;   // top-k from the threads' largest logits
     const bool split = a.split.parts > 1 && !first_only && !by_k && (by_p || !(min_p > 0.0f));
-    if (split ? REST && !by_p && part : REST || part) return;   // what one workgroup, or the first launch's, has all of
+    if (split ? !FIRST && !by_p && part : FIRST || part) return;   // what one workgroup has all of
     bool counted = L::COUNTED && !split && !first_only && !near && (by_k || by_p);
     if (t < kPowers) s.powers[t] = exp2_series((double)t / kPowers);
     if (t == 0) s.bin = s.below = 0;
@@ -873,10 +872,9 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
     int mine_at = 0;
     uint32_t mine_key = 0;
     uint64_t best;
-    if constexpr (REST) {
+    if (!FIRST && split) {
         best = *a.split.best(r);
         __syncthreads();
-        if (best == 0) return;
     } else {
         const auto look = [&](float x, int i) {
             if (x > mine) {
@@ -905,14 +903,14 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
         });
         mine_key = L::key((T)mine);
         best = reduce<Larger>(s, mine_key ? (uint64_t)mine_key << 32 | (uint32_t)~mine_at : 0);
-        if (split && part == 0 && t == 0) {
-            *a.split.best(r) = best;
-            *a.split.done(r) = 0;
-        }
-        if (best == 0) {   // nothing that may be drawn
-            if (part == 0 && t == 0) answer(-1, __builtin_nanf(""));
-            return;
-        }
+    }
+    if (FIRST && part == 0 && t == 0) {
+        *a.split.best(r) = best;
+        *a.split.done(r) = 0;
+    }
+    if (best == 0) {   // nothing that may be drawn
+        if (!FIRST && part == 0 && t == 0) answer(-1, __builtin_nanf(""));
+        return;
     }
     const uint32_t top_key = (uint32_t)(best >> 32);
     if (first_only) {
@@ -926,7 +924,7 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
     const float topf = L::value(top_key), finite_top = __builtin_fminf(topf, __FLT_MAX__);
     const Weights w{topf, (double)finite_top, topf > __FLT_MAX__ ? 1e300 : kPowers * 1.4426950408889634074 / (double)temperature,
                     (double)(1ull << a.shift), s.powers};
-    Row f{0, a.vocab, top_key, L::BITS, 0, 1.0f, 0, Cut{0, 0xFFFFFFFFu}, 0, u, temperature};
+    Row f{0, a.vocab, top_key, L::BITS, 0, 1.0f, Cut{0, 0xFFFFFFFFu}, 0, u, temperature};
     if (min_p > 0.0f) {   // w >= min-p where the logit is M + T ln(min-p) or more
         const double least = min_p == 1.0f ? (double)topf : (double)topf + (double)temperature * s.log_min_p;
         f.least = L::first_from(least);
@@ -940,12 +938,10 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
             return d < (float)(kSampleBins - 1) ? (int)d : kSampleBins - 1;
         };
     };
-    if constexpr (!REST) {
-        if (split) {
-            if (by_p) sum_part<T, true>(s, a.split, row, a.vocab, r, part, w, bins_of(false));
-            else sum_part<T, false>(s, a.split, row, a.vocab, r, part, w, bins_of(false));
-            return;
-        }
+    if constexpr (FIRST) {
+        if (by_p) sum_part<T, true>(s, a.split, row, a.vocab, r, part, w, bins_of(false));
+        else sum_part<T, false>(s, a.split, row, a.vocab, r, part, w, bins_of(false));
+        return;
     }
 
     // Elements that want(value) asks for, which no NaN or -infinity passes, into the
@@ -1001,50 +997,48 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
     };
 
     uint64_t bins[2] = {0, 0};   // of the row's histogram, the thread's two
-    bool summed = REST && !by_p;   // whether the parts' sums of tiles hold what is left
-    if constexpr (REST) {
-        if (by_p) {
-            typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+    bool summed = split && !by_p;   // whether the parts' sums of tiles hold what is left
+    if (split && by_p) {
+        typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
 #pragma unroll 8
-            for (int p = 0; p < a.split.parts; ++p) {
-                const u64x2 x = *gptr<u64x2>(a.split.bins(r, p) + 2 * t);
-                bins[0] += x[0];
-                bins[1] += x[1];
+        for (int p = 0; p < a.split.parts; ++p) {
+            const u64x2 x = *gptr<u64x2>(a.split.bins(r, p) + 2 * t);
+            bins[0] += x[0];
+            bins[1] += x[1];
+        }
+        const uint64_t need = find_row_bin(s, bins[0], bins[1], [&](uint64_t all) { return share_of(top_p, all); });
+        const int bin = (int)s.bin;
+        const uint64_t behind = need - s.below;
+        if (!cut_part<T>(s, a.split, row, a.vocab, r, part, w, bins_of(false), bin, f.least)) return;
+        summed = join_lists(s, a.split, r, f.count);
+        if (summed) {
+            // the bin's keys lie close together
+            uint32_t most = 0, rest = 0;
+            for (int i = t; i < f.count; i += kSampleThreads) {
+                const uint32_t k = (uint32_t)(s.list[i] >> 32);
+                most = std::max(most, k);
+                rest = std::max(rest, ~k);
             }
-            const uint64_t need = find_row_bin(s, bins[0], bins[1], [&](uint64_t all) { return share_of(top_p, all); });
-            const int bin = (int)s.bin;
-            const uint64_t behind = need - s.below;
-            if (!cut_part<T>(s, a.split, row, a.vocab, r, part, w, bins_of(false), bin, f.least)) return;
-            summed = join_lists(s, a.split, r, f.count);
-            if (summed) {
-                // the bin's keys lie close together
-                uint32_t most = 0, rest = 0;
+            most = (uint32_t)reduce<Larger>(s, most);
+            rest = most - ~(uint32_t)reduce<Larger>(s, rest);
+            uint64_t skipped;
+            const uint32_t key = most - select(s, rest ? 32 - __builtin_clz(rest) : 0, behind, skipped, [&](auto&& g) {
                 for (int i = t; i < f.count; i += kSampleThreads) {
                     const uint32_t k = (uint32_t)(s.list[i] >> 32);
-                    most = std::max(most, k);
-                    rest = std::max(rest, ~k);
+                    g(most - k, w.of(L::value(k)));
                 }
-                most = (uint32_t)reduce<Larger>(s, most);
-                rest = most - ~(uint32_t)reduce<Larger>(s, rest);
-                uint64_t skipped;
-                const uint32_t key = most - select(s, rest ? 32 - __builtin_clz(rest) : 0, behind, skipped, [&](auto&& g) {
-                    for (int i = t; i < f.count; i += kSampleThreads) {
-                        const uint32_t k = (uint32_t)(s.list[i] >> 32);
-                        g(most - k, w.of(L::value(k)));
-                    }
-                });
-                const uint64_t one = w.of(L::value(key));
-                f.cut = Cut{key, (uint32_t)((behind - skipped + one - 1) / one)};
-            }
+            });
+            const uint64_t one = w.of(L::value(key));
+            f.cut = Cut{key, (uint32_t)((behind - skipped + one - 1) / one)};
         }
     }
     bool held = false;   // whether the list holds all that the filters can leave
     if (!summed && (by_k || by_p || f.least)) {
-        if (!REST && !by_k && !by_p) {
+        if (!by_k && !by_p) {
             f.count = collect_from(f.least);
             held = f.count <= kSampleList;
         }
-        if (!REST && near) {
+        if (near) {
             // a threshold that top_k threads' largest logits reach, to 1/64 of a power of two
             const auto coarse = [&](uint32_t k) { return min((top_key >> L::COARSE) - (k >> L::COARSE), (1u << kDigit) - 1); };
             const uint64_t want = std::min<uint64_t>(top_k, reduce(s, mine_key ? 1 : 0));
@@ -1059,7 +1053,7 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
             f.top_p = top_p;
             if (!any) f.key_bits = L::COARSE + kDigit;
         }
-        if constexpr (L::COUNTED && !REST) {
+        if constexpr (L::COUNTED) {
             // With top-k, top-p is left to the list if that can hold what top-k leaves.
             bool weights = by_p && !(by_k && top_k <= kSampleList / 2);
             uint32_t kept = 0;   // at the cut or above
@@ -1100,13 +1094,13 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
             f.top_k = 0;
             f.top_p = 1.0f;
 #pragma unroll 1
-            for (int filter = !REST && by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
-                const bool counts = !REST && filter == 0;
+            for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
+                const bool counts = filter == 0;
                 const auto bin_of = bins_of(counts);
                 const bool none = f.cut.key == 0;
                 const T cut = none ? nothing : (T)L::value(f.cut.key);
                 const auto left = [&](T x) { return none ? x > cut : x >= cut; };
-                if constexpr (!REST) {
+                if (!split) {
                     __syncthreads();
                     s.bins[t] = s.bins[t + kSampleThreads] = 0;
                     __syncthreads();
@@ -1169,7 +1163,7 @@ template <class T, bool REST> __global__ __launch_bounds__(kSampleThreads) void 
                 f.cut = Cut{top_key - d, (uint32_t)((need - skipped + one - 1) / one)};
             }
         }
-        if (held && f.count <= 128) {
+        if (held && f.count <= kSampleFew) {
             finish_few<T>(s, w, f, answer);
             return;
         }
@@ -1326,10 +1320,10 @@ int sample_parts(int rows, int vocab) {
     return vocab < kSampleSplit ? 1 : std::max(1, std::min(std::min(kSampleParts, vocab / kSampleShare), kSampleWorkgroups / rows));
 }
 
-template <bool REST> exq_status sample_call(int bits, const SampleArgs& a, hipStream_t s) {
+template <bool FIRST> exq_status sample_call(int bits, const SampleArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.rows * a.split.parts));
-    if (bits == 16) hipLaunchKernelGGL((sample_kernel<_Float16, REST>), grid, dim3(kSampleThreads), 0, s, a);
-    else hipLaunchKernelGGL((sample_kernel<float, REST>), grid, dim3(kSampleThreads), 0, s, a);
+    if (bits == 16) hipLaunchKernelGGL((sample_kernel<_Float16, FIRST>), grid, dim3(kSampleThreads), 0, s, a);
+    else hipLaunchKernelGGL((sample_kernel<float, FIRST>), grid, dim3(kSampleThreads), 0, s, a);
     return launched("sample launch");
 }
 
@@ -1396,6 +1390,6 @@ extern "C" exq_status exq_sample(const void* logits, int bits, int rows, int voc
                        {static_cast<uint64_t*>(workspace), rows, parts}};
     const hipStream_t s = static_cast<hipStream_t>(stream);
     exq_status st;
-    if ((st = sample_call<false>(bits, a, s)) != EXQ_OK || parts == 1) return st;
-    return sample_call<true>(bits, a, s);
+    if (parts > 1 && (st = sample_call<true>(bits, a, s)) != EXQ_OK) return st;
+    return sample_call<false>(bits, a, s);
 }
