@@ -210,6 +210,7 @@ struct SampleShared {
     // counters' sums: for each power of two (and sign), the largest values first
     double block_weight[64];
     uint32_t block_count[64];
+    double tops[2][128];
     double steps[32][4];   // weights 0, 1, 2, 3 magnitudes behind one, to its own, for each power of two
     double part_count[4], part_weight[4];
     // a cut found among them
@@ -460,23 +461,50 @@ __device__ __forceinline__ int sum_counters(SampleShared& s, const Weights& w, u
     const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64), lane = t & 63;
     if (weights && t < 32 * 4)   // neighbours of a power of two lie 2^(block - 25) apart
         s.steps[t / 4][t % 4] = w.power(-(t % 4) * __builtin_ldexp(w.c, max(t / 4, 1) - 25));
+    // the weight of the largest value of 256 magnitudes (whatever it is above the largest logit)
+    if (weights && t < 256) s.tops[t / 128][t % 128] = w.real(Logit<_Float16>::value(t < 128 ? 0x80FFu + 256 * t : 0x7FFFu - 256 * (t - 128)));
     __syncthreads();
     uint64_t all = 0;
 #pragma unroll 1
     for (int block = wave; block < 32; block += kSampleWaves) {
         uint32_t n[2] = {0, 0};
         double sum[2] = {0, 0};
+        // of four magnitudes 4 i behind the largest of 256
+        const double behind = weights ? w.power(-4.0 * lane * __builtin_ldexp(w.c, max(block, 1) - 25)) : 0.0, ahead = __shfl(behind, 63 - lane);
+        const double s1 = s.steps[block][1], s2 = s.steps[block][2], s3 = s.steps[block][3];
 #pragma unroll 1
-        for (int part = 0; part < 4; ++part) {
-            const uint32_t m0 = 1024 * block + 256 * part + 4 * lane;
+        for (int quarter = 4 * block; quarter < 4 * block + 4; ++quarter) {
+            const uint32_t m0 = 256 * quarter + 4 * lane;
             const u4v c = *reinterpret_cast<const u4v*>(&s.counts[m0]);
             if (__ballot((c[0] | c[1] | c[2] | c[3]) != 0) == 0) continue;
-            Four x = four_from<false>(c, m0);
-            n[0] += x.all;
-            if (weights) sum[0] += weigh(s, w, top_key, block, x);
-            x = four_from<true>(c, m0);
-            n[1] += x.all;
-            if (weights) sum[1] += weigh(s, w, top_key, block, x);
+            // 0, infinities and NaN, or values above the largest logit among them
+            if (quarter == 0 || block == 31 || quarter == (int)((top_key & 0x8000u ? top_key & 0x7FFFu : 0x7FFFu - top_key) >> 8)) {
+                Four x = four_from<false>(c, m0);
+                n[0] += x.all;
+                if (weights) sum[0] += weigh(s, w, top_key, block, x);
+                x = four_from<true>(c, m0);
+                n[1] += x.all;
+                if (weights) sum[1] += weigh(s, w, top_key, block, x);
+                continue;
+            }
+            uint32_t low[4], high[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                low[e] = c[e] & 0xFFFFu;
+                high[e] = c[e] >> 16;
+            }
+            const uint32_t lows = low[0] + low[1] + low[2] + low[3], highs = high[0] + high[1] + high[2] + high[3];
+            n[0] += lows;
+            n[1] += highs;
+            if (!weights) continue;
+            if (__ballot(lows != 0)) {
+                const double x = __builtin_fma(s1, (double)low[2], (double)low[3]), y = __builtin_fma(s3, (double)low[0], s2 * (double)low[1]);
+                sum[0] = __builtin_fma(s.tops[0][quarter] * ahead, x + y, sum[0]);
+            }
+            if (__ballot(highs != 0)) {
+                const double x = __builtin_fma(s1, (double)high[1], (double)high[0]), y = __builtin_fma(s3, (double)high[3], s2 * (double)high[2]);
+                sum[1] = __builtin_fma(s.tops[1][quarter] * behind, x + y, sum[1]);
+            }
         }
         const uint64_t both = prefix64((uint64_t)n[1] << 32 | n[0]);
         all += n[0] + n[1];
