@@ -112,11 +112,76 @@ template <int T> __device__ __forceinline__ LoraTile lora_tile_of_few(const Lora
     return LoraTile{-1, 0, 0, 0.0f};
 }
 
+// The same for up to kLoraSome rows by a workgroup of THREADS, which counts the rows
+// of all adapters (THREADS - 2 at most), finds the tile's and then its rows among
+// theirs, in order of the threads that hold them.
+constexpr int kLoraSome = 4096;
+template <int T, int THREADS> __device__ __forceinline__ LoraTile lora_tile_of_some(const LoraArgs& a, int no, int& row) {
+    constexpr int EACH = kLoraSome / THREADS, WAVES = THREADS / 64;
+    static_assert(WAVES == 8 || WAVES == 16, "a row of lanes adds up the waves");
+    __shared__ int32_t bin_rows[THREADS], tile_rows[T], found[3];
+    __shared__ uint64_t waves[2][16];
+    const int t = threadIdx.x, lane = t % 64, wave = __builtin_amdgcn_readfirstlane(t / 64);
+    const auto before_of = [&](uint64_t (&sums)[16], int x) {   // the threads' before; a barrier is in it
+        const uint64_t upto = prefix64((uint64_t)x);
+        if (lane == 63) sums[wave] = upto;
+        __syncthreads();
+        const uint64_t to = prefix16(sums[lane & 15]);
+        return (int)(upto - x + (wave ? lane_value(to, wave - 1) : 0));
+    };
+    int bin[EACH];
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        const int r = t + e * THREADS, i = r < a.rows ? a.ids[r] : -1;
+        bin[e] = r >= a.rows ? -1 : i < 0 ? a.adapters : i < a.adapters ? i : a.adapters + 1;
+    }
+    bin_rows[t] = 0;
+    if (t < 32) waves[t / 16][t % 16] = 0;
+    if (t == 0) found[2] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) {
+        // those of the first lane's adapter at once: rows often come in runs
+        const int one = __builtin_amdgcn_readfirstlane(bin[e]);
+        const uint64_t same = __ballot(bin[e] == one);
+        if (one >= 0 && lane == 0) atomicAdd(&bin_rows[one], __builtin_popcountll(same));
+        if (bin[e] >= 0 && bin[e] != one) atomicAdd(&bin_rows[bin[e]], 1);
+    }
+    __syncthreads();
+    const int mine = bin_rows[t];
+    // rows without an adapter need nothing where out is y
+    const int tiles = t == a.adapters && a.in_place ? 0 : (mine + T - 1) / T, first = before_of(waves[0], tiles);
+    if (first <= no && no < first + tiles) {
+        found[0] = t;
+        found[1] = (no - first) * T;
+        found[2] = mine;
+    }
+    __syncthreads();
+    row = 0;
+    if (found[2] == 0) return LoraTile{-1, 0, 0, 0.0f};
+    const int its = found[0], from = found[1], adapter = its < a.adapters ? its : its == a.adapters ? -1 : -2;
+    const int count = min(T, found[2] - from), rank = lora_rank(a, adapter);
+    const float scale = lora_scale(a, adapter);
+    int same = 0;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) same += bin[e] == its;
+    int place = before_of(waves[1], same) - from;
+#pragma unroll
+    for (int e = 0; e < EACH; ++e)
+        if (bin[e] == its) {
+            if (place >= 0 && place < T) tile_rows[place] = t + e * THREADS;
+            ++place;
+        }
+    __syncthreads();
+    if (lane < count) row = tile_rows[lane % T];
+    return LoraTile{adapter, count, rank, scale};
+}
+
 constexpr int kLoraGroupThreads = 1024;
 constexpr int kLoraGroupEach = 8;   // rows whose places a thread keeps in registers
 constexpr int kLoraMaxAdapters = 8192;
 
-// Counting sort of the rows by adapter.  Which of an adapter's rows share a tile
+// Counting sort of more rows by adapter.  Which of an adapter's rows share a tile
 // depends on the order of atomics; a row's result does not depend on that.
 // One workgroup, a chain of look-ups: 2048 rows of 6 adapters take 4 us of a
 // call's 45.
@@ -185,7 +250,10 @@ constexpr int shrink_waves(int T) { return T == 64 ? 16 : 8; }
 constexpr int shrink_rows(int T) { return T == 64 ? 2 : 1; }   // in units of 16
 template <int TT, int RT> constexpr int kShrinkSteps = RT == 4 && TT == 2 ? 2 : 4;
 
-template <bool FEW, int T, int RT>
+// By whom a tile's rows are looked for.
+enum LoraGroup { kByWave, kByWorkgroup, kByLaunch };
+
+template <LoraGroup GROUP, int T, int RT>
 __global__ __launch_bounds__(64 * shrink_waves(T)) void lora_shrink_kernel(LoraArgs a) {
     constexpr int TT = shrink_rows(T), W = shrink_waves(T);
     __shared__ f4 parts[W / 2][RT * TT][64];
@@ -193,8 +261,11 @@ __global__ __launch_bounds__(64 * shrink_waves(T)) void lora_shrink_kernel(LoraA
     const int split = blockIdx.x % a.splits, no = blockIdx.x / a.splits / SUBS, slot0 = blockIdx.x / a.splits % SUBS * 16 * TT;
     const int t = threadIdx.x, wave = t / 64, lane = t % 64, i16 = lane % 16, q = lane / 16;
     int rows_of_tile;
-    const LoraTile tile = FEW ? lora_tile_of_few<T>(a, no, rows_of_tile) : lora_tile<T>(a, no, rows_of_tile);
-    if (FEW && split == 0 && blockIdx.y == 0 && wave == 0) {   // for lora_expand_kernel
+    LoraTile tile;
+    if constexpr (GROUP == kByWave) tile = lora_tile_of_few<T>(a, no, rows_of_tile);
+    else if constexpr (GROUP == kByWorkgroup) tile = lora_tile_of_some<T, 64 * W>(a, no, rows_of_tile);
+    else tile = lora_tile<T>(a, no, rows_of_tile);
+    if (GROUP != kByLaunch && split == 0 && slot0 == 0 && blockIdx.y == 0 && wave == 0) {   // for lora_expand_kernel
         if (lane == 0) a.tiles[no] = tile;
         if (lane < T) a.tile_rows[no * T + lane] = rows_of_tile;
     }
@@ -445,7 +516,7 @@ namespace {
 
 // Shape of a call.
 struct LoraPlan {
-    bool few;
+    LoraGroup group;
     int tile_rows, tiles, splits, slice, rank_tiles;
     size_t rows_at, place_at, low_at, bytes;   // of the workspace
 };
@@ -455,10 +526,11 @@ exq_status plan_lora(const exq_adapters* h, int rows, LoraPlan* p) {
     if (rows < 0) return fail(EXQ_ERR_INVALID_ARG, "rows=%d", rows);
     *p = LoraPlan{};
     if (rows == 0) return EXQ_OK;
-    p->few = rows <= kLoraFew;
     p->tile_rows = rows >= 512 && h->rank <= kExpandRank64 ? 64 : 16;
+    p->group = rows <= kLoraFew ? kByWave
+               : rows <= kLoraSome && h->count + 2 <= 64 * shrink_waves(p->tile_rows) ? kByWorkgroup : kByLaunch;
     p->tiles = (int)std::min<int64_t>(rows, (int64_t)rows / p->tile_rows + h->count + 2);
-    p->rank_tiles = h->rank <= 16 ? 1 : h->rank <= 32 || p->few ? 2 : 4;
+    p->rank_tiles = h->rank <= 16 ? 1 : h->rank <= 32 || p->group == kByWave ? 2 : 4;
     // a wave's channels are all in flight at once, or there are four waves a SIMD
     // already: workgroups that wait for a place would double the time (2048 rows of
     // 8192 in 4 parts, 280 workgroups, 21 us, in 3 parts 18.5)
@@ -478,18 +550,18 @@ exq_status plan_lora(const exq_adapters* h, int rows, LoraPlan* p) {
     return EXQ_OK;
 }
 
-template <bool FEW, int T> exq_status launch_lora(const LoraArgs& a, const LoraPlan& p, hipStream_t s) {
+template <LoraGroup GROUP, int T> exq_status launch_lora(const LoraArgs& a, const LoraPlan& p, hipStream_t s) {
     exq_status st;
-    if (!FEW) {
+    if (GROUP == kByLaunch) {
         hipLaunchKernelGGL(lora_group_kernel, dim3(1), dim3(kLoraGroupThreads), 0, s, a, T, p.tiles);
         if ((st = launched("adapters group launch")) != EXQ_OK) return st;
     }
     const int ranks = 16 * p.rank_tiles;
     const dim3 grid((unsigned)(p.tiles * (T / 16 / shrink_rows(T)) * p.splits), (unsigned)((a.rank + ranks - 1) / ranks));
     const dim3 block(64 * shrink_waves(T));
-    if (p.rank_tiles == 1) hipLaunchKernelGGL((lora_shrink_kernel<FEW, T, 1>), grid, block, 0, s, a);
-    else if (FEW || p.rank_tiles == 2) hipLaunchKernelGGL((lora_shrink_kernel<FEW, T, 2>), grid, block, 0, s, a);
-    else if constexpr (!FEW) hipLaunchKernelGGL((lora_shrink_kernel<FEW, T, 4>), grid, block, 0, s, a);
+    if (p.rank_tiles == 1) hipLaunchKernelGGL((lora_shrink_kernel<GROUP, T, 1>), grid, block, 0, s, a);
+    else if (GROUP == kByWave || p.rank_tiles == 2) hipLaunchKernelGGL((lora_shrink_kernel<GROUP, T, 2>), grid, block, 0, s, a);
+    else if constexpr (GROUP != kByWave) hipLaunchKernelGGL((lora_shrink_kernel<GROUP, T, 4>), grid, block, 0, s, a);
     if ((st = launched("adapters shrink launch")) != EXQ_OK) return st;
     const int pitch = (a.rank + 31) / 32 * 32 + kLowPad;
     hipLaunchKernelGGL((lora_expand_kernel<T>), dim3((unsigned)(p.tiles * a.blocks)), dim3(64 * kExpandWaves), 2u * 2u * T * pitch, s, a);
@@ -583,13 +655,15 @@ exq_status exq_lora_add(exq_adapters_t h, const void* x, int64_t x_row_stride, i
     a.in_place = in_place;
     // blocks that make at most about 750 workgroups, which run side by side
     const int unit = 16 * (p.tile_rows == 64 ? 2 : 4) * kExpandWaves, units = (h->N + unit - 1) / unit;
-    const int busy = p.few ? std::min(rows, h->count + 1) : std::min(p.tiles, rows / p.tile_rows + 1);
+    const int busy = p.group == kByWave ? std::min(rows, h->count + 1) : std::min(p.tiles, rows / p.tile_rows + 1);
     a.columns = unit * (int)std::min<int64_t>(units, ((int64_t)units * busy + 749) / 750);
     a.blocks = (h->N + a.columns - 1) / a.columns;
     if ((int64_t)p.tiles * std::max(a.blocks, p.splits * (p.tile_rows / 16)) > kMaxLaunchThreads / 512)
         return fail(EXQ_ERR_UNSUPPORTED, "%d rows in one call", rows);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    return p.few ? launch_lora<true, 16>(a, p, s) : p.tile_rows == 64 ? launch_lora<false, 64>(a, p, s) : launch_lora<false, 16>(a, p, s);
+    if (p.group == kByWave) return launch_lora<kByWave, 16>(a, p, s);
+    if (p.group == kByWorkgroup) return p.tile_rows == 64 ? launch_lora<kByWorkgroup, 64>(a, p, s) : launch_lora<kByWorkgroup, 16>(a, p, s);
+    return p.tile_rows == 64 ? launch_lora<kByLaunch, 64>(a, p, s) : launch_lora<kByLaunch, 16>(a, p, s);
 }
 
 }  // extern "C"
