@@ -136,14 +136,6 @@ __device__ __forceinline__ RowPlace row_place(const CacheDev& c, const TableDev&
 // bits 22.6 and 24, 10.6 and 12).
 constexpr int kRowsThreads = 256;
 
-// Orders a wave's own LDS writes before its reads, and its reads before its
-// next writes.
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 // The rows of a lane and where they lie.
 struct RowsBlock {
     int row, head;     // row < 0: none

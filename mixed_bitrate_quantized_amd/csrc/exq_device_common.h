@@ -121,6 +121,14 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 // been seen to read element 0 whatever i is.
 __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, v); }
 
+// Orders a wave's own LDS writes before its reads, and its reads before its
+// next writes.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Moves a value within a wave: lanes without a source get 0.
 template <int HOW, int ROWS> __device__ __forceinline__ uint64_t moved(uint64_t x) {
     const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, HOW, ROWS, 0xF, false);

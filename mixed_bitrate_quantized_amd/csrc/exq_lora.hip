@@ -341,6 +341,25 @@ __global__ __launch_bounds__(64 * shrink_waves(T)) void lora_shrink_kernel(LoraA
         }
 }
 
+// Rows without an adapter are copied, those of a number out of range refused.
+__device__ __forceinline__ void lora_copy(const LoraArgs& a, const LoraTile& tile, int rows_of_tile, int n_begin, int n_end) {
+    const _Float16 nan = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
+    const h8 nans = {nan, nan, nan, nan, nan, nan, nan, nan};
+    for (int r = 0; r < tile.count; ++r) {
+        const int64_t row = __shfl(rows_of_tile, r);
+        for (int n = n_begin + 8 * (int)threadIdx.x; n < n_end; n += 8 * (int)blockDim.x)
+            *gptr_w<h8>(a.out + row * a.out_row + n) = tile.adapter == -1 ? *gptr<h8>(a.y + row * a.y_row + n) : nans;
+    }
+}
+
+// Power of two that takes a row's largest finite |low| below 2^15, and the cut of a value in two.
+__device__ __forceinline__ int lora_shift(float most) { return most > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(most), 126) : 0; }
+__device__ __forceinline__ void lora_cut(float x, int e2, _Float16& high, _Float16& rest) {
+    x = __builtin_ldexpf(x, e2);
+    high = (_Float16)x;
+    rest = (_Float16)(x - (float)high);
+}
+
 constexpr int kExpandWaves = 4;
 constexpr int kLowPad = 8;   // fp16 after each row of low in LDS, against bank conflicts
 constexpr int kExpandRank16 = 256, kExpandRank64 = 128;   // largest ranks of tiles of 16 and of 64 rows
@@ -358,14 +377,8 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
     if (tile.count == 0) return;
     const int t = threadIdx.x, lane = t % 64, wave = t / 64, i16 = lane % 16, q = lane / 16;
     const int n_begin = block * a.columns, n_end = min(a.N, n_begin + a.columns);
-    if (tile.adapter < 0) {   // copied, or refused
-        const _Float16 nan = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
-        const h8 nans = {nan, nan, nan, nan, nan, nan, nan, nan};
-        for (int r = 0; r < tile.count; ++r) {
-            const int64_t row = __shfl(rows_of_tile, r);
-            for (int n = n_begin + 8 * t; n < n_end; n += 8 * 64 * kExpandWaves)
-                *gptr_w<h8>(a.out + row * a.out_row + n) = tile.adapter == -1 ? *gptr<h8>(a.y + row * a.y_row + n) : nans;
-        }
+    if (tile.adapter < 0) {
+        lora_copy(a, tile, rows_of_tile, n_begin, n_end);
         return;
     }
     const int padded = (a.rank + 31) / 32 * 32, pitch = padded + kLowPad;
@@ -434,7 +447,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
             }
 #pragma unroll
         for (int d = 1; d < LANES; d *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, d));
-        const int e2 = most > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(most), 126) : 0;
+        const int e2 = lora_shift(most);
 #pragma unroll
         for (int m = 0; m < MOST; ++m) {
             const int j = first + 4 * LANES * m;
@@ -442,9 +455,10 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
             h4 h, l;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = __builtin_ldexpf(v[m][e], e2);
-                h[e] = (_Float16)x;
-                l[e] = (_Float16)(x - (float)h[e]);
+                _Float16 high, rest;
+                lora_cut(v[m][e], e2, high, rest);
+                h[e] = high;
+                l[e] = rest;
             }
             *reinterpret_cast<h4*>(hi + low_row * pitch + j) = h;
             *reinterpret_cast<h4*>(lo + low_row * pitch + j) = l;
@@ -506,6 +520,128 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
     }
 }
 
+// All of it for a few rows of small adapters, ranks up to 16: every workgroup takes
+// x A^T for itself, K cut over its waves, and a block of columns.  A comes by whole
+// lines and is turned into operands in LDS, which a wave has to itself: as operands
+// straight from memory, half a line of 16 rows at a time, a CU reads 13 bytes of A a
+// clock (K of 8192 12.0 us in a graph, 8.4 so).
+constexpr int kAloneWaves = 8, kAloneChunk = 256;   // channels that a wave turns at a time
+constexpr int kAlonePitch = kAloneChunk + 8;
+constexpr int kAloneColumns = 32 * kAloneWaves;     // of a step
+
+__global__ __launch_bounds__(64 * kAloneWaves) void lora_alone_kernel(LoraArgs a) {
+    __shared__ f4 parts[kAloneWaves][64];
+    __shared__ __attribute__((aligned(16))) uint16_t turned[kAloneWaves][16 * kAlonePitch];
+    const int block = blockIdx.x % a.blocks;
+    int rows_of_tile;
+    const LoraTile tile = lora_tile_of_few<16>(a, blockIdx.x / a.blocks, rows_of_tile);
+    if (tile.count == 0) return;
+    const int t = threadIdx.x, lane = t % 64, wave = t / 64, i16 = lane % 16, q = lane / 16;
+    const int n_begin = block * a.columns, n_end = min(a.N, n_begin + a.columns);
+    if (tile.adapter < 0) {
+        lora_copy(a, tile, rows_of_tile, n_begin, n_end);
+        return;
+    }
+    const bool in = i16 < tile.count;
+    const int64_t row = __shfl(rows_of_tile, i16);
+    const uint16_t* b = a.b + (int64_t)tile.adapter * a.N * a.rank;
+    struct Loaded {   // for a step of columns, 8 of a row to a lane
+        h8 y, b[2];
+    };
+    const auto load = [&](int n0) {
+        Loaded x;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const int c = n0 + 8 * (i16 / 4) + 4 * m + i16 % 4, j = 8 * q;
+            x.b[m] = c < n_end && j < tile.rank ? *gptr<h8>(b + (int64_t)c * a.rank + j) : h8{};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x.b[m][e] = j + e < tile.rank ? x.b[m][e] : (_Float16)0.0f;   // what lies behind may be anything
+        }
+        const int n = n0 + 8 * q;
+        x.y = in && n < n_end ? *gptr<h8>(a.y + row * a.y_row + n) : h8{};
+        return x;
+    };
+    int n0 = n_begin + 32 * wave;
+    Loaded next = load(n0);
+
+    const int per = ((a.K + kAloneWaves - 1) / kAloneWaves + 31) / 32 * 32, k_begin = wave * per, k_end = min(a.K, k_begin + per);
+    const EXQ_GLOBAL uint16_t *ap = gptr<uint16_t>(a.a + (int64_t)tile.adapter * a.rank * a.K), *xp = gptr<uint16_t>(a.x + row * a.x_row);
+    constexpr int STEPS = kAloneChunk / 32;
+    struct Chunk {   // two ranks' channels to a load of A, an operand to one of x
+        h8 a[8], x[STEPS];
+    };
+    const auto ask = [&](int k0) {   // K and slices are multiples of 8
+        Chunk c;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 2 * i + lane / 32, k = k0 + 8 * (lane % 32);
+            c.a[i] = k < k_end && r < tile.rank ? *(const EXQ_GLOBAL h8*)(ap + (int64_t)r * a.K + k) : h8{};
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int k = k0 + 32 * s + 8 * q;
+            c.x[s] = k < k_end && in ? *(const EXQ_GLOBAL h8*)(xp + k) : h8{};
+        }
+        return c;
+    };
+    f4 acc{};
+    Chunk coming = ask(k_begin);
+    for (int k0 = k_begin; k0 < k_end; k0 += kAloneChunk) {
+        const Chunk c = coming;
+        if (k0 + kAloneChunk < k_end) coming = ask(k0 + kAloneChunk);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<h8*>(&turned[wave][(2 * i + lane / 32) * kAlonePitch + 8 * (lane % 32)]) = c.a[i];
+        wave_lds_fence();
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const h8*>(&turned[wave][i16 * kAlonePitch + 32 * s + 8 * q]), c.x[s],
+                                                         acc, 0, 0, 0);
+        wave_lds_fence();
+    }
+    parts[wave][lane] = acc;
+    __syncthreads();
+    // ranks 8 q .. + 7 of row i16, as the second product takes them
+    f4 low[2] = {f4{}, f4{}};
+    float most = 0.0f;
+    if (q < 2) {
+#pragma unroll
+        for (int w = 0; w < kAloneWaves; ++w)
+#pragma unroll
+            for (int part = 0; part < 2; ++part) low[part] += parts[w][16 * (2 * q + part) + i16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = __builtin_fabsf(low[e / 4][e % 4]);
+            most = x < __builtin_huge_valf() ? __builtin_fmaxf(most, x) : most;
+        }
+    }
+    most = __builtin_fmaxf(most, __shfl_xor(most, 16));
+    most = __builtin_fmaxf(most, __shfl_xor(most, 32));
+    const int e2 = lora_shift(most);
+    h8 high, rest;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        _Float16 h, l;
+        lora_cut(low[e / 4][e % 4], e2, h, l);
+        high[e] = h;
+        rest[e] = l;
+    }
+    const float f = __builtin_ldexpf(tile.scale, -e2);
+    for (; n0 < n_end; n0 += kAloneColumns) {
+        const Loaded x = next;
+        if (n0 + kAloneColumns < n_end) next = load(n0 + kAloneColumns);
+        h8 o;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            f4 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.b[m], high, f4{}, 0, 0, 0);
+            sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.b[m], rest, sum, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[4 * m + e] = (_Float16)__builtin_fmaf(sum[e], f, (float)x.y[4 * m + e]);
+        }
+        const int n = n0 + 8 * q;
+        if (in && n < n_end) *gptr_w<h8>(a.out + row * a.out_row + n) = o;
+    }
+}
+
 }  // namespace exq
 
 // =================================================================== host
@@ -517,6 +653,7 @@ namespace {
 // Shape of a call.
 struct LoraPlan {
     LoraGroup group;
+    bool alone;   // in one launch
     int tile_rows, tiles, splits, slice, rank_tiles;
     size_t rows_at, place_at, low_at, bytes;   // of the workspace
 };
@@ -531,6 +668,10 @@ exq_status plan_lora(const exq_adapters* h, int rows, LoraPlan* p) {
                : rows <= kLoraSome && h->count + 2 <= 64 * shrink_waves(p->tile_rows) ? kByWorkgroup : kByLaunch;
     p->tiles = (int)std::min<int64_t>(rows, (int64_t)rows / p->tile_rows + h->count + 2);
     p->rank_tiles = h->rank <= 16 ? 1 : h->rank <= 32 || p->group == kByWave ? 2 : 4;
+    // Two launches and one, in a graph (us): K and N of 1024 and 4096 7.9, 5.2; 4096 8.2, 6.5, 8 rows 9.1, 7.4; 8192
+    // 8.4, 8.6, 4 rows 8.9, 9.7.  A call costs the host 8 and 4.4 us.
+    p->alone = h->rank <= 16 && (rows <= 2 ? h->K <= 8192 : rows <= 16 && h->K <= 4096);
+    if (p->alone) return EXQ_OK;
     // a wave's channels are all in flight at once, or there are four waves a SIMD
     // already: workgroups that wait for a place would double the time (2048 rows of
     // 8192 in 4 parts, 280 workgroups, 21 us, in 3 parts 18.5)
@@ -611,7 +752,7 @@ exq_status exq_lora_add(exq_adapters_t h, const void* x, int64_t x_row_stride, i
     const bool in_place = y == out && (rows == 1 || y_row_stride == out_row_stride);
     if (operands_meet(xo, oo) || (!in_place && operands_meet(yo, oo)))
         return fail(EXQ_ERR_INVALID_ARG, "out overlaps x, or y without being the same");
-    if (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes)
+    if (p.bytes && (!workspace || !aligned(workspace, 16) || workspace_bytes < p.bytes))
         return fail(EXQ_ERR_INVALID_ARG, "workspace of %zu bytes: %zu 16-byte aligned ones are needed", workspace_bytes, p.bytes);
     const struct {
         const char* name;
@@ -653,6 +794,15 @@ exq_status exq_lora_add(exq_adapters_t h, const void* x, int64_t x_row_stride, i
     a.splits = p.splits;
     a.slice = p.slice;
     a.in_place = in_place;
+    if (p.alone) {
+        const int steps = (h->N + kAloneColumns - 1) / kAloneColumns;
+        a.columns = kAloneColumns * std::max(1, (int)((int64_t)steps * std::min(p.tiles, h->count + 1) / 256));
+        a.blocks = (h->N + a.columns - 1) / a.columns;
+        const hipStream_t s = static_cast<hipStream_t>(stream);
+        const dim3 grid((unsigned)(p.tiles * a.blocks)), block(64 * kAloneWaves);
+        hipLaunchKernelGGL(lora_alone_kernel, grid, block, 0, s, a);
+        return launched("adapters launch");
+    }
     // blocks that make at most about 750 workgroups, which run side by side
     const int unit = 16 * (p.tile_rows == 64 ? 2 : 4) * kExpandWaves, units = (h->N + unit - 1) / unit;
     const int busy = p.group == kByWave ? std::min(rows, h->count + 1) : std::min(p.tiles, rows / p.tile_rows + 1);

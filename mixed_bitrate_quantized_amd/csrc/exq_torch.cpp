@@ -455,15 +455,17 @@ PyObject* lora_add(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (!out_o || !matrix_operand("out", out_o, c, rows, N, out)) return nullptr;
         const size_t need = exq_lora_workspace_bytes(h, (int)rows);
         at::Tensor own;
-        const at::Tensor* w = &own;
+        const at::Tensor* w = nullptr;
         if (a[9] != Py_None) {
             if (!(w = tensor("workspace", a[9]))) return nullptr;
             if (!w->is_cuda() || w->get_device() != c.index || !w->is_contiguous())
                 return refuse("workspace must be contiguous on cuda:%d", c.index);
-        } else {
+        } else if (need) {
             own = empty(c, {(int64_t)need}, at::kByte);
+            w = &own;
         }
-        return status_or(exq_lora_add(h, x.p, x.row, (int)rows, ids, y.p, y.row, out.p, out.row, w->data_ptr(), w->nbytes(), c.stream),
+        return status_or(exq_lora_add(h, x.p, x.row, (int)rows, ids, y.p, y.row, out.p, out.row, w ? w->data_ptr() : nullptr,
+                                      w ? w->nbytes() : 0, c.stream),
                          "exq_lora_add", std::move(out_o));
     });
 }

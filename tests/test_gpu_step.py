@@ -236,7 +236,8 @@ def stack(rng, count, K, N, rank):
 
 
 @pytest.mark.parametrize("K,N,rank,count", [(256, 512, 16, 3), (8, 8, 8, 1), (1000, 1016, 24, 7), (4096, 264, 64, 40), (520, 2056, 128, 2),
-                                            (136, 72, 200, 3), (2048, 1024, 256, 2)])
+                                            (136, 72, 200, 3), (2048, 1024, 256, 2), (8192, 264, 16, 5), (4096, 4104, 8, 3),
+                                            (4104, 520, 16, 2), (1000, 1016, 16, 7)])
 def test_lora_matches_reference(exq, K, N, rank, count):
     note("lora K=%d N=%d rank=%d" % (K, N, rank))
     rng = np.random.default_rng(K + N + rank)

@@ -145,7 +145,7 @@ def test_adapters_reject(status, args):
 
 
 def lora_args(h, **kw):
-    a = dict(x=at(4), xs=256, rows=9, ids=at(5), y=at(6), ys=512, out=at(7), os=512, ws=at(8), wsb=1 << 20)
+    a = dict(x=at(4), xs=256, rows=40, ids=at(5), y=at(6), ys=512, out=at(7), os=512, ws=at(8), wsb=1 << 20)
     a.update(kw)
     return [h] + [a[x] for x in ("x", "xs", "rows", "ids", "y", "ys", "out", "os", "ws", "wsb")] + [0]
 
@@ -167,8 +167,9 @@ def test_lora_without_rows_or_adapters(adapters):
     expect(I, exq.exq_lora_add, *lora_args(None))
     assert exq.exq_lora_workspace_bytes(None, 3) == exq.exq_lora_workspace_bytes(adapters, 0) == 0
     assert exq.exq_lora_workspace_bytes(adapters, -1) == 0
-    sizes = [exq.exq_lora_workspace_bytes(adapters, r) for r in (1, 16, 500, 600, 5000)]
-    assert 0 < sizes[0] and max(sizes) < 1 << 24
+    assert exq.exq_lora_workspace_bytes(adapters, 1) == exq.exq_lora_workspace_bytes(adapters, 16) == 0   # one launch, nothing between
+    sizes = [exq.exq_lora_workspace_bytes(adapters, r) for r in (17, 64, 65, 500, 600, 5000)]
+    assert 0 < min(sizes) and max(sizes) < 1 << 24
     exq.exq_adapters_destroy(None)
 
 
