@@ -43,7 +43,8 @@
  *   - arguments are validated before anything is launched; a call that
  *     fails validation launches nothing and leaves outputs untouched.
  *   - results are deterministic: the same inputs give the same bits.
- *   - exq_gemm, exq_gemm_gated, exq_dequant and exq_plan_run launch kernels
+ *   - exq_gemm, exq_gemm_gated, exq_dequant, exq_plan_run, exq_pages_extend,
+ *     exq_pages_trim, exq_rotate, exq_lora_add and exq_sample launch kernels
  *     only (no allocation, memset or wait), so they may be captured in a HIP
  *     graph, whose replays then read and write the buffers bound at capture.
  *     The one exception is the first call that expands a layer's quantized
@@ -570,8 +571,8 @@ exq_status exq_adapters_create(int count, int K, int N, int rank, const void* a,
 /* Release a handle (not the weights).  NULL is a no-op. */
 void exq_adapters_destroy(exq_adapters_t adapters);
 
-/* Bytes of workspace exq_lora_add needs for that many rows (0: none, or an
- * argument is invalid). */
+/* Bytes of workspace exq_lora_add needs for that many rows (0: none, as for a few
+ * rows of small adapters, or an argument is invalid). */
 size_t exq_lora_workspace_bytes(exq_adapters_t adapters, int rows);
 
 /* out[r] = y[r] + scales[i] * (x[r] a[i]^T) b[i]^T,  i = ids[r], for rows of any
@@ -582,15 +583,15 @@ size_t exq_lora_workspace_bytes(exq_adapters_t adapters, int rows);
  *            more: out[r] is NaN
  *   out      as y, no element twice; y itself (same pointer and stride) or apart
  *            from it, and apart from x, ids and the handle's arrays
- *   workspace   device, 16-byte aligned, any content; apart from all others.  Calls
- *            that may run at the same time need one each
+ *   workspace   device, 16-byte aligned, any content; apart from all others (NULL where
+ *            none is needed).  Calls that may run at the same time need one each
  * Accuracy, with L_j = |x[r]| . |a[i][j]| the sum of magnitudes of one inner product
  * and S = sum_j |b[n][j]| L_j:
  *   |out - out_ref| <= 2^-11 |out_ref| + |scales[i]| S (K + rank + 64) 2^-23 + 2^-24
  * (fp32 sums; the inner products enter the second product with 22 bits).  A row's
  * result does not depend on the other rows' values or ids, but for its summation
- * over K, which depends on the number of rows; deterministic.  x or y with an infinity or a NaN makes that row's
- * results infinite or NaN.
+ * over K, which depends on the number of rows; deterministic.  x or y with an
+ * infinity or a NaN makes that row's results infinite or NaN.
  * Capturable: no allocation, no wait.  rows == 0 is a no-op.  Errors: INVALID_ARG,
  * UNSUPPORTED (rows beyond a launch), HIP. */
 exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_stride, int rows, const int32_t* ids,
@@ -618,15 +619,20 @@ exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_st
  *            that follows, for all rows
  *   tokens   device int32 [rows], written
  *   logprobs device fp32 [rows] or NULL: ln of the token's share of the weights left
- *   workspace  device, 16-byte aligned, exq_sample_workspace_bytes(rows, vocab) bytes,
- *            written, or NULL.  With it, few rows of many logits are shared out over
- *            the GPU (1 x 131072 fp32 logits drawn from all: XX us, without YY)
+ *   workspace  device, 16-byte aligned, exq_sample_workspace_bytes(rows, vocab) bytes of
+ *            any content, apart from all others, or NULL.  With it, up to 128 rows of
+ *            16384 logits or more are shared out over the GPU where top_k does not
+ *            leave few (1 x 131072 fp32 logits, drawn from all: 19 us, without it 58).
+ *            Calls that may run at the same time need one each
  * A row without a logit that may be drawn, or with a u, T, top_p or min_p that is
  * NaN, or a negative T, gets token -1 and logprob NaN.
- * Weights are computed in 64 bits and summed exactly, in units of 2^-42 (vocab of
- * 2^21) to 2^-51 (4096 and fewer) of the largest: deterministic.  A logprob is
- * within 2^-23 of its value relative, or 2^-30.
- * rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, misaligned, a bad size, stride or
+ * Weights are computed in 64 bits, to 2^-45 relative, and summed exactly, in units of
+ * 2^-42 (vocab of 2^21) to 2^-51 (4096 and fewer) of the largest; where one weight
+ * stands for all equal fp16 logits, in 64-bit floating point.  The same call gives the
+ * same tokens.  With and without a workspace a sum may differ by its rounding, and
+ * then a token whose border lies that close to u.  A logprob is within 2^-23 of its
+ * value relative, or 2^-30.
+ * Capturable: no allocation, no wait.  rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, misaligned, a bad size, stride or
  * setting, tokens or logprobs overlapping an input or each other), UNSUPPORTED
  * (bits, vocab), HIP. */
 size_t exq_sample_workspace_bytes(int rows, int vocab);   /* 0: none is needed */

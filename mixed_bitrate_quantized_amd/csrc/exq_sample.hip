@@ -5,22 +5,35 @@
 //   w_i = e^{(l_i - M) / T} = 2^t,  t = (l_i - M) log2(e) / T,
 // computed in 64 bits and held as a whole number of units of 2^-shift.  Sums of
 // whole numbers do not depend on their order, so weights may be added through LDS
-// atomics and still give the same token every time; and 2^-45 units keep a border
-// between two tokens where the real numbers have it.
+// atomics and still give the same token every time; and 2^-42 to 2^-51 a unit keep a
+// border between two tokens where the real numbers have it.  Where a weight counts
+// for every logit of one fp16 key, sums are taken in 64-bit floating point, in a fixed
+// order.
 //
 // One workgroup takes a row; nothing is sorted.  Every filter leaves the tokens
 // above a cut: a key (a logit's bits, in order) and how many of those with that key.
-//   fp16   a counter in LDS for every key.  The counters say where top-k ends, and
-//          with a weight for every key instead of every token (64-bit arithmetic
-//          takes 8 cycles an instruction: weights of 131072 tokens take 44 us) what the
-//          weights add up to and where top-p ends.
-//   fp32   top-k: the k-th largest of the threads' own largest logits is a threshold
-//          that at least k logits reach and, with the row dealt out over 1024
-//          threads, not many more.  top-p: a histogram of the weights, 64 bins for a
-//          power of two.  What may be left goes to LDS, where the cut is found digit by
-//          digit of the keys.
-// The draw runs over what is left, in LDS, digit by digit of the index, or over
-// the row where that is too much: sums of tiles, then the tile that holds it.
+//   top-k   up to 900: the k-th largest of the threads' own largest logits is a
+//           threshold that at least k logits reach and, with the row dealt out over
+//           1024 threads, not many more.
+//   fp16    top-p, or more of top-k: a counter in LDS for every key.  The counters say
+//           where top-k ends, and with a weight for every key instead of every token
+//           (64-bit arithmetic takes 8 cycles an instruction: weights of 131072 tokens
+//           take 36 us) what the weights add up to and where top-p ends.
+//   fp32    these: a histogram of the logits, or of the weights, 64 bins for a power of
+//           two.  What may be left goes to LDS, where the cut is found digit by digit
+//           of the keys.
+// The draw runs over what is left: up to 256 candidates are compared with one another;
+// longer lists, or the row where that is too much, go through sums of tiles, then the
+// tile that holds the draw.
+// Rows that have to be weighed whole (no top-k; top-p or nothing) are shared out over
+// several workgroups where there are few rows.
+//
+// The bytes of the logits are the floor (256 x 131072 fp16: 67 MB, 9.6 us).  What a call
+// takes is a chain of looks with barriers between: 1 x 32000 with a top-k of 40 11.5 us,
+// 16 x 50001 fp32 with settings of all kinds 26.1 (launch of the shares 9, the rest 17),
+// 256 x 131072 with top-p 38: the first look 24000 cycles and 8000 until its last
+// wave, the counters 13000, the end of top-p 4500, the second look, for the list,
+// 28500, cut and draw 16000.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -144,6 +157,7 @@ template <> struct Logit<float> {
 };
 
 constexpr double kLn2d = 0.69314718055994530942;
+constexpr double kInfinite = 0x1p128;   // in an infinite logit's place
 
 // 2^f for |f| <= 1 from its series; the first term left out is below 2^-53 of it
 // at 1/2, and 2^-40 at 1.
@@ -158,7 +172,7 @@ __device__ __forceinline__ double exp2_series(double f) {
 // behind r^3: within 2^-45.
 struct Weights {
     float topf;
-    double top, c;   // largest logit, 256 log2(e) / T; beside an infinity all else weighs nothing
+    double top, c;   // largest logit (kInfinite), 256 log2(e) / T; beside an infinity all else weighs nothing
     double scale;    // 2^shift
     const double* powers;
     __device__ __forceinline__ double power(double t) const {   // 2^(t / 256)
@@ -175,7 +189,7 @@ struct Weights {
     }
     __device__ __forceinline__ double real(float l) const {   // l: at most the largest
 #pragma clang fp contract(off)
-        return power(((double)__builtin_fminf(l, __FLT_MAX__) - top) * c);
+        return power((__builtin_fmin((double)l, kInfinite) - top) * c);
     }
     // In units, rounded: 2^52 + w * 2^shift has the whole number in its lower bits.
     __device__ __forceinline__ uint64_t units(double w) const {
@@ -950,7 +964,7 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
         return;
     }
     const float topf = L::value(top_key), finite_top = __builtin_fminf(topf, __FLT_MAX__);
-    const Weights w{topf, (double)finite_top, topf > __FLT_MAX__ ? 1e300 : kPowers * 1.4426950408889634074 / (double)temperature,
+    const Weights w{topf, __builtin_fmin((double)topf, kInfinite), topf > __FLT_MAX__ ? 1e300 : kPowers * 1.4426950408889634074 / (double)temperature,
                     (double)(1ull << a.shift), s.powers};
     Row f{0, a.vocab, top_key, L::BITS, 0, 1.0f, Cut{0, 0xFFFFFFFFu}, 0, u, temperature};
     if (min_p > 0.0f) {   // w >= min-p where the logit is M + T ln(min-p) or more

@@ -422,6 +422,10 @@ def test_sample_masked_infinite_and_nan_logits(exq, wide):
     for settings in (dict(), dict(top_k=30), dict(top_p=0.9), dict(top_k=2500, top_p=0.5), dict(min_p=0.1), dict(temperature=0.0),
                      dict(temperature=1e-30), dict(temperature=1e30), dict(temperature=np.inf)):
         check_sample(exq, x, rng.random(9), str(settings), wide, **settings)
+    if wide:      # the largest finite value beside infinities is not drawn
+        x[4, :200] = np.finfo(np.float32).max
+        for settings in (dict(), dict(top_k=30), dict(top_p=0.9), dict(top_k=2500, top_p=0.5), dict(min_p=0.1)):
+            check_sample(exq, x, rng.random(9), "beside infinities %s" % settings, wide, **settings)
     lowest = np.full((3, 2000), np.finfo(np.float32 if wide else np.float16).min)
     lowest[1, 1500] = 0.0
     check_sample(exq, lowest, np.array([0.3, 0.6, 0.9]), "lowest", wide, top_p=0.9)
