@@ -6,9 +6,15 @@
 // Bound by the bytes of x, y, out and the adapters in use; for a few rows by
 // the launches.  Rows of one adapter are gathered into tiles, so that an adapter
 // in use is read once for a tile of its rows, in whatever order they come:
-//   group   the rows sorted by adapter (up to 64 rows every wave does that for itself);
-//   shrink  low = x A^T for 16 rows, K cut over waves and workgroups;
+//   group   the rows sorted by adapter: up to 64 rows by every wave for itself, up to
+//           4096 by every shrinking workgroup, more by a launch of their own;
+//   shrink  low = x A^T for 16 or 32 rows, K cut over waves and workgroups;
 //   expand  out = y + s low B^T for a tile and a block of columns.
+// A few rows of small adapters take one launch, which does all of that.
+// 48 rows of 16 adapters of rank 64 beside 8192 x 28672 take 23.3 us: shrinking 7,
+// expanding 15 of them, B's lines (59 MB) at 3.9 TB/s with the start.  2048 rows of 6
+// adapters of rank 32 beside 8192 x 8192 take 41.0: 105 MB; shrinking 18.4 (grouping
+// 3 of them), expanding 18, 67 MB at 3.7 TB/s.
 // Products run on v_mfma_f32_16x16x32_f16, sums are fp32.  low enters the second
 // product as two fp16 numbers whose sum has 22 bits, scaled by a power of two
 // to the row's largest: rounded to one fp16 it would cost half of the error
@@ -183,8 +189,8 @@ constexpr int kLoraMaxAdapters = 8192;
 
 // Counting sort of more rows by adapter.  Which of an adapter's rows share a tile
 // depends on the order of atomics; a row's result does not depend on that.
-// One workgroup, a chain of look-ups: 2048 rows of 6 adapters take 4 us of a
-// call's 45.
+// One workgroup, a chain of look-ups: 2048 rows of 6 adapters would take 5.8 us,
+// the shrinking workgroups' own look 3.
 __global__ __launch_bounds__(kLoraGroupThreads) void lora_group_kernel(LoraArgs a, int T, int most_tiles) {
     __shared__ int32_t bin_rows[kLoraMaxAdapters + 2], first_tile[kLoraMaxAdapters + 2];
     __shared__ int32_t wave_tiles[kLoraGroupThreads / 64];
@@ -524,7 +530,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
 // x A^T for itself, K cut over its waves, and a block of columns.  A comes by whole
 // lines and is turned into operands in LDS, which a wave has to itself: as operands
 // straight from memory, half a line of 16 rows at a time, a CU reads 13 bytes of A a
-// clock (K of 8192 12.0 us in a graph, 8.4 so).
+// clock (K of 8192 12.0 us in a graph, 8.6 so).
 constexpr int kAloneWaves = 8, kAloneChunk = 256;   // channels that a wave turns at a time
 constexpr int kAlonePitch = kAloneChunk + 8;
 constexpr int kAloneColumns = 32 * kAloneWaves;     // of a step

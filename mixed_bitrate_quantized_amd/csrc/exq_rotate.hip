@@ -7,7 +7,8 @@
 // and reduced to a part of a turn there, so far positions cost no accuracy;
 // its sine and cosine then have the accuracy of 32 bits.  A thread has the
 // same eight pairs of several heads of a row, so that the angles are paid for
-// once.
+// once.  4096 rows of 72 heads of 128 (151 MB in and out) take 26.3 to 29.3 us, 5.1
+// to 5.7 TB/s, where a large copy has 5.3; one row takes 2.9 us on the GPU.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
