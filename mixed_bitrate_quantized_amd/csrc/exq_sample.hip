@@ -183,7 +183,8 @@ struct Weights {
         const double f = t - (n - 6755399441055744.0);
         const int j = (int)(uint32_t)__builtin_bit_cast(uint64_t, n);
         const double near = powers[j & (kPowers - 1)];
-        const double q = __builtin_fma(f, __builtin_fma(f, a * a * a / 6, a * a / 2), a);
+        // |f| <= 1/2; the square's factor is a little above 1/2, which takes the error from 2^-42.7 to 2^-45.2
+        const double q = __builtin_fma(f, __builtin_fma(f, a * a * a / 6, a * a * (0.5 + 0.0345178 * a * a / 4)), a);
         const double w = __builtin_fma(near * f, q, near);
         return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, w) + ((uint64_t)(uint32_t)((j >> 8) << 20) << 32));
     }
