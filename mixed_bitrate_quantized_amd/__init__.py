@@ -673,7 +673,7 @@ class PagePool:
         `rows` its sequence (-1 behind the last) and position, and for sequence s its first row offsets[s].
 
         Where pages, rows or the table's width do not suffice, the first sequence concerned and all after it get nothing;
-        `served` (int32 [1]) tells how many were served."""
+        `served` (int32 [1]) tells how many were served.  New outputs are chunks of one allocation."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
             return _call_on(stream, self.device, self.extend, counts, rows, seqs, positions, offsets)
@@ -754,7 +754,7 @@ class Rotary:
 
     def rotate(self, q, positions, k=None, q_out=None, k_out=None, stream=None):
         """q (fp16 [rows][heads][head_dim]), and k if given, turned by positions (int32 [rows]; < 0: left as it was in the
-        output) -> q_out, or (q_out, k_out).  An output may be its input."""
+        output) -> q_out, or (q_out, k_out), new ones as chunks of one allocation.  An output may be its input."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
             return _call_on(stream, self.device, self.rotate, q, positions, k, q_out, k_out)
@@ -816,7 +816,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
 
     temperature, top_p, min_p: a number, or fp32 [rows]; top_k: a number, or int32 [rows] (0: off).  Filters apply in the
     order top-k, top-p, min-p (include/exq.h) -> tokens int32 [rows], or (tokens, logprobs fp32 [rows]) with the logarithm of
-    the probability each was drawn with.  A row with u < 0 is left as it was; one without a token to draw gets -1.  Runs on
+    the probability each was drawn with; new ones are chunks of one allocation.  A row with u < 0 is left as it was; one
+    without a token to draw gets -1.  Runs on
     `stream` (default: the current stream of the logits' device) and may be captured."""
     global _sample
     if _sample is None:

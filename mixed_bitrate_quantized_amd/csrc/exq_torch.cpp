@@ -271,8 +271,8 @@ PyObject* given_or_empty(PyObject* o, const Call& c, at::IntArrayRef shape, at::
     return o == Py_None ? THPVariable_Wrap(empty(c, shape, type)) : Py_NewRef(o);
 }
 
-// New outputs of a call, contiguous, in one allocation: one of them costs the host a
-// microsecond, a tensor on it a tenth of that.
+// New outputs of a call, contiguous, in one allocation, like the chunks of a tensor: an
+// allocation costs the host 1.8 us, a tensor on it a tenth of that.
 struct Output {
     at::IntArrayRef shape;
     at::ScalarType type;

@@ -3,6 +3,8 @@ sizes, strides and values where it can go wrong, and a decoding step made of all
 
 Tolerances are those that include/exq.h states: one rounding of the result to fp16 (2^-11 of it), 32-bit sums of the number
 of terms, and for logprobs one rounding to fp32 of a value known to 2^-30.  Whole numbers are equal."""
+import io
+
 import numpy as np
 import pytest
 
@@ -652,6 +654,64 @@ def test_shared_out_draws_on_two_streams_and_in_graphs(exq):
             for tokens, logs in got[i] + [graphs[i][1]]:
                 assert torch.equal(tokens, want[i][0]) and torch.equal(logs, want[i][1]), (rep, i)
             assert host(want[i][0]).tolist() == [ref.sample_row(l, x, top_p=np.float32(0.9))[0] for l, x in zip(host(logits[i]), host(u[i]))]
+
+
+def test_offsets_past_32_bits(exq):
+    """Rows 2^30 elements apart: the third lies past 2^31 elements and 2^32 bytes."""
+    rng = np.random.default_rng(26)
+    space = torch.empty(2 * (1 << 30) + (1 << 20), dtype=torch.float16, device="cuda")
+    view = lambda offset, *shape: space.as_strided((3, *shape), (1 << 30, *([shape[-1], 1] if len(shape) == 2 else [1])), offset)
+    logits = likely(rng, 3, 20000).astype(np.float16)
+    l = view(8, 20000)
+    l.copy_(to_dev(logits))
+    u = rng.random(3)
+    for settings in (dict(), dict(top_k=40), dict(top_p=0.9)):
+        got = host(exq.sample(l, f32(u), **settings))
+        assert got.tolist() == [ref.sample_row(x, np.float32(v), **{k: np.float32(p) if k == "top_p" else p for k, p in settings.items()})[0]
+                                for x, v in zip(logits, u)], settings
+    x = rng.standard_normal((3, 4, 64)).astype(np.float16)
+    q, out, p = view(1 << 16, 4, 64), view(1 << 17, 4, 64), i32([7, -1, 1 << 20])
+    q.copy_(to_dev(x))
+    out.zero_()
+    rotary = exq.Rotary(64)
+    assert torch.equal(rotary.rotate(q, p, q_out=out)[::2], rotary.rotate(to_dev(x), p)[::2]) and not out[1].any()
+    a, b, scales, ranks = stack(rng, 2, 64, 512, 16)
+    adapters = exq.Adapters(to_dev(a), to_dev(b), f32(scales), i32(ranks))
+    x, y, ids = rng.standard_normal((3, 64)).astype(np.float16), rng.standard_normal((3, 512)).astype(np.float16), i32([0, -1, 1])
+    fx, fy = view(1 << 18, 64), view(1 << 19, 512)
+    fx.copy_(to_dev(x))
+    fy.copy_(to_dev(y))
+    want = adapters.add(to_dev(x), ids, to_dev(y))
+    assert torch.equal(adapters.add(fx, ids, fy), want)
+    assert torch.equal(adapters.add(fx, ids, fy, out=fy), want)
+
+
+def test_outputs_are_ordinary_tensors(exq):
+    """Outputs of one call are chunks of an allocation: each can be changed, saved and used in a gradient by itself."""
+    rng = np.random.default_rng(27)
+    x, p = to_dev(rng.standard_normal((5, 3, 64)).astype(np.float16)), i32([0, 1, 2, 3, 4])
+    rotary = exq.Rotary(64)
+    q, k = rotary.rotate(x, p, k=x[:, :2])
+    one = rotary.rotate(x, p)
+    for t, shape in ((q, (5, 3, 64)), (k, (5, 2, 64))):
+        assert t.shape == shape and t.is_contiguous() and t.device == x.device and not t.requires_grad and t.data_ptr() % 256 == 0
+        assert torch.equal(t, one[:, :shape[1]])
+    k.zero_()
+    assert torch.equal(q, one)
+    saved = io.BytesIO()
+    torch.save(q, saved)
+    saved.seek(0)
+    assert torch.equal(torch.load(saved, weights_only=True), one)
+    q.requires_grad_()
+    (q.float() * 2).sum().backward()
+    assert torch.all(q.grad == 2)
+    tokens, logs = exq.sample(to_dev(likely(rng, 4, 1000).astype(np.float16)), f32(rng.random(4)), return_logprobs=True)
+    kept = logs.clone()
+    tokens.fill_(7)
+    assert torch.equal(logs, kept)
+    with torch.inference_mode():
+        a, b = rotary.rotate(x, p, k=x)
+        assert a.is_inference() and torch.equal(a, one)
 
 
 def test_calls_are_deterministic(exq):
