@@ -351,10 +351,22 @@ __global__ __launch_bounds__(64 * shrink_waves(T)) void lora_shrink_kernel(LoraA
 __device__ __forceinline__ void lora_copy(const LoraArgs& a, const LoraTile& tile, int rows_of_tile, int n_begin, int n_end) {
     const _Float16 nan = __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
     const h8 nans = {nan, nan, nan, nan, nan, nan, nan, nan};
-    for (int r = 0; r < tile.count; ++r) {
-        const int64_t row = __shfl(rows_of_tile, r);
-        for (int n = n_begin + 8 * (int)threadIdx.x; n < n_end; n += 8 * (int)blockDim.x)
-            *gptr_w<h8>(a.out + row * a.out_row + n) = tile.adapter == -1 ? *gptr<h8>(a.y + row * a.y_row + n) : nans;
+    // runs of 8 columns of all rows dealt out over the threads, four of each under way
+    const int runs = (n_end - n_begin) / 8, all = tile.count * runs;
+    for (int i0 = 0; i0 < all; i0 += 4 * (int)blockDim.x) {
+        h8 x[4];
+        int64_t row[4];
+        int n[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const int i = i0 + m * (int)blockDim.x + (int)threadIdx.x, r = min(i / runs, tile.count - 1);
+            row[m] = __shfl(rows_of_tile, r);
+            n[m] = i < all ? n_begin + 8 * (i - r * runs) : -1;
+            x[m] = tile.adapter == -1 && n[m] >= 0 ? *gptr<h8>(a.y + row[m] * a.y_row + n[m]) : nans;
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            if (n[m] >= 0) *gptr_w<h8>(a.out + row[m] * a.out_row + n[m]) = x[m];
     }
 }
 

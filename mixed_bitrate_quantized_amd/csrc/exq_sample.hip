@@ -53,6 +53,7 @@ constexpr int kSampleFew = 256;               // candidates that are compared on
 constexpr int kDigit = 9;                     // bits looked at together
 constexpr int kSampleBins = 2048;             // of a row's histogram
 constexpr int kSampleParts = 16;              // of a row, at most
+constexpr int kSampleCountedShare = 32768;    // logits of a part of an fp16 row with top-p, at most
 constexpr int kSamplePartList = 1024;         // candidates of a part
 constexpr int kSampleMaxVocabLog2 = 21;
 constexpr int kPowers = 256;                  // 2^(i / 256) in LDS
@@ -903,7 +904,8 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
     const bool first_only = temperature == 0.0f || top_k == 1 || top_p <= 0.0f || min_p > 1.0f;
     const bool by_k = top_k > 0 && top_k < a.vocab, by_p = top_p < 1.0f;
     const bool near = by_k && top_k <= kSampleNear;   // top-k from the threads' largest logits
-    const bool split = a.split.parts > 1 && !first_only && !by_k && (by_p || !(min_p > 0.0f));
+    // (fp16's counters cost less than weighing a large part of a row twice)
+    const bool split = a.split.parts > 1 && !(L::COUNTED && by_p && a.vocab > kSampleCountedShare * a.split.parts) && !first_only && !by_k && (by_p || !(min_p > 0.0f));
     if (split ? !FIRST && !by_p && part : FIRST || part) return;   // what one workgroup has all of
     bool counted = L::COUNTED && !split && !first_only && !near && (by_k || by_p);
     if (t < kPowers) s.powers[t] = exp2_series((double)t / kPowers);
@@ -1136,6 +1138,7 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
         if (!counted && !held && (by_k || by_p)) {
             f.top_k = 0;
             f.top_p = 1.0f;
+            f.key_bits = L::BITS;
 #pragma unroll 1
             for (int filter = by_k ? 0 : 1; filter < (by_p ? 2 : 1); ++filter) {
                 const bool counts = filter == 0;
@@ -1182,9 +1185,14 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
                 uint64_t skipped;
                 uint32_t d;
                 if (count <= kSampleList) {
-                    if (from == 0 && filter == (by_p ? 1 : 0)) {   // the last filter
+                    if (from == 0) {   // all that is left
                         held = true;
                         f.count = count;
+                    }
+                    if (held && counts) {   // top-k is left to the list, and top-p of that
+                        f.top_k = top_k;
+                        f.top_p = top_p;
+                        break;
                     }
                     const uint64_t behind = from ? before : 0;
                     d = select(s, L::BITS, need - behind, skipped, [&](auto&& g) {
@@ -1359,6 +1367,10 @@ constexpr int kSampleShare = 4096;       // logits of a part, at least
 //   1 x 8192 fp32    9.1, 10.6   19.5, 22.6       1 x 131072 fp16   47, 16.5   39, 30
 //   1 x 16384 fp32   12.5, 11.2  25.1, 22.0       128 x 50001 fp16  23.8, 19.2   34.6, 36.2
 //   1 x 32000 fp16   16.9, 12.3  23.7, 23.5       128 x 50001 fp32  28.9, 22.4   53, 40
+// fp16 with top-p takes 1.1 us for every 1000 logits of a part, and 0.13 for every 1000
+// of the row by its counters: rows with large parts are left to these (108 x 120076 in
+// two 84 us, by counters 37; 73 x 117468 of mixed settings in three 60, 51; 49 x 78985
+// in five 35.5, 40; 32 x 237653, flat ones among them, in eight 46, 100).
 int sample_parts(int rows, int vocab) {
     return vocab < kSampleSplit ? 1 : std::max(1, std::min(std::min(kSampleParts, vocab / kSampleShare), kSampleWorkgroups / rows));
 }
@@ -1425,6 +1437,7 @@ extern "C" exq_status exq_sample(const void* logits, int bits, int rows, int voc
         const bool no_row = (!temperatures && temperature == 0) || (!top_ks && top_k > 0 && top_k < vocab) || (!top_ps && top_p <= 0) ||
                             (!min_ps && min_p > 0 && !top_ps && top_p >= 1);
         if (need && !no_row) parts = sample_parts(rows, vocab);
+        if (bits == 16 && vocab > kSampleCountedShare * parts && !top_ps && top_p < 1) parts = 1;
     }
     int log2 = 0;
     while ((1 << log2) < vocab) ++log2;
