@@ -921,15 +921,13 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
         best = *a.split.best(r);
         __syncthreads();
     } else {
-        const auto look = [&](float x, int i) {
-            if (x > mine) {
-                mine = x;
-                mine_at = i;
-            }
-        };
         for_vectors<T, 6, false>(row, a.vocab, [&](const vec& x, int i, bool in) {
             if (!in) return;
-            look(L::largest(x), i);
+            const float most = L::largest(x);
+            if (most > mine) {
+                mine = most;
+                mine_at = i;
+            }
             if constexpr (L::COUNTED) {
                 if (counted) {
                     const u4v bits = __builtin_bit_cast(u4v, x);
@@ -941,7 +939,11 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
                 }
             }
         }, [&](T x, int i) {
-            look((float)x, i);
+            // the row's first elements come behind its vectors: of equal logits the lower index
+            if ((float)x > mine || ((float)x == mine && i < mine_at)) {
+                mine = (float)x;
+                mine_at = i;
+            }
             if constexpr (L::COUNTED) {
                 if (counted) count(s, __builtin_bit_cast(uint16_t, x));
             }

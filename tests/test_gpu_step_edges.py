@@ -1,0 +1,93 @@
+"""Borders of the calls around a decoding step that test_gpu_step.py leaves out: ties of a greedy draw in rows that begin
+anywhere."""
+import numpy as np
+import pytest
+
+from tests.gpu_helpers import note
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def exq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import mixed_bitrate_quantized_amd as m
+    return m
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def f32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.float32, device="cuda")
+
+
+def host(x):
+    return x.cpu().numpy()
+
+
+# ------------------------------------------------------------------ sample
+
+GREEDY = [dict(temperature=0.0), dict(top_k=1), dict(top_p=0.0), dict(top_p=-1.0), dict(min_p=2.0), dict(temperature=0.0, top_k=7)]
+
+
+def tied_rows(rng, vocab, per, offset):
+    """Rows of `vocab` logits whose largest value stands in several places, for rows that begin `offset` elements behind a border
+    of 16 bytes (`per` elements)."""
+    head = min(vocab, (per - offset) % per)
+    rows = [np.zeros(vocab), np.full(vocab, -3.0), np.full(vocab, np.inf), rng.integers(0, 2, vocab) * 1.0,
+            np.where(rng.random(vocab) < 0.5, -0.0, 0.0), np.where(rng.random(vocab) < 0.7, -np.inf, 5.0),
+            np.where(rng.random(vocab) < 0.3, np.nan, rng.integers(-1, 1, vocab))]
+    for t in range(head):     # a place before the border, and vectors of 16 bytes that the same thread may look at
+        row = rng.standard_normal(vocab) - 10
+        row[t] = 7.0
+        for vector in (t, t + 1024, t + 2048):
+            at = head + per * vector + int(rng.integers(0, per))
+            if at < vocab:
+                row[at] = 7.0
+        rows.append(row)
+        tail = row.copy()     # and the end of the row
+        tail[:head] = -20
+        tail[vocab - 1 - t] = 7.0
+        rows.append(tail)
+    return np.stack(rows)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("vocab", [1, 3, 17, 4097, 50257])
+def test_greedy_draws_take_the_first_of_equal_logits(exq, vocab, wide):
+    """The lowest index of the largest logit, wherever a row begins: at every offset from a border of 16 bytes."""
+    rng = np.random.default_rng(vocab)
+    kind, per = (np.float32, 4) if wide else (np.float16, 8)
+    for offset in range(9):
+        note("greedy %d offset %d" % (vocab, offset))
+        rows = tied_rows(rng, vocab, per, offset % per).astype(kind)
+        want = np.array([np.argmax(np.where(np.isnan(r), -np.inf, r)) for r in rows])
+        want[[np.all(np.isnan(r) | (r == -np.inf)) for r in rows]] = -1
+        pitch = (vocab + offset + per) // per * per          # so that all rows begin alike
+        space = torch.full((len(rows), pitch), float("nan"), dtype=torch.float32 if wide else torch.float16, device="cuda")
+        d = space[:, offset:offset + vocab]
+        d.copy_(torch.from_numpy(rows))
+        u = f32(rng.random(len(rows)))
+        for settings in GREEDY:
+            tokens, logs = exq.sample(d, u, return_logprobs=True, **settings)
+            np.testing.assert_array_equal(host(tokens), want, "%d offset %d %s" % (vocab, offset, settings))
+            assert np.all(host(logs)[want >= 0] == 0)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_greedy_rows_of_an_odd_vocabulary_and_settings_of_each(exq, wide):
+    """Contiguous rows of an odd length each begin elsewhere."""
+    rows, vocab = 16, 50257
+    d = torch.zeros((rows, vocab), dtype=torch.float32 if wide else torch.float16, device="cuda")
+    u = f32(np.linspace(0, 0.99, rows))
+    for settings in GREEDY:
+        assert torch.all(exq.sample(d, u, **settings) == 0), settings
+    kinds = np.arange(rows) % 4
+    each = dict(temperature=f32(np.where(kinds == 0, 0.0, 1.0)), top_k=i32(np.where(kinds == 1, 1, 0)),
+                top_p=f32(np.where(kinds == 2, 0.0, 1.0)), min_p=f32(np.where(kinds == 3, 1.5, 0.0)))
+    assert torch.all(exq.sample(d, u, **each) == 0)
