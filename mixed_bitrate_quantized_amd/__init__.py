@@ -432,15 +432,16 @@ def _on(stream, device):
     return scope
 
 
-def _call_on(stream, device, call, *args):
-    """call(*args) under `stream` and `device`.  The tensors among args may belong to another stream: they stay allocated until
-    the named one is through with the call, also if the caller drops them before.  (Not for the handle of a stream that is not
-    PyTorch's: its owner may destroy it before the tensors are dropped, and PyTorch would still wait for it then.)"""
+def _call_on(stream, device, call, *args, own=()):
+    """call(*args) under `stream` and `device`.  The tensors among args, and those that the called object keeps (`own`), may
+    belong to another stream: they stay allocated until the named one is through with the call, also if the caller drops them
+    before.  (Not for the handle of a stream that is not PyTorch's: its owner may destroy it before the tensors are dropped, and
+    PyTorch would still wait for it then.)"""
     import torch
     with _on(stream, device):
         result = call(*args)
         if isinstance(stream, torch.cuda.Stream) and not isinstance(stream, torch.cuda.ExternalStream):
-            for x in args:
+            for x in (*args, *own):
                 if isinstance(x, torch.Tensor) and x.device == device:
                     x.record_stream(stream)
     return result
@@ -647,7 +648,9 @@ class PagePool:
     Owns `table` (int32 [sequences][width], -1 where there is no page), `lengths` (int32 [sequences]), and the list of free
     pages (`free`, `free_count`).  extend() makes room for new tokens and says where they go; trim() cuts sequences; nothing is
     read back.  table and lengths are what KVCache's calls take.  Every call runs on `stream` (default: the current stream of
-    the pool's device) and may be captured; calls on one pool, and what reads its tensors, are ordered by the caller.
+    the pool's device) and may be captured; calls on one pool, and what reads its tensors, are ordered by the caller.  A call
+    that names a torch.cuda.Stream keeps its tensors' memory and the pool's until that stream is through with them; otherwise
+    drop the pool, like any tensor, after the last call on another stream than its own, and after the graphs that hold calls.
     """
 
     def __init__(self, n_pages: int, page_size: int, sequences: int, width: int, device="cuda"):
@@ -668,6 +671,9 @@ class PagePool:
         if self.table.is_cuda:   # the first call may come on any stream
             torch.cuda.current_stream(self.device).synchronize()
 
+    def _own(self):
+        return self.table, self.lengths, self.free, self.free_count, self.served, self._workspace
+
     def extend(self, counts, rows: int, seqs=None, positions=None, offsets=None, stream=None):
         """Make room for counts[s] (int32 [sequences]) more tokens of every sequence -> (seqs, positions, offsets): for row r of
         `rows` its sequence (-1 behind the last) and position, and for sequence s its first row offsets[s].
@@ -676,7 +682,7 @@ class PagePool:
         `served` (int32 [1]) tells how many were served.  New outputs are chunks of one allocation."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            return _call_on(stream, self.device, self.extend, counts, rows, seqs, positions, offsets)
+            return _call_on(stream, self.device, self.extend, counts, rows, seqs, positions, offsets, own=self._own())
         return self._calls.extend(index, C._cuda_getCurrentRawStream(index), self.page_size, self.table, self.lengths, self.free,
                                   self.free_count, self.served, self._workspace, counts, rows, seqs, positions, offsets)
 
@@ -684,7 +690,7 @@ class PagePool:
         """Cut every sequence s to its first keep[s] tokens (int32 [sequences]; 0 releases it, negative leaves it as it is)."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            return _call_on(stream, self.device, self.trim, keep)
+            return _call_on(stream, self.device, self.trim, keep, own=self._own())
         self._calls.trim(index, C._cuda_getCurrentRawStream(index), self.page_size, self.table, self.lengths, self.free,
                          self.free_count, self._workspace, keep)
 
@@ -731,7 +737,9 @@ class Rotary:
     """Rotary positions of a model's heads: the angles of its pairs of channels on the GPU.
 
     rotary_dim: the channels that turn (default: all); interleaved: pairs are neighbours, else halves apart; base and
-    scaling: rotary_rates.  Or `rates` (angles per token, one a pair) and `factor` directly."""
+    scaling: rotary_rates.  Or `rates` (angles per token, one a pair) and `factor` directly.  A call that names a
+    torch.cuda.Stream keeps its tensors' memory and the rates' until that stream is through with them; otherwise drop the
+    object, like any tensor, after the last call on another stream than its own, and after the graphs that hold calls."""
 
     def __init__(self, head_dim: int, rotary_dim=None, base: float = 10000.0, interleaved: bool = False, scaling=None, rates=None,
                  factor=None, device="cuda"):
@@ -757,14 +765,16 @@ class Rotary:
         output) -> q_out, or (q_out, k_out), new ones as chunks of one allocation.  An output may be its input."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            return _call_on(stream, self.device, self.rotate, q, positions, k, q_out, k_out)
+            return _call_on(stream, self.device, self.rotate, q, positions, k, q_out, k_out, own=(self.rates,))
         return self._calls.rotate(index, C._cuda_getCurrentRawStream(index), self.head_dim, self.rotary_dim, self.interleaved,
                                   self.rates, self.factor, q, positions, k, q_out, k_out)
 
 
 class Adapters:
     """Low-rank adapters of one linear: a fp16 [count][rank][K], b fp16 [count][N][rank], contiguous on the GPU (kept, not
-    copied).  scales: fp32 [count]; ranks: int32 [count], where adapters have fewer than the stack's."""
+    copied).  scales: fp32 [count]; ranks: int32 [count], where adapters have fewer than the stack's.  A call that names a
+    torch.cuda.Stream keeps its tensors' memory and the adapters' until that stream is through with them; otherwise drop the
+    adapters, like any tensor, after the last call on another stream than their own, and after the graphs that hold calls."""
 
     def __init__(self, a, b, scales=None, ranks=None):
         import torch
@@ -791,7 +801,8 @@ class Adapters:
         [rows][N].  `out` may be y.  workspace: uint8, exq_lora_workspace_bytes() of them (default: allocated)."""
         index, C = self._index, self._C
         if stream is not None or C._cuda_getDevice() != index:
-            return _call_on(stream, self.device, self.add, x, ids, y, out, workspace)
+            return _call_on(stream, self.device, self.add, x, ids, y, out, workspace,
+                            own=(self.a, self.b, self.scales, self.ranks))
         return self._calls.lora_add(index, C._cuda_getCurrentRawStream(index), self.handle, self.K, self.N, x, ids, y, out,
                                     workspace)
 

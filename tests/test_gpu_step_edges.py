@@ -1,5 +1,5 @@
 """Borders of the calls around a decoding step that test_gpu_step.py leaves out: ties of a greedy draw in rows that begin
-anywhere."""
+anywhere, objects dropped while another stream has their calls before it."""
 import numpy as np
 import pytest
 
@@ -91,3 +91,42 @@ def test_greedy_rows_of_an_odd_vocabulary_and_settings_of_each(exq, wide):
     each = dict(temperature=f32(np.where(kinds == 0, 0.0, 1.0)), top_k=i32(np.where(kinds == 1, 1, 0)),
                 top_p=f32(np.where(kinds == 2, 0.0, 1.0)), min_p=f32(np.where(kinds == 3, 1.5, 0.0)))
     assert torch.all(exq.sample(d, u, **each) == 0)
+
+
+# ----------------------------------------------------------------- streams
+
+@pytest.mark.parametrize("call", ["rotate", "add", "extend", "trim"])
+def test_objects_dropped_after_a_call_on_another_stream_stay_until_it_is_through(exq, call):
+    """What an object keeps for its calls (rates, adapters, a pool's arrays) is not given out again while a stream that a call
+    named has that call still before it."""
+    half = lambda *shape: torch.ones(shape, dtype=torch.float16, device="cuda")
+    if call == "rotate":
+        thing = exq.Rotary(65536)
+        own = [thing.rates]
+        q, p = half(3, 1, 65536), i32([1, 2, 3])
+        run = lambda t: t.rotate(q, p, stream=side)
+    elif call == "add":
+        own = [half(7, 16, 4096), half(7, 4104, 16), torch.ones(7, device="cuda"), i32([16] * 7)]
+        thing = exq.Adapters(*own)
+        x, ids, y = half(40, 4096), i32(np.arange(40) % 7), half(40, 4104)
+        run = lambda t: t.add(x, ids, y, stream=side)
+    else:
+        thing = exq.PagePool(70000, 16, 3000, 20)
+        own = [thing.table, thing.lengths, thing.free, thing.free_count, thing.served, thing._workspace]
+        change = i32([5] * 3000)
+        run = lambda t: t.extend(change, 15000, stream=side) if call == "extend" else t.trim(change, stream=side)
+    side = torch.cuda.Stream()
+    run(thing)      # what the first call of a kind loads is loaded
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    note("objects on another stream: %s" % call)
+    kept = run(thing)
+    before = {x.data_ptr() for x in own}
+    kinds = [(x.shape, x.dtype) for x in own]
+    del thing, own
+    after = [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(20) for shape, dtype in kinds]
+    waiting = not side.query()
+    torch.cuda.synchronize()
+    assert not (waiting and before & {x.data_ptr() for x in after})
+    del kept
