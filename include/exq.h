@@ -588,7 +588,8 @@ size_t exq_lora_workspace_bytes(exq_adapters_t adapters, int rows);
  * Accuracy, with L_j = |x[r]| . |a[i][j]| the sum of magnitudes of one inner product
  * and S = sum_j |b[n][j]| L_j:
  *   |out - out_ref| <= 2^-11 |out_ref| + |scales[i]| S (K + rank + 64) 2^-23 + 2^-24
- * (fp32 sums; the inner products enter the second product with 22 bits).  A row's
+ * (fp32 sums; the inner products enter the second product with 22 bits, those of a rank
+ * far below the row's largest with 18 at least).  A row's
  * result does not depend on the other rows' values or ids, but for its summation
  * over K, which depends on the number of rows; deterministic.  x or y with an
  * infinity or a NaN makes that row's results infinite or NaN.

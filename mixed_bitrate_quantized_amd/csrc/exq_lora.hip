@@ -18,7 +18,8 @@
 // Products run on v_mfma_f32_16x16x32_f16, sums are fp32.  low enters the second
 // product as two fp16 numbers whose sum has 22 bits, scaled by a power of two
 // to the row's largest: rounded to one fp16 it would cost half of the error
-// the result's own rounding makes, and overflow beyond 65504.
+// the result's own rounding makes, and overflow beyond 65504.  Rows with a rank
+// too far below the largest for fp16's range take the second product in fp32.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -378,6 +379,37 @@ __device__ __forceinline__ void lora_cut(float x, int e2, _Float16& high, _Float
     high = (_Float16)x;
     rest = (_Float16)(x - (float)high);
 }
+// Whether the cut loses more than 2^-18 of the value.  The rest is good to 2^-22 of it
+// or, subnormal, to 2^-25, so values from 2^-7 on lose less; they are 2^21 below the
+// largest.  (2^-18 of each rank's product is half of the 64 * 2^-23 that the stated
+// accuracy has beside the sums.  Of a million normally distributed ranks about one is
+// as small.)
+__device__ __forceinline__ bool lora_lost(float x, int e2) {
+    x = __builtin_fabsf(__builtin_ldexpf(x, e2));
+    return x > 0.0f && x < 0x1p-7f;
+}
+
+// The second product of one row in fp32, its products `low` of the first in LDS
+// (16-byte aligned, to a multiple of 8), of columns `first` and on, `step` apart.  By
+// the row's own values alone, as in the tiles: what shares a tile with it does not
+// change it.  48 rows of rank 64 beside 8192 x 28672 take 23.2 us, with one such row
+// 26.4, with nothing else 66; 2048 rows of rank 32 beside 8192 x 8192 38, 38 and 205;
+// one row of rank 16 8.8 and 9.2.
+__device__ __forceinline__ void lora_expand_row(const LoraArgs& a, const LoraTile& tile, int64_t row, int first, int n_end, int step, const float* low) {
+    const uint16_t* b = a.b + (int64_t)tile.adapter * a.N * a.rank;
+    for (int c = first; c < n_end; c += step) {
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int j = 0; j < tile.rank; j += 8) {   // a.rank is a multiple of 8
+            const h8 x = *gptr<h8>(b + (int64_t)c * a.rank + j);
+            const f4 l[2] = {*reinterpret_cast<const f4*>(low + j), *reinterpret_cast<const f4*>(low + j + 4)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)   // what lies behind the adapter's own rank may be anything
+                sum = __builtin_fmaf(l[e / 4][e % 4], j + e < tile.rank ? (float)x[e] : 0.0f, sum);
+        }
+        *gptr_w<_Float16>(a.out + row * a.out_row + c) = (_Float16)__builtin_fmaf(sum, tile.scale, (float)*gptr<_Float16>(a.y + row * a.y_row + c));
+    }
+}
 
 constexpr int kExpandWaves = 4;
 constexpr int kLowPad = 8;   // fp16 after each row of low in LDS, against bank conflicts
@@ -389,7 +421,9 @@ template <int T>
 __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint16_t lds[];
     __shared__ float unscale[T];
-    constexpr int TT = T / 16, NT = T == 64 ? 2 : 4, COLS = 16 * NT;
+    constexpr int TT = T / 16, NT = T == 64 ? 2 : 4, COLS = 16 * NT, RANK = T == 64 ? kExpandRank64 : kExpandRank16;
+    __shared__ bool lost[T];   // rows for lora_expand_row
+    __shared__ __attribute__((aligned(16))) float row_low[kExpandWaves][RANK];
     const int block = blockIdx.x % a.blocks;
     int rows_of_tile;
     const LoraTile tile = lora_tile<T>(a, blockIdx.x / a.blocks, rows_of_tile);
@@ -404,7 +438,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
     uint16_t *hi = lds, *lo = lds + T * pitch;
     // low: a few lanes a row add up its parts, all asked for at once
     constexpr int LANES = 64 * kExpandWaves / T;   // of a row: 16 or 4
-    constexpr int MOST = (T == 64 ? kExpandRank64 : kExpandRank16) / (4 * LANES);
+    constexpr int MOST = RANK / (4 * LANES);
     const int low_row = t / LANES, first = 4 * (t % LANES);
     const float* from = a.low + (int64_t)__shfl(rows_of_tile, low_row) * a.rank;
     const int64_t part = (int64_t)a.rows * a.rank;
@@ -467,6 +501,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
 #pragma unroll
         for (int d = 1; d < LANES; d *= 2) most = __builtin_fmaxf(most, __shfl_xor(most, d));
         const int e2 = lora_shift(most);
+        bool mine = false;
 #pragma unroll
         for (int m = 0; m < MOST; ++m) {
             const int j = first + 4 * LANES * m;
@@ -476,18 +511,27 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
             for (int e = 0; e < 4; ++e) {
                 _Float16 high, rest;
                 lora_cut(v[m][e], e2, high, rest);
+                mine = mine || lora_lost(v[m][e], e2);
                 h[e] = high;
                 l[e] = rest;
             }
             *reinterpret_cast<h4*>(hi + low_row * pitch + j) = h;
             *reinterpret_cast<h4*>(lo + low_row * pitch + j) = l;
         }
-        if (first == 0) unscale[low_row] = __builtin_ldexpf(tile.scale, -e2);
+        const uint64_t any = __ballot(mine) >> (lane / LANES * LANES) & ((1ull << LANES) - 1);
+        if (first == 0) {
+            unscale[low_row] = __builtin_ldexpf(tile.scale, -e2);
+            lost[low_row] = any != 0;
+        }
     }
     __syncthreads();
+    uint64_t lost_rows = __ballot(lane < T && lost[lane % T]);
     float f[TT];
 #pragma unroll
-    for (int j = 0; j < TT; ++j) f[j] = unscale[16 * j + i16];
+    for (int j = 0; j < TT; ++j) {
+        f[j] = unscale[16 * j + i16];
+        in[j] = in[j] && !(lost_rows >> (16 * j + i16) & 1);
+    }
     const auto step = [&](Loaded& x, int n0) {
         f4 acc[NT][TT];
 #pragma unroll
@@ -537,6 +581,19 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
         if (n0 + 2 * STEP < n_end) load(l0, n0 + 2 * STEP);
         step(l1, n0 + STEP);
     }
+    for (; lost_rows; lost_rows &= lost_rows - 1) {   // seldom any
+        // (nothing that the loop above would have to keep a register for)
+        const int64_t at = a.tile_rows[(int64_t)(blockIdx.x / a.blocks) * T + __builtin_ctzll(lost_rows)];
+        const int own = __builtin_amdgcn_readfirstlane(wave), l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+        wave_lds_fence();
+        for (int j = l; j < a.rank; j += 64) {
+            float x = 0.0f;
+            for (int p = 0; p < a.splits; ++p) x += *gptr<float>(a.low + p * part + at * a.rank + j);   // in the order of above
+            row_low[own][j] = x;
+        }
+        wave_lds_fence();
+        lora_expand_row(a, tile, at, n_begin + 64 * own + l, n_end, 64 * kExpandWaves, row_low[own]);
+    }
 }
 
 // All of it for a few rows of small adapters, ranks up to 16: every workgroup takes
@@ -561,7 +618,7 @@ __global__ __launch_bounds__(64 * kAloneWaves) void lora_alone_kernel(LoraArgs a
         lora_copy(a, tile, rows_of_tile, n_begin, n_end);
         return;
     }
-    const bool in = i16 < tile.count;
+    bool in = i16 < tile.count;
     const int64_t row = __shfl(rows_of_tile, i16);
     const uint16_t* b = a.b + (int64_t)tile.adapter * a.N * a.rank;
     struct Loaded {   // for a step of columns, 8 of a row to a lane
@@ -637,13 +694,18 @@ __global__ __launch_bounds__(64 * kAloneWaves) void lora_alone_kernel(LoraArgs a
     most = __builtin_fmaxf(most, __shfl_xor(most, 32));
     const int e2 = lora_shift(most);
     h8 high, rest;
+    bool mine = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         _Float16 h, l;
         lora_cut(low[e / 4][e % 4], e2, h, l);
+        mine = mine || lora_lost(low[e / 4][e % 4], e2);
         high[e] = h;
         rest[e] = l;
     }
+    uint64_t lost_rows = __ballot(mine);
+    lost_rows = (lost_rows | lost_rows >> 16) & 0xFFFF;
+    in = in && !(lost_rows >> i16 & 1);
     const float f = __builtin_ldexpf(tile.scale, -e2);
     for (; n0 < n_end; n0 += kAloneColumns) {
         const Loaded x = next;
@@ -658,6 +720,17 @@ __global__ __launch_bounds__(64 * kAloneWaves) void lora_alone_kernel(LoraArgs a
         }
         const int n = n0 + 8 * q;
         if (in && n < n_end) *gptr_w<h8>(a.out + row * a.out_row + n) = o;
+    }
+    for (; lost_rows; lost_rows &= lost_rows - 1) {   // seldom any
+        const int i = __builtin_ctzll(lost_rows);
+        float* x = reinterpret_cast<float*>(turned[wave]);
+        wave_lds_fence();
+        if (q < 2 && i16 == i) {
+            *reinterpret_cast<f4*>(x + 8 * q) = low[0];
+            *reinterpret_cast<f4*>(x + 8 * q + 4) = low[1];
+        }
+        wave_lds_fence();
+        lora_expand_row(a, tile, __builtin_amdgcn_readlane(rows_of_tile, i), n_begin + t, n_end, 64 * kAloneWaves, x);
     }
 }
 

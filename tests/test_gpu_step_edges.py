@@ -1,9 +1,12 @@
 """Borders of the calls around a decoding step that test_gpu_step.py leaves out: ties of a greedy draw in rows that begin
-anywhere, objects dropped while another stream has their calls before it."""
+anywhere, objects dropped while another stream has their calls before it, adapters whose ranks differ by orders of magnitude.
+
+The adapters' tolerance is the one that include/exq.h states."""
 import numpy as np
 import pytest
 
-from tests.gpu_helpers import note
+from oracle import stepref as ref
+from tests.gpu_helpers import note, to_dev as dev
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +133,68 @@ def test_objects_dropped_after_a_call_on_another_stream_stay_until_it_is_through
     torch.cuda.synchronize()
     assert not (waiting and before & {x.data_ptr() for x in after})
     del kept
+
+
+# ---------------------------------------------------------------- adapters
+
+def check_lora(out, x, ids, y, a, b, scales, ranks, what):
+    """Results that round past 65504 are infinite: 65536, the next step of fp16's grid, on both sides."""
+    want, size = ref.lora(x, ids, y, a, b, scales, ranks)
+    bound = 2.0 ** -11 * np.abs(want) + size * (a.shape[2] + a.shape[1] + 64) * 2.0 ** -23 + 2.0 ** -24
+    got = host(out).astype(np.float64)
+    got, want = np.where(np.isinf(got), np.copysign(65536.0, got), got), np.clip(want, -65536, 65536)
+    e = np.abs(got - want) / bound
+    assert e.max() <= 1, "%s: %.3g of the bound" % (what, e.max())
+
+
+def uneven_stack(rng, count, K, N, rank):
+    """Adapters whose ranks differ by up to 2^39: the largest inner products meet zeros of b in half of the columns, so that
+    the small ones alone make the result there."""
+    a = rng.uniform(0.5, 1, (count, rank, K)) * rng.choice([-1, 1], (count, rank, K))
+    power = rng.integers(-22, 15, (count, rank, 1))
+    power[:, 0], power[:, 1] = 15, -22
+    a = (a * 2.0 ** power).astype(np.float16)
+    b = rng.standard_normal((count, N, rank)).astype(np.float16)
+    b[:, ::2, power[0, :, 0] > -12] = 0
+    b[:, ::2] *= np.float16(2.0 ** 12)
+    return a, b
+
+
+@pytest.mark.parametrize("K,N,rank", [(8, 64, 8), (8, 520, 16), (256, 264, 16), (8192, 136, 16), (8, 264, 40), (520, 1032, 64), (72, 136, 128),
+                                      (64, 72, 256)])
+def test_lora_ranks_of_very_different_size(exq, K, N, rank):
+    """What the largest inner product of a row leaves of the smallest, in one launch and in two, by every size of tile."""
+    rng = np.random.default_rng(K + N + rank)
+    a, b = uneven_stack(rng, 2, K, N, rank)
+    if K == 8 and rank == 8:      # sums of one sign: by hand 3 * 2^-24 * 65504 * 8
+        a[1], b[1] = 0, 0
+        a[1, 0], a[1, 1], b[1, :, 1] = 32768, 3 * 2.0 ** -24, 65504
+    adapters = exq.Adapters(dev(a), dev(b))
+    for rows in (1, 2, 16, 17, 70, 600):
+        note("lora of uneven ranks, %d rows" % rows)
+        x = rng.standard_normal((rows, K)).astype(np.float16)
+        x[0] = 1
+        y = np.zeros((rows, N), dtype=np.float16)
+        ids = rng.integers(0, 2, rows)
+        ids[0] = 1
+        check_lora(adapters.add(dev(x), i32(ids), dev(y)), x, ids, y, a, b, None, None, "%d rows" % rows)
+
+
+@pytest.mark.parametrize("K,rank", [(256, 8), (256, 64)])
+def test_a_row_of_uneven_products_leaves_the_others_alone(exq, K, rank):
+    rng = np.random.default_rng(K + rank)
+    a = (rng.standard_normal((1, rank, K)) * K ** -0.5).astype(np.float16)
+    b = rng.standard_normal((1, 264, rank)).astype(np.float16)
+    a[0, 1], a[0, 1, 0] = 0, 2.0 ** -24
+    adapters = exq.Adapters(dev(a), dev(b))
+    for rows in (5, 40, 600):
+        x = rng.standard_normal((rows, K)).astype(np.float16)
+        x[:, 0] = 0
+        y = rng.standard_normal((rows, 264)).astype(np.float16)
+        ids = i32([0] * rows)
+        plain = host(adapters.add(dev(x), ids, dev(y)))
+        x[3, 0] = 2.0 ** -3       # rank 1 of this row is 2^-27
+        mixed = host(adapters.add(dev(x), ids, dev(y)))
+        rest = np.arange(rows) != 3
+        np.testing.assert_array_equal(mixed[rest], plain[rest])
+        check_lora(adapters.add(dev(x), ids, dev(y)), x, [0] * rows, y, a, b, None, None, "%d rows" % rows)
