@@ -540,9 +540,10 @@ exq_status exq_pages_trim(int32_t* table, int sequences, int table_width, int64_
  *   rates      device double [rotary_dim / 2], angles per token
  *   factor     finite; multiplies the turned channels (1 but for stretched contexts)
  *   positions  device int32 [rows]
- * Accuracy: t in 64 bits (|p rates[i]| < 2^40), its sine and cosine and the products
- * in fp32: |u' - u'_ref| <= 2^-11 |u'_ref| + 2^-20 |factor| (|u| + |v|) + 2^-24.  Fastest where
- * rotary_dim is a multiple of 16.
+ * Accuracy: t the exact product, reduced to a part of a turn in 64 bits, for |t| < 2^40;
+ * its sine and cosine and the products in fp32:
+ *   |u' - u'_ref| <= 2^-11 |u'_ref| + 2^-20 |factor| (|u| + |v|) + 2^-24
+ * Fastest where rotary_dim is a multiple of 16.
  * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED (rows * heads beyond a
  * launch), HIP. */
 exq_status exq_rotate(const void* q, int64_t q_row_stride, int64_t q_head_stride, void* q_out,

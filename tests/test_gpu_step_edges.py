@@ -1,7 +1,10 @@
 """Borders of the calls around a decoding step that test_gpu_step.py leaves out: ties of a greedy draw in rows that begin
-anywhere, objects dropped while another stream has their calls before it, adapters whose ranks differ by orders of magnitude.
+anywhere, objects dropped while another stream has their calls before it, adapters whose ranks differ by orders of magnitude,
+angles up to 2^40.
 
-The adapters' tolerance is the one that include/exq.h states."""
+The tolerances of adapters and angles are those that include/exq.h states."""
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 
@@ -198,3 +201,58 @@ def test_a_row_of_uneven_products_leaves_the_others_alone(exq, K, rank):
         rest = np.arange(rows) != 3
         np.testing.assert_array_equal(mixed[rest], plain[rest])
         check_lora(adapters.add(dev(x), ids, dev(y)), x, [0] * rows, y, a, b, None, None, "%d rows" % rows)
+
+
+# ------------------------------------------------------------------ rotate
+
+TWO_PI = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+
+
+def turned(x, positions, rates, interleaved):
+    """x [rows][heads][2 * pairs] turned by the exact product of position and rate, and |u| + |v| of each channel's pair."""
+    out, pair = np.zeros(x.shape), np.zeros(x.shape)
+    half = len(rates)
+    with localcontext() as context:
+        context.prec = 120
+        for r, p in enumerate(positions):
+            for i, rate in enumerate(rates):
+                t = float(Decimal(int(p)) * Decimal(float(rate)) % TWO_PI)
+                a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+                u, v = x[r, :, a].astype(np.float64), x[r, :, b].astype(np.float64)
+                out[r, :, a], out[r, :, b] = u * np.cos(t) - v * np.sin(t), u * np.sin(t) + v * np.cos(t)
+                pair[r, :, a] = pair[r, :, b] = np.abs(u) + np.abs(v)
+    return out, pair
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim", [32, 24])
+def test_rotate_far_angles(exq, dim, interleaved):
+    """Angles up to 2^40: those of the stated accuracy, 2^-20 of a pair beside the result's rounding.  fp16 results round at
+    2^-11 of themselves, so pairs (1, 0) at the angles where a channel is small show the angle's error."""
+    rng = np.random.default_rng(dim)
+    rows = 60
+    positions = np.concatenate([[2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30 + 1, 1 << 30], rng.integers(1 << 29, 2 ** 31, rows - 4)])
+    x = np.zeros((rows, 2, dim), dtype=np.float16)
+    x[:, 0, :] = 1.0
+    x[:, 1, 0::2] = 1.0
+    for top in (2, 2 ** 3, 2 ** 6, 2 ** 9):       # angles up to 2^40
+        rates = rng.uniform(0.5, 1, dim // 2) * top
+        note("rotate by up to 2^%d" % (30 + np.log2(top)))
+        # of many pairs, those that a turn takes within 2^-9 of an axis, where fp16 has 2^-20 and less
+        rates[: dim // 4] = near_axis(positions[0], rates[: dim // 4])
+        rotary = exq.Rotary(dim, interleaved=interleaved, rates=rates)
+        got = host(rotary.rotate(dev(x), i32(positions))).astype(np.float64)
+        want, pair = turned(x, positions, host(rotary.rates), interleaved)
+        bound = 2.0 ** -11 * np.abs(want) + 2.0 ** -20 * pair + 2.0 ** -24
+        assert np.all(np.abs(got - want) <= bound), "up to 2^%d: %.3g of the bound" % (30 + np.log2(top), np.max(np.abs(got - want) / bound))
+
+
+def near_axis(position, rates):
+    """The rates, each moved so that `position` times it lies within 2^-14 of a multiple of half a turn, or as near as doubles get."""
+    out = []
+    with localcontext() as context:
+        context.prec = 120
+        for rate in rates:
+            turns = (Decimal(int(position)) * Decimal(float(rate)) / (TWO_PI / 2)).to_integral_value()
+            out.append(float(turns * (TWO_PI / 2) / int(position)))
+    return np.array(out)
