@@ -628,9 +628,10 @@ exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_st
  *            Calls that may run at the same time need one each
  * A row without a logit that may be drawn, or with a u, T, top_p or min_p that is
  * NaN, or a negative T, gets token -1 and logprob NaN.
- * Weights are computed in 64 bits, to 2^-45 relative, and summed exactly, in units of
- * 2^-42 (vocab of 2^21) to 2^-51 (4096 and fewer) of the largest; where one weight
- * stands for all equal fp16 logits, in 64-bit floating point.  The same call gives the
+ * Weights are computed in 64 bits, those of 2^-51 of the largest and more to 2^-43
+ * relative, and summed exactly, in units of 2^-42 (vocab of 2^21) to 2^-51 (4096 and
+ * fewer) of the largest; where one weight stands for all equal fp16 logits, in 64-bit
+ * floating point.  The same call gives the
  * same tokens.  With and without a workspace a sum may differ by its rounding, and
  * then a token whose border lies that close to u.  A logprob is within 2^-23 of its
  * value relative, or 2^-30.

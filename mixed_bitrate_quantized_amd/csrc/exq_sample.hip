@@ -41,6 +41,7 @@
 #include "exq_device_common.h"
 #include "exq_internal.h"
 #include "exq_operand.h"
+#include "exq_powers.h"
 
 namespace exq {
 
@@ -56,7 +57,6 @@ constexpr int kSampleParts = 16;              // of a row, at most
 constexpr int kSampleCountedShare = 32768;    // logits of a part of an fp16 row with top-p, at most
 constexpr int kSamplePartList = 1024;         // candidates of a part
 constexpr int kSampleMaxVocabLog2 = 21;
-constexpr int kPowers = 256;                  // 2^(i / 256) in LDS
 constexpr int kCounters = 1 << 15;            // of 16 bits for each sign
 
 // A setting of every row: from memory, or the same for all.
@@ -157,38 +157,17 @@ template <> struct Logit<float> {
     __device__ __forceinline__ static float value(uint32_t k) { return __builtin_bit_cast(float, k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu)); }
 };
 
-constexpr double kLn2d = 0.69314718055994530942;
 constexpr double kInfinite = 0x1p128;   // in an infinite logit's place
 
-// 2^f for |f| <= 1 from its series; the first term left out is below 2^-53 of it
-// at 1/2, and 2^-40 at 1.
-__device__ __forceinline__ double exp2_series(double f) {
-    double p = 1.0;
-#pragma unroll
-    for (int i = 13; i >= 1; --i) p = __builtin_fma(p, f * (kLn2d / i), 1.0);
-    return p;
-}
-
-// Weights of a row: 2^(j / 256) from LDS times 2^r, |r| <= 1/512, whose series is cut
-// behind r^3: within 2^-45.
+// Weights of a row.  A power is good to 2^-45.2, and the exponent's roundings cost a
+// weight w 2^-51 |ln w|: 2^-45.9 at 2^-51.  Where up to three powers are multiplied
+// (sum_counters) that makes 2^-43.3.
 struct Weights {
     float topf;
     double top, c;   // largest logit (kInfinite), 256 log2(e) / T; beside an infinity all else weighs nothing
     double scale;    // 2^shift
     const double* powers;
-    __device__ __forceinline__ double power(double t) const {   // 2^(t / 256)
-#pragma clang fp contract(off)   // the same bits wherever the compiler puts it
-        constexpr double a = kLn2d / kPowers;
-        t = __builtin_fmax(t, -256.0 * 1000);
-        const double n = t + 6755399441055744.0;   // 1.5 * 2^52: rounds t, and leaves it in the sum's low bits
-        const double f = t - (n - 6755399441055744.0);
-        const int j = (int)(uint32_t)__builtin_bit_cast(uint64_t, n);
-        const double near = powers[j & (kPowers - 1)];
-        // |f| <= 1/2; the square's factor is a little above 1/2, which takes the error from 2^-42.7 to 2^-45.2
-        const double q = __builtin_fma(f, __builtin_fma(f, a * a * a / 6, a * a * (0.5 + 0.0345178 * a * a / 4)), a);
-        const double w = __builtin_fma(near * f, q, near);
-        return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, w) + ((uint64_t)(uint32_t)((j >> 8) << 20) << 32));
-    }
+    __device__ __forceinline__ double power(double t) const { return power_of(powers, t); }   // 2^(t / 256)
     __device__ __forceinline__ double real(float l) const {   // l: at most the largest
 #pragma clang fp contract(off)
         return power((__builtin_fmin((double)l, kInfinite) - top) * c);
