@@ -155,9 +155,9 @@ __global__ __launch_bounds__(kPagesThreads) void pages_scan_kernel(PagesArgs a) 
             add[i] = need[i] = 0;
             if (EXTEND) {
                 add[i] = n[i] < 0 ? 0 : max(c, 0);
-                // what does not fit the table counts as more than there can be
+                // what does not fit the table counts as 2^32 - 1 pages, more than a list has
                 const int64_t end = (int64_t)n[i] + add[i];
-                need[i] = add[i] == 0 ? 0 : end > most ? 0x7FFFFFFF : pages_of(end, a.page_size) - pages_of(n[i], a.page_size);
+                need[i] = add[i] == 0 ? 0 : end > most ? -1 : pages_of(end, a.page_size) - pages_of(n[i], a.page_size);
                 rows += (uint32_t)add[i];
             } else if (c >= 0 && c < n[i]) {
                 add[i] = 1;   // the length changes

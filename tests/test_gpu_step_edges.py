@@ -1,6 +1,6 @@
 """Borders of the calls around a decoding step that test_gpu_step.py leaves out: ties of a greedy draw in rows that begin
 anywhere, objects dropped while another stream has their calls before it, adapters whose ranks differ by orders of magnitude,
-angles up to 2^40.
+angles up to 2^40, the largest list of pages.
 
 The tolerances of adapters and angles are those that include/exq.h states."""
 from decimal import Decimal, localcontext
@@ -256,3 +256,23 @@ def near_axis(position, rates):
             turns = (Decimal(int(position)) * Decimal(float(rate)) / (TWO_PI / 2)).to_integral_value()
             out.append(float(turns * (TWO_PI / 2) / int(position)))
     return np.array(out)
+
+
+# ------------------------------------------------------------------- pages
+
+def test_a_row_too_long_for_the_table_is_not_served_from_the_largest_list(exq):
+    """2^31 - 1 free pages: what does not fit a row of the table has to count as more."""
+    note("a list of 2^31 - 1 pages")
+    n = 2 ** 31 - 1
+    pool = exq.PagePool(n, 16, 3, 2)
+    for counts, served, rows in (([33, 1, 1], 0, 0), ([32, 2 ** 31 - 1, 1], 1, 32), ([1, 1, 1], 0, 0), ([0, 32, 33], 2, 32)):
+        seqs, positions, offsets = pool.extend(i32(counts), 40)
+        assert int(pool.served) == served and int(offsets[-1]) == rows, counts
+        assert int((seqs >= 0).sum()) == rows
+    np.testing.assert_array_equal(host(pool.table), [[0, 1], [2, 3], [-1, -1]])
+    np.testing.assert_array_equal(host(pool.lengths), [32, 32, 0])
+    assert int(pool.free_count) == n - 4 and int(pool.free[n - 5]) == 4
+    pool.trim(i32([0, 0, 0]))
+    assert int(pool.free_count) == n and host(pool.free[-4:]).tolist() == [3, 2, 1, 0]
+    del pool
+    torch.cuda.empty_cache()
