@@ -637,7 +637,7 @@ exq_status exq_lora_add(exq_adapters_t adapters, const void* x, int64_t x_row_st
  * value relative, or 2^-30.
  * Capturable: no allocation, no wait.  rows == 0 is a no-op.  Errors: INVALID_ARG (NULL, misaligned, a bad size, stride or
  * setting, tokens or logprobs overlapping an input or each other), UNSUPPORTED
- * (bits, vocab), HIP. */
+ * (bits, vocab, 2^22 rows and more), HIP. */
 size_t exq_sample_workspace_bytes(int rows, int vocab);   /* 0: none is needed */
 exq_status exq_sample(const void* logits, int bits, int rows, int vocab, int64_t row_stride, const float* u,
                       const float* temperatures, float temperature, const int32_t* top_ks, int top_k,

@@ -1420,6 +1420,7 @@ extern "C" exq_status exq_sample(const void* logits, int bits, int rows, int voc
         if (need && !no_row) parts = sample_parts(rows, vocab);
         if (bits == 16 && vocab > kSampleCountedShare * parts && !top_ps && top_p < 1) parts = 1;
     }
+    if ((int64_t)rows * parts * kSampleThreads > kMaxLaunchThreads) return fail(EXQ_ERR_UNSUPPORTED, "%d rows in one call", rows);
     int log2 = 0;
     while ((1 << log2) < vocab) ++log2;
     const SampleArgs a{logits, row_stride, rows, vocab, std::min(51, 63 - log2), u, {temperatures, temperature},
