@@ -379,6 +379,12 @@ __device__ __forceinline__ void lora_cut(float x, int e2, _Float16& high, _Float
     high = (_Float16)x;
     rest = (_Float16)(x - (float)high);
 }
+// What takes a sum back: the adapter's scale over the row's.  Past fp32's range it stays
+// at the largest: what it meets is 0, or far beyond fp16 either way.
+__device__ __forceinline__ float lora_unscale(float scale, int e2) {
+    const float f = __builtin_ldexpf(scale, -e2);
+    return __builtin_fabsf(scale) <= __FLT_MAX__ ? __builtin_fmaxf(__builtin_fminf(f, __FLT_MAX__), -__FLT_MAX__) : f;
+}
 // Whether the cut loses more than 2^-18 of the value.  The rest is good to 2^-22 of it
 // or, subnormal, to 2^-25, so values from 2^-7 on lose less; they are 2^21 below the
 // largest.  (2^-18 of each rank's product is half of the 64 * 2^-23 that the stated
@@ -520,7 +526,7 @@ __global__ __launch_bounds__(64 * kExpandWaves, 3) void lora_expand_kernel(LoraA
         }
         const uint64_t any = __ballot(mine) >> (lane / LANES * LANES) & ((1ull << LANES) - 1);
         if (first == 0) {
-            unscale[low_row] = __builtin_ldexpf(tile.scale, -e2);
+            unscale[low_row] = lora_unscale(tile.scale, e2);
             lost[low_row] = any != 0;
         }
     }
@@ -706,7 +712,7 @@ __global__ __launch_bounds__(64 * kAloneWaves) void lora_alone_kernel(LoraArgs a
     uint64_t lost_rows = __ballot(mine);
     lost_rows = (lost_rows | lost_rows >> 16) & 0xFFFF;
     in = in && !(lost_rows >> i16 & 1);
-    const float f = __builtin_ldexpf(tile.scale, -e2);
+    const float f = lora_unscale(tile.scale, e2);
     for (; n0 < n_end; n0 += kAloneColumns) {
         const Loaded x = next;
         if (n0 + kAloneColumns < n_end) next = load(n0 + kAloneColumns);

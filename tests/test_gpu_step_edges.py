@@ -203,6 +203,23 @@ def test_a_row_of_uneven_products_leaves_the_others_alone(exq, K, rank):
         check_lora(adapters.add(dev(x), ids, dev(y)), x, [0] * rows, y, a, b, None, None, "%d rows" % rows)
 
 
+@pytest.mark.parametrize("K,rank", [(4096, 16), (4096, 64)])
+def test_lora_of_the_largest_scales(exq, K, rank):
+    """Inner products of 2^44 by a scale of 2^100 and more: past fp16, but y where b is 0."""
+    a = np.full((2, rank, K), 65504, dtype=np.float16)
+    b = np.zeros((2, 264, rank), dtype=np.float16)
+    b[:, 1::2] = np.float16(2.0 ** -24)
+    adapters = exq.Adapters(dev(a), dev(b), f32([2.0 ** 100, -np.finfo(np.float32).max]))
+    for rows in (1, 30, 600):
+        x = np.full((rows, K), 65504, dtype=np.float16)
+        y = np.random.default_rng(rows).standard_normal((rows, 264)).astype(np.float16)
+        ids = np.arange(rows) % 2
+        note("lora of the largest scales, %d rows" % rows)
+        got = host(adapters.add(dev(x), i32(ids), dev(y)))
+        np.testing.assert_array_equal(got[:, ::2], y[:, ::2])
+        np.testing.assert_array_equal(got[:, 1::2], np.where(ids[:, None], -np.inf, np.inf) * np.ones((1, 132)))
+
+
 # ------------------------------------------------------------------ rotate
 
 TWO_PI = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
