@@ -685,6 +685,11 @@ template <class T> __device__ __forceinline__ void filter_list(SampleShared& s, 
         const uint64_t one = counts ? 1 : w.of(L::value(key));
         f.cut = Cut{key, (uint32_t)((need - below + one - 1) / one)};
     }
+    if (f.cut.key == 0) {   // the whole list is left, and the draw looks at the row: from the list's smallest key on
+        uint64_t rest = 0;
+        each([&](uint32_t k, uint64_t) { rest = std::max<uint64_t>(rest, ~k); });
+        f.cut = Cut{~(uint32_t)reduce<Larger>(s, rest), 0xFFFFFFFFu};
+    }
 }
 
 // The row in tiles: its head, groups of 64 vectors (a wave's look), its tail.

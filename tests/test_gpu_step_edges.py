@@ -99,6 +99,43 @@ def test_greedy_rows_of_an_odd_vocabulary_and_settings_of_each(exq, wide):
     assert torch.all(exq.sample(d, u, **each) == 0)
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("vocab,k", [(2400, 300), (8000, 899), (1334, 901), (5406, 2000), (20011, 1500), (40000, 4000), (70001, 4096)])
+def test_a_top_k_that_ends_at_a_gap(exq, vocab, k, wide):
+    """The first k logits far above the others, so that what is looked at more closely is exactly those k; at a high temperature
+    the others would weigh as much."""
+    rng = np.random.default_rng(vocab + k)
+    rows = 24
+    x = rng.uniform(-1, 1, (rows, vocab))
+    for r, row in enumerate(x):
+        # neighbours 16 bytes apart, where they fit so, or anywhere
+        places = np.arange(k) * 8 if r % 2 and 8 * k <= vocab else rng.permutation(vocab)[:k]
+        row[places] = 8 + rng.uniform(0, 1, k)
+        if r % 3 == 2:
+            row[rng.permutation(vocab)[:vocab // 5]] = -np.inf
+    x = x.astype(np.float32 if wide else np.float16)
+    u = rng.random(rows).astype(np.float32)
+    note("top-k %d of %d at a gap" % (k, vocab))
+    for settings in (dict(top_k=k), dict(top_k=k, min_p=1e-3), dict(top_k=k, top_p=0.999), dict(top_k=k, top_p=0.5)):
+        got = host(exq.sample(dev(x), f32(u), temperature=10.0, **settings))
+        one = {z: v if z == "top_k" else np.float32(v) for z, v in settings.items()}
+        want = [ref.sample_row(l, v, np.float32(10.0), **one)[0] for l, v in zip(x, u)]
+        np.testing.assert_array_equal(got, want, "%d of %d %s" % (k, vocab, settings))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("vocab", [351, 462, 1334, 5406])
+def test_a_top_k_of_hundreds_in_short_rows(exq, vocab, wide):
+    """Many rows of few logits: by chance the list ends at the k-th in some."""
+    rng = np.random.default_rng(vocab)
+    x = (3 * rng.standard_normal((140, vocab))).astype(np.float32 if wide else np.float16)
+    u = rng.random(140).astype(np.float32)
+    for k in (300, vocab // 2 + 100, vocab - 20):
+        for t in (1.0, 10.0):
+            got = host(exq.sample(dev(x), f32(u), temperature=t, top_k=k))
+            np.testing.assert_array_equal(got, [ref.sample_row(l, v, np.float32(t), k)[0] for l, v in zip(x, u)], "%d of %d" % (k, vocab))
+
+
 # ----------------------------------------------------------------- streams
 
 @pytest.mark.parametrize("call", ["rotate", "add", "extend", "trim"])
