@@ -957,7 +957,8 @@ template <class T, bool FIRST> __global__ __launch_bounds__(kSampleThreads) void
                     (double)(1ull << a.shift), s.powers};
     Row f{0, a.vocab, top_key, L::BITS, 0, 1.0f, Cut{0, 0xFFFFFFFFu}, 0, u, temperature};
     if (min_p > 0.0f) {   // w >= min-p where the logit is M + T ln(min-p) or more
-        const double least = min_p == 1.0f ? (double)topf : (double)topf + (double)temperature * s.log_min_p;
+        // (at an infinite temperature all weigh 1: infinity times ln(min-p), 0 for 1, is no number from which on)
+        const double least = min_p == 1.0f && temperature <= __FLT_MAX__ ? (double)topf : (double)topf + (double)temperature * s.log_min_p;
         f.least = L::first_from(least);
     }
 

@@ -136,6 +136,28 @@ def test_a_top_k_of_hundreds_in_short_rows(exq, vocab, wide):
             np.testing.assert_array_equal(got, [ref.sample_row(l, v, np.float32(t), k)[0] for l, v in zip(x, u)], "%d of %d" % (k, vocab))
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("vocab", [50, 3001, 40000])
+def test_min_p_at_an_infinite_temperature(exq, vocab, wide):
+    """Every logit weighs e^0 there: no min-p up to 1 drops any; a large finite one leaves the largest alone."""
+    rng = np.random.default_rng(vocab)
+    x = rng.standard_normal((6, vocab)).astype(np.float32 if wide else np.float16)
+    x[1, ::3] = -np.inf
+    x[2, 5:9] = np.inf
+    u = rng.random(6).astype(np.float32)
+    for min_p in (1.0, 0.5, 1e-30):
+        for settings in (dict(), dict(top_k=40), dict(top_k=vocab // 2), dict(top_p=0.5)):
+            for each in (False, True):
+                t = f32([np.inf] * 6) if each else float("inf")
+                m = f32([min_p] * 6) if each else min_p
+                got = host(exq.sample(dev(x), f32(u), temperature=t, min_p=m, **settings))
+                one = {z: v if z == "top_k" else np.float32(v) for z, v in settings.items()}
+                want = [ref.sample_row(l, v, np.float32(np.inf), min_p=np.float32(min_p), **one)[0] for l, v in zip(x, u)]
+                np.testing.assert_array_equal(got, want, "%d %g %s" % (vocab, min_p, settings))
+    got = host(exq.sample(dev(x[3:]), f32(u[3:]), temperature=1e30, min_p=1.0))
+    np.testing.assert_array_equal(got, [np.argmax(l) for l in x[3:]])
+
+
 # ----------------------------------------------------------------- streams
 
 @pytest.mark.parametrize("call", ["rotate", "add", "extend", "trim"])
