@@ -704,6 +704,8 @@ def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling=None):
       {"kind": "parts", "factor": s, "context": c, "low": 1, "high": 32, "attention": None}
           pairs by the number of turns they make in the trained context of c tokens: below `low` divided by s, above
           `high` as they are, a mixture between; and the channels times `attention` (None: 0.1 ln s + 1).
+          The mixture is linear in the number of turns.  Where a model was stretched with one that is linear in the pair's
+          index, between bounds rounded to whole pairs, give Rotary those `rates`.
     """
     if rotary_dim < 2 or rotary_dim % 2 or not base > 0:
         raise ExqError(EXQ_ERR_INVALID_ARG, "argument check", "rotary_dim=%d base=%r" % (rotary_dim, base))

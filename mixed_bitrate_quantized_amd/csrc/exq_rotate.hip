@@ -160,7 +160,9 @@ extern "C" exq_status exq_rotate(const void* q, int64_t q_row_stride, int64_t q_
     }
     if (q_heads && k_heads && (operands_meet(out[0], out[1]) || operands_meet(out[0], in[1]) || operands_meet(out[1], in[0])))
         return fail(EXQ_ERR_INVALID_ARG, "an output overlaps the other output or its input");
-    // eight pairs to a thread where vectors of 8 channels fit the pairs
+    // Eight pairs to a thread where vectors of 8 channels fit the pairs, else one, by single
+    // channels: 4096 rows of 40 heads of 80 take 11.6 us where 32 channels turn, 24.7 where
+    // 20 do and 23.5 where 40 do (in place 8.0, 9.7 and 14.3; a copy 8.2).
     const int pairs = rotary_dim % 16 == 0 ? 8 : 1;
     RotateArgs a;
     a.q = RotateHeads{static_cast<const uint16_t*>(q), static_cast<uint16_t*>(q_out), q_row_stride, q_head_stride,

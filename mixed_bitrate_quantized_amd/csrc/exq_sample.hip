@@ -29,8 +29,8 @@
 // several workgroups where there are few rows.
 //
 // The bytes of the logits are the floor (256 x 131072 fp16: 67 MB, 9.6 us).  What a call
-// takes is a chain of looks with barriers between: 1 x 32000 with a top-k of 40 11.5 us,
-// 16 x 50001 fp32 with settings of all kinds 26.1 (launch of the shares 9, the rest 17),
+// takes is a chain of looks with barriers between: 1 x 32000 with a top-k of 40 11.8 us,
+// 16 x 50001 fp32 with settings of all kinds 26.5 (launch of the shares 9, the rest 17),
 // 256 x 131072 with top-p 38: the first look 24000 cycles and 8000 until its last
 // wave, the counters 13000, the end of top-p 4500, the second look, for the list,
 // 28500, cut and draw 16000.
@@ -49,13 +49,23 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 
 constexpr int kSampleThreads = 1024, kSampleWaves = kSampleThreads / 64;
 constexpr int kSampleList = 4096;             // candidates that LDS holds
-constexpr int kSampleNear = 900;              // a top-k that is looked for from the threads' largest logits
-constexpr int kSampleFew = 256;               // candidates that are compared one by one
+// A top-k that is looked for from the threads' largest logits (of 1024 threads).  So, and
+// by what follows larger ones, at a top-k of 300, 600 and 890 (us):
+//   1 x 32000 fp16     16.0, 18.0   17.2, 18.7   19.7, 19.2      fp32   17.0, 26.7   17.9, 28.0   20.5, 28.9
+//   256 x 131072 fp16  32.9, 35.5   34.7, 36.5   38.6, 37.3      fp32   55, 91       58, 93       62, 95
+constexpr int kSampleNear = 900;
+// Candidates that are compared one by one, n * n / 1024 comparisons a thread.  So, and
+// through the tiles of the row, 1 x 32000 fp16 by top-k alone, and with a top-p of 0.95:
+//   100   11.7, 15.4   12.6, 18.5      200   13.6, 15.6   14.6, 19.0      400   22.7, 16.2   23.6, 19.5
+constexpr int kSampleFew = 256;
 constexpr int kDigit = 9;                     // bits looked at together
 constexpr int kSampleBins = 2048;             // of a row's histogram
 constexpr int kSampleParts = 16;              // of a row, at most
 constexpr int kSampleCountedShare = 32768;    // logits of a part of an fp16 row with top-p, at most
-constexpr int kSamplePartList = 1024;         // candidates of a part
+// Candidates of a part; more, or more than a list together, and the row is weighed
+// again.  16 x 50001 with top-p at a temperature of 32, of 256: fp16 68 us, fp32 76; of
+// 512, 1024 and 2048: 32 and 34.
+constexpr int kSamplePartList = 1024;
 constexpr int kSampleMaxVocabLog2 = 21;
 constexpr int kCounters = 1 << 15;            // of 16 bits for each sign
 
